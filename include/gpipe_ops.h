@@ -125,6 +125,55 @@ int gpipe_op_attention_bwd(int nseq, int seq, int heads, const void* qkv, const 
                            const void* dout, const float* lse, float* dvec, void* dqkv,
                            void* stream);
 
+/* Causal attention with a sliding window, sinks and a learned relative position
+ * bias, bf16, head width 64, scale 1/8.  Query i of a sequence sees key j when
+ * j <= i and (i - j < window or j < sinks); its score is
+ *   q_i . k_j / 8 + table[bucket(i - j), head].
+ * qkv [nseq*seq, (heads + 2 kv_heads)*64] (query | key | value column blocks;
+ * heads / kv_heads consecutive query heads share a key/value head), o
+ * [nseq*seq, heads*64], lse fp32 [nseq*seq, heads] (natural log).
+ *   window    >= 1: keys a query sees, itself included (>= seq: every earlier one).
+ *   sinks     0..64: first tokens of a sequence that stay visible to all of it.
+ *   lens      int32 [nseq] on the device, or NULL for full sequences: tokens of
+ *             each sequence (clamped to [0, seq]).  The rows behind them are
+ *             padding: nothing of them is used (they may hold anything, NaN
+ *             included), and their o and dqkv rows are written as zeros, their
+ *             lse as -inf.
+ *   table     fp32 [num_buckets, heads], or NULL with num_buckets 0.  An entry
+ *             of -1e30 or less (-inf, the lowest finite value) hides its bucket.
+ *             A query that sees nothing has o = 0, lse = -inf, zero gradients.
+ *   bucket(d) d itself below e = num_buckets / 2, then e + floor(log(d / e) /
+ *             log(max_distance / e) * (num_buckets - e)), at most
+ *             num_buckets - 1, decided in exact arithmetic
+ *             (gpipe_op_position_bucket_starts); 2 <= num_buckets <= 64,
+ *             num_buckets / 2 < max_distance <= 4096.
+ * Any seq >= 1; nseq * seq <= 2^30.  Cost grows with the visible pairs. */
+int gpipe_op_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
+                                  const int32_t* lens, const float* table, int num_buckets,
+                                  int max_distance, const void* qkv, void* o, float* lse, void* stream);
+
+/* Its backward pass: dqkv gets dQ | dK | dV (a shared key/value head's summed
+ * over its query heads); dtable_acc fp32 [num_buckets, heads] (or NULL) gets
+ * += sum of dS over the pairs of each bucket.  o and lse are the forward's, with
+ * the same lens and table.  scratch: gpipe_op_attention_window_scratch_bytes,
+ * 256-byte aligned, written before it is read (calls that may overlap on the
+ * GPU, captured ones included, need one each).  No atomics: results are
+ * bit-reproducible. */
+int gpipe_op_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
+                                  const int32_t* lens, const float* table, int num_buckets,
+                                  int max_distance, const void* qkv, const void* o, const void* dout,
+                                  const float* lse, void* dqkv, float* dtable_acc, void* scratch,
+                                  void* stream);
+
+/* Bytes of scratch the backward pass needs (num_buckets 0: no table gradient);
+ * 0 for sizes that it would reject. */
+size_t gpipe_op_attention_window_scratch_bytes(int nseq, int seq, int heads, int window, int sinks,
+                                               int num_buckets);
+
+/* starts[b] = the smallest distance of bucket b, or of the next one that is not
+ * empty (host memory, num_buckets values; no GPU work). */
+int gpipe_op_position_bucket_starts(int num_buckets, int max_distance, int32_t* starts);
+
 /* Next-token softmax cross-entropy on fp32 logits [rows, vocab].
  * Row r is token row0 + r of the mini-batch (tokens [N*seq] int32); its target
  * is tokens[row0 + r + 1] unless (row0 + r) % seq == seq - 1 (no target).
@@ -146,6 +195,35 @@ int gpipe_op_cross_entropy(int rows, int vocab, int seq, const int32_t* tokens, 
 int gpipe_op_cross_entropy_clip(int rows, int vocab, int seq, const int32_t* tokens, int row0,
                                 float inv_count, float clip, float* logits, float* loss_rows,
                                 int want_grad, void* stream);
+
+/* Distillation from a teacher's top logits, with the hard-label cross-entropy
+ * of gpipe_op_cross_entropy beside it.  Per row of student logits z (dtype
+ * elements, leading dimension ld >= vocab), teacher logits t_k = top_logit[r,k]
+ * (fp32 [rows, topk]) at tokens i_k = top_idx[r,k] (int32 [rows, topk]; i_k < 0:
+ * an empty slot, whose logit is not used), p = softmax(t / temperature) over the
+ * filled slots and q_T = softmax(z / T):
+ *   loss_rows[r] = kd_scale T^2 sum_k p_k (log p_k - log q_T[i_k])
+ *                + ce_scale (-log q_1[target])
+ *   dz           = kd_scale T (q_T - sum_k p_k onehot(i_k))
+ *                + ce_scale (q_1 - onehot(target))
+ * (T = temperature > 0, finite).  The target of row r is that of
+ * gpipe_op_cross_entropy: tokens[row0 + r + 1] unless (row0 + r) % seq ==
+ * seq - 1; tokens is not read when ce_scale = 0 and may then be NULL.  A row
+ * whose slots are all empty (or whose filled teacher logits are all -inf) has
+ * no teacher term, a row without a target no label term.  Slots that name the
+ * same token count as separate terms of the sum.  A token id of vocab or more
+ * is treated as an empty slot, a target outside [0, vocab) as no target; both
+ * set the device error flag.
+ * dz is bf16 [rows, vocab] with leading dimension lddz, or NULL for the loss
+ * alone.  It may be the logits themselves (same address, and the same row
+ * stride in bytes: lddz = ld for bf16, 2 ld for fp32); any other overlap is
+ * rejected.  Elements of a row behind the vocab-th are neither read nor written.
+ * 1 <= topk <= 256, vocab >= 1 (any; rows that start on 16-byte boundaries take
+ * wide loads).  No atomics: results are bit-reproducible. */
+int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t ld, int topk,
+                     const int32_t* top_idx, const float* top_logit, float temperature,
+                     float kd_scale, int seq, const int32_t* tokens, int row0, float ce_scale,
+                     float* loss_rows, void* dz, int64_t lddz, void* stream);
 
 /* MSE rows: loss_rows[r] = sum_j (y - t)^2 * inv_count; dy = 2 (y - t) inv_count. */
 int gpipe_op_mse(int rows, int d, const float* y, const float* t, float inv_count,

@@ -93,6 +93,15 @@ _SIGS = {
     "gpipe_op_attention_fwd": (c_int, [c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
     "gpipe_op_attention_bwd": (c_int, [c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                        c_void_p, c_void_p]),
+    "gpipe_op_attention_window_fwd": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int,
+                                              c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "gpipe_op_attention_window_bwd": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int,
+                                              c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                              c_void_p, c_void_p]),
+    "gpipe_op_attention_window_scratch_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "gpipe_op_position_bucket_starts": (c_int, [c_int, c_int, POINTER(c_int32)]),
+    "gpipe_op_distill": (c_int, [c_int, c_int, c_int, c_void_p, c_int64, c_int, c_void_p, c_void_p, c_float, c_float,
+                                 c_int, c_void_p, c_int, c_float, c_void_p, c_void_p, c_int64, c_void_p]),
     "gpipe_op_cross_entropy_clip": (c_int, [c_int, c_int, c_int, c_void_p, c_int, c_float, c_float, c_void_p, c_void_p,
                                             c_int, c_void_p]),
     "gpipe_op_cross_entropy": (c_int, [c_int, c_int, c_int, c_void_p, c_int, c_float, c_void_p, c_void_p, c_int,

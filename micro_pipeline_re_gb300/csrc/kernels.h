@@ -104,6 +104,25 @@ int launch_attention_fwd(int nseq, int seq, int heads, const void* qkv, void* o,
 int launch_attention_bwd(int nseq, int seq, int heads, const void* qkv, const void* o, const void* dout,
                          const float* lse, float* dvec, void* dqkv, cudaStream_t stream);
 
+// Causal attention with a sliding window, sinks and a bucketed position bias
+// (attention_window.cu); table NULL and buckets 0: no bias; lens NULL: full
+// sequences; dtable_acc NULL: no table gradient.
+int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks, const int32_t* lens,
+                                const float* table, int buckets, int max_distance, const void* qkv, void* o,
+                                float* lse, cudaStream_t stream);
+int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks, const int32_t* lens,
+                                const float* table, int buckets, int max_distance, const void* qkv, const void* o,
+                                const void* dout, const float* lse, void* dqkv, float* dtable_acc, void* scratch,
+                                cudaStream_t stream);
+size_t attention_window_scratch_bytes(int nseq, int seq, int heads, int window, int sinks, int buckets);
+// First distance of every bucket (host arithmetic).
+int position_bucket_starts(int buckets, int max_distance, int32_t* starts);
+
+// Distillation loss (and its gradient, dz not NULL) from a teacher's top logits.
+int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t ld, int topk, const int32_t* top_idx,
+                   const float* top_logit, float temperature, float kd_scale, int seq, const int32_t* tokens, int row0,
+                   float ce_scale, float* loss_rows, void* dz, int64_t lddz, cudaStream_t stream);
+
 int launch_cross_entropy(int rows, int vocab, int seq, const int32_t* tokens, int row0, float inv_count,
                          float* logits, float* loss_rows, int want_grad, cudaStream_t stream, float clip = 0.f);
 int launch_mse(int rows, int d, const float* y, const float* t, float inv_count, float* loss_rows, float* dy,

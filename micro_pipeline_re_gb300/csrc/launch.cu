@@ -176,6 +176,37 @@ int gpipe_op_attention_bwd(int nseq, int seq, int heads, const void* qkv, const 
                                   static_cast<cudaStream_t>(stream));
 }
 
+int gpipe_op_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
+                                  const int32_t* lens, const float* table, int num_buckets, int max_distance,
+                                  const void* qkv, void* o, float* lse, void* stream) {
+  return gp::launch_attention_window_fwd(nseq, seq, heads, kv_heads, window, sinks, lens, table, num_buckets,
+                                         max_distance, qkv, o, lse, static_cast<cudaStream_t>(stream));
+}
+
+size_t gpipe_op_attention_window_scratch_bytes(int nseq, int seq, int heads, int window, int sinks, int num_buckets) {
+  return gp::attention_window_scratch_bytes(nseq, seq, heads, window, sinks, num_buckets);
+}
+
+int gpipe_op_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
+                                  const int32_t* lens, const float* table, int num_buckets, int max_distance,
+                                  const void* qkv, const void* o, const void* dout, const float* lse, void* dqkv,
+                                  float* dtable_acc, void* scratch, void* stream) {
+  return gp::launch_attention_window_bwd(nseq, seq, heads, kv_heads, window, sinks, lens, table, num_buckets,
+                                         max_distance, qkv, o, dout, lse, dqkv, dtable_acc, scratch,
+                                         static_cast<cudaStream_t>(stream));
+}
+
+int gpipe_op_position_bucket_starts(int num_buckets, int max_distance, int32_t* starts) {
+  return gp::position_bucket_starts(num_buckets, max_distance, starts);
+}
+
+int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t ld, int topk, const int32_t* top_idx,
+                     const float* top_logit, float temperature, float kd_scale, int seq, const int32_t* tokens,
+                     int row0, float ce_scale, float* loss_rows, void* dz, int64_t lddz, void* stream) {
+  return gp::launch_distill(dtype, rows, vocab, logits, ld, topk, top_idx, top_logit, temperature, kd_scale, seq,
+                            tokens, row0, ce_scale, loss_rows, dz, lddz, static_cast<cudaStream_t>(stream));
+}
+
 int gpipe_op_cross_entropy(int rows, int vocab, int seq, const int32_t* tokens, int row0, float inv_count,
                            float* logits, float* loss_rows, int want_grad, void* stream) {
   return gp::launch_cross_entropy(rows, vocab, seq, tokens, row0, inv_count, logits, loss_rows, want_grad,
