@@ -46,6 +46,8 @@
 //
 // Every mbarrier wait is bounded as in attention.cu.  The shared-memory tiles'
 // layout is described in attention_tiles.cuh.
+#include <cuda_fp16.h>
+
 #include <atomic>
 #include <cmath>
 
@@ -79,7 +81,56 @@ __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
   return a.lens ? max(0, min(a.lens[b], a.seq)) : a.seq;
 }
 
-// A barrier of the 128 row threads on an mbarrier, with the bounded wait: a warp
+constexpr int ROW_THREADS = 256;  // two warpgroups of row threads
+// The issuer's warpgroup runs one of its four warps: whole warpgroups can pass
+// registers on.  Launched with 168 registers a thread (384 x 168 = 64512), the
+// row threads go up to 208 and the issuer's group down to 88
+// (256 x 208 + 128 x 88 = 64512).
+constexpr int WIN_THREADS = ROW_THREADS + 128;
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+
+// Bounded wait (2 s) that gives up at once after any earlier give-up in the
+// CTA.  A phase that is already complete costs one test: the issuer's waits are
+// on the way of every product.
+__device__ __forceinline__ bool lane_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(at, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(err, code);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// The whole warp waits; the answer is the same in every lane.
+__device__ __forceinline__ bool warp_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
+  return __all_sync(0xffffffffu, lane_await(bar, parity, err, code, abort));
+}
+
+// One lane of a converged warp, always the same one.  Unlike a comparison with
+// the lane number it tells the compiler that what depends on it runs once per
+// warp, so the products' operands go to uniform registers directly.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// The warp's number, known to be uniform.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
+
+// A matrix descriptor as its first k step's; the following steps add to the
+// address field (16-byte units): 2 along a K-major row, 128 down an MN-major tile.
+__device__ __forceinline__ uint64_t kdesc0(uint32_t tile) { return kdesc(tile, 0); }
+__device__ __forceinline__ uint64_t mndesc0(uint32_t tile) { return mndesc(tile, 0); }
+constexpr uint64_t kKStep = 2, kMnStep = 128;
+
+// A barrier of the row threads on an mbarrier, with the bounded wait: a warp
 // that gave up a wait and left its loop cannot strand the others here.
 struct RowSync {
   uint64_t* bar;
@@ -88,37 +139,71 @@ struct RowSync {
   uint32_t phase;
   __device__ __forceinline__ bool operator()() {
     mbar_arrive1(bar);
-    return __all_sync(0xffffffffu, await(bar, phase++ & 1u, err, DERR_ACC_WAIT, abort));
+    return warp_await(bar, phase++ & 1u, err, DERR_ACC_WAIT, abort);
   }
 };
 
-// The bias by distance, log2 domain: lut[kLutLow + d] for d = -kLutLow ..
-// last + kLutHigh - 1 (the last bucket's value from `last` on; a negative
-// distance is masked, whatever is read for it).  A tile of 128 x 128 whose
-// smallest distance is at most `last` reads no further than last + 254.
-constexpr int kLutLow = 128, kLutHigh = 256;
-__host__ __device__ constexpr int lut_words(int last) { return (kLutLow + last + kLutHigh + 3) & ~3; }
+// The bias of one head in shared memory: its value by distance in the log2
+// domain, and the rank of a distance's bucket.
+//   value[kLow + d], d = -kLow .. last + kHigh - 1: the last bucket's value from
+//   `last` on; a negative distance is masked, whatever is read for it.  A tile
+//   of 128 x 128 with a distance below `last` reads no further than last + 254.
+//   rank[d], d = 0 .. last (rank_of clamps).
+struct Bias {
+  static constexpr int kLow = 128, kHigh = 256;
+  float* value;
+  uint8_t* rank;
+  int last;
+  static __host__ __device__ constexpr int value_words(int last) { return (kLow + last + kHigh + 3) & ~3; }
+  static __host__ __device__ constexpr int rank_bytes(int last) { return (last + 16) & ~15; }
+  static __host__ __device__ constexpr int bytes(int last) { return value_words(last) * 4 + rank_bytes(last); }
 
-// Filled by the 128 row threads; val: room for kMaxBuckets floats.
-__device__ __forceinline__ bool fill_lut(const WindowArgs& a, int head, float* lut, float* val, int r, RowSync& sync) {
-  bool ok = sync();  // nobody reads the previous table any more
-  if (r < a.ranks) {
-    const float x = a.table[static_cast<int64_t>(a.bucket[r]) * a.heads + head];
-    val[r] = x <= kHidden ? -INFINITY : x * kLog2e;
+  __device__ __forceinline__ int rank_of(int d) const { return rank[max(0, min(d, last))]; }
+  // Filled by the row threads (tid < ROW_THREADS); val: room for kMaxBuckets floats.
+  __device__ __forceinline__ bool fill(const WindowArgs& a, int head, float* val, int tid, RowSync& sync) {
+    bool ok = sync();  // nobody reads the previous head's any more
+    if (tid < a.ranks) {
+      const float x = a.table[static_cast<int64_t>(a.bucket[tid]) * a.heads + head];
+      val[tid] = x <= kHidden ? -INFINITY : x * kLog2e;
+    }
+    ok = sync() && ok;
+    for (int k = 0; k < a.ranks; ++k) {
+      const int from = k == 0 ? -kLow : a.start[k];
+      const int to = k + 1 < a.ranks ? a.start[k + 1] : a.last + kHigh;
+      const float x = val[k];
+      for (int d = from + tid; d < to; d += ROW_THREADS) {
+        value[kLow + d] = x;
+        if (d >= 0 && d <= a.last) rank[d] = static_cast<uint8_t>(k);
+      }
+    }
+    return sync() && ok;
   }
-  ok = sync() && ok;
-  for (int k = 0; k < a.ranks; ++k) {
-    const int from = k == 0 ? -kLutLow : a.start[k];
-    const int to = k + 1 < a.ranks ? a.start[k + 1] : a.last + kLutHigh;
-    const float x = val[k];
-    for (int d = from + r; d < to; d += 128) lut[kLutLow + d] = x;
-  }
-  return sync() && ok;
-}
+};
 
 // Bits 0..x of a word (x < 0: none, x >= 31: all).
 __device__ __forceinline__ uint32_t bits_to(int x) {
   return x < 0 ? 0u : (x >= 31 ? 0xffffffffu : (2u << x) - 1u);
+}
+
+// Hide the columns of v whose bit in `see` is not set.
+__device__ __forceinline__ void hide32(float* v, uint32_t see) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (!((see >> i) & 1u)) v[i] = -INFINITY;
+}
+
+// 64 values as bf16 into 32 tensor-memory columns (an A operand) of this thread's lane.
+__device__ __forceinline__ void st_row64_tmem(uint32_t taddr, const float* v) {
+  uint32_t u[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) u[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  tmem_st32(taddr, u);
+}
+__device__ __forceinline__ void st_zero64_tmem(uint32_t taddr) {
+  uint32_t u[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) u[i] = 0u;
+  tmem_st32(taddr, u);
 }
 
 // Zero rows [from, to) of a tile of 128-byte rows, by one warp, for the async proxy.
@@ -127,20 +212,16 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to, int l
     *reinterpret_cast<uint4*>(tile + x * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Store 64 fp32 TMEM columns of this thread's lane, times scale, as bf16 to dst
+// Store 32 fp32 TMEM columns of this thread's lane, times scale, as bf16 to dst
 // when `valid`; zeros unless `keep` (whatever the accumulator holds then).
-__device__ __forceinline__ void store_row64_or_zero(uint32_t taddr, __nv_bfloat16* dst, float scale, bool valid,
-                                                    bool keep) {
+__device__ __forceinline__ void store_row32(uint32_t taddr, __nv_bfloat16* dst, float scale, bool valid, bool keep) {
+  float v[32];
+  ld_row32(taddr, v);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float v[32];
-    ld_row32(taddr + 32 * h, v);
+  for (int i = 0; i < 32; ++i) v[i] = keep ? v[i] * scale : 0.f;
+  if (valid) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = keep ? v[i] * scale : 0.f;
-    if (valid) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) store8(dst + 32 * h + 8 * u, v + 8 * u);
-    }
+    for (int u = 0; u < 4; ++u) store8(dst + 8 * u, v + 8 * u);
   }
 }
 
@@ -149,248 +230,290 @@ __device__ __forceinline__ void zero_row64(__nv_bfloat16* dst) {
   for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// The whole warp waits; the answer is the same in every lane.
-__device__ __forceinline__ bool warp_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
-  return __all_sync(0xffffffffu, await(bar, parity, err, code, abort));
+// A position in a ring of stages: stage, and the parity of its current use.
+struct RingPos {
+  int stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ bool misaligned(const uint8_t* sm, int* err) {
+  if (!(reinterpret_cast<uintptr_t>(sm) & 1023u)) return false;  // the tiles' swizzle needs 1024-byte alignment
+  if (threadIdx.x == 0) atomicExch(err, DERR_ALIGN);
+  return true;
 }
 
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
-// The hand-offs are those of attention.cu's forward kernel.  Tile t of nt is the
-// sinks' narrow block first (where the window has left it), then the window's
-// 128-key blocks up to the diagonal.
-constexpr int WIN_THREADS = 160;
-constexpr int FWD_BAR = 7 * T128;
-constexpr int FWD_VAL = FWD_BAR + 128;
-constexpr int FWD_LUT = FWD_VAL + kMaxBuckets * 4;
+// A CTA takes 256 queries as two tiles of 128, one for each warpgroup of row
+// threads (warps 0-3, 4-7), which share the key and value tiles of a ring.  A
+// key tile is used by the query tiles that see some of it.  Warp 8 + g issues
+// the products of query tile g, warp 10 the copies: what an issuer does between
+// two products is on the rows' way (a wait and a commit take some hundred
+// cycles), so each has as little to do as possible.  Per query tile g and key
+// tile t:
+//   issuer:  S_g = Q_g K_{t+1}^T as soon as the rows have read S_g of tile t ->
+//            commit bs[g];  O_g += P_g V_t once the rows wrote P_g -> commit
+//            bo[g], empty[stage].
+//   loader:  tile t + 4 into the stage of tile t once that is empty.
+//   rows:    wait bs[g]; read S_g; arrive bsc[g]; bias, mask, maximum; wait for
+//            the previous O product; write P_g; arrive bp[g].
+// P goes through tensor memory: as an A operand there it costs the products no
+// shared-memory reads (at head width 64 an O product with P in shared memory
+// reads 6 KB for 32 cycles of tensor work, above the 128 B a cycle there is).
+// A row's maximum is only moved when a tile exceeds it by 2^8: P is then at most
+// 2^8, which neither bf16 nor the fp32 sums mind, and O is seldom rescaled.
+constexpr int FWD_STAGES = 4;
+constexpr int FWD_RING = 2 * T128;
+constexpr int FWD_BAR = FWD_RING + FWD_STAGES * 2 * T128;
+constexpr int FWD_VAL = FWD_BAR + 256;
+constexpr int FWD_BIAS = FWD_VAL + kMaxBuckets * 4;
+constexpr float kMaxStep = 8.f;
 
 template <bool BIAS>
-__global__ void __maxnreg__(168) attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tq,
-                                                        const __grid_constant__ WindowArgs a,
-                                                        __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                                                        int* err) {
+__global__ void __launch_bounds__(WIN_THREADS, 1)
+    attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ WindowArgs a,
+                           __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int* err) {
   extern __shared__ __align__(1024) uint8_t sm[];
-  if (reinterpret_cast<uintptr_t>(sm) & 1023u) {  // the tiles' swizzle needs 1024-byte alignment
-    if (threadIdx.x == 0) atomicExch(err, DERR_ALIGN);
-    return;
-  }
+  if (misaligned(sm, err)) return;
   uint8_t* sQ = sm;
-  uint8_t* sK = sm + T128;      // two buffers
-  uint8_t* sV = sm + 3 * T128;  // two buffers
-  uint8_t* sP = sm + 5 * T128;  // keys 0..63 | keys 64..127
+  uint8_t* ring = sm + FWD_RING;  // stages of K | V
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + FWD_BAR);
-  uint64_t *bq = bar, *bk = bar + 1, *bv = bar + 3, *bs = bar + 5, *bsc = bar + 6, *bp = bar + 7, *bo = bar + 8,
-           *bfin = bar + 9, *brow = bar + 10;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 12);
+  uint64_t *full = bar, *bs = bar + 4, *bo = bar + 6, *bfin = bar + 8, *bq = bar + 10, *empty = bar + 12,
+           *bsc = bar + 16, *bp = bar + 18, *brow = bar + 20;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 21);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   float* val = reinterpret_cast<float*>(sm + FWD_VAL);
-  float* lut = reinterpret_cast<float*>(sm + FWD_LUT);
+  Bias bias{reinterpret_cast<float*>(sm + FWD_BIAS), sm + FWD_BIAS + Bias::value_words(a.last) * 4, a.last};
 
-  const int r = threadIdx.x, warp = r >> 5, ln = r & 31;
-  const int nqb = (a.seq + 127) / 128;
-  // heads fastest, then sequences, then query blocks from the last (the longest rows first)
+  const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
+  const int nqp = (a.seq + 255) / 256;
+  // heads fastest, then sequences, then pairs of query tiles from the last (the longest rows first)
   const int h = static_cast<int>(blockIdx.x) % a.heads;
-  const int bq_lin = static_cast<int>(blockIdx.x) / a.heads;
-  const int b = bq_lin % a.nseq;
-  const int qb = nqb - 1 - bq_lin / a.nseq;
-  const int q0 = qb * 128, qi = q0 + r;
+  const int lin = static_cast<int>(blockIdx.x) / a.heads;
+  const int b = lin % a.nseq;
+  const int q00 = (nqp - 1 - lin / a.nseq) * 256;
   const int64_t row0 = static_cast<int64_t>(b) * a.seq;
   const int D = a.heads * HD;
   const int kcol = D + (h / (a.heads / a.kv_heads)) * HD, vcol = kcol + a.kv_heads * HD;
 
   griddep_wait();
   const int n = seq_len(a, b);
-  if (q0 >= n) {  // a block of padding
-    if (qi < a.seq && r < 128) {
+  if (q00 >= n) {  // nothing but padding
+    const int qi = q00 + tid;
+    if (tid < ROW_THREADS && qi < a.seq) {
       zero_row64(out + (row0 + qi) * D + h * HD);
       lse[(row0 + qi) * a.heads + h] = -INFINITY;
     }
     return;
   }
-  const int ws = max(0, q0 - a.window + 1) / 128;  // the window's first key block
-  const bool sink_tile = a.sinks > 0 && ws > 0;
-  const int nt = qb - ws + 1 + (sink_tile ? 1 : 0);
-  auto tile_key = [&](int t) { return sink_tile ? (t == 0 ? 0 : (ws + t - 1) * 128) : (ws + t) * 128; };
-  auto tile_width = [&](int t) {  // keys of a tile, in steps of 32
-    return sink_tile && t == 0 ? (a.sinks + 31) & ~31 : min(128, (n - tile_key(t) + 31) & ~31);
+  // key tiles: the sinks' (where the window has left it), then the window's up to the diagonal
+  const int ws[2] = {max(0, q00 - a.window + 1) / 128, max(0, q00 + 128 - a.window + 1) / 128};
+  const bool two = q00 + 128 < n;  // the second query tile has queries
+  const int kt0 = a.sinks > 0 && ws[0] > 0 ? 1 : 0;
+  const int nt = kt0 + q00 / 128 + (two ? 1 : 0) - ws[0] + 1;
+  auto tile = [&](int t) { return t < kt0 ? 0 : ws[0] + t - kt0; };
+  auto width = [&](int t) {  // keys of a tile, in steps of 32
+    return t < kt0 ? (a.sinks + 31) & ~31 : min(128, (n - tile(t) * 128 + 31) & ~31);
   };
+  // the tiles that query tile g uses: first[g] .. last[g], and tile 0 where that holds sinks
+  const int first[2] = {kt0, kt0 + ws[1] - ws[0]};
+  const int last[2] = {kt0 + q00 / 128 - ws[0], two ? kt0 + q00 / 128 + 1 - ws[0] : -1};
+  const bool zero = a.sinks > 0 && tile(0) == 0;
 
-  if (r == 0) {
+  if (tid == 0) {
     prefetch_tmap(&tq);
-    for (int i = 0; i < 6; ++i) mbar_init(&bar[i], 1);
-    mbar_init(bsc, 128);
-    mbar_init(bp, 128);
-    mbar_init(bo, 1);
-    mbar_init(bfin, 1);
-    mbar_init(brow, 128);
+    for (int i = 0; i < 11; ++i) mbar_init(&bar[i], 1);
+    for (int i = 0; i < FWD_STAGES; ++i) mbar_init(&empty[i], two ? 2 : 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&bsc[g], 128);
+      mbar_init(&bp[g], 128);
+    }
+    mbar_init(brow, ROW_THREADS);
     *abort = 0;
     fence_barrier_init();
   }
   if (warp == 0) {
-    tmem_alloc(tslot, 256);
+    tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  const uint32_t tS = tmem, tO = tmem + 128;
+  // S_g at 128 g, O_g at 256 + 64 g, P_g at 384 + 64 g
 
-  if (warp == 4) {  // ---- issuer: the warp waits together, lane 0 issues ----
-    constexpr uint32_t idO = mma_idesc_bf16(128, 64, false, true);
-    int nk[2] = {0, 0}, nv[2] = {0, 0};
-    auto load = [&](uint8_t* dst, int col, int row, uint64_t* bar_) {
-      if (ln == 0) {
-        mbar_arrive_expect_tx(bar_, T128);
-        tma_load_3d(dst, &tq, col, row, b, bar_);
-      }
-    };
-    load(sQ, h * HD, q0, bq);
-    for (int t = 0; t < 2 && t < nt; ++t) {
-      load(sK + t * T128, kcol, tile_key(t), &bk[t]);
-      ++nk[t];
-      load(sV + t * T128, vcol, tile_key(t), &bv[t]);
-      ++nv[t];
-    }
-    auto issue_s = [&](int t) {  // S_t = Q K_t^T into TMEM (K_t loaded, S_{t-1} read out)
-      const uint32_t q = smem_u32(sQ), k = smem_u32(sK + (t & 1) * T128);
-      const uint32_t idS = mma_idesc_bf16(128, tile_width(t), false, false);
-      if (ln == 0) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, kdesc(q, kk), kdesc(k, kk), idS, kk ? 1u : 0u);
-        tc_commit(bs);
-      }
-    };
-    bool go = warp_await(bq, 0, err, DERR_MMA_WAIT, abort) && warp_await(&bk[0], 0, err, DERR_MMA_WAIT, abort);
-    if (go) {
-      tc_fence_after();
-      issue_s(0);
-    }
-    for (int t = 0; t < nt && go; ++t) {
-      const int kb = t & 1;
-      if (t + 1 < nt) {  // S_{t+1} as soon as the rows have read S_t: it computes during tile t's softmax
-        if (!warp_await(&bk[(t + 1) & 1], ((t + 1) >> 1) & 1, err, DERR_MMA_WAIT, abort)) break;
-        if (!warp_await(bsc, t & 1, err, DERR_MMA_WAIT, abort)) break;
-        tc_fence_after();
-        issue_s(t + 1);
-        if (t + 2 < nt) {  // K buffer of tile t: S_t is done
-          load(sK + kb * T128, kcol, tile_key(t + 2), &bk[kb]);
-          ++nk[kb];
+  if (warp >= 8) {
+    give_registers();
+    if (warp == 10) {  // ---- loader ----
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bq, two ? 2 * T128 : T128);
+        tma_load_3d(sQ, &tq, h * HD, q00, b, bq);
+        if (two) tma_load_3d(sQ + T128, &tq, h * HD, q00 + 128, b, bq);
+        int t = 0;
+        for (; t < nt; ++t) {
+          const int st = t % FWD_STAGES;
+          if (t >= FWD_STAGES &&
+              !lane_await(&empty[st], (t / FWD_STAGES - 1) & 1, err, DERR_TMA_WAIT, abort))
+            break;
+          uint8_t* dst = ring + st * 2 * T128;
+          mbar_arrive_expect_tx(&full[st], 2 * T128);
+          tma_load_3d(dst, &tq, kcol, tile(t) * 128, b, &full[st]);
+          tma_load_3d(dst + T128, &tq, vcol, tile(t) * 128, b, &full[st]);
         }
+        // no copy may still be landing when the CTA exits
+        for (int u = max(0, t - FWD_STAGES); u < t; ++u)
+          mbar_wait_bounded(&full[u % FWD_STAGES], (u / FWD_STAGES) & 1, err, DERR_DRAIN_WAIT);
+        mbar_wait_bounded(bq, 0, err, DERR_DRAIN_WAIT);
       }
-      if (!warp_await(&bv[kb], (t >> 1) & 1, err, DERR_MMA_WAIT, abort)) break;
-      const int w = tile_width(t), left = n - tile_key(t);
-      if (left < w) {  // values behind the sequence's end: their P is 0, they themselves may be anything
-        zero_rows(sV + kb * T128, left, w, ln);
-        fence_proxy_async_smem();
-        __syncwarp();
+      __syncwarp();
+    } else if (warp < 10 && last[warp - 8] >= 0) {  // ---- issuer of query tile g: waits together, one lane issues ----
+      const int g = warp - 8, first_g = first[g], last_g = last[g];
+      constexpr uint32_t idO = mma_idesc_bf16(128, 64, false, true);
+      const uint32_t tS = tmem + 128 * g, tO = tmem + 256 + 64 * g, tP = tmem + 384 + 64 * g;
+      const uint64_t qd = kdesc0(smem_u32(sQ + g * T128)), kd = kdesc0(smem_u32(ring)),
+                     vd = mndesc0(smem_u32(ring + T128));
+      constexpr uint64_t kStage = 2 * T128 / 16;
+      const bool at0 = zero && first_g > 0;  // the sinks' tile comes before the window's
+      if (!at0 && elect_one())
+        for (int t = 0; t < first_g; ++t) mbar_arrive1(&empty[t]);  // tiles (at most one) that only the other uses
+      if (at0 && first_g > 1 && elect_one()) mbar_arrive1(&empty[1]);
+      auto issue_s = [&](int t) {
+        const int st = t % FWD_STAGES;
+        const uint32_t idS = mma_idesc_bf16(128, width(t), false, false);
+        const uint64_t k = kd + st * kStage;
+        if (!warp_await(&full[st], (t / FWD_STAGES) & 1, err, DERR_MMA_WAIT, abort)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, qd + kk * kKStep, k + kk * kKStep, idS, kk ? 1u : 0u);
+          tc_commit(&bs[g]);
+        }
+        return true;
+      };
+      int t = at0 ? 0 : first_g;
+      bool go = warp_await(bq, 0, err, DERR_MMA_WAIT, abort) && issue_s(t);
+      for (uint32_t c = 0; go; ++c) {
+        const int tn = t < first_g ? first_g : t + 1;
+        if (tn <= last_g) {  // the next S as soon as the rows have read this one
+          go = warp_await(&bsc[g], c & 1, err, DERR_MMA_WAIT, abort) && issue_s(tn);
+          if (!go) break;
+        }
+        const int st = t % FWD_STAGES, w = width(t), left = n - tile(t) * 128;
+        if (left < w) {  // values behind the sequence's end: their P is 0, they themselves may be anything
+          zero_rows(ring + st * 2 * T128 + T128, left, w, ln);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint64_t v = vd + st * kStage;
+        go = warp_await(&bp[g], c & 1, err, DERR_MMA_WAIT, abort);  // P written, O rescaled
+        if (!go) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (16 * kk < w) tc_mma_f16_ta(tO, tP + 8 * kk, v + kk * kMnStep, idO, (c | kk) ? 1u : 0u);
+          tc_commit(&bo[g]);
+          if (t + FWD_STAGES < nt) tc_commit(&empty[st]);
+        }
+        if (tn > last_g) break;
+        t = tn;
       }
-      if (!warp_await(bp, t & 1, err, DERR_MMA_WAIT, abort)) break;                 // P_t written, O rescaled
-      if (t > 0 && !warp_await(bo, (t - 1) & 1, err, DERR_MMA_WAIT, abort)) break;  // O += P_{t-1} V_{t-1} done
-      if (t >= 1 && t + 1 < nt) {                                                  // V buffer of tile t-1 is free
-        const int nb = (t + 1) & 1;
-        load(sV + nb * T128, vcol, tile_key(t + 1), &bv[nb]);
-        ++nv[nb];
+      if (elect_one()) {  // no product may still be running when the CTA exits
+        tc_commit(&bfin[g]);
+        mbar_wait_bounded(&bfin[g], 0, err, DERR_DRAIN_WAIT);
       }
-      tc_fence_after();
-      if (ln == 0) {
-        const uint32_t p = smem_u32(sP), v = smem_u32(sV + kb * T128);
-        for (int kk = 0; kk < w / 16; ++kk)
-          tc_mma_f16(tO, kdesc(p + (kk >> 2) * T128, kk & 3), mndesc(v, kk), idO, (t | kk) ? 1u : 0u);
-        tc_commit(bo);
-      }
+      __syncwarp();
     }
-    // no copy may still be landing, and no product still running, when the CTA exits
-    if (ln == 0) {
-      tc_commit(bfin);
-      mbar_wait_bounded(bfin, 0, err, DERR_DRAIN_WAIT);
-      for (int bb = 0; bb < 2; ++bb) {
-        if (nk[bb]) mbar_wait_bounded(&bk[bb], (nk[bb] - 1) & 1, err, DERR_DRAIN_WAIT);
-        if (nv[bb]) mbar_wait_bounded(&bv[bb], (nv[bb] - 1) & 1, err, DERR_DRAIN_WAIT);
-      }
-      mbar_wait_bounded(bq, 0, err, DERR_DRAIN_WAIT);
-    }
-    __syncwarp();
   } else {  // ---- rows ----
-    const uint32_t lane = static_cast<uint32_t>(warp * 32) << 16;
+    take_registers();
+    const int g = warp >> 2;
+    const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int q0 = q00 + 128 * g, qi = q0 + (tid & 127);
+    const uint32_t tS = tmem + 128 * g + lane, tO = tmem + 256 + 64 * g + lane, tP = tmem + 384 + 64 * g + lane;
     RowSync sync{brow, err, abort, 0u};
     float m = -INFINITY, l = 0.f;
-    bool ok = !BIAS || fill_lut(a, h, lut, val, r, sync);
-    for (int t = 0; t < nt && ok; ++t) {
-      const int j0 = tile_key(t), w = tile_width(t);
-      ok = warp_await(bs, t & 1, err, DERR_ACC_WAIT, abort);
+    bool ok = !BIAS || bias.fill(a, h, val, tid, sync);
+    uint32_t count = 0;  // tiles done
+    const int first_g = first[g], last_g = last[g];
+    for (int t = zero ? 0 : first_g; t <= last_g && ok; t = t < first_g ? first_g : t + 1) {
+      const int j0 = tile(t) * 128, w = width(t);
+      ok = warp_await(&bs[g], count & 1, err, DERR_ACC_WAIT, abort);
       if (!ok) break;
       tc_fence_after();
       float sv[128];
       {
         // columns behind the tile's width hold what was there before: the mask hides them
-        const uint32_t at[4] = {tS + lane, tS + lane + 32, tS + lane + 64, tS + lane + 96};
+        const uint32_t at[4] = {tS, tS + 32, tS + 64, tS + 96};
         ld_rows<4>(at, sv);
       }
       tc_fence_before();
-      mbar_arrive1(bsc);  // S may be overwritten by the next tile's product
-      // scores = sc * s + cb (log2 domain): the raw scores with a constant bias,
-      // or with the bias by distance already added
+      mbar_arrive1(&bsc[g]);  // S may be overwritten by the next tile's product
+      // scores = sc * s + cb (log2 domain): the raw scores with a bias that is the
+      // same all along the row, or with the bias by distance already added
       float sc = kScaleLog2, cb = 0.f;
       if (BIAS) {
-        if (q0 - (j0 + 127) >= a.last) {
-          cb = lut[kLutLow + a.last];
+        const int d = qi - j0;
+        if (__all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d - 127))) {
+          cb = bias.value[Bias::kLow + max(0, min(d, a.last))];
         } else {
-          const float* at = lut + kLutLow + (qi - j0);
+          const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
           for (int i = 0; i < 128; ++i) sv[i] = fmaf(sv[i], kScaleLog2, at[-i]);
           sc = 1.f;
         }
       }
-      if (w < 128 || !(j0 + 127 <= q0 && q0 + 127 - j0 < a.window)) {  // some pair is hidden
+      if (__builtin_expect(w < 128 || !(j0 + 127 <= q0 && q0 + 127 - j0 < a.window), 0)) {  // some pair is hidden
         const int hi = qi - j0, lo = hi - a.window + 1, sk = a.sinks - j0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t see = bits_to(hi - 32 * c) & (~bits_to(lo - 1 - 32 * c) | bits_to(sk - 1 - 32 * c));
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((see >> i) & 1u)) sv[32 * c + i] = -INFINITY;
-        }
+        for (int c = 0; c < 4; ++c)
+          hide32(sv + 32 * c, bits_to(hi - 32 * c) & (~bits_to(lo - 1 - 32 * c) | bits_to(sk - 1 - 32 * c)));
       }
       float mx8[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 128; i += 2) mx8[(i >> 1) & 7] = fmax3(mx8[(i >> 1) & 7], sv[i], sv[i + 1]);
-      const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
-      const float mn = fmaxf(m, fmaf(mx, sc, cb));
+      const float mx = fmaf(
+          fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7])), sc, cb);
+      const float mn = mx > m + kMaxStep ? mx : m;  // (m = -inf: as soon as anything is visible)
       const float ms = mn == -INFINITY ? 0.f : mn;  // nothing visible yet: exp2(-inf - 0) = 0
-      const float alpha = ex2_approx(m - ms);
+      const float alpha = m == mn ? 1.f : ex2_approx(m - ms);
       m = mn;
-      if (t > 0) {  // the previous O product reads P and writes O
-        ok = warp_await(bo, (t - 1) & 1, err, DERR_ACC_WAIT, abort);
+      if (count > 0) {  // the previous O product reads P and writes O
+        ok = warp_await(&bo[g], (count - 1) & 1, err, DERR_ACC_WAIT, abort);
         if (!ok) break;
         tc_fence_after();
       }
       const float off = cb - ms;
       float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (32 * c < w) {
-          float* pc = sv + 32 * c;
+      for (int c = 0; c < 2; ++c) {
+        if (64 * c < w) {
+          float* pc = sv + 64 * c;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < 64; i += 2) {
             ffma2(pc[i], pc[i + 1], pc[i], pc[i + 1], sc, sc, off, off);
             pc[i] = ex2_approx(pc[i]);
             pc[i + 1] = ex2_approx(pc[i + 1]);
             const int e = (i >> 1) & 3;
             fadd2(rs8[2 * e], rs8[2 * e + 1], rs8[2 * e], rs8[2 * e + 1], pc[i], pc[i + 1]);
           }
-          st_row32_bf16(sP + (c >> 1) * T128, r, (c & 1) * 4, pc);
+          st_row64_tmem(tP + 32 * c, pc);
         }
       }
       const float rs = ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
-      if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // warp-uniform: tcgen05 loads/stores are per warp
+      if (count > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // warp-uniform: tcgen05 loads/stores are per warp
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t u[32];
-          tmem_ld32(tO + lane + 32 * c, u);
+          tmem_ld32(tO + 32 * c, u);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
@@ -399,28 +522,35 @@ __global__ void __maxnreg__(168) attn_window_fwd_kernel(const __grid_constant__ 
             u[i] = __float_as_uint(a0);
             u[i + 1] = __float_as_uint(a1);
           }
-          tmem_st32(tO + lane + 32 * c, u);
+          tmem_st32(tO + 32 * c, u);
         }
-        tmem_st_wait();
       }
+      tmem_st_wait();
       l = l * alpha + rs;
-      fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive1(bp);
+      mbar_arrive1(&bp[g]);
+      ++count;
     }
-    if (ok) ok = warp_await(bo, (nt - 1) & 1, err, DERR_ACC_WAIT, abort);
+    if (ok && count > 0) ok = warp_await(&bo[g], (count - 1) & 1, err, DERR_ACC_WAIT, abort);
     tc_fence_after();
-    if (ok) {
+    if (ok && qi < a.seq && count == 0) {  // a second tile of padding
+      zero_row64(out + (row0 + qi) * D + h * HD);
+      lse[(row0 + qi) * a.heads + h] = -INFINITY;
+    }
+    if (ok && count > 0) {
       // l = 0: a row that sees nothing (padding, or every bucket of its keys hidden)
-      store_row64_or_zero(tO + lane, out + (row0 + qi) * D + h * HD, 1.0f / l, qi < a.seq, qi < n && l != 0.f);
-      if (qi < a.seq) lse[(row0 + qi) * a.heads + h] = qi < n && l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      const bool keep = qi < n && l != 0.f;
+      __nv_bfloat16* dst = out + (row0 + qi) * D + h * HD;
+      store_row32(tO, dst, 1.0f / l, qi < a.seq, keep);
+      store_row32(tO + 32, dst + 32, 1.0f / l, qi < a.seq, keep);
+      if (qi < a.seq) lse[(row0 + qi) * a.heads + h] = keep ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -476,44 +606,121 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
   if (in && sub == 0) ld[(b * a.heads + h) * seqpad + i] = make_float2(L, -d);
 }
 
-constexpr int BWD_TILES = 6 * T128;
-constexpr int BWD_LD = BWD_TILES;  // dK/dV: -LSE and -D of two query blocks (1 KB)
-constexpr int BWD_BAR = BWD_LD + 4 * 64 * 4;
-constexpr int BWD_VAL = BWD_BAR + 128;
-constexpr int BWD_LUT = BWD_VAL + kMaxBuckets * 4;
+// Both kinds of CTA work on 128 x 128 tiles: S and dP (or their transposes) take
+// 128 tensor-memory columns each, warpgroup g of the row threads has columns
+// 64 g .. 64 g + 63 of every row, and P, dS go back into tensor memory as bf16 A
+// operands.  With operands A from shared memory the two wide products keep the
+// 128 B a cycle of shared memory just busy (8 KB for 64 cycles of tensor work);
+// with A from tensor memory the three 64-wide ones need half of it.
+//   warp 8:  S, dP of tile t+1 as soon as the rows have read tile t's -> commit
+//            bs.
+//   warp 9:  the gradient products of tile t once the rows wrote P, dS ->
+//            commit bo, empty[stage].
+//   warp 10: the copies; a tile into the ring once its stage is empty.
+//   rows:    wait bs; read S, dP; arrive bsc; the elementwise gradient; wait
+//            bo of tile t-1 (it reads P, dS); write them; arrive bp.
+constexpr int BWD_STAGE = 2 * T128;
+constexpr int BWD_STAGES = 3;  // at most (2 where a large table's sums need the room)
+constexpr int BWD_RING = 2 * T128;
+// behind the ring: -lse log2(e), -D of the stages' queries (dK/dV), barriers, bias
+constexpr int BWD_LD_BYTES = BWD_STAGES * 128 * 8;
+constexpr int BWD_FIXED = BWD_LD_BYTES + 256 + kMaxBuckets * 4;
+
+struct BwdSmem {
+  uint8_t *a, *b, *ring;
+  float2* ld;
+  uint64_t *full, *empty, *b0, *bs, *bo, *bfin, *bsc, *bp, *brow;
+  uint32_t* tslot;
+  volatile int* abort;
+  float* val;
+  Bias bias;
+  uint8_t* rest;
+  __device__ BwdSmem(uint8_t* sm, int stages, const WindowArgs& w) {
+    a = sm;
+    b = sm + T128;
+    ring = sm + BWD_RING;
+    uint8_t* p = ring + stages * BWD_STAGE;
+    ld = reinterpret_cast<float2*>(p);
+    full = reinterpret_cast<uint64_t*>(p + BWD_LD_BYTES);
+    empty = full + 3;
+    b0 = full + 6;
+    bs = full + 7;
+    bo = full + 8;
+    bfin = full + 9;  // two
+    bsc = full + 11;
+    bp = full + 12;
+    brow = full + 13;
+    tslot = reinterpret_cast<uint32_t*>(full + 14);
+    abort = reinterpret_cast<volatile int*>(tslot + 1);
+    val = reinterpret_cast<float*>(p + BWD_LD_BYTES + 256);
+    uint8_t* t = p + BWD_FIXED;
+    bias = Bias{reinterpret_cast<float*>(t), t + Bias::value_words(w.last) * 4, w.last};
+    rest = t + (w.ranks ? Bias::bytes(w.last) : 0);
+  }
+  __device__ uint32_t start(int warp, const CUtensorMap* m0, const CUtensorMap* m1) {
+    if (threadIdx.x == 0) {
+      prefetch_tmap(m0);
+      prefetch_tmap(m1);
+      for (int i = 0; i < 11; ++i) mbar_init(&full[i], 1);
+      mbar_init(bsc, ROW_THREADS);
+      mbar_init(bp, ROW_THREADS);
+      mbar_init(brow, ROW_THREADS);
+      *abort = 0;
+      fence_barrier_init();
+    }
+    if (warp == 0) {
+      tmem_alloc(tslot, 512);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return *tslot;
+  }
+  __device__ void finish(int warp, uint32_t tmem) {
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
+  }
+};
+
+// An issuer's last act (one lane): none of its products may still be running when the CTA exits.
+__device__ __forceinline__ void drain_products(uint64_t* bfin, int* err) {
+  tc_commit(bfin);
+  mbar_wait_bounded(bfin, 0, err, DERR_DRAIN_WAIT);
+}
+// The loader's (one lane): none of its `loaded` copies into the ring may still be landing.
+__device__ __forceinline__ void drain_copies(const BwdSmem& s, int loaded, int stages, int* err) {
+  for (int t = max(0, loaded - stages); t < loaded; ++t)
+    mbar_wait_bounded(&s.full[t % stages], (t / stages) & 1, err, DERR_DRAIN_WAIT);
+  mbar_wait_bounded(s.b0, 0, err, DERR_DRAIN_WAIT);
+}
 
 // MODE 0: no bias; 1: bias; 2: bias and its gradient.
 //
-// dQ CTA.  Key blocks of 64 by rising key, the sinks' block last.  In the
-// gradient of the table a row's distances fall along the walk, so its bucket
-// falls too: the running sums of dS and P are added to the row's own word of
-// the bucket (no two threads share one) where a bucket ends.
+// dQ CTA: 128 queries, the window's key tiles by rising key, the sinks' (64
+// wide) last.  For the gradient of the table each row thread adds its dS and P
+// by bucket into words of its own (no two threads share one): a tile along
+// whose row the bucket does not change adds one sum; elsewhere the running sum
+// is put down at the columns where a bucket ends.
 template <int MODE>
-__device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
-                              const CUtensorMap* td128, const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv,
-                              int item, int* err, uint8_t* sm) {
-  uint8_t* sQ = sm;
-  uint8_t* sdO = sm + T128;
-  uint8_t* sKV = sm + 2 * T128;  // two slots of K (64 rows) | V (64 rows)
-  uint8_t* sP = sm + 4 * T128;   // 128 queries x 64 keys (the sinks' block only)
-  uint8_t* sdS = sm + 5 * T128;  // 128 queries x 64 keys
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + BWD_BAR);
-  uint64_t *bq = bar, *bkv = bar + 1, *bs = bar + 3, *bsc = bar + 4, *bp = bar + 5, *bo = bar + 6, *bfin = bar + 7,
-           *brow = bar + 10;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 12);
-  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  float* val = reinterpret_cast<float*>(sm + BWD_VAL);
-  float* lut = reinterpret_cast<float*>(sm + BWD_LUT);
-  float* accS = lut + lut_words(a.last);   // [ranks][128]
-  float* accP = accS + a.ranks * 128;      // [ranks][128]
-  uint32_t* ends = reinterpret_cast<uint32_t*>(accP + a.ranks * 128);  // bit d: distance d is its bucket's first
+__device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td,
+                              const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int stages,
+                              int* err, uint8_t* sm) {
+  BwdSmem s(sm, stages, a);
+  float* accS = reinterpret_cast<float*>(s.rest);                             // [ranks][256]
+  __half* accP = reinterpret_cast<__half*>(accS + a.ranks * ROW_THREADS);     // [ranks][256]
+  uint32_t* ends = reinterpret_cast<uint32_t*>(accP + a.ranks * ROW_THREADS);  // bit d: d is its bucket's first
 
-  const int r = threadIdx.x, warp = r >> 5, ln = r & 31;
+  const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int nqb = (a.seq + 127) / 128;
   const int h = item % a.heads;
   const int b = (item / a.heads) % a.nseq;
   const int qb = nqb - 1 - item / (a.heads * a.nseq);
-  const int q0 = qb * 128, qi = q0 + r;
+  const int q0 = qb * 128;
   const int64_t row0 = static_cast<int64_t>(b) * a.seq;
   const int D = a.heads * HD;
   const int64_t ld = static_cast<int64_t>(a.heads + 2 * a.kv_heads) * HD;
@@ -523,262 +730,258 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
   const int n = seq_len(a, b);
   float* tab = MODE == 2 ? ws_.tab + ((static_cast<int64_t>(b) * nqb + qb) * a.heads + h) * a.ranks : nullptr;
   if (q0 >= n) {  // a block of padding
-    if (qi < a.seq && r < 128) zero_row64(dqkv + (row0 + qi) * ld + h * HD);
-    if (MODE == 2 && r < a.ranks) tab[r] = 0.f;
+    if (tid < 128 && q0 + tid < a.seq) zero_row64(dqkv + (row0 + q0 + tid) * ld + h * HD);
+    if (MODE == 2 && tid < a.ranks) tab[tid] = 0.f;
     return;
   }
-  const bool sink_tile = a.sinks > 0 && qb >= first_far_block(a.window);
-  const int kb0 = a.sinks > 0 && !sink_tile ? 0 : max(0, q0 - a.window + 1) / 64;
-  const int nwin = min(q0 + 127, n - 1) / 64 - kb0 + 1;
+  const int kt0 = max(0, q0 - a.window + 1) / 128;
+  const bool sink_tile = a.sinks > 0 && kt0 > 0;
+  const int nwin = qb - kt0 + 1;
   const int nt = nwin + (sink_tile ? 1 : 0);
-  auto tile_key = [&](int t) { return t < nwin ? (kb0 + t) * 64 : 0; };
+  auto tile_key = [&](int t) { return t < nwin ? (kt0 + t) * 128 : 0; };
 
-  if (r == 0) {
-    prefetch_tmap(tq64);
-    prefetch_tmap(tq128);
-    prefetch_tmap(td128);
-    for (int i = 0; i < 4; ++i) mbar_init(&bar[i], 1);
-    mbar_init(bsc, 128);
-    mbar_init(bp, 128);
-    mbar_init(bo, 1);
-    mbar_init(bfin, 1);
-    mbar_init(brow, 128);
-    *abort = 0;
-    fence_barrier_init();
-  }
-  if (warp == 0) {
-    tmem_alloc(tslot, 256);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
-  const uint32_t tS = tmem, tP = tmem + 64, tQ = tmem + 128;
+  const uint32_t tmem = s.start(warp, tq, td);
+  // S at 0, dP at 128, dQ at 256, dS (bf16) at 320
+  const uint32_t tS = tmem, tP = tmem + 128, tQ = tmem + 256, tdS = tmem + 320;
+  // the sinks' P and dS in shared memory: the stage behind the last tile's, free by then
+  uint8_t* sinkP = s.ring + (nt % stages) * BWD_STAGE;
 
-  if (warp == 4) {  // ---- issuer ----
-    constexpr uint32_t idSP = mma_idesc_bf16(128, 64, false, false);
-    constexpr uint32_t idQ = mma_idesc_bf16(128, 64, false, true);
-    constexpr uint32_t idT = mma_idesc_bf16(128, 64, true, true);
-    int nkv[2] = {0, 0};
-    if (ln == 0) {
-      mbar_arrive_expect_tx(bq, 2 * T128);
-      tma_load_3d(sQ, tq128, h * HD, q0, b, bq);
-      tma_load_3d(sdO, td128, h * HD, q0, b, bq);
-    }
-    auto load_kv = [&](int t) {
-      const int s = t & 1;
-      if (ln == 0) {
-        mbar_arrive_expect_tx(&bkv[s], 2 * T64);
-        tma_load_3d(sKV + s * T128, tq64, kcol, tile_key(t), b, &bkv[s]);
-        tma_load_3d(sKV + s * T128 + T64, tq64, vcol, tile_key(t), b, &bkv[s]);
-      }
-      ++nkv[s];
-    };
-    for (int t = 0; t < 2 && t < nt; ++t) load_kv(t);
-    auto issue_sp = [&](int t) {  // S = Q K_t^T, dP = dO V_t^T (tile t loaded, tile t-1's read out)
-      uint8_t* kv = sKV + (t & 1) * T128;
-      const int left = n - tile_key(t);
-      if (left < 64) {  // keys behind the sequence's end: P = dS = 0, the rows themselves may be anything
-        zero_rows(kv, left, 64, ln);
-        zero_rows(kv + T64, left, 64, ln);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      const uint32_t q = smem_u32(sQ), dO = smem_u32(sdO), k = smem_u32(kv), v = smem_u32(kv + T64);
-      if (ln == 0) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, kdesc(q, kk), kdesc(k, kk), idSP, kk ? 1u : 0u);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tP, kdesc(dO, kk), kdesc(v, kk), idSP, kk ? 1u : 0u);
-        tc_commit(bs);
-      }
-    };
-    bool go = warp_await(bq, 0, err, DERR_MMA_WAIT, abort) && warp_await(&bkv[0], 0, err, DERR_MMA_WAIT, abort);
-    if (go) {
-      if (n - q0 < 128) {  // padded queries: with Q = dO = 0 and P = 0 they add nothing to the sinks' sums
-        zero_rows(sQ, n - q0, 128, ln);
-        zero_rows(sdO, n - q0, 128, ln);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      tc_fence_after();
-      issue_sp(0);
-    }
-    for (int t = 0; t < nt && go; ++t) {
-      if (t + 1 < nt) {  // the next tile's S, dP as soon as the rows have read tile t's
-        if (!warp_await(&bkv[(t + 1) & 1], ((t + 1) >> 1) & 1, err, DERR_MMA_WAIT, abort)) break;
-        if (!warp_await(bsc, t & 1, err, DERR_MMA_WAIT, abort)) break;
-        tc_fence_after();
-        issue_sp(t + 1);
-      }
-      if (!warp_await(bp, t & 1, err, DERR_MMA_WAIT, abort)) break;  // dS_t written
-      tc_fence_after();
-      if (ln == 0) {
-        const uint32_t ds = smem_u32(sdS), k = smem_u32(sKV + (t & 1) * T128);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tQ, kdesc(ds, kk), mndesc(k, kk), idQ, (t | kk) ? 1u : 0u);
-        if (t >= nwin) {
-          // the sinks' dV = P^T dO and dK = dS^T Q over this block's queries, in the columns of S and
-          // dP: P and dS read MN-major.  Rows 64..127 of the products come from the addresses 1024
-          // bytes further (inside the CTA's shared memory) and are not read.
-          const uint32_t p = smem_u32(sP), q = smem_u32(sQ), dO = smem_u32(sdO);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_f16(tS, sw128_desc(p + kk * 2048, 1024, 1024), mndesc(dO, kk), idT, kk ? 1u : 0u);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_f16(tP, sw128_desc(ds + kk * 2048, 1024, 1024), mndesc(q, kk), idT, kk ? 1u : 0u);
+  if (warp >= 8) {
+    give_registers();
+    if (warp == 10) {  // ---- loader ----
+      if (elect_one()) {
+        mbar_arrive_expect_tx(s.b0, 2 * T128);
+        tma_load_3d(s.a, tq, h * HD, q0, b, s.b0);
+        tma_load_3d(s.b, td, h * HD, q0, b, s.b0);
+        RingPos lp;
+        int t = 0;
+        for (; t < nt; ++t) {
+          if (t >= stages && !lane_await(&s.empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
+          uint8_t* dst = s.ring + lp.stage * BWD_STAGE;
+          mbar_arrive_expect_tx(&s.full[lp.stage], 2 * T128);
+          tma_load_3d(dst, tq, kcol, tile_key(t), b, &s.full[lp.stage]);
+          tma_load_3d(dst + T128, tq, vcol, tile_key(t), b, &s.full[lp.stage]);
+          lp.next(stages);
         }
-        tc_commit(bo);
+        drain_copies(s, t, stages, err);
       }
-      if (t + 2 < nt) {  // tile t's slot, once dQ += dS_t K_t is done
-        if (!warp_await(bo, t & 1, err, DERR_MMA_WAIT, abort)) break;
-        load_kv(t + 2);
+      __syncwarp();
+    } else if (warp == 8) {  // ---- S = Q K_t^T, dP = dO V_t^T ----
+      bool go = warp_await(s.b0, 0, err, DERR_MMA_WAIT, s.abort);
+      if (go && n - q0 < 128) {  // padded queries: with Q = dO = 0 and P = 0 they add nothing to the sinks' sums
+        zero_rows(s.a, n - q0, 128, ln);
+        zero_rows(s.b, n - q0, 128, ln);
+        fence_proxy_async_smem();
+        __syncwarp();
       }
+      const uint64_t q = kdesc0(smem_u32(s.a)), dO = kdesc0(smem_u32(s.b)), kd = kdesc0(smem_u32(s.ring));
+      RingPos sp;
+      for (int t = 0; t < nt && go; ++t) {
+        go = warp_await(&s.full[sp.stage], sp.parity, err, DERR_MMA_WAIT, s.abort);
+        const int left = n - tile_key(t);
+        if (left < 128) {  // keys behind the sequence's end: P = dS = 0, the rows themselves may be anything
+          uint8_t* kv = s.ring + sp.stage * BWD_STAGE;
+          zero_rows(kv, left, 128, ln);
+          zero_rows(kv + T128, left, 128, ln);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint64_t k = kd + sp.stage * (BWD_STAGE / 16), v = k + T128 / 16;
+        const uint32_t id = mma_idesc_bf16(128, t < nwin ? 128 : 64, false, false);
+        if (t > 0) go = go && warp_await(s.bsc, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // tile t-1's read out
+        if (!go) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, q + kk * kKStep, k + kk * kKStep, id, kk ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tP, dO + kk * kKStep, v + kk * kKStep, id, kk ? 1u : 0u);
+          tc_commit(s.bs);
+        }
+        sp.next(stages);
+      }
+      if (elect_one()) drain_products(&s.bfin[0], err);
+      __syncwarp();
+    } else if (warp == 9) {  // ---- dQ += dS K_t ----
+      constexpr uint32_t idQ = mma_idesc_bf16(128, 64, false, true);
+      constexpr uint32_t idT = mma_idesc_bf16(128, 64, true, true);
+      const uint64_t kd = mndesc0(smem_u32(s.ring));
+      RingPos gp_;
+      for (int t = 0; t < nt; ++t) {
+        const uint64_t k = kd + gp_.stage * (BWD_STAGE / 16);
+        if (!warp_await(s.bp, t & 1, err, DERR_MMA_WAIT, s.abort)) break;  // dS_t written
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < 4 || t < nwin) tc_mma_f16_ta(tQ, tdS + 8 * kk, k + kk * kMnStep, idQ, (t | kk) ? 1u : 0u);
+          if (t >= nwin) {
+            // the sinks' dV = P^T dO and dK = dS^T Q over this block's queries, in the columns of S and
+            // dP: P and dS read MN-major.  Rows 64..127 of the products come from the addresses 1024
+            // bytes further (inside the CTA's shared memory) and are not read.
+            const uint32_t p = smem_u32(sinkP), q = smem_u32(s.a), dO = smem_u32(s.b);
+#pragma unroll 1
+            for (int kk = 0; kk < 8; ++kk) {
+              tc_mma_f16(tS, sw128_desc(p + kk * 2048, 1024, 1024), mndesc(dO, kk), idT, kk ? 1u : 0u);
+              tc_mma_f16(tP, sw128_desc(p + T128 + kk * 2048, 1024, 1024), mndesc(q, kk), idT, kk ? 1u : 0u);
+            }
+          }
+          tc_commit(s.bo);
+          tc_commit(&s.empty[gp_.stage]);
+        }
+        gp_.next(stages);
+      }
+      if (elect_one()) drain_products(&s.bfin[1], err);
+      __syncwarp();
     }
-    if (ln == 0) {
-      tc_commit(bfin);
-      mbar_wait_bounded(bfin, 0, err, DERR_DRAIN_WAIT);
-      for (int s = 0; s < 2; ++s)
-        if (nkv[s]) mbar_wait_bounded(&bkv[s], (nkv[s] - 1) & 1, err, DERR_DRAIN_WAIT);
-      mbar_wait_bounded(bq, 0, err, DERR_DRAIN_WAIT);
-    }
-    __syncwarp();
   } else {  // ---- rows ----
-    const uint32_t lane = static_cast<uint32_t>(warp * 32) << 16;
-    RowSync sync{brow, err, abort, 0u};
-    bool ok = !MODE || fill_lut(a, h, lut, val, r, sync);
-    int rank = -1;                   // the bucket (by rank) of the running sums
-    float runS = 0.f, runP = 0.f;
+    take_registers();
+    const int g = warp >> 2, r = tid & 127, qi = q0 + r;
+    const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    RowSync sync{s.brow, err, s.abort, 0u};
+    const Bias& bias = s.bias;
+    bool ok = !MODE || s.bias.fill(a, h, s.val, tid, sync);
     const int nend = a.last / 32 + 1;
+    float farS = 0.f, farP = 0.f;  // the last bucket's sums
     if (MODE == 2) {
-      for (int k = 0; k < 2 * a.ranks; ++k) accS[k * 128 + r] = 0.f;
-      for (int x = r; x < nend; x += 128) ends[x] = 0u;
+      for (int k = 0; k < a.ranks; ++k) {
+        accS[k * ROW_THREADS + tid] = 0.f;
+        accP[k * ROW_THREADS + tid] = __float2half(0.f);
+      }
+      for (int x = tid; x < nend; x += ROW_THREADS) ends[x] = 0u;
       ok = sync() && ok;
-      if (r < a.ranks) atomicOr(&ends[a.start[r] >> 5], 1u << (a.start[r] & 31));
+      if (tid < a.ranks) atomicOr(&ends[a.start[tid] >> 5], 1u << (a.start[tid] & 31));
       ok = sync() && ok;
     }
-    auto rank_of = [&](int d) {
-      int k = a.ranks - 1;
-      while (k > 0 && a.start[k] > d) --k;
-      return k;
+    auto put = [&](int rank, float x, float p) {
+      accS[rank * ROW_THREADS + tid] += x;
+      __half* at = accP + rank * ROW_THREADS + tid;
+      *at = __float2half(__half2float(*at) + p);
     };
-    auto flush = [&]() {
-      if (rank >= 0) {
-        accS[rank * 128 + r] += runS;
-        accP[rank * 128 + r] += runP;
-      }
-      runS = runP = 0.f;
-    };
-    if (MODE == 2) rank = rank_of(qi - kb0 * 64);
     const float2 LD = ws_.ld[(static_cast<int64_t>(b) * a.heads + h) * pad128(a.seq) + qi];
     for (int t = 0; t < nt && ok; ++t) {
-      const int j0 = tile_key(t);
       const bool sink = t >= nwin;
-      ok = warp_await(bs, t & 1, err, DERR_ACC_WAIT, abort);
+      const int j0 = tile_key(t) + 64 * g;  // the key of this thread's column 0
+      uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
+      if (sink || !(j0 + 63 <= q0 && q0 + 127 - j0 < a.window)) {
+        const int hi = qi - j0, lo = hi - a.window + 1, sk = a.sinks - j0;
+        const uint32_t n0 = sink ? 0u : ~bits_to(lo - 1), n1 = sink ? 0u : ~bits_to(lo - 33);
+        see0 = bits_to(hi) & (n0 | bits_to(sk - 1));
+        see1 = bits_to(hi - 32) & (n1 | bits_to(sk - 33));
+      }
+      const bool any = __any_sync(0xffffffffu, (see0 | see1) != 0u);
+      ok = warp_await(s.bs, t & 1, err, DERR_ACC_WAIT, s.abort);
       if (!ok) break;
       tc_fence_after();
       float v[128];  // S (64 columns), then dP (64 columns), one round trip
-      {
-        const uint32_t at[4] = {tS + lane, tS + lane + 32, tP + lane, tP + lane + 32};
+      if (any) {
+        const uint32_t c = lane + 64 * g;
+        const uint32_t at[4] = {tS + c, tS + c + 32, tP + c, tP + c + 32};
         ld_rows<4>(at, v);
       }
       tc_fence_before();
-      mbar_arrive1(bsc);
-      const bool near = MODE && q0 - (j0 + 63) <= a.last;  // not all pairs inside the last bucket
-      if (near) {
-        const float* bias = lut + kLutLow + (qi - j0);
+      mbar_arrive1(s.bsc);
+      if (any) {
+        const int d = qi - j0;  // distances d, d - 1, .. d - 63
+        int rank = 0;
+        bool flat = true;
+        if (MODE) {
+          rank = bias.rank_of(d);
+          flat = __all_sync(0xffffffffu, rank == bias.rank_of(d - 63));
+        }
+        if (flat) {
+          const float c = (MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f) + LD.x;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) v[i] = fmaf(v[i], kScaleLog2, bias[-i] + LD.x);
-      } else {
-        const float c = (MODE ? lut[kLutLow + a.last] : 0.f) + LD.x;
+          for (int i = 0; i < 64; i += 2) ffma2(v[i], v[i + 1], v[i], v[i + 1], kScaleLog2, kScaleLog2, c, c);
+        } else {
+          const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) ffma2(v[i], v[i + 1], v[i], v[i + 1], kScaleLog2, kScaleLog2, c, c);
+          for (int i = 0; i < 64; ++i) v[i] = fmaf(v[i], kScaleLog2, at[-i] + LD.x);
+        }
+        if (!__all_sync(0xffffffffu, (see0 & see1) == 0xffffffffu)) {
+          hide32(v, see0);
+          hide32(v + 32, see1);
+        }
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          v[i] = ex2_approx(v[i]);  // P
+          v[i + 1] = ex2_approx(v[i + 1]);
+          float d0, d1;
+          fadd2(d0, d1, v[64 + i], v[65 + i], LD.y, LD.y);
+          fmul2(v[64 + i], v[65 + i], v[i], v[i + 1], d0, d1);  // dS
+        }
+        if (MODE == 2) {
+          if (flat) {
+            float s4[4] = {0.f, 0.f, 0.f, 0.f}, p4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+              fadd2(s4[0], s4[1], s4[0], s4[1], v[64 + i], v[65 + i]);
+              fadd2(s4[2], s4[3], s4[2], s4[3], v[66 + i], v[67 + i]);
+              fadd2(p4[0], p4[1], p4[0], p4[1], v[i], v[i + 1]);
+              fadd2(p4[2], p4[3], p4[2], p4[3], v[i + 2], v[i + 3]);
+            }
+            const float x = (s4[0] + s4[1]) + (s4[2] + s4[3]), p = (p4[0] + p4[1]) + (p4[2] + p4[3]);
+            if (__all_sync(0xffffffffu, rank == a.ranks - 1)) {
+              farS += x;
+              farP += p;
+            } else {
+              put(rank, x, p);
+            }
+          } else {
+            float runS = 0.f, runP = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // bit i: column 32 c + i ends its bucket (its distance is the bucket's first).  From the
+              // bitmap, distances low .. low + 31, the reverse of the columns' order.
+              const int low = d - 32 * c - 31;
+              const int wd = low >> 5;  // floor division
+              const uint32_t w0 = wd >= 0 && wd < nend ? ends[wd] : 0u;
+              const uint32_t w1 = wd + 1 >= 0 && wd + 1 < nend ? ends[wd + 1] : 0u;
+              const uint32_t stop = __brev(__funnelshift_r(w0, w1, low & 31));
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                runS += v[64 + 32 * c + i];
+                runP += v[32 * c + i];
+                if ((stop >> i) & 1u) {
+                  put(rank, runS, runP);
+                  runS = runP = 0.f;
+                  --rank;
+                }
+              }
+            }
+            if (rank >= 0) put(rank, runS, runP);  // (below 0: only columns behind the diagonal are left)
+          }
+        }
       }
-      if (sink || !(j0 + 63 <= q0 && (q0 + 127 - j0 < a.window || j0 + 64 <= a.sinks))) {
-        const int hi = qi - j0, lo = hi - a.window + 1, sk = a.sinks - j0;
+      if (t > 0) {  // the previous dQ product reads dS
+        ok = warp_await(s.bo, (t - 1) & 1, err, DERR_ACC_WAIT, s.abort);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (!any) st_zero64_tmem(tdS + lane + 32 * g);
+      else st_row64_tmem(tdS + lane + 32 * g, v + 64);
+      if (sink && g == 0) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint32_t near_bits = sink ? 0u : ~bits_to(lo - 1 - 32 * c);
-          const uint32_t see = bits_to(hi - 32 * c) & (near_bits | bits_to(sk - 1 - 32 * c));
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((see >> i) & 1u)) v[32 * c + i] = -INFINITY;
+          st_row32_bf16(sinkP, r, 4 * c, v + 32 * c);
+          st_row32_bf16(sinkP + T128, r, 4 * c, v + 64 + 32 * c);
         }
+        fence_proxy_async_smem();
       }
-#pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        v[i] = ex2_approx(v[i]);  // P
-        v[i + 1] = ex2_approx(v[i + 1]);
-        float d0, d1;
-        fadd2(d0, d1, v[64 + i], v[65 + i], LD.y, LD.y);
-        fmul2(v[64 + i], v[65 + i], v[i], v[i + 1], d0, d1);  // dS
-      }
-      if (MODE == 2) {
-        if (sink) {  // distances start again, further away
-          flush();
-          rank = rank_of(qi);
-        }
-        if (near) {
-          // bit i: column i ends its bucket (distance qi - j0 - i is the bucket's first)
-          uint64_t stop = 0;
-          const int top = qi - j0;  // distance of column 0
-#pragma unroll
-          for (int i = 0; i < 64; i += 32) {
-            // distances top - i - 31 .. top - i, lowest first, from the bitmap; reversed
-            const int d = top - i - 31;
-            const int q = d >> 5, s = d & 31;  // floor division
-            const uint32_t w0 = q >= 0 && q < nend ? ends[q] : 0u;
-            const uint32_t w1 = q + 1 >= 0 && q + 1 < nend ? ends[q + 1] : 0u;
-            stop |= static_cast<uint64_t>(__brev(__funnelshift_r(w0, w1, s))) << i;
-          }
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            runS += v[64 + i];
-            runP += v[i];
-            if ((stop >> i) & 1u) {
-              flush();
-              --rank;
-            }
-          }
-        } else {
-          float s4[4] = {0.f, 0.f, 0.f, 0.f}, p4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            fadd2(s4[0], s4[1], s4[0], s4[1], v[64 + i], v[65 + i]);
-            fadd2(s4[2], s4[3], s4[2], s4[3], v[66 + i], v[67 + i]);
-            fadd2(p4[0], p4[1], p4[0], p4[1], v[i], v[i + 1]);
-            fadd2(p4[2], p4[3], p4[2], p4[3], v[i + 2], v[i + 3]);
-          }
-          runS += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          runP += (p4[0] + p4[1]) + (p4[2] + p4[3]);
-        }
-      }
-      if (t > 0) {  // the previous dQ product reads the dS tile
-        ok = warp_await(bo, (t - 1) & 1, err, DERR_ACC_WAIT, abort);
-        if (!ok) break;
-      }
-      if (sink) {
-        st_row32_bf16(sP, r, 0, v);
-        st_row32_bf16(sP, r, 4, v + 32);
-      }
-      st_row32_bf16(sdS, r, 0, v + 64);
-      st_row32_bf16(sdS, r, 4, v + 96);
-      fence_proxy_async_smem();
+      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive1(bp);
+      mbar_arrive1(s.bp);
     }
-    if (ok) ok = warp_await(bo, (nt - 1) & 1, err, DERR_ACC_WAIT, abort);
+    if (ok) ok = warp_await(s.bo, (nt - 1) & 1, err, DERR_ACC_WAIT, s.abort);
     tc_fence_after();
     if (ok) {
-      store_row64_or_zero(tQ + lane, dqkv + (row0 + qi) * ld + h * HD, 0.125f, qi < a.seq, qi < n);
-      if (sink_tile) {
-        float* part = ws_.far + (((static_cast<int64_t>(b) * a.heads + h) * nqb + qb) * a.sinks + r) * 128;
+      store_row32(tQ + lane + 32 * g, dqkv + (row0 + qi) * ld + h * HD + 32 * g, 0.125f, qi < a.seq, qi < n);
+      if (sink_tile) {  // dV | dK
+        float* part = ws_.far + (((static_cast<int64_t>(b) * a.heads + h) * nqb + qb) * a.sinks + r) * 128 + 64 * g;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // dV | dK
+        for (int c = 0; c < 2; ++c) {
           float x[32];
-          ld_row32((c < 2 ? tS : tP) + lane + 32 * (c & 1), x);
+          ld_row32((g ? tP : tS) + lane + 32 * c, x);
           if (r < a.sinks) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) store8(part + 32 * c + i, x + i);
@@ -787,57 +990,41 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
       }
     }
     if (MODE == 2) {
-      flush();
+      put(a.ranks - 1, farS, farP);
+      sync();
+      // thread r of each warpgroup: half of the ranks of row r, both warpgroups' columns
       float e = 0.f;  // the error of D: the row's dS sum to it instead of 0
-      for (int k = 0; k < a.ranks; ++k) e += accS[k * 128 + r];
-      for (int k = 0; k < a.ranks; ++k) {
-        const float x = accS[k * 128 + r] - e * accP[k * 128 + r];
-        accS[k * 128 + r] = qi < n ? x : 0.f;
+      for (int k = 0; k < a.ranks; ++k) e += accS[k * ROW_THREADS + r] + accS[k * ROW_THREADS + 128 + r];
+      sync();
+      for (int k = g; k < a.ranks; k += 2) {
+        const float p = __half2float(accP[k * ROW_THREADS + r]) + __half2float(accP[k * ROW_THREADS + 128 + r]);
+        const float x = (accS[k * ROW_THREADS + r] + accS[k * ROW_THREADS + 128 + r]) - e * p;
+        accS[k * ROW_THREADS + r] = qi < n ? x : 0.f;
       }
       sync();
-      for (int k = warp; k < a.ranks; k += 4) {
-        const float* row = accS + k * 128;
+      for (int k = warp; k < a.ranks; k += 8) {
+        const float* row = accS + k * ROW_THREADS;
         const float x = warp_sum((row[ln] + row[ln + 32]) + (row[ln + 64] + row[ln + 96]));
         if (ln == 0) tab[k] = x;
       }
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 256);
-  }
+  s.finish(warp, tmem);
 }
 
 // dK/dV CTA of 128 keys of one key/value head: iterations t = 0 .. group * nq - 1
-// over the 64-query blocks that see them, one query head after the other.
+// over the 128-query blocks that see them, one query head after the other.
 template <int MODE>
-__device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
-                               const CUtensorMap* td64, const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv,
-                               int item, int* err, uint8_t* sm) {
-  uint8_t* sK = sm;
-  uint8_t* sV = sm + T128;
-  uint8_t* sQ = sm + 2 * T128;   // two slots of Q (64 rows) | dO (64 rows)
-  uint8_t* sPt = sm + 4 * T128;  // 128 keys x 64 queries
-  uint8_t* sdSt = sm + 5 * T128; // 128 keys x 64 queries
-  float* sL = reinterpret_cast<float*>(sm + BWD_LD);  // [2][64] -LSE (log2 domain)
-  float* sD = sL + 128;                               // [2][64] -D
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + BWD_BAR);
-  uint64_t *bkv = bar, *bq = bar + 1, *bs = bar + 3, *bsc = bar + 4, *bp = bar + 5, *bo = bar + 6, *bfin = bar + 7,
-           *bld = bar + 8,  // bld[2]: the LSE and D of a block are in their slot (64 writers)
-           *brow = bar + 10;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 12);
-  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  float* val = reinterpret_cast<float*>(sm + BWD_VAL);
-  float* lut = reinterpret_cast<float*>(sm + BWD_LUT);
-
-  const int r = threadIdx.x, warp = r >> 5, ln = r & 31;
+__device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td,
+                               const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int stages,
+                               int* err, uint8_t* sm) {
+  BwdSmem s(sm, stages, a);
+  const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int kvh = item % a.kv_heads;
   const int b = (item / a.kv_heads) % a.nseq;
   const int kb = item / (a.kv_heads * a.nseq);  // by rising key: in a full causal pass the longest first
   const int group = a.heads / a.kv_heads, h0 = kvh * group;
-  const int k0 = kb * 128, kr = k0 + r;
+  const int k0 = kb * 128;
   const int64_t row0 = static_cast<int64_t>(b) * a.seq;
   const int D = a.heads * HD;
   const int64_t ld = static_cast<int64_t>(a.heads + 2 * a.kv_heads) * HD;
@@ -847,212 +1034,207 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
   griddep_wait();
   const int n = seq_len(a, b);
   if (k0 >= n) {  // a block of padding
-    if (kr < a.seq && r < 128) {
-      zero_row64(dqkv + (row0 + kr) * ld + kcol);
-      zero_row64(dqkv + (row0 + kr) * ld + vcol);
-    }
+    if (tid < ROW_THREADS && k0 + (tid & 127) < a.seq)
+      zero_row64(dqkv + (row0 + k0 + (tid & 127)) * ld + (tid < 128 ? kcol : vcol));
     return;
   }
   // the queries of this block: those whose window reaches it, and, for the sinks' block, the rest of
   // the 128-query blocks whose window reaches it (the dQ CTAs of the others account for the sinks)
-  const int i0 = k0 / 64;
   const int imax = min(n - 1, kb == 0 && a.sinks > 0 ? first_far_block(a.window) * 128 - 1 : k0 + 127 + a.window - 1);
-  const int nq = imax / 64 - i0 + 1;
+  const int nq = imax / 128 - kb + 1;
   const int niter = group * nq;
 
-  if (r == 0) {
-    prefetch_tmap(tq64);
-    prefetch_tmap(tq128);
-    prefetch_tmap(td64);
-    for (int i = 0; i < 4; ++i) mbar_init(&bar[i], 1);
-    mbar_init(bsc, 128);
-    mbar_init(bp, 128);
-    mbar_init(bo, 1);
-    mbar_init(bfin, 1);
-    mbar_init(&bld[0], 64);
-    mbar_init(&bld[1], 64);
-    mbar_init(brow, 128);
-    *abort = 0;
-    fence_barrier_init();
-  }
-  if (warp == 0) {
-    tmem_alloc(tslot, 256);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
-  const uint32_t tS = tmem, tP = tmem + 64, tV = tmem + 128, tK = tmem + 192;
+  const uint32_t tmem = s.start(warp, tq, td);
+  // S^T at 0, dP^T at 128, dV at 256, dK at 320, P^T (bf16) at 384, dS^T at 448
+  const uint32_t tS = tmem, tdP = tmem + 128, tV = tmem + 256, tK = tmem + 320, tP = tmem + 384, tdS = tmem + 448;
 
-  if (warp == 4) {  // ---- issuer ----
-    constexpr uint32_t idSP = mma_idesc_bf16(128, 64, false, false);
-    constexpr uint32_t idKV = mma_idesc_bf16(128, 64, false, true);
-    int nqi[2] = {0, 0};
-    if (ln == 0) {
-      mbar_arrive_expect_tx(bkv, 2 * T128);
-      tma_load_3d(sK, tq128, kcol, k0, b, bkv);
-      tma_load_3d(sV, tq128, vcol, k0, b, bkv);
-    }
-    auto load_q = [&](int t) {
-      const int s = t & 1;
-      if (ln == 0) {
-        const int h = h0 + t / nq, q0 = (i0 + t % nq) * 64;
-        mbar_arrive_expect_tx(&bq[s], 2 * T64);
-        tma_load_3d(sQ + s * T128, tq64, h * HD, q0, b, &bq[s]);
-        tma_load_3d(sQ + s * T128 + T64, td64, h * HD, q0, b, &bq[s]);
+  if (warp >= 8) {
+    give_registers();
+    if (warp == 10) {  // ---- loader ----
+      if (elect_one()) {
+        mbar_arrive_expect_tx(s.b0, 2 * T128);
+        tma_load_3d(s.a, tq, kcol, k0, b, s.b0);
+        tma_load_3d(s.b, tq, vcol, k0, b, s.b0);
+        RingPos lp;
+        int t = 0, lh = h0, lq = kb;
+        for (; t < niter; ++t) {
+          if (t >= stages && !lane_await(&s.empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
+          uint8_t* dst = s.ring + lp.stage * BWD_STAGE;
+          uint64_t* full = &s.full[lp.stage];
+          mbar_arrive_expect_tx(full, 2 * T128 + 128 * 8);
+          tma_load_3d(dst, tq, lh * HD, lq * 128, b, full);
+          tma_load_3d(dst + T128, td, lh * HD, lq * 128, b, full);
+          bulk_load(s.ld + lp.stage * 128, ws_.ld + (static_cast<int64_t>(b) * a.heads + lh) * seqpad + lq * 128,
+                    128 * 8, full);
+          if (++lq == kb + nq) {
+            lq = kb;
+            ++lh;
+          }
+          lp.next(stages);
+        }
+        drain_copies(s, t, stages, err);
       }
-      ++nqi[s];
-    };
-    for (int t = 0; t < 2 && t < niter; ++t) load_q(t);
-    auto issue_sp = [&](int t) {  // S^T = K Q_t^T, dP^T = V dO_t^T
-      uint8_t* qd = sQ + (t & 1) * T128;
-      const int left = n - (i0 + t % nq) * 64;
-      if (left < 64) {  // padded queries: P = dS = 0, the rows themselves may be anything
-        zero_rows(qd, left, 64, ln);
-        zero_rows(qd + T64, left, 64, ln);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      const uint32_t k = smem_u32(sK), v = smem_u32(sV), q = smem_u32(qd), dO = smem_u32(qd + T64);
-      if (ln == 0) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, kdesc(k, kk), kdesc(q, kk), idSP, kk ? 1u : 0u);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tP, kdesc(v, kk), kdesc(dO, kk), idSP, kk ? 1u : 0u);
-        tc_commit(bs);
-      }
-    };
-    bool go = warp_await(bkv, 0, err, DERR_MMA_WAIT, abort) && warp_await(&bq[0], 0, err, DERR_MMA_WAIT, abort);
-    if (go) {
-      tc_fence_after();
-      issue_sp(0);
-    }
-    for (int t = 0; t < niter && go; ++t) {
-      if (t + 1 < niter) {  // the next block's S^T, dP^T as soon as the rows have read block t's
-        if (!warp_await(&bq[(t + 1) & 1], ((t + 1) >> 1) & 1, err, DERR_MMA_WAIT, abort)) break;
-        if (!warp_await(bsc, t & 1, err, DERR_MMA_WAIT, abort)) break;
+      __syncwarp();
+    } else if (warp == 8) {  // ---- S^T = K Q_t^T, dP^T = V dO_t^T ----
+      constexpr uint32_t idSP = mma_idesc_bf16(128, 128, false, false);
+      const uint64_t k = kdesc0(smem_u32(s.a)), v = kdesc0(smem_u32(s.b)), qd = kdesc0(smem_u32(s.ring));
+      RingPos sp;
+      int qb = kb;
+      bool go = warp_await(s.b0, 0, err, DERR_MMA_WAIT, s.abort);
+      for (int t = 0; t < niter && go; ++t) {
+        go = warp_await(&s.full[sp.stage], sp.parity, err, DERR_MMA_WAIT, s.abort);
+        const int left = n - qb * 128;
+        if (left < 128) {  // padded queries: P = dS = 0, the rows themselves may be anything
+          uint8_t* at = s.ring + sp.stage * BWD_STAGE;
+          zero_rows(at, left, 128, ln);
+          zero_rows(at + T128, left, 128, ln);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint64_t q = qd + sp.stage * (BWD_STAGE / 16), dO = q + T128 / 16;
+        if (t > 0) go = go && warp_await(s.bsc, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // block t-1's read out
+        if (!go) break;
         tc_fence_after();
-        issue_sp(t + 1);
-      }
-      if (!warp_await(bp, t & 1, err, DERR_MMA_WAIT, abort)) break;  // P^T, dS^T of block t written
-      tc_fence_after();
-      if (ln == 0) {
-        const uint32_t pt = smem_u32(sPt), dst = smem_u32(sdSt), q = smem_u32(sQ + (t & 1) * T128), dO = q + T64;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tV, kdesc(pt, kk), mndesc(dO, kk), idKV, (t | kk) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, k + kk * kKStep, q + kk * kKStep, idSP, kk ? 1u : 0u);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tK, kdesc(dst, kk), mndesc(q, kk), idKV, (t | kk) ? 1u : 0u);
-        tc_commit(bo);
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tdP, v + kk * kKStep, dO + kk * kKStep, idSP, kk ? 1u : 0u);
+          tc_commit(s.bs);
+        }
+        if (++qb == kb + nq) qb = kb;
+        sp.next(stages);
       }
-      if (t + 2 < niter) {  // block t's slot, once dV, dK of block t are done
-        if (!warp_await(bo, t & 1, err, DERR_MMA_WAIT, abort)) break;
-        load_q(t + 2);
+      if (elect_one()) drain_products(&s.bfin[0], err);
+      __syncwarp();
+    } else if (warp == 9) {  // ---- dV += P^T dO_t, dK += dS^T Q_t ----
+      constexpr uint32_t idKV = mma_idesc_bf16(128, 64, false, true);
+      const uint64_t qd = mndesc0(smem_u32(s.ring));
+      RingPos gp_;
+      for (int t = 0; t < niter; ++t) {
+        const uint64_t q = qd + gp_.stage * (BWD_STAGE / 16), dO = q + T128 / 16;
+        if (!warp_await(s.bp, t & 1, err, DERR_MMA_WAIT, s.abort)) break;  // P^T, dS^T of block t written
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) tc_mma_f16_ta(tV, tP + 8 * kk, dO + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) tc_mma_f16_ta(tK, tdS + 8 * kk, q + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
+          tc_commit(s.bo);
+          tc_commit(&s.empty[gp_.stage]);
+        }
+        gp_.next(stages);
       }
+      if (elect_one()) drain_products(&s.bfin[1], err);
+      __syncwarp();
     }
-    if (ln == 0) {
-      tc_commit(bfin);
-      mbar_wait_bounded(bfin, 0, err, DERR_DRAIN_WAIT);
-      for (int s = 0; s < 2; ++s)
-        if (nqi[s]) mbar_wait_bounded(&bq[s], (nqi[s] - 1) & 1, err, DERR_DRAIN_WAIT);
-      mbar_wait_bounded(bkv, 0, err, DERR_DRAIN_WAIT);
-    }
-    __syncwarp();
   } else {  // ---- rows ----
-    const uint32_t lane = static_cast<uint32_t>(warp * 32) << 16;
-    // -LSE and -D of a block's 64 queries, each read one block ahead; block t sits in slot t & 1 and is
-    // published by the (t >> 1)-th phase of bld[t & 1]
-    auto ld_at = [&](int t) {
-      return ws_.ld[(static_cast<int64_t>(b) * a.heads + h0 + t / nq) * seqpad + (i0 + t % nq) * 64 + r];
-    };
-    if (r < 64) {
-      const float2 x = ld_at(0);
-      sL[r] = x.x;
-      sD[r] = x.y;
-      mbar_arrive1(&bld[0]);
-    }
-    RowSync sync{brow, err, abort, 0u};
+    take_registers();
+    const int g = warp >> 2, r = tid & 127, kr = k0 + r;
+    const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    RowSync sync{s.brow, err, s.abort, 0u};
+    const Bias& bias = s.bias;
+    RingPos rp;
     bool ok = true;
+    int hq = h0, qb = kb;
     for (int t = 0; t < niter; ++t) {
-      const int q0 = (i0 + t % nq) * 64, s = t & 1;
-      if (MODE && t % nq == 0) ok = fill_lut(a, h0 + t / nq, lut, val, r, sync);
-      if (ok) ok = warp_await(&bld[s], (t >> 1) & 1, err, DERR_ACC_WAIT, abort);
-      float2 next = make_float2(0.f, 0.f);
-      if (r < 64 && t + 1 < niter) next = ld_at(t + 1);
-      if (ok) ok = warp_await(bs, t & 1, err, DERR_ACC_WAIT, abort);
+      if (MODE && qb == kb) ok = s.bias.fill(a, hq, s.val, tid, sync);
+      const int q0 = qb * 128 + 64 * g;  // the query of this thread's column 0
+      uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
+      if (!(q0 >= k0 + 127 && q0 + 63 - k0 < a.window)) {  // some pair may be hidden
+        const int lo = kr - q0, hi = kr < a.sinks ? 63 : lo + a.window - 1;
+        see0 = bits_to(hi) & ~bits_to(lo - 1);
+        see1 = bits_to(hi - 32) & ~bits_to(lo - 33);
+      }
+      const bool any = __any_sync(0xffffffffu, (see0 | see1) != 0u);
+      // the block's -lse and -D came with its tiles
+      if (ok) ok = warp_await(&s.full[rp.stage], rp.parity, err, DERR_ACC_WAIT, s.abort);
+      if (ok) ok = warp_await(s.bs, t & 1, err, DERR_ACC_WAIT, s.abort);
       if (!ok) break;
       tc_fence_after();
       float v[128];  // S^T (64 columns), then dP^T (64 columns), one round trip
-      {
-        const uint32_t at[4] = {tS + lane, tS + lane + 32, tP + lane, tP + lane + 32};
+      if (any) {
+        const uint32_t c = lane + 64 * g;
+        const uint32_t at[4] = {tS + c, tS + c + 32, tdP + c, tdP + c + 32};
         ld_rows<4>(at, v);
       }
       tc_fence_before();
-      mbar_arrive1(bsc);
-      const float* L = sL + s * 64;
-      const float* Dq = sD + s * 64;
-      if (MODE && q0 - (k0 + 127) < a.last) {
-        const float* bias = lut + kLutLow + (q0 - kr);
+      mbar_arrive1(s.bsc);
+      if (any) {
+        const float4* LD = reinterpret_cast<const float4*>(s.ld + rp.stage * 128 + 64 * g);  // two queries each
+        const int d = q0 - kr;  // distances d .. d + 63
+        bool flat = true;
+        if (MODE) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d + 63));
+        if (flat) {
+          const float c = MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f;
 #pragma unroll
-        for (int q = 0; q < 64; ++q) v[q] = fmaf(v[q], kScaleLog2, bias[q] + L[q]);
-      } else {
-        const float c = MODE ? lut[kLutLow + a.last] : 0.f;
+          for (int q = 0; q < 64; q += 2) {
+            const float4 x = LD[q / 2];
+            float l0 = x.x, l1 = x.z;
+            if (MODE) fadd2(l0, l1, l0, l1, c, c);
+            ffma2(v[q], v[q + 1], v[q], v[q + 1], kScaleLog2, kScaleLog2, l0, l1);
+            fadd2(v[64 + q], v[65 + q], v[64 + q], v[65 + q], x.y, x.w);
+          }
+        } else {
+          const float* at = bias.value + Bias::kLow + d;
+#pragma unroll
+          for (int q = 0; q < 64; q += 2) {
+            const float4 x = LD[q / 2];
+            float l0, l1;
+            fadd2(l0, l1, x.x, x.z, at[q], at[q + 1]);
+            ffma2(v[q], v[q + 1], v[q], v[q + 1], kScaleLog2, kScaleLog2, l0, l1);
+            fadd2(v[64 + q], v[65 + q], v[64 + q], v[65 + q], x.y, x.w);
+          }
+        }
+        if (!__all_sync(0xffffffffu, (see0 & see1) == 0xffffffffu)) {
+          hide32(v, see0);
+          hide32(v + 32, see1);
+        }
 #pragma unroll
         for (int q = 0; q < 64; q += 2) {
-          float l0 = L[q], l1 = L[q + 1];
-          if (MODE) fadd2(l0, l1, l0, l1, c, c);
-          ffma2(v[q], v[q + 1], v[q], v[q + 1], kScaleLog2, kScaleLog2, l0, l1);
+          v[q] = ex2_approx(v[q]);  // P^T
+          v[q + 1] = ex2_approx(v[q + 1]);
+          fmul2(v[64 + q], v[65 + q], v[q], v[q + 1], v[64 + q], v[65 + q]);  // dS^T
         }
       }
-      if (!(q0 >= k0 + 127 && q0 + 63 - k0 < a.window)) {  // some pair may be hidden
-        const int lo = kr - q0, hi = kr < a.sinks ? 63 : lo + a.window - 1;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t see = bits_to(hi - 32 * c) & ~bits_to(lo - 1 - 32 * c);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((see >> i) & 1u)) v[32 * c + i] = -INFINITY;
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 64; q += 2) {
-        v[q] = ex2_approx(v[q]);  // P^T
-        v[q + 1] = ex2_approx(v[q + 1]);
-        float d0, d1;
-        fadd2(d0, d1, v[64 + q], v[65 + q], Dq[q], Dq[q + 1]);
-        fmul2(v[64 + q], v[65 + q], v[q], v[q + 1], d0, d1);  // dS^T
-      }
-      if (t > 0) {  // the previous dV, dK products read the P^T and dS^T tiles
-        ok = warp_await(bo, (t - 1) & 1, err, DERR_ACC_WAIT, abort);
+      if (t > 0) {  // the previous dV, dK products read P^T and dS^T
+        ok = warp_await(s.bo, (t - 1) & 1, err, DERR_ACC_WAIT, s.abort);
         if (!ok) break;
+        tc_fence_after();
       }
-      st_row32_bf16(sPt, r, 0, v);
-      st_row32_bf16(sPt, r, 4, v + 32);
-      st_row32_bf16(sdSt, r, 0, v + 64);
-      st_row32_bf16(sdSt, r, 4, v + 96);
-      if (r < 64 && t + 1 < niter) {  // the next block's
-        sL[(s ^ 1) * 64 + r] = next.x;
-        sD[(s ^ 1) * 64 + r] = next.y;
-        mbar_arrive1(&bld[s ^ 1]);
+      if (!any) {
+        st_zero64_tmem(tP + lane + 32 * g);
+        st_zero64_tmem(tdS + lane + 32 * g);
+      } else {
+        st_row64_tmem(tP + lane + 32 * g, v);
+        st_row64_tmem(tdS + lane + 32 * g, v + 64);
       }
-      fence_proxy_async_smem();
+      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive1(bp);
+      mbar_arrive1(s.bp);
+      rp.next(stages);
+      if (++qb == kb + nq) {
+        qb = kb;
+        ++hq;
+      }
     }
-    if (ok) ok = warp_await(bo, (niter - 1) & 1, err, DERR_ACC_WAIT, abort);
+    if (ok) ok = warp_await(s.bo, (niter - 1) & 1, err, DERR_ACC_WAIT, s.abort);
     tc_fence_after();
     if (ok) {
-      // the sinks' rows go on to the finish kernel, where query blocks far from them add to them
+      // warpgroup 0 stores dV, warpgroup 1 dK.  The sinks' rows go on to the finish kernel, where
+      // query blocks far from them add to them.
       const bool on = ws_.far && kr < a.sinks && kr < n;
-      __nv_bfloat16* dst = dqkv + (row0 + kr) * ld;
-      store_row64_or_zero(tK + lane, dst + kcol, 0.125f, kr < a.seq && !on, kr < n);
-      store_row64_or_zero(tV + lane, dst + vcol, 1.0f, kr < a.seq && !on, kr < n);
-      if (ws_.far && kb == 0) {
-        float* part = ws_.base + ((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + r) * 128;
+      const uint32_t acc = (g ? tK : tV) + lane;
+      __nv_bfloat16* dst = dqkv + (row0 + kr) * ld + (g ? kcol : vcol);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // dV | dK
+      for (int c = 0; c < 2; ++c)
+        store_row32(acc + 32 * c, dst + 32 * c, g ? 0.125f : 1.f, kr < a.seq && !on, kr < n);
+      if (ws_.far && kb == 0) {
+        float* part = ws_.base + ((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + r) * 128 + 64 * g;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // dV | dK
           float x[32];
-          ld_row32((c < 2 ? tV : tK) + lane + 32 * (c & 1), x);
+          ld_row32(acc + 32 * c, x);
           if (on) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) store8(part + 32 * c + i, x + i);
@@ -1061,33 +1243,22 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       }
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 256);
-  }
+  s.finish(warp, tmem);
 }
 
 // One launch for both kinds, the dK/dV CTAs first (they have more to do).
 template <int MODE>
-__global__ void __maxnreg__(168) attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq64,
-                                                        const __grid_constant__ CUtensorMap tq128,
-                                                        const __grid_constant__ CUtensorMap td64,
-                                                        const __grid_constant__ CUtensorMap td128,
-                                                        const __grid_constant__ WindowArgs a,
-                                                        const __grid_constant__ WindowScratch ws_,
-                                                        __nv_bfloat16* __restrict__ dqkv, int n_dkv, int* err) {
+__global__ void __launch_bounds__(WIN_THREADS, 1)
+    attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap td,
+                           const __grid_constant__ WindowArgs a, const __grid_constant__ WindowScratch ws_,
+                           __nv_bfloat16* __restrict__ dqkv, int n_dkv, int stages, int* err) {
   extern __shared__ __align__(1024) uint8_t sm[];
-  if (reinterpret_cast<uintptr_t>(sm) & 1023u) {
-    if (threadIdx.x == 0) atomicExch(err, DERR_ALIGN);
-    return;
-  }
+  if (misaligned(sm, err)) return;
   const int x = static_cast<int>(blockIdx.x);
   if (x < n_dkv)
-    window_bwd_dkv<MODE>(a, &tq64, &tq128, &td64, ws_, dqkv, x, err, sm);
+    window_bwd_dkv<MODE>(a, &tq, &td, ws_, dqkv, x, stages, err, sm);
   else
-    window_bwd_dq<MODE>(a, &tq64, &tq128, &td128, ws_, dqkv, x - n_dkv, err, sm);
+    window_bwd_dq<MODE>(a, &tq, &td, ws_, dqkv, x - n_dkv, stages, err, sm);
 }
 
 // Blocks 0 .. n_sink-1: one sink key of one (sequence, key/value head); thread c
@@ -1249,19 +1420,23 @@ WindowScratch window_scratch(void* base, int nseq, int seq, int heads, int windo
   return w;
 }
 
-int fwd_smem(const WindowArgs& a) { return FWD_LUT + (a.ranks ? lut_words(a.last) * 4 : 0); }
-int bwd_smem(const WindowArgs& a, bool grad) {
-  int s = BWD_LUT + (a.ranks ? lut_words(a.last) * 4 : 0);
-  if (grad) s += 2 * a.ranks * 128 * 4 + (a.last / 32 + 1) * 4;
+constexpr int kMaxSmem = 227 * 1024;
+int fwd_smem(const WindowArgs& a) { return FWD_BIAS + (a.ranks ? Bias::bytes(a.last) : 0); }
+int bwd_smem(const WindowArgs& a, bool grad, int stages) {
+  int s = BWD_RING + stages * BWD_STAGE + BWD_FIXED + (a.ranks ? Bias::bytes(a.last) : 0);
+  if (grad) s += a.ranks * ROW_THREADS * 6 + (a.last / 32 + 1) * 4;
   return s;
 }
+static_assert(FWD_BIAS + Bias::bytes(kMaxDistance) <= kMaxSmem, "the largest table fits beside the forward's tiles");
+static_assert(BWD_RING + 2 * BWD_STAGE + BWD_FIXED + Bias::bytes(kMaxDistance) + kMaxBuckets * ROW_THREADS * 6 +
+                      (kMaxDistance / 32 + 1) * 4 <= kMaxSmem,
+              "the largest table's sums fit beside two stages");
 
 int prepare_attention_window() {
   static std::atomic<unsigned long long> done{0};
   return once_per_device(done, []() -> int {
-    constexpr int most = 227 * 1024;
     auto set = [](const void* f) {
-      return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     };
     const void* all[] = {reinterpret_cast<const void*>(attn_window_fwd_kernel<false>),
                          reinterpret_cast<const void*>(attn_window_fwd_kernel<true>),
@@ -1314,7 +1489,7 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
   CUtensorMap tq;
   if (!make_tmap(&tq, qkv, static_cast<int64_t>(heads + 2 * kv_heads) * HD, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_fwd: tensor map creation failed");
-  const int grid = ((seq + 127) / 128) * heads * nseq;
+  const int grid = ((seq + 255) / 256) * heads * nseq;
   (void)launch_k<true>(a.ranks ? attn_window_fwd_kernel<true> : attn_window_fwd_kernel<false>, grid, WIN_THREADS,
                        fwd_smem(a), s, tq, a, static_cast<__nv_bfloat16*>(o), lse, err);
   return check_launch("attention_window_fwd");
@@ -1339,9 +1514,8 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   int* err = device_error_ptr();
   if (!err) return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: no device error word");
   const int64_t cols = static_cast<int64_t>(heads + 2 * kv_heads) * HD, D = static_cast<int64_t>(heads) * HD;
-  CUtensorMap tq64, tq128, td64, td128;
-  if (!make_tmap(&tq64, qkv, cols, seq, nseq, 64) || !make_tmap(&tq128, qkv, cols, seq, nseq, 128) ||
-      !make_tmap(&td64, dout, D, seq, nseq, 64) || !make_tmap(&td128, dout, D, seq, nseq, 128))
+  CUtensorMap tq, td;
+  if (!make_tmap(&tq, qkv, cols, seq, nseq, 128) || !make_tmap(&td, dout, D, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: tensor map creation failed");
   const WindowScratch w = window_scratch(scratch, nseq, seq, heads, window, sinks, dtable_acc ? a.ranks : 0);
   const int64_t prep = static_cast<int64_t>(nseq) * pad128(seq) * heads * 8;
@@ -1351,8 +1525,10 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   if (rc) return rc;
   const int nqb = (seq + 127) / 128, n_dkv = nqb * kv_heads * nseq, n_dq = nqb * heads * nseq;
   auto kern = dtable_acc ? attn_window_bwd_kernel<2> : (a.ranks ? attn_window_bwd_kernel<1> : attn_window_bwd_kernel<0>);
-  (void)launch_k<true>(kern, n_dkv + n_dq, WIN_THREADS, bwd_smem(a, dtable_acc != nullptr), s, tq64, tq128, td64, td128,
-                       a, w, static_cast<__nv_bfloat16*>(dqkv), n_dkv, err);
+  const bool grad = dtable_acc != nullptr;
+  const int stages = bwd_smem(a, grad, BWD_STAGES) <= kMaxSmem ? BWD_STAGES : 2;
+  (void)launch_k<true>(kern, n_dkv + n_dq, WIN_THREADS, bwd_smem(a, grad, stages), s, tq, td, a, w,
+                       static_cast<__nv_bfloat16*>(dqkv), n_dkv, stages, err);
   rc = check_launch("attention_window_bwd");
   if (rc) return rc;
   const int n_sink = w.far ? nseq * kv_heads * a.sinks : 0;
