@@ -81,18 +81,20 @@ __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
   return a.lens ? max(0, min(a.lens[b], a.seq)) : a.seq;
 }
 
-constexpr int ROW_THREADS = 256;  // two warpgroups of row threads
-// The issuer's warpgroup runs one of its four warps: whole warpgroups can pass
-// registers on.  Launched with 168 registers a thread (384 x 168 = 64512), the
-// row threads go up to 208 and the issuer's group down to 88
-// (256 x 208 + 128 x 88 = 64512).
-constexpr int WIN_THREADS = ROW_THREADS + 128;
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+// Row threads: two warpgroups in the forward kernel (a thread has a whole row of
+// a tile, so a row's maximum needs no exchange), four in the backward one (a
+// thread has a quarter of a row).  The issuers and the loader are warps of one
+// more warpgroup, since registers are passed on by whole warpgroups:
+//   forward   384 threads launched with 168 registers (64512); the row threads go
+//             up to 208, the others down to 88 (256 x 208 + 128 x 88 = 64512);
+//   backward  640 launched with 96 (61440); up to 104, down to 64
+//             (512 x 104 + 128 x 64 = 61440).
+constexpr int FWD_ROWS = 256, BWD_ROWS = 512;
+constexpr int FWD_THREADS = FWD_ROWS + 128, BWD_THREADS = BWD_ROWS + 128;
 
-// Bounded wait (2 s) that gives up at once after any earlier give-up in the
-// CTA.  A phase that is already complete costs one test: the issuer's waits are
-// on the way of every product.
+// Bounded waits (2 s; a wait that gives up sets the error word, after which the
+// others of the CTA give up at once).  A phase that is already complete costs
+// one test and one branch: the waits are on the way of every tile.
 __device__ __forceinline__ bool lane_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
   const uint32_t at = smem_u32(bar);
   if (mbar_try_wait(at, parity)) return true;
@@ -112,6 +114,18 @@ __device__ __forceinline__ bool lane_await(uint64_t* bar, uint32_t parity, int* 
 __device__ __forceinline__ bool warp_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
   return __all_sync(0xffffffffu, lane_await(bar, parity, err, code, abort));
 }
+// For the row threads, which carry on after a wait that gave up: what they then
+// compute is wrong and reported as such, but they read and write where they
+// would have, all later waits return at once, and no thread is left waiting for
+// one that has gone.
+struct RowWait {
+  int* err;
+  volatile int* abort;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) const {
+    (void)lane_await(bar, parity, err, DERR_ACC_WAIT, abort);
+    __syncwarp();
+  }
+};
 
 // One lane of a converged warp, always the same one.  Unlike a comparison with
 // the lane number it tells the compiler that what depends on it runs once per
@@ -130,27 +144,26 @@ __device__ __forceinline__ uint64_t kdesc0(uint32_t tile) { return kdesc(tile, 0
 __device__ __forceinline__ uint64_t mndesc0(uint32_t tile) { return mndesc(tile, 0); }
 constexpr uint64_t kKStep = 2, kMnStep = 128;
 
-// A barrier of the row threads on an mbarrier, with the bounded wait: a warp
-// that gave up a wait and left its loop cannot strand the others here.
+// A barrier of the row threads.
 struct RowSync {
   uint64_t* bar;
-  int* err;
-  volatile int* abort;
+  RowWait wait;
   uint32_t phase;
-  __device__ __forceinline__ bool operator()() {
+  __device__ __forceinline__ void operator()() {
     mbar_arrive1(bar);
-    return warp_await(bar, phase++ & 1u, err, DERR_ACC_WAIT, abort);
+    wait(bar, phase++ & 1u);
   }
 };
 
 // The bias of one head in shared memory: its value by distance in the log2
 // domain, and the rank of a distance's bucket.
 //   value[kLow + d], d = -kLow .. last + kHigh - 1: the last bucket's value from
-//   `last` on; a negative distance is masked, whatever is read for it.  A tile
-//   of 128 x 128 with a distance below `last` reads no further than last + 254.
+//   `last` on; a negative distance is masked, whatever is read for it.  Only a
+//   warp along some of whose rows the bucket changes reads it by column: 32 rows
+//   and up to 128 columns with a distance below `last`, so none of last + 158 on.
 //   rank[d], d = 0 .. last (rank_of clamps).
 struct Bias {
-  static constexpr int kLow = 128, kHigh = 256;
+  static constexpr int kLow = 128, kHigh = 160;
   float* value;
   uint8_t* rank;
   int last;
@@ -159,24 +172,23 @@ struct Bias {
   static __host__ __device__ constexpr int bytes(int last) { return value_words(last) * 4 + rank_bytes(last); }
 
   __device__ __forceinline__ int rank_of(int d) const { return rank[max(0, min(d, last))]; }
-  // Filled by the row threads (tid < ROW_THREADS); val: room for kMaxBuckets floats.
-  __device__ __forceinline__ bool fill(const WindowArgs& a, int head, float* val, int tid, RowSync& sync) {
-    bool ok = sync();  // nobody reads the previous head's any more
-    if (tid < a.ranks) {
-      const float x = a.table[static_cast<int64_t>(a.bucket[tid]) * a.heads + head];
-      val[tid] = x <= kHidden ? -INFINITY : x * kLog2e;
+  // Filled by the N row threads.
+  template <int N>
+  __device__ __forceinline__ void fill(const WindowArgs& a, int head, int tid, RowSync& sync) {
+    sync();  // nobody reads the previous head's any more
+    for (int x = tid; x < kLow + last + kHigh; x += N) {
+      const int d = max(0, min(x - kLow, last));
+      int k = 0, bucket = a.bucket[0];
+      for (int i = 1; i < a.ranks; ++i)
+        if (a.start[i] <= d) {
+          k = i;
+          bucket = a.bucket[i];
+        }
+      const float t = a.table[static_cast<int64_t>(bucket) * a.heads + head];
+      value[x] = t <= kHidden ? -INFINITY : t * kLog2e;
+      if (x >= kLow && x <= kLow + last) rank[d] = static_cast<uint8_t>(k);
     }
-    ok = sync() && ok;
-    for (int k = 0; k < a.ranks; ++k) {
-      const int from = k == 0 ? -kLow : a.start[k];
-      const int to = k + 1 < a.ranks ? a.start[k + 1] : a.last + kHigh;
-      const float x = val[k];
-      for (int d = from + tid; d < to; d += ROW_THREADS) {
-        value[kLow + d] = x;
-        if (d >= 0 && d <= a.last) rank[d] = static_cast<uint8_t>(k);
-      }
-    }
-    return sync() && ok;
+    sync();
   }
 };
 
@@ -192,19 +204,10 @@ __device__ __forceinline__ void hide32(float* v, uint32_t see) {
     if (!((see >> i) & 1u)) v[i] = -INFINITY;
 }
 
-// 64 values as bf16 into 32 tensor-memory columns (an A operand) of this thread's lane.
-__device__ __forceinline__ void st_row64_tmem(uint32_t taddr, const float* v) {
-  uint32_t u[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) u[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-  tmem_st32(taddr, u);
-}
-__device__ __forceinline__ void st_zero64_tmem(uint32_t taddr) {
-  uint32_t u[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) u[i] = 0u;
-  tmem_st32(taddr, u);
-}
+__device__ __forceinline__ void take_registers_fwd() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+__device__ __forceinline__ void give_registers_fwd() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+__device__ __forceinline__ void take_registers_bwd() { asm volatile("setmaxnreg.inc.sync.aligned.u32 104;"); }
+__device__ __forceinline__ void give_registers_bwd() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
 
 // Zero rows [from, to) of a tile of 128-byte rows, by one warp, for the async proxy.
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to, int lane) {
@@ -272,12 +275,11 @@ __device__ __forceinline__ bool misaligned(const uint8_t* sm, int* err) {
 constexpr int FWD_STAGES = 4;
 constexpr int FWD_RING = 2 * T128;
 constexpr int FWD_BAR = FWD_RING + FWD_STAGES * 2 * T128;
-constexpr int FWD_VAL = FWD_BAR + 256;
-constexpr int FWD_BIAS = FWD_VAL + kMaxBuckets * 4;
+constexpr int FWD_BIAS = FWD_BAR + 256;
 constexpr float kMaxStep = 8.f;
 
 template <bool BIAS>
-__global__ void __launch_bounds__(WIN_THREADS, 1)
+__global__ void __launch_bounds__(FWD_THREADS, 1)
     attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ WindowArgs a,
                            __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int* err) {
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -289,7 +291,6 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
            *bsc = bar + 16, *bp = bar + 18, *brow = bar + 20;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 21);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  float* val = reinterpret_cast<float*>(sm + FWD_VAL);
   Bias bias{reinterpret_cast<float*>(sm + FWD_BIAS), sm + FWD_BIAS + Bias::value_words(a.last) * 4, a.last};
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
   const int n = seq_len(a, b);
   if (q00 >= n) {  // nothing but padding
     const int qi = q00 + tid;
-    if (tid < ROW_THREADS && qi < a.seq) {
+    if (tid < FWD_ROWS && qi < a.seq) {
       zero_row64(out + (row0 + qi) * D + h * HD);
       lse[(row0 + qi) * a.heads + h] = -INFINITY;
     }
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
       mbar_init(&bsc[g], 128);
       mbar_init(&bp[g], 128);
     }
-    mbar_init(brow, ROW_THREADS);
+    mbar_init(brow, FWD_ROWS);
     *abort = 0;
     fence_barrier_init();
   }
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
   // S_g at 128 g, O_g at 256 + 64 g, P_g at 384 + 64 g
 
   if (warp >= 8) {
-    give_registers();
+    give_registers_fwd();
     if (warp == 10) {  // ---- loader ----
       if (elect_one()) {
         mbar_arrive_expect_tx(bq, two ? 2 * T128 : T128);
@@ -432,20 +433,23 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
       __syncwarp();
     }
   } else {  // ---- rows ----
-    take_registers();
+    take_registers_fwd();
     const int g = warp >> 2;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int q0 = q00 + 128 * g, qi = q0 + (tid & 127);
     const uint32_t tS = tmem + 128 * g + lane, tO = tmem + 256 + 64 * g + lane, tP = tmem + 384 + 64 * g + lane;
-    RowSync sync{brow, err, abort, 0u};
+    const RowWait wait{err, abort};
+    RowSync sync{brow, wait, 0u};
     float m = -INFINITY, l = 0.f;
-    bool ok = !BIAS || bias.fill(a, h, val, tid, sync);
+    if (BIAS) bias.fill<FWD_ROWS>(a, h, tid, sync);
     uint32_t count = 0;  // tiles done
     const int first_g = first[g], last_g = last[g];
-    for (int t = zero ? 0 : first_g; t <= last_g && ok; t = t < first_g ? first_g : t + 1) {
+    for (int t = zero ? 0 : first_g; t <= last_g; t = t < first_g ? first_g : t + 1) {
       const int j0 = tile(t) * 128, w = width(t);
-      ok = warp_await(&bs[g], count & 1, err, DERR_ACC_WAIT, abort);
-      if (!ok) break;
+      const int d = qi - j0;  // distances d, d - 1, .. d - 127
+      bool flat = true;
+      if (BIAS) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d - 127));
+      wait(&bs[g], count & 1);
       tc_fence_after();
       float sv[128];
       {
@@ -459,8 +463,7 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
       // same all along the row, or with the bias by distance already added
       float sc = kScaleLog2, cb = 0.f;
       if (BIAS) {
-        const int d = qi - j0;
-        if (__all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d - 127))) {
+        if (flat) {
           cb = bias.value[Bias::kLow + max(0, min(d, a.last))];
         } else {
           const float* at = bias.value + Bias::kLow + d;
@@ -470,10 +473,12 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
         }
       }
       if (__builtin_expect(w < 128 || !(j0 + 127 <= q0 && q0 + 127 - j0 < a.window), 0)) {  // some pair is hidden
-        const int hi = qi - j0, lo = hi - a.window + 1, sk = a.sinks - j0;
+        const int lo = d - a.window + 1, sk = a.sinks - j0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          hide32(sv + 32 * c, bits_to(hi - 32 * c) & (~bits_to(lo - 1 - 32 * c) | bits_to(sk - 1 - 32 * c)));
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t see = bits_to(d - 32 * c) & (~bits_to(lo - 1 - 32 * c) | bits_to(sk - 1 - 32 * c));
+          if (!__all_sync(0xffffffffu, see == 0xffffffffu)) hide32(sv + 32 * c, see);
+        }
       }
       float mx8[8];
 #pragma unroll
@@ -487,29 +492,31 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
       const float alpha = m == mn ? 1.f : ex2_approx(m - ms);
       m = mn;
       if (count > 0) {  // the previous O product reads P and writes O
-        ok = warp_await(&bo[g], (count - 1) & 1, err, DERR_ACC_WAIT, abort);
-        if (!ok) break;
+        wait(&bo[g], (count - 1) & 1);
         tc_fence_after();
       }
-      const float off = cb - ms;
-      float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      const f32x2 sc2 = pack2(sc, sc), off2 = pack2(cb - ms, cb - ms);
+      f32x2 rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (64 * c < w) {
-          float* pc = sv + 64 * c;
+          uint32_t u[32];
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
-            ffma2(pc[i], pc[i + 1], pc[i], pc[i + 1], sc, sc, off, off);
-            pc[i] = ex2_approx(pc[i]);
-            pc[i + 1] = ex2_approx(pc[i + 1]);
-            const int e = (i >> 1) & 3;
-            fadd2(rs8[2 * e], rs8[2 * e + 1], rs8[2 * e], rs8[2 * e + 1], pc[i], pc[i + 1]);
+          for (int i = 0; i < 32; ++i) {
+            float p0, p1;
+            unpack2(fma2(pack2(sv[64 * c + 2 * i], sv[64 * c + 2 * i + 1]), sc2, off2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            rs[i & 3] = add2(rs[i & 3], pack2(p0, p1));
+            u[i] = pack_bf16x2(p0, p1);
           }
-          st_row64_tmem(tP + 32 * c, pc);
+          tmem_st32(tP + 32 * c, u);
         }
       }
-      const float rs = ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
+      float r0, r1;
+      unpack2(add2(add2(rs[0], rs[1]), add2(rs[2], rs[3])), r0, r1);
       if (count > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // warp-uniform: tcgen05 loads/stores are per warp
+        const f32x2 al2 = pack2(alpha, alpha);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t u[32];
@@ -518,7 +525,7 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float a0, a1;
-            fmul2(a0, a1, __uint_as_float(u[i]), __uint_as_float(u[i + 1]), alpha, alpha);
+            unpack2(mul2(pack2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), al2), a0, a1);
             u[i] = __float_as_uint(a0);
             u[i + 1] = __float_as_uint(a1);
           }
@@ -526,25 +533,20 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
         }
       }
       tmem_st_wait();
-      l = l * alpha + rs;
+      l = l * alpha + (r0 + r1);
       tc_fence_before();
       mbar_arrive1(&bp[g]);
       ++count;
     }
-    if (ok && count > 0) ok = warp_await(&bo[g], (count - 1) & 1, err, DERR_ACC_WAIT, abort);
+    if (count > 0) wait(&bo[g], (count - 1) & 1);
     tc_fence_after();
-    if (ok && qi < a.seq && count == 0) {  // a second tile of padding
-      zero_row64(out + (row0 + qi) * D + h * HD);
-      lse[(row0 + qi) * a.heads + h] = -INFINITY;
-    }
-    if (ok && count > 0) {
-      // l = 0: a row that sees nothing (padding, or every bucket of its keys hidden)
-      const bool keep = qi < n && l != 0.f;
-      __nv_bfloat16* dst = out + (row0 + qi) * D + h * HD;
-      store_row32(tO, dst, 1.0f / l, qi < a.seq, keep);
-      store_row32(tO + 32, dst + 32, 1.0f / l, qi < a.seq, keep);
-      if (qi < a.seq) lse[(row0 + qi) * a.heads + h] = keep ? (m + log2f(l)) * kLn2 : -INFINITY;
-    }
+    // count = 0: a second tile of padding; l = 0: a row that sees nothing (padding, or every
+    // bucket of its keys hidden)
+    const bool keep = count > 0 && qi < n && l != 0.f;
+    __nv_bfloat16* dst = out + (row0 + qi) * D + h * HD;
+    store_row32(tO, dst, 1.0f / l, qi < a.seq, keep);
+    store_row32(tO + 32, dst + 32, 1.0f / l, qi < a.seq, keep);
+    if (qi < a.seq) lse[(row0 + qi) * a.heads + h] = keep ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
   tc_fence_before();
   __syncthreads();
@@ -608,52 +610,55 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
 
 // Both kinds of CTA work on 128 x 128 tiles: S and dP (or their transposes) take
 // 128 tensor-memory columns each, warpgroup g of the row threads has columns
-// 64 g .. 64 g + 63 of every row, and P, dS go back into tensor memory as bf16 A
+// 32 g .. 32 g + 31 of every row, and P, dS go back into tensor memory as bf16 A
 // operands.  With operands A from shared memory the two wide products keep the
 // 128 B a cycle of shared memory just busy (8 KB for 64 cycles of tensor work);
 // with A from tensor memory the three 64-wide ones need half of it.
-//   warp 8:  S, dP of tile t+1 as soon as the rows have read tile t's -> commit
+//   warp 16: S, dP of tile t+1 as soon as the rows have read tile t's -> commit
 //            bs.
-//   warp 9:  the gradient products of tile t once the rows wrote P, dS ->
+//   warp 17: the gradient products of tile t once the rows wrote P, dS ->
 //            commit bo, empty[stage].
-//   warp 10: the copies; a tile into the ring once its stage is empty.
+//   warp 18: the copies; a tile into the ring once its stage is empty.
 //   rows:    wait bs; read S, dP; arrive bsc; the elementwise gradient; wait
 //            bo of tile t-1 (it reads P, dS); write them; arrive bp.
-constexpr int BWD_STAGE = 2 * T128;
-constexpr int BWD_STAGES = 3;  // at most (2 where a large table's sums need the room)
-constexpr int BWD_RING = 2 * T128;
-// behind the ring: -lse log2(e), -D of the stages' queries (dK/dV), barriers, bias
-constexpr int BWD_LD_BYTES = BWD_STAGES * 128 * 8;
-constexpr int BWD_FIXED = BWD_LD_BYTES + 256 + kMaxBuckets * 4;
+constexpr int BWD_ISSUER = BWD_ROWS / 32;  // the issuers' first warp
+// dK/dV: a ring of three stages of Q | dO | -lse, -D of a query block (all of
+// which the last products of the block need).  dQ: a ring of `stages` (3, or 2
+// where a large table's sums need the room) key tiles, which the dQ product
+// needs, and one of two value tiles, which are free as soon as dP is there.
+constexpr int DKV_STAGE = 2 * T128, DKV_STAGES = 3, DQ_V_STAGES = 2;
+constexpr int DKV_LD_BYTES = DKV_STAGES * 128 * 8;
+constexpr int BWD_BARS = 256;
 
 struct BwdSmem {
   uint8_t *a, *b, *ring;
   float2* ld;
-  uint64_t *full, *empty, *b0, *bs, *bo, *bfin, *bsc, *bp, *brow;
+  uint64_t *full, *empty, *full2, *empty2, *b0, *bs, *bo, *bfin, *bsc, *bp, *brow;
   uint32_t* tslot;
   volatile int* abort;
-  float* val;
   Bias bias;
   uint8_t* rest;
-  __device__ BwdSmem(uint8_t* sm, int stages, const WindowArgs& w) {
+  // ring_bytes, ld_bytes: what this kind of CTA needs of each
+  __device__ BwdSmem(uint8_t* sm, int ring_bytes, int ld_bytes, const WindowArgs& w) {
     a = sm;
     b = sm + T128;
-    ring = sm + BWD_RING;
-    uint8_t* p = ring + stages * BWD_STAGE;
+    ring = sm + 2 * T128;
+    uint8_t* p = ring + ring_bytes;
     ld = reinterpret_cast<float2*>(p);
-    full = reinterpret_cast<uint64_t*>(p + BWD_LD_BYTES);
-    empty = full + 3;
-    b0 = full + 6;
-    bs = full + 7;
-    bo = full + 8;
-    bfin = full + 9;  // two
-    bsc = full + 11;
-    bp = full + 12;
-    brow = full + 13;
-    tslot = reinterpret_cast<uint32_t*>(full + 14);
+    full = reinterpret_cast<uint64_t*>(p + ld_bytes);
+    full2 = full + 3;
+    b0 = full + 5;
+    bs = full + 6;
+    bo = full + 7;
+    bfin = full + 8;  // two
+    empty = full + 10;
+    empty2 = full + 13;
+    bsc = full + 15;
+    bp = full + 16;
+    brow = full + 17;
+    tslot = reinterpret_cast<uint32_t*>(full + 18);
     abort = reinterpret_cast<volatile int*>(tslot + 1);
-    val = reinterpret_cast<float*>(p + BWD_LD_BYTES + 256);
-    uint8_t* t = p + BWD_FIXED;
+    uint8_t* t = p + ld_bytes + BWD_BARS;
     bias = Bias{reinterpret_cast<float*>(t), t + Bias::value_words(w.last) * 4, w.last};
     rest = t + (w.ranks ? Bias::bytes(w.last) : 0);
   }
@@ -661,10 +666,10 @@ struct BwdSmem {
     if (threadIdx.x == 0) {
       prefetch_tmap(m0);
       prefetch_tmap(m1);
-      for (int i = 0; i < 11; ++i) mbar_init(&full[i], 1);
-      mbar_init(bsc, ROW_THREADS);
-      mbar_init(bp, ROW_THREADS);
-      mbar_init(brow, ROW_THREADS);
+      for (int i = 0; i < 15; ++i) mbar_init(&full[i], 1);
+      mbar_init(bsc, BWD_ROWS);
+      mbar_init(bp, BWD_ROWS);
+      mbar_init(brow, BWD_ROWS);
       *abort = 0;
       fence_barrier_init();
     }
@@ -692,28 +697,36 @@ __device__ __forceinline__ void drain_products(uint64_t* bfin, int* err) {
   tc_commit(bfin);
   mbar_wait_bounded(bfin, 0, err, DERR_DRAIN_WAIT);
 }
-// The loader's (one lane): none of its `loaded` copies into the ring may still be landing.
-__device__ __forceinline__ void drain_copies(const BwdSmem& s, int loaded, int stages, int* err) {
+// The loader's (one lane): none of the last copies into a ring, `loaded` in all, may still be landing.
+__device__ __forceinline__ void drain_copies(uint64_t* full, int loaded, int stages, int* err) {
   for (int t = max(0, loaded - stages); t < loaded; ++t)
-    mbar_wait_bounded(&s.full[t % stages], (t / stages) & 1, err, DERR_DRAIN_WAIT);
-  mbar_wait_bounded(s.b0, 0, err, DERR_DRAIN_WAIT);
+    mbar_wait_bounded(&full[t % stages], (t / stages) & 1, err, DERR_DRAIN_WAIT);
 }
+
+// Row threads that keep sums for the table's gradient (a fixed number of bytes for each bucket).
+constexpr int kWideRanks = 32;
+__host__ __device__ constexpr int table_threads(int ranks) { return ranks <= kWideRanks ? BWD_ROWS : 256; }
 
 // MODE 0: no bias; 1: bias; 2: bias and its gradient.
 //
 // dQ CTA: 128 queries, the window's key tiles by rising key, the sinks' (64
 // wide) last.  For the gradient of the table each row thread adds its dS and P
-// by bucket into words of its own (no two threads share one): a tile along
-// whose row the bucket does not change adds one sum; elsewhere the running sum
-// is put down at the columns where a bucket ends.
+// by bucket into words of its own (no two threads share one).  Columns along
+// which the bucket does not change add one sum.  Elsewhere the running sums are
+// put down where a bucket ends: a bucket that begins and ends among the thread's
+// columns is met nowhere else, so its sums are stored; only the first and the
+// last are added to what is there.  With more than kWideRanks buckets the words
+// of four warpgroups do not fit into shared memory: two take 64 columns each.
 template <int MODE>
 __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td,
                               const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int stages,
                               int* err, uint8_t* sm) {
-  BwdSmem s(sm, stages, a);
-  float* accS = reinterpret_cast<float*>(s.rest);                             // [ranks][256]
-  __half* accP = reinterpret_cast<__half*>(accS + a.ranks * ROW_THREADS);     // [ranks][256]
-  uint32_t* ends = reinterpret_cast<uint32_t*>(accP + a.ranks * ROW_THREADS);  // bit d: d is its bucket's first
+  BwdSmem s(sm, (stages + DQ_V_STAGES) * T128, 0, a);
+  const int accs = MODE == 2 ? table_threads(a.ranks) : 0;            // row threads with words
+  float* row_e = reinterpret_cast<float*>(s.rest);                    // [4][128]
+  float* accS = row_e + BWD_ROWS;                                     // [ranks + 1][accs]
+  __half* accP = reinterpret_cast<__half*>(accS + (a.ranks + 1) * accs);  // [ranks + 1][accs]
+  uint32_t* ends = reinterpret_cast<uint32_t*>(accP + (a.ranks + 1) * accs);  // bit d: d is its bucket's first
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int nqb = (a.seq + 127) / 128;
@@ -743,30 +756,35 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
   const uint32_t tmem = s.start(warp, tq, td);
   // S at 0, dP at 128, dQ at 256, dS (bf16) at 320
   const uint32_t tS = tmem, tP = tmem + 128, tQ = tmem + 256, tdS = tmem + 320;
-  // the sinks' P and dS in shared memory: the stage behind the last tile's, free by then
-  uint8_t* sinkP = s.ring + (nt % stages) * BWD_STAGE;
+  uint8_t* ringV = s.ring + stages * T128;
+  // the sinks' P and dS in shared memory: the stages behind the last tile's, free by then
+  uint8_t *sinkP = s.ring + (nt % stages) * T128, *sinkdS = ringV + (nt % DQ_V_STAGES) * T128;
 
-  if (warp >= 8) {
-    give_registers();
-    if (warp == 10) {  // ---- loader ----
+  if (warp >= BWD_ISSUER) {
+    give_registers_bwd();
+    if (warp == BWD_ISSUER + 2) {  // ---- loader ----
       if (elect_one()) {
         mbar_arrive_expect_tx(s.b0, 2 * T128);
         tma_load_3d(s.a, tq, h * HD, q0, b, s.b0);
         tma_load_3d(s.b, td, h * HD, q0, b, s.b0);
-        RingPos lp;
+        RingPos kp, vp;
         int t = 0;
         for (; t < nt; ++t) {
-          if (t >= stages && !lane_await(&s.empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
-          uint8_t* dst = s.ring + lp.stage * BWD_STAGE;
-          mbar_arrive_expect_tx(&s.full[lp.stage], 2 * T128);
-          tma_load_3d(dst, tq, kcol, tile_key(t), b, &s.full[lp.stage]);
-          tma_load_3d(dst + T128, tq, vcol, tile_key(t), b, &s.full[lp.stage]);
-          lp.next(stages);
+          if (t >= stages && !lane_await(&s.empty[kp.stage], kp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
+          if (t >= DQ_V_STAGES && !lane_await(&s.empty2[vp.stage], vp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
+          mbar_arrive_expect_tx(&s.full[kp.stage], T128);
+          tma_load_3d(s.ring + kp.stage * T128, tq, kcol, tile_key(t), b, &s.full[kp.stage]);
+          mbar_arrive_expect_tx(&s.full2[vp.stage], T128);
+          tma_load_3d(ringV + vp.stage * T128, tq, vcol, tile_key(t), b, &s.full2[vp.stage]);
+          kp.next(stages);
+          vp.next(DQ_V_STAGES);
         }
-        drain_copies(s, t, stages, err);
+        drain_copies(s.full, t, stages, err);
+        drain_copies(s.full2, t, DQ_V_STAGES, err);
+        mbar_wait_bounded(s.b0, 0, err, DERR_DRAIN_WAIT);
       }
       __syncwarp();
-    } else if (warp == 8) {  // ---- S = Q K_t^T, dP = dO V_t^T ----
+    } else if (warp == BWD_ISSUER) {  // ---- S = Q K_t^T, dP = dO V_t^T ----
       bool go = warp_await(s.b0, 0, err, DERR_MMA_WAIT, s.abort);
       if (go && n - q0 < 128) {  // padded queries: with Q = dO = 0 and P = 0 they add nothing to the sinks' sums
         zero_rows(s.a, n - q0, 128, ln);
@@ -774,19 +792,20 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
         fence_proxy_async_smem();
         __syncwarp();
       }
-      const uint64_t q = kdesc0(smem_u32(s.a)), dO = kdesc0(smem_u32(s.b)), kd = kdesc0(smem_u32(s.ring));
-      RingPos sp;
+      const uint64_t q = kdesc0(smem_u32(s.a)), dO = kdesc0(smem_u32(s.b)), kd = kdesc0(smem_u32(s.ring)),
+                     vd = kdesc0(smem_u32(ringV));
+      RingPos kp, vp;
       for (int t = 0; t < nt && go; ++t) {
-        go = warp_await(&s.full[sp.stage], sp.parity, err, DERR_MMA_WAIT, s.abort);
+        go = warp_await(&s.full[kp.stage], kp.parity, err, DERR_MMA_WAIT, s.abort) &&
+             warp_await(&s.full2[vp.stage], vp.parity, err, DERR_MMA_WAIT, s.abort);
         const int left = n - tile_key(t);
-        if (left < 128) {  // keys behind the sequence's end: P = dS = 0, the rows themselves may be anything
-          uint8_t* kv = s.ring + sp.stage * BWD_STAGE;
-          zero_rows(kv, left, 128, ln);
-          zero_rows(kv + T128, left, 128, ln);
+        if (go && left < 128) {  // keys behind the sequence's end: P = dS = 0, the rows themselves may be anything
+          zero_rows(s.ring + kp.stage * T128, left, 128, ln);
+          zero_rows(ringV + vp.stage * T128, left, 128, ln);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint64_t k = kd + sp.stage * (BWD_STAGE / 16), v = k + T128 / 16;
+        const uint64_t k = kd + kp.stage * (T128 / 16), v = vd + vp.stage * (T128 / 16);
         const uint32_t id = mma_idesc_bf16(128, t < nwin ? 128 : 64, false, false);
         if (t > 0) go = go && warp_await(s.bsc, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // tile t-1's read out
         if (!go) break;
@@ -797,18 +816,20 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tP, dO + kk * kKStep, v + kk * kKStep, id, kk ? 1u : 0u);
           tc_commit(s.bs);
+          tc_commit(&s.empty2[vp.stage]);
         }
-        sp.next(stages);
+        kp.next(stages);
+        vp.next(DQ_V_STAGES);
       }
       if (elect_one()) drain_products(&s.bfin[0], err);
       __syncwarp();
-    } else if (warp == 9) {  // ---- dQ += dS K_t ----
+    } else if (warp == BWD_ISSUER + 1) {  // ---- dQ += dS K_t ----
       constexpr uint32_t idQ = mma_idesc_bf16(128, 64, false, true);
       constexpr uint32_t idT = mma_idesc_bf16(128, 64, true, true);
       const uint64_t kd = mndesc0(smem_u32(s.ring));
       RingPos gp_;
       for (int t = 0; t < nt; ++t) {
-        const uint64_t k = kd + gp_.stage * (BWD_STAGE / 16);
+        const uint64_t k = kd + gp_.stage * (T128 / 16);
         if (!warp_await(s.bp, t & 1, err, DERR_MMA_WAIT, s.abort)) break;  // dS_t written
         tc_fence_after();
         if (elect_one()) {
@@ -819,11 +840,11 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
             // the sinks' dV = P^T dO and dK = dS^T Q over this block's queries, in the columns of S and
             // dP: P and dS read MN-major.  Rows 64..127 of the products come from the addresses 1024
             // bytes further (inside the CTA's shared memory) and are not read.
-            const uint32_t p = smem_u32(sinkP), q = smem_u32(s.a), dO = smem_u32(s.b);
+            const uint32_t p = smem_u32(sinkP), ds = smem_u32(sinkdS), q = smem_u32(s.a), dO = smem_u32(s.b);
 #pragma unroll 1
             for (int kk = 0; kk < 8; ++kk) {
               tc_mma_f16(tS, sw128_desc(p + kk * 2048, 1024, 1024), mndesc(dO, kk), idT, kk ? 1u : 0u);
-              tc_mma_f16(tP, sw128_desc(p + T128 + kk * 2048, 1024, 1024), mndesc(q, kk), idT, kk ? 1u : 0u);
+              tc_mma_f16(tP, sw128_desc(ds + kk * 2048, 1024, 1024), mndesc(q, kk), idT, kk ? 1u : 0u);
             }
           }
           tc_commit(s.bo);
@@ -835,176 +856,188 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
       __syncwarp();
     }
   } else {  // ---- rows ----
-    take_registers();
+    take_registers_bwd();
     const int g = warp >> 2, r = tid & 127, qi = q0 + r;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    RowSync sync{s.brow, err, s.abort, 0u};
+    const RowWait wait{err, s.abort};
+    RowSync sync{s.brow, wait, 0u};
     const Bias& bias = s.bias;
-    bool ok = !MODE || s.bias.fill(a, h, s.val, tid, sync);
     const int nend = a.last / 32 + 1;
     float farS = 0.f, farP = 0.f;  // the last bucket's sums
+    float rowS = 0.f;              // all of this thread's dS
     if (MODE == 2) {
-      for (int k = 0; k < a.ranks; ++k) {
-        accS[k * ROW_THREADS + tid] = 0.f;
-        accP[k * ROW_THREADS + tid] = __float2half(0.f);
+      if (tid < accs)
+        for (int k = 0; k < a.ranks; ++k) {
+          accS[k * accs + tid] = 0.f;
+          accP[k * accs + tid] = __float2half(0.f);
+        }
+      for (int x = tid; x < nend; x += BWD_ROWS) {
+        uint32_t w = 0u;
+        for (int k = 0; k < a.ranks; ++k)
+          if (a.start[k] >> 5 == x) w |= 1u << (a.start[k] & 31);
+        ends[x] = w;
       }
-      for (int x = tid; x < nend; x += ROW_THREADS) ends[x] = 0u;
-      ok = sync() && ok;
-      if (tid < a.ranks) atomicOr(&ends[a.start[tid] >> 5], 1u << (a.start[tid] & 31));
-      ok = sync() && ok;
     }
+    if (MODE) s.bias.fill<BWD_ROWS>(a, h, tid, sync);
     auto put = [&](int rank, float x, float p) {
-      accS[rank * ROW_THREADS + tid] += x;
-      __half* at = accP + rank * ROW_THREADS + tid;
+      accS[rank * accs + tid] += x;
+      __half* at = accP + rank * accs + tid;
       *at = __float2half(__half2float(*at) + p);
     };
+    // column chunks of 32: one a warpgroup, or two for each of the first two
+    const int chunk_step = MODE == 2 ? accs / 128 : 4;
     const float2 LD = ws_.ld[(static_cast<int64_t>(b) * a.heads + h) * pad128(a.seq) + qi];
-    for (int t = 0; t < nt && ok; ++t) {
+    const f32x2 scale2 = pack2(kScaleLog2, kScaleLog2), D2 = pack2(LD.y, LD.y);
+    for (int t = 0; t < nt; ++t) {
       const bool sink = t >= nwin;
-      const int j0 = tile_key(t) + 64 * g;  // the key of this thread's column 0
-      uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
-      if (sink || !(j0 + 63 <= q0 && q0 + 127 - j0 < a.window)) {
-        const int hi = qi - j0, lo = hi - a.window + 1, sk = a.sinks - j0;
-        const uint32_t n0 = sink ? 0u : ~bits_to(lo - 1), n1 = sink ? 0u : ~bits_to(lo - 33);
-        see0 = bits_to(hi) & (n0 | bits_to(sk - 1));
-        see1 = bits_to(hi - 32) & (n1 | bits_to(sk - 33));
-      }
-      const bool any = __any_sync(0xffffffffu, (see0 | see1) != 0u);
-      ok = warp_await(s.bs, t & 1, err, DERR_ACC_WAIT, s.abort);
-      if (!ok) break;
+      const int chunks = sink ? 2 : 4;
+      wait(s.bs, t & 1);
       tc_fence_after();
-      float v[128];  // S (64 columns), then dP (64 columns), one round trip
-      if (any) {
-        const uint32_t c = lane + 64 * g;
-        const uint32_t at[4] = {tS + c, tS + c + 32, tP + c, tP + c + 32};
-        ld_rows<4>(at, v);
-      }
-      tc_fence_before();
-      mbar_arrive1(s.bsc);
-      if (any) {
-        const int d = qi - j0;  // distances d, d - 1, .. d - 63
+#pragma unroll 1
+      for (int c = g; c < chunks && (MODE < 2 || g < chunk_step); c += chunk_step) {
+        const int j0 = tile_key(t) + 32 * c;  // the key of this thread's column 0
+        const int d = qi - j0;                // distances d, d - 1, .. d - 31
         int rank = 0;
         bool flat = true;
         if (MODE) {
           rank = bias.rank_of(d);
-          flat = __all_sync(0xffffffffu, rank == bias.rank_of(d - 63));
+          flat = __all_sync(0xffffffffu, rank == bias.rank_of(d - 31));
         }
-        if (flat) {
-          const float c = (MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f) + LD.x;
-#pragma unroll
-          for (int i = 0; i < 64; i += 2) ffma2(v[i], v[i + 1], v[i], v[i + 1], kScaleLog2, kScaleLog2, c, c);
-        } else {
+        float v[64];  // S (32 columns), then dP (32 columns), one round trip
+        {
+          const uint32_t at[2] = {tS + lane + 32 * c, tP + lane + 32 * c};
+          ld_rows<2>(at, v);
+        }
+        if (c + chunk_step >= chunks) {  // this thread's last chunk of the tile
+          tc_fence_before();
+          mbar_arrive1(s.bsc);
+        }
+        if (MODE && !flat) {
           const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) v[i] = fmaf(v[i], kScaleLog2, at[-i] + LD.x);
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kScaleLog2, at[-i] + LD.x);
+        } else {
+          const float x = (MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f) + LD.x;
+          const f32x2 x2 = pack2(x, x);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) unpack2(fma2(pack2(v[i], v[i + 1]), scale2, x2), v[i], v[i + 1]);
         }
-        if (!__all_sync(0xffffffffu, (see0 & see1) == 0xffffffffu)) {
-          hide32(v, see0);
-          hide32(v + 32, see1);
+        if (__builtin_expect(sink || !(j0 + 31 <= q0 && q0 + 127 - j0 < a.window), 0)) {
+          const uint32_t window = sink ? 0u : ~bits_to(d - a.window);
+          hide32(v, bits_to(d) & (window | bits_to(a.sinks - j0 - 1)));
         }
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
+        for (int i = 0; i < 32; i += 2) {
           v[i] = ex2_approx(v[i]);  // P
           v[i + 1] = ex2_approx(v[i + 1]);
-          float d0, d1;
-          fadd2(d0, d1, v[64 + i], v[65 + i], LD.y, LD.y);
-          fmul2(v[64 + i], v[65 + i], v[i], v[i + 1], d0, d1);  // dS
+          unpack2(mul2(pack2(v[i], v[i + 1]), add2(pack2(v[32 + i], v[33 + i]), D2)), v[32 + i], v[33 + i]);  // dS
         }
         if (MODE == 2) {
-          if (flat) {
-            float s4[4] = {0.f, 0.f, 0.f, 0.f}, p4[4] = {0.f, 0.f, 0.f, 0.f};
+          f32x2 s2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-              fadd2(s4[0], s4[1], s4[0], s4[1], v[64 + i], v[65 + i]);
-              fadd2(s4[2], s4[3], s4[2], s4[3], v[66 + i], v[67 + i]);
-              fadd2(p4[0], p4[1], p4[0], p4[1], v[i], v[i + 1]);
-              fadd2(p4[2], p4[3], p4[2], p4[3], v[i + 2], v[i + 3]);
-            }
-            const float x = (s4[0] + s4[1]) + (s4[2] + s4[3]), p = (p4[0] + p4[1]) + (p4[2] + p4[3]);
+          for (int i = 0; i < 32; i += 2) s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], pack2(v[32 + i], v[33 + i]));
+          float x0, x1;
+          unpack2(add2(s2[0], s2[1]), x0, x1);
+          rowS += x0 + x1;
+          if (flat) {
+            f32x2 p2[2] = {0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) p2[(i >> 1) & 1] = add2(p2[(i >> 1) & 1], pack2(v[i], v[i + 1]));
+            float y0, y1;
+            unpack2(add2(p2[0], p2[1]), y0, y1);
             if (__all_sync(0xffffffffu, rank == a.ranks - 1)) {
-              farS += x;
-              farP += p;
+              farS += x0 + x1;
+              farP += y0 + y1;
             } else {
-              put(rank, x, p);
+              put(rank, x0 + x1, y0 + y1);
             }
           } else {
+            // bit i: column i ends its bucket (its distance is the bucket's first).  From the bitmap,
+            // distances low .. low + 31, the reverse of the columns' order.
+            const int low = d - 31;
+            const int wd = low >> 5;  // floor division
+            const uint32_t w0 = wd >= 0 && wd < nend ? ends[wd] : 0u;
+            const uint32_t w1 = wd + 1 >= 0 && wd + 1 < nend ? ends[wd + 1] : 0u;
+            const uint32_t stop = __brev(__funnelshift_r(w0, w1, low & 31));
             float runS = 0.f, runP = 0.f;
+            int at = a.ranks * accs + tid;      // the first bucket's sums wait in a spare word
+            int next = (rank - 1) * accs + tid;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              // bit i: column 32 c + i ends its bucket (its distance is the bucket's first).  From the
-              // bitmap, distances low .. low + 31, the reverse of the columns' order.
-              const int low = d - 32 * c - 31;
-              const int wd = low >> 5;  // floor division
-              const uint32_t w0 = wd >= 0 && wd < nend ? ends[wd] : 0u;
-              const uint32_t w1 = wd + 1 >= 0 && wd + 1 < nend ? ends[wd + 1] : 0u;
-              const uint32_t stop = __brev(__funnelshift_r(w0, w1, low & 31));
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                runS += v[64 + 32 * c + i];
-                runP += v[32 * c + i];
-                if ((stop >> i) & 1u) {
-                  put(rank, runS, runP);
-                  runS = runP = 0.f;
-                  --rank;
-                }
+            for (int i = 0; i < 32; ++i) {
+              runS += v[32 + i];
+              runP += v[i];
+              if ((stop >> i) & 1u) {
+                accS[at] = runS;
+                accP[at] = __float2half(runP);
+                runS = runP = 0.f;
+                at = next;
+                next -= accs;
               }
             }
-            if (rank >= 0) put(rank, runS, runP);  // (below 0: only columns behind the diagonal are left)
+            if (stop) put(rank, accS[a.ranks * accs + tid], __half2float(accP[a.ranks * accs + tid]));
+            rank -= __popc(stop);
+            if (rank >= 0) put(rank, runS, runP);  // (below 0: only columns behind the diagonal were left)
           }
         }
-      }
-      if (t > 0) {  // the previous dQ product reads dS
-        ok = warp_await(s.bo, (t - 1) & 1, err, DERR_ACC_WAIT, s.abort);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      if (!any) st_zero64_tmem(tdS + lane + 32 * g);
-      else st_row64_tmem(tdS + lane + 32 * g, v + 64);
-      if (sink && g == 0) {
+        uint32_t u[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          st_row32_bf16(sinkP, r, 4 * c, v + 32 * c);
-          st_row32_bf16(sinkP + T128, r, 4 * c, v + 64 + 32 * c);
+        for (int i = 0; i < 16; ++i) u[i] = pack_bf16x2(v[32 + 2 * i], v[33 + 2 * i]);
+        if (t > 0 && c == g) {  // the previous dQ product reads dS
+          wait(s.bo, (t - 1) & 1);
+          tc_fence_after();
         }
-        fence_proxy_async_smem();
+        tmem_st16(tdS + lane + 16 * c, u);
+        if (sink) {
+          st_row32_bf16(sinkP, r, 4 * c, v);
+          st_row32_bf16(sinkdS, r, 4 * c, v + 32);
+          fence_proxy_async_smem();
+        }
+      }
+      if (g >= chunks || (MODE == 2 && g >= chunk_step)) {  // no columns for this warpgroup
+        mbar_arrive1(s.bsc);
+        if (t > 0) wait(s.bo, (t - 1) & 1);
       }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive1(s.bp);
     }
-    if (ok) ok = warp_await(s.bo, (nt - 1) & 1, err, DERR_ACC_WAIT, s.abort);
+    wait(s.bo, (nt - 1) & 1);
     tc_fence_after();
-    if (ok) {
+    if (g < 2) {
       store_row32(tQ + lane + 32 * g, dqkv + (row0 + qi) * ld + h * HD + 32 * g, 0.125f, qi < a.seq, qi < n);
-      if (sink_tile) {  // dV | dK
-        float* part = ws_.far + (((static_cast<int64_t>(b) * a.heads + h) * nqb + qb) * a.sinks + r) * 128 + 64 * g;
+    } else if (sink_tile) {  // dV | dK
+      float* part =
+          ws_.far + (((static_cast<int64_t>(b) * a.heads + h) * nqb + qb) * a.sinks + r) * 128 + 64 * (g - 2);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float x[32];
-          ld_row32((g ? tP : tS) + lane + 32 * c, x);
-          if (r < a.sinks) {
+      for (int c = 0; c < 2; ++c) {
+        float x[32];
+        ld_row32((g == 3 ? tP : tS) + lane + 32 * c, x);
+        if (r < a.sinks) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) store8(part + 32 * c + i, x + i);
-          }
+          for (int i = 0; i < 32; i += 8) store8(part + 32 * c + i, x + i);
         }
       }
     }
     if (MODE == 2) {
-      put(a.ranks - 1, farS, farP);
+      if (tid < accs) put(a.ranks - 1, farS, farP);
+      row_e[tid] = rowS;
       sync();
-      // thread r of each warpgroup: half of the ranks of row r, both warpgroups' columns
-      float e = 0.f;  // the error of D: the row's dS sum to it instead of 0
-      for (int k = 0; k < a.ranks; ++k) e += accS[k * ROW_THREADS + r] + accS[k * ROW_THREADS + 128 + r];
-      sync();
-      for (int k = g; k < a.ranks; k += 2) {
-        const float p = __half2float(accP[k * ROW_THREADS + r]) + __half2float(accP[k * ROW_THREADS + 128 + r]);
-        const float x = (accS[k * ROW_THREADS + r] + accS[k * ROW_THREADS + 128 + r]) - e * p;
-        accS[k * ROW_THREADS + r] = qi < n ? x : 0.f;
+      // the error of D: a row's dS sum to it instead of 0 (a padded row's sums are 0 themselves)
+      float e[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float* at = row_e + 32 * c + ln;
+        e[c] = (at[0] + at[128]) + (at[256] + at[384]);
       }
-      sync();
-      for (int k = warp; k < a.ranks; k += 8) {
-        const float* row = accS + k * ROW_THREADS;
-        const float x = warp_sum((row[ln] + row[ln + 32]) + (row[ln + 64] + row[ln + 96]));
+      for (int k = warp; k < a.ranks; k += BWD_ISSUER) {
+        float x = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          if (32 * c < accs) {
+            const int at = k * accs + 32 * c + ln;
+            x += accS[at] - e[c & 3] * __half2float(accP[at]);
+          }
+        x = warp_sum(x);
         if (ln == 0) tab[k] = x;
       }
     }
@@ -1016,9 +1049,8 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
 // over the 128-query blocks that see them, one query head after the other.
 template <int MODE>
 __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td,
-                               const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int stages,
-                               int* err, uint8_t* sm) {
-  BwdSmem s(sm, stages, a);
+                               const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int* err, uint8_t* sm) {
+  BwdSmem s(sm, DKV_STAGES * DKV_STAGE, DKV_LD_BYTES, a);
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int kvh = item % a.kv_heads;
   const int b = (item / a.kv_heads) % a.nseq;
@@ -1034,7 +1066,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
   griddep_wait();
   const int n = seq_len(a, b);
   if (k0 >= n) {  // a block of padding
-    if (tid < ROW_THREADS && k0 + (tid & 127) < a.seq)
+    if (tid < 256 && k0 + (tid & 127) < a.seq)
       zero_row64(dqkv + (row0 + k0 + (tid & 127)) * ld + (tid < 128 ? kcol : vcol));
     return;
   }
@@ -1048,9 +1080,9 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
   // S^T at 0, dP^T at 128, dV at 256, dK at 320, P^T (bf16) at 384, dS^T at 448
   const uint32_t tS = tmem, tdP = tmem + 128, tV = tmem + 256, tK = tmem + 320, tP = tmem + 384, tdS = tmem + 448;
 
-  if (warp >= 8) {
-    give_registers();
-    if (warp == 10) {  // ---- loader ----
+  if (warp >= BWD_ISSUER) {
+    give_registers_bwd();
+    if (warp == BWD_ISSUER + 2) {  // ---- loader ----
       if (elect_one()) {
         mbar_arrive_expect_tx(s.b0, 2 * T128);
         tma_load_3d(s.a, tq, kcol, k0, b, s.b0);
@@ -1058,8 +1090,8 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
         RingPos lp;
         int t = 0, lh = h0, lq = kb;
         for (; t < niter; ++t) {
-          if (t >= stages && !lane_await(&s.empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
-          uint8_t* dst = s.ring + lp.stage * BWD_STAGE;
+          if (t >= DKV_STAGES && !lane_await(&s.empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
+          uint8_t* dst = s.ring + lp.stage * DKV_STAGE;
           uint64_t* full = &s.full[lp.stage];
           mbar_arrive_expect_tx(full, 2 * T128 + 128 * 8);
           tma_load_3d(dst, tq, lh * HD, lq * 128, b, full);
@@ -1070,12 +1102,13 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
             lq = kb;
             ++lh;
           }
-          lp.next(stages);
+          lp.next(DKV_STAGES);
         }
-        drain_copies(s, t, stages, err);
+        drain_copies(s.full, t, DKV_STAGES, err);
+        mbar_wait_bounded(s.b0, 0, err, DERR_DRAIN_WAIT);
       }
       __syncwarp();
-    } else if (warp == 8) {  // ---- S^T = K Q_t^T, dP^T = V dO_t^T ----
+    } else if (warp == BWD_ISSUER) {  // ---- S^T = K Q_t^T, dP^T = V dO_t^T ----
       constexpr uint32_t idSP = mma_idesc_bf16(128, 128, false, false);
       const uint64_t k = kdesc0(smem_u32(s.a)), v = kdesc0(smem_u32(s.b)), qd = kdesc0(smem_u32(s.ring));
       RingPos sp;
@@ -1085,13 +1118,13 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
         go = warp_await(&s.full[sp.stage], sp.parity, err, DERR_MMA_WAIT, s.abort);
         const int left = n - qb * 128;
         if (left < 128) {  // padded queries: P = dS = 0, the rows themselves may be anything
-          uint8_t* at = s.ring + sp.stage * BWD_STAGE;
+          uint8_t* at = s.ring + sp.stage * DKV_STAGE;
           zero_rows(at, left, 128, ln);
           zero_rows(at + T128, left, 128, ln);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint64_t q = qd + sp.stage * (BWD_STAGE / 16), dO = q + T128 / 16;
+        const uint64_t q = qd + sp.stage * (DKV_STAGE / 16), dO = q + T128 / 16;
         if (t > 0) go = go && warp_await(s.bsc, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // block t-1's read out
         if (!go) break;
         tc_fence_after();
@@ -1103,16 +1136,16 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
           tc_commit(s.bs);
         }
         if (++qb == kb + nq) qb = kb;
-        sp.next(stages);
+        sp.next(DKV_STAGES);
       }
       if (elect_one()) drain_products(&s.bfin[0], err);
       __syncwarp();
-    } else if (warp == 9) {  // ---- dV += P^T dO_t, dK += dS^T Q_t ----
+    } else if (warp == BWD_ISSUER + 1) {  // ---- dV += P^T dO_t, dK += dS^T Q_t ----
       constexpr uint32_t idKV = mma_idesc_bf16(128, 64, false, true);
       const uint64_t qd = mndesc0(smem_u32(s.ring));
       RingPos gp_;
       for (int t = 0; t < niter; ++t) {
-        const uint64_t q = qd + gp_.stage * (BWD_STAGE / 16), dO = q + T128 / 16;
+        const uint64_t q = qd + gp_.stage * (DKV_STAGE / 16), dO = q + T128 / 16;
         if (!warp_await(s.bp, t & 1, err, DERR_MMA_WAIT, s.abort)) break;  // P^T, dS^T of block t written
         tc_fence_after();
         if (elect_one()) {
@@ -1123,122 +1156,113 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
           tc_commit(s.bo);
           tc_commit(&s.empty[gp_.stage]);
         }
-        gp_.next(stages);
+        gp_.next(DKV_STAGES);
       }
       if (elect_one()) drain_products(&s.bfin[1], err);
       __syncwarp();
     }
   } else {  // ---- rows ----
-    take_registers();
+    take_registers_bwd();
     const int g = warp >> 2, r = tid & 127, kr = k0 + r;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    RowSync sync{s.brow, err, s.abort, 0u};
+    const RowWait wait{err, s.abort};
+    RowSync sync{s.brow, wait, 0u};
     const Bias& bias = s.bias;
     RingPos rp;
-    bool ok = true;
     int hq = h0, qb = kb;
+    const f32x2 scale2 = pack2(kScaleLog2, kScaleLog2);
     for (int t = 0; t < niter; ++t) {
-      if (MODE && qb == kb) ok = s.bias.fill(a, hq, s.val, tid, sync);
-      const int q0 = qb * 128 + 64 * g;  // the query of this thread's column 0
-      uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
-      if (!(q0 >= k0 + 127 && q0 + 63 - k0 < a.window)) {  // some pair may be hidden
-        const int lo = kr - q0, hi = kr < a.sinks ? 63 : lo + a.window - 1;
-        see0 = bits_to(hi) & ~bits_to(lo - 1);
-        see1 = bits_to(hi - 32) & ~bits_to(lo - 33);
+      if (MODE && qb == kb) s.bias.fill<BWD_ROWS>(a, hq, tid, sync);
+      const int q0 = qb * 128 + 32 * g;  // the query of this thread's column 0
+      const int d = q0 - kr;             // distances d .. d + 31
+      bool flat = true;
+      if (MODE) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d + 31));
+      uint32_t see = 0xffffffffu;
+      bool any = true;
+      if (__builtin_expect(!(q0 >= k0 + 127 && q0 + 31 - k0 < a.window), 0)) {  // some pair may be hidden
+        see = bits_to(kr < a.sinks ? 31 : a.window - 1 - d) & ~bits_to(-d - 1);
+        any = __any_sync(0xffffffffu, see != 0u);
       }
-      const bool any = __any_sync(0xffffffffu, (see0 | see1) != 0u);
-      // the block's -lse and -D came with its tiles
-      if (ok) ok = warp_await(&s.full[rp.stage], rp.parity, err, DERR_ACC_WAIT, s.abort);
-      if (ok) ok = warp_await(s.bs, t & 1, err, DERR_ACC_WAIT, s.abort);
-      if (!ok) break;
+      wait(&s.full[rp.stage], rp.parity);  // the block's -lse and -D came with its tiles
+      wait(s.bs, t & 1);
       tc_fence_after();
-      float v[128];  // S^T (64 columns), then dP^T (64 columns), one round trip
+      uint32_t up[16], us[16];
       if (any) {
-        const uint32_t c = lane + 64 * g;
-        const uint32_t at[4] = {tS + c, tS + c + 32, tdP + c, tdP + c + 32};
-        ld_rows<4>(at, v);
-      }
-      tc_fence_before();
-      mbar_arrive1(s.bsc);
-      if (any) {
-        const float4* LD = reinterpret_cast<const float4*>(s.ld + rp.stage * 128 + 64 * g);  // two queries each
-        const int d = q0 - kr;  // distances d .. d + 63
-        bool flat = true;
-        if (MODE) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d + 63));
-        if (flat) {
-          const float c = MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f;
-#pragma unroll
-          for (int q = 0; q < 64; q += 2) {
-            const float4 x = LD[q / 2];
-            float l0 = x.x, l1 = x.z;
-            if (MODE) fadd2(l0, l1, l0, l1, c, c);
-            ffma2(v[q], v[q + 1], v[q], v[q + 1], kScaleLog2, kScaleLog2, l0, l1);
-            fadd2(v[64 + q], v[65 + q], v[64 + q], v[65 + q], x.y, x.w);
-          }
-        } else {
+        float v[64];  // S^T (32 columns), then dP^T (32 columns), one round trip
+        {
+          const uint32_t at[2] = {tS + lane + 32 * g, tdP + lane + 32 * g};
+          ld_rows<2>(at, v);
+        }
+        tc_fence_before();
+        mbar_arrive1(s.bsc);
+        const float4* LD = reinterpret_cast<const float4*>(s.ld + rp.stage * 128 + 32 * g);  // two queries each
+        if (MODE && !flat) {
           const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
-          for (int q = 0; q < 64; q += 2) {
+          for (int q = 0; q < 32; q += 2) {
             const float4 x = LD[q / 2];
-            float l0, l1;
-            fadd2(l0, l1, x.x, x.z, at[q], at[q + 1]);
-            ffma2(v[q], v[q + 1], v[q], v[q + 1], kScaleLog2, kScaleLog2, l0, l1);
-            fadd2(v[64 + q], v[65 + q], v[64 + q], v[65 + q], x.y, x.w);
+            unpack2(fma2(pack2(v[q], v[q + 1]), scale2, add2(pack2(x.x, x.z), pack2(at[q], at[q + 1]))), v[q], v[q + 1]);
+            unpack2(add2(pack2(v[32 + q], v[33 + q]), pack2(x.y, x.w)), v[32 + q], v[33 + q]);
+          }
+        } else {
+          const float c = MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f;
+          const f32x2 c2 = pack2(c, c);
+#pragma unroll
+          for (int q = 0; q < 32; q += 2) {
+            const float4 x = LD[q / 2];
+            f32x2 l2 = pack2(x.x, x.z);
+            if (MODE) l2 = add2(l2, c2);
+            unpack2(fma2(pack2(v[q], v[q + 1]), scale2, l2), v[q], v[q + 1]);
+            unpack2(add2(pack2(v[32 + q], v[33 + q]), pack2(x.y, x.w)), v[32 + q], v[33 + q]);
           }
         }
-        if (!__all_sync(0xffffffffu, (see0 & see1) == 0xffffffffu)) {
-          hide32(v, see0);
-          hide32(v + 32, see1);
-        }
+        if (__builtin_expect(!__all_sync(0xffffffffu, see == 0xffffffffu), 0)) hide32(v, see);
 #pragma unroll
-        for (int q = 0; q < 64; q += 2) {
-          v[q] = ex2_approx(v[q]);  // P^T
-          v[q + 1] = ex2_approx(v[q + 1]);
-          fmul2(v[64 + q], v[65 + q], v[q], v[q + 1], v[64 + q], v[65 + q]);  // dS^T
+        for (int q = 0; q < 32; q += 2) {
+          const float p0 = ex2_approx(v[q]), p1 = ex2_approx(v[q + 1]);  // P^T
+          float s0, s1;
+          unpack2(mul2(pack2(p0, p1), pack2(v[32 + q], v[33 + q])), s0, s1);  // dS^T
+          up[q / 2] = pack_bf16x2(p0, p1);
+          us[q / 2] = pack_bf16x2(s0, s1);
         }
+      } else {
+        mbar_arrive1(s.bsc);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) up[i] = us[i] = 0u;
       }
       if (t > 0) {  // the previous dV, dK products read P^T and dS^T
-        ok = warp_await(s.bo, (t - 1) & 1, err, DERR_ACC_WAIT, s.abort);
-        if (!ok) break;
+        wait(s.bo, (t - 1) & 1);
         tc_fence_after();
       }
-      if (!any) {
-        st_zero64_tmem(tP + lane + 32 * g);
-        st_zero64_tmem(tdS + lane + 32 * g);
-      } else {
-        st_row64_tmem(tP + lane + 32 * g, v);
-        st_row64_tmem(tdS + lane + 32 * g, v + 64);
-      }
+      tmem_st16(tP + lane + 16 * g, up);
+      tmem_st16(tdS + lane + 16 * g, us);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive1(s.bp);
-      rp.next(stages);
+      rp.next(DKV_STAGES);
       if (++qb == kb + nq) {
         qb = kb;
         ++hq;
       }
     }
-    if (ok) ok = warp_await(s.bo, (niter - 1) & 1, err, DERR_ACC_WAIT, s.abort);
+    wait(s.bo, (niter - 1) & 1);
     tc_fence_after();
-    if (ok) {
-      // warpgroup 0 stores dV, warpgroup 1 dK.  The sinks' rows go on to the finish kernel, where
-      // query blocks far from them add to them.
+    {
+      // warpgroups 0, 1 store dV, 2, 3 dK (32 columns each).  The sinks' rows go on to the finish
+      // kernel, where query blocks far from them add to them.
       const bool on = ws_.far && kr < a.sinks && kr < n;
-      const uint32_t acc = (g ? tK : tV) + lane;
-      __nv_bfloat16* dst = dqkv + (row0 + kr) * ld + (g ? kcol : vcol);
+      const bool is_k = g >= 2;
+      const int col = 32 * (g & 1);
+      const uint32_t acc = (is_k ? tK : tV) + lane + col;
+      __nv_bfloat16* dst = dqkv + (row0 + kr) * ld + (is_k ? kcol : vcol) + col;
+      store_row32(acc, dst, is_k ? 0.125f : 1.f, kr < a.seq && !on, kr < n);
+      if (ws_.far && kb == 0) {  // dV | dK
+        float* part = ws_.base + ((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + r) * 128 + 32 * g;
+        float x[32];
+        ld_row32(acc, x);
+        if (on) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        store_row32(acc + 32 * c, dst + 32 * c, g ? 0.125f : 1.f, kr < a.seq && !on, kr < n);
-      if (ws_.far && kb == 0) {
-        float* part = ws_.base + ((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + r) * 128 + 64 * g;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {  // dV | dK
-          float x[32];
-          ld_row32(acc + 32 * c, x);
-          if (on) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) store8(part + 32 * c + i, x + i);
-          }
+          for (int i = 0; i < 32; i += 8) store8(part + i, x + i);
         }
       }
     }
@@ -1248,7 +1272,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
 
 // One launch for both kinds, the dK/dV CTAs first (they have more to do).
 template <int MODE>
-__global__ void __launch_bounds__(WIN_THREADS, 1)
+__global__ void __launch_bounds__(BWD_THREADS, 1)
     attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap td,
                            const __grid_constant__ WindowArgs a, const __grid_constant__ WindowScratch ws_,
                            __nv_bfloat16* __restrict__ dqkv, int n_dkv, int stages, int* err) {
@@ -1256,7 +1280,7 @@ __global__ void __launch_bounds__(WIN_THREADS, 1)
   if (misaligned(sm, err)) return;
   const int x = static_cast<int>(blockIdx.x);
   if (x < n_dkv)
-    window_bwd_dkv<MODE>(a, &tq, &td, ws_, dqkv, x, stages, err, sm);
+    window_bwd_dkv<MODE>(a, &tq, &td, ws_, dqkv, x, err, sm);
   else
     window_bwd_dq<MODE>(a, &tq, &td, ws_, dqkv, x - n_dkv, stages, err, sm);
 }
@@ -1422,15 +1446,20 @@ WindowScratch window_scratch(void* base, int nseq, int seq, int heads, int windo
 
 constexpr int kMaxSmem = 227 * 1024;
 int fwd_smem(const WindowArgs& a) { return FWD_BIAS + (a.ranks ? Bias::bytes(a.last) : 0); }
-int bwd_smem(const WindowArgs& a, bool grad, int stages) {
-  int s = BWD_RING + stages * BWD_STAGE + BWD_FIXED + (a.ranks ? Bias::bytes(a.last) : 0);
-  if (grad) s += a.ranks * ROW_THREADS * 6 + (a.last / 32 + 1) * 4;
-  return s;
+constexpr int table_bytes(int ranks, int last) {
+  return BWD_ROWS * 4 + (ranks + 1) * table_threads(ranks) * 6 + (last / 32 + 1) * 4;
+}
+constexpr int dq_smem(int stages, int bias_bytes, int table) {
+  return (2 + stages + DQ_V_STAGES) * T128 + BWD_BARS + bias_bytes + table;
+}
+constexpr int dkv_smem(int bias_bytes) {
+  return 2 * T128 + DKV_STAGES * DKV_STAGE + DKV_LD_BYTES + BWD_BARS + bias_bytes;
 }
 static_assert(FWD_BIAS + Bias::bytes(kMaxDistance) <= kMaxSmem, "the largest table fits beside the forward's tiles");
-static_assert(BWD_RING + 2 * BWD_STAGE + BWD_FIXED + Bias::bytes(kMaxDistance) + kMaxBuckets * ROW_THREADS * 6 +
-                      (kMaxDistance / 32 + 1) * 4 <= kMaxSmem,
-              "the largest table's sums fit beside two stages");
+static_assert(dq_smem(2, Bias::bytes(kMaxDistance), table_bytes(kWideRanks, kMaxDistance)) <= kMaxSmem &&
+                  dq_smem(2, Bias::bytes(kMaxDistance), table_bytes(kMaxBuckets, kMaxDistance)) <= kMaxSmem &&
+                  dkv_smem(Bias::bytes(kMaxDistance)) <= kMaxSmem,
+              "the largest table's sums fit beside two key tiles");
 
 int prepare_attention_window() {
   static std::atomic<unsigned long long> done{0};
@@ -1490,7 +1519,7 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
   if (!make_tmap(&tq, qkv, static_cast<int64_t>(heads + 2 * kv_heads) * HD, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_fwd: tensor map creation failed");
   const int grid = ((seq + 255) / 256) * heads * nseq;
-  (void)launch_k<true>(a.ranks ? attn_window_fwd_kernel<true> : attn_window_fwd_kernel<false>, grid, WIN_THREADS,
+  (void)launch_k<true>(a.ranks ? attn_window_fwd_kernel<true> : attn_window_fwd_kernel<false>, grid, FWD_THREADS,
                        fwd_smem(a), s, tq, a, static_cast<__nv_bfloat16*>(o), lse, err);
   return check_launch("attention_window_fwd");
 }
@@ -1526,8 +1555,10 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   const int nqb = (seq + 127) / 128, n_dkv = nqb * kv_heads * nseq, n_dq = nqb * heads * nseq;
   auto kern = dtable_acc ? attn_window_bwd_kernel<2> : (a.ranks ? attn_window_bwd_kernel<1> : attn_window_bwd_kernel<0>);
   const bool grad = dtable_acc != nullptr;
-  const int stages = bwd_smem(a, grad, BWD_STAGES) <= kMaxSmem ? BWD_STAGES : 2;
-  (void)launch_k<true>(kern, n_dkv + n_dq, WIN_THREADS, bwd_smem(a, grad, stages), s, tq, td, a, w,
+  const int bias_bytes = a.ranks ? Bias::bytes(a.last) : 0, sums = grad ? table_bytes(a.ranks, a.last) : 0;
+  const int stages = dq_smem(3, bias_bytes, sums) <= kMaxSmem ? 3 : 2;
+  const int dq_bytes = dq_smem(stages, bias_bytes, sums), dkv_bytes = dkv_smem(bias_bytes);
+  (void)launch_k<true>(kern, n_dkv + n_dq, BWD_THREADS, dq_bytes > dkv_bytes ? dq_bytes : dkv_bytes, s, tq, td, a, w,
                        static_cast<__nv_bfloat16*>(dqkv), n_dkv, stages, err);
   rc = check_launch("attention_window_bwd");
   if (rc) return rc;
