@@ -73,8 +73,8 @@ struct WindowArgs {
   const float* table;   // [buckets][heads], or NULL
   int ranks;            // non-empty buckets, by rising distance (0: no bias)
   int last;             // first distance of the last of them
-  int16_t start[kMaxBuckets];
-  uint8_t bucket[kMaxBuckets];
+  int start[kMaxBuckets];  // (first distance << 8) | bucket of each
+  __host__ __device__ int first(int rank) const { return start[rank] >> 8; }
 };
 
 __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
@@ -178,13 +178,15 @@ struct Bias {
     sync();  // nobody reads the previous head's any more
     for (int x = tid; x < kLow + last + kHigh; x += N) {
       const int d = max(0, min(x - kLow, last));
-      int k = 0, bucket = a.bucket[0];
-      for (int i = 1; i < a.ranks; ++i)
-        if (a.start[i] <= d) {
-          k = i;
-          bucket = a.bucket[i];
-        }
-      const float t = a.table[static_cast<int64_t>(bucket) * a.heads + head];
+      int k = -1, at = 0;
+#pragma unroll 8
+      for (int i = 0; i < a.ranks; ++i) {
+        const int start = a.start[i];
+        const bool reached = start <= (d << 8 | 255);
+        k += reached;
+        at = reached ? start : at;
+      }
+      const float t = a.table[static_cast<int64_t>(at & 255) * a.heads + head];
       value[x] = t <= kHidden ? -INFINITY : t * kLog2e;
       if (x >= kLow && x <= kLow + last) rank[d] = static_cast<uint8_t>(k);
     }
@@ -215,16 +217,28 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to, int l
     *reinterpret_cast<uint4*>(tile + x * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Store 32 fp32 TMEM columns of this thread's lane, times scale, as bf16 to dst
-// when `valid`; zeros unless `keep` (whatever the accumulator holds then).
-__device__ __forceinline__ void store_row32(uint32_t taddr, __nv_bfloat16* dst, float scale, bool valid, bool keep) {
+// 32 fp32 TMEM columns of this thread's lane, times scale, as bf16 into row r of a
+// swizzled tile (units u0..u0+3) for the tile store; zeros unless `keep`
+// (whatever the accumulator holds then).
+__device__ __forceinline__ void stage_row32(uint32_t taddr, uint8_t* tile, int r, int u0, float scale, bool keep) {
   float v[32];
   ld_row32(taddr, v);
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = keep ? v[i] * scale : 0.f;
-  if (valid) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) store8(dst + 8 * u, v + 8 * u);
+  st_row32_bf16(tile, r, u0, v);
+}
+
+// Send a staged tile of 128 rows out, once `threads` of the row threads (whole
+// warps, barrier `id`) have written it; rows behind the sequence's last are cut
+// off.  Every thread of them comes here, whatever it waited for in vain.
+__device__ __forceinline__ void send_tile(const CUtensorMap* map, int x, int y, int z, const uint8_t* tile, int id,
+                                          int threads, bool leader) {
+  fence_proxy_async_smem();
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+  if (leader) {
+    tma_store_3d(map, x, y, z, tile);
+    bulk_commit();
+    bulk_wait_read_all();  // before the CTA's shared memory goes
   }
 }
 
@@ -280,8 +294,9 @@ constexpr float kMaxStep = 8.f;
 
 template <bool BIAS>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
-    attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ WindowArgs a,
-                           __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int* err) {
+    attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to,
+                           const __grid_constant__ WindowArgs a, __nv_bfloat16* __restrict__ out,
+                           float* __restrict__ lse, int* err) {
   extern __shared__ __align__(1024) uint8_t sm[];
   if (misaligned(sm, err)) return;
   uint8_t* sQ = sm;
@@ -328,8 +343,15 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
   const int last[2] = {kt0 + q00 / 128 - ws[0], two ? kt0 + q00 / 128 + 1 - ws[0] : -1};
   const bool zero = a.sinks > 0 && tile(0) == 0;
 
-  if (tid == 0) {
-    prefetch_tmap(&tq);
+  auto load_tile = [&](int t) {
+    const int st = t % FWD_STAGES;
+    uint8_t* dst = ring + st * 2 * T128;
+    mbar_arrive_expect_tx(&full[st], 2 * T128);
+    tma_load_3d(dst, &tq, kcol, tile(t) * 128, b, &full[st]);
+    tma_load_3d(dst + T128, &tq, vcol, tile(t) * 128, b, &full[st]);
+  };
+  const int ahead = min(nt, FWD_STAGES);
+  if (tid == FWD_THREADS - 32) {  // the first copies leave before anything else is set up
     for (int i = 0; i < 11; ++i) mbar_init(&bar[i], 1);
     for (int i = 0; i < FWD_STAGES; ++i) mbar_init(&empty[i], two ? 2 : 1);
     for (int g = 0; g < 2; ++g) {
@@ -339,6 +361,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     mbar_init(brow, FWD_ROWS);
     *abort = 0;
     fence_barrier_init();
+    mbar_arrive_expect_tx(bq, two ? 2 * T128 : T128);
+    tma_load_3d(sQ, &tq, h * HD, q00, b, bq);
+    if (two) tma_load_3d(sQ + T128, &tq, h * HD, q00 + 128, b, bq);
+    for (int t = 0; t < ahead; ++t) load_tile(t);
   }
   if (warp == 0) {
     tmem_alloc(tslot, 512);
@@ -354,19 +380,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     give_registers_fwd();
     if (warp == 10) {  // ---- loader ----
       if (elect_one()) {
-        mbar_arrive_expect_tx(bq, two ? 2 * T128 : T128);
-        tma_load_3d(sQ, &tq, h * HD, q00, b, bq);
-        if (two) tma_load_3d(sQ + T128, &tq, h * HD, q00 + 128, b, bq);
-        int t = 0;
+        int t = ahead;
         for (; t < nt; ++t) {
-          const int st = t % FWD_STAGES;
-          if (t >= FWD_STAGES &&
-              !lane_await(&empty[st], (t / FWD_STAGES - 1) & 1, err, DERR_TMA_WAIT, abort))
-            break;
-          uint8_t* dst = ring + st * 2 * T128;
-          mbar_arrive_expect_tx(&full[st], 2 * T128);
-          tma_load_3d(dst, &tq, kcol, tile(t) * 128, b, &full[st]);
-          tma_load_3d(dst + T128, &tq, vcol, tile(t) * 128, b, &full[st]);
+          if (!lane_await(&empty[t % FWD_STAGES], (t / FWD_STAGES - 1) & 1, err, DERR_TMA_WAIT, abort)) break;
+          load_tile(t);
         }
         // no copy may still be landing when the CTA exits
         for (int u = max(0, t - FWD_STAGES); u < t; ++u)
@@ -543,9 +560,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     // count = 0: a second tile of padding; l = 0: a row that sees nothing (padding, or every
     // bucket of its keys hidden)
     const bool keep = count > 0 && qi < n && l != 0.f;
-    __nv_bfloat16* dst = out + (row0 + qi) * D + h * HD;
-    store_row32(tO, dst, 1.0f / l, qi < a.seq, keep);
-    store_row32(tO + 32, dst + 32, 1.0f / l, qi < a.seq, keep);
+    uint8_t* tile_o = sQ + g * T128;  // Q_g's place: its products are done
+    stage_row32(tO, tile_o, tid & 127, 0, 1.0f / l, keep);
+    stage_row32(tO + 32, tile_o, tid & 127, 4, 1.0f / l, keep);
+    if (q0 < a.seq) send_tile(&to, h * HD, q0, b, tile_o, 1 + g, 128, (tid & 127) == 0);
     if (qi < a.seq) lse[(row0 + qi) * a.heads + h] = keep ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
   tc_fence_before();
@@ -662,16 +680,17 @@ struct BwdSmem {
     bias = Bias{reinterpret_cast<float*>(t), t + Bias::value_words(w.last) * 4, w.last};
     rest = t + (w.ranks ? Bias::bytes(w.last) : 0);
   }
-  __device__ uint32_t start(int warp, const CUtensorMap* m0, const CUtensorMap* m1) {
-    if (threadIdx.x == 0) {
-      prefetch_tmap(m0);
-      prefetch_tmap(m1);
+  // first(): the first copies, which leave before anything else is set up
+  template <typename F>
+  __device__ __forceinline__ uint32_t start(int warp, F&& first) {
+    if (threadIdx.x == BWD_THREADS - 32) {
       for (int i = 0; i < 15; ++i) mbar_init(&full[i], 1);
       mbar_init(bsc, BWD_ROWS);
       mbar_init(bp, BWD_ROWS);
       mbar_init(brow, BWD_ROWS);
       *abort = 0;
       fence_barrier_init();
+      first();
     }
     if (warp == 0) {
       tmem_alloc(tslot, 512);
@@ -707,6 +726,15 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int loaded, int sta
 constexpr int kWideRanks = 32;
 __host__ __device__ constexpr int table_threads(int ranks) { return ranks <= kWideRanks ? BWD_ROWS : 256; }
 
+// Two predicated stores (a branch around them at every column costs more than they do).
+__device__ __forceinline__ void store_if(uint32_t on, uint32_t at, float x, uint32_t at16, float x16) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b16 h;\n setp.ne.u32 p, %0, 0;\n cvt.rn.f16.f32 h, %4;\n"
+      " @p st.shared.f32 [%1], %2;\n @p st.shared.b16 [%3], h;\n}\n" ::"r"(on),
+      "r"(at), "f"(x), "r"(at16), "f"(x16)
+      : "memory");
+}
+
 // MODE 0: no bias; 1: bias; 2: bias and its gradient.
 //
 // dQ CTA: 128 queries, the window's key tiles by rising key, the sinks' (64
@@ -718,7 +746,7 @@ __host__ __device__ constexpr int table_threads(int ranks) { return ranks <= kWi
 // last are added to what is there.  With more than kWideRanks buckets the words
 // of four warpgroups do not fit into shared memory: two take 64 columns each.
 template <int MODE>
-__device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td,
+__device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td, const CUtensorMap* tg,
                               const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int stages,
                               int* err, uint8_t* sm) {
   BwdSmem s(sm, (stages + DQ_V_STAGES) * T128, 0, a);
@@ -753,10 +781,27 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
   const int nt = nwin + (sink_tile ? 1 : 0);
   auto tile_key = [&](int t) { return t < nwin ? (kt0 + t) * 128 : 0; };
 
-  const uint32_t tmem = s.start(warp, tq, td);
+  uint8_t* ringV = s.ring + stages * T128;
+  auto load_k = [&](int t, int stage) {
+    mbar_arrive_expect_tx(&s.full[stage], T128);
+    tma_load_3d(s.ring + stage * T128, tq, kcol, tile_key(t), b, &s.full[stage]);
+  };
+  auto load_v = [&](int t, int stage) {
+    mbar_arrive_expect_tx(&s.full2[stage], T128);
+    tma_load_3d(ringV + stage * T128, tq, vcol, tile_key(t), b, &s.full2[stage]);
+  };
+  const int ahead = min(nt, DQ_V_STAGES);
+  const uint32_t tmem = s.start(warp, [&] {
+    mbar_arrive_expect_tx(s.b0, 2 * T128);
+    tma_load_3d(s.a, tq, h * HD, q0, b, s.b0);
+    tma_load_3d(s.b, td, h * HD, q0, b, s.b0);
+    for (int t = 0; t < ahead; ++t) {
+      load_k(t, t);
+      load_v(t, t);
+    }
+  });
   // S at 0, dP at 128, dQ at 256, dS (bf16) at 320
   const uint32_t tS = tmem, tP = tmem + 128, tQ = tmem + 256, tdS = tmem + 320;
-  uint8_t* ringV = s.ring + stages * T128;
   // the sinks' P and dS in shared memory: the stages behind the last tile's, free by then
   uint8_t *sinkP = s.ring + (nt % stages) * T128, *sinkdS = ringV + (nt % DQ_V_STAGES) * T128;
 
@@ -764,18 +809,17 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
     give_registers_bwd();
     if (warp == BWD_ISSUER + 2) {  // ---- loader ----
       if (elect_one()) {
-        mbar_arrive_expect_tx(s.b0, 2 * T128);
-        tma_load_3d(s.a, tq, h * HD, q0, b, s.b0);
-        tma_load_3d(s.b, td, h * HD, q0, b, s.b0);
         RingPos kp, vp;
-        int t = 0;
+        for (int i = 0; i < ahead; ++i) {
+          kp.next(stages);
+          vp.next(DQ_V_STAGES);
+        }
+        int t = ahead;
         for (; t < nt; ++t) {
           if (t >= stages && !lane_await(&s.empty[kp.stage], kp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
-          if (t >= DQ_V_STAGES && !lane_await(&s.empty2[vp.stage], vp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
-          mbar_arrive_expect_tx(&s.full[kp.stage], T128);
-          tma_load_3d(s.ring + kp.stage * T128, tq, kcol, tile_key(t), b, &s.full[kp.stage]);
-          mbar_arrive_expect_tx(&s.full2[vp.stage], T128);
-          tma_load_3d(ringV + vp.stage * T128, tq, vcol, tile_key(t), b, &s.full2[vp.stage]);
+          if (!lane_await(&s.empty2[vp.stage], vp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
+          load_k(t, kp.stage);
+          load_v(t, vp.stage);
           kp.next(stages);
           vp.next(DQ_V_STAGES);
         }
@@ -874,7 +918,7 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
       for (int x = tid; x < nend; x += BWD_ROWS) {
         uint32_t w = 0u;
         for (int k = 0; k < a.ranks; ++k)
-          if (a.start[k] >> 5 == x) w |= 1u << (a.start[k] & 31);
+          if (a.first(k) >> 5 == x) w |= 1u << (a.first(k) & 31);
         ends[x] = w;
       }
     }
@@ -960,19 +1004,21 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
             const uint32_t w1 = wd + 1 >= 0 && wd + 1 < nend ? ends[wd + 1] : 0u;
             const uint32_t stop = __brev(__funnelshift_r(w0, w1, low & 31));
             float runS = 0.f, runP = 0.f;
-            int at = a.ranks * accs + tid;      // the first bucket's sums wait in a spare word
-            int next = (rank - 1) * accs + tid;
+            // the first bucket's sums wait in a spare word, the next ones go to their own
+            uint32_t atS = smem_u32(accS + a.ranks * accs + tid), atP = smem_u32(accP + a.ranks * accs + tid);
+            int step = (rank - 1 - a.ranks) * accs;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               runS += v[32 + i];
               runP += v[i];
-              if ((stop >> i) & 1u) {
-                accS[at] = runS;
-                accP[at] = __float2half(runP);
-                runS = runP = 0.f;
-                at = next;
-                next -= accs;
-              }
+              const uint32_t ends_here = stop & (1u << i);
+              store_if(ends_here, atS, runS, atP, runP);
+              runS = ends_here ? 0.f : runS;
+              runP = ends_here ? 0.f : runP;
+              const int by = ends_here ? step : 0;
+              step = ends_here ? -accs : step;
+              atS += 4 * by;
+              atP += 2 * by;
             }
             if (stop) put(rank, accS[a.ranks * accs + tid], __half2float(accP[a.ranks * accs + tid]));
             rank -= __popc(stop);
@@ -1004,7 +1050,8 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
     wait(s.bo, (nt - 1) & 1);
     tc_fence_after();
     if (g < 2) {
-      store_row32(tQ + lane + 32 * g, dqkv + (row0 + qi) * ld + h * HD + 32 * g, 0.125f, qi < a.seq, qi < n);
+      stage_row32(tQ + lane + 32 * g, s.a, r, 4 * g, 0.125f, qi < n);  // in Q's place: its products are done
+      send_tile(tg, h * HD, q0, b, s.a, 1, 256, tid == 0);
     } else if (sink_tile) {  // dV | dK
       float* part =
           ws_.far + (((static_cast<int64_t>(b) * a.heads + h) * nqb + qb) * a.sinks + r) * 128 + 64 * (g - 2);
@@ -1048,7 +1095,7 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
 // dK/dV CTA of 128 keys of one key/value head: iterations t = 0 .. group * nq - 1
 // over the 128-query blocks that see them, one query head after the other.
 template <int MODE>
-__device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td,
+__device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td, const CUtensorMap* tg,
                                const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int* err, uint8_t* sm) {
   BwdSmem s(sm, DKV_STAGES * DKV_STAGE, DKV_LD_BYTES, a);
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
@@ -1076,7 +1123,22 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
   const int nq = imax / 128 - kb + 1;
   const int niter = group * nq;
 
-  const uint32_t tmem = s.start(warp, tq, td);
+  auto load_q = [&](int t, int stage) {
+    const int lh = h0 + t / nq, lq = kb + t % nq;
+    uint8_t* dst = s.ring + stage * DKV_STAGE;
+    uint64_t* full = &s.full[stage];
+    mbar_arrive_expect_tx(full, 2 * T128 + 128 * 8);
+    tma_load_3d(dst, tq, lh * HD, lq * 128, b, full);
+    tma_load_3d(dst + T128, td, lh * HD, lq * 128, b, full);
+    bulk_load(s.ld + stage * 128, ws_.ld + (static_cast<int64_t>(b) * a.heads + lh) * seqpad + lq * 128, 128 * 8, full);
+  };
+  const int ahead = min(niter, DKV_STAGES);
+  const uint32_t tmem = s.start(warp, [&] {
+    mbar_arrive_expect_tx(s.b0, 2 * T128);
+    tma_load_3d(s.a, tq, kcol, k0, b, s.b0);
+    tma_load_3d(s.b, tq, vcol, k0, b, s.b0);
+    for (int t = 0; t < ahead; ++t) load_q(t, t);
+  });
   // S^T at 0, dP^T at 128, dV at 256, dK at 320, P^T (bf16) at 384, dS^T at 448
   const uint32_t tS = tmem, tdP = tmem + 128, tV = tmem + 256, tK = tmem + 320, tP = tmem + 384, tdS = tmem + 448;
 
@@ -1084,24 +1146,12 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
     give_registers_bwd();
     if (warp == BWD_ISSUER + 2) {  // ---- loader ----
       if (elect_one()) {
-        mbar_arrive_expect_tx(s.b0, 2 * T128);
-        tma_load_3d(s.a, tq, kcol, k0, b, s.b0);
-        tma_load_3d(s.b, tq, vcol, k0, b, s.b0);
         RingPos lp;
-        int t = 0, lh = h0, lq = kb;
+        for (int i = 0; i < ahead; ++i) lp.next(DKV_STAGES);
+        int t = ahead;
         for (; t < niter; ++t) {
-          if (t >= DKV_STAGES && !lane_await(&s.empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
-          uint8_t* dst = s.ring + lp.stage * DKV_STAGE;
-          uint64_t* full = &s.full[lp.stage];
-          mbar_arrive_expect_tx(full, 2 * T128 + 128 * 8);
-          tma_load_3d(dst, tq, lh * HD, lq * 128, b, full);
-          tma_load_3d(dst + T128, td, lh * HD, lq * 128, b, full);
-          bulk_load(s.ld + lp.stage * 128, ws_.ld + (static_cast<int64_t>(b) * a.heads + lh) * seqpad + lq * 128,
-                    128 * 8, full);
-          if (++lq == kb + nq) {
-            lq = kb;
-            ++lh;
-          }
+          if (!lane_await(&s.empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
+          load_q(t, lp.stage);
           lp.next(DKV_STAGES);
         }
         drain_copies(s.full, t, DKV_STAGES, err);
@@ -1248,14 +1298,14 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
     wait(s.bo, (niter - 1) & 1);
     tc_fence_after();
     {
-      // warpgroups 0, 1 store dV, 2, 3 dK (32 columns each).  The sinks' rows go on to the finish
-      // kernel, where query blocks far from them add to them.
+      // warpgroups 0, 1 store dV, 2, 3 dK (32 columns each), in the place of V and K, whose products are
+      // done.  Of the sinks' rows the finish kernel makes the sum with the query blocks far from them.
       const bool on = ws_.far && kr < a.sinks && kr < n;
       const bool is_k = g >= 2;
-      const int col = 32 * (g & 1);
-      const uint32_t acc = (is_k ? tK : tV) + lane + col;
-      __nv_bfloat16* dst = dqkv + (row0 + kr) * ld + (is_k ? kcol : vcol) + col;
-      store_row32(acc, dst, is_k ? 0.125f : 1.f, kr < a.seq && !on, kr < n);
+      const uint32_t acc = (is_k ? tK : tV) + lane + 32 * (g & 1);
+      uint8_t* tile_out = is_k ? s.a : s.b;
+      stage_row32(acc, tile_out, r, 4 * (g & 1), is_k ? 0.125f : 1.f, kr < n);
+      send_tile(tg, is_k ? kcol : vcol, k0, b, tile_out, 1 + (g >> 1), 256, (tid & 255) == 0);
       if (ws_.far && kb == 0) {  // dV | dK
         float* part = ws_.base + ((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + r) * 128 + 32 * g;
         float x[32];
@@ -1274,15 +1324,15 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
 template <int MODE>
 __global__ void __launch_bounds__(BWD_THREADS, 1)
     attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap td,
-                           const __grid_constant__ WindowArgs a, const __grid_constant__ WindowScratch ws_,
+                           const __grid_constant__ CUtensorMap tg, const __grid_constant__ WindowArgs a, const __grid_constant__ WindowScratch ws_,
                            __nv_bfloat16* __restrict__ dqkv, int n_dkv, int stages, int* err) {
   extern __shared__ __align__(1024) uint8_t sm[];
   if (misaligned(sm, err)) return;
   const int x = static_cast<int>(blockIdx.x);
   if (x < n_dkv)
-    window_bwd_dkv<MODE>(a, &tq, &td, ws_, dqkv, x, err, sm);
+    window_bwd_dkv<MODE>(a, &tq, &td, &tg, ws_, dqkv, x, err, sm);
   else
-    window_bwd_dq<MODE>(a, &tq, &td, ws_, dqkv, x - n_dkv, stages, err, sm);
+    window_bwd_dq<MODE>(a, &tq, &td, &tg, ws_, dqkv, x - n_dkv, stages, err, sm);
 }
 
 // Blocks 0 .. n_sink-1: one sink key of one (sequence, key/value head); thread c
@@ -1320,7 +1370,7 @@ __global__ void __launch_bounds__(128) attn_window_finish_kernel(const __grid_co
   const int64_t parts = static_cast<int64_t>(a.nseq) * nqb;
 #pragma unroll 8
   for (int64_t p = 0; p < parts; ++p) s += ws_.tab[(p * a.heads + h) * a.ranks + c];
-  dtable[static_cast<int64_t>(a.bucket[c]) * a.heads + h] += static_cast<float>(s);
+  dtable[static_cast<int64_t>(a.start[c] & 255) * a.heads + h] += static_cast<float>(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1412,11 +1462,9 @@ int window_args(WindowArgs& a, int nseq, int seq, int heads, int kv_heads, int w
   for (int b = 0; b < buckets; ++b) {
     // a bucket that begins where the next one does is empty, one that begins behind the longest distance unused
     if ((b + 1 < buckets && starts[b + 1] == starts[b]) || starts[b] >= seq) continue;
-    a.start[a.ranks] = static_cast<int16_t>(starts[b]);
-    a.bucket[a.ranks] = static_cast<uint8_t>(b);
-    ++a.ranks;
+    a.start[a.ranks++] = starts[b] << 8 | b;
   }
-  a.last = a.start[a.ranks - 1];
+  a.last = a.first(a.ranks - 1);
   return GPIPE_OK;
 }
 
@@ -1515,12 +1563,13 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
   if (rc) return rc;
   int* err = device_error_ptr();
   if (!err) return set_error(GPIPE_ERR_CUDA, "attention_window_fwd: no device error word");
-  CUtensorMap tq;
-  if (!make_tmap(&tq, qkv, static_cast<int64_t>(heads + 2 * kv_heads) * HD, seq, nseq, 128))
+  CUtensorMap tq, to;
+  if (!make_tmap(&tq, qkv, static_cast<int64_t>(heads + 2 * kv_heads) * HD, seq, nseq, 128) ||
+      !make_tmap(&to, o, static_cast<int64_t>(heads) * HD, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_fwd: tensor map creation failed");
   const int grid = ((seq + 255) / 256) * heads * nseq;
   (void)launch_k<true>(a.ranks ? attn_window_fwd_kernel<true> : attn_window_fwd_kernel<false>, grid, FWD_THREADS,
-                       fwd_smem(a), s, tq, a, static_cast<__nv_bfloat16*>(o), lse, err);
+                       fwd_smem(a), s, tq, to, a, static_cast<__nv_bfloat16*>(o), lse, err);
   return check_launch("attention_window_fwd");
 }
 
@@ -1543,8 +1592,9 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   int* err = device_error_ptr();
   if (!err) return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: no device error word");
   const int64_t cols = static_cast<int64_t>(heads + 2 * kv_heads) * HD, D = static_cast<int64_t>(heads) * HD;
-  CUtensorMap tq, td;
-  if (!make_tmap(&tq, qkv, cols, seq, nseq, 128) || !make_tmap(&td, dout, D, seq, nseq, 128))
+  CUtensorMap tq, td, tg;
+  if (!make_tmap(&tq, qkv, cols, seq, nseq, 128) || !make_tmap(&td, dout, D, seq, nseq, 128) ||
+      !make_tmap(&tg, dqkv, cols, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: tensor map creation failed");
   const WindowScratch w = window_scratch(scratch, nseq, seq, heads, window, sinks, dtable_acc ? a.ranks : 0);
   const int64_t prep = static_cast<int64_t>(nseq) * pad128(seq) * heads * 8;
@@ -1558,7 +1608,7 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   const int bias_bytes = a.ranks ? Bias::bytes(a.last) : 0, sums = grad ? table_bytes(a.ranks, a.last) : 0;
   const int stages = dq_smem(3, bias_bytes, sums) <= kMaxSmem ? 3 : 2;
   const int dq_bytes = dq_smem(stages, bias_bytes, sums), dkv_bytes = dkv_smem(bias_bytes);
-  (void)launch_k<true>(kern, n_dkv + n_dq, BWD_THREADS, dq_bytes > dkv_bytes ? dq_bytes : dkv_bytes, s, tq, td, a, w,
+  (void)launch_k<true>(kern, n_dkv + n_dq, BWD_THREADS, dq_bytes > dkv_bytes ? dq_bytes : dkv_bytes, s, tq, td, tg, a, w,
                        static_cast<__nv_bfloat16*>(dqkv), n_dkv, stages, err);
   rc = check_launch("attention_window_bwd");
   if (rc) return rc;
