@@ -218,8 +218,8 @@ int gpipe_op_cross_entropy_clip(int rows, int vocab, int seq, const int32_t* tok
  * alone.  It may be the logits themselves (same address, and the same row
  * stride in bytes: lddz = ld for bf16, 2 ld for fp32); any other overlap is
  * rejected.  Elements of a row behind the vocab-th are neither read nor written.
- * 1 <= topk <= 256, vocab >= 1 (any; rows that start on 16-byte boundaries take
- * wide loads).  No atomics: results are bit-reproducible. */
+ * 1 <= topk <= 256, 1 <= rows <= 2^27, 1 <= vocab <= 2^30 (any; rows that start on
+ * 16-byte boundaries take wide loads).  No atomics: results are bit-reproducible. */
 int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t ld, int topk,
                      const int32_t* top_idx, const float* top_logit, float temperature,
                      float kd_scale, int seq, const int32_t* tokens, int row0, float ce_scale,

@@ -96,9 +96,6 @@ __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, int* err, 
   *abort = 1;
   return false;
 }
-__device__ __forceinline__ void mbar_arrive1(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
 // ---------------------------------------------------------------------------
 // Host side

@@ -92,24 +92,6 @@ __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
 constexpr int FWD_ROWS = 256, BWD_ROWS = 512;
 constexpr int FWD_THREADS = FWD_ROWS + 128, BWD_THREADS = BWD_ROWS + 128;
 
-// Bounded waits (2 s; a wait that gives up sets the error word, after which the
-// others of the CTA give up at once).  A phase that is already complete costs
-// one test and one branch: the waits are on the way of every tile.
-__device__ __forceinline__ bool lane_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
-  const uint32_t at = smem_u32(bar);
-  if (mbar_try_wait(at, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(at, parity)) {
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      atomicExch(err, code);
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
 // The whole warp waits; the answer is the same in every lane.
 __device__ __forceinline__ bool warp_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
   return __all_sync(0xffffffffu, lane_await(bar, parity, err, code, abort));

@@ -275,6 +275,25 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same for a CTA whose threads share an abort flag in shared memory: a wait
+// that gives up raises it, after which the others give up at once.  A phase that
+// is already complete costs one test and one branch.
+__device__ __forceinline__ bool lane_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(at, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(err, code);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------------------
 // TMA (tensor copies global -> shared, completing on an mbarrier)
 // ---------------------------------------------------------------------------
@@ -344,6 +363,9 @@ __device__ __forceinline__ float4 ld_peer_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+__device__ __forceinline__ void mbar_arrive1(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
@@ -470,6 +492,27 @@ __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_
       return false;
     }
   }
+}
+
+__device__ __forceinline__ bool lane_await_cluster(uint64_t* bar, uint32_t parity, int* err, int code,
+                                                   volatile int* abort) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait_cluster(at, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait_cluster(at, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(err, code);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// Store to a peer CTA's shared memory (a shared::cluster address).
+__device__ __forceinline__ void st_peer_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // 32 lanes x 32 consecutive 32-bit columns: thread t of the warp gets lane

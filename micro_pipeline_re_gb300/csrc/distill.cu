@@ -9,11 +9,16 @@
 // T^2 keeps the size of the gradient at any temperature.  A row without a
 // filled slot has no teacher term, one without a target no label term.
 //
+// The operator is bound by memory: a row is read once and written once.
+//
 // Both softmaxes share the maximum m of z: q_T = e^{(z - m) / T} / s_T.  The
 // subtraction comes first, so the exponent is exact to fp32 however large the
 // logits are.  The top tokens are few, so dz is written as if there were none
 // and their elements are written again; slots that name the same token are
 // added by the first of them, in slot order, so that nothing depends on timing.
+#include <atomic>
+#include <type_traits>
+
 #include "../../include/gpipe.h"
 #include "attention_tiles.cuh"
 #include "common.cuh"
@@ -76,6 +81,712 @@ __device__ __forceinline__ void join(float& m, float& s, float& st, float om, fl
   m = nm;
 }
 
+// The teacher's side of a row, by one warp: p over the filled slots into pk (all
+// zero without one), and sum p (log p - log q_T) when `kl`.  Returns whether any
+// slot is filled.
+__device__ __forceinline__ bool teacher(const DistillArgs& a, const float* tl, const float* zt, float* pk, float m,
+                                        float st, bool want_kl, float& kl, int lane) {
+  float tm = -INFINITY;
+  for (int k = lane; k < a.topk; k += 32) tm = fmaxf(tm, tl[k]);
+  tm = warp_max(tm);
+  const float tb = tm == -INFINITY ? 0.f : tm;
+  float ts = 0.f;
+  for (int k = lane; k < a.topk; k += 32) ts += expf(tl[k] - tb);
+  ts = warp_sum(ts);
+  const float log_ts = logf(ts), log_st = want_kl ? logf(st) : 0.f;
+  float x = 0.f;
+  for (int k = lane; k < a.topk; k += 32) {
+    const float p = ts == 0.f ? 0.f : expf(tl[k] - tb) / ts;
+    pk[k] = p;
+    if (want_kl && p != 0.f) x += p * ((tl[k] - tb - log_ts) - ((zt[k] - m) * a.inv_t - log_st));
+  }
+  kl = warp_sum(x);
+  return ts != 0.f;
+}
+
+// The target of row r, or -1; an id outside the vocabulary is flagged (by `flag`).
+__device__ __forceinline__ int target_of(const DistillArgs& a, int64_t r, bool flag) {
+  if (!(a.ce > 0.f)) return -1;
+  const int64_t g = a.row0 + r;
+  if (g % a.seq == a.seq - 1) return -1;
+  const int t = a.tokens[g + 1];
+  if (t >= 0 && t < a.vocab) return t;
+  if (flag) atomicExch(a.err, DERR_BAD_TOKEN);
+  return -1;
+}
+
+// Write the element of slot or target `me` (student logit x + m), once: by the
+// first slot that names it, or the target's thread (k = topk) if none does.
+__device__ __forceinline__ void fix_up(const DistillArgs& a, const int* idx, const float* pk, int k, int me, float x,
+                                       int target, float gt, float g1, __nv_bfloat16* out) {
+  float p = 0.f;
+  bool first = true;
+  for (int i = 0; i < a.topk; ++i)
+    if (idx[i] == me) {
+      if (i < k) first = false;
+      p += pk[i];
+    }
+  if (!first) return;
+  float g = gt != 0.f ? ex2_approx(x * (kLog2e * a.inv_t)) * gt - a.kd_grad * p : 0.f;
+  if (g1 != 0.f) g += ex2_approx(x * kLog2e) * g1;
+  if (me == target) g -= a.ce;
+  out[me] = f2bf(g);
+}
+
+// ---------------------------------------------------------------------------
+// A row in registers
+// ---------------------------------------------------------------------------
+// A cluster of C CTAs takes a row, each a slice of `per` elements, 16 bytes a
+// load and up to NV loads a thread, all of them issued before the first is used.
+// The row is read once, its maximum and sums are joined over the cluster, and dz
+// is made from the registers: the bytes the operator cannot do without and no
+// others.  Two CTAs of 256 threads on an SM hold 128 KB of rows, so that one's
+// loads run during the other's exponentials and stores.
+constexpr int kRowThreads = 256;
+
+// What a thread keeps of its slice: NV vectors as they came.
+template <typename T, bool VEC, int NV>
+struct Slice {
+  static constexpr int E = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
+  static constexpr int kElems = kRowThreads * NV * E;
+  using Word = typename std::conditional<VEC, uint4, float>::type;
+  Word w[NV];
+
+  __device__ __forceinline__ void load(const T* z, int n, int tid) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = (j * kRowThreads + tid) * E;
+      if constexpr (VEC) {
+        if (i + E <= n) {
+          w[j] = *reinterpret_cast<const uint4*>(z + i);
+        } else if constexpr (sizeof(T) == 4) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = i + e < n ? z[i + e] : -INFINITY;
+          w[j] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        } else {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = i + e < n ? Elem<T>::ld(z + i + e) : -INFINITY;
+          w[j] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                            pack_bf16x2(v[6], v[7]));
+        }
+      } else {
+        w[j] = i < n ? Elem<T>::ld(z + i) : -INFINITY;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int j, float* v) const {
+    if constexpr (!VEC) {
+      v[0] = w[j];
+    } else if constexpr (sizeof(T) == 4) {
+      v[0] = __uint_as_float(w[j].x);
+      v[1] = __uint_as_float(w[j].y);
+      v[2] = __uint_as_float(w[j].z);
+      v[3] = __uint_as_float(w[j].w);
+    } else {
+      const float2 a = unpack_bf16x2(w[j].x), b = unpack_bf16x2(w[j].y), c = unpack_bf16x2(w[j].z),
+                   d = unpack_bf16x2(w[j].w);
+      v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y; v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
+    }
+  }
+};
+
+template <typename T, bool VEC, int NV>
+__global__ void __launch_bounds__(kRowThreads, 2) distill_row_kernel(const T* logits, __nv_bfloat16* dz,
+                                                                    const __grid_constant__ DistillArgs a, int ctas,
+                                                                    int per) {
+  griddep_wait();
+  griddep_launch();
+  using S = Slice<T, VEC, NV>;
+  constexpr int E = S::E, W = kRowThreads / 32;
+  __shared__ float sm_m[W], sm_s[W], sm_t[W];
+  __shared__ __align__(16) float mine[4];  // this CTA's maximum and sums, for the cluster
+  __shared__ int idx[kMaxTop];
+  __shared__ float tl[kMaxTop], zt[kMaxTop], pk[kMaxTop];
+  __shared__ float sh_z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t r = blockIdx.x / ctas;
+  const int rank = blockIdx.x % ctas;
+  const int lo = rank * per, n = max(0, min(a.vocab - lo, per));
+  const T* z = logits + r * a.ld;
+  const float c1 = kLog2e, ct = kLog2e * a.inv_t;
+
+  S row;
+  row.load(z + lo, n, tid);
+  const int target = target_of(a, r, rank == 0 && tid == 0);
+  if (tid < a.topk) {
+    int i = a.top_idx[r * a.topk + tid];
+    if (i >= a.vocab) {
+      if (rank == 0) atomicExch(a.err, DERR_BAD_TOKEN);
+      i = -1;
+    }
+    idx[tid] = i;
+    tl[tid] = i >= 0 ? a.top_logit[r * a.topk + tid] * a.inv_t : -INFINITY;
+    zt[tid] = i >= 0 ? Elem<T>::ld(z + i) : 0.f;
+  }
+  if (tid == 0 && target >= 0) sh_z = Elem<T>::ld(z + target);
+
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float v[E];
+    row.get(j, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = fmaxf(m, v[e]);
+  }
+  float s1 = 0.f, st = 0.f;
+  {
+    const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float v[E];
+      row.get(j, v);
+      if (E * j * kRowThreads < n) {  // (uniform)
+#pragma unroll
+        for (int e = 0; e < E; ++e) st += ex2_approx((v[e] - ms) * ct);
+        if (a.ce > 0.f) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) s1 += ex2_approx((v[e] - ms) * c1);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s1, o),
+                ot = __shfl_xor_sync(0xffffffffu, st, o);
+    join(m, s1, st, om, os, ot, c1, ct);
+  }
+  if (lane == 0) {
+    sm_m[warp] = m;
+    sm_s[warp] = s1;
+    sm_t[warp] = st;
+  }
+  __syncthreads();
+  m = sm_m[0];
+  s1 = sm_s[0];
+  st = sm_t[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) join(m, s1, st, sm_m[w], sm_s[w], sm_t[w], c1, ct);
+  if (ctas > 1) {
+    if (tid == 0) {
+      mine[0] = m;
+      mine[1] = s1;
+      mine[2] = st;
+    }
+    // also: nobody writes dz, which may lie over the logits, before all have read theirs
+    cluster_sync();
+    m = -INFINITY;
+    s1 = st = 0.f;
+    for (int c = 0; c < ctas; ++c) {  // in rank order, the same in every CTA
+      const uint32_t at = map_peer(smem_u32(mine), c);
+      join(m, s1, st, ld_peer_f32(at), ld_peer_f32(at + 4), ld_peer_f32(at + 8), c1, ct);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  float kl = 0.f;
+  __shared__ float sh_has;
+  if (warp == 0) {
+    const bool has = teacher(a, tl, zt, pk, m, st, rank == 0, kl, lane);
+    if (lane == 0) {
+      sh_has = has ? 1.f : 0.f;
+      if (rank == 0) {
+        float loss = a.kd * kl;
+        if (target >= 0) loss += a.ce * (logf(s1) - (sh_z - m));
+        a.loss[r] = loss;
+      }
+    }
+  }
+  __syncthreads();
+  if (dz) {
+    const float gt = sh_has != 0.f ? a.kd_grad / st : 0.f;
+    const float g1 = target >= 0 ? a.ce / s1 : 0.f;
+    __nv_bfloat16* out = dz + r * a.lddz;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = (j * kRowThreads + tid) * E;
+      if (i < n) {
+        float v[E], g[E];
+        row.get(j, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] = gt != 0.f ? ex2_approx((v[e] - m) * ct) * gt : 0.f;
+        if (g1 != 0.f) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) g[e] = fmaf(ex2_approx((v[e] - m) * c1), g1, g[e]);
+        }
+        if (i + E <= n) {
+          Vec<T, VEC>::store(out + lo + i, g);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (i + e < n) out[lo + i + e] = f2bf(g[e]);
+        }
+      }
+    }
+    __syncthreads();
+    // the elements of the top tokens and of the target in this slice, once each
+    const int me = tid < a.topk ? idx[tid] : -1;
+    if (me >= lo && me < lo + n) fix_up(a, idx, pk, tid, me, zt[tid] - m, target, gt, g1, out);
+    if (tid == 0 && target >= lo && target < lo + n) fix_up(a, idx, pk, a.topk, target, sh_z - m, target, gt, g1, out);
+  }
+  // the others may still be reading this CTA's sums
+  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Rows in a stream
+// ---------------------------------------------------------------------------
+// A cluster of C CTAs, one on an SM, takes rows one after the other, each CTA a
+// slice of them.  Slices pass through a ring of 32 KB chunks in shared memory:
+// the copies run ahead by whatever the ring has left beside the current slice,
+// so that memory is never idle while a row's sums are joined, and a row is read
+// from memory once although it is used twice.
+//   warp 20      copies: the chunks of row after row, as the ring empties.
+//   warps 0-15   pass A over a slice's chunks (maximum and sums), joined over the
+//                warps and, through remote shared memory, over the cluster; pass
+//                B over the same chunks, which writes dz and frees them.
+//   warps 16-19  the teacher of the next row (its tokens, the student's logits
+//                there, p), then the current row's loss and, once pass B is done,
+//                the elements of its top tokens.
+constexpr int kChunk = 32768, kChunks = 6, kMaxSliceChunks = 4;
+constexpr int kPassThreads = 512, kTeachThreads = 128, kStreamThreads = kPassThreads + kTeachThreads + 32;
+constexpr int kMaxCluster = 8;
+
+struct StreamShared {
+  uint64_t full[kChunks], empty[kChunks];
+  uint64_t ready[2];  // the teacher of a row of this parity is known (kTeachThreads arrivals)
+  uint64_t sums[2];   // its maximum and sums are
+  uint64_t done[2];   // its pass B is (one arrival a warp)
+  uint64_t cross[2];  // every CTA of the cluster has sent its sums
+  float part[2][3][kPassThreads / 32];
+  float sent[2][kMaxCluster][4];
+  float total[2][4];
+  float has[2], label[2];  // whether the row has a teacher, a target
+  int idx[2][kMaxTop];
+  float pk[2][kMaxTop];
+  float kl[kTeachThreads / 32];
+  int abort;
+};
+constexpr int kStreamSmem = kChunks * kChunk + static_cast<int>(sizeof(StreamShared));
+
+__device__ __forceinline__ void pass_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPassThreads) : "memory"); }
+__device__ __forceinline__ void teach_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kTeachThreads) : "memory"); }
+
+// What a teacher thread has of its (up to two) slots of a row, step by step.
+struct Fetched {
+  int id[2];
+  float logit[2];
+  int target;
+};
+struct Gathered {
+  int id[2];
+  float tl[2], z[2];
+  int target;
+  float zt;
+};
+struct Slots {
+  int me[2];   // the token, or -1 (empty, or named by an earlier slot)
+  float z[2];  // the student's logit there
+  float p[2];  // the slot's probability, and log p
+  float logp[2];
+  float sum[2];  // over all slots of that token
+  int target;
+  float zt;
+  bool fix_target;  // the target's element is this thread's: no slot names it
+};
+
+template <typename T, bool CE>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    distill_stream_kernel(const T* logits, __nv_bfloat16* dz, const __grid_constant__ DistillArgs a, int rows, int ctas,
+                          int per) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  StreamShared& sh = *reinterpret_cast<StreamShared*>(ring + kChunks * kChunk);
+  volatile int* abort = &sh.abort;
+  constexpr int E = 16 / static_cast<int>(sizeof(T)), kPer = kChunk / static_cast<int>(sizeof(T));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % ctas, clusters = gridDim.x / ctas;
+  const int lo = rank * per, n = max(0, min(a.vocab - lo, per));
+  const int whole = n / E * E;  // elements that come by copies; the last few are read directly
+  const int chunks = (whole + kPer - 1) / kPer;
+  const int row0 = blockIdx.x / ctas;
+  const float c1 = kLog2e, ct = kLog2e * a.inv_t;
+
+  if (tid == 0) {
+    for (int i = 0; i < kChunks; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kPassThreads / 32);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.ready[i], kTeachThreads);
+      mbar_init(&sh.sums[i], 1);
+      mbar_init(&sh.done[i], kPassThreads / 32);
+      mbar_init(&sh.cross[i], ctas);
+    }
+    sh.abort = 0;
+    fence_barrier_init();
+  }
+  griddep_wait();
+  if (ctas > 1) cluster_sync();  // the peers' barriers are there before anything is sent to them
+  else __syncthreads();
+
+  if (warp == kStreamThreads / 32 - 1) {  // ---- copies ----
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t parity = 1;  // of the wait for an empty slot; in the first round there is none
+      int64_t count = 0;
+      bool go = true;
+      for (int r = row0; r < rows && go; r += clusters) {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(logits + static_cast<int64_t>(r) * a.ld + lo);
+        for (int c = 0; c < chunks; ++c) {
+          if (count >= kChunks && !lane_await(&sh.empty[slot], parity, a.err, DERR_TMA_WAIT, abort)) {
+            go = false;
+            break;
+          }
+          const uint32_t bytes = static_cast<uint32_t>(min(kPer, whole - c * kPer)) * sizeof(T);
+          mbar_arrive_expect_tx(&sh.full[slot], bytes);
+          bulk_load(ring + slot * kChunk, src + static_cast<int64_t>(c) * kChunk, bytes, &sh.full[slot]);
+          ++count;
+          if (++slot == kChunks) {
+            slot = 0;
+            parity ^= 1u;
+          }
+        }
+      }
+      // no copy may still be landing when the CTA exits
+      for (int64_t k = count > kChunks ? count - kChunks : 0; k < count; ++k)
+        mbar_wait_bounded(&sh.full[k % kChunks], static_cast<uint32_t>(k / kChunks) & 1u, a.err, DERR_DRAIN_WAIT);
+    }
+    __syncwarp();
+  } else if (warp >= kPassThreads / 32) {  // ---- the teacher ----
+    const int t = tid - kPassThreads, w = t >> 5;
+    // A row's loads are issued one turn (its tokens) and two turns (the student's
+    // logits there) before they are used, while the rows before it are finished.
+    auto fetch = [&](int64_t r) {
+      Fetched f = {{-1, -1}, {0.f, 0.f}, -1};
+      if (r >= rows) return f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int slot = t + k * kTeachThreads;
+        if (slot < a.topk) {
+          f.id[k] = a.top_idx[r * a.topk + slot];
+          f.logit[k] = a.top_logit[r * a.topk + slot];
+        }
+      }
+      f.target = target_of(a, r, rank == 0 && t == 0);
+      return f;
+    };
+    auto gather = [&](const Fetched& f, int64_t r) {
+      Gathered g;
+      const T* z = logits + r * a.ld;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        int i = f.id[k];
+        if (i >= a.vocab) {
+          if (rank == 0) atomicExch(a.err, DERR_BAD_TOKEN);
+          i = -1;
+        }
+        g.id[k] = i;
+        g.tl[k] = i >= 0 ? f.logit[k] * a.inv_t : -INFINITY;
+        g.z[k] = i >= 0 ? Elem<T>::ld(z + i) : 0.f;
+      }
+      g.target = f.target;
+      g.zt = f.target >= 0 ? Elem<T>::ld(z + f.target) : 0.f;
+      return g;
+    };
+    auto prepare = [&](const Gathered& g, int b) {
+      Slots s;
+      s.target = g.target;
+      s.zt = g.zt;
+      const int* id = g.id;
+      const float* tl = g.tl;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int slot = t + k * kTeachThreads;
+        s.z[k] = g.z[k];
+        if (slot < a.topk) {
+          sh.idx[b][slot] = id[k];
+          sh.pk[b][slot] = tl[k];
+        }
+      }
+      teach_sync();
+      // every warp takes the maximum and the sum over all slots by itself
+      float tm = -INFINITY;
+      for (int k = lane; k < a.topk; k += 32) tm = fmaxf(tm, sh.pk[b][k]);
+      tm = warp_max(tm);
+      const float tb = tm == -INFINITY ? 0.f : tm;
+      float ts = 0.f;
+      for (int k = lane; k < a.topk; k += 32) ts += expf(sh.pk[b][k] - tb);
+      ts = warp_sum(ts);
+      const float log_ts = logf(ts);
+      teach_sync();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int slot = t + k * kTeachThreads;
+        s.p[k] = ts == 0.f || id[k] < 0 ? 0.f : expf(tl[k] - tb) / ts;
+        s.logp[k] = tl[k] - tb - log_ts;
+        if (slot < a.topk) sh.pk[b][slot] = s.p[k];
+      }
+      if (t == 0) {
+        sh.has[b] = ts == 0.f ? 0.f : 1.f;
+        sh.label[b] = s.target >= 0 ? 1.f : 0.f;
+      }
+      teach_sync();
+      s.fix_target = t == 0 && s.target >= 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int slot = t + k * kTeachThreads;
+        s.me[k] = id[k];
+        s.sum[k] = 0.f;
+        if (id[k] >= 0)
+          for (int i = 0; i < a.topk; ++i)
+            if (sh.idx[b][i] == id[k]) {
+              if (i < slot) s.me[k] = -1;
+              s.sum[k] += sh.pk[b][i];
+            }
+      }
+      if (s.fix_target)
+        for (int i = 0; i < a.topk; ++i)
+          if (sh.idx[b][i] == s.target) s.fix_target = false;
+      mbar_arrive1(&sh.ready[b]);
+      return s;
+    };
+    auto finish = [&](const Slots& s, int r, int b, uint32_t parity) {
+      (void)lane_await(&sh.sums[b], parity, a.err, DERR_ACC_WAIT, abort);
+      __syncwarp();
+      const float m = sh.total[b][0], s1 = sh.total[b][1], st = sh.total[b][2];
+      if (rank == 0) {
+        const float log_st = logf(st);
+        float kl = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (s.p[k] != 0.f) kl += s.p[k] * (s.logp[k] - ((s.z[k] - m) * a.inv_t - log_st));
+        kl = warp_sum(kl);
+        if (lane == 0) sh.kl[w] = kl;
+        teach_sync();
+        if (t == 0) {
+          float loss = a.kd * ((sh.kl[0] + sh.kl[1]) + (sh.kl[2] + sh.kl[3]));
+          if (s.target >= 0) loss += a.ce * (logf(s1) - (s.zt - m));
+          a.loss[r] = loss;
+        }
+      }
+      if (!dz) return;
+      const float gt = sh.has[b] != 0.f ? a.kd_grad / st : 0.f;
+      const float g1 = s.target >= 0 ? a.ce / s1 : 0.f;
+      __nv_bfloat16* out = dz + static_cast<int64_t>(r) * a.lddz;
+      auto value = [&](float x, float p, bool is_target) {
+        float g = gt != 0.f ? ex2_approx(x * ct) * gt - a.kd_grad * p : 0.f;
+        if (g1 != 0.f) g += ex2_approx(x * c1) * g1;
+        return f2bf(is_target ? g - a.ce : g);
+      };
+      (void)lane_await(&sh.done[b], parity, a.err, DERR_ACC_WAIT, abort);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (s.me[k] >= lo && s.me[k] < lo + n) out[s.me[k]] = value(s.z[k] - m, s.sum[k], s.me[k] == s.target);
+      if (s.fix_target && s.target >= lo && s.target < lo + n) out[s.target] = value(s.zt - m, 0.f, true);
+    };
+    const int64_t stride = clusters;
+    Gathered g = {};
+    Slots cur = {};
+    if (row0 < rows) {
+      g = gather(fetch(row0), row0);
+      cur = prepare(g, 0);
+    }
+    if (row0 + stride < rows) g = gather(fetch(row0 + stride), row0 + stride);
+    Fetched f = fetch(row0 + 2 * stride);
+    int i = 0;
+    for (int64_t r = row0; r < rows; r += stride, ++i) {
+      const Gathered ready = g;  // of the next row
+      if (r + 2 * stride < rows) g = gather(f, r + 2 * stride);
+      f = fetch(r + 3 * stride);
+      Slots next = {};
+      if (r + stride < rows) next = prepare(ready, (i + 1) & 1);
+      finish(cur, static_cast<int>(r), i & 1, (i >> 1) & 1);
+      cur = next;
+    }
+  } else {  // ---- passes ----
+    constexpr int V = kPer / (E * kPassThreads);  // vectors a thread takes of a chunk
+    const f32x2 c12 = pack2(c1, c1), ct2 = pack2(ct, ct);
+    auto load_chunk = [&](const T* at, int left, float* v) {  // elements behind the `left` of a last chunk: -inf
+      at += tid * E;
+#pragma unroll
+      for (int j = 0; j < V; ++j) Vec<T, true>::load(at + j * kPassThreads * E, v + j * E);
+      if (left < kPer) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if ((j * kPassThreads + tid) * E >= left) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[j * E + e] = -INFINITY;
+          }
+      }
+    };
+    int slot = 0, i = 0;
+    uint32_t parity = 0;
+    for (int r = row0; r < rows; r += clusters, ++i) {
+      const int b = i & 1;
+      const uint32_t turn = (i >> 1) & 1;
+      // the last elements of the slice, kept for pass B (dz may lie over them by then)
+      float tail = -INFINITY;
+      if (tid < n - whole) tail = Elem<T>::ld(logits + static_cast<int64_t>(r) * a.ld + lo + whole + tid);
+      // pass A: running maximum (one check a chunk) and the sums
+      float m = tail;
+      f32x2 s12 = 0ull, st2 = 0ull;
+      if (tid < n - whole) s12 = st2 = pack2(tail == -INFINITY ? 0.f : ex2_approx(tail - tail), 0.f);  // 1 (NaN stays NaN)
+      int sl = slot;
+      uint32_t pa = parity;
+      for (int c = 0; c < chunks; ++c) {
+        (void)lane_await(&sh.full[sl], pa, a.err, DERR_ACC_WAIT, abort);
+        __syncwarp();
+        float v[V * E];
+        load_chunk(reinterpret_cast<const T*>(ring + sl * kChunk), min(kPer, whole - c * kPer), v);
+        float mx = v[0];
+#pragma unroll
+        for (int e = 1; e + 1 < V * E; e += 2) mx = fmax3(mx, v[e], v[e + 1]);
+        mx = fmaxf(mx, v[V * E - 1]);
+        if (mx > m) {
+          const float d = m == -INFINITY ? m : m - mx;
+          const float a1 = ex2_approx(d * c1), at = ex2_approx(d * ct);
+          if (CE) s12 = mul2(s12, pack2(a1, a1));
+          st2 = mul2(st2, pack2(at, at));
+          m = mx;
+        }
+        const float ms = m == -INFINITY ? 0.f : -m;
+        const f32x2 ms2 = pack2(ms, ms);
+#pragma unroll
+        for (int e = 0; e < V * E; e += 2) {
+          const f32x2 d = add2(pack2(v[e], v[e + 1]), ms2);
+          float x0, x1;
+          unpack2(mul2(d, ct2), x0, x1);
+          st2 = add2(st2, pack2(ex2_approx(x0), ex2_approx(x1)));
+          if (CE) {
+            unpack2(mul2(d, c12), x0, x1);
+            s12 = add2(s12, pack2(ex2_approx(x0), ex2_approx(x1)));
+          }
+        }
+        if (++sl == kChunks) {
+          sl = 0;
+          pa ^= 1u;
+        }
+      }
+      float s1, st, half;
+      unpack2(s12, s1, half);
+      s1 += half;
+      unpack2(st2, st, half);
+      st += half;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s1, o),
+                    ot = __shfl_xor_sync(0xffffffffu, st, o);
+        join(m, s1, st, om, os, ot, c1, ct);
+      }
+      if (lane == 0) {
+        sh.part[b][0][warp] = m;
+        sh.part[b][1][warp] = s1;
+        sh.part[b][2][warp] = st;
+      }
+      pass_sync();
+      {  // every warp joins the warps' sums by itself
+        constexpr int W = kPassThreads / 32;
+        m = lane < W ? sh.part[b][0][lane] : -INFINITY;
+        s1 = lane < W ? sh.part[b][1][lane] : 0.f;
+        st = lane < W ? sh.part[b][2][lane] : 0.f;
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) {
+          const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s1, o),
+                      ot = __shfl_xor_sync(0xffffffffu, st, o);
+          join(m, s1, st, om, os, ot, c1, ct);
+        }
+        m = __shfl_sync(0xffffffffu, m, 0);
+        s1 = __shfl_sync(0xffffffffu, s1, 0);
+        st = __shfl_sync(0xffffffffu, st, 0);
+      }
+      // the teacher has read the logits of this row that it needs: dz may be written over them
+      (void)lane_await(&sh.ready[b], turn, a.err, DERR_ACC_WAIT, abort);
+      __syncwarp();
+      if (ctas > 1) {
+        if (tid < ctas) {  // to every CTA, this one among them
+          const uint32_t at = map_peer(smem_u32(sh.sent[b][rank]), lane);
+          st_peer_f32(at, m);
+          st_peer_f32(at + 4, s1);
+          st_peer_f32(at + 8, st);
+          mbar_arrive_cluster(map_peer(smem_u32(&sh.cross[b]), lane));
+        }
+        (void)lane_await_cluster(&sh.cross[b], turn, a.err, DERR_ACC_WAIT, abort);
+        __syncwarp();
+        m = -INFINITY;
+        s1 = st = 0.f;
+        for (int c = 0; c < ctas; ++c)  // in rank order, the same in every CTA
+          join(m, s1, st, sh.sent[b][c][0], sh.sent[b][c][1], sh.sent[b][c][2], c1, ct);
+      }
+      if (tid == 0) {
+        sh.total[b][0] = m;
+        sh.total[b][1] = s1;
+        sh.total[b][2] = st;
+        mbar_arrive1(&sh.sums[b]);
+      }
+      // pass B
+      const float gt = sh.has[b] != 0.f ? a.kd_grad / st : 0.f;
+      const float g1 = sh.label[b] != 0.f ? a.ce / s1 : 0.f;
+      __nv_bfloat16* out = dz ? dz + static_cast<int64_t>(r) * a.lddz + lo : nullptr;
+      const f32x2 m2 = pack2(-m, -m), gt2 = pack2(gt, gt), g12 = pack2(g1, g1);
+      // dz of pairs, by which of the two terms the row has
+      auto pass_b = [&](auto grad2) {
+        for (int c = 0; c < chunks; ++c) {
+          if (out) {
+            const int left = min(kPer, whole - c * kPer);
+            float v[V * E];
+            load_chunk(reinterpret_cast<const T*>(ring + slot * kChunk), left, v);
+#pragma unroll
+            for (int e = 0; e < V * E; e += 2) unpack2(grad2(add2(pack2(v[e], v[e + 1]), m2)), v[e], v[e + 1]);
+            __nv_bfloat16* to = out + c * kPer + tid * E;
+            if (left == kPer) {
+#pragma unroll
+              for (int j = 0; j < V; ++j) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
+            } else {
+#pragma unroll
+              for (int j = 0; j < V; ++j)
+                if ((j * kPassThreads + tid) * E < left) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive1(&sh.empty[slot]);
+          if (++slot == kChunks) {
+            slot = 0;
+            parity ^= 1u;
+          }
+        }
+        if (out && tid < n - whole) {
+          float g, other;
+          unpack2(grad2(add2(pack2(tail, tail), m2)), g, other);
+          out[whole + tid] = f2bf(g);
+        }
+      };
+      auto exps = [&](f32x2 d, f32x2 scale) {
+        float x0, x1;
+        unpack2(mul2(d, scale), x0, x1);
+        return pack2(ex2_approx(x0), ex2_approx(x1));
+      };
+      if (gt != 0.f && (!CE || g1 == 0.f))
+        pass_b([&](f32x2 d) { return mul2(exps(d, ct2), gt2); });
+      else if (CE && gt != 0.f)
+        pass_b([&](f32x2 d) { return fma2(exps(d, c12), g12, mul2(exps(d, ct2), gt2)); });
+      else if (CE && g1 != 0.f)
+        pass_b([&](f32x2 d) { return mul2(exps(d, c12), g12); });
+      else
+        pass_b([&](f32x2) { return f32x2(0); });
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&sh.done[b]);
+    }
+  }
+  // the peers may still be sending to this CTA
+  if (ctas > 1) cluster_sync();
+}
+
+// ---------------------------------------------------------------------------
+// A row in two passes
+// ---------------------------------------------------------------------------
+// For vocabularies beyond eight slices: the second pass reads the row again.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logits,
                                                                  __nv_bfloat16* dz, DistillArgs a) {
@@ -93,17 +804,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logit
   const T* z = logits + r * a.ld;
   const float c1 = kLog2e, ct = kLog2e * a.inv_t;
 
-  int target = -1;
-  if (a.ce > 0.f) {
-    const int64_t g = a.row0 + r;
-    if (g % a.seq != a.seq - 1) {
-      target = a.tokens[g + 1];
-      if (target < 0 || target >= a.vocab) {
-        if (tid == 0) atomicExch(a.err, DERR_BAD_TOKEN);
-        target = -1;
-      }
-    }
-  }
+  const int target = target_of(a, r, tid == 0);
   if (tid < a.topk) {
     int i = a.top_idx[r * a.topk + tid];
     if (i >= a.vocab) {
@@ -164,27 +865,13 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logit
                   ot = __shfl_xor_sync(0xffffffffu, st, o);
       join(m, s1, st, om, os, ot, c1, ct);
     }
-    // teacher: p over the filled slots
-    float tm = -INFINITY;
-    for (int k = lane; k < a.topk; k += 32) tm = fmaxf(tm, tl[k]);
-    tm = warp_max(tm);
-    const float tb = tm == -INFINITY ? 0.f : tm;
-    float ts = 0.f;
-    for (int k = lane; k < a.topk; k += 32) ts += expf(tl[k] - tb);
-    ts = warp_sum(ts);
-    const float log_ts = logf(ts), log_st = logf(st);
-    float kl = 0.f;
-    for (int k = lane; k < a.topk; k += 32) {
-      const float p = ts == 0.f ? 0.f : expf(tl[k] - tb) / ts;
-      pk[k] = p;
-      if (p != 0.f) kl += p * ((tl[k] - tb - log_ts) - ((zt[k] - m) * a.inv_t - log_st));
-    }
-    kl = warp_sum(kl);
+    float kl;
+    const bool has = teacher(a, tl, zt, pk, m, st, true, kl, lane);
     if (lane == 0) {
       sh[0] = m;
       sh[1] = s1;
       sh[2] = st;
-      sh_has = ts == 0.f ? 0.f : 1.f;
+      sh_has = has ? 1.f : 0.f;
       float loss = a.kd * kl;
       if (target >= 0) loss += a.ce * (logf(s1) - (sh_z - m));
       a.loss[r] = loss;
@@ -225,24 +912,94 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logit
   }
   __syncthreads();
   // the elements of the top tokens and of the target, once each
-  const bool slot = tid < a.topk && idx[tid] >= 0;
-  if (slot || (tid == a.topk && target >= 0)) {
-    const int me = slot ? idx[tid] : target;
-    const float x = (slot ? zt[tid] : sh_z) - m;
-    float p = 0.f;
-    bool first = true;
-    for (int k = 0; k < a.topk; ++k)
-      if (idx[k] == me) {
-        if (k < tid) first = false;
-        p += pk[k];
-      }
-    if (first) {
-      float g = gt != 0.f ? ex2_approx(x * ct) * gt - a.kd_grad * p : 0.f;
-      if (g1 != 0.f) g += ex2_approx(x * c1) * g1;
-      if (me == target) g -= a.ce;
-      out[me] = f2bf(g);
+  if (tid < a.topk && idx[tid] >= 0) fix_up(a, idx, pk, tid, idx[tid], zt[tid] - m, target, gt, g1, out);
+  if (tid == 0 && target >= 0) fix_up(a, idx, pk, a.topk, target, sh_z - m, target, gt, g1, out);
+}
+
+// Launch the register kernel on clusters of `ctas`.
+template <typename T, bool VEC, int NV>
+cudaError_t launch_row(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int64_t rows, int ctas, int per,
+                       cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[3];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  set_priority_attr(attr[2], s);
+  cfg.attrs = attr;
+  cfg.numAttrs = 3;
+  return cudaLaunchKernelEx(&cfg, distill_row_kernel<T, VEC, NV>, z, dz, a, ctas, per);
+}
+
+template <typename T, bool CE>
+cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, int ctas, int per,
+                          cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  if (once_per_device(done, [] {
+        return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem));
+      }))
+    return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = kStreamSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  set_priority_attr(attr[1], s);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  // as many clusters as run at once (a cluster lives within one GPC, so large ones may leave SMs over)
+  static std::atomic<int> at_once[kMaxCluster + 1];
+  int clusters = at_once[ctas].load(std::memory_order_relaxed);
+  if (clusters == 0) {
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / ctas * ctas));
+    if (cudaOccupancyMaxActiveClusters(&clusters, distill_stream_kernel<T, CE>, &cfg) != cudaSuccess || clusters < 1) {
+      (void)cudaGetLastError();
+      clusters = 1;
     }
+    at_once[ctas].store(clusters, std::memory_order_relaxed);
   }
+  cfg.gridDim = dim3(static_cast<unsigned>((rows < clusters ? rows : clusters) * ctas));
+  return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE>, z, dz, a, rows, ctas, per);
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, cudaStream_t s) {
+  constexpr int kLong = VEC ? 16 : 64, kShort = VEC ? 4 : 16;  // loads a thread
+  constexpr int most = Slice<T, VEC, kLong>::kElems, few = Slice<T, VEC, kShort>::kElems;
+  if (VEC && a.vocab > few) {
+    constexpr int slice = kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T));
+    int ctas = 1;
+    while (ctas < kMaxCluster && static_cast<int64_t>(slice) * ctas < a.vocab) ctas *= 2;
+    while (ctas < kMaxCluster && static_cast<int64_t>(rows) * ctas * 2 <= num_sms() &&
+           static_cast<int64_t>(few) * ctas < a.vocab)
+      ctas *= 2;
+    const int per = ((a.vocab + ctas - 1) / ctas + 7) & ~7;
+    if (static_cast<int64_t>(slice) * ctas >= a.vocab)
+      return a.ce > 0.f ? launch_stream<T, true>(z, dz, a, rows, ctas, per, s)
+                        : launch_stream<T, false>(z, dz, a, rows, ctas, per, s);
+  }
+  int ctas = 1;
+  while (ctas < kMaxCluster && static_cast<int64_t>(most) * ctas < a.vocab) ctas *= 2;
+  if (static_cast<int64_t>(most) * ctas < a.vocab)
+    return launch_k(distill_kernel<T, VEC>, rows, kDistillThreads, 0, s, z, dz, a);
+  // few rows: more SMs a row, down to slices that a thread reads in four loads
+  while (ctas < kMaxCluster && static_cast<int64_t>(rows) * ctas * 2 <= num_sms() &&
+         static_cast<int64_t>(few) * ctas < a.vocab)
+    ctas *= 2;
+  const int per = ((a.vocab + ctas - 1) / ctas + 7) & ~7;
+  return per <= few ? launch_row<T, VEC, kShort>(z, dz, a, rows, ctas, per, s)
+                    : launch_row<T, VEC, kLong>(z, dz, a, rows, ctas, per, s);
 }
 
 }  // namespace
@@ -251,8 +1008,9 @@ int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t l
                    const float* top_logit, float temperature, float kd_scale, int seq, const int32_t* tokens, int row0,
                    float ce_scale, float* loss_rows, void* dz, int64_t lddz, cudaStream_t s) {
   if (dtype != DT_F32 && dtype != DT_BF16) return set_error(GPIPE_ERR_UNSUPPORTED, "distill: dtype must be 0 or 1");
-  if (rows < 1 || vocab < 1 || ld < vocab || topk < 1 || topk > kMaxTop)
-    return set_error(GPIPE_ERR_INVALID_ARG, "distill: need rows, vocab >= 1, ld >= vocab and 1 <= topk <= %d", kMaxTop);
+  if (rows < 1 || rows > (1 << 27) || vocab < 1 || vocab > (1 << 30) || ld < vocab || topk < 1 || topk > kMaxTop)
+    return set_error(GPIPE_ERR_INVALID_ARG,
+                     "distill: need 1 <= rows <= 2^27, 1 <= vocab <= 2^30, ld >= vocab and 1 <= topk <= %d", kMaxTop);
   if (!(temperature > 0.f) || !(temperature < INFINITY) || !(kd_scale >= 0.f) || !(kd_scale < INFINITY) ||
       !(ce_scale >= 0.f) || !(ce_scale < INFINITY))
     return set_error(GPIPE_ERR_INVALID_ARG, "distill: need a finite temperature > 0 and finite scales >= 0");
@@ -298,11 +1056,10 @@ int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t l
   __nv_bfloat16* d = static_cast<__nv_bfloat16*>(dz);
   if (dtype == DT_F32) {
     const float* z = static_cast<const float*>(logits);
-    (void)launch_k(vec ? distill_kernel<float, true> : distill_kernel<float, false>, rows, kDistillThreads, 0, s, z, d, a);
+    (void)(vec ? launch_rows<float, true>(z, d, a, rows, s) : launch_rows<float, false>(z, d, a, rows, s));
   } else {
     const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(logits);
-    (void)launch_k(vec ? distill_kernel<__nv_bfloat16, true> : distill_kernel<__nv_bfloat16, false>, rows,
-                   kDistillThreads, 0, s, z, d, a);
+    (void)(vec ? launch_rows<__nv_bfloat16, true>(z, d, a, rows, s) : launch_rows<__nv_bfloat16, false>(z, d, a, rows, s));
   }
   count_launch();
   const cudaError_t e = cudaGetLastError();
