@@ -81,15 +81,15 @@ __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
   return a.lens ? max(0, min(a.lens[b], a.seq)) : a.seq;
 }
 
-// Row threads: two warpgroups in the forward kernel (a thread has a whole row of
+// Row threads: one warpgroup in the forward kernel (a thread has a whole row of
 // a tile, so a row's maximum needs no exchange), four in the backward one (a
 // thread has a quarter of a row).  The issuers and the loader are warps of one
 // more warpgroup, since registers are passed on by whole warpgroups:
-//   forward   384 threads launched with 168 registers (64512); the row threads go
-//             up to 208, the others down to 88 (256 x 208 + 128 x 88 = 64512);
+//   forward   256 threads launched with 128 registers (32768); the row threads go
+//             up to 208, the others down to 48 (128 x 208 + 128 x 48 = 32768);
 //   backward  640 launched with 96 (61440); up to 104, down to 64
 //             (512 x 104 + 128 x 64 = 61440).
-constexpr int FWD_ROWS = 256, BWD_ROWS = 512;
+constexpr int FWD_ROWS = 128, BWD_ROWS = 512;
 constexpr int FWD_THREADS = FWD_ROWS + 128, BWD_THREADS = BWD_ROWS + 128;
 
 // The whole warp waits; the answer is the same in every lane.
@@ -189,7 +189,7 @@ __device__ __forceinline__ void hide32(float* v, uint32_t see) {
 }
 
 __device__ __forceinline__ void take_registers_fwd() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
-__device__ __forceinline__ void give_registers_fwd() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+__device__ __forceinline__ void give_registers_fwd() { asm volatile("setmaxnreg.dec.sync.aligned.u32 48;"); }
 __device__ __forceinline__ void take_registers_bwd() { asm volatile("setmaxnreg.inc.sync.aligned.u32 104;"); }
 __device__ __forceinline__ void give_registers_bwd() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
 
@@ -247,64 +247,74 @@ __device__ __forceinline__ bool misaligned(const uint8_t* sm, int* err) {
   return true;
 }
 
+// An issuer's last act (one lane): none of its products may still be running when the CTA exits.
+__device__ __forceinline__ void drain_products(uint64_t* bfin, int* err) {
+  tc_commit(bfin);
+  mbar_wait_bounded(bfin, 0, err, DERR_DRAIN_WAIT);
+}
+// The loader's (one lane): none of the last copies into a ring, `loaded` in all, may still be landing.
+__device__ __forceinline__ void drain_copies(uint64_t* full, int loaded, int stages, int* err) {
+  for (int t = max(0, loaded - stages); t < loaded; ++t)
+    mbar_wait_bounded(&full[t % stages], (t / stages) & 1, err, DERR_DRAIN_WAIT);
+}
+
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
-// A CTA takes 256 queries as two tiles of 128, one for each warpgroup of row
-// threads (warps 0-3, 4-7), which share the key and value tiles of a ring.  A
-// key tile is used by the query tiles that see some of it.  Warp 8 + g issues
-// the products of query tile g, warp 10 the copies: what an issuer does between
-// two products is on the rows' way (a wait and a commit take some hundred
-// cycles), so each has as little to do as possible.  Per query tile g and key
-// tile t:
-//   issuer:  S_g = Q_g K_{t+1}^T as soon as the rows have read S_g of tile t ->
-//            commit bs[g];  O_g += P_g V_t once the rows wrote P_g -> commit
-//            bo[g], empty[stage].
-//   loader:  tile t + 4 into the stage of tile t once that is empty.
-//   rows:    wait bs[g]; read S_g; arrive bsc[g]; bias, mask, maximum; wait for
-//            the previous O product; write P_g; arrive bp[g].
+// A CTA takes 128 queries of one head; two of them share an SM, so that one's
+// set-up, waits and stores run during the other's work.  Warps 0-3 are the rows,
+// warp 4 issues the products, warp 5 the copies: what an issuer does between two
+// products is on the rows' way (a wait and a commit take some hundred cycles),
+// so each has as little to do as possible.  Per key tile t:
+//   issuer:  S = Q K_{t+1}^T as soon as the rows have read S of tile t -> commit
+//            bs;  O += P V_t once the rows wrote P -> commit bo, empty[stage].
+//   loader:  the tile after the ring's last into a stage once that is empty.
+//   rows:    wait bs; read S; arrive bsc; bias, mask, maximum; wait for the
+//            previous O product; write P; arrive bp.
 // P goes through tensor memory: as an A operand there it costs the products no
 // shared-memory reads (at head width 64 an O product with P in shared memory
 // reads 6 KB for 32 cycles of tensor work, above the 128 B a cycle there is).
 // A row's maximum is only moved when a tile exceeds it by 2^8: P is then at most
 // 2^8, which neither bf16 nor the fp32 sums mind, and O is seldom rescaled.
-constexpr int FWD_STAGES = 4;
-constexpr int FWD_RING = 2 * T128;
-constexpr int FWD_BAR = FWD_RING + FWD_STAGES * 2 * T128;
-constexpr int FWD_BIAS = FWD_BAR + 256;
+// The ring has three stages of K | V, two where the bias needs the room.
+constexpr int FWD_RING = T128;
 constexpr float kMaxStep = 8.f;
+constexpr int fwd_smem(int stages, int bias_bytes) { return FWD_RING + stages * 2 * T128 + 256 + bias_bytes; }
 
 template <bool BIAS>
-__global__ void __launch_bounds__(FWD_THREADS, 1)
+__global__ void __launch_bounds__(FWD_THREADS, 2)
     attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to,
                            const __grid_constant__ WindowArgs a, __nv_bfloat16* __restrict__ out,
                            float* __restrict__ lse, int* err) {
+  constexpr int kStages = BIAS ? 2 : 3;
   extern __shared__ __align__(1024) uint8_t sm[];
   if (misaligned(sm, err)) return;
   uint8_t* sQ = sm;
   uint8_t* ring = sm + FWD_RING;  // stages of K | V
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + FWD_BAR);
-  uint64_t *full = bar, *bs = bar + 4, *bo = bar + 6, *bfin = bar + 8, *bq = bar + 10, *empty = bar + 12,
-           *bsc = bar + 16, *bp = bar + 18, *brow = bar + 20;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 21);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(ring + kStages * 2 * T128);
+  uint64_t *full = bar, *empty = bar + 3, *bs = bar + 6, *bo = bar + 7, *bfin = bar + 8, *bq = bar + 9, *bsc = bar + 10,
+           *bp = bar + 11, *brow = bar + 12;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 13);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  Bias bias{reinterpret_cast<float*>(sm + FWD_BIAS), sm + FWD_BIAS + Bias::value_words(a.last) * 4, a.last};
+  uint8_t* rest = reinterpret_cast<uint8_t*>(bar) + 256;
+  Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
-  const int nqp = (a.seq + 255) / 256;
-  // heads fastest, then sequences, then pairs of query tiles from the last (the longest rows first)
+  const int nqb = (a.seq + 127) / 128;
+  // heads fastest, then sequences, then query blocks from the last (the longest rows first)
   const int h = static_cast<int>(blockIdx.x) % a.heads;
   const int lin = static_cast<int>(blockIdx.x) / a.heads;
   const int b = lin % a.nseq;
-  const int q00 = (nqp - 1 - lin / a.nseq) * 256;
+  const int qb = nqb - 1 - lin / a.nseq;
+  const int q0 = qb * 128;
   const int64_t row0 = static_cast<int64_t>(b) * a.seq;
   const int D = a.heads * HD;
   const int kcol = D + (h / (a.heads / a.kv_heads)) * HD, vcol = kcol + a.kv_heads * HD;
 
   griddep_wait();
   const int n = seq_len(a, b);
-  if (q00 >= n) {  // nothing but padding
-    const int qi = q00 + tid;
+  if (q0 >= n) {  // nothing but padding
+    const int qi = q0 + tid;
     if (tid < FWD_ROWS && qi < a.seq) {
       zero_row64(out + (row0 + qi) * D + h * HD);
       lse[(row0 + qi) * a.heads + h] = -INFINITY;
@@ -312,143 +322,120 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     return;
   }
   // key tiles: the sinks' (where the window has left it), then the window's up to the diagonal
-  const int ws[2] = {max(0, q00 - a.window + 1) / 128, max(0, q00 + 128 - a.window + 1) / 128};
-  const bool two = q00 + 128 < n;  // the second query tile has queries
-  const int kt0 = a.sinks > 0 && ws[0] > 0 ? 1 : 0;
-  const int nt = kt0 + q00 / 128 + (two ? 1 : 0) - ws[0] + 1;
-  auto tile = [&](int t) { return t < kt0 ? 0 : ws[0] + t - kt0; };
+  const int ws = max(0, q0 - a.window + 1) / 128;
+  const int kt0 = a.sinks > 0 && ws > 0 ? 1 : 0;
+  const int nt = kt0 + qb - ws + 1;
+  auto tile_key = [&](int t) { return t < kt0 ? 0 : (ws + t - kt0) * 128; };
   auto width = [&](int t) {  // keys of a tile, in steps of 32
-    return t < kt0 ? (a.sinks + 31) & ~31 : min(128, (n - tile(t) * 128 + 31) & ~31);
+    return t < kt0 ? (a.sinks + 31) & ~31 : min(128, (n - tile_key(t) + 31) & ~31);
   };
-  // the tiles that query tile g uses: first[g] .. last[g], and tile 0 where that holds sinks
-  const int first[2] = {kt0, kt0 + ws[1] - ws[0]};
-  const int last[2] = {kt0 + q00 / 128 - ws[0], two ? kt0 + q00 / 128 + 1 - ws[0] : -1};
-  const bool zero = a.sinks > 0 && tile(0) == 0;
-
-  auto load_tile = [&](int t) {
-    const int st = t % FWD_STAGES;
+  auto load_tile = [&](int t, int st) {
     uint8_t* dst = ring + st * 2 * T128;
     mbar_arrive_expect_tx(&full[st], 2 * T128);
-    tma_load_3d(dst, &tq, kcol, tile(t) * 128, b, &full[st]);
-    tma_load_3d(dst + T128, &tq, vcol, tile(t) * 128, b, &full[st]);
+    tma_load_3d(dst, &tq, kcol, tile_key(t), b, &full[st]);
+    tma_load_3d(dst + T128, &tq, vcol, tile_key(t), b, &full[st]);
   };
-  const int ahead = min(nt, FWD_STAGES);
+  const int ahead = min(nt, kStages);
   if (tid == FWD_THREADS - 32) {  // the first copies leave before anything else is set up
-    for (int i = 0; i < 11; ++i) mbar_init(&bar[i], 1);
-    for (int i = 0; i < FWD_STAGES; ++i) mbar_init(&empty[i], two ? 2 : 1);
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(&bsc[g], 128);
-      mbar_init(&bp[g], 128);
-    }
+    for (int i = 0; i < 10; ++i) mbar_init(&bar[i], 1);
+    mbar_init(bsc, FWD_ROWS);
+    mbar_init(bp, FWD_ROWS);
     mbar_init(brow, FWD_ROWS);
     *abort = 0;
     fence_barrier_init();
-    mbar_arrive_expect_tx(bq, two ? 2 * T128 : T128);
-    tma_load_3d(sQ, &tq, h * HD, q00, b, bq);
-    if (two) tma_load_3d(sQ + T128, &tq, h * HD, q00 + 128, b, bq);
-    for (int t = 0; t < ahead; ++t) load_tile(t);
+    mbar_arrive_expect_tx(bq, T128);
+    tma_load_3d(sQ, &tq, h * HD, q0, b, bq);
+    for (int t = 0; t < ahead; ++t) load_tile(t, t);
   }
   if (warp == 0) {
-    tmem_alloc(tslot, 512);
+    tmem_alloc(tslot, 256);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  // S_g at 128 g, O_g at 256 + 64 g, P_g at 384 + 64 g
+  // S at 0, O at 128, P (bf16) at 192
 
-  if (warp >= 8) {
+  if (warp >= FWD_ROWS / 32) {
     give_registers_fwd();
-    if (warp == 10) {  // ---- loader ----
+    if (warp == FWD_ROWS / 32 + 1) {  // ---- loader ----
       if (elect_one()) {
+        RingPos lp;
+        for (int i = 0; i < ahead; ++i) lp.next(kStages);
         int t = ahead;
         for (; t < nt; ++t) {
-          if (!lane_await(&empty[t % FWD_STAGES], (t / FWD_STAGES - 1) & 1, err, DERR_TMA_WAIT, abort)) break;
-          load_tile(t);
+          if (!lane_await(&empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, abort)) break;
+          load_tile(t, lp.stage);
+          lp.next(kStages);
         }
         // no copy may still be landing when the CTA exits
-        for (int u = max(0, t - FWD_STAGES); u < t; ++u)
-          mbar_wait_bounded(&full[u % FWD_STAGES], (u / FWD_STAGES) & 1, err, DERR_DRAIN_WAIT);
+        drain_copies(full, t, kStages, err);
         mbar_wait_bounded(bq, 0, err, DERR_DRAIN_WAIT);
       }
       __syncwarp();
-    } else if (warp < 10 && last[warp - 8] >= 0) {  // ---- issuer of query tile g: waits together, one lane issues ----
-      const int g = warp - 8, first_g = first[g], last_g = last[g];
+    } else if (warp == FWD_ROWS / 32) {  // ---- issuer: waits together, one lane issues ----
       constexpr uint32_t idO = mma_idesc_bf16(128, 64, false, true);
-      const uint32_t tS = tmem + 128 * g, tO = tmem + 256 + 64 * g, tP = tmem + 384 + 64 * g;
-      const uint64_t qd = kdesc0(smem_u32(sQ + g * T128)), kd = kdesc0(smem_u32(ring)),
-                     vd = mndesc0(smem_u32(ring + T128));
+      const uint32_t tS = tmem, tO = tmem + 128, tP = tmem + 192;
+      const uint64_t qd = kdesc0(smem_u32(sQ)), kd = kdesc0(smem_u32(ring)), vd = mndesc0(smem_u32(ring + T128));
       constexpr uint64_t kStage = 2 * T128 / 16;
-      const bool at0 = zero && first_g > 0;  // the sinks' tile comes before the window's
-      if (!at0 && elect_one())
-        for (int t = 0; t < first_g; ++t) mbar_arrive1(&empty[t]);  // tiles (at most one) that only the other uses
-      if (at0 && first_g > 1 && elect_one()) mbar_arrive1(&empty[1]);
+      RingPos sp, op;  // of the next S, of the next O product
       auto issue_s = [&](int t) {
-        const int st = t % FWD_STAGES;
         const uint32_t idS = mma_idesc_bf16(128, width(t), false, false);
-        const uint64_t k = kd + st * kStage;
-        if (!warp_await(&full[st], (t / FWD_STAGES) & 1, err, DERR_MMA_WAIT, abort)) return false;
+        const uint64_t k = kd + sp.stage * kStage;
+        if (!warp_await(&full[sp.stage], sp.parity, err, DERR_MMA_WAIT, abort)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, qd + kk * kKStep, k + kk * kKStep, idS, kk ? 1u : 0u);
-          tc_commit(&bs[g]);
+          tc_commit(bs);
         }
+        sp.next(kStages);
         return true;
       };
-      int t = at0 ? 0 : first_g;
-      bool go = warp_await(bq, 0, err, DERR_MMA_WAIT, abort) && issue_s(t);
-      for (uint32_t c = 0; go; ++c) {
-        const int tn = t < first_g ? first_g : t + 1;
-        if (tn <= last_g) {  // the next S as soon as the rows have read this one
-          go = warp_await(&bsc[g], c & 1, err, DERR_MMA_WAIT, abort) && issue_s(tn);
+      bool go = warp_await(bq, 0, err, DERR_MMA_WAIT, abort) && issue_s(0);
+      for (int t = 0; t < nt && go; ++t) {
+        if (t + 1 < nt) {  // the next S as soon as the rows have read this one
+          go = warp_await(bsc, t & 1, err, DERR_MMA_WAIT, abort) && issue_s(t + 1);
           if (!go) break;
         }
-        const int st = t % FWD_STAGES, w = width(t), left = n - tile(t) * 128;
+        const int w = width(t), left = n - tile_key(t);
         if (left < w) {  // values behind the sequence's end: their P is 0, they themselves may be anything
-          zero_rows(ring + st * 2 * T128 + T128, left, w, ln);
+          zero_rows(ring + op.stage * 2 * T128 + T128, left, w, ln);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint64_t v = vd + st * kStage;
-        go = warp_await(&bp[g], c & 1, err, DERR_MMA_WAIT, abort);  // P written, O rescaled
+        const uint64_t v = vd + op.stage * kStage;
+        go = warp_await(bp, t & 1, err, DERR_MMA_WAIT, abort);  // P written, O rescaled
         if (!go) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            if (16 * kk < w) tc_mma_f16_ta(tO, tP + 8 * kk, v + kk * kMnStep, idO, (c | kk) ? 1u : 0u);
-          tc_commit(&bo[g]);
-          if (t + FWD_STAGES < nt) tc_commit(&empty[st]);
+            if (16 * kk < w) tc_mma_f16_ta(tO, tP + 8 * kk, v + kk * kMnStep, idO, (t | kk) ? 1u : 0u);
+          tc_commit(bo);
+          tc_commit(&empty[op.stage]);
         }
-        if (tn > last_g) break;
-        t = tn;
+        op.next(kStages);
       }
-      if (elect_one()) {  // no product may still be running when the CTA exits
-        tc_commit(&bfin[g]);
-        mbar_wait_bounded(&bfin[g], 0, err, DERR_DRAIN_WAIT);
-      }
+      if (elect_one()) drain_products(bfin, err);
       __syncwarp();
     }
   } else {  // ---- rows ----
     take_registers_fwd();
-    const int g = warp >> 2;
-    const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int q0 = q00 + 128 * g, qi = q0 + (tid & 127);
-    const uint32_t tS = tmem + 128 * g + lane, tO = tmem + 256 + 64 * g + lane, tP = tmem + 384 + 64 * g + lane;
+    const uint32_t lane = static_cast<uint32_t>(warp * 32) << 16;
+    const int qi = q0 + tid;
+    const uint32_t tS = tmem + lane, tO = tmem + 128 + lane, tP = tmem + 192 + lane;
     const RowWait wait{err, abort};
     RowSync sync{brow, wait, 0u};
     float m = -INFINITY, l = 0.f;
     if (BIAS) bias.fill<FWD_ROWS>(a, h, tid, sync);
-    uint32_t count = 0;  // tiles done
-    const int first_g = first[g], last_g = last[g];
-    for (int t = zero ? 0 : first_g; t <= last_g; t = t < first_g ? first_g : t + 1) {
-      const int j0 = tile(t) * 128, w = width(t);
+    for (int t = 0; t < nt; ++t) {
+      const int j0 = tile_key(t), w = width(t);
       const int d = qi - j0;  // distances d, d - 1, .. d - 127
       bool flat = true;
       if (BIAS) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d - 127));
-      wait(&bs[g], count & 1);
+      wait(bs, t & 1);
       tc_fence_after();
       float sv[128];
       {
@@ -457,7 +444,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         ld_rows<4>(at, sv);
       }
       tc_fence_before();
-      mbar_arrive1(&bsc[g]);  // S may be overwritten by the next tile's product
+      mbar_arrive1(bsc);  // S may be overwritten by the next tile's product
       // scores = sc * s + cb (log2 domain): the raw scores with a bias that is the
       // same all along the row, or with the bias by distance already added
       float sc = kScaleLog2, cb = 0.f;
@@ -490,8 +477,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
       const float ms = mn == -INFINITY ? 0.f : mn;  // nothing visible yet: exp2(-inf - 0) = 0
       const float alpha = m == mn ? 1.f : ex2_approx(m - ms);
       m = mn;
-      if (count > 0) {  // the previous O product reads P and writes O
-        wait(&bo[g], (count - 1) & 1);
+      if (t > 0) {  // the previous O product reads P and writes O
+        wait(bo, (t - 1) & 1);
         tc_fence_after();
       }
       const f32x2 sc2 = pack2(sc, sc), off2 = pack2(cb - ms, cb - ms);
@@ -514,7 +501,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
       }
       float r0, r1;
       unpack2(add2(add2(rs[0], rs[1]), add2(rs[2], rs[3])), r0, r1);
-      if (count > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // warp-uniform: tcgen05 loads/stores are per warp
+      if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // warp-uniform: tcgen05 loads/stores are per warp
         const f32x2 al2 = pack2(alpha, alpha);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -534,25 +521,22 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
       tmem_st_wait();
       l = l * alpha + (r0 + r1);
       tc_fence_before();
-      mbar_arrive1(&bp[g]);
-      ++count;
+      mbar_arrive1(bp);
     }
-    if (count > 0) wait(&bo[g], (count - 1) & 1);
+    wait(bo, (nt - 1) & 1);
     tc_fence_after();
-    // count = 0: a second tile of padding; l = 0: a row that sees nothing (padding, or every
-    // bucket of its keys hidden)
-    const bool keep = count > 0 && qi < n && l != 0.f;
-    uint8_t* tile_o = sQ + g * T128;  // Q_g's place: its products are done
-    stage_row32(tO, tile_o, tid & 127, 0, 1.0f / l, keep);
-    stage_row32(tO + 32, tile_o, tid & 127, 4, 1.0f / l, keep);
-    if (q0 < a.seq) send_tile(&to, h * HD, q0, b, tile_o, 1 + g, 128, (tid & 127) == 0);
+    // l = 0: a row that sees nothing (padding, or every bucket of its keys hidden)
+    const bool keep = qi < n && l != 0.f;
+    stage_row32(tO, sQ, tid, 0, 1.0f / l, keep);  // in Q's place: its products are done
+    stage_row32(tO + 32, sQ, tid, 4, 1.0f / l, keep);
+    send_tile(&to, h * HD, q0, b, sQ, 1, FWD_ROWS, tid == 0);
     if (qi < a.seq) lse[(row0 + qi) * a.heads + h] = keep ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -692,17 +676,6 @@ struct BwdSmem {
     }
   }
 };
-
-// An issuer's last act (one lane): none of its products may still be running when the CTA exits.
-__device__ __forceinline__ void drain_products(uint64_t* bfin, int* err) {
-  tc_commit(bfin);
-  mbar_wait_bounded(bfin, 0, err, DERR_DRAIN_WAIT);
-}
-// The loader's (one lane): none of the last copies into a ring, `loaded` in all, may still be landing.
-__device__ __forceinline__ void drain_copies(uint64_t* full, int loaded, int stages, int* err) {
-  for (int t = max(0, loaded - stages); t < loaded; ++t)
-    mbar_wait_bounded(&full[t % stages], (t / stages) & 1, err, DERR_DRAIN_WAIT);
-}
 
 // Row threads that keep sums for the table's gradient (a fixed number of bytes for each bucket).
 constexpr int kWideRanks = 32;
@@ -1475,7 +1448,6 @@ WindowScratch window_scratch(void* base, int nseq, int seq, int heads, int windo
 }
 
 constexpr int kMaxSmem = 227 * 1024;
-int fwd_smem(const WindowArgs& a) { return FWD_BIAS + (a.ranks ? Bias::bytes(a.last) : 0); }
 constexpr int table_bytes(int ranks, int last) {
   return BWD_ROWS * 4 + (ranks + 1) * table_threads(ranks) * 6 + (last / 32 + 1) * 4;
 }
@@ -1485,7 +1457,7 @@ constexpr int dq_smem(int stages, int bias_bytes, int table) {
 constexpr int dkv_smem(int bias_bytes) {
   return 2 * T128 + DKV_STAGES * DKV_STAGE + DKV_LD_BYTES + BWD_BARS + bias_bytes;
 }
-static_assert(FWD_BIAS + Bias::bytes(kMaxDistance) <= kMaxSmem, "the largest table fits beside the forward's tiles");
+static_assert(fwd_smem(2, Bias::bytes(kMaxDistance)) <= kMaxSmem / 2 && fwd_smem(3, 0) <= kMaxSmem / 2, "two forward CTAs share an SM, with the largest table too");
 static_assert(dq_smem(2, Bias::bytes(kMaxDistance), table_bytes(kWideRanks, kMaxDistance)) <= kMaxSmem &&
                   dq_smem(2, Bias::bytes(kMaxDistance), table_bytes(kMaxBuckets, kMaxDistance)) <= kMaxSmem &&
                   dkv_smem(Bias::bytes(kMaxDistance)) <= kMaxSmem,
@@ -1549,9 +1521,10 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
   if (!make_tmap(&tq, qkv, static_cast<int64_t>(heads + 2 * kv_heads) * HD, seq, nseq, 128) ||
       !make_tmap(&to, o, static_cast<int64_t>(heads) * HD, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_fwd: tensor map creation failed");
-  const int grid = ((seq + 255) / 256) * heads * nseq;
+  const int grid = ((seq + 127) / 128) * heads * nseq;
+  const int smem = a.ranks ? fwd_smem(2, Bias::bytes(a.last)) : fwd_smem(3, 0);
   (void)launch_k<true>(a.ranks ? attn_window_fwd_kernel<true> : attn_window_fwd_kernel<false>, grid, FWD_THREADS,
-                       fwd_smem(a), s, tq, to, a, static_cast<__nv_bfloat16*>(o), lse, err);
+                       smem, s, tq, to, a, static_cast<__nv_bfloat16*>(o), lse, err);
   return check_launch("attention_window_fwd");
 }
 
