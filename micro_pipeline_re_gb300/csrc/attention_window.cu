@@ -82,14 +82,14 @@ __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
 }
 
 // Row threads: one warpgroup in the forward kernel (a thread has a whole row of
-// a tile, so a row's maximum needs no exchange), four in the backward one (a
-// thread has a quarter of a row).  The issuers and the loader are warps of one
-// more warpgroup, since registers are passed on by whole warpgroups:
+// a tile, so a row's maximum needs no exchange), two in the backward one (a
+// thread has half a row).  The issuers and the loader are warps of one more
+// warpgroup, since registers are passed on by whole warpgroups:
 //   forward   256 threads launched with 128 registers (32768); the row threads go
 //             up to 208, the others down to 48 (128 x 208 + 128 x 48 = 32768);
-//   backward  640 launched with 96 (61440); up to 104, down to 64
-//             (512 x 104 + 128 x 64 = 61440).
-constexpr int FWD_ROWS = 128, BWD_ROWS = 512;
+//   backward  384 launched with 80 (30720); up to 96, down to 48
+//             (256 x 96 + 128 x 48 = 30720).
+constexpr int FWD_ROWS = 128, BWD_ROWS = 256;
 constexpr int FWD_THREADS = FWD_ROWS + 128, BWD_THREADS = BWD_ROWS + 128;
 
 // The whole warp waits; the answer is the same in every lane.
@@ -126,16 +126,11 @@ __device__ __forceinline__ uint64_t kdesc0(uint32_t tile) { return kdesc(tile, 0
 __device__ __forceinline__ uint64_t mndesc0(uint32_t tile) { return mndesc(tile, 0); }
 constexpr uint64_t kKStep = 2, kMnStep = 128;
 
-// A barrier of the row threads.
-struct RowSync {
-  uint64_t* bar;
-  RowWait wait;
-  uint32_t phase;
-  __device__ __forceinline__ void operator()() {
-    mbar_arrive1(bar);
-    wait(bar, phase++ & 1u);
-  }
-};
+// A barrier of the N row threads, all of which come to it whatever they waited for in vain.
+template <int N>
+__device__ __forceinline__ void rows_barrier() {
+  asm volatile("bar.sync 3, %0;" ::"n"(N) : "memory");
+}
 
 // The bias of one head in shared memory: its value by distance in the log2
 // domain, and the rank of a distance's bucket.
@@ -156,8 +151,8 @@ struct Bias {
   __device__ __forceinline__ int rank_of(int d) const { return rank[max(0, min(d, last))]; }
   // Filled by the N row threads.
   template <int N>
-  __device__ __forceinline__ void fill(const WindowArgs& a, int head, int tid, RowSync& sync) {
-    sync();  // nobody reads the previous head's any more
+  __device__ __forceinline__ void fill(const WindowArgs& a, int head, int tid) {
+    rows_barrier<N>();  // nobody reads the previous head's any more
     for (int x = tid; x < kLow + last + kHigh; x += N) {
       const int d = max(0, min(x - kLow, last));
       int k = -1, at = 0;
@@ -172,7 +167,7 @@ struct Bias {
       value[x] = t <= kHidden ? -INFINITY : t * kLog2e;
       if (x >= kLow && x <= kLow + last) rank[d] = static_cast<uint8_t>(k);
     }
-    sync();
+    rows_barrier<N>();
   }
 };
 
@@ -190,8 +185,8 @@ __device__ __forceinline__ void hide32(float* v, uint32_t see) {
 
 __device__ __forceinline__ void take_registers_fwd() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
 __device__ __forceinline__ void give_registers_fwd() { asm volatile("setmaxnreg.dec.sync.aligned.u32 48;"); }
-__device__ __forceinline__ void take_registers_bwd() { asm volatile("setmaxnreg.inc.sync.aligned.u32 104;"); }
-__device__ __forceinline__ void give_registers_bwd() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+__device__ __forceinline__ void take_registers_bwd() { asm volatile("setmaxnreg.inc.sync.aligned.u32 96;"); }
+__device__ __forceinline__ void give_registers_bwd() { asm volatile("setmaxnreg.dec.sync.aligned.u32 48;"); }
 
 // Zero rows [from, to) of a tile of 128-byte rows, by one warp, for the async proxy.
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to, int lane) {
@@ -293,8 +288,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
   uint8_t* ring = sm + FWD_RING;  // stages of K | V
   uint64_t* bar = reinterpret_cast<uint64_t*>(ring + kStages * 2 * T128);
   uint64_t *full = bar, *empty = bar + 3, *bs = bar + 6, *bo = bar + 7, *bfin = bar + 8, *bq = bar + 9, *bsc = bar + 10,
-           *bp = bar + 11, *brow = bar + 12;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 13);
+           *bp = bar + 11;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 12);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   uint8_t* rest = reinterpret_cast<uint8_t*>(bar) + 256;
   Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
@@ -340,7 +335,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
     for (int i = 0; i < 10; ++i) mbar_init(&bar[i], 1);
     mbar_init(bsc, FWD_ROWS);
     mbar_init(bp, FWD_ROWS);
-    mbar_init(brow, FWD_ROWS);
     *abort = 0;
     fence_barrier_init();
     mbar_arrive_expect_tx(bq, T128);
@@ -427,9 +421,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
     const int qi = q0 + tid;
     const uint32_t tS = tmem + lane, tO = tmem + 128 + lane, tP = tmem + 192 + lane;
     const RowWait wait{err, abort};
-    RowSync sync{brow, wait, 0u};
     float m = -INFINITY, l = 0.f;
-    if (BIAS) bias.fill<FWD_ROWS>(a, h, tid, sync);
+    if (BIAS) bias.fill<FWD_ROWS>(a, h, tid);
     for (int t = 0; t < nt; ++t) {
       const int j0 = tile_key(t), w = width(t);
       const int d = qi - j0;  // distances d, d - 1, .. d - 127
@@ -592,74 +585,56 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
   if (in && sub == 0) ld[(b * a.heads + h) * seqpad + i] = make_float2(L, -d);
 }
 
-// Both kinds of CTA work on 128 x 128 tiles: S and dP (or their transposes) take
-// 128 tensor-memory columns each, warpgroup g of the row threads has columns
-// 32 g .. 32 g + 31 of every row, and P, dS go back into tensor memory as bf16 A
-// operands.  With operands A from shared memory the two wide products keep the
-// 128 B a cycle of shared memory just busy (8 KB for 64 cycles of tensor work);
-// with A from tensor memory the three 64-wide ones need half of it.
-//   warp 16: S, dP of tile t+1 as soon as the rows have read tile t's -> commit
+// Both kinds of CTA own 128 rows and walk 64-wide tiles; two CTAs share an SM,
+// so that one's set-up, waits and stores run during the other's work.  S and dP
+// (or their transposes) take 64 tensor-memory columns each; warpgroup g of the
+// two row warpgroups has columns 32 g .. 32 g + 31 of every row.
+//   warp 8:  S, dP of tile t+1 as soon as the rows have read tile t's -> commit
 //            bs.
-//   warp 17: the gradient products of tile t once the rows wrote P, dS ->
-//            commit bo, empty[stage].
-//   warp 18: the copies; a tile into the ring once its stage is empty.
+//   warp 9:  the gradient products of tile t once the rows wrote P, dS ->
+//            commit bo, and the ring's stage as empty.
+//   warp 10: the copies; a tile into the ring once its stage is empty.
 //   rows:    wait bs; read S, dP; arrive bsc; the elementwise gradient; wait
 //            bo of tile t-1 (it reads P, dS); write them; arrive bp.
 constexpr int BWD_ISSUER = BWD_ROWS / 32;  // the issuers' first warp
-// dK/dV: a ring of three stages of Q | dO | -lse, -D of a query block (all of
-// which the last products of the block need).  dQ: a ring of `stages` (3, or 2
-// where a large table's sums need the room) key tiles, which the dQ product
-// needs, and one of two value tiles, which are free as soon as dP is there.
-constexpr int DKV_STAGE = 2 * T128, DKV_STAGES = 3, DQ_V_STAGES = 2;
-constexpr int DKV_LD_BYTES = DKV_STAGES * 128 * 8;
+constexpr int DQ_V_STAGES = 2;
 constexpr int BWD_BARS = 256;
+constexpr int kMaxSmem = 227 * 1024, kHalfSmem = 113 * 1024;  // of a CTA, and of each of two on an SM
 
-struct BwdSmem {
-  uint8_t *a, *b, *ring;
-  float2* ld;
-  uint64_t *full, *empty, *full2, *empty2, *b0, *bs, *bo, *bfin, *bsc, *bp, *brow;
+struct BwdBars {
+  uint64_t *full, *full2, *one, *bs, *bo, *bfin, *bsink, *bsd, *empty, *empty2, *bsc, *bp, *brow, *bq;
   uint32_t* tslot;
   volatile int* abort;
-  Bias bias;
-  uint8_t* rest;
-  // ring_bytes, ld_bytes: what this kind of CTA needs of each
-  __device__ BwdSmem(uint8_t* sm, int ring_bytes, int ld_bytes, const WindowArgs& w) {
-    a = sm;
-    b = sm + T128;
-    ring = sm + 2 * T128;
-    uint8_t* p = ring + ring_bytes;
-    ld = reinterpret_cast<float2*>(p);
-    full = reinterpret_cast<uint64_t*>(p + ld_bytes);
+  __device__ __forceinline__ explicit BwdBars(uint8_t* at) {
+    full = reinterpret_cast<uint64_t*>(at);
     full2 = full + 3;
-    b0 = full + 5;
+    one = full + 5;   // the operands that stay for the whole walk
     bs = full + 6;
     bo = full + 7;
     bfin = full + 8;  // two
-    empty = full + 10;
-    empty2 = full + 13;
-    bsc = full + 15;
-    bp = full + 16;
-    brow = full + 17;
-    tslot = reinterpret_cast<uint32_t*>(full + 18);
+    bsink = full + 10;
+    bsd = full + 11;
+    empty = full + 12;
+    empty2 = full + 15;
+    bsc = full + 17;
+    bp = full + 18;
+    brow = full + 19;
+    bq = full + 20;
+    tslot = reinterpret_cast<uint32_t*>(full + 21);
     abort = reinterpret_cast<volatile int*>(tslot + 1);
-    uint8_t* t = p + ld_bytes + BWD_BARS;
-    bias = Bias{reinterpret_cast<float*>(t), t + Bias::value_words(w.last) * 4, w.last};
-    rest = t + (w.ranks ? Bias::bytes(w.last) : 0);
   }
   // first(): the first copies, which leave before anything else is set up
   template <typename F>
   __device__ __forceinline__ uint32_t start(int warp, F&& first) {
     if (threadIdx.x == BWD_THREADS - 32) {
-      for (int i = 0; i < 15; ++i) mbar_init(&full[i], 1);
-      mbar_init(bsc, BWD_ROWS);
-      mbar_init(bp, BWD_ROWS);
-      mbar_init(brow, BWD_ROWS);
+      for (int i = 0; i < 17; ++i) mbar_init(&full[i], 1);
+      for (int i = 17; i < 21; ++i) mbar_init(&full[i], BWD_ROWS);
       *abort = 0;
       fence_barrier_init();
       first();
     }
     if (warp == 0) {
-      tmem_alloc(tslot, 512);
+      tmem_alloc(tslot, 256);
       tmem_relinquish();
     }
     tc_fence_before();
@@ -667,19 +642,15 @@ struct BwdSmem {
     tc_fence_after();
     return *tslot;
   }
-  __device__ void finish(int warp, uint32_t tmem) {
+  __device__ __forceinline__ void finish(int warp, uint32_t tmem) {
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
       tc_fence_after();
-      tmem_dealloc(tmem, 512);
+      tmem_dealloc(tmem, 256);
     }
   }
 };
-
-// Row threads that keep sums for the table's gradient (a fixed number of bytes for each bucket).
-constexpr int kWideRanks = 32;
-__host__ __device__ constexpr int table_threads(int ranks) { return ranks <= kWideRanks ? BWD_ROWS : 256; }
 
 // Two predicated stores (a branch around them at every column costs more than they do).
 __device__ __forceinline__ void store_if(uint32_t on, uint32_t at, float x, uint32_t at16, float x16) {
@@ -690,26 +661,52 @@ __device__ __forceinline__ void store_if(uint32_t on, uint32_t at, float x, uint
       : "memory");
 }
 
+// Shared memory of a dQ CTA: dO | two value tiles | `stages` key tiles |
+// barriers | bias | sums of the table's gradient | a Q tile for the sinks'
+// products, in the place of the sums (which are done by then) where those are
+// large enough.  Q itself is an A operand in tensor memory: the S product then
+// reads 2 KB of shared memory for 32 cycles of tensor work instead of 6.
+constexpr int DQ_V = T128, DQ_K = DQ_V + DQ_V_STAGES * T64;
+constexpr int dq_sums(int ranks, int last) {
+  return BWD_ROWS * 4 + (ranks + 1) * BWD_ROWS * 6 + (last / 32 + 1) * 4;
+}
+constexpr int dq_smem(int stages, int bias_bytes, int sums, bool far) {
+  const int tile = T128 + 1024;  // with what its alignment may take
+  return DQ_K + stages * T64 + BWD_BARS + bias_bytes + (far && sums < tile ? tile : sums);
+}
+// Shared memory of a dK/dV CTA: K | V | P^T | dS^T | `stages` of Q | dO | -lse,
+// -D of the stages' queries | barriers | bias.
+constexpr int DKV_P = 2 * T128, DKV_DS = 3 * T128, DKV_RING = 4 * T128, DKV_STAGE = 2 * T64, DKV_LD = 64 * 8;
+constexpr int dkv_smem(int stages, int bias_bytes) {
+  return DKV_RING + stages * (DKV_STAGE + DKV_LD) + BWD_BARS + bias_bytes;
+}
+
 // MODE 0: no bias; 1: bias; 2: bias and its gradient.
 //
-// dQ CTA: 128 queries, the window's key tiles by rising key, the sinks' (64
-// wide) last.  For the gradient of the table each row thread adds its dS and P
-// by bucket into words of its own (no two threads share one).  Columns along
-// which the bucket does not change add one sum.  Elsewhere the running sums are
-// put down where a bucket ends: a bucket that begins and ends among the thread's
-// columns is met nowhere else, so its sums are stored; only the first and the
-// last are added to what is there.  With more than kWideRanks buckets the words
-// of four warpgroups do not fit into shared memory: two take 64 columns each.
+// dQ CTA: 128 queries, the window's 64-key tiles by rising key, the sinks' last.
+// For the gradient of the table each row thread adds its dS and P by bucket into
+// words of its own (no two threads share one).  Columns along which the bucket
+// does not change add one sum.  Elsewhere the running sums are put down where a
+// bucket ends: a bucket that begins and ends among the thread's columns is met
+// nowhere else, so its sums are stored; only the first and the last are added to
+// what is there.  P's sums only weigh the error of D, which is some 2^-9 of dS:
+// fp16 is more than they need.
 template <int MODE>
-__device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td, const CUtensorMap* tg,
-                              const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int stages,
-                              int* err, uint8_t* sm) {
-  BwdSmem s(sm, (stages + DQ_V_STAGES) * T128, 0, a);
-  const int accs = MODE == 2 ? table_threads(a.ranks) : 0;            // row threads with words
-  float* row_e = reinterpret_cast<float*>(s.rest);                    // [4][128]
-  float* accS = row_e + BWD_ROWS;                                     // [ranks + 1][accs]
-  __half* accP = reinterpret_cast<__half*>(accS + (a.ranks + 1) * accs);  // [ranks + 1][accs]
-  uint32_t* ends = reinterpret_cast<uint32_t*>(accP + (a.ranks + 1) * accs);  // bit d: d is its bucket's first
+__device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
+                              const CUtensorMap* td128, const CUtensorMap* tg, const WindowScratch& ws_,
+                              const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* __restrict__ dqkv, int item,
+                              int stages, int* err, uint8_t* sm) {
+  uint8_t *sdO = sm, *ringV = sm + DQ_V, *ringK = sm + DQ_K;
+  uint8_t* rest = ringK + stages * T64;
+  BwdBars s(rest);
+  rest += BWD_BARS;
+  Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
+  if (MODE) rest += Bias::bytes(a.last);
+  float* row_e = reinterpret_cast<float*>(rest);                               // [2][128]
+  float* accS = row_e + BWD_ROWS;                                              // [ranks + 1][256]
+  __half* accP = reinterpret_cast<__half*>(accS + (a.ranks + 1) * BWD_ROWS);   // [ranks + 1][256]
+  uint32_t* ends = reinterpret_cast<uint32_t*>(accP + (a.ranks + 1) * BWD_ROWS);  // bit d: d is its bucket's first
+  uint8_t* sinkQ = align1024(rest);
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int nqb = (a.seq + 127) / 128;
@@ -730,35 +727,30 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
     if (MODE == 2 && tid < a.ranks) tab[tid] = 0.f;
     return;
   }
-  const int kt0 = max(0, q0 - a.window + 1) / 128;
-  const bool sink_tile = a.sinks > 0 && kt0 > 0;
-  const int nwin = qb - kt0 + 1;
+  const bool sink_tile = a.sinks > 0 && qb >= first_far_block(a.window);
+  const int kt0 = a.sinks > 0 && !sink_tile ? 0 : max(0, q0 - a.window + 1) / 64;
+  const int nwin = min(q0 + 127, n - 1) / 64 - kt0 + 1;
   const int nt = nwin + (sink_tile ? 1 : 0);
-  auto tile_key = [&](int t) { return t < nwin ? (kt0 + t) * 128 : 0; };
-
-  uint8_t* ringV = s.ring + stages * T128;
+  auto tile_key = [&](int t) { return t < nwin ? (kt0 + t) * 64 : 0; };
   auto load_k = [&](int t, int stage) {
-    mbar_arrive_expect_tx(&s.full[stage], T128);
-    tma_load_3d(s.ring + stage * T128, tq, kcol, tile_key(t), b, &s.full[stage]);
+    mbar_arrive_expect_tx(&s.full[stage], T64);
+    tma_load_3d(ringK + stage * T64, tq64, kcol, tile_key(t), b, &s.full[stage]);
   };
   auto load_v = [&](int t, int stage) {
-    mbar_arrive_expect_tx(&s.full2[stage], T128);
-    tma_load_3d(ringV + stage * T128, tq, vcol, tile_key(t), b, &s.full2[stage]);
+    mbar_arrive_expect_tx(&s.full2[stage], T64);
+    tma_load_3d(ringV + stage * T64, tq64, vcol, tile_key(t), b, &s.full2[stage]);
   };
   const int ahead = min(nt, DQ_V_STAGES);
   const uint32_t tmem = s.start(warp, [&] {
-    mbar_arrive_expect_tx(s.b0, 2 * T128);
-    tma_load_3d(s.a, tq, h * HD, q0, b, s.b0);
-    tma_load_3d(s.b, td, h * HD, q0, b, s.b0);
+    mbar_arrive_expect_tx(s.one, T128);
+    tma_load_3d(sdO, td128, h * HD, q0, b, s.one);
     for (int t = 0; t < ahead; ++t) {
       load_k(t, t);
       load_v(t, t);
     }
   });
-  // S at 0, dP at 128, dQ at 256, dS (bf16) at 320
-  const uint32_t tS = tmem, tP = tmem + 128, tQ = tmem + 256, tdS = tmem + 320;
-  // the sinks' P and dS in shared memory: the stages behind the last tile's, free by then
-  uint8_t *sinkP = s.ring + (nt % stages) * T128, *sinkdS = ringV + (nt % DQ_V_STAGES) * T128;
+  // S at 0, dP at 64, dQ at 128, dS (bf16) at 192, Q (bf16) at 224
+  const uint32_t tS = tmem, tP = tmem + 64, tQ = tmem + 128, tdS = tmem + 192, tQa = tmem + 224;
 
   if (warp >= BWD_ISSUER) {
     give_registers_bwd();
@@ -780,38 +772,36 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
         }
         drain_copies(s.full, t, stages, err);
         drain_copies(s.full2, t, DQ_V_STAGES, err);
-        mbar_wait_bounded(s.b0, 0, err, DERR_DRAIN_WAIT);
+        mbar_wait_bounded(s.one, 0, err, DERR_DRAIN_WAIT);
       }
       __syncwarp();
     } else if (warp == BWD_ISSUER) {  // ---- S = Q K_t^T, dP = dO V_t^T ----
-      bool go = warp_await(s.b0, 0, err, DERR_MMA_WAIT, s.abort);
+      constexpr uint32_t id = mma_idesc_bf16(128, 64, false, false);
+      bool go = warp_await(s.one, 0, err, DERR_MMA_WAIT, s.abort) && warp_await(s.bq, 0, err, DERR_MMA_WAIT, s.abort);
       if (go && n - q0 < 128) {  // padded queries: with Q = dO = 0 and P = 0 they add nothing to the sinks' sums
-        zero_rows(s.a, n - q0, 128, ln);
-        zero_rows(s.b, n - q0, 128, ln);
+        zero_rows(sdO, n - q0, 128, ln);
         fence_proxy_async_smem();
         __syncwarp();
       }
-      const uint64_t q = kdesc0(smem_u32(s.a)), dO = kdesc0(smem_u32(s.b)), kd = kdesc0(smem_u32(s.ring)),
-                     vd = kdesc0(smem_u32(ringV));
+      const uint64_t dO = kdesc0(smem_u32(sdO)), kd = kdesc0(smem_u32(ringK)), vd = kdesc0(smem_u32(ringV));
       RingPos kp, vp;
       for (int t = 0; t < nt && go; ++t) {
         go = warp_await(&s.full[kp.stage], kp.parity, err, DERR_MMA_WAIT, s.abort) &&
              warp_await(&s.full2[vp.stage], vp.parity, err, DERR_MMA_WAIT, s.abort);
         const int left = n - tile_key(t);
-        if (go && left < 128) {  // keys behind the sequence's end: P = dS = 0, the rows themselves may be anything
-          zero_rows(s.ring + kp.stage * T128, left, 128, ln);
-          zero_rows(ringV + vp.stage * T128, left, 128, ln);
+        if (go && left < 64) {  // keys behind the sequence's end: P = dS = 0, the rows themselves may be anything
+          zero_rows(ringK + kp.stage * T64, left, 64, ln);
+          zero_rows(ringV + vp.stage * T64, left, 64, ln);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint64_t k = kd + kp.stage * (T128 / 16), v = vd + vp.stage * (T128 / 16);
-        const uint32_t id = mma_idesc_bf16(128, t < nwin ? 128 : 64, false, false);
+        const uint64_t k = kd + kp.stage * (T64 / 16), v = vd + vp.stage * (T64 / 16);
         if (t > 0) go = go && warp_await(s.bsc, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // tile t-1's read out
         if (!go) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, q + kk * kKStep, k + kk * kKStep, id, kk ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16_ta(tS, tQa + 8 * kk, k + kk * kKStep, id, kk ? 1u : 0u);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tP, dO + kk * kKStep, v + kk * kKStep, id, kk ? 1u : 0u);
           tc_commit(s.bs);
@@ -825,31 +815,53 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
     } else if (warp == BWD_ISSUER + 1) {  // ---- dQ += dS K_t ----
       constexpr uint32_t idQ = mma_idesc_bf16(128, 64, false, true);
       constexpr uint32_t idT = mma_idesc_bf16(128, 64, true, true);
-      const uint64_t kd = mndesc0(smem_u32(s.ring));
+      const uint64_t kd = mndesc0(smem_u32(ringK));
       RingPos gp_;
+      bool go = true;
       for (int t = 0; t < nt; ++t) {
-        const uint64_t k = kd + gp_.stage * (T128 / 16);
-        if (!warp_await(s.bp, t & 1, err, DERR_MMA_WAIT, s.abort)) break;  // dS_t written
+        const uint64_t k = kd + gp_.stage * (T64 / 16);
+        go = warp_await(s.bp, t & 1, err, DERR_MMA_WAIT, s.abort);  // dS_t written
+        if (!go) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < 4 || t < nwin) tc_mma_f16_ta(tQ, tdS + 8 * kk, k + kk * kMnStep, idQ, (t | kk) ? 1u : 0u);
-          if (t >= nwin) {
-            // the sinks' dV = P^T dO and dK = dS^T Q over this block's queries, in the columns of S and
-            // dP: P and dS read MN-major.  Rows 64..127 of the products come from the addresses 1024
-            // bytes further (inside the CTA's shared memory) and are not read.
-            const uint32_t p = smem_u32(sinkP), ds = smem_u32(sinkdS), q = smem_u32(s.a), dO = smem_u32(s.b);
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16_ta(tQ, tdS + 8 * kk, k + kk * kMnStep, idQ, (t | kk) ? 1u : 0u);
+          tc_commit(s.bo);
+          tc_commit(&s.empty[gp_.stage]);
+        }
+        gp_.next(stages);
+      }
+      if (sink_tile && go) {
+        // The sinks' dV = P^T dO and dK = dS^T Q over this block's queries, in the columns of S and dP:
+        // P (in the value tiles' place) and dS (in the key tiles') read MN-major.  Rows 64..127 of the
+        // products come from the addresses 1024 bytes further (inside the CTA's shared memory) and are
+        // not read.  Q comes once more, as a tile.
+        go = warp_await(s.brow, 0, err, DERR_MMA_WAIT, s.abort);  // P, dS written, the table's sums done with
+        if (go) {
+          if (elect_one()) {
+            mbar_arrive_expect_tx(s.bsink, T128);
+            tma_load_3d(sinkQ, tq128, h * HD, q0, b, s.bsink);
+          }
+          __syncwarp();
+          go = warp_await(s.bsink, 0, err, DERR_MMA_WAIT, s.abort);
+        }
+        if (go) {
+          if (n - q0 < 128) {
+            zero_rows(sinkQ, n - q0, 128, ln);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t p = smem_u32(ringV), ds = smem_u32(ringK), q = smem_u32(sinkQ), dO = smem_u32(sdO);
 #pragma unroll 1
             for (int kk = 0; kk < 8; ++kk) {
               tc_mma_f16(tS, sw128_desc(p + kk * 2048, 1024, 1024), mndesc(dO, kk), idT, kk ? 1u : 0u);
               tc_mma_f16(tP, sw128_desc(ds + kk * 2048, 1024, 1024), mndesc(q, kk), idT, kk ? 1u : 0u);
             }
+            tc_commit(s.bsd);
           }
-          tc_commit(s.bo);
-          tc_commit(&s.empty[gp_.stage]);
         }
-        gp_.next(stages);
       }
       if (elect_one()) drain_products(&s.bfin[1], err);
       __syncwarp();
@@ -859,17 +871,30 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
     const int g = warp >> 2, r = tid & 127, qi = q0 + r;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const RowWait wait{err, s.abort};
-    RowSync sync{s.brow, wait, 0u};
-    const Bias& bias = s.bias;
+    {  // Q into tensor memory: half a row a thread, zeros for padded rows
+      uint32_t u[16];
+      const uint4* src = reinterpret_cast<const uint4*>(qkv + (row0 + min(qi, n - 1)) * ld + h * HD + 32 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = qi < n ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        u[4 * i] = x.x;
+        u[4 * i + 1] = x.y;
+        u[4 * i + 2] = x.z;
+        u[4 * i + 3] = x.w;
+      }
+      tmem_st16(tQa + lane + 16 * g, u);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive1(s.bq);
+    }
     const int nend = a.last / 32 + 1;
     float farS = 0.f, farP = 0.f;  // the last bucket's sums
     float rowS = 0.f;              // all of this thread's dS
     if (MODE == 2) {
-      if (tid < accs)
-        for (int k = 0; k < a.ranks; ++k) {
-          accS[k * accs + tid] = 0.f;
-          accP[k * accs + tid] = __float2half(0.f);
-        }
+      for (int k = 0; k < a.ranks; ++k) {
+        accS[k * BWD_ROWS + tid] = 0.f;
+        accP[k * BWD_ROWS + tid] = __float2half(0.f);
+      }
       for (int x = tid; x < nend; x += BWD_ROWS) {
         uint32_t w = 0u;
         for (int k = 0; k < a.ranks; ++k)
@@ -877,182 +902,181 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq, const 
         ends[x] = w;
       }
     }
-    if (MODE) s.bias.fill<BWD_ROWS>(a, h, tid, sync);
+    if (MODE) bias.fill<BWD_ROWS>(a, h, tid);
     auto put = [&](int rank, float x, float p) {
-      accS[rank * accs + tid] += x;
-      __half* at = accP + rank * accs + tid;
+      accS[rank * BWD_ROWS + tid] += x;
+      __half* at = accP + rank * BWD_ROWS + tid;
       *at = __float2half(__half2float(*at) + p);
     };
-    // column chunks of 32: one a warpgroup, or two for each of the first two
-    const int chunk_step = MODE == 2 ? accs / 128 : 4;
     const float2 LD = ws_.ld[(static_cast<int64_t>(b) * a.heads + h) * pad128(a.seq) + qi];
     const f32x2 scale2 = pack2(kScaleLog2, kScaleLog2), D2 = pack2(LD.y, LD.y);
     for (int t = 0; t < nt; ++t) {
       const bool sink = t >= nwin;
-      const int chunks = sink ? 2 : 4;
+      const int j0 = tile_key(t) + 32 * g;  // the key of this thread's column 0
+      const int d = qi - j0;                // distances d, d - 1, .. d - 31
+      int rank = 0;
+      bool flat = true;
+      if (MODE) {
+        rank = bias.rank_of(d);
+        flat = __all_sync(0xffffffffu, rank == bias.rank_of(d - 31));
+      }
       wait(s.bs, t & 1);
       tc_fence_after();
-#pragma unroll 1
-      for (int c = g; c < chunks && (MODE < 2 || g < chunk_step); c += chunk_step) {
-        const int j0 = tile_key(t) + 32 * c;  // the key of this thread's column 0
-        const int d = qi - j0;                // distances d, d - 1, .. d - 31
-        int rank = 0;
-        bool flat = true;
-        if (MODE) {
-          rank = bias.rank_of(d);
-          flat = __all_sync(0xffffffffu, rank == bias.rank_of(d - 31));
-        }
-        float v[64];  // S (32 columns), then dP (32 columns), one round trip
-        {
-          const uint32_t at[2] = {tS + lane + 32 * c, tP + lane + 32 * c};
-          ld_rows<2>(at, v);
-        }
-        if (c + chunk_step >= chunks) {  // this thread's last chunk of the tile
-          tc_fence_before();
-          mbar_arrive1(s.bsc);
-        }
-        if (MODE && !flat) {
-          const float* at = bias.value + Bias::kLow + d;
+      float v[64];  // S (32 columns), then dP (32 columns), one round trip
+      {
+        const uint32_t at[2] = {tS + lane + 32 * g, tP + lane + 32 * g};
+        ld_rows<2>(at, v);
+      }
+      tc_fence_before();
+      mbar_arrive1(s.bsc);
+      if (MODE && !flat) {
+        const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kScaleLog2, at[-i] + LD.x);
-        } else {
-          const float x = (MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f) + LD.x;
-          const f32x2 x2 = pack2(x, x);
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kScaleLog2, at[-i] + LD.x);
+      } else {
+        const float x = (MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f) + LD.x;
+        const f32x2 x2 = pack2(x, x);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) unpack2(fma2(pack2(v[i], v[i + 1]), scale2, x2), v[i], v[i + 1]);
-        }
-        if (__builtin_expect(sink || !(j0 + 31 <= q0 && q0 + 127 - j0 < a.window), 0)) {
-          const uint32_t window = sink ? 0u : ~bits_to(d - a.window);
-          hide32(v, bits_to(d) & (window | bits_to(a.sinks - j0 - 1)));
-        }
+        for (int i = 0; i < 32; i += 2) unpack2(fma2(pack2(v[i], v[i + 1]), scale2, x2), v[i], v[i + 1]);
+      }
+      if (__builtin_expect(sink || !(j0 + 31 <= q0 && q0 + 127 - j0 < a.window), 0)) {
+        const uint32_t window = sink ? 0u : ~bits_to(d - a.window);
+        hide32(v, bits_to(d) & (window | bits_to(a.sinks - j0 - 1)));
+      }
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          v[i] = ex2_approx(v[i]);  // P
-          v[i + 1] = ex2_approx(v[i + 1]);
-          unpack2(mul2(pack2(v[i], v[i + 1]), add2(pack2(v[32 + i], v[33 + i]), D2)), v[32 + i], v[33 + i]);  // dS
-        }
-        if (MODE == 2) {
-          f32x2 s2[2] = {0ull, 0ull};
+      for (int i = 0; i < 32; i += 2) {
+        v[i] = ex2_approx(v[i]);  // P
+        v[i + 1] = ex2_approx(v[i + 1]);
+        unpack2(mul2(pack2(v[i], v[i + 1]), add2(pack2(v[32 + i], v[33 + i]), D2)), v[32 + i], v[33 + i]);  // dS
+      }
+      if (MODE == 2) {
+        f32x2 s2[2] = {0ull, 0ull};
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], pack2(v[32 + i], v[33 + i]));
-          float x0, x1;
-          unpack2(add2(s2[0], s2[1]), x0, x1);
-          rowS += x0 + x1;
-          if (flat) {
-            f32x2 p2[2] = {0ull, 0ull};
+        for (int i = 0; i < 32; i += 2) s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], pack2(v[32 + i], v[33 + i]));
+        float x0, x1;
+        unpack2(add2(s2[0], s2[1]), x0, x1);
+        rowS += x0 + x1;
+        if (flat) {
+          f32x2 p2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) p2[(i >> 1) & 1] = add2(p2[(i >> 1) & 1], pack2(v[i], v[i + 1]));
-            float y0, y1;
-            unpack2(add2(p2[0], p2[1]), y0, y1);
-            if (__all_sync(0xffffffffu, rank == a.ranks - 1)) {
-              farS += x0 + x1;
-              farP += y0 + y1;
-            } else {
-              put(rank, x0 + x1, y0 + y1);
-            }
+          for (int i = 0; i < 32; i += 2) p2[(i >> 1) & 1] = add2(p2[(i >> 1) & 1], pack2(v[i], v[i + 1]));
+          float y0, y1;
+          unpack2(add2(p2[0], p2[1]), y0, y1);
+          if (__all_sync(0xffffffffu, rank == a.ranks - 1)) {
+            farS += x0 + x1;
+            farP += y0 + y1;
           } else {
-            // bit i: column i ends its bucket (its distance is the bucket's first).  From the bitmap,
-            // distances low .. low + 31, the reverse of the columns' order.
-            const int low = d - 31;
-            const int wd = low >> 5;  // floor division
-            const uint32_t w0 = wd >= 0 && wd < nend ? ends[wd] : 0u;
-            const uint32_t w1 = wd + 1 >= 0 && wd + 1 < nend ? ends[wd + 1] : 0u;
-            const uint32_t stop = __brev(__funnelshift_r(w0, w1, low & 31));
-            float runS = 0.f, runP = 0.f;
-            // the first bucket's sums wait in a spare word, the next ones go to their own
-            uint32_t atS = smem_u32(accS + a.ranks * accs + tid), atP = smem_u32(accP + a.ranks * accs + tid);
-            int step = (rank - 1 - a.ranks) * accs;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              runS += v[32 + i];
-              runP += v[i];
-              const uint32_t ends_here = stop & (1u << i);
-              store_if(ends_here, atS, runS, atP, runP);
-              runS = ends_here ? 0.f : runS;
-              runP = ends_here ? 0.f : runP;
-              const int by = ends_here ? step : 0;
-              step = ends_here ? -accs : step;
-              atS += 4 * by;
-              atP += 2 * by;
-            }
-            if (stop) put(rank, accS[a.ranks * accs + tid], __half2float(accP[a.ranks * accs + tid]));
-            rank -= __popc(stop);
-            if (rank >= 0) put(rank, runS, runP);  // (below 0: only columns behind the diagonal were left)
+            put(rank, x0 + x1, y0 + y1);
           }
-        }
-        uint32_t u[16];
+        } else {
+          // bit i: column i ends its bucket (its distance is the bucket's first).  From the bitmap,
+          // distances low .. low + 31, the reverse of the columns' order.
+          const int low = d - 31;
+          const int wd = low >> 5;  // floor division
+          const uint32_t w0 = wd >= 0 && wd < nend ? ends[wd] : 0u;
+          const uint32_t w1 = wd + 1 >= 0 && wd + 1 < nend ? ends[wd + 1] : 0u;
+          const uint32_t stop = __brev(__funnelshift_r(w0, w1, low & 31));
+          float runS = 0.f, runP = 0.f;
+          // the first bucket's sums wait in a spare word, the next ones go to their own
+          uint32_t atS = smem_u32(accS + a.ranks * BWD_ROWS + tid), atP = smem_u32(accP + a.ranks * BWD_ROWS + tid);
+          int step = (rank - 1 - a.ranks) * BWD_ROWS;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = pack_bf16x2(v[32 + 2 * i], v[33 + 2 * i]);
-        if (t > 0 && c == g) {  // the previous dQ product reads dS
-          wait(s.bo, (t - 1) & 1);
-          tc_fence_after();
-        }
-        tmem_st16(tdS + lane + 16 * c, u);
-        if (sink) {
-          st_row32_bf16(sinkP, r, 4 * c, v);
-          st_row32_bf16(sinkdS, r, 4 * c, v + 32);
-          fence_proxy_async_smem();
+          for (int i = 0; i < 32; ++i) {
+            runS += v[32 + i];
+            runP += v[i];
+            const uint32_t ends_here = stop & (1u << i);
+            store_if(ends_here, atS, runS, atP, runP);
+            runS = ends_here ? 0.f : runS;
+            runP = ends_here ? 0.f : runP;
+            const int by = ends_here ? step : 0;
+            step = ends_here ? -BWD_ROWS : step;
+            atS += 4 * by;
+            atP += 2 * by;
+          }
+          if (stop) put(rank, accS[a.ranks * BWD_ROWS + tid], __half2float(accP[a.ranks * BWD_ROWS + tid]));
+          rank -= __popc(stop);
+          if (rank >= 0) put(rank, runS, runP);  // (below 0: only columns behind the diagonal were left)
         }
       }
-      if (g >= chunks || (MODE == 2 && g >= chunk_step)) {  // no columns for this warpgroup
-        mbar_arrive1(s.bsc);
-        if (t > 0) wait(s.bo, (t - 1) & 1);
+      uint32_t u[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) u[i] = pack_bf16x2(v[32 + 2 * i], v[33 + 2 * i]);
+      if (t > 0) {  // the previous dQ product reads dS
+        wait(s.bo, (t - 1) & 1);
+        tc_fence_after();
       }
+      tmem_st16(tdS + lane + 16 * g, u);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive1(s.bp);
-    }
-    wait(s.bo, (nt - 1) & 1);
-    tc_fence_after();
-    if (g < 2) {
-      stage_row32(tQ + lane + 32 * g, s.a, r, 4 * g, 0.125f, qi < n);  // in Q's place: its products are done
-      send_tile(tg, h * HD, q0, b, s.a, 1, 256, tid == 0);
-    } else if (sink_tile) {  // dV | dK
-      float* part =
-          ws_.far + (((static_cast<int64_t>(b) * a.heads + h) * nqb + qb) * a.sinks + r) * 128 + 64 * (g - 2);
+      if (sink) {  // the last tile: its dP is there, so the value tiles' place is free; the key tiles' after dQ
+        st_row32_bf16(ringV, r, 4 * g, v);
+        wait(s.bo, t & 1);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(ringK + swz(r, 4 * g + i)) =
+              make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+      }
+    }
+    if (MODE == 2) {
+      put(a.ranks - 1, farS, farP);
+      row_e[tid] = rowS;
+      rows_barrier<BWD_ROWS>();
+      // the error of D: a row's dS sum to it instead of 0 (a padded row's sums are 0 themselves)
+      float e[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) e[c] = row_e[32 * c + ln] + row_e[32 * c + ln + 128];
+      for (int k = warp; k < a.ranks; k += BWD_ISSUER) {
+        float x = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int at = k * BWD_ROWS + 32 * c + ln;
+          x += accS[at] - e[c & 3] * __half2float(accP[at]);
+        }
+        x = warp_sum(x);
+        if (ln == 0) tab[k] = x;
+      }
+    }
+    if (sink_tile) {
+      fence_proxy_async_smem();
+      mbar_arrive1(s.brow);
+      wait(s.bsd, 0);
+      tc_fence_after();
+      float* part = ws_.far + (((static_cast<int64_t>(b) * a.heads + h) * nqb + qb) * a.sinks + r) * 128 + 64 * g;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // dV | dK
         float x[32];
-        ld_row32((g == 3 ? tP : tS) + lane + 32 * c, x);
+        ld_row32((g ? tP : tS) + lane + 32 * c, x);
         if (r < a.sinks) {
 #pragma unroll
           for (int i = 0; i < 32; i += 8) store8(part + 32 * c + i, x + i);
         }
       }
+    } else {
+      wait(s.bo, (nt - 1) & 1);
+      tc_fence_after();
     }
-    if (MODE == 2) {
-      if (tid < accs) put(a.ranks - 1, farS, farP);
-      row_e[tid] = rowS;
-      sync();
-      // the error of D: a row's dS sum to it instead of 0 (a padded row's sums are 0 themselves)
-      float e[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float* at = row_e + 32 * c + ln;
-        e[c] = (at[0] + at[128]) + (at[256] + at[384]);
-      }
-      for (int k = warp; k < a.ranks; k += BWD_ISSUER) {
-        float x = 0.f;
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (32 * c < accs) {
-            const int at = k * accs + 32 * c + ln;
-            x += accS[at] - e[c & 3] * __half2float(accP[at]);
-          }
-        x = warp_sum(x);
-        if (ln == 0) tab[k] = x;
-      }
-    }
+    stage_row32(tQ + lane + 32 * g, sdO, r, 4 * g, 0.125f, qi < n);  // in dO's place: its products are done
+    send_tile(tg, h * HD, q0, b, sdO, 1, BWD_ROWS, tid == 0);
   }
   s.finish(warp, tmem);
 }
 
 // dK/dV CTA of 128 keys of one key/value head: iterations t = 0 .. group * nq - 1
-// over the 128-query blocks that see them, one query head after the other.
+// over the 64-query blocks that see them, one query head after the other.  dV
+// and dK fill what S^T and dP^T leave of the tensor memory, so P^T and dS^T go
+// through shared memory.
 template <int MODE>
-__device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const CUtensorMap* td, const CUtensorMap* tg,
-                               const WindowScratch& ws_, __nv_bfloat16* __restrict__ dqkv, int item, int* err, uint8_t* sm) {
-  BwdSmem s(sm, DKV_STAGES * DKV_STAGE, DKV_LD_BYTES, a);
+__device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
+                               const CUtensorMap* td64, const CUtensorMap* tg, const WindowScratch& ws_,
+                               __nv_bfloat16* __restrict__ dqkv, int item, int stages, int* err, uint8_t* sm) {
+  uint8_t *sK = sm, *sV = sm + T128, *sPt = sm + DKV_P, *sdSt = sm + DKV_DS, *ring = sm + DKV_RING;
+  float2* sLD = reinterpret_cast<float2*>(ring + stages * DKV_STAGE);
+  uint8_t* rest = ring + stages * (DKV_STAGE + DKV_LD);
+  BwdBars s(rest);
+  rest += BWD_BARS;
+  Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
+
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int kvh = item % a.kv_heads;
   const int b = (item / a.kv_heads) % a.nseq;
@@ -1075,61 +1099,63 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
   // the queries of this block: those whose window reaches it, and, for the sinks' block, the rest of
   // the 128-query blocks whose window reaches it (the dQ CTAs of the others account for the sinks)
   const int imax = min(n - 1, kb == 0 && a.sinks > 0 ? first_far_block(a.window) * 128 - 1 : k0 + 127 + a.window - 1);
-  const int nq = imax / 128 - kb + 1;
+  const int i0 = k0 / 64, nq = imax / 64 - i0 + 1;
   const int niter = group * nq;
-
-  auto load_q = [&](int t, int stage) {
-    const int lh = h0 + t / nq, lq = kb + t % nq;
-    uint8_t* dst = s.ring + stage * DKV_STAGE;
+  auto load_q = [&](int lh, int lq, int stage) {
+    uint8_t* dst = ring + stage * DKV_STAGE;
     uint64_t* full = &s.full[stage];
-    mbar_arrive_expect_tx(full, 2 * T128 + 128 * 8);
-    tma_load_3d(dst, tq, lh * HD, lq * 128, b, full);
-    tma_load_3d(dst + T128, td, lh * HD, lq * 128, b, full);
-    bulk_load(s.ld + stage * 128, ws_.ld + (static_cast<int64_t>(b) * a.heads + lh) * seqpad + lq * 128, 128 * 8, full);
+    mbar_arrive_expect_tx(full, DKV_STAGE + DKV_LD);
+    tma_load_3d(dst, tq64, lh * HD, lq * 64, b, full);
+    tma_load_3d(dst + T64, td64, lh * HD, lq * 64, b, full);
+    bulk_load(sLD + stage * 64, ws_.ld + (static_cast<int64_t>(b) * a.heads + lh) * seqpad + lq * 64, DKV_LD, full);
   };
-  const int ahead = min(niter, DKV_STAGES);
+  const int ahead = min(niter, stages);
   const uint32_t tmem = s.start(warp, [&] {
-    mbar_arrive_expect_tx(s.b0, 2 * T128);
-    tma_load_3d(s.a, tq, kcol, k0, b, s.b0);
-    tma_load_3d(s.b, tq, vcol, k0, b, s.b0);
-    for (int t = 0; t < ahead; ++t) load_q(t, t);
+    mbar_arrive_expect_tx(s.one, 2 * T128);
+    tma_load_3d(sK, tq128, kcol, k0, b, s.one);
+    tma_load_3d(sV, tq128, vcol, k0, b, s.one);
+    for (int t = 0; t < ahead; ++t) load_q(h0 + t / nq, i0 + t % nq, t);
   });
-  // S^T at 0, dP^T at 128, dV at 256, dK at 320, P^T (bf16) at 384, dS^T at 448
-  const uint32_t tS = tmem, tdP = tmem + 128, tV = tmem + 256, tK = tmem + 320, tP = tmem + 384, tdS = tmem + 448;
+  // S^T at 0, dP^T at 64, dV at 128, dK at 192
+  const uint32_t tS = tmem, tdP = tmem + 64, tV = tmem + 128, tK = tmem + 192;
 
   if (warp >= BWD_ISSUER) {
     give_registers_bwd();
     if (warp == BWD_ISSUER + 2) {  // ---- loader ----
       if (elect_one()) {
         RingPos lp;
-        for (int i = 0; i < ahead; ++i) lp.next(DKV_STAGES);
-        int t = ahead;
+        for (int i = 0; i < ahead; ++i) lp.next(stages);
+        int t = ahead, lh = h0 + t / nq, lq = i0 + t % nq;
         for (; t < niter; ++t) {
           if (!lane_await(&s.empty[lp.stage], lp.parity ^ 1u, err, DERR_TMA_WAIT, s.abort)) break;
-          load_q(t, lp.stage);
-          lp.next(DKV_STAGES);
+          load_q(lh, lq, lp.stage);
+          lp.next(stages);
+          if (++lq == i0 + nq) {
+            lq = i0;
+            ++lh;
+          }
         }
-        drain_copies(s.full, t, DKV_STAGES, err);
-        mbar_wait_bounded(s.b0, 0, err, DERR_DRAIN_WAIT);
+        drain_copies(s.full, t, stages, err);
+        mbar_wait_bounded(s.one, 0, err, DERR_DRAIN_WAIT);
       }
       __syncwarp();
     } else if (warp == BWD_ISSUER) {  // ---- S^T = K Q_t^T, dP^T = V dO_t^T ----
-      constexpr uint32_t idSP = mma_idesc_bf16(128, 128, false, false);
-      const uint64_t k = kdesc0(smem_u32(s.a)), v = kdesc0(smem_u32(s.b)), qd = kdesc0(smem_u32(s.ring));
+      constexpr uint32_t idSP = mma_idesc_bf16(128, 64, false, false);
+      const uint64_t k = kdesc0(smem_u32(sK)), v = kdesc0(smem_u32(sV)), qd = kdesc0(smem_u32(ring));
       RingPos sp;
-      int qb = kb;
-      bool go = warp_await(s.b0, 0, err, DERR_MMA_WAIT, s.abort);
+      int qb = i0;
+      bool go = warp_await(s.one, 0, err, DERR_MMA_WAIT, s.abort);
       for (int t = 0; t < niter && go; ++t) {
         go = warp_await(&s.full[sp.stage], sp.parity, err, DERR_MMA_WAIT, s.abort);
-        const int left = n - qb * 128;
-        if (left < 128) {  // padded queries: P = dS = 0, the rows themselves may be anything
-          uint8_t* at = s.ring + sp.stage * DKV_STAGE;
-          zero_rows(at, left, 128, ln);
-          zero_rows(at + T128, left, 128, ln);
+        const int left = n - qb * 64;
+        if (left < 64) {  // padded queries: P = dS = 0, the rows themselves may be anything
+          uint8_t* at = ring + sp.stage * DKV_STAGE;
+          zero_rows(at, left, 64, ln);
+          zero_rows(at + T64, left, 64, ln);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint64_t q = qd + sp.stage * (DKV_STAGE / 16), dO = q + T128 / 16;
+        const uint64_t q = qd + sp.stage * (DKV_STAGE / 16), dO = q + T64 / 16;
         if (t > 0) go = go && warp_await(s.bsc, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // block t-1's read out
         if (!go) break;
         tc_fence_after();
@@ -1140,28 +1166,28 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
           for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tdP, v + kk * kKStep, dO + kk * kKStep, idSP, kk ? 1u : 0u);
           tc_commit(s.bs);
         }
-        if (++qb == kb + nq) qb = kb;
-        sp.next(DKV_STAGES);
+        if (++qb == i0 + nq) qb = i0;
+        sp.next(stages);
       }
       if (elect_one()) drain_products(&s.bfin[0], err);
       __syncwarp();
     } else if (warp == BWD_ISSUER + 1) {  // ---- dV += P^T dO_t, dK += dS^T Q_t ----
       constexpr uint32_t idKV = mma_idesc_bf16(128, 64, false, true);
-      const uint64_t qd = mndesc0(smem_u32(s.ring));
+      const uint64_t pt = kdesc0(smem_u32(sPt)), dst = kdesc0(smem_u32(sdSt)), qd = mndesc0(smem_u32(ring));
       RingPos gp_;
       for (int t = 0; t < niter; ++t) {
-        const uint64_t q = qd + gp_.stage * (DKV_STAGE / 16), dO = q + T128 / 16;
+        const uint64_t q = qd + gp_.stage * (DKV_STAGE / 16), dO = q + T64 / 16;
         if (!warp_await(s.bp, t & 1, err, DERR_MMA_WAIT, s.abort)) break;  // P^T, dS^T of block t written
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) tc_mma_f16_ta(tV, tP + 8 * kk, dO + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tV, pt + kk * kKStep, dO + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) tc_mma_f16_ta(tK, tdS + 8 * kk, q + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tK, dst + kk * kKStep, q + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
           tc_commit(s.bo);
           tc_commit(&s.empty[gp_.stage]);
         }
-        gp_.next(DKV_STAGES);
+        gp_.next(stages);
       }
       if (elect_one()) drain_products(&s.bfin[1], err);
       __syncwarp();
@@ -1171,103 +1197,84 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
     const int g = warp >> 2, r = tid & 127, kr = k0 + r;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const RowWait wait{err, s.abort};
-    RowSync sync{s.brow, wait, 0u};
-    const Bias& bias = s.bias;
     RingPos rp;
-    int hq = h0, qb = kb;
+    int hq = h0, qb = i0;
     const f32x2 scale2 = pack2(kScaleLog2, kScaleLog2);
     for (int t = 0; t < niter; ++t) {
-      if (MODE && qb == kb) s.bias.fill<BWD_ROWS>(a, hq, tid, sync);
-      const int q0 = qb * 128 + 32 * g;  // the query of this thread's column 0
-      const int d = q0 - kr;             // distances d .. d + 31
+      if (MODE && qb == i0) bias.fill<BWD_ROWS>(a, hq, tid);
+      const int q0 = qb * 64 + 32 * g;  // the query of this thread's column 0
+      const int d = q0 - kr;            // distances d .. d + 31
       bool flat = true;
       if (MODE) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d + 31));
-      uint32_t see = 0xffffffffu;
-      bool any = true;
-      if (__builtin_expect(!(q0 >= k0 + 127 && q0 + 31 - k0 < a.window), 0)) {  // some pair may be hidden
-        see = bits_to(kr < a.sinks ? 31 : a.window - 1 - d) & ~bits_to(-d - 1);
-        any = __any_sync(0xffffffffu, see != 0u);
-      }
       wait(&s.full[rp.stage], rp.parity);  // the block's -lse and -D came with its tiles
       wait(s.bs, t & 1);
       tc_fence_after();
-      uint32_t up[16], us[16];
-      if (any) {
-        float v[64];  // S^T (32 columns), then dP^T (32 columns), one round trip
-        {
-          const uint32_t at[2] = {tS + lane + 32 * g, tdP + lane + 32 * g};
-          ld_rows<2>(at, v);
-        }
-        tc_fence_before();
-        mbar_arrive1(s.bsc);
-        const float4* LD = reinterpret_cast<const float4*>(s.ld + rp.stage * 128 + 32 * g);  // two queries each
-        if (MODE && !flat) {
-          const float* at = bias.value + Bias::kLow + d;
-#pragma unroll
-          for (int q = 0; q < 32; q += 2) {
-            const float4 x = LD[q / 2];
-            unpack2(fma2(pack2(v[q], v[q + 1]), scale2, add2(pack2(x.x, x.z), pack2(at[q], at[q + 1]))), v[q], v[q + 1]);
-            unpack2(add2(pack2(v[32 + q], v[33 + q]), pack2(x.y, x.w)), v[32 + q], v[33 + q]);
-          }
-        } else {
-          const float c = MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f;
-          const f32x2 c2 = pack2(c, c);
-#pragma unroll
-          for (int q = 0; q < 32; q += 2) {
-            const float4 x = LD[q / 2];
-            f32x2 l2 = pack2(x.x, x.z);
-            if (MODE) l2 = add2(l2, c2);
-            unpack2(fma2(pack2(v[q], v[q + 1]), scale2, l2), v[q], v[q + 1]);
-            unpack2(add2(pack2(v[32 + q], v[33 + q]), pack2(x.y, x.w)), v[32 + q], v[33 + q]);
-          }
-        }
-        if (__builtin_expect(!__all_sync(0xffffffffu, see == 0xffffffffu), 0)) hide32(v, see);
+      float v[64];  // S^T (32 columns), then dP^T (32 columns), one round trip
+      {
+        const uint32_t at[2] = {tS + lane + 32 * g, tdP + lane + 32 * g};
+        ld_rows<2>(at, v);
+      }
+      tc_fence_before();
+      mbar_arrive1(s.bsc);
+      const float4* LD = reinterpret_cast<const float4*>(sLD + rp.stage * 64 + 32 * g);  // two queries each
+      if (MODE && !flat) {
+        const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
         for (int q = 0; q < 32; q += 2) {
-          const float p0 = ex2_approx(v[q]), p1 = ex2_approx(v[q + 1]);  // P^T
-          float s0, s1;
-          unpack2(mul2(pack2(p0, p1), pack2(v[32 + q], v[33 + q])), s0, s1);  // dS^T
-          up[q / 2] = pack_bf16x2(p0, p1);
-          us[q / 2] = pack_bf16x2(s0, s1);
+          const float4 x = LD[q / 2];
+          unpack2(fma2(pack2(v[q], v[q + 1]), scale2, add2(pack2(x.x, x.z), pack2(at[q], at[q + 1]))), v[q], v[q + 1]);
+          unpack2(add2(pack2(v[32 + q], v[33 + q]), pack2(x.y, x.w)), v[32 + q], v[33 + q]);
         }
       } else {
-        mbar_arrive1(s.bsc);
+        const float c = MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f;
+        const f32x2 c2 = pack2(c, c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) up[i] = us[i] = 0u;
+        for (int q = 0; q < 32; q += 2) {
+          const float4 x = LD[q / 2];
+          f32x2 l2 = pack2(x.x, x.z);
+          if (MODE) l2 = add2(l2, c2);
+          unpack2(fma2(pack2(v[q], v[q + 1]), scale2, l2), v[q], v[q + 1]);
+          unpack2(add2(pack2(v[32 + q], v[33 + q]), pack2(x.y, x.w)), v[32 + q], v[33 + q]);
+        }
       }
-      if (t > 0) {  // the previous dV, dK products read P^T and dS^T
-        wait(s.bo, (t - 1) & 1);
-        tc_fence_after();
+      if (__builtin_expect(!(q0 >= k0 + 127 && q0 + 31 - k0 < a.window), 0))  // some pair may be hidden
+        hide32(v, bits_to(kr < a.sinks ? 31 : a.window - 1 - d) & ~bits_to(-d - 1));
+#pragma unroll
+      for (int q = 0; q < 32; q += 2) {
+        v[q] = ex2_approx(v[q]);  // P^T
+        v[q + 1] = ex2_approx(v[q + 1]);
+        unpack2(mul2(pack2(v[q], v[q + 1]), pack2(v[32 + q], v[33 + q])), v[32 + q], v[33 + q]);  // dS^T
       }
-      tmem_st16(tP + lane + 16 * g, up);
-      tmem_st16(tdS + lane + 16 * g, us);
-      tmem_st_wait();
+      if (t > 0) wait(s.bo, (t - 1) & 1);  // the previous dV, dK products read P^T and dS^T
+      st_row32_bf16(sPt, r, 4 * g, v);
+      st_row32_bf16(sdSt, r, 4 * g, v + 32);
+      fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive1(s.bp);
-      rp.next(DKV_STAGES);
-      if (++qb == kb + nq) {
-        qb = kb;
+      rp.next(stages);
+      if (++qb == i0 + nq) {
+        qb = i0;
         ++hq;
       }
     }
     wait(s.bo, (niter - 1) & 1);
     tc_fence_after();
-    {
-      // warpgroups 0, 1 store dV, 2, 3 dK (32 columns each), in the place of V and K, whose products are
-      // done.  Of the sinks' rows the finish kernel makes the sum with the query blocks far from them.
-      const bool on = ws_.far && kr < a.sinks && kr < n;
-      const bool is_k = g >= 2;
-      const uint32_t acc = (is_k ? tK : tV) + lane + 32 * (g & 1);
-      uint8_t* tile_out = is_k ? s.a : s.b;
-      stage_row32(acc, tile_out, r, 4 * (g & 1), is_k ? 0.125f : 1.f, kr < n);
-      send_tile(tg, is_k ? kcol : vcol, k0, b, tile_out, 1 + (g >> 1), 256, (tid & 255) == 0);
-      if (ws_.far && kb == 0) {  // dV | dK
-        float* part = ws_.base + ((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + r) * 128 + 32 * g;
-        float x[32];
-        ld_row32(acc, x);
-        if (on) {
+    // warpgroup 0 stores dV, 1 dK, in the place of V and K, whose products are done.  Of the sinks'
+    // rows the finish kernel makes the sum with the query blocks far from them.
+    const uint32_t acc = (g ? tK : tV) + lane;
+    uint8_t* tile_out = g ? sK : sV;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) store8(part + i, x + i);
+    for (int c = 0; c < 2; ++c) stage_row32(acc + 32 * c, tile_out, r, 4 * c, g ? 0.125f : 1.f, kr < n);
+    send_tile(tg, g ? kcol : vcol, k0, b, tile_out, 1 + g, 128, r == 0);
+    if (ws_.far && kb == 0) {  // dV | dK
+      float* part = ws_.base + ((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + r) * 128 + 64 * g;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x[32];
+        ld_row32(acc + 32 * c, x);
+        if (kr < a.sinks && kr < n) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) store8(part + 32 * c + i, x + i);
         }
       }
     }
@@ -1277,55 +1284,73 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq, const
 
 // One launch for both kinds, the dK/dV CTAs first (they have more to do).
 template <int MODE>
-__global__ void __launch_bounds__(BWD_THREADS, 1)
-    attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap td,
-                           const __grid_constant__ CUtensorMap tg, const __grid_constant__ WindowArgs a, const __grid_constant__ WindowScratch ws_,
-                           __nv_bfloat16* __restrict__ dqkv, int n_dkv, int stages, int* err) {
+__global__ void __launch_bounds__(BWD_THREADS, 2)
+    attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap tq128,
+                           const __grid_constant__ CUtensorMap td64, const __grid_constant__ CUtensorMap td128,
+                           const __grid_constant__ CUtensorMap tg, const __grid_constant__ WindowArgs a,
+                           const __grid_constant__ WindowScratch ws_, const __nv_bfloat16* __restrict__ qkv,
+                           __nv_bfloat16* __restrict__ dqkv, int n_dkv, int dkv_stages, int dq_stages, int* err) {
   extern __shared__ __align__(1024) uint8_t sm[];
   if (misaligned(sm, err)) return;
   const int x = static_cast<int>(blockIdx.x);
   if (x < n_dkv)
-    window_bwd_dkv<MODE>(a, &tq, &td, &tg, ws_, dqkv, x, err, sm);
+    window_bwd_dkv<MODE>(a, &tq64, &tq128, &td64, &tg, ws_, dqkv, x, dkv_stages, err, sm);
   else
-    window_bwd_dq<MODE>(a, &tq, &td, &tg, ws_, dqkv, x - n_dkv, stages, err, sm);
+    window_bwd_dq<MODE>(a, &tq64, &tq128, &td128, &tg, ws_, qkv, dqkv, x - n_dkv, dq_stages, err, sm);
 }
 
-// Blocks 0 .. n_sink-1: one sink key of one (sequence, key/value head); thread c
-// adds column c of its dV | dK over the query blocks far from it, in order.
-// Blocks n_sink ..: dtable of one head, added over (sequence, query block).
-__global__ void __launch_bounds__(128) attn_window_finish_kernel(const __grid_constant__ WindowArgs a,
-                                                                 const __grid_constant__ WindowScratch ws_,
-                                                                 __nv_bfloat16* __restrict__ dqkv,
-                                                                 float* __restrict__ dtable, int n_sink) {
+// Blocks 0 .. n_sink-1: one sink key of one (sequence, key/value head); thread
+// (slice, c) adds column c of its dV | dK over every fourth far query block, and
+// the slices are added in order.  Blocks n_sink ..: dtable of one head; a warp
+// adds every sixteenth (sequence, query block), lanes over the ranks, and the
+// warps are added in order.
+constexpr int kFinishThreads = 512;
+__global__ void __launch_bounds__(kFinishThreads) attn_window_finish_kernel(const __grid_constant__ WindowArgs a,
+                                                                            const __grid_constant__ WindowScratch ws_,
+                                                                            __nv_bfloat16* __restrict__ dqkv,
+                                                                            float* __restrict__ dtable, int n_sink) {
   griddep_wait();
   griddep_launch();
-  const int nqb = (a.seq + 127) / 128, c = threadIdx.x;
-  int x = static_cast<int>(blockIdx.x);
+  __shared__ double part[kFinishThreads / 32][kMaxBuckets];
+  __shared__ float slice_sum[4][128];
+  const int nqb = (a.seq + 127) / 128, tid = threadIdx.x;
+  const int x = static_cast<int>(blockIdx.x);
   if (x < n_sink) {
+    const int c = tid & 127, slice = tid >> 7;
     const int j = x % a.sinks, kvh = (x / a.sinks) % a.kv_heads, b = x / (a.sinks * a.kv_heads);
     const int n = seq_len(a, b);
     if (j >= n) return;
     const int group = a.heads / a.kv_heads, D = a.heads * HD;
-    float v = ws_.base[((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + j) * 128 + c];
+    float v = slice ? 0.f : ws_.base[((static_cast<int64_t>(b) * a.kv_heads + kvh) * a.sinks + j) * 128 + c];
     for (int g = 0; g < group; ++g) {
       const float* far = ws_.far + (static_cast<int64_t>(b) * a.heads + kvh * group + g) * nqb * a.sinks * 128;
 #pragma unroll 8
-      for (int qb = first_far_block(a.window); qb <= (n - 1) / 128; ++qb)
+      for (int qb = first_far_block(a.window) + slice; qb <= (n - 1) / 128; qb += 4)
         v += far[(static_cast<int64_t>(qb) * a.sinks + j) * 128 + c];
     }
+    slice_sum[slice][c] = v;
+    __syncthreads();
+    if (slice) return;
+    v = ((slice_sum[0][c] + slice_sum[1][c]) + slice_sum[2][c]) + slice_sum[3][c];
     const int64_t ld = static_cast<int64_t>(a.heads + 2 * a.kv_heads) * HD;
     __nv_bfloat16* dst = dqkv + (static_cast<int64_t>(b) * a.seq + j) * ld + D + kvh * HD;
     if (c < 64) dst[a.kv_heads * HD + c] = f2bf(v);
     else dst[c - 64] = f2bf(v * 0.125f);
     return;
   }
-  const int h = x - n_sink;
-  if (c >= a.ranks) return;
-  double s = 0.0;
+  const int h = x - n_sink, warp = tid >> 5, ln = tid & 31;
   const int64_t parts = static_cast<int64_t>(a.nseq) * nqb;
+  for (int k = ln; k < a.ranks; k += 32) {
+    double s = 0.0;
 #pragma unroll 8
-  for (int64_t p = 0; p < parts; ++p) s += ws_.tab[(p * a.heads + h) * a.ranks + c];
-  dtable[static_cast<int64_t>(a.start[c] & 255) * a.heads + h] += static_cast<float>(s);
+    for (int64_t p = warp; p < parts; p += kFinishThreads / 32) s += ws_.tab[(p * a.heads + h) * a.ranks + k];
+    part[warp][k] = s;
+  }
+  __syncthreads();
+  if (tid >= a.ranks) return;
+  double s = 0.0;
+  for (int w = 0; w < kFinishThreads / 32; ++w) s += part[w][tid];
+  dtable[static_cast<int64_t>(a.start[tid] & 255) * a.heads + h] += static_cast<float>(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1447,21 +1472,11 @@ WindowScratch window_scratch(void* base, int nseq, int seq, int heads, int windo
   return w;
 }
 
-constexpr int kMaxSmem = 227 * 1024;
-constexpr int table_bytes(int ranks, int last) {
-  return BWD_ROWS * 4 + (ranks + 1) * table_threads(ranks) * 6 + (last / 32 + 1) * 4;
-}
-constexpr int dq_smem(int stages, int bias_bytes, int table) {
-  return (2 + stages + DQ_V_STAGES) * T128 + BWD_BARS + bias_bytes + table;
-}
-constexpr int dkv_smem(int bias_bytes) {
-  return 2 * T128 + DKV_STAGES * DKV_STAGE + DKV_LD_BYTES + BWD_BARS + bias_bytes;
-}
-static_assert(fwd_smem(2, Bias::bytes(kMaxDistance)) <= kMaxSmem / 2 && fwd_smem(3, 0) <= kMaxSmem / 2, "two forward CTAs share an SM, with the largest table too");
-static_assert(dq_smem(2, Bias::bytes(kMaxDistance), table_bytes(kWideRanks, kMaxDistance)) <= kMaxSmem &&
-                  dq_smem(2, Bias::bytes(kMaxDistance), table_bytes(kMaxBuckets, kMaxDistance)) <= kMaxSmem &&
-                  dkv_smem(Bias::bytes(kMaxDistance)) <= kMaxSmem,
-              "the largest table's sums fit beside two key tiles");
+static_assert(fwd_smem(2, Bias::bytes(kMaxDistance)) <= kHalfSmem && fwd_smem(3, 0) <= kHalfSmem,
+              "two forward CTAs share an SM, with the largest table too");
+static_assert(dq_smem(2, Bias::bytes(kMaxDistance), dq_sums(kMaxBuckets, kMaxDistance), true) <= kMaxSmem &&
+                  dkv_smem(3, Bias::bytes(kMaxDistance)) <= kMaxSmem,
+              "the largest table and its sums fit beside the tiles");
 
 int prepare_attention_window() {
   static std::atomic<unsigned long long> done{0};
@@ -1547,8 +1562,9 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   int* err = device_error_ptr();
   if (!err) return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: no device error word");
   const int64_t cols = static_cast<int64_t>(heads + 2 * kv_heads) * HD, D = static_cast<int64_t>(heads) * HD;
-  CUtensorMap tq, td, tg;
-  if (!make_tmap(&tq, qkv, cols, seq, nseq, 128) || !make_tmap(&td, dout, D, seq, nseq, 128) ||
+  CUtensorMap tq64, tq128, td64, td128, tg;
+  if (!make_tmap(&tq64, qkv, cols, seq, nseq, 64) || !make_tmap(&tq128, qkv, cols, seq, nseq, 128) ||
+      !make_tmap(&td64, dout, D, seq, nseq, 64) || !make_tmap(&td128, dout, D, seq, nseq, 128) ||
       !make_tmap(&tg, dqkv, cols, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: tensor map creation failed");
   const WindowScratch w = window_scratch(scratch, nseq, seq, heads, window, sinks, dtable_acc ? a.ranks : 0);
@@ -1559,17 +1575,29 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   if (rc) return rc;
   const int nqb = (seq + 127) / 128, n_dkv = nqb * kv_heads * nseq, n_dq = nqb * heads * nseq;
   auto kern = dtable_acc ? attn_window_bwd_kernel<2> : (a.ranks ? attn_window_bwd_kernel<1> : attn_window_bwd_kernel<0>);
-  const bool grad = dtable_acc != nullptr;
-  const int bias_bytes = a.ranks ? Bias::bytes(a.last) : 0, sums = grad ? table_bytes(a.ranks, a.last) : 0;
-  const int stages = dq_smem(3, bias_bytes, sums) <= kMaxSmem ? 3 : 2;
-  const int dq_bytes = dq_smem(stages, bias_bytes, sums), dkv_bytes = dkv_smem(bias_bytes);
-  (void)launch_k<true>(kern, n_dkv + n_dq, BWD_THREADS, dq_bytes > dkv_bytes ? dq_bytes : dkv_bytes, s, tq, td, tg, a, w,
-                       static_cast<__nv_bfloat16*>(dqkv), n_dkv, stages, err);
+  // three stages a ring where two CTAs still fit on an SM, or where they do not anyway
+  const int bias_bytes = a.ranks ? Bias::bytes(a.last) : 0;
+  const int sums = dtable_acc ? dq_sums(a.ranks, a.last) : 0;
+  const bool far = w.far != nullptr;
+  auto bytes = [&](int dkv, int dq) {
+    const int x = dkv_smem(dkv, bias_bytes), y = dq_smem(dq, bias_bytes, sums, far);
+    return x > y ? x : y;
+  };
+  int dkv_stages = 3, dq_stages = 3;
+  if (bytes(2, 2) <= kHalfSmem) {
+    if (bytes(3, 2) > kHalfSmem) dkv_stages = 2;
+    if (bytes(dkv_stages, 3) > kHalfSmem) dq_stages = 2;
+  } else if (bytes(3, 3) > kMaxSmem) {
+    dq_stages = 2;
+  }
+  (void)launch_k<true>(kern, n_dkv + n_dq, BWD_THREADS, bytes(dkv_stages, dq_stages), s, tq64, tq128, td64, td128, tg, a,
+                       w, static_cast<const __nv_bfloat16*>(qkv), static_cast<__nv_bfloat16*>(dqkv), n_dkv, dkv_stages,
+                       dq_stages, err);
   rc = check_launch("attention_window_bwd");
   if (rc) return rc;
   const int n_sink = w.far ? nseq * kv_heads * a.sinks : 0;
   if (n_sink || dtable_acc) {
-    (void)launch_k(attn_window_finish_kernel, n_sink + (dtable_acc ? heads : 0), 128, 0, s, a, w,
+    (void)launch_k(attn_window_finish_kernel, n_sink + (dtable_acc ? heads : 0), kFinishThreads, 0, s, a, w,
                    static_cast<__nv_bfloat16*>(dqkv), dtable_acc, n_sink);
     rc = check_launch("attention_window_bwd (finish)");
   }
