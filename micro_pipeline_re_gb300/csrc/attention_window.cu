@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
 //            bo of tile t-1 (it reads P, dS); write them; arrive bp.
 constexpr int BWD_ISSUER = BWD_ROWS / 32;  // the issuers' first warp
 constexpr int DQ_V_STAGES = 2;
-constexpr int BWD_BARS = 256;
+constexpr int BWD_BARS = 1024;  // the barriers come first, at addresses that take no registers
 constexpr int kMaxSmem = 227 * 1024, kHalfSmem = 113 * 1024;  // of a CTA, and of each of two on an SM
 
 struct BwdBars {
@@ -625,7 +625,7 @@ struct BwdBars {
   }
   // first(): the first copies, which leave before anything else is set up
   template <typename F>
-  __device__ __forceinline__ uint32_t start(int warp, F&& first) {
+  __device__ __forceinline__ uint32_t start(int warp, F&& first) const {
     if (threadIdx.x == BWD_THREADS - 32) {
       for (int i = 0; i < 17; ++i) mbar_init(&full[i], 1);
       for (int i = 17; i < 21; ++i) mbar_init(&full[i], BWD_ROWS);
@@ -642,7 +642,7 @@ struct BwdBars {
     tc_fence_after();
     return *tslot;
   }
-  __device__ __forceinline__ void finish(int warp, uint32_t tmem) {
+  __device__ __forceinline__ void finish(int warp, uint32_t tmem) const {
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -661,24 +661,24 @@ __device__ __forceinline__ void store_if(uint32_t on, uint32_t at, float x, uint
       : "memory");
 }
 
-// Shared memory of a dQ CTA: dO | two value tiles | `stages` key tiles |
-// barriers | bias | sums of the table's gradient | a Q tile for the sinks'
+// Shared memory of a dQ CTA: barriers | dO | two value tiles | `stages` key
+// tiles | bias | sums of the table's gradient | a Q tile for the sinks'
 // products, in the place of the sums (which are done by then) where those are
 // large enough.  Q itself is an A operand in tensor memory: the S product then
 // reads 2 KB of shared memory for 32 cycles of tensor work instead of 6.
-constexpr int DQ_V = T128, DQ_K = DQ_V + DQ_V_STAGES * T64;
+constexpr int DQ_DO = BWD_BARS, DQ_V = DQ_DO + T128, DQ_K = DQ_V + DQ_V_STAGES * T64;
 constexpr int dq_sums(int ranks, int last) {
   return BWD_ROWS * 4 + (ranks + 1) * BWD_ROWS * 6 + (last / 32 + 1) * 4;
 }
 constexpr int dq_smem(int stages, int bias_bytes, int sums, bool far) {
   const int tile = T128 + 1024;  // with what its alignment may take
-  return DQ_K + stages * T64 + BWD_BARS + bias_bytes + (far && sums < tile ? tile : sums);
+  return DQ_K + stages * T64 + bias_bytes + (far && sums < tile ? tile : sums);
 }
-// Shared memory of a dK/dV CTA: K | V | P^T | dS^T | `stages` of Q | dO | -lse,
-// -D of the stages' queries | barriers | bias.
-constexpr int DKV_P = 2 * T128, DKV_DS = 3 * T128, DKV_RING = 4 * T128, DKV_STAGE = 2 * T64, DKV_LD = 64 * 8;
+// Shared memory of a dK/dV CTA: barriers | K | V | `stages` of Q | dO | -lse, -D
+// of the stages' queries | bias.
+constexpr int DKV_K = BWD_BARS, DKV_V = DKV_K + T128, DKV_RING = DKV_V + T128, DKV_STAGE = 2 * T64, DKV_LD = 64 * 8;
 constexpr int dkv_smem(int stages, int bias_bytes) {
-  return DKV_RING + stages * (DKV_STAGE + DKV_LD) + BWD_BARS + bias_bytes;
+  return DKV_RING + stages * (DKV_STAGE + DKV_LD) + bias_bytes;
 }
 
 // MODE 0: no bias; 1: bias; 2: bias and its gradient.
@@ -695,11 +695,11 @@ template <int MODE>
 __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
                               const CUtensorMap* td128, const CUtensorMap* tg, const WindowScratch& ws_,
                               const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* __restrict__ dqkv, int item,
-                              int stages, int* err, uint8_t* sm) {
-  uint8_t *sdO = sm, *ringV = sm + DQ_V, *ringK = sm + DQ_K;
+                              int stages, int* err) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const BwdBars s(sm);
+  uint8_t *sdO = sm + DQ_DO, *ringV = sm + DQ_V, *ringK = sm + DQ_K;
   uint8_t* rest = ringK + stages * T64;
-  BwdBars s(rest);
-  rest += BWD_BARS;
   Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
   if (MODE) rest += Bias::bytes(a.last);
   float* row_e = reinterpret_cast<float*>(rest);                               // [2][128]
@@ -1064,17 +1064,21 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
 
 // dK/dV CTA of 128 keys of one key/value head: iterations t = 0 .. group * nq - 1
 // over the 64-query blocks that see them, one query head after the other.  dV
-// and dK fill what S^T and dP^T leave of the tensor memory, so P^T and dS^T go
-// through shared memory.
+// and dK fill what S^T and dP^T leave of the CTA's half of the tensor memory, so
+// P^T and dS^T take the place of S^T and dP^T, and the next S^T follows the
+// products that read them; meanwhile the SM's other CTA has the tensor cores.
+// (With P^T and dS^T in shared memory instead, the products and the rows together
+// moved 3.0 KB a cycle's worth of it per 128 x 128 pairs, and a tile took 1.6 times
+// as long.)
 template <int MODE>
 __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
                                const CUtensorMap* td64, const CUtensorMap* tg, const WindowScratch& ws_,
-                               __nv_bfloat16* __restrict__ dqkv, int item, int stages, int* err, uint8_t* sm) {
-  uint8_t *sK = sm, *sV = sm + T128, *sPt = sm + DKV_P, *sdSt = sm + DKV_DS, *ring = sm + DKV_RING;
+                               __nv_bfloat16* __restrict__ dqkv, int item, int stages, int* err) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const BwdBars s(sm);
+  uint8_t *sK = sm + DKV_K, *sV = sm + DKV_V, *ring = sm + DKV_RING;
   float2* sLD = reinterpret_cast<float2*>(ring + stages * DKV_STAGE);
   uint8_t* rest = ring + stages * (DKV_STAGE + DKV_LD);
-  BwdBars s(rest);
-  rest += BWD_BARS;
   Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
@@ -1116,7 +1120,8 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
     tma_load_3d(sV, tq128, vcol, k0, b, s.one);
     for (int t = 0; t < ahead; ++t) load_q(h0 + t / nq, i0 + t % nq, t);
   });
-  // S^T at 0, dP^T at 64, dV at 128, dK at 192
+  // S^T at 0, dP^T at 64, dV at 128, dK at 192; P^T and dS^T (bf16) over the columns of S^T and dP^T that
+  // their thread has read: columns 0..31 of a tile at 0, columns 32..63 at 32
   const uint32_t tS = tmem, tdP = tmem + 64, tV = tmem + 128, tK = tmem + 192;
 
   if (warp >= BWD_ISSUER) {
@@ -1156,7 +1161,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
           __syncwarp();
         }
         const uint64_t q = qd + sp.stage * (DKV_STAGE / 16), dO = q + T64 / 16;
-        if (t > 0) go = go && warp_await(s.bsc, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // block t-1's read out
+        if (t > 0) go = go && warp_await(s.bo, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // P^T, dS^T read
         if (!go) break;
         tc_fence_after();
         if (elect_one()) {
@@ -1173,7 +1178,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       __syncwarp();
     } else if (warp == BWD_ISSUER + 1) {  // ---- dV += P^T dO_t, dK += dS^T Q_t ----
       constexpr uint32_t idKV = mma_idesc_bf16(128, 64, false, true);
-      const uint64_t pt = kdesc0(smem_u32(sPt)), dst = kdesc0(smem_u32(sdSt)), qd = mndesc0(smem_u32(ring));
+      const uint64_t qd = mndesc0(smem_u32(ring));
       RingPos gp_;
       for (int t = 0; t < niter; ++t) {
         const uint64_t q = qd + gp_.stage * (DKV_STAGE / 16), dO = q + T64 / 16;
@@ -1181,9 +1186,11 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tV, pt + kk * kKStep, dO + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_ta(tV, tS + 32 * (kk >> 1) + 8 * (kk & 1), dO + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tK, dst + kk * kKStep, q + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_ta(tK, tdP + 32 * (kk >> 1) + 8 * (kk & 1), q + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
           tc_commit(s.bo);
           tc_commit(&s.empty[gp_.stage]);
         }
@@ -1214,8 +1221,6 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
         const uint32_t at[2] = {tS + lane + 32 * g, tdP + lane + 32 * g};
         ld_rows<2>(at, v);
       }
-      tc_fence_before();
-      mbar_arrive1(s.bsc);
       const float4* LD = reinterpret_cast<const float4*>(sLD + rp.stage * 64 + 32 * g);  // two queries each
       if (MODE && !flat) {
         const float* at = bias.value + Bias::kLow + d;
@@ -1239,16 +1244,18 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       }
       if (__builtin_expect(!(q0 >= k0 + 127 && q0 + 31 - k0 < a.window), 0))  // some pair may be hidden
         hide32(v, bits_to(kr < a.sinks ? 31 : a.window - 1 - d) & ~bits_to(-d - 1));
+      uint32_t up[16], us[16];
 #pragma unroll
       for (int q = 0; q < 32; q += 2) {
-        v[q] = ex2_approx(v[q]);  // P^T
-        v[q + 1] = ex2_approx(v[q + 1]);
-        unpack2(mul2(pack2(v[q], v[q + 1]), pack2(v[32 + q], v[33 + q])), v[32 + q], v[33 + q]);  // dS^T
+        const float p0 = ex2_approx(v[q]), p1 = ex2_approx(v[q + 1]);  // P^T
+        float s0, s1;
+        unpack2(mul2(pack2(p0, p1), pack2(v[32 + q], v[33 + q])), s0, s1);  // dS^T
+        up[q / 2] = pack_bf16x2(p0, p1);
+        us[q / 2] = pack_bf16x2(s0, s1);
       }
-      if (t > 0) wait(s.bo, (t - 1) & 1);  // the previous dV, dK products read P^T and dS^T
-      st_row32_bf16(sPt, r, 4 * g, v);
-      st_row32_bf16(sdSt, r, 4 * g, v + 32);
-      fence_proxy_async_smem();
+      tmem_st16(tS + lane + 32 * g, up);
+      tmem_st16(tdP + lane + 32 * g, us);
+      tmem_st_wait();
       tc_fence_before();
       mbar_arrive1(s.bp);
       rp.next(stages);
@@ -1294,9 +1301,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 2)
   if (misaligned(sm, err)) return;
   const int x = static_cast<int>(blockIdx.x);
   if (x < n_dkv)
-    window_bwd_dkv<MODE>(a, &tq64, &tq128, &td64, &tg, ws_, dqkv, x, dkv_stages, err, sm);
+    window_bwd_dkv<MODE>(a, &tq64, &tq128, &td64, &tg, ws_, dqkv, x, dkv_stages, err);
   else
-    window_bwd_dq<MODE>(a, &tq64, &tq128, &td128, &tg, ws_, qkv, dqkv, x - n_dkv, dq_stages, err, sm);
+    window_bwd_dq<MODE>(a, &tq64, &tq128, &td128, &tg, ws_, qkv, dqkv, x - n_dkv, dq_stages, err);
 }
 
 // Blocks 0 .. n_sink-1: one sink key of one (sequence, key/value head); thread
