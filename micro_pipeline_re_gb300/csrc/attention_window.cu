@@ -538,11 +538,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
 // ---------------------------------------------------------------------------
 // Workspace, in this order (each part 256-byte aligned):
 //   ld     float2 [nseq][heads][seqpad]: (-lse log2(e), -D) of every query, seqpad = seq rounded up to 128
+//   terms  the same two as matrix operands, [nseq][heads][seqpad / 64][2][2 KB] (see kTerms)
 //   far    float [nseq][heads][query blocks][sinks][128]: dV | dK of the sinks from one query block
 //   base   float [nseq][kv_heads][sinks][128]: their dV | dK from the queries near them
 //   tab    float [nseq][query blocks][heads][ranks]: dtable from one query block
 struct WindowScratch {
   float2* ld;
+  uint8_t* terms;
   float* far;   // NULL: no query block is far from the sinks
   float* base;
   float* tab;   // NULL: no table gradient
@@ -553,10 +555,32 @@ __host__ __device__ constexpr int pad128(int x) { return (x + 127) / 128 * 128; 
 // The first query block whose window has left the first key block.
 __host__ __device__ constexpr int first_far_block(int window) { return (window + 254) / 128; }
 
+// In the dK/dV CTAs a query is a column, and -lse and -D differ from column to
+// column: added by the row threads they would be read from shared memory again by
+// every row.  Instead the tensor cores add them, as one more k step of 16: A is 1
+// in its first three columns and 0 in the others, B holds -8 lse (the score's
+// scale is applied afterwards) or -D of the 64 queries in its first three columns,
+// as a sum of three bf16 terms (24 bits).  Both are tiles without swizzle: 8 rows
+// of 16 bytes (8 columns) follow each other, the two column halves are 128 bytes
+// apart, the groups of 8 rows 256.
+constexpr int kTerms = 2048;       // bytes of B for 64 queries
+constexpr int kOnes = 4096;        // of A
+__device__ __forceinline__ uint64_t terms_desc(uint32_t tile) {
+  return static_cast<uint64_t>((tile & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 16 |
+         static_cast<uint64_t>(256 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+// x as three bf16 terms, the rest of the 16 bytes zero (an infinity: in the first term).
+__device__ __forceinline__ uint4 three_terms(float x) {
+  const float hi = bf2f(f2bf(x)), r1 = isinf(hi) ? 0.f : x - hi;
+  const float mid = bf2f(f2bf(r1)), lo = r1 - mid;
+  return make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.f), 0u, 0u);
+}
+
 __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_constant__ WindowArgs a,
                                                                const __nv_bfloat16* __restrict__ o,
                                                                const __nv_bfloat16* __restrict__ dout,
-                                                               const float* __restrict__ lse, float2* __restrict__ ld) {
+                                                               const float* __restrict__ lse, float2* __restrict__ ld,
+                                                               uint8_t* __restrict__ terms) {
   griddep_wait();
   griddep_launch();
   // eight threads per (sequence, query, head), each 8 of the 64 columns
@@ -582,7 +606,15 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
   }
 #pragma unroll
   for (int s = 4; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
-  if (in && sub == 0) ld[(b * a.heads + h) * seqpad + i] = make_float2(L, -d);
+  if (!in) return;
+  const int64_t at = (b * a.heads + h) * seqpad + i;
+  if (sub == 4) ld[at] = make_float2(L, -d);
+  if (sub < 4) {  // the two column halves of both
+    uint8_t* tile = terms + (at >> 6) * (2 * kTerms) + (sub >> 1) * kTerms;
+    const float x = sub & 2 ? -d : L * (1.f / kScaleLog2);
+    *reinterpret_cast<uint4*>(tile + (i >> 3 & 7) * 256 + (sub & 1) * 128 + (i & 7) * 16) =
+        sub & 1 ? make_uint4(0u, 0u, 0u, 0u) : three_terms(x);
+  }
 }
 
 // Both kinds of CTA own 128 rows and walk 64-wide tiles; two CTAs share an SM,
@@ -674,11 +706,12 @@ constexpr int dq_smem(int stages, int bias_bytes, int sums, bool far) {
   const int tile = T128 + 1024;  // with what its alignment may take
   return DQ_K + stages * T64 + bias_bytes + (far && sums < tile ? tile : sums);
 }
-// Shared memory of a dK/dV CTA: barriers | K | V | `stages` of Q | dO | -lse, -D
-// of the stages' queries | bias.
-constexpr int DKV_K = BWD_BARS, DKV_V = DKV_K + T128, DKV_RING = DKV_V + T128, DKV_STAGE = 2 * T64, DKV_LD = 64 * 8;
+// Shared memory of a dK/dV CTA: barriers | K | V | ones | `stages` of Q | dO |
+// terms of -lse | terms of -D | bias.
+constexpr int DKV_K = BWD_BARS, DKV_V = DKV_K + T128, DKV_ONES = DKV_V + T128, DKV_RING = DKV_ONES + kOnes,
+              DKV_STAGE = 2 * T64 + 2 * kTerms;
 constexpr int dkv_smem(int stages, int bias_bytes) {
-  return DKV_RING + stages * (DKV_STAGE + DKV_LD) + bias_bytes;
+  return DKV_RING + stages * DKV_STAGE + bias_bytes;
 }
 
 // MODE 0: no bias; 1: bias; 2: bias and its gradient.
@@ -1077,8 +1110,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
   extern __shared__ __align__(1024) uint8_t sm[];
   const BwdBars s(sm);
   uint8_t *sK = sm + DKV_K, *sV = sm + DKV_V, *ring = sm + DKV_RING;
-  float2* sLD = reinterpret_cast<float2*>(ring + stages * DKV_STAGE);
-  uint8_t* rest = ring + stages * (DKV_STAGE + DKV_LD);
+  uint8_t* rest = ring + stages * DKV_STAGE;
   Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
@@ -1108,10 +1140,11 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
   auto load_q = [&](int lh, int lq, int stage) {
     uint8_t* dst = ring + stage * DKV_STAGE;
     uint64_t* full = &s.full[stage];
-    mbar_arrive_expect_tx(full, DKV_STAGE + DKV_LD);
+    mbar_arrive_expect_tx(full, DKV_STAGE);
     tma_load_3d(dst, tq64, lh * HD, lq * 64, b, full);
     tma_load_3d(dst + T64, td64, lh * HD, lq * 64, b, full);
-    bulk_load(sLD + stage * 64, ws_.ld + (static_cast<int64_t>(b) * a.heads + lh) * seqpad + lq * 64, DKV_LD, full);
+    bulk_load(dst + 2 * T64, ws_.terms + ((static_cast<int64_t>(b) * a.heads + lh) * (seqpad / 64) + lq) * (2 * kTerms),
+              2 * kTerms, full);
   };
   const int ahead = min(niter, stages);
   const uint32_t tmem = s.start(warp, [&] {
@@ -1149,7 +1182,8 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       const uint64_t k = kdesc0(smem_u32(sK)), v = kdesc0(smem_u32(sV)), qd = kdesc0(smem_u32(ring));
       RingPos sp;
       int qb = i0;
-      bool go = warp_await(s.one, 0, err, DERR_MMA_WAIT, s.abort);
+      const uint64_t ones = terms_desc(smem_u32(sm + DKV_ONES));
+      bool go = warp_await(s.one, 0, err, DERR_MMA_WAIT, s.abort) && warp_await(s.bq, 0, err, DERR_MMA_WAIT, s.abort);
       for (int t = 0; t < niter && go; ++t) {
         go = warp_await(&s.full[sp.stage], sp.parity, err, DERR_MMA_WAIT, s.abort);
         const int left = n - qb * 64;
@@ -1161,14 +1195,17 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
           __syncwarp();
         }
         const uint64_t q = qd + sp.stage * (DKV_STAGE / 16), dO = q + T64 / 16;
+        const uint64_t tL = terms_desc(smem_u32(ring + sp.stage * DKV_STAGE + 2 * T64)), tD = tL + kTerms / 16;
         if (t > 0) go = go && warp_await(s.bo, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // P^T, dS^T read
         if (!go) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, k + kk * kKStep, q + kk * kKStep, idSP, kk ? 1u : 0u);
+          tc_mma_f16(tS, ones, tL, idSP, 1u);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tdP, v + kk * kKStep, dO + kk * kKStep, idSP, kk ? 1u : 0u);
+          tc_mma_f16(tdP, ones, tD, idSP, 1u);
           tc_commit(s.bs);
         }
         if (++qb == i0 + nq) qb = i0;
@@ -1204,8 +1241,14 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
     const int g = warp >> 2, r = tid & 127, kr = k0 + r;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const RowWait wait{err, s.abort};
-    RingPos rp;
     int hq = h0, qb = i0;
+    {  // the ones: this thread's half of row r
+      uint8_t* at = sm + DKV_ONES + (r >> 3) * 256 + g * 128 + (r & 7) * 16;
+      *reinterpret_cast<uint4*>(at) =
+          g ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(pack_bf16x2(1.f, 1.f), pack_bf16x2(1.f, 0.f), 0u, 0u);
+      fence_proxy_async_smem();
+      mbar_arrive1(s.bq);
+    }
     const f32x2 scale2 = pack2(kScaleLog2, kScaleLog2);
     for (int t = 0; t < niter; ++t) {
       if (MODE && qb == i0) bias.fill<BWD_ROWS>(a, hq, tid);
@@ -1213,34 +1256,26 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       const int d = q0 - kr;            // distances d .. d + 31
       bool flat = true;
       if (MODE) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d + 31));
-      wait(&s.full[rp.stage], rp.parity);  // the block's -lse and -D came with its tiles
       wait(s.bs, t & 1);
       tc_fence_after();
-      float v[64];  // S^T (32 columns), then dP^T (32 columns), one round trip
+      float v[64];  // S^T - 8 lse (32 columns), then dP^T - D (32 columns), one round trip
       {
         const uint32_t at[2] = {tS + lane + 32 * g, tdP + lane + 32 * g};
         ld_rows<2>(at, v);
       }
-      const float4* LD = reinterpret_cast<const float4*>(sLD + rp.stage * 64 + 32 * g);  // two queries each
       if (MODE && !flat) {
         const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
-        for (int q = 0; q < 32; q += 2) {
-          const float4 x = LD[q / 2];
-          unpack2(fma2(pack2(v[q], v[q + 1]), scale2, add2(pack2(x.x, x.z), pack2(at[q], at[q + 1]))), v[q], v[q + 1]);
-          unpack2(add2(pack2(v[32 + q], v[33 + q]), pack2(x.y, x.w)), v[32 + q], v[33 + q]);
-        }
-      } else {
-        const float c = MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f;
+        for (int q = 0; q < 32; q += 2)
+          unpack2(fma2(pack2(v[q], v[q + 1]), scale2, pack2(at[q], at[q + 1])), v[q], v[q + 1]);
+      } else if (MODE) {
+        const float c = bias.value[Bias::kLow + max(0, min(d, a.last))];
         const f32x2 c2 = pack2(c, c);
 #pragma unroll
-        for (int q = 0; q < 32; q += 2) {
-          const float4 x = LD[q / 2];
-          f32x2 l2 = pack2(x.x, x.z);
-          if (MODE) l2 = add2(l2, c2);
-          unpack2(fma2(pack2(v[q], v[q + 1]), scale2, l2), v[q], v[q + 1]);
-          unpack2(add2(pack2(v[32 + q], v[33 + q]), pack2(x.y, x.w)), v[32 + q], v[33 + q]);
-        }
+        for (int q = 0; q < 32; q += 2) unpack2(fma2(pack2(v[q], v[q + 1]), scale2, c2), v[q], v[q + 1]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 32; q += 2) unpack2(mul2(pack2(v[q], v[q + 1]), scale2), v[q], v[q + 1]);
       }
       if (__builtin_expect(!(q0 >= k0 + 127 && q0 + 31 - k0 < a.window), 0))  // some pair may be hidden
         hide32(v, bits_to(kr < a.sinks ? 31 : a.window - 1 - d) & ~bits_to(-d - 1));
@@ -1258,7 +1293,6 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive1(s.bp);
-      rp.next(stages);
       if (++qb == i0 + nq) {
         qb = i0;
         ++hq;
@@ -1469,6 +1503,7 @@ WindowScratch window_scratch(void* base, int nseq, int seq, int heads, int windo
   };
   const size_t nqb = (static_cast<size_t>(seq) + 127) / 128, nh = static_cast<size_t>(nseq) * heads;
   w.ld = reinterpret_cast<float2*>(take(nh * nqb * 128 * sizeof(float2)));
+  w.terms = take(nh * nqb * 4 * kTerms);
   if (has_far(seq, window, sinks)) {
     const size_t s = sinks < seq ? sinks : seq;
     w.far = reinterpret_cast<float*>(take(nh * nqb * s * 128 * sizeof(float)));
@@ -1577,7 +1612,7 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   const WindowScratch w = window_scratch(scratch, nseq, seq, heads, window, sinks, dtable_acc ? a.ranks : 0);
   const int64_t prep = static_cast<int64_t>(nseq) * pad128(seq) * heads * 8;
   (void)launch_k(attn_window_prep_kernel, static_cast<unsigned>((prep + 255) / 256), 256, 0, s, a,
-                 static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, w.ld);
+                 static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, w.ld, w.terms);
   rc = check_launch("attention_window_bwd (prep)");
   if (rc) return rc;
   const int nqb = (seq + 127) / 128, n_dkv = nqb * kv_heads * nseq, n_dq = nqb * heads * nseq;

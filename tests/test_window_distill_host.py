@@ -54,12 +54,12 @@ def test_bucket_starts_refusals(b, buckets, max_distance):
 
 def test_scratch_bytes(b):
     f = b.lib().gpipe_op_attention_window_scratch_bytes
-    rows = 8 * 2 * 3 * 128  # (-lse, -D) of 2 sequences x 3 heads x one block of 128 queries
+    rows = (8 + 64) * 2 * 3 * 128  # (-lse, -D) of 2 sequences x 3 heads x one block of 128 queries, twice
     assert f(2, 100, 3, 100, 0, 0) == rows
     assert f(2, 100, 3, 100, 64, 0) == rows          # no query block is far from the sinks
     assert f(2, 100, 3, 100, 64, 32) == rows + 2 * 3 * 32 * 4
     # 4 blocks of queries, window 1: blocks 1..3 are far from the sinks
-    assert f(1, 512, 1, 1, 2, 0) == 8 * 512 + 4 * 2 * 128 * 4 + 2 * 128 * 4
+    assert f(1, 512, 1, 1, 2, 0) == (8 + 64) * 512 + 4 * 2 * 128 * 4 + 2 * 128 * 4
     for bad in [(0, 64, 1, 1, 0, 0), (1, 0, 1, 1, 0, 0), (1, 64, 0, 1, 0, 0), (1, 64, 1, 0, 0, 0), (1, 64, 1, 1, -1, 0),
                 (1, 64, 1, 1, 65, 0), (1, 64, 1, 1, 0, 1), (1, 64, 1, 1, 0, 65), (1 << 20, 1 << 20, 1, 1, 0, 0)]:
         assert f(*bad) == 0, bad
