@@ -1098,8 +1098,10 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
 // dK/dV CTA of 128 keys of one key/value head: iterations t = 0 .. group * nq - 1
 // over the 64-query blocks that see them, one query head after the other.  dV
 // and dK fill what S^T and dP^T leave of the CTA's half of the tensor memory, so
-// P^T and dS^T take the place of S^T and dP^T, and the next S^T follows the
-// products that read them; meanwhile the SM's other CTA has the tensor cores.
+// P^T and dS^T take the place of S^T and dP^T, and the next S^T and dP^T follow
+// the products that read them.  Each of the four has its own hand-off, so that
+// dV += P^T dO and the next S^T run while the rows make dS^T, and dK += dS^T Q
+// and the next dP^T while they make P^T.
 // (With P^T and dS^T in shared memory instead, the products and the rows together
 // moved 3.0 KB a cycle's worth of it per 128 x 128 pairs, and a tile took 1.6 times
 // as long.)
@@ -1153,6 +1155,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
     tma_load_3d(sV, tq128, vcol, k0, b, s.one);
     for (int t = 0; t < ahead; ++t) load_q(h0 + t / nq, i0 + t % nq, t);
   });
+  uint64_t *got_s = s.bs, *got_dp = s.bsd, *wrote_p = s.bp, *wrote_ds = s.bsc, *done_v = s.bo, *done_k = s.bsink;
   // S^T at 0, dP^T at 64, dV at 128, dK at 192; P^T and dS^T (bf16) over the columns of S^T and dP^T that
   // their thread has read: columns 0..31 of a tile at 0, columns 32..63 at 32
   const uint32_t tS = tmem, tdP = tmem + 64, tV = tmem + 128, tK = tmem + 192;
@@ -1196,17 +1199,22 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
         }
         const uint64_t q = qd + sp.stage * (DKV_STAGE / 16), dO = q + T64 / 16;
         const uint64_t tL = terms_desc(smem_u32(ring + sp.stage * DKV_STAGE + 2 * T64)), tD = tL + kTerms / 16;
-        if (t > 0) go = go && warp_await(s.bo, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // P^T, dS^T read
+        if (t > 0) go = go && warp_await(done_v, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort);  // P^T of t-1 read
         if (!go) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tS, k + kk * kKStep, q + kk * kKStep, idSP, kk ? 1u : 0u);
           tc_mma_f16(tS, ones, tL, idSP, 1u);
+          tc_commit(got_s);
+        }
+        if (t > 0 && !warp_await(done_k, (t - 1) & 1, err, DERR_MMA_WAIT, s.abort)) break;  // dS^T of t-1 read
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc_mma_f16(tdP, v + kk * kKStep, dO + kk * kKStep, idSP, kk ? 1u : 0u);
           tc_mma_f16(tdP, ones, tD, idSP, 1u);
-          tc_commit(s.bs);
+          tc_commit(got_dp);
         }
         if (++qb == i0 + nq) qb = i0;
         sp.next(stages);
@@ -1219,16 +1227,21 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       RingPos gp_;
       for (int t = 0; t < niter; ++t) {
         const uint64_t q = qd + gp_.stage * (DKV_STAGE / 16), dO = q + T64 / 16;
-        if (!warp_await(s.bp, t & 1, err, DERR_MMA_WAIT, s.abort)) break;  // P^T, dS^T of block t written
+        if (!warp_await(wrote_p, t & 1, err, DERR_MMA_WAIT, s.abort)) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_f16_ta(tV, tS + 32 * (kk >> 1) + 8 * (kk & 1), dO + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
+          tc_commit(done_v);
+        }
+        if (!warp_await(wrote_ds, t & 1, err, DERR_MMA_WAIT, s.abort)) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_f16_ta(tK, tdP + 32 * (kk >> 1) + 8 * (kk & 1), q + kk * kMnStep, idKV, (t | kk) ? 1u : 0u);
-          tc_commit(s.bo);
+          tc_commit(done_k);
           tc_commit(&s.empty[gp_.stage]);
         }
         gp_.next(stages);
@@ -1256,13 +1269,10 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       const int d = q0 - kr;            // distances d .. d + 31
       bool flat = true;
       if (MODE) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d + 31));
-      wait(s.bs, t & 1);
+      wait(got_s, t & 1);
       tc_fence_after();
-      float v[64];  // S^T - 8 lse (32 columns), then dP^T - D (32 columns), one round trip
-      {
-        const uint32_t at[2] = {tS + lane + 32 * g, tdP + lane + 32 * g};
-        ld_rows<2>(at, v);
-      }
+      float v[32];  // S^T - 8 lse
+      ld_row32(tS + lane + 32 * g, v);
       if (MODE && !flat) {
         const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
@@ -1279,26 +1289,38 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       }
       if (__builtin_expect(!(q0 >= k0 + 127 && q0 + 31 - k0 < a.window), 0))  // some pair may be hidden
         hide32(v, bits_to(kr < a.sinks ? 31 : a.window - 1 - d) & ~bits_to(-d - 1));
-      uint32_t up[16], us[16];
+      uint32_t u[16];
 #pragma unroll
       for (int q = 0; q < 32; q += 2) {
-        const float p0 = ex2_approx(v[q]), p1 = ex2_approx(v[q + 1]);  // P^T
-        float s0, s1;
-        unpack2(mul2(pack2(p0, p1), pack2(v[32 + q], v[33 + q])), s0, s1);  // dS^T
-        up[q / 2] = pack_bf16x2(p0, p1);
-        us[q / 2] = pack_bf16x2(s0, s1);
+        v[q] = ex2_approx(v[q]);  // P^T
+        v[q + 1] = ex2_approx(v[q + 1]);
+        u[q / 2] = pack_bf16x2(v[q], v[q + 1]);
       }
-      tmem_st16(tS + lane + 32 * g, up);
-      tmem_st16(tdP + lane + 32 * g, us);
+      tmem_st16(tS + lane + 32 * g, u);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive1(s.bp);
+      mbar_arrive1(wrote_p);
+      wait(got_dp, t & 1);
+      tc_fence_after();
+      float w[32];  // dP^T - D
+      ld_row32(tdP + lane + 32 * g, w);
+#pragma unroll
+      for (int q = 0; q < 32; q += 2) {
+        float s0, s1;
+        unpack2(mul2(pack2(v[q], v[q + 1]), pack2(w[q], w[q + 1])), s0, s1);  // dS^T
+        u[q / 2] = pack_bf16x2(s0, s1);
+      }
+      tmem_st16(tdP + lane + 32 * g, u);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive1(wrote_ds);
       if (++qb == i0 + nq) {
         qb = i0;
         ++hq;
       }
     }
-    wait(s.bo, (niter - 1) & 1);
+    wait(done_v, (niter - 1) & 1);
+    wait(done_k, (niter - 1) & 1);
     tc_fence_after();
     // warpgroup 0 stores dV, 1 dK, in the place of V and K, whose products are done.  Of the sinks'
     // rows the finish kernel makes the sum with the query blocks far from them.
