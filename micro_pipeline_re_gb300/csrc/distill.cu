@@ -82,10 +82,9 @@ __device__ __forceinline__ void join(float& m, float& s, float& st, float om, fl
 }
 
 // The teacher's side of a row, by one warp: p over the filled slots into pk (all
-// zero without one), and sum p (log p - log q_T) when `kl`.  Returns whether any
-// slot is filled.
-__device__ __forceinline__ bool teacher(const DistillArgs& a, const float* tl, const float* zt, float* pk, float m,
-                                        float st, bool want_kl, float& kl, int lane) {
+// zero without one) and log p in place of the logits tl.  Returns whether any slot
+// is filled.
+__device__ __forceinline__ bool teacher(const DistillArgs& a, float* tl, float* pk, int lane) {
   float tm = -INFINITY;
   for (int k = lane; k < a.topk; k += 32) tm = fmaxf(tm, tl[k]);
   tm = warp_max(tm);
@@ -93,15 +92,21 @@ __device__ __forceinline__ bool teacher(const DistillArgs& a, const float* tl, c
   float ts = 0.f;
   for (int k = lane; k < a.topk; k += 32) ts += expf(tl[k] - tb);
   ts = warp_sum(ts);
-  const float log_ts = logf(ts), log_st = want_kl ? logf(st) : 0.f;
-  float x = 0.f;
+  const float log_ts = logf(ts);
   for (int k = lane; k < a.topk; k += 32) {
-    const float p = ts == 0.f ? 0.f : expf(tl[k] - tb) / ts;
-    pk[k] = p;
-    if (want_kl && p != 0.f) x += p * ((tl[k] - tb - log_ts) - ((zt[k] - m) * a.inv_t - log_st));
+    pk[k] = ts == 0.f ? 0.f : expf(tl[k] - tb) / ts;
+    tl[k] = tl[k] - tb - log_ts;
   }
-  kl = warp_sum(x);
   return ts != 0.f;
+}
+// sum p (log p - log q_T), by one warp.
+__device__ __forceinline__ float divergence(const DistillArgs& a, const float* lp, const float* zt, const float* pk,
+                                            float m, float st, int lane) {
+  const float log_st = logf(st);
+  float x = 0.f;
+  for (int k = lane; k < a.topk; k += 32)
+    if (pk[k] != 0.f) x += pk[k] * (lp[k] - ((zt[k] - m) * a.inv_t - log_st));
+  return warp_sum(x);
 }
 
 // The target of row r, or -1; an id outside the vocabulary is flagged (by `flag`).
@@ -140,22 +145,21 @@ __device__ __forceinline__ void fix_up(const DistillArgs& a, const int* idx, con
 // load and up to NV loads a thread, all of them issued before the first is used.
 // The row is read once, its maximum and sums are joined over the cluster, and dz
 // is made from the registers: the bytes the operator cannot do without and no
-// others.  Two CTAs of 256 threads on an SM hold 128 KB of rows, so that one's
-// loads run during the other's exponentials and stores.
-constexpr int kRowThreads = 256;
-
+// others.  The teacher's side is made while the row's loads are on their way.
+// Short rows take CTAs of 64 threads, so that many of them are under way on an
+// SM: a row's time is a chain of loads, sums and stores however short it is.
 // What a thread keeps of its slice: NV vectors as they came.
-template <typename T, bool VEC, int NV>
+template <typename T, bool VEC, int NV, int TH>
 struct Slice {
   static constexpr int E = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
-  static constexpr int kElems = kRowThreads * NV * E;
+  static constexpr int kElems = TH * NV * E;
   using Word = typename std::conditional<VEC, uint4, float>::type;
   Word w[NV];
 
   __device__ __forceinline__ void load(const T* z, int n, int tid) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = (j * kRowThreads + tid) * E;
+      const int i = (j * TH + tid) * E;
       if constexpr (VEC) {
         if (i + E <= n) {
           w[j] = *reinterpret_cast<const uint4*>(z + i);
@@ -192,14 +196,13 @@ struct Slice {
   }
 };
 
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(kRowThreads, 2) distill_row_kernel(const T* logits, __nv_bfloat16* dz,
-                                                                    const __grid_constant__ DistillArgs a, int ctas,
-                                                                    int per) {
+template <typename T, bool VEC, int NV, int TH>
+__global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_bfloat16* dz,
+                                                         const __grid_constant__ DistillArgs a, int ctas, int per) {
   griddep_wait();
   griddep_launch();
-  using S = Slice<T, VEC, NV>;
-  constexpr int E = S::E, W = kRowThreads / 32;
+  using S = Slice<T, VEC, NV, TH>;
+  constexpr int E = S::E, W = TH / 32;
   __shared__ float sm_m[W], sm_s[W], sm_t[W];
   __shared__ __align__(16) float mine[4];  // this CTA's maximum and sums, for the cluster
   __shared__ int idx[kMaxTop];
@@ -215,17 +218,23 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_row_kernel(const T* lo
   S row;
   row.load(z + lo, n, tid);
   const int target = target_of(a, r, rank == 0 && tid == 0);
-  if (tid < a.topk) {
-    int i = a.top_idx[r * a.topk + tid];
+  for (int k = tid; k < a.topk; k += TH) {
+    int i = a.top_idx[r * a.topk + k];
     if (i >= a.vocab) {
       if (rank == 0) atomicExch(a.err, DERR_BAD_TOKEN);
       i = -1;
     }
-    idx[tid] = i;
-    tl[tid] = i >= 0 ? a.top_logit[r * a.topk + tid] * a.inv_t : -INFINITY;
-    zt[tid] = i >= 0 ? Elem<T>::ld(z + i) : 0.f;
+    idx[k] = i;
+    tl[k] = i >= 0 ? a.top_logit[r * a.topk + k] * a.inv_t : -INFINITY;
+    zt[k] = i >= 0 ? Elem<T>::ld(z + i) : 0.f;
   }
   if (tid == 0 && target >= 0) sh_z = Elem<T>::ld(z + target);
+  __syncthreads();
+  __shared__ float sh_has;
+  if (warp == W - 1) {
+    const bool has = teacher(a, tl, pk, lane);
+    if (lane == 0) sh_has = has ? 1.f : 0.f;
+  }
 
   float m = -INFINITY;
 #pragma unroll
@@ -242,7 +251,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_row_kernel(const T* lo
     for (int j = 0; j < NV; ++j) {
       float v[E];
       row.get(j, v);
-      if (E * j * kRowThreads < n) {  // (uniform)
+      if (E * j * TH < n) {  // (uniform)
 #pragma unroll
         for (int e = 0; e < E; ++e) st += ex2_approx((v[e] - ms) * ct);
         if (a.ce > 0.f) {
@@ -285,27 +294,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_row_kernel(const T* lo
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
-  float kl = 0.f;
-  __shared__ float sh_has;
-  if (warp == 0) {
-    const bool has = teacher(a, tl, zt, pk, m, st, rank == 0, kl, lane);
+  if (rank == 0 && warp == W - 1) {
+    const float kl = divergence(a, tl, zt, pk, m, st, lane);
     if (lane == 0) {
-      sh_has = has ? 1.f : 0.f;
-      if (rank == 0) {
-        float loss = a.kd * kl;
-        if (target >= 0) loss += a.ce * (logf(s1) - (sh_z - m));
-        a.loss[r] = loss;
-      }
+      float loss = a.kd * kl;
+      if (target >= 0) loss += a.ce * (logf(s1) - (sh_z - m));
+      a.loss[r] = loss;
     }
   }
-  __syncthreads();
   if (dz) {
     const float gt = sh_has != 0.f ? a.kd_grad / st : 0.f;
     const float g1 = target >= 0 ? a.ce / s1 : 0.f;
     __nv_bfloat16* out = dz + r * a.lddz;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = (j * kRowThreads + tid) * E;
+      const int i = (j * TH + tid) * E;
       if (i < n) {
         float v[E], g[E];
         row.get(j, v);
@@ -326,8 +329,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_row_kernel(const T* lo
     }
     __syncthreads();
     // the elements of the top tokens and of the target in this slice, once each
-    const int me = tid < a.topk ? idx[tid] : -1;
-    if (me >= lo && me < lo + n) fix_up(a, idx, pk, tid, me, zt[tid] - m, target, gt, g1, out);
+    for (int k = tid; k < a.topk; k += TH) {
+      const int me = idx[k];
+      if (me >= lo && me < lo + n) fix_up(a, idx, pk, k, me, zt[k] - m, target, gt, g1, out);
+    }
     if (tid == 0 && target >= lo && target < lo + n) fix_up(a, idx, pk, a.topk, target, sh_z - m, target, gt, g1, out);
   }
   // the others may still be reading this CTA's sums
@@ -342,15 +347,16 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_row_kernel(const T* lo
 // the copies run ahead by whatever the ring has left beside the current slice,
 // so that memory is never idle while a row's sums are joined, and a row is read
 // from memory once although it is used twice.
-//   warp 20      copies: the chunks of row after row, as the ring empties.
+//   warp 24      copies: the chunks of row after row, as the ring empties.
 //   warps 0-15   pass A over a slice's chunks (maximum and sums), joined over the
 //                warps and, through remote shared memory, over the cluster; pass
 //                B over the same chunks, which writes dz and frees them.
-//   warps 16-19  the teacher of the next row (its tokens, the student's logits
-//                there, p), then the current row's loss and, once pass B is done,
-//                the elements of its top tokens.
+//   warps 16-23  two groups, of the even and the odd rows: the teacher of a row ahead
+//                of time (its tokens, the student's logits there, p), then, once its
+//                sums are known, its loss and, once pass B is done, the elements of
+//                its top tokens.
 constexpr int kChunk = 32768, kChunks = 6, kMaxSliceChunks = 4;
-constexpr int kPassThreads = 512, kTeachThreads = 128, kStreamThreads = kPassThreads + kTeachThreads + 32;
+constexpr int kPassThreads = 512, kTeachThreads = 128, kStreamThreads = kPassThreads + 2 * kTeachThreads + 32;
 constexpr int kMaxCluster = 8;
 
 struct StreamShared {
@@ -363,15 +369,17 @@ struct StreamShared {
   float sent[2][kMaxCluster][4];
   float total[2][4];
   float has[2], label[2];  // whether the row has a teacher, a target
-  int idx[2][kMaxTop];
+  __align__(16) int idx[2][kMaxTop];
   float pk[2][kMaxTop];
-  float kl[kTeachThreads / 32];
+  float kl[2][kTeachThreads / 32];
   int abort;
 };
 constexpr int kStreamSmem = kChunks * kChunk + static_cast<int>(sizeof(StreamShared));
 
 __device__ __forceinline__ void pass_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPassThreads) : "memory"); }
-__device__ __forceinline__ void teach_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kTeachThreads) : "memory"); }
+__device__ __forceinline__ void teach_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "n"(kTeachThreads) : "memory");
+}
 
 // What a teacher thread has of its (up to two) slots of a row, step by step.
 struct Fetched {
@@ -459,9 +467,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kPassThreads / 32) {  // ---- the teacher ----
-    const int t = tid - kPassThreads, w = t >> 5;
-    // A row's loads are issued one turn (its tokens) and two turns (the student's
-    // logits there) before they are used, while the rows before it are finished.
+    const int b = (tid - kPassThreads) / kTeachThreads;  // the group, and the parity of its rows
+    const int t = tid - kPassThreads - b * kTeachThreads, w = t >> 5;
+    // A row's tokens are loaded two of this group's rows ahead, the student's logits
+    // there one ahead, before the row in hand is finished.
     auto fetch = [&](int64_t r) {
       Fetched f = {{-1, -1}, {0.f, 0.f}, -1};
       if (r >= rows) return f;
@@ -494,7 +503,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       g.zt = f.target >= 0 ? Elem<T>::ld(z + f.target) : 0.f;
       return g;
     };
-    auto prepare = [&](const Gathered& g, int b) {
+    auto prepare = [&](const Gathered& g) {
       Slots s;
       s.target = g.target;
       s.zt = g.zt;
@@ -504,12 +513,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       for (int k = 0; k < 2; ++k) {
         const int slot = t + k * kTeachThreads;
         s.z[k] = g.z[k];
-        if (slot < a.topk) {
-          sh.idx[b][slot] = id[k];
-          sh.pk[b][slot] = tl[k];
-        }
+        sh.idx[b][slot] = id[k];  // (-1 behind the last slot too)
+        sh.pk[b][slot] = tl[k];
       }
-      teach_sync();
+      teach_sync(b);
       // every warp takes the maximum and the sum over all slots by itself
       float tm = -INFINITY;
       for (int k = lane; k < a.topk; k += 32) tm = fmaxf(tm, sh.pk[b][k]);
@@ -519,39 +526,45 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       for (int k = lane; k < a.topk; k += 32) ts += expf(sh.pk[b][k] - tb);
       ts = warp_sum(ts);
       const float log_ts = logf(ts);
-      teach_sync();
+      teach_sync(b);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int slot = t + k * kTeachThreads;
         s.p[k] = ts == 0.f || id[k] < 0 ? 0.f : expf(tl[k] - tb) / ts;
         s.logp[k] = tl[k] - tb - log_ts;
-        if (slot < a.topk) sh.pk[b][slot] = s.p[k];
+        sh.pk[b][slot] = s.p[k];
       }
       if (t == 0) {
         sh.has[b] = ts == 0.f ? 0.f : 1.f;
         sh.label[b] = s.target >= 0 ? 1.f : 0.f;
       }
-      teach_sync();
+      teach_sync(b);
+      // slots of the same token: usually there are none but the slot itself
       s.fix_target = t == 0 && s.target >= 0;
+      s.me[0] = id[0];
+      s.me[1] = id[1];
+      s.sum[0] = s.sum[1] = 0.f;
+      const int4* all = reinterpret_cast<const int4*>(sh.idx[b]);
+      for (int i = 0; i < (a.topk + 3) / 4; ++i) {
+        const int4 v = all[i];
+        const int four[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int slot = t + k * kTeachThreads;
-        s.me[k] = id[k];
-        s.sum[k] = 0.f;
-        if (id[k] >= 0)
-          for (int i = 0; i < a.topk; ++i)
-            if (sh.idx[b][i] == id[k]) {
-              if (i < slot) s.me[k] = -1;
-              s.sum[k] += sh.pk[b][i];
-            }
+        for (int k = 0; k < 2; ++k)
+          if (id[k] >= 0 && (v.x == id[k] || v.y == id[k] || v.z == id[k] || v.w == id[k])) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (four[j] == id[k]) {
+                if (4 * i + j < t + k * kTeachThreads) s.me[k] = -1;
+                s.sum[k] += sh.pk[b][4 * i + j];
+              }
+          }
+        if (s.fix_target && (v.x == s.target || v.y == s.target || v.z == s.target || v.w == s.target))
+          s.fix_target = false;
       }
-      if (s.fix_target)
-        for (int i = 0; i < a.topk; ++i)
-          if (sh.idx[b][i] == s.target) s.fix_target = false;
       mbar_arrive1(&sh.ready[b]);
       return s;
     };
-    auto finish = [&](const Slots& s, int r, int b, uint32_t parity) {
+    auto finish = [&](const Slots& s, int r, uint32_t parity) {
       (void)lane_await(&sh.sums[b], parity, a.err, DERR_ACC_WAIT, abort);
       __syncwarp();
       const float m = sh.total[b][0], s1 = sh.total[b][1], st = sh.total[b][2];
@@ -562,10 +575,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         for (int k = 0; k < 2; ++k)
           if (s.p[k] != 0.f) kl += s.p[k] * (s.logp[k] - ((s.z[k] - m) * a.inv_t - log_st));
         kl = warp_sum(kl);
-        if (lane == 0) sh.kl[w] = kl;
-        teach_sync();
+        if (lane == 0) sh.kl[b][w] = kl;
+        teach_sync(b);
         if (t == 0) {
-          float loss = a.kd * ((sh.kl[0] + sh.kl[1]) + (sh.kl[2] + sh.kl[3]));
+          float loss = a.kd * ((sh.kl[b][0] + sh.kl[b][1]) + (sh.kl[b][2] + sh.kl[b][3]));
           if (s.target >= 0) loss += a.ce * (logf(s1) - (s.zt - m));
           a.loss[r] = loss;
         }
@@ -586,24 +599,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (s.me[k] >= lo && s.me[k] < lo + n) out[s.me[k]] = value(s.z[k] - m, s.sum[k], s.me[k] == s.target);
       if (s.fix_target && s.target >= lo && s.target < lo + n) out[s.target] = value(s.zt - m, 0.f, true);
     };
-    const int64_t stride = clusters;
+    const int64_t first = row0 + static_cast<int64_t>(b) * clusters, stride = 2 * static_cast<int64_t>(clusters);
     Gathered g = {};
-    Slots cur = {};
-    if (row0 < rows) {
-      g = gather(fetch(row0), row0);
-      cur = prepare(g, 0);
-    }
-    if (row0 + stride < rows) g = gather(fetch(row0 + stride), row0 + stride);
-    Fetched f = fetch(row0 + 2 * stride);
-    int i = 0;
-    for (int64_t r = row0; r < rows; r += stride, ++i) {
-      const Gathered ready = g;  // of the next row
-      if (r + 2 * stride < rows) g = gather(f, r + 2 * stride);
-      f = fetch(r + 3 * stride);
-      Slots next = {};
-      if (r + stride < rows) next = prepare(ready, (i + 1) & 1);
-      finish(cur, static_cast<int>(r), i & 1, (i >> 1) & 1);
-      cur = next;
+    if (first < rows) g = gather(fetch(first), first);
+    Fetched f = fetch(first + stride);
+    uint32_t parity = 0;
+    for (int64_t r = first; r < rows; r += stride, parity ^= 1u) {
+      const Slots cur = prepare(g);
+      if (r + stride < rows) g = gather(f, r + stride);
+      f = fetch(r + 2 * stride);
+      finish(cur, static_cast<int>(r), parity);
     }
   } else {  // ---- passes ----
     constexpr int V = kPer / (E * kPassThreads);  // vectors a thread takes of a chunk
@@ -865,8 +870,8 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logit
                   ot = __shfl_xor_sync(0xffffffffu, st, o);
       join(m, s1, st, om, os, ot, c1, ct);
     }
-    float kl;
-    const bool has = teacher(a, tl, zt, pk, m, st, true, kl, lane);
+    const bool has = teacher(a, tl, pk, lane);
+    const float kl = divergence(a, tl, zt, pk, m, st, lane);
     if (lane == 0) {
       sh[0] = m;
       sh[1] = s1;
@@ -917,12 +922,12 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logit
 }
 
 // Launch the register kernel on clusters of `ctas`.
-template <typename T, bool VEC, int NV>
+template <typename T, bool VEC, int NV, int TH>
 cudaError_t launch_row(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int64_t rows, int ctas, int per,
                        cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
-  cfg.blockDim = dim3(kRowThreads);
+  cfg.blockDim = dim3(TH);
   cfg.stream = s;
   cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -934,7 +939,7 @@ cudaError_t launch_row(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int6
   set_priority_attr(attr[2], s);
   cfg.attrs = attr;
   cfg.numAttrs = 3;
-  return cudaLaunchKernelEx(&cfg, distill_row_kernel<T, VEC, NV>, z, dz, a, ctas, per);
+  return cudaLaunchKernelEx(&cfg, distill_row_kernel<T, VEC, NV, TH>, z, dz, a, ctas, per);
 }
 
 template <typename T, bool CE>
@@ -973,33 +978,48 @@ cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, i
   return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE>, z, dz, a, rows, ctas, per);
 }
 
+// Clusters of `ctas` for slices of at most `most` elements; with rows for less than
+// half of the SMs, more of them a row, down to slices of `few`.
+int row_ctas(int rows, int vocab, int64_t most, int64_t few) {
+  int ctas = 1;
+  while (ctas < kMaxCluster && most * ctas < vocab) ctas *= 2;
+  while (ctas < kMaxCluster && static_cast<int64_t>(rows) * ctas * 2 <= num_sms() && few * ctas < vocab) ctas *= 2;
+  return ctas;
+}
+
+// Which kernel takes the rows:
+//   up to 16 KB (aligned) or 4096 elements   registers, 64 threads up to a quarter
+//       of that and 256 above: 65536 rows of 512 fp32 take 364 us with 64 threads
+//       and 767 with 256, 8192 x 2048 take 88 and 110
+//   longer, aligned                          the stream: 2048 x 32000 bf16 81 us,
+//       115 with the row in registers
+//   longer, unaligned                        one element a load and a store.  Many
+//       rows of up to 256 KB read the row twice (2048 x 32001: 155 us fp32, 149
+//       bf16; 177 and 228 from registers), since the second time it is in L2; rows
+//       above that, or few, stay in registers (1000 x 100001 fp32: 280 us, 350
+//       read twice)
+//   what no cluster of 8 holds               is read twice
 template <typename T, bool VEC>
 cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, cudaStream_t s) {
-  constexpr int kLong = VEC ? 16 : 64, kShort = VEC ? 4 : 16;  // loads a thread
-  constexpr int most = Slice<T, VEC, kLong>::kElems, few = Slice<T, VEC, kShort>::kElems;
-  if (VEC && a.vocab > few) {
-    constexpr int slice = kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T));
-    int ctas = 1;
-    while (ctas < kMaxCluster && static_cast<int64_t>(slice) * ctas < a.vocab) ctas *= 2;
-    while (ctas < kMaxCluster && static_cast<int64_t>(rows) * ctas * 2 <= num_sms() &&
-           static_cast<int64_t>(few) * ctas < a.vocab)
-      ctas *= 2;
-    const int per = ((a.vocab + ctas - 1) / ctas + 7) & ~7;
-    if (static_cast<int64_t>(slice) * ctas >= a.vocab)
-      return a.ce > 0.f ? launch_stream<T, true>(z, dz, a, rows, ctas, per, s)
-                        : launch_stream<T, false>(z, dz, a, rows, ctas, per, s);
+  constexpr int kShort = VEC ? 4 : 16;  // loads a thread
+  constexpr int few = Slice<T, VEC, kShort, 256>::kElems, tiny = Slice<T, VEC, kShort, 64>::kElems;
+  const auto slice = [&](int ctas) { return ((a.vocab + ctas - 1) / ctas + 7) & ~7; };
+  if (a.vocab <= tiny) return launch_row<T, VEC, kShort, 64>(z, dz, a, rows, 1, slice(1), s);
+  if (a.vocab <= few) return launch_row<T, VEC, kShort, 256>(z, dz, a, rows, 1, slice(1), s);
+  if constexpr (VEC) {
+    constexpr int64_t most = kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T));
+    const int ctas = row_ctas(rows, a.vocab, most, few);
+    if (most * ctas >= a.vocab)
+      return a.ce > 0.f ? launch_stream<T, true>(z, dz, a, rows, ctas, slice(ctas), s)
+                        : launch_stream<T, false>(z, dz, a, rows, ctas, slice(ctas), s);
+  } else {
+    constexpr int kLong = 64;
+    constexpr int64_t most = Slice<T, VEC, kLong, 256>::kElems;
+    const int ctas = row_ctas(rows, a.vocab, most, few);
+    const bool again = rows > num_sms() && static_cast<int64_t>(a.vocab) * sizeof(T) <= (256 << 10);
+    if (!again && most * ctas >= a.vocab) return launch_row<T, VEC, kLong, 256>(z, dz, a, rows, ctas, slice(ctas), s);
   }
-  int ctas = 1;
-  while (ctas < kMaxCluster && static_cast<int64_t>(most) * ctas < a.vocab) ctas *= 2;
-  if (static_cast<int64_t>(most) * ctas < a.vocab)
-    return launch_k(distill_kernel<T, VEC>, rows, kDistillThreads, 0, s, z, dz, a);
-  // few rows: more SMs a row, down to slices that a thread reads in four loads
-  while (ctas < kMaxCluster && static_cast<int64_t>(rows) * ctas * 2 <= num_sms() &&
-         static_cast<int64_t>(few) * ctas < a.vocab)
-    ctas *= 2;
-  const int per = ((a.vocab + ctas - 1) / ctas + 7) & ~7;
-  return per <= few ? launch_row<T, VEC, kShort>(z, dz, a, rows, ctas, per, s)
-                    : launch_row<T, VEC, kLong>(z, dz, a, rows, ctas, per, s);
+  return launch_k(distill_kernel<T, VEC>, rows, kDistillThreads, 0, s, z, dz, a);
 }
 
 }  // namespace
