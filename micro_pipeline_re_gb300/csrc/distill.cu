@@ -988,9 +988,11 @@ int row_ctas(int rows, int vocab, int64_t most, int64_t few) {
 }
 
 // Which kernel takes the rows:
-//   up to 16 KB (aligned) or 4096 elements   registers, 64 threads up to a quarter
-//       of that and 256 above: 65536 rows of 512 fp32 take 364 us with 64 threads
-//       and 767 with 256, 8192 x 2048 take 88 and 110
+//   up to 16 KB (aligned) or 4096 elements   registers, in the fewest threads that
+//       keep 4 or 8 loads each (16 or 32 of one element).  With 64 threads 65536
+//       rows of 512 fp32 take 364 us at 4 loads and 413 at 8, 8192 x 2048 take 88
+//       with 256 x 4 and 60 with 64 x 8, 8192 x 4096 take 91 with 256 x 4, 81 with
+//       64 x 16 and 72 with 128 x 8
 //   longer, aligned                          the stream: 2048 x 32000 bf16 81 us,
 //       115 with the row in registers
 //   longer, unaligned                        one element a load and a store.  Many
@@ -1001,11 +1003,13 @@ int row_ctas(int rows, int vocab, int64_t most, int64_t few) {
 //   what no cluster of 8 holds               is read twice
 template <typename T, bool VEC>
 cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, cudaStream_t s) {
-  constexpr int kShort = VEC ? 4 : 16;  // loads a thread
-  constexpr int few = Slice<T, VEC, kShort, 256>::kElems, tiny = Slice<T, VEC, kShort, 64>::kElems;
+  constexpr int kFew = VEC ? 4 : 16, kMore = VEC ? 8 : 32;  // loads a thread
+  constexpr int tiny = Slice<T, VEC, kFew, 64>::kElems, small = Slice<T, VEC, kMore, 64>::kElems,
+                few = Slice<T, VEC, kMore, 128>::kElems;
   const auto slice = [&](int ctas) { return ((a.vocab + ctas - 1) / ctas + 7) & ~7; };
-  if (a.vocab <= tiny) return launch_row<T, VEC, kShort, 64>(z, dz, a, rows, 1, slice(1), s);
-  if (a.vocab <= few) return launch_row<T, VEC, kShort, 256>(z, dz, a, rows, 1, slice(1), s);
+  if (a.vocab <= tiny) return launch_row<T, VEC, kFew, 64>(z, dz, a, rows, 1, slice(1), s);
+  if (a.vocab <= small) return launch_row<T, VEC, kMore, 64>(z, dz, a, rows, 1, slice(1), s);
+  if (a.vocab <= few) return launch_row<T, VEC, kMore, 128>(z, dz, a, rows, 1, slice(1), s);
   if constexpr (VEC) {
     constexpr int64_t most = kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T));
     const int ctas = row_ctas(rows, a.vocab, most, few);
