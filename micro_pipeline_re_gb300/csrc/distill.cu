@@ -350,13 +350,14 @@ __global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_b
 //   warp 24      copies: the chunks of row after row, as the ring empties.
 //   warps 0-15   pass A over a slice's chunks (maximum and sums), joined over the
 //                warps and, through remote shared memory, over the cluster; pass
-//                B over the same chunks, which writes dz and frees them.
+//                B over the same chunks, which writes dz and frees them.  For the loss alone
+//                pass A frees them, and a slice may be longer than the ring.
 //   warps 16-23  two groups, of the even and the odd rows: the teacher of a row ahead
 //                of time (its tokens, the student's logits there, p), then, once its
 //                sums are known, its loss and, once pass B is done, the elements of
 //                its top tokens.
 constexpr int kChunk = 32768, kChunks = 6, kMaxSliceChunks = 4;
-constexpr int kPassThreads = 512, kTeachThreads = 128, kStreamThreads = kPassThreads + 2 * kTeachThreads + 32;
+constexpr int kPassThreads = 512, kTeachThreads = 64, kSlots = kMaxTop / kTeachThreads, kStreamThreads = kPassThreads + 2 * kTeachThreads + 32;
 constexpr int kMaxCluster = 8;
 
 struct StreamShared {
@@ -383,28 +384,28 @@ __device__ __forceinline__ void teach_sync(int group) {
 
 // What a teacher thread has of its (up to two) slots of a row, step by step.
 struct Fetched {
-  int id[2];
-  float logit[2];
+  int id[kSlots];
+  float logit[kSlots];
   int target;
 };
 struct Gathered {
-  int id[2];
-  float tl[2], z[2];
+  int id[kSlots];
+  float tl[kSlots], z[kSlots];
   int target;
   float zt;
 };
 struct Slots {
-  int me[2];   // the token, or -1 (empty, or named by an earlier slot)
-  float z[2];  // the student's logit there
-  float p[2];  // the slot's probability, and log p
-  float logp[2];
-  float sum[2];  // over all slots of that token
+  int me[kSlots];   // the token, or -1 (empty, or named by an earlier slot)
+  float z[kSlots];  // the student's logit there
+  float p[kSlots];  // the slot's probability, and log p
+  float logp[kSlots];
+  float sum[kSlots];  // over all slots of that token
   int target;
   float zt;
   bool fix_target;  // the target's element is this thread's: no slot names it
 };
 
-template <typename T, bool CE>
+template <typename T, bool CE, bool GRAD>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     distill_stream_kernel(const T* logits, __nv_bfloat16* dz, const __grid_constant__ DistillArgs a, int rows, int ctas,
                           int per) {
@@ -472,10 +473,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     // A row's tokens are loaded two of this group's rows ahead, the student's logits
     // there one ahead, before the row in hand is finished.
     auto fetch = [&](int64_t r) {
-      Fetched f = {{-1, -1}, {0.f, 0.f}, -1};
+      Fetched f;
+      f.target = -1;
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) {
+        f.id[k] = -1;
+        f.logit[k] = 0.f;
+      }
       if (r >= rows) return f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kSlots; ++k) {
         const int slot = t + k * kTeachThreads;
         if (slot < a.topk) {
           f.id[k] = a.top_idx[r * a.topk + slot];
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       Gathered g;
       const T* z = logits + r * a.ld;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kSlots; ++k) {
         int i = f.id[k];
         if (i >= a.vocab) {
           if (rank == 0) atomicExch(a.err, DERR_BAD_TOKEN);
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const int* id = g.id;
       const float* tl = g.tl;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kSlots; ++k) {
         const int slot = t + k * kTeachThreads;
         s.z[k] = g.z[k];
         sh.idx[b][slot] = id[k];  // (-1 behind the last slot too)
@@ -528,7 +535,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const float log_ts = logf(ts);
       teach_sync(b);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kSlots; ++k) {
         const int slot = t + k * kTeachThreads;
         s.p[k] = ts == 0.f || id[k] < 0 ? 0.f : expf(tl[k] - tb) / ts;
         s.logp[k] = tl[k] - tb - log_ts;
@@ -541,15 +548,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       teach_sync(b);
       // slots of the same token: usually there are none but the slot itself
       s.fix_target = t == 0 && s.target >= 0;
-      s.me[0] = id[0];
-      s.me[1] = id[1];
-      s.sum[0] = s.sum[1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) {
+        s.me[k] = id[k];
+        s.sum[k] = 0.f;
+      }
       const int4* all = reinterpret_cast<const int4*>(sh.idx[b]);
       for (int i = 0; i < (a.topk + 3) / 4; ++i) {
         const int4 v = all[i];
         const int four[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < kSlots; ++k)
           if (id[k] >= 0 && (v.x == id[k] || v.y == id[k] || v.z == id[k] || v.w == id[k])) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -572,18 +581,23 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const float log_st = logf(st);
         float kl = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < kSlots; ++k)
           if (s.p[k] != 0.f) kl += s.p[k] * (s.logp[k] - ((s.z[k] - m) * a.inv_t - log_st));
         kl = warp_sum(kl);
         if (lane == 0) sh.kl[b][w] = kl;
         teach_sync(b);
         if (t == 0) {
-          float loss = a.kd * ((sh.kl[b][0] + sh.kl[b][1]) + (sh.kl[b][2] + sh.kl[b][3]));
+          float loss = 0.f;
+          for (int i = 0; i < kTeachThreads / 32; ++i) loss += sh.kl[b][i];
+          loss *= a.kd;
           if (s.target >= 0) loss += a.ce * (logf(s1) - (s.zt - m));
           a.loss[r] = loss;
         }
       }
-      if (!dz) return;
+      // (without dz too: a pass warp must have seen this row's teacher before the next one's is ready)
+      (void)lane_await(&sh.done[b], parity, a.err, DERR_ACC_WAIT, abort);
+      __syncwarp();
+      if (!GRAD) return;
       const float gt = sh.has[b] != 0.f ? a.kd_grad / st : 0.f;
       const float g1 = s.target >= 0 ? a.ce / s1 : 0.f;
       __nv_bfloat16* out = dz + static_cast<int64_t>(r) * a.lddz;
@@ -592,10 +606,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (g1 != 0.f) g += ex2_approx(x * c1) * g1;
         return f2bf(is_target ? g - a.ce : g);
       };
-      (void)lane_await(&sh.done[b], parity, a.err, DERR_ACC_WAIT, abort);
-      __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < kSlots; ++k)
         if (s.me[k] >= lo && s.me[k] < lo + n) out[s.me[k]] = value(s.z[k] - m, s.sum[k], s.me[k] == s.target);
       if (s.fix_target && s.target >= lo && s.target < lo + n) out[s.target] = value(s.zt - m, 0.f, true);
     };
@@ -669,6 +681,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             s12 = add2(s12, pack2(ex2_approx(x0), ex2_approx(x1)));
           }
         }
+        if (!GRAD) {  // no pass B
+          __syncwarp();
+          if (lane == 0) mbar_arrive1(&sh.empty[sl]);
+        }
         if (++sl == kChunks) {
           sl = 0;
           pa ^= 1u;
@@ -730,29 +746,34 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         sh.total[b][2] = st;
         mbar_arrive1(&sh.sums[b]);
       }
+      if (!GRAD) {
+        slot = sl;
+        parity = pa;
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&sh.done[b]);
+        continue;
+      }
       // pass B
       const float gt = sh.has[b] != 0.f ? a.kd_grad / st : 0.f;
       const float g1 = sh.label[b] != 0.f ? a.ce / s1 : 0.f;
-      __nv_bfloat16* out = dz ? dz + static_cast<int64_t>(r) * a.lddz + lo : nullptr;
+      __nv_bfloat16* out = dz + static_cast<int64_t>(r) * a.lddz + lo;
       const f32x2 m2 = pack2(-m, -m), gt2 = pack2(gt, gt), g12 = pack2(g1, g1);
       // dz of pairs, by which of the two terms the row has
       auto pass_b = [&](auto grad2) {
         for (int c = 0; c < chunks; ++c) {
-          if (out) {
-            const int left = min(kPer, whole - c * kPer);
-            float v[V * E];
-            load_chunk(reinterpret_cast<const T*>(ring + slot * kChunk), left, v);
+          const int left = min(kPer, whole - c * kPer);
+          float v[V * E];
+          load_chunk(reinterpret_cast<const T*>(ring + slot * kChunk), left, v);
 #pragma unroll
-            for (int e = 0; e < V * E; e += 2) unpack2(grad2(add2(pack2(v[e], v[e + 1]), m2)), v[e], v[e + 1]);
-            __nv_bfloat16* to = out + c * kPer + tid * E;
-            if (left == kPer) {
+          for (int e = 0; e < V * E; e += 2) unpack2(grad2(add2(pack2(v[e], v[e + 1]), m2)), v[e], v[e + 1]);
+          __nv_bfloat16* to = out + c * kPer + tid * E;
+          if (left == kPer) {
 #pragma unroll
-              for (int j = 0; j < V; ++j) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
-            } else {
+            for (int j = 0; j < V; ++j) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
+          } else {
 #pragma unroll
-              for (int j = 0; j < V; ++j)
-                if ((j * kPassThreads + tid) * E < left) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
-            }
+            for (int j = 0; j < V; ++j)
+              if ((j * kPassThreads + tid) * E < left) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive1(&sh.empty[slot]);
@@ -761,7 +782,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             parity ^= 1u;
           }
         }
-        if (out && tid < n - whole) {
+        if (tid < n - whole) {
           float g, other;
           unpack2(grad2(add2(pack2(tail, tail), m2)), g, other);
           out[whole + tid] = f2bf(g);
@@ -942,12 +963,12 @@ cudaError_t launch_row(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int6
   return cudaLaunchKernelEx(&cfg, distill_row_kernel<T, VEC, NV, TH>, z, dz, a, ctas, per);
 }
 
-template <typename T, bool CE>
+template <typename T, bool CE, bool GRAD>
 cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, int ctas, int per,
                           cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   if (once_per_device(done, [] {
-        return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE>,
+        return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE, GRAD>,
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem));
       }))
     return cudaErrorInvalidValue;
@@ -968,14 +989,14 @@ cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, i
   int clusters = at_once[ctas].load(std::memory_order_relaxed);
   if (clusters == 0) {
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / ctas * ctas));
-    if (cudaOccupancyMaxActiveClusters(&clusters, distill_stream_kernel<T, CE>, &cfg) != cudaSuccess || clusters < 1) {
+    if (cudaOccupancyMaxActiveClusters(&clusters, distill_stream_kernel<T, CE, GRAD>, &cfg) != cudaSuccess || clusters < 1) {
       (void)cudaGetLastError();
       clusters = 1;
     }
     at_once[ctas].store(clusters, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(static_cast<unsigned>((rows < clusters ? rows : clusters) * ctas));
-  return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE>, z, dz, a, rows, ctas, per);
+  return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE, GRAD>, z, dz, a, rows, ctas, per);
 }
 
 // Clusters of `ctas` for slices of at most `most` elements; with rows for less than
@@ -1011,11 +1032,14 @@ cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int
   if (a.vocab <= small) return launch_row<T, VEC, kMore, 64>(z, dz, a, rows, 1, slice(1), s);
   if (a.vocab <= few) return launch_row<T, VEC, kMore, 128>(z, dz, a, rows, 1, slice(1), s);
   if constexpr (VEC) {
-    constexpr int64_t most = kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T));
+    // without dz a slice need not fit in the ring: 100 x 50001 fp32 take EVALNEW us in one slice, EVALOLD in two
+    const int64_t most = dz ? kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T)) : a.vocab;
     const int ctas = row_ctas(rows, a.vocab, most, few);
     if (most * ctas >= a.vocab)
-      return a.ce > 0.f ? launch_stream<T, true>(z, dz, a, rows, ctas, slice(ctas), s)
-                        : launch_stream<T, false>(z, dz, a, rows, ctas, slice(ctas), s);
+      return dz ? (a.ce > 0.f ? launch_stream<T, true, true>(z, dz, a, rows, ctas, slice(ctas), s)
+                              : launch_stream<T, false, true>(z, dz, a, rows, ctas, slice(ctas), s))
+                : (a.ce > 0.f ? launch_stream<T, true, false>(z, dz, a, rows, ctas, slice(ctas), s)
+                              : launch_stream<T, false, false>(z, dz, a, rows, ctas, slice(ctas), s));
   } else {
     constexpr int kLong = 64;
     constexpr int64_t most = Slice<T, VEC, kLong, 256>::kElems;
