@@ -65,6 +65,7 @@ using namespace attn;
 constexpr int kMaxBuckets = 64;
 constexpr int kMaxDistance = 4096;
 constexpr int kMaxSinks = 64;
+constexpr int kWide = 128;  // distances along a row of the widest tile
 constexpr float kHidden = -1e30f;  // a table entry at or below it hides its bucket
 
 struct WindowArgs {
@@ -73,6 +74,7 @@ struct WindowArgs {
   const float* table;   // [buckets][heads], or NULL
   int ranks;            // non-empty buckets, by rising distance (0: no bias)
   int last;             // first distance of the last of them
+  int near;             // from it on buckets have kWide distances or more (at most last)
   int start[kMaxBuckets];  // (first distance << 8) | bucket of each
   __host__ __device__ int first(int rank) const { return start[rank] >> 8; }
 };
@@ -132,41 +134,53 @@ __device__ __forceinline__ void rows_barrier() {
   asm volatile("bar.sync 3, %0;" ::"n"(N) : "memory");
 }
 
-// The bias of one head in shared memory: its value by distance in the log2
-// domain, and the rank of a distance's bucket.
-//   value[kLow + d], d = -kLow .. last + kHigh - 1: the last bucket's value from
-//   `last` on; a negative distance is masked, whatever is read for it.  Only a
-//   warp along some of whose rows the bucket changes reads it by column: 32 rows
-//   and up to 128 columns with a distance below `last`, so none of last + 158 on.
+// The bias of one head in shared memory, in the log2 domain, and the rank of a
+// distance's bucket.
+//   value[kLow + d], d = -kLow .. near + kHigh - 1: by distance, for warps along
+//   some of whose rows the bucket changes near the diagonal; a negative distance
+//   is masked, whatever is read for it.  Such a warp has 32 rows and up to 128
+//   columns with a distance below `near`, so none of near + 158 on.
+//   by_rank[k]: a bucket's value.  It is all a row needs that lies in one bucket,
+//   and beyond `near`, where a row meets at most two of them.
 //   rank[d], d = 0 .. last (rank_of clamps).
+// A table of values for every distance would be 16 KB larger at 4096 and leave an
+// SM one backward CTA instead of two: that of 2 x 4096 tokens, 16 heads, 32
+// buckets up to 4096 and their gradient then takes 572 us instead of BIGTAB.
 struct Bias {
   static constexpr int kLow = 128, kHigh = 160;
-  float* value;
+  float *value, *by_rank;
   uint8_t* rank;
-  int last;
-  static __host__ __device__ constexpr int value_words(int last) { return (kLow + last + kHigh + 3) & ~3; }
+  int near, last;
+  static __host__ __device__ constexpr int value_words(int near) { return (kLow + near + kHigh + 3) & ~3; }
   static __host__ __device__ constexpr int rank_bytes(int last) { return (last + 16) & ~15; }
-  static __host__ __device__ constexpr int bytes(int last) { return value_words(last) * 4 + rank_bytes(last); }
+  static __host__ __device__ constexpr int bytes(int near, int last) {
+    return (value_words(near) + kMaxBuckets) * 4 + rank_bytes(last);
+  }
+  __device__ __forceinline__ Bias(uint8_t* at, const WindowArgs& a) {
+    value = reinterpret_cast<float*>(at);
+    by_rank = value + value_words(a.near);
+    rank = reinterpret_cast<uint8_t*>(by_rank + kMaxBuckets);
+    near = a.near;
+    last = a.last;
+  }
 
   __device__ __forceinline__ int rank_of(int d) const { return rank[max(0, min(d, last))]; }
-  // Filled by the N row threads.
+  // By the N row threads: the ranks, once (the first head's values come after a barrier).
+  template <int N>
+  __device__ __forceinline__ void fill_ranks(const WindowArgs& a, int tid) {
+    for (int k = tid >> 5; k < a.ranks; k += N / 32)
+      for (int d = a.first(k) + (tid & 31), end = k + 1 < a.ranks ? a.first(k + 1) : last + 1; d < end; d += 32)
+        rank[d] = static_cast<uint8_t>(k);
+  }
   template <int N>
   __device__ __forceinline__ void fill(const WindowArgs& a, int head, int tid) {
     rows_barrier<N>();  // nobody reads the previous head's any more
-    for (int x = tid; x < kLow + last + kHigh; x += N) {
-      const int d = max(0, min(x - kLow, last));
-      int k = -1, at = 0;
-#pragma unroll 8
-      for (int i = 0; i < a.ranks; ++i) {
-        const int start = a.start[i];
-        const bool reached = start <= (d << 8 | 255);
-        k += reached;
-        at = reached ? start : at;
-      }
-      const float t = a.table[static_cast<int64_t>(at & 255) * a.heads + head];
-      value[x] = t <= kHidden ? -INFINITY : t * kLog2e;
-      if (x >= kLow && x <= kLow + last) rank[d] = static_cast<uint8_t>(k);
+    if (tid < a.ranks) {
+      const float t = a.table[static_cast<int64_t>(a.start[tid] & 255) * a.heads + head];
+      by_rank[tid] = t <= kHidden ? -INFINITY : t * kLog2e;
     }
+    rows_barrier<N>();
+    for (int x = tid; x < kLow + near + kHigh; x += N) value[x] = by_rank[rank_of(x - kLow)];
     rows_barrier<N>();
   }
 };
@@ -292,7 +306,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 12);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   uint8_t* rest = reinterpret_cast<uint8_t*>(bar) + 256;
-  Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
+  Bias bias(rest, a);
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int nqb = (a.seq + 127) / 128;
@@ -422,12 +436,20 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
     const uint32_t tS = tmem + lane, tO = tmem + 128 + lane, tP = tmem + 192 + lane;
     const RowWait wait{err, abort};
     float m = -INFINITY, l = 0.f;
-    if (BIAS) bias.fill<FWD_ROWS>(a, h, tid);
+    if (BIAS) {
+      bias.fill_ranks<FWD_ROWS>(a, tid);
+      bias.fill<FWD_ROWS>(a, h, tid);
+    }
     for (int t = 0; t < nt; ++t) {
       const int j0 = tile_key(t), w = width(t);
       const int d = qi - j0;  // distances d, d - 1, .. d - 127
+      int rank = 0, other = 0;
       bool flat = true;
-      if (BIAS) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d - 127));
+      if (BIAS) {
+        rank = bias.rank_of(d);
+        other = bias.rank_of(d - 127);
+        flat = __all_sync(0xffffffffu, rank == other);
+      }
       wait(bs, t & 1);
       tc_fence_after();
       float sv[128];
@@ -443,7 +465,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
       float sc = kScaleLog2, cb = 0.f;
       if (BIAS) {
         if (flat) {
-          cb = bias.value[Bias::kLow + max(0, min(d, a.last))];
+          cb = bias.by_rank[rank];
+        } else if (__all_sync(0xffffffffu, d - 127 >= bias.near)) {  // two buckets at most
+          const float x = bias.by_rank[rank], y = bias.by_rank[other];
+          const int first = d - a.first(rank);  // the column of the first bucket's first distance
+#pragma unroll
+          for (int i = 0; i < 128; ++i) sv[i] = fmaf(sv[i], kScaleLog2, i <= first ? x : y);
+          sc = 1.f;
         } else {
           const float* at = bias.value + Bias::kLow + d;
 #pragma unroll
@@ -733,8 +761,8 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
   const BwdBars s(sm);
   uint8_t *sdO = sm + DQ_DO, *ringV = sm + DQ_V, *ringK = sm + DQ_K;
   uint8_t* rest = ringK + stages * T64;
-  Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
-  if (MODE) rest += Bias::bytes(a.last);
+  Bias bias(rest, a);
+  if (MODE) rest += Bias::bytes(a.near, a.last);
   float* row_e = reinterpret_cast<float*>(rest);                               // [2][128]
   float* accS = row_e + BWD_ROWS;                                              // [ranks + 1][256]
   __half* accP = reinterpret_cast<__half*>(accS + (a.ranks + 1) * BWD_ROWS);   // [ranks + 1][256]
@@ -935,7 +963,10 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
         ends[x] = w;
       }
     }
-    if (MODE) bias.fill<BWD_ROWS>(a, h, tid);
+    if (MODE) {
+      bias.fill_ranks<BWD_ROWS>(a, tid);
+      bias.fill<BWD_ROWS>(a, h, tid);
+    }
     auto put = [&](int rank, float x, float p) {
       accS[rank * BWD_ROWS + tid] += x;
       __half* at = accP + rank * BWD_ROWS + tid;
@@ -947,11 +978,12 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
       const bool sink = t >= nwin;
       const int j0 = tile_key(t) + 32 * g;  // the key of this thread's column 0
       const int d = qi - j0;                // distances d, d - 1, .. d - 31
-      int rank = 0;
+      int rank = 0, other = 0;
       bool flat = true;
       if (MODE) {
         rank = bias.rank_of(d);
-        flat = __all_sync(0xffffffffu, rank == bias.rank_of(d - 31));
+        other = bias.rank_of(d - 31);
+        flat = __all_sync(0xffffffffu, rank == other);
       }
       wait(s.bs, t & 1);
       tc_fence_after();
@@ -963,11 +995,18 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
       tc_fence_before();
       mbar_arrive1(s.bsc);
       if (MODE && !flat) {
-        const float* at = bias.value + Bias::kLow + d;
+        if (__all_sync(0xffffffffu, d - 31 >= bias.near)) {  // two buckets at most
+          const float x = bias.by_rank[rank] + LD.x, y = bias.by_rank[other] + LD.x;
+          const int first = d - a.first(rank);  // the column of the first bucket's first distance
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kScaleLog2, at[-i] + LD.x);
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kScaleLog2, i <= first ? x : y);
+        } else {
+          const float* at = bias.value + Bias::kLow + d;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kScaleLog2, at[-i] + LD.x);
+        }
       } else {
-        const float x = (MODE ? bias.value[Bias::kLow + max(0, min(d, a.last))] : 0.f) + LD.x;
+        const float x = (MODE ? bias.by_rank[rank] : 0.f) + LD.x;
         const f32x2 x2 = pack2(x, x);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) unpack2(fma2(pack2(v[i], v[i + 1]), scale2, x2), v[i], v[i + 1]);
@@ -1113,7 +1152,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
   const BwdBars s(sm);
   uint8_t *sK = sm + DKV_K, *sV = sm + DKV_V, *ring = sm + DKV_RING;
   uint8_t* rest = ring + stages * DKV_STAGE;
-  Bias bias{reinterpret_cast<float*>(rest), rest + Bias::value_words(a.last) * 4, a.last};
+  Bias bias(rest, a);
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int kvh = item % a.kv_heads;
@@ -1264,22 +1303,35 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
     }
     const f32x2 scale2 = pack2(kScaleLog2, kScaleLog2);
     for (int t = 0; t < niter; ++t) {
+      if (MODE && t == 0) bias.fill_ranks<BWD_ROWS>(a, tid);
       if (MODE && qb == i0) bias.fill<BWD_ROWS>(a, hq, tid);
       const int q0 = qb * 64 + 32 * g;  // the query of this thread's column 0
       const int d = q0 - kr;            // distances d .. d + 31
+      int rank = 0, other = 0;
       bool flat = true;
-      if (MODE) flat = __all_sync(0xffffffffu, bias.rank_of(d) == bias.rank_of(d + 31));
+      if (MODE) {
+        rank = bias.rank_of(d + 31);
+        other = bias.rank_of(d);
+        flat = __all_sync(0xffffffffu, rank == other);
+      }
       wait(got_s, t & 1);
       tc_fence_after();
       float v[32];  // S^T - 8 lse
       ld_row32(tS + lane + 32 * g, v);
       if (MODE && !flat) {
-        const float* at = bias.value + Bias::kLow + d;
+        if (__all_sync(0xffffffffu, d >= bias.near)) {  // two buckets at most
+          const float x = bias.by_rank[rank], y = bias.by_rank[other];
+          const int first = a.first(rank) - d;  // the column of the second bucket's first distance
 #pragma unroll
-        for (int q = 0; q < 32; q += 2)
-          unpack2(fma2(pack2(v[q], v[q + 1]), scale2, pack2(at[q], at[q + 1])), v[q], v[q + 1]);
+          for (int q = 0; q < 32; ++q) v[q] = fmaf(v[q], kScaleLog2, q >= first ? x : y);
+        } else {
+          const float* at = bias.value + Bias::kLow + d;
+#pragma unroll
+          for (int q = 0; q < 32; q += 2)
+            unpack2(fma2(pack2(v[q], v[q + 1]), scale2, pack2(at[q], at[q + 1])), v[q], v[q + 1]);
+        }
       } else if (MODE) {
-        const float c = bias.value[Bias::kLow + max(0, min(d, a.last))];
+        const float c = bias.by_rank[rank];
         const f32x2 c2 = pack2(c, c);
 #pragma unroll
         for (int q = 0; q < 32; q += 2) unpack2(fma2(pack2(v[q], v[q + 1]), scale2, c2), v[q], v[q + 1]);
@@ -1507,7 +1559,8 @@ int window_args(WindowArgs& a, int nseq, int seq, int heads, int kv_heads, int w
     if ((b + 1 < buckets && starts[b + 1] == starts[b]) || starts[b] >= seq) continue;
     a.start[a.ranks++] = starts[b] << 8 | b;
   }
-  a.last = a.first(a.ranks - 1);
+  a.last = a.near = a.first(a.ranks - 1);
+  for (int k = a.ranks - 2; k >= 0 && a.first(k + 1) - a.first(k) >= kWide; --k) a.near = a.first(k);
   return GPIPE_OK;
 }
 
@@ -1536,10 +1589,10 @@ WindowScratch window_scratch(void* base, int nseq, int seq, int heads, int windo
   return w;
 }
 
-static_assert(fwd_smem(2, Bias::bytes(kMaxDistance)) <= kHalfSmem && fwd_smem(3, 0) <= kHalfSmem,
+static_assert(fwd_smem(2, Bias::bytes(kMaxDistance, kMaxDistance)) <= kHalfSmem && fwd_smem(3, 0) <= kHalfSmem,
               "two forward CTAs share an SM, with the largest table too");
-static_assert(dq_smem(2, Bias::bytes(kMaxDistance), dq_sums(kMaxBuckets, kMaxDistance), true) <= kMaxSmem &&
-                  dkv_smem(3, Bias::bytes(kMaxDistance)) <= kMaxSmem,
+static_assert(dq_smem(2, Bias::bytes(kMaxDistance, kMaxDistance), dq_sums(kMaxBuckets, kMaxDistance), true) <= kMaxSmem &&
+                  dkv_smem(3, Bias::bytes(kMaxDistance, kMaxDistance)) <= kMaxSmem,
               "the largest table and its sums fit beside the tiles");
 
 int prepare_attention_window() {
@@ -1601,7 +1654,7 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
       !make_tmap(&to, o, static_cast<int64_t>(heads) * HD, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_fwd: tensor map creation failed");
   const int grid = ((seq + 127) / 128) * heads * nseq;
-  const int smem = a.ranks ? fwd_smem(2, Bias::bytes(a.last)) : fwd_smem(3, 0);
+  const int smem = a.ranks ? fwd_smem(2, Bias::bytes(a.near, a.last)) : fwd_smem(3, 0);
   (void)launch_k<true>(a.ranks ? attn_window_fwd_kernel<true> : attn_window_fwd_kernel<false>, grid, FWD_THREADS,
                        smem, s, tq, to, a, static_cast<__nv_bfloat16*>(o), lse, err);
   return check_launch("attention_window_fwd");
@@ -1640,7 +1693,7 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   const int nqb = (seq + 127) / 128, n_dkv = nqb * kv_heads * nseq, n_dq = nqb * heads * nseq;
   auto kern = dtable_acc ? attn_window_bwd_kernel<2> : (a.ranks ? attn_window_bwd_kernel<1> : attn_window_bwd_kernel<0>);
   // three stages a ring where two CTAs still fit on an SM, or where they do not anyway
-  const int bias_bytes = a.ranks ? Bias::bytes(a.last) : 0;
+  const int bias_bytes = a.ranks ? Bias::bytes(a.near, a.last) : 0;
   const int sums = dtable_acc ? dq_sums(a.ranks, a.last) : 0;
   const bool far = w.far != nullptr;
   auto bytes = [&](int dkv, int dq) {
