@@ -147,7 +147,8 @@ int gpipe_op_attention_bwd(int nseq, int seq, int heads, const void* qkv, const 
  *             num_buckets - 1, decided in exact arithmetic
  *             (gpipe_op_position_bucket_starts); 2 <= num_buckets <= 64,
  *             num_buckets / 2 < max_distance <= 4096.
- * Any seq >= 1; nseq * seq <= 2^30.  Cost grows with the visible pairs. */
+ * Any seq >= 1; nseq * seq <= 2^30.  Cost grows with the visible pairs.  Outputs
+ * that overlap each other or qkv are rejected. */
 int gpipe_op_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
                                   const int32_t* lens, const float* table, int num_buckets,
                                   int max_distance, const void* qkv, void* o, float* lse, void* stream);
@@ -157,8 +158,8 @@ int gpipe_op_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, in
  * += sum of dS over the pairs of each bucket.  o and lse are the forward's, with
  * the same lens and table.  scratch: gpipe_op_attention_window_scratch_bytes,
  * 256-byte aligned, written before it is read (calls that may overlap on the
- * GPU, captured ones included, need one each).  No atomics: results are
- * bit-reproducible. */
+ * GPU, captured ones included, need one each).  dqkv and scratch may overlap
+ * neither the inputs nor each other.  No atomics: results are bit-reproducible. */
 int gpipe_op_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
                                   const int32_t* lens, const float* table, int num_buckets,
                                   int max_distance, const void* qkv, const void* o, const void* dout,

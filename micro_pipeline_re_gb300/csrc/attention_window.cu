@@ -50,6 +50,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/gpipe.h"
 #include "attention_tiles.cuh"
@@ -1485,7 +1486,7 @@ bool make_tmap(CUtensorMap* m, const void* base, int64_t cols, int64_t seq, int6
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// n^e >= md^k me^(e - k), in whole numbers of 32 words (4096^64 has 769 bits).
+// n^e >= md^k me^(e - k), in whole numbers of 32 words (e is at most 32, and 4096^32 has 385 bits).
 bool power_at_least(int n, int e, int md, int k, int me) {
   uint32_t x[32] = {1}, y[32] = {1};
   auto times = [](uint32_t* v, uint32_t f) {
@@ -1613,6 +1614,27 @@ int prepare_attention_window() {
   });
 }
 
+struct Range {
+  const void* at;
+  size_t bytes;
+};
+// The sizes of one call's tensors.
+struct Sizes {
+  size_t qkv, o, lse;
+  Sizes(const WindowArgs& a)
+      : qkv(static_cast<size_t>(a.nseq) * a.seq * (a.heads + 2 * a.kv_heads) * HD * 2),
+        o(static_cast<size_t>(a.nseq) * a.seq * a.heads * HD * 2),
+        lse(static_cast<size_t>(a.nseq) * a.seq * a.heads * 4) {}
+};
+bool overlaps(Range out, std::initializer_list<Range> others) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out.at);
+  for (const Range& r : others) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(r.at);
+    if (a < b + r.bytes && b < a + out.bytes) return true;
+  }
+  return false;
+}
+
 int check_launch(const char* what) {
   count_launch();
   const cudaError_t e = cudaGetLastError();
@@ -1645,6 +1667,9 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
   if (rc) return rc;
   if (!qkv || !o || !lse || !al16(qkv) || !al16(o))
     return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_fwd: qkv and o must be 16-B aligned, lse not NULL");
+  const Sizes size(a);
+  if (overlaps({o, size.o}, {{qkv, size.qkv}, {lse, size.lse}}) || overlaps({lse, size.lse}, {{qkv, size.qkv}}))
+    return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_fwd: o and lse may not overlap each other or qkv");
   rc = prepare_attention_window();
   if (rc) return rc;
   int* err = device_error_ptr();
@@ -1674,6 +1699,14 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
     return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: scratch must be 256-B aligned");
   if (dtable_acc && !table)
     return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: a table gradient needs the table");
+  const WindowScratch w = window_scratch(scratch, nseq, seq, heads, window, sinks, dtable_acc ? a.ranks : 0);
+  const Sizes size(a);
+  const Range read[] = {{qkv, size.qkv}, {o, size.o}, {dout, size.o}, {lse, size.lse}};
+  for (const Range& r : read)
+    if (overlaps(r, {{dqkv, size.qkv}, {scratch, w.bytes}}))
+      return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: dqkv and scratch may not overlap the inputs");
+  if (overlaps({dqkv, size.qkv}, {{scratch, w.bytes}}))
+    return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: dqkv and scratch may not overlap");
   rc = prepare_attention_window();
   if (rc) return rc;
   int* err = device_error_ptr();
@@ -1684,7 +1717,6 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
       !make_tmap(&td64, dout, D, seq, nseq, 64) || !make_tmap(&td128, dout, D, seq, nseq, 128) ||
       !make_tmap(&tg, dqkv, cols, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: tensor map creation failed");
-  const WindowScratch w = window_scratch(scratch, nseq, seq, heads, window, sinks, dtable_acc ? a.ranks : 0);
   const int64_t prep = static_cast<int64_t>(nseq) * pad128(seq) * heads * 8;
   (void)launch_k(attn_window_prep_kernel, static_cast<unsigned>((prep + 255) / 256), 256, 0, s, a,
                  static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, w.ld, w.terms);

@@ -248,6 +248,20 @@ def test_attention_window(b, shape):
     c.check()
 
 
+@pytest.mark.parametrize("shape", [
+    (1, 1500, 2, 1, 1500, 0, 8, 2000, None),    # buckets of 4, 13, 57, 251, 1119 .. distances
+    (1, 1300, 2, 2, 700, 40, 8, 1000, [1290]),  # the sinks' distances in wide buckets, some of them across a tile
+    (1, 1700, 3, 1, 900, 3, 48, 4096, None),    # sums of 48 buckets: one backward CTA on an SM
+    (2, 1200, 4, 2, 1200, 0, 2, 600, None),     # two buckets, the boundary far from the diagonal
+])
+def test_attention_window_wide_buckets(b, shape):
+    """Distances from which on every bucket is wider than a tile."""
+    c = Case(b, *shape[:8], lens=shape[8])
+    c.fwd()
+    c.bwd()
+    c.check()
+
+
 @pytest.mark.parametrize("hide", ["-inf", "lowest", "all", "nearest"])
 def test_attention_window_hidden_buckets(b, hide):
     """Table entries that hide a bucket; with the nearest bucket hidden the first
@@ -510,6 +524,28 @@ class Distill:
 ])
 def test_distill(b, dtype, rows, vocab, topk, kw):
     Distill(b, rows, vocab, topk, dtype, **kw).run().check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab,topk,kw", [
+    (400, 9000, 200, dict(seq=100)),          # several rows a CTA, one after the other
+    (330, 9000, 5, dict(ce=0.0, in_place=True)),
+    (170, 9001, 70, dict(seq=10)),            # unaligned rows, more than SMs
+    (3, 100001, 9, dict(seq=3)),              # unaligned, across a cluster
+    (2, 270001, 33, {}),                      # unaligned, more than a cluster holds
+])
+def test_distill_many_and_long_rows(b, dtype, rows, vocab, topk, kw):
+    Distill(b, rows, vocab, topk, dtype, **kw).run().check()
+
+
+@pytest.mark.parametrize("dtype,rows,vocab,kw", [
+    ("f32", 160, 70004, dict(seq=16)),        # a row is more than the ring of chunks holds
+    ("bf16", 200, 150000, dict(ce=0.0)),
+    ("f32", 1, 300003, dict(ld=300004)),
+    ("f32", 500, 6000, dict(seq=5)),
+])
+def test_distill_loss_alone_of_long_rows(b, dtype, rows, vocab, kw):
+    Distill(b, rows, vocab, 12, dtype, **kw).run(want=False).check()
 
 
 @pytest.mark.parametrize("vocab", [5, 4000, 131072])

@@ -102,6 +102,25 @@ def test_attention_window_bwd_refusals(b, bad):
     assert _bwd(b, **bad) == -1
 
 
+# tensors that do not touch each other: 2 x 64 rows of 512 (qkv, dqkv) or 256 (o, dout) columns, bf16
+APART = dict(qkv=1 << 20, o=2 << 20, dout=3 << 20, lse=4 << 20, dqkv=5 << 20, scratch=6 << 20)
+
+
+@pytest.mark.parametrize("bad", [dict(o=1 << 20), dict(o=(1 << 20) + 128 * 1024 - 16), dict(o=(1 << 20) - 128 * 512 + 16),
+                                 dict(lse=1 << 20), dict(lse=(2 << 20) + 128 * 512 - 4), dict(lse=(2 << 20) - 16)])
+def test_attention_window_refuses_overlapping_outputs(b, bad):
+    assert _fwd(b, **dict(APART, **bad)) == -1
+    assert b"overlap" in b.lib().gpipe_last_error(None)
+
+
+@pytest.mark.parametrize("bad", [dict(dqkv=1 << 20), dict(dqkv=(2 << 20) - 128 * 1024 + 16), dict(dqkv=3 << 20),
+                                 dict(dqkv=4 << 20), dict(dqkv=6 << 20), dict(scratch=1 << 20), dict(scratch=2 << 20),
+                                 dict(scratch=3 << 20), dict(scratch=4 << 20), dict(scratch=5 << 20)])
+def test_attention_window_bwd_refuses_overlaps(b, bad):
+    assert _bwd(b, **dict(APART, **bad)) == -1
+    assert b"overlap" in b.lib().gpipe_last_error(None)
+
+
 GOOD = dict(dtype=0, rows=4, vocab=32, logits=1 << 20, ld=32, topk=4, idx=256, val=256, t=2.0, kd=1.0, seq=4,
             tokens=256, row0=0, ce=1.0, loss=256, dz=1 << 30, lddz=32)
 
