@@ -611,7 +611,6 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
                                                                const float* __restrict__ lse, float2* __restrict__ ld,
                                                                uint8_t* __restrict__ terms) {
   griddep_wait();
-  griddep_launch();
   // eight threads per (sequence, query, head), each 8 of the 64 columns
   const int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
   const int sub = threadIdx.x & 7;
@@ -635,6 +634,7 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
   }
 #pragma unroll
   for (int s = 4; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+  griddep_launch();  // nothing but stores is left, so the main kernel's CTAs take no room for long before they run
   if (!in) return;
   const int64_t at = (b * a.heads + h) * seqpad + i;
   if (sub == 4) ld[at] = make_float2(L, -d);
@@ -1739,7 +1739,7 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   } else if (bytes(3, 3) > kMaxSmem) {
     dq_stages = 2;
   }
-  (void)launch_k<true>(kern, n_dkv + n_dq, BWD_THREADS, bytes(dkv_stages, dq_stages), s, tq64, tq128, td64, td128, tg, a,
+  (void)launch_k(kern, n_dkv + n_dq, BWD_THREADS, bytes(dkv_stages, dq_stages), s, tq64, tq128, td64, td128, tg, a,
                        w, static_cast<const __nv_bfloat16*>(qkv), static_cast<__nv_bfloat16*>(dqkv), n_dkv, dkv_stages,
                        dq_stages, err);
   rc = check_launch("attention_window_bwd");
