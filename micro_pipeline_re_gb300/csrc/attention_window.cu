@@ -27,8 +27,10 @@
 // in which the rows of a warp read consecutive words.
 //
 // The backward pass uses no atomics, so its results are bit-reproducible:
-//   prep    -lse log2(e) and -D of every (head, query), in a layout that the
-//           main kernel reads in rows; -inf for padded rows, whose P is then 0.
+//   prep    -lse log2(e) and -D of every (head, query), in rows for the dQ CTAs
+//           and as matrix operands for the dK/dV CTAs; -inf in the place of
+//           -lse log2(e) for padded rows and rows that see nothing, whose P is
+//           then 0.
 //   main    dQ CTAs (128 queries, 64-key blocks) and dK/dV CTAs (128 keys,
 //           64-query blocks, one query head of the group after the other).
 //           The pairs of the sinks with queries that have left the window far
@@ -43,6 +45,11 @@
 // sum dS and sum P by bucket; sum over all buckets of its dS is then the error
 // of D, e = D_exact - D, and the exact contribution of bucket b is
 // sum_b dS - e sum_b P.
+//
+// What is rounded to bf16, and why: P and dS, since the products that read them
+// take bf16 operands (fp16 ones would have to be o, dO, Q and K as well, whose
+// range they do not have), and o, dQ, dK, dV, the results.  Each costs at most
+// 2^-9 of the value; maxima, sums, D, lse and dtable are fp32 and wider.
 //
 // Every mbarrier wait is bounded as in attention.cu.  The shared-memory tiles'
 // layout is described in attention_tiles.cuh.
@@ -88,10 +95,10 @@ __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
 // a tile, so a row's maximum needs no exchange), two in the backward one (a
 // thread has half a row).  The issuers and the loader are warps of one more
 // warpgroup, since registers are passed on by whole warpgroups:
-//   forward   256 threads launched with 128 registers (32768); the row threads go
-//             up to 208, the others down to 48 (128 x 208 + 128 x 48 = 32768);
-//   backward  384 launched with 80 (30720); up to 96, down to 48
-//             (256 x 96 + 128 x 48 = 30720).
+//   forward   256 threads launched with 128 registers; the row threads go up to
+//             208, the others down to 48 (128 x 208 + 128 x 48 = 256 x 128);
+//   backward  384 launched with 80; up to 96, down to 48
+//             (256 x 96 + 128 x 48 = 384 x 80).
 constexpr int FWD_ROWS = 128, BWD_ROWS = 256;
 constexpr int FWD_THREADS = FWD_ROWS + 128, BWD_THREADS = BWD_ROWS + 128;
 
@@ -146,7 +153,7 @@ __device__ __forceinline__ void rows_barrier() {
 //   rank[d], d = 0 .. last (rank_of clamps).
 // A table of values for every distance would be 16 KB larger at 4096 and leave an
 // SM one backward CTA instead of two: that of 2 x 4096 tokens, 16 heads, 32
-// buckets up to 4096 and their gradient then takes 572 us instead of BIGTAB.
+// buckets up to 4096 and their gradient then takes 572 us instead of 355.
 struct Bias {
   static constexpr int kLow = 128, kHigh = 160;
   float *value, *by_rank;
@@ -286,7 +293,17 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int loaded, int sta
 // reads 6 KB for 32 cycles of tensor work, above the 128 B a cycle there is).
 // A row's maximum is only moved when a tile exceeds it by 2^8: P is then at most
 // 2^8, which neither bf16 nor the fp32 sums mind, and O is seldom rescaled.
-// The ring has three stages of K | V, two where the bias needs the room.
+// The ring has three stages of K | V (57 us at 16384 tokens, 8 heads over 2, a
+// window of 1024; 59 us with two), two where the bias needs the room.
+//
+// Bound by the row threads: a tile is a chain of one load of 128 scores, their
+// maximum, exponentials, sums and the store of P, with two such warps on each
+// quarter of an SM.  At that size 57 us is 583 TFLOP/s; the quarters issue in
+// 48 % of the cycles, the exponentials' unit is busy for 34 %, the tensor cores
+// for 32 %.  Two threads a row (64 columns each, a maximum exchanged) and the
+// bias in steps of 32 columns were slower (the latter 107 us to 104 us at 8192
+// tokens, 16 heads, a window of 2048).  4 x 512 tokens, 16 heads, a window of
+// 128: 10 us, of which the launch is most.
 constexpr int FWD_RING = T128;
 constexpr float kMaxStep = 8.f;
 constexpr int fwd_smem(int stages, int bias_bytes) { return FWD_RING + stages * 2 * T128 + 256 + bias_bytes; }
@@ -605,6 +622,8 @@ __device__ __forceinline__ uint4 three_terms(float x) {
   return make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.f), 0u, 0u);
 }
 
+// Bound by memory: reads o and dout, writes 136 bytes a (head, query), of which
+// 128 are the two operands.  8192 tokens, 16 heads: 10.4 us for 52 MB (5.0 TB/s).
 __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_constant__ WindowArgs a,
                                                                const __nv_bfloat16* __restrict__ o,
                                                                const __nv_bfloat16* __restrict__ dout,
@@ -753,6 +772,10 @@ constexpr int dkv_smem(int stages, int bias_bytes) {
 // nowhere else, so its sums are stored; only the first and the last are added to
 // what is there.  P's sums only weigh the error of D, which is some 2^-9 of dS:
 // fp16 is more than they need.
+//
+// Bound by the row threads' instructions: some 2000 cycles a tile with the
+// other CTA's work beside it, 4400 where the buckets change from column to
+// column.  Figures of the whole backward pass are at its kernel.
 template <int MODE>
 __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
                               const CUtensorMap* td128, const CUtensorMap* tg, const WindowScratch& ws_,
@@ -1142,9 +1165,11 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
 // the products that read them.  Each of the four has its own hand-off, so that
 // dV += P^T dO and the next S^T run while the rows make dS^T, and dK += dS^T Q
 // and the next dP^T while they make P^T.
-// (With P^T and dS^T in shared memory instead, the products and the rows together
-// moved 3.0 KB a cycle's worth of it per 128 x 128 pairs, and a tile took 1.6 times
-// as long.)
+// (With P^T and dS^T in shared memory instead, the products' reads of them and the
+// rows' writes kept it busy, and a tile took 1.6 times as long.)
+//
+// Bound by the latency of that chain of four hand-offs, with the other CTA's to
+// fill it.
 template <int MODE>
 __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
                                const CUtensorMap* td64, const CUtensorMap* tg, const WindowScratch& ws_,
@@ -1399,6 +1424,11 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
 }
 
 // One launch for both kinds, the dK/dV CTAs first (they have more to do).
+// 2 x 4096 tokens, 16 heads, everything visible, 32 buckets with their gradient:
+// 283 us (five products: 606 TFLOP/s); the quarters of an SM issue in 56 % of the
+// cycles, the tensor cores are busy for 41 %, the exponentials' unit for 22 %.
+// 8192 tokens, a window of 2048, 16 sinks: 323 us.  4 x 512 tokens, a window of
+// 128, no table: 21 us.
 template <int MODE>
 __global__ void __launch_bounds__(BWD_THREADS, 2)
     attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap tq128,
@@ -1419,7 +1449,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 2)
 // (slice, c) adds column c of its dV | dK over every fourth far query block, and
 // the slices are added in order.  Blocks n_sink ..: dtable of one head; a warp
 // adds every sixteenth (sequence, query block), lanes over the ranks, and the
-// warps are added in order.
+// warps are added in order.  Bound by latency: 4 us for 4 sinks of 64 (sequence,
+// head)s, 6.7 us for 16 sinks of 16 heads over 46 query blocks and the table.  (The
+// last CTA of the main kernel to leave a partial sum adding them instead, by a
+// counter, saved the launch and cost each CTA more: 437 us became 446 us for
+// forward and backward of 8192 tokens.)
 constexpr int kFinishThreads = 512;
 __global__ void __launch_bounds__(kFinishThreads) attn_window_finish_kernel(const __grid_constant__ WindowArgs a,
                                                                             const __grid_constant__ WindowScratch ws_,
@@ -1724,7 +1758,10 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   if (rc) return rc;
   const int nqb = (seq + 127) / 128, n_dkv = nqb * kv_heads * nseq, n_dq = nqb * heads * nseq;
   auto kern = dtable_acc ? attn_window_bwd_kernel<2> : (a.ranks ? attn_window_bwd_kernel<1> : attn_window_bwd_kernel<0>);
-  // three stages a ring where two CTAs still fit on an SM, or where they do not anyway
+  // Three stages a ring where two CTAs still fit on an SM, or where they do not anyway.  2 x 4096 tokens,
+  // 16 heads, everything visible, forward and backward: 391 us with three, 406 us with two (32 buckets up
+  // to 128).  With 36 buckets up to 1024 the backward pass takes 370 us with two stages in the dQ CTAs
+  // and two CTAs on an SM, 530 us with three and one.
   const int bias_bytes = a.ranks ? Bias::bytes(a.near, a.last) : 0;
   const int sums = dtable_acc ? dq_sums(a.ranks, a.last) : 0;
   const bool far = w.far != nullptr;

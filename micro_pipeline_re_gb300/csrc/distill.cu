@@ -347,17 +347,27 @@ __global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_b
 // the copies run ahead by whatever the ring has left beside the current slice,
 // so that memory is never idle while a row's sums are joined, and a row is read
 // from memory once although it is used twice.
-//   warp 24      copies: the chunks of row after row, as the ring empties.
+//   warp 20      copies: the chunks of row after row, as the ring empties.
 //   warps 0-15   pass A over a slice's chunks (maximum and sums), joined over the
 //                warps and, through remote shared memory, over the cluster; pass
 //                B over the same chunks, which writes dz and frees them.  For the loss alone
 //                pass A frees them, and a slice may be longer than the ring.
-//   warps 16-23  two groups, of the even and the odd rows: the teacher of a row ahead
+//   warps 16-19  two groups, of the even and the odd rows: the teacher of a row ahead
 //                of time (its tokens, the student's logits there, p), then, once its
 //                sums are known, its loss and, once pass B is done, the elements of
 //                its top tokens.
+//
+// Bound by memory where the label term is off (4096 x 131072 bf16: 381 us, 5.6
+// TB/s); with it, four exponentials and some 14 instructions an element share the
+// bound with it (2048 x 32000 fp32: 76 us, 5.2 TB/s, an SM's quarters issuing in
+// 64 % of the cycles; 4096 x 131072 bf16: 473 us).  Part of the label's
+// exponentials as polynomials, for the exponentials' unit's sake, made that 511 us
+// (a quarter of them) and 667 us (all).  One CTA of 512 pass threads was as fast
+// as two of half the ring, and 64 teacher threads a group leave the pass warps the
+// registers that 128 do not (381 and 395 us).
 constexpr int kChunk = 32768, kChunks = 6, kMaxSliceChunks = 4;
-constexpr int kPassThreads = 512, kTeachThreads = 64, kSlots = kMaxTop / kTeachThreads, kStreamThreads = kPassThreads + 2 * kTeachThreads + 32;
+constexpr int kPassThreads = 512, kTeachThreads = 64, kStreamThreads = kPassThreads + 2 * kTeachThreads + 32;
+constexpr int kSlots = kMaxTop / kTeachThreads;  // slots a teacher thread
 constexpr int kMaxCluster = 8;
 
 struct StreamShared {
@@ -382,7 +392,7 @@ __device__ __forceinline__ void teach_sync(int group) {
   asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "n"(kTeachThreads) : "memory");
 }
 
-// What a teacher thread has of its (up to two) slots of a row, step by step.
+// What a teacher thread has of its slots of a row, step by step.
 struct Fetched {
   int id[kSlots];
   float logit[kSlots];
@@ -812,7 +822,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // ---------------------------------------------------------------------------
 // A row in two passes
 // ---------------------------------------------------------------------------
-// For vocabularies beyond eight slices: the second pass reads the row again.
+// For rows that no cluster holds, and for the many unaligned ones that are still in
+// L2 when the second pass reads them again (figures at launch_rows).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logits,
                                                                  __nv_bfloat16* dz, DistillArgs a) {
@@ -989,7 +1000,8 @@ cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, i
   int clusters = at_once[ctas].load(std::memory_order_relaxed);
   if (clusters == 0) {
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / ctas * ctas));
-    if (cudaOccupancyMaxActiveClusters(&clusters, distill_stream_kernel<T, CE, GRAD>, &cfg) != cudaSuccess || clusters < 1) {
+    if (cudaOccupancyMaxActiveClusters(&clusters, distill_stream_kernel<T, CE, GRAD>, &cfg) != cudaSuccess ||
+        clusters < 1) {
       (void)cudaGetLastError();
       clusters = 1;
     }
@@ -1032,7 +1044,7 @@ cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int
   if (a.vocab <= small) return launch_row<T, VEC, kMore, 64>(z, dz, a, rows, 1, slice(1), s);
   if (a.vocab <= few) return launch_row<T, VEC, kMore, 128>(z, dz, a, rows, 1, slice(1), s);
   if constexpr (VEC) {
-    // without dz a slice need not fit in the ring: 100 x 50001 fp32 take EVALNEW us in one slice, EVALOLD in two
+    // without dz a slice need not fit in the ring: 1000 x 200000 bf16 take 87 us in one slice, 178 in four
     const int64_t most = dz ? kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T)) : a.vocab;
     const int ctas = row_ctas(rows, a.vocab, most, few);
     if (most * ctas >= a.vocab)
