@@ -1074,6 +1074,8 @@ int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t l
   if (!(temperature > 0.f) || !(temperature < INFINITY) || !(kd_scale >= 0.f) || !(kd_scale < INFINITY) ||
       !(ce_scale >= 0.f) || !(ce_scale < INFINITY))
     return set_error(GPIPE_ERR_INVALID_ARG, "distill: need a finite temperature > 0 and finite scales >= 0");
+  if (!(1.f / temperature < INFINITY) || !(kd_scale * temperature * temperature < INFINITY))
+    return set_error(GPIPE_ERR_INVALID_ARG, "distill: 1 / temperature and kd_scale temperature^2 must be finite in fp32");
   if (!logits || !top_idx || !top_logit || !loss_rows)
     return set_error(GPIPE_ERR_INVALID_ARG, "distill: NULL logits, top_idx, top_logit or loss_rows");
   if (ce_scale > 0.f && (!tokens || seq < 1 || row0 < 0))

@@ -531,6 +531,7 @@ def test_distill(b, dtype, rows, vocab, topk, kw):
     (400, 9000, 200, dict(seq=100)),          # several rows a CTA, one after the other
     (330, 9000, 5, dict(ce=0.0, in_place=True)),
     (170, 9001, 70, dict(seq=10)),            # unaligned rows, more than SMs
+    (160, 9001, 70, dict(in_place=True)),
     (3, 100001, 9, dict(seq=3)),              # unaligned, across a cluster
     (2, 270001, 33, {}),                      # unaligned, more than a cluster holds
 ])

@@ -146,5 +146,12 @@ def test_distill_refusals(b, bad):
     assert b"distill" in b.lib().gpipe_last_error(None)
 
 
+@pytest.mark.parametrize("bad", [dict(t=1e-40), dict(t=3e20), dict(t=1e10, kd=1e30)])
+def test_distill_refuses_temperatures_out_of_range(b, bad):
+    """Finite ones whose reciprocal, or whose square times the scale, is not."""
+    assert _distill(b, **bad) == -1
+    assert b"temperature" in b.lib().gpipe_last_error(None)
+
+
 def test_distill_refuses_other_types(b):
     assert _distill(b, dtype=2) == -6
