@@ -73,7 +73,7 @@ using namespace attn;
 constexpr int kMaxBuckets = 64;
 constexpr int kMaxDistance = 4096;
 constexpr int kMaxSinks = 64;
-constexpr int kWide = 128;  // distances along a row of the widest tile
+constexpr int kFwdColumns = 128, kBwdColumns = 32;  // of a tile that one thread has
 constexpr float kHidden = -1e30f;  // a table entry at or below it hides its bucket
 
 struct WindowArgs {
@@ -82,7 +82,7 @@ struct WindowArgs {
   const float* table;   // [buckets][heads], or NULL
   int ranks;            // non-empty buckets, by rising distance (0: no bias)
   int last;             // first distance of the last of them
-  int near;             // from it on buckets have kWide distances or more (at most last)
+  int near[2];          // from it on buckets have as many distances as a row has columns: [0] 128, [1] 32
   int start[kMaxBuckets];  // (first distance << 8) | bucket of each
   __host__ __device__ int first(int rank) const { return start[rank] >> 8; }
 };
@@ -153,7 +153,7 @@ __device__ __forceinline__ void rows_barrier() {
 //   rank[d], d = 0 .. last (rank_of clamps).
 // A table of values for every distance would be 16 KB larger at 4096 and leave an
 // SM one backward CTA instead of two: that of 2 x 4096 tokens, 16 heads, 32
-// buckets up to 4096 and their gradient then takes 572 us instead of 355.
+// buckets up to 4096 and their gradient took 572 us instead of 355.
 struct Bias {
   static constexpr int kLow = 128, kHigh = 160;
   float *value, *by_rank;
@@ -164,12 +164,10 @@ struct Bias {
   static __host__ __device__ constexpr int bytes(int near, int last) {
     return (value_words(near) + kMaxBuckets) * 4 + rank_bytes(last);
   }
-  __device__ __forceinline__ Bias(uint8_t* at, const WindowArgs& a) {
+  __device__ __forceinline__ Bias(uint8_t* at, int near_, int last_) : near(near_), last(last_) {
     value = reinterpret_cast<float*>(at);
-    by_rank = value + value_words(a.near);
+    by_rank = value + value_words(near);
     rank = reinterpret_cast<uint8_t*>(by_rank + kMaxBuckets);
-    near = a.near;
-    last = a.last;
   }
 
   __device__ __forceinline__ int rank_of(int d) const { return rank[max(0, min(d, last))]; }
@@ -324,7 +322,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 12);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   uint8_t* rest = reinterpret_cast<uint8_t*>(bar) + 256;
-  Bias bias(rest, a);
+  Bias bias(rest, a.near[0], a.last);
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int nqb = (a.seq + 127) / 128;
@@ -762,7 +760,8 @@ constexpr int dkv_smem(int stages, int bias_bytes) {
   return DKV_RING + stages * DKV_STAGE + bias_bytes;
 }
 
-// MODE 0: no bias; 1: bias; 2: bias and its gradient.
+// MODE 0: no bias; 1: bias; 2: bias and its gradient.  WIDE: there are buckets beyond
+// Bias::near besides the last one.
 //
 // dQ CTA: 128 queries, the window's 64-key tiles by rising key, the sinks' last.
 // For the gradient of the table each row thread adds its dS and P by bucket into
@@ -770,13 +769,15 @@ constexpr int dkv_smem(int stages, int bias_bytes) {
 // does not change add one sum.  Elsewhere the running sums are put down where a
 // bucket ends: a bucket that begins and ends among the thread's columns is met
 // nowhere else, so its sums are stored; only the first and the last are added to
-// what is there.  P's sums only weigh the error of D, which is some 2^-9 of dS:
+// what is there.  Beyond the narrow buckets a row meets at most two, and adds each
+// column to one of two sums: 2 x 4096 tokens, 16 heads, 32 buckets up to 4096 take
+// 322 us instead of 353 (backward), 64 of them 541 instead of 594.  P's sums only weigh the error of D, which is some 2^-9 of dS:
 // fp16 is more than they need.
 //
 // Bound by the row threads' instructions: some 2000 cycles a tile with the
 // other CTA's work beside it, 4400 where the buckets change from column to
 // column.  Figures of the whole backward pass are at its kernel.
-template <int MODE>
+template <int MODE, bool WIDE>
 __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
                               const CUtensorMap* td128, const CUtensorMap* tg, const WindowScratch& ws_,
                               const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* __restrict__ dqkv, int item,
@@ -785,8 +786,8 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
   const BwdBars s(sm);
   uint8_t *sdO = sm + DQ_DO, *ringV = sm + DQ_V, *ringK = sm + DQ_K;
   uint8_t* rest = ringK + stages * T64;
-  Bias bias(rest, a);
-  if (MODE) rest += Bias::bytes(a.near, a.last);
+  Bias bias(rest, a.near[1], a.last);
+  if (MODE) rest += Bias::bytes(a.near[1], a.last);
   float* row_e = reinterpret_cast<float*>(rest);                               // [2][128]
   float* accS = row_e + BWD_ROWS;                                              // [ranks + 1][256]
   __half* accP = reinterpret_cast<__half*>(accS + (a.ranks + 1) * BWD_ROWS);   // [ranks + 1][256]
@@ -1002,13 +1003,16 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
       const bool sink = t >= nwin;
       const int j0 = tile_key(t) + 32 * g;  // the key of this thread's column 0
       const int d = qi - j0;                // distances d, d - 1, .. d - 31
-      int rank = 0, other = 0;
+      int rank = 0;
       bool flat = true;
       if (MODE) {
         rank = bias.rank_of(d);
-        other = bias.rank_of(d - 31);
-        flat = __all_sync(0xffffffffu, rank == other);
+        flat = __all_sync(0xffffffffu, rank == bias.rank_of(d - 31));
       }
+      // Two buckets at most: that of column 0 up to column last_of_first(), then that of distance d - 31.
+      // (Asked for again where it is needed, which is cheaper than the registers to keep it in.)
+      auto two = [&] { return WIDE && __all_sync(0xffffffffu, d - 31 >= bias.near); };
+      auto last_of_first = [&] { return d - a.first(rank); };
       wait(s.bs, t & 1);
       tc_fence_after();
       float v[64];  // S (32 columns), then dP (32 columns), one round trip
@@ -1019,9 +1023,9 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
       tc_fence_before();
       mbar_arrive1(s.bsc);
       if (MODE && !flat) {
-        if (__all_sync(0xffffffffu, d - 31 >= bias.near)) {  // two buckets at most
-          const float x = bias.by_rank[rank] + LD.x, y = bias.by_rank[other] + LD.x;
-          const int first = d - a.first(rank);  // the column of the first bucket's first distance
+        if (two()) {
+          const float x = bias.by_rank[rank] + LD.x, y = bias.by_rank[bias.rank_of(d - 31)] + LD.x;
+          const int first = last_of_first();
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kScaleLog2, i <= first ? x : y);
         } else {
@@ -1064,6 +1068,21 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
           } else {
             put(rank, x0 + x1, y0 + y1);
           }
+        } else if (two()) {
+          const int first = last_of_first(), other = bias.rank_of(d - 31);
+          float s0 = 0.f, p0 = 0.f, s1 = 0.f, p1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (i <= first) {
+              s0 += v[32 + i];
+              p0 += v[i];
+            } else {
+              s1 += v[32 + i];
+              p1 += v[i];
+            }
+          }
+          put(rank, s0, p0);
+          if (other != rank) put(other, s1, p1);
         } else {
           // bit i: column i ends its bucket (its distance is the bucket's first).  From the bitmap,
           // distances low .. low + 31, the reverse of the columns' order.
@@ -1170,7 +1189,7 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
 //
 // Bound by the latency of that chain of four hand-offs, with the other CTA's to
 // fill it.
-template <int MODE>
+template <int MODE, bool WIDE>
 __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
                                const CUtensorMap* td64, const CUtensorMap* tg, const WindowScratch& ws_,
                                __nv_bfloat16* __restrict__ dqkv, int item, int stages, int* err) {
@@ -1178,7 +1197,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
   const BwdBars s(sm);
   uint8_t *sK = sm + DKV_K, *sV = sm + DKV_V, *ring = sm + DKV_RING;
   uint8_t* rest = ring + stages * DKV_STAGE;
-  Bias bias(rest, a);
+  Bias bias(rest, a.near[1], a.last);
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int kvh = item % a.kv_heads;
@@ -1345,7 +1364,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       float v[32];  // S^T - 8 lse
       ld_row32(tS + lane + 32 * g, v);
       if (MODE && !flat) {
-        if (__all_sync(0xffffffffu, d >= bias.near)) {  // two buckets at most
+        if (WIDE && __all_sync(0xffffffffu, d >= bias.near)) {  // two buckets at most
           const float x = bias.by_rank[rank], y = bias.by_rank[other];
           const int first = a.first(rank) - d;  // the column of the second bucket's first distance
 #pragma unroll
@@ -1427,9 +1446,9 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
 // 2 x 4096 tokens, 16 heads, everything visible, 32 buckets with their gradient:
 // 283 us (five products: 606 TFLOP/s); the quarters of an SM issue in 56 % of the
 // cycles, the tensor cores are busy for 41 %, the exponentials' unit for 22 %.
-// 8192 tokens, a window of 2048, 16 sinks: 323 us.  4 x 512 tokens, a window of
+// 8192 tokens, a window of 2048, 16 sinks, buckets up to 1024: 305 us.  4 x 512 tokens, a window of
 // 128, no table: 21 us.
-template <int MODE>
+template <int MODE, bool WIDE>
 __global__ void __launch_bounds__(BWD_THREADS, 2)
     attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap tq128,
                            const __grid_constant__ CUtensorMap td64, const __grid_constant__ CUtensorMap td128,
@@ -1440,9 +1459,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 2)
   if (misaligned(sm, err)) return;
   const int x = static_cast<int>(blockIdx.x);
   if (x < n_dkv)
-    window_bwd_dkv<MODE>(a, &tq64, &tq128, &td64, &tg, ws_, dqkv, x, dkv_stages, err);
+    window_bwd_dkv<MODE, WIDE>(a, &tq64, &tq128, &td64, &tg, ws_, dqkv, x, dkv_stages, err);
   else
-    window_bwd_dq<MODE>(a, &tq64, &tq128, &td128, &tg, ws_, qkv, dqkv, x - n_dkv, dq_stages, err);
+    window_bwd_dq<MODE, WIDE>(a, &tq64, &tq128, &td128, &tg, ws_, qkv, dqkv, x - n_dkv, dq_stages, err);
 }
 
 // Blocks 0 .. n_sink-1: one sink key of one (sequence, key/value head); thread
@@ -1452,8 +1471,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 2)
 // warps are added in order.  Bound by latency: 4 us for 4 sinks of 64 (sequence,
 // head)s, 6.7 us for 16 sinks of 16 heads over 46 query blocks and the table.  (The
 // last CTA of the main kernel to leave a partial sum adding them instead, by a
-// counter, saved the launch and cost each CTA more: 437 us became 446 us for
-// forward and backward of 8192 tokens.)
+// counter, saved the launch and cost each CTA more: 393 us became 401 us for
+// forward and backward of 2 x 4096 tokens.)
 constexpr int kFinishThreads = 512;
 __global__ void __launch_bounds__(kFinishThreads) attn_window_finish_kernel(const __grid_constant__ WindowArgs a,
                                                                             const __grid_constant__ WindowScratch ws_,
@@ -1594,8 +1613,10 @@ int window_args(WindowArgs& a, int nseq, int seq, int heads, int kv_heads, int w
     if ((b + 1 < buckets && starts[b + 1] == starts[b]) || starts[b] >= seq) continue;
     a.start[a.ranks++] = starts[b] << 8 | b;
   }
-  a.last = a.near = a.first(a.ranks - 1);
-  for (int k = a.ranks - 2; k >= 0 && a.first(k + 1) - a.first(k) >= kWide; --k) a.near = a.first(k);
+  a.last = a.near[0] = a.near[1] = a.first(a.ranks - 1);
+  for (int i = 0; i < 2; ++i)
+    for (int k = a.ranks - 2; k >= 0 && a.first(k + 1) - a.first(k) >= (i ? kBwdColumns : kFwdColumns); --k)
+      a.near[i] = a.first(k);
   return GPIPE_OK;
 }
 
@@ -1638,9 +1659,11 @@ int prepare_attention_window() {
     };
     const void* all[] = {reinterpret_cast<const void*>(attn_window_fwd_kernel<false>),
                          reinterpret_cast<const void*>(attn_window_fwd_kernel<true>),
-                         reinterpret_cast<const void*>(attn_window_bwd_kernel<0>),
-                         reinterpret_cast<const void*>(attn_window_bwd_kernel<1>),
-                         reinterpret_cast<const void*>(attn_window_bwd_kernel<2>)};
+                         reinterpret_cast<const void*>(attn_window_bwd_kernel<0, false>),
+                         reinterpret_cast<const void*>(attn_window_bwd_kernel<1, false>),
+                         reinterpret_cast<const void*>(attn_window_bwd_kernel<1, true>),
+                         reinterpret_cast<const void*>(attn_window_bwd_kernel<2, false>),
+                         reinterpret_cast<const void*>(attn_window_bwd_kernel<2, true>)};
     for (const void* f : all)
       if (set(f) != cudaSuccess) return set_error(GPIPE_ERR_CUDA, "attention_window: shared-memory attribute failed");
     if (!encode_fn()) return set_error(GPIPE_ERR_CUDA, "attention_window: cuTensorMapEncodeTiled entry point not found");
@@ -1713,7 +1736,7 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
       !make_tmap(&to, o, static_cast<int64_t>(heads) * HD, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_fwd: tensor map creation failed");
   const int grid = ((seq + 127) / 128) * heads * nseq;
-  const int smem = a.ranks ? fwd_smem(2, Bias::bytes(a.near, a.last)) : fwd_smem(3, 0);
+  const int smem = a.ranks ? fwd_smem(2, Bias::bytes(a.near[0], a.last)) : fwd_smem(3, 0);
   (void)launch_k<true>(a.ranks ? attn_window_fwd_kernel<true> : attn_window_fwd_kernel<false>, grid, FWD_THREADS,
                        smem, s, tq, to, a, static_cast<__nv_bfloat16*>(o), lse, err);
   return check_launch("attention_window_fwd");
@@ -1757,12 +1780,17 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   rc = check_launch("attention_window_bwd (prep)");
   if (rc) return rc;
   const int nqb = (seq + 127) / 128, n_dkv = nqb * kv_heads * nseq, n_dq = nqb * heads * nseq;
-  auto kern = dtable_acc ? attn_window_bwd_kernel<2> : (a.ranks ? attn_window_bwd_kernel<1> : attn_window_bwd_kernel<0>);
+  // Without wide buckets, what is there for them costs some 2 % (8 x up to 1000 tokens, 12 heads over 4, 32
+  // buckets up to 200, forward and backward: 104.5 us instead of 101.8); what they gain is at window_bwd_dq.
+  const bool wide = a.near[1] < a.last;
+  auto kern = dtable_acc ? (wide ? attn_window_bwd_kernel<2, true> : attn_window_bwd_kernel<2, false>)
+              : !a.ranks ? attn_window_bwd_kernel<0, false>
+                         : (wide ? attn_window_bwd_kernel<1, true> : attn_window_bwd_kernel<1, false>);
   // Three stages a ring where two CTAs still fit on an SM, or where they do not anyway.  2 x 4096 tokens,
   // 16 heads, everything visible, forward and backward: 391 us with three, 406 us with two (32 buckets up
   // to 128).  With 36 buckets up to 1024 the backward pass takes 370 us with two stages in the dQ CTAs
   // and two CTAs on an SM, 530 us with three and one.
-  const int bias_bytes = a.ranks ? Bias::bytes(a.near, a.last) : 0;
+  const int bias_bytes = a.ranks ? Bias::bytes(a.near[1], a.last) : 0;
   const int sums = dtable_acc ? dq_sums(a.ranks, a.last) : 0;
   const bool far = w.far != nullptr;
   auto bytes = [&](int dkv, int dq) {

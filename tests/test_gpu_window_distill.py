@@ -293,6 +293,18 @@ def test_attention_window_frozen_table(b):
     assert T().equal(first, c.dqkv)
 
 
+def test_attention_window_wide_buckets_frozen_table(b):
+    c = Case(b, 1, 900, 2, 1, 600, 5, 8, 1000)
+    c.fwd()
+    c.bwd()
+    c.check()
+    first, c.dtable = c.dqkv.clone(), None
+    c.dqkv.fill_(7.0)
+    c.bwd()
+    sync()
+    assert T().equal(first, c.dqkv)
+
+
 def test_attention_window_equals_plain_attention(b):
     """A window over everything is gpipe_op_attention_fwd, up to roundings."""
     t = T()
