@@ -141,14 +141,14 @@ __device__ __forceinline__ void fix_up(const DistillArgs& a, const int* idx, con
 // ---------------------------------------------------------------------------
 // A row in registers
 // ---------------------------------------------------------------------------
-// A cluster of C CTAs takes a row, each a slice of `per` elements, 16 bytes a
-// load and up to NV loads a thread, all of them issued before the first is used.
-// The row is read once, its maximum and sums are joined over the cluster, and dz
-// is made from the registers: the bytes the operator cannot do without and no
-// others.  The teacher's side is made while the row's loads are on their way.
+// A CTA takes a row, 16 bytes a load (one element, where rows do not start on
+// 16-byte boundaries) and up to NV loads a thread, all of them issued before the
+// first is used.  The row is read once and dz is made from the registers: the bytes
+// the operator cannot do without and no others.  The teacher's side is made while the row's loads are on their way.
 // Short rows take CTAs of 64 threads, so that many of them are under way on an
 // SM: a row's time is a chain of loads, sums and stores however short it is.
-// What a thread keeps of its slice: NV vectors as they came.
+//
+// What a thread keeps of its row: NV vectors as they came.
 template <typename T, bool VEC, int NV, int TH>
 struct Slice {
   static constexpr int E = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
@@ -198,30 +198,28 @@ struct Slice {
 
 template <typename T, bool VEC, int NV, int TH>
 __global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_bfloat16* dz,
-                                                         const __grid_constant__ DistillArgs a, int ctas, int per) {
+                                                         const __grid_constant__ DistillArgs a) {
   griddep_wait();
   griddep_launch();
   using S = Slice<T, VEC, NV, TH>;
   constexpr int E = S::E, W = TH / 32;
   __shared__ float sm_m[W], sm_s[W], sm_t[W];
-  __shared__ __align__(16) float mine[4];  // this CTA's maximum and sums, for the cluster
   __shared__ int idx[kMaxTop];
   __shared__ float tl[kMaxTop], zt[kMaxTop], pk[kMaxTop];
   __shared__ float sh_z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t r = blockIdx.x / ctas;
-  const int rank = blockIdx.x % ctas;
-  const int lo = rank * per, n = max(0, min(a.vocab - lo, per));
+  const int64_t r = blockIdx.x;
+  const int n = a.vocab;
   const T* z = logits + r * a.ld;
   const float c1 = kLog2e, ct = kLog2e * a.inv_t;
 
   S row;
-  row.load(z + lo, n, tid);
-  const int target = target_of(a, r, rank == 0 && tid == 0);
+  row.load(z, n, tid);
+  const int target = target_of(a, r, tid == 0);
   for (int k = tid; k < a.topk; k += TH) {
     int i = a.top_idx[r * a.topk + k];
     if (i >= a.vocab) {
-      if (rank == 0) atomicExch(a.err, DERR_BAD_TOKEN);
+      atomicExch(a.err, DERR_BAD_TOKEN);
       i = -1;
     }
     idx[k] = i;
@@ -278,23 +276,7 @@ __global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_b
   st = sm_t[0];
 #pragma unroll
   for (int w = 1; w < W; ++w) join(m, s1, st, sm_m[w], sm_s[w], sm_t[w], c1, ct);
-  if (ctas > 1) {
-    if (tid == 0) {
-      mine[0] = m;
-      mine[1] = s1;
-      mine[2] = st;
-    }
-    // also: nobody writes dz, which may lie over the logits, before all have read theirs
-    cluster_sync();
-    m = -INFINITY;
-    s1 = st = 0.f;
-    for (int c = 0; c < ctas; ++c) {  // in rank order, the same in every CTA
-      const uint32_t at = map_peer(smem_u32(mine), c);
-      join(m, s1, st, ld_peer_f32(at), ld_peer_f32(at + 4), ld_peer_f32(at + 8), c1, ct);
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  }
-  if (rank == 0 && warp == W - 1) {
+  if (warp == W - 1) {
     const float kl = divergence(a, tl, zt, pk, m, st, lane);
     if (lane == 0) {
       float loss = a.kd * kl;
@@ -319,24 +301,22 @@ __global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_b
           for (int e = 0; e < E; ++e) g[e] = fmaf(ex2_approx((v[e] - m) * c1), g1, g[e]);
         }
         if (i + E <= n) {
-          Vec<T, VEC>::store(out + lo + i, g);
+          Vec<T, VEC>::store(out + i, g);
         } else {
 #pragma unroll
           for (int e = 0; e < E; ++e)
-            if (i + e < n) out[lo + i + e] = f2bf(g[e]);
+            if (i + e < n) out[i + e] = f2bf(g[e]);
         }
       }
     }
     __syncthreads();
-    // the elements of the top tokens and of the target in this slice, once each
+    // the elements of the top tokens and of the target, once each
     for (int k = tid; k < a.topk; k += TH) {
       const int me = idx[k];
-      if (me >= lo && me < lo + n) fix_up(a, idx, pk, k, me, zt[k] - m, target, gt, g1, out);
+      if (me >= 0) fix_up(a, idx, pk, k, me, zt[k] - m, target, gt, g1, out);
     }
-    if (tid == 0 && target >= lo && target < lo + n) fix_up(a, idx, pk, a.topk, target, sh_z - m, target, gt, g1, out);
+    if (tid == 0 && target >= 0) fix_up(a, idx, pk, a.topk, target, sh_z - m, target, gt, g1, out);
   }
-  // the others may still be reading this CTA's sums
-  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -360,8 +340,8 @@ __global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_b
 // Bound by memory where the label term is off (4096 x 131072 bf16: 381 us, 5.6
 // TB/s); with it, four exponentials and some 14 instructions an element share the
 // bound with it (2048 x 32000 fp32: 76 us, 5.2 TB/s, an SM's quarters issuing in
-// 64 % of the cycles; 4096 x 131072 bf16: 473 us).  Part of the label's
-// exponentials as polynomials, for the exponentials' unit's sake, made that 511 us
+// 64 % of the cycles; 4096 x 131072 bf16: 492 us).  Part of the label's
+// exponentials as polynomials, for the exponentials' unit's sake, made 511 us of 473
 // (a quarter of them) and 667 us (all).  One CTA of 512 pass threads was as fast
 // as two of half the ring, and 64 teacher threads a group leave the pass warps the
 // registers that 128 do not (381 and 395 us).
@@ -415,7 +395,13 @@ struct Slots {
   bool fix_target;  // the target's element is this thread's: no slot names it
 };
 
-template <typename T, bool CE, bool GRAD>
+// GRAD: the loss alone, or with dz by wide stores, or, where a row of dz is not aligned
+// for them when its logits are, by single ones (2048 x 32001 logits in rows of 32008, dz
+// in rows of 32001, bf16: 91 us; 82 where both are alike, 150 with rows read twice).
+// ALIGNED: every row of logits starts on a 16-byte boundary, so that a CTA's part is the
+// same of all rows (4096 x 131072 bf16 381 us, 386 with a part made row by row).
+enum Grad { kLoss, kWide, kSingle };
+template <typename T, bool CE, Grad GRAD, bool ALIGNED>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     distill_stream_kernel(const T* logits, __nv_bfloat16* dz, const __grid_constant__ DistillArgs a, int rows, int ctas,
                           int per) {
@@ -425,9 +411,23 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   constexpr int E = 16 / static_cast<int>(sizeof(T)), kPer = kChunk / static_cast<int>(sizeof(T));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % ctas, clusters = gridDim.x / ctas;
-  const int lo = rank * per, n = max(0, min(a.vocab - lo, per));
-  const int whole = n / E * E;  // elements that come by copies; the last few are read directly
-  const int chunks = (whole + kPer - 1) / kPer;
+  // This CTA's part of row r: elements lo .. hi - 1, of which `whole` from the first
+  // 16-byte boundary on come by copies and the few before and behind them are read directly.
+  struct Part {
+    int lo, hi, from, whole, chunks;
+  };
+  auto part_of = [&](int64_t r) {
+    // (in 32 bits: E is a power of two, and only the low bits count)
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(logits) / sizeof(T)) +
+                        static_cast<uint32_t>(r) * static_cast<uint32_t>(a.ld);
+    Part p;
+    p.from = (ALIGNED ? 0 : static_cast<int>(-at & (E - 1))) + rank * per;
+    p.lo = rank ? min(p.from, a.vocab) : 0;
+    p.hi = min(a.vocab, p.from + per);
+    p.whole = max(0, p.hi - p.from) / E * E;
+    p.chunks = (p.whole + kPer - 1) / kPer;
+    return p;
+  };
   const int row0 = blockIdx.x / ctas;
   const float c1 = kLog2e, ct = kLog2e * a.inv_t;
 
@@ -456,13 +456,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       int64_t count = 0;
       bool go = true;
       for (int r = row0; r < rows && go; r += clusters) {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(logits + static_cast<int64_t>(r) * a.ld + lo);
-        for (int c = 0; c < chunks; ++c) {
+        const Part p = part_of(r);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(logits + static_cast<int64_t>(r) * a.ld + p.from);
+        for (int c = 0; c < p.chunks; ++c) {
           if (count >= kChunks && !lane_await(&sh.empty[slot], parity, a.err, DERR_TMA_WAIT, abort)) {
             go = false;
             break;
           }
-          const uint32_t bytes = static_cast<uint32_t>(min(kPer, whole - c * kPer)) * sizeof(T);
+          const uint32_t bytes = static_cast<uint32_t>(min(kPer, p.whole - c * kPer)) * sizeof(T);
           mbar_arrive_expect_tx(&sh.full[slot], bytes);
           bulk_load(ring + slot * kChunk, src + static_cast<int64_t>(c) * kChunk, bytes, &sh.full[slot]);
           ++count;
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       // (without dz too: a pass warp must have seen this row's teacher before the next one's is ready)
       (void)lane_await(&sh.done[b], parity, a.err, DERR_ACC_WAIT, abort);
       __syncwarp();
-      if (!GRAD) return;
+      if (GRAD == kLoss) return;
       const float gt = sh.has[b] != 0.f ? a.kd_grad / st : 0.f;
       const float g1 = s.target >= 0 ? a.ce / s1 : 0.f;
       __nv_bfloat16* out = dz + static_cast<int64_t>(r) * a.lddz;
@@ -616,10 +617,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (g1 != 0.f) g += ex2_approx(x * c1) * g1;
         return f2bf(is_target ? g - a.ce : g);
       };
+      const Part part = part_of(r);
 #pragma unroll
       for (int k = 0; k < kSlots; ++k)
-        if (s.me[k] >= lo && s.me[k] < lo + n) out[s.me[k]] = value(s.z[k] - m, s.sum[k], s.me[k] == s.target);
-      if (s.fix_target && s.target >= lo && s.target < lo + n) out[s.target] = value(s.zt - m, 0.f, true);
+        if (s.me[k] >= part.lo && s.me[k] < part.hi) out[s.me[k]] = value(s.z[k] - m, s.sum[k], s.me[k] == s.target);
+      if (s.fix_target && s.target >= part.lo && s.target < part.hi) out[s.target] = value(s.zt - m, 0.f, true);
     };
     const int64_t first = row0 + static_cast<int64_t>(b) * clusters, stride = 2 * static_cast<int64_t>(clusters);
     Gathered g = {};
@@ -653,13 +655,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     for (int r = row0; r < rows; r += clusters, ++i) {
       const int b = i & 1;
       const uint32_t turn = (i >> 1) & 1;
-      // the last elements of the slice, kept for pass B (dz may lie over them by then)
-      float tail = -INFINITY;
-      if (tid < n - whole) tail = Elem<T>::ld(logits + static_cast<int64_t>(r) * a.ld + lo + whole + tid);
+      const Part p = part_of(r);
+      const int whole = p.whole, chunks = p.chunks;
+      // the first and the last few elements, one a thread, kept for pass B (dz may lie over them by then)
+      auto edge_of = [&] {
+        if (ALIGNED) return p.from + whole + tid < p.hi ? p.from + whole + tid : -1;
+        const int at = tid < 16 ? tid : p.from + whole + tid - 16;
+        return tid < 32 && at >= p.lo && at < (tid < 16 ? p.from : p.hi) ? at : -1;
+      };
+      float edge = -INFINITY;
+      const int at_edge = edge_of();
+      if (at_edge >= 0) edge = Elem<T>::ld(logits + static_cast<int64_t>(r) * a.ld + at_edge);
       // pass A: running maximum (one check a chunk) and the sums
-      float m = tail;
+      float m = edge;
       f32x2 s12 = 0ull, st2 = 0ull;
-      if (tid < n - whole) s12 = st2 = pack2(tail == -INFINITY ? 0.f : ex2_approx(tail - tail), 0.f);  // 1 (NaN stays NaN)
+      if (at_edge >= 0) s12 = st2 = pack2(edge == -INFINITY ? 0.f : ex2_approx(edge - edge), 0.f);  // 1 (NaN stays NaN)
       int sl = slot;
       uint32_t pa = parity;
       for (int c = 0; c < chunks; ++c) {
@@ -691,7 +701,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             s12 = add2(s12, pack2(ex2_approx(x0), ex2_approx(x1)));
           }
         }
-        if (!GRAD) {  // no pass B
+        if (GRAD == kLoss) {  // no pass B
           __syncwarp();
           if (lane == 0) mbar_arrive1(&sh.empty[sl]);
         }
@@ -756,7 +766,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         sh.total[b][2] = st;
         mbar_arrive1(&sh.sums[b]);
       }
-      if (!GRAD) {
+      if (GRAD == kLoss) {
         slot = sl;
         parity = pa;
         __syncwarp();
@@ -766,24 +776,42 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       // pass B
       const float gt = sh.has[b] != 0.f ? a.kd_grad / st : 0.f;
       const float g1 = sh.label[b] != 0.f ? a.ce / s1 : 0.f;
-      __nv_bfloat16* out = dz + static_cast<int64_t>(r) * a.lddz + lo;
+      __nv_bfloat16* out = dz + static_cast<int64_t>(r) * a.lddz + p.from;
       const f32x2 m2 = pack2(-m, -m), gt2 = pack2(gt, gt), g12 = pack2(g1, g1);
       // dz of pairs, by which of the two terms the row has
       auto pass_b = [&](auto grad2) {
         for (int c = 0; c < chunks; ++c) {
           const int left = min(kPer, whole - c * kPer);
+          const T* chunk = reinterpret_cast<const T*>(ring + slot * kChunk);
           float v[V * E];
-          load_chunk(reinterpret_cast<const T*>(ring + slot * kChunk), left, v);
+          if constexpr (GRAD == kWide) {
+            load_chunk(chunk, left, v);
+          } else {  // element by element, neighbours to neighbouring threads
+#pragma unroll
+            for (int e = 0; e < V * E; ++e) {
+              const int at = e * kPassThreads + tid;
+              v[e] = at < left ? Elem<T>::ld(chunk + at) : -INFINITY;
+            }
+          }
 #pragma unroll
           for (int e = 0; e < V * E; e += 2) unpack2(grad2(add2(pack2(v[e], v[e + 1]), m2)), v[e], v[e + 1]);
-          __nv_bfloat16* to = out + c * kPer + tid * E;
-          if (left == kPer) {
+          __nv_bfloat16* to = out + c * kPer;
+          if constexpr (GRAD == kWide) {
+            to += tid * E;
+            if (left == kPer) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
+              for (int j = 0; j < V; ++j) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
+            } else {
+#pragma unroll
+              for (int j = 0; j < V; ++j)
+                if ((j * kPassThreads + tid) * E < left) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
+            }
           } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-              if ((j * kPassThreads + tid) * E < left) Vec<T, true>::store(to + j * kPassThreads * E, v + j * E);
+            for (int e = 0; e < V * E; ++e) {
+              const int at = e * kPassThreads + tid;
+              if (at < left) to[at] = f2bf(v[e]);
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive1(&sh.empty[slot]);
@@ -792,10 +820,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             parity ^= 1u;
           }
         }
-        if (tid < n - whole) {
+        if (at_edge >= 0) {
           float g, other;
-          unpack2(grad2(add2(pack2(tail, tail), m2)), g, other);
-          out[whole + tid] = f2bf(g);
+          unpack2(grad2(add2(pack2(edge, edge), m2)), g, other);
+          out[at_edge - p.from] = f2bf(g);
         }
       };
       auto exps = [&](f32x2 d, f32x2 scale) {
@@ -822,8 +850,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // ---------------------------------------------------------------------------
 // A row in two passes
 // ---------------------------------------------------------------------------
-// For rows that no cluster holds, and for the many unaligned ones that are still in
-// L2 when the second pass reads them again (figures at launch_rows).
+// For rows that no cluster holds, and for short unaligned ones, which the second pass
+// still finds in L2 (figures at launch_rows).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logits,
                                                                  __nv_bfloat16* dz, DistillArgs a) {
@@ -953,33 +981,12 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logit
   if (tid == 0 && target >= 0) fix_up(a, idx, pk, a.topk, target, sh_z - m, target, gt, g1, out);
 }
 
-// Launch the register kernel on clusters of `ctas`.
-template <typename T, bool VEC, int NV, int TH>
-cudaError_t launch_row(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int64_t rows, int ctas, int per,
-                       cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
-  cfg.blockDim = dim3(TH);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[3];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-  set_priority_attr(attr[2], s);
-  cfg.attrs = attr;
-  cfg.numAttrs = 3;
-  return cudaLaunchKernelEx(&cfg, distill_row_kernel<T, VEC, NV, TH>, z, dz, a, ctas, per);
-}
-
-template <typename T, bool CE, bool GRAD>
+template <typename T, bool CE, Grad GRAD, bool ALIGNED>
 cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, int ctas, int per,
                           cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   if (once_per_device(done, [] {
-        return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE, GRAD>,
+        return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE, GRAD, ALIGNED>,
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem));
       }))
     return cudaErrorInvalidValue;
@@ -1000,7 +1007,7 @@ cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, i
   int clusters = at_once[ctas].load(std::memory_order_relaxed);
   if (clusters == 0) {
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / ctas * ctas));
-    if (cudaOccupancyMaxActiveClusters(&clusters, distill_stream_kernel<T, CE, GRAD>, &cfg) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveClusters(&clusters, distill_stream_kernel<T, CE, GRAD, ALIGNED>, &cfg) != cudaSuccess ||
         clusters < 1) {
       (void)cudaGetLastError();
       clusters = 1;
@@ -1008,7 +1015,20 @@ cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, i
     at_once[ctas].store(clusters, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(static_cast<unsigned>((rows < clusters ? rows : clusters) * ctas));
-  return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE, GRAD>, z, dz, a, rows, ctas, per);
+  return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE, GRAD, ALIGNED>, z, dz, a, rows, ctas, per);
+}
+
+template <typename T, Grad GRAD>
+cudaError_t launch_stream_ce(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, int ctas, int per,
+                             bool aligned, cudaStream_t s) {
+  const bool ce = a.ce > 0.f;
+  if constexpr (GRAD != kSingle) {
+    if (aligned)
+      return ce ? launch_stream<T, true, GRAD, true>(z, dz, a, rows, ctas, per, s)
+                : launch_stream<T, false, GRAD, true>(z, dz, a, rows, ctas, per, s);
+  }
+  return ce ? launch_stream<T, true, GRAD, false>(z, dz, a, rows, ctas, per, s)
+            : launch_stream<T, false, GRAD, false>(z, dz, a, rows, ctas, per, s);
 }
 
 // Clusters of `ctas` for slices of at most `most` elements; with rows for less than
@@ -1020,46 +1040,38 @@ int row_ctas(int rows, int vocab, int64_t most, int64_t few) {
   return ctas;
 }
 
+constexpr int kShortBytes = 16384;
+
 // Which kernel takes the rows:
-//   up to 16 KB (aligned) or 4096 elements   registers, in the fewest threads that
-//       keep 4 or 8 loads each (16 or 32 of one element).  With 64 threads 65536
-//       rows of 512 fp32 take 364 us at 4 loads and 413 at 8, 8192 x 2048 take 88
-//       with 256 x 4 and 60 with 64 x 8, 8192 x 4096 take 91 with 256 x 4, 81 with
-//       64 x 16 and 72 with 128 x 8
-//   longer, aligned                          the stream: 2048 x 32000 bf16 81 us,
-//       115 with the row in registers
-//   longer, unaligned                        one element a load and a store.  Many
-//       rows of up to 256 KB read the row twice (2048 x 32001: 155 us fp32, 149
-//       bf16; 177 and 228 from registers), since the second time it is in L2; rows
-//       above that, or few, stay in registers (1000 x 100001 fp32: 280 us, 350
-//       read twice)
-//   what no cluster of 8 holds               is read twice
+//   up to 16 KB (where all rows are aligned for wide loads and stores) or 4096
+//       elements   registers, in the fewest threads that keep 4 or 8 loads each (16
+//       or 32 of one element).  With 64 threads 65536 rows of 512 fp32 take 364 us at
+//       4 loads and 413 at 8, 8192 x 2048 take 88 with 256 x 4 and 60 with 64 x 8,
+//       8192 x 4096 take 91 with 256 x 4, 81 with 64 x 16 and 72 with 128 x 8
+//   longer         the stream: 2048 x 32000 fp32 76 us, 115 with the row in
+//       registers; 2048 x 32001 bf16, unaligned, 82 us, 149 read twice, 1000 x
+//       100001 fp32 144 and 280 (in registers; 350 read twice).  Unaligned bf16
+//       rows of 8 to 16 KB are read twice: 8192 x 5001 158 us, 184 in the stream
+//   what no cluster of 8 holds   is read twice
 template <typename T, bool VEC>
-cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, cudaStream_t s) {
+cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, bool aligned, bool wide,
+                        cudaStream_t s) {
   constexpr int kFew = VEC ? 4 : 16, kMore = VEC ? 8 : 32;  // loads a thread
-  constexpr int tiny = Slice<T, VEC, kFew, 64>::kElems, small = Slice<T, VEC, kMore, 64>::kElems,
-                few = Slice<T, VEC, kMore, 128>::kElems;
-  const auto slice = [&](int ctas) { return ((a.vocab + ctas - 1) / ctas + 7) & ~7; };
-  if (a.vocab <= tiny) return launch_row<T, VEC, kFew, 64>(z, dz, a, rows, 1, slice(1), s);
-  if (a.vocab <= small) return launch_row<T, VEC, kMore, 64>(z, dz, a, rows, 1, slice(1), s);
-  if (a.vocab <= few) return launch_row<T, VEC, kMore, 128>(z, dz, a, rows, 1, slice(1), s);
-  if constexpr (VEC) {
-    // without dz a slice need not fit in the ring: 1000 x 200000 bf16 take 87 us in one slice, 178 in four
-    const int64_t most = dz ? kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T)) : a.vocab;
-    const int ctas = row_ctas(rows, a.vocab, most, few);
-    if (most * ctas >= a.vocab)
-      return dz ? (a.ce > 0.f ? launch_stream<T, true, true>(z, dz, a, rows, ctas, slice(ctas), s)
-                              : launch_stream<T, false, true>(z, dz, a, rows, ctas, slice(ctas), s))
-                : (a.ce > 0.f ? launch_stream<T, true, false>(z, dz, a, rows, ctas, slice(ctas), s)
-                              : launch_stream<T, false, false>(z, dz, a, rows, ctas, slice(ctas), s));
-  } else {
-    constexpr int kLong = 64;
-    constexpr int64_t most = Slice<T, VEC, kLong, 256>::kElems;
-    const int ctas = row_ctas(rows, a.vocab, most, few);
-    const bool again = rows > num_sms() && static_cast<int64_t>(a.vocab) * sizeof(T) <= (256 << 10);
-    if (!again && most * ctas >= a.vocab) return launch_row<T, VEC, kLong, 256>(z, dz, a, rows, ctas, slice(ctas), s);
-  }
-  return launch_k(distill_kernel<T, VEC>, rows, kDistillThreads, 0, s, z, dz, a);
+  if (a.vocab <= Slice<T, VEC, kFew, 64>::kElems)
+    return launch_k(distill_row_kernel<T, VEC, kFew, 64>, rows, 64, 0, s, z, dz, a);
+  if (a.vocab <= Slice<T, VEC, kMore, 64>::kElems)
+    return launch_k(distill_row_kernel<T, VEC, kMore, 64>, rows, 64, 0, s, z, dz, a);
+  if (a.vocab <= Slice<T, VEC, kMore, 128>::kElems)
+    return launch_k(distill_row_kernel<T, VEC, kMore, 128>, rows, 128, 0, s, z, dz, a);
+  // without dz a slice need not fit in the ring: 1000 x 200000 bf16 take 87 us in one slice, 178 in four
+  const int64_t most = dz ? kMaxSliceChunks * kChunk / static_cast<int>(sizeof(T)) : a.vocab;
+  const int ctas = row_ctas(rows, a.vocab, most, kShortBytes / static_cast<int>(sizeof(T)));
+  if (most * ctas < a.vocab || (!VEC && a.vocab * sizeof(T) <= kShortBytes))
+    return launch_k(distill_kernel<T, VEC>, rows, kDistillThreads, 0, s, z, dz, a);
+  const int per = ((a.vocab + ctas - 1) / ctas + 7) & ~7;
+  if (!dz) return launch_stream_ce<T, kLoss>(z, dz, a, rows, ctas, per, aligned, s);
+  if (wide) return launch_stream_ce<T, kWide>(z, dz, a, rows, ctas, per, aligned, s);
+  return launch_stream_ce<T, kSingle>(z, dz, a, rows, ctas, per, false, s);
 }
 
 }  // namespace
@@ -1112,16 +1124,22 @@ int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t l
   a.err = device_error_ptr();
   a.in_place = in_place;
   if (!a.err) return set_error(GPIPE_ERR_CUDA, "distill: no device error word");
-  // rows whose every start is aligned for 16-byte loads (and the stores that go with them)
-  const bool vec = al16(logits) && ld * static_cast<int64_t>(es) % 16 == 0 &&
-                   (!dz || (reinterpret_cast<uintptr_t>(dz) % (es == 4 ? 8 : 16) == 0 && lddz % (es == 4 ? 4 : 8) == 0));
+  const int64_t vec_elems = 16 / static_cast<int64_t>(es);
+  // where a row of logits meets a 16-byte boundary, its dz is aligned for the stores of as many elements
+  const bool wide = (lddz - ld) % vec_elems == 0 &&
+                    (reinterpret_cast<uintptr_t>(dz) / 2 - reinterpret_cast<uintptr_t>(logits) / es) % vec_elems ==
+                        0;
+  const bool aligned = al16(logits) && (rows == 1 || ld % vec_elems == 0);
+  // rows whose every start is aligned for 16-byte loads and the stores that go with them
+  const bool vec = aligned && ld % vec_elems == 0 &&
+                   (!dz || (reinterpret_cast<uintptr_t>(dz) % (es == 4 ? 8 : 16) == 0 && lddz % vec_elems == 0));
   __nv_bfloat16* d = static_cast<__nv_bfloat16*>(dz);
   if (dtype == DT_F32) {
     const float* z = static_cast<const float*>(logits);
-    (void)(vec ? launch_rows<float, true>(z, d, a, rows, s) : launch_rows<float, false>(z, d, a, rows, s));
+    (void)(vec ? launch_rows<float, true>(z, d, a, rows, aligned, wide, s) : launch_rows<float, false>(z, d, a, rows, aligned, wide, s));
   } else {
     const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(logits);
-    (void)(vec ? launch_rows<__nv_bfloat16, true>(z, d, a, rows, s) : launch_rows<__nv_bfloat16, false>(z, d, a, rows, s));
+    (void)(vec ? launch_rows<__nv_bfloat16, true>(z, d, a, rows, aligned, wide, s) : launch_rows<__nv_bfloat16, false>(z, d, a, rows, aligned, wide, s));
   }
   count_launch();
   const cudaError_t e = cudaGetLastError();

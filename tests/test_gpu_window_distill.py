@@ -545,6 +545,11 @@ def test_distill(b, dtype, rows, vocab, topk, kw):
     (170, 9001, 70, dict(seq=10)),            # unaligned rows, more than SMs
     (160, 9001, 70, dict(in_place=True)),
     (3, 100001, 9, dict(seq=3)),              # unaligned, across a cluster
+    (30, 5001, 20, dict(seq=10)),
+    (30, 5001, 20, dict(in_place=True)),
+    (5, 20001, 30, dict(lddz=20002)),         # logits and dz of different alignments
+    (200, 9001, 40, dict(ld=9003)),
+    (9, 100003, 256, dict(ld=100005, lddz=100013, seq=3)),
     (2, 270001, 33, {}),                      # unaligned, more than a cluster holds
 ])
 def test_distill_many_and_long_rows(b, dtype, rows, vocab, topk, kw):
