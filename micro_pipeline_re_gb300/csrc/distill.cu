@@ -1134,15 +1134,16 @@ int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t l
   const bool vec = aligned && ld % vec_elems == 0 &&
                    (!dz || (reinterpret_cast<uintptr_t>(dz) % (es == 4 ? 8 : 16) == 0 && lddz % vec_elems == 0));
   __nv_bfloat16* d = static_cast<__nv_bfloat16*>(dz);
-  if (dtype == DT_F32) {
-    const float* z = static_cast<const float*>(logits);
-    (void)(vec ? launch_rows<float, true>(z, d, a, rows, aligned, wide, s) : launch_rows<float, false>(z, d, a, rows, aligned, wide, s));
-  } else {
-    const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(logits);
-    (void)(vec ? launch_rows<__nv_bfloat16, true>(z, d, a, rows, aligned, wide, s) : launch_rows<__nv_bfloat16, false>(z, d, a, rows, aligned, wide, s));
-  }
+  auto launch = [&](auto* z) {
+    using T = std::remove_const_t<std::remove_pointer_t<decltype(z)>>;
+    return vec ? launch_rows<T, true>(z, d, a, rows, aligned, wide, s)
+               : launch_rows<T, false>(z, d, a, rows, aligned, wide, s);
+  };
+  cudaError_t e = dtype == DT_F32 ? launch(static_cast<const float*>(logits))
+                                  : launch(static_cast<const __nv_bfloat16*>(logits));
   count_launch();
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t last = cudaGetLastError();
+  if (e == cudaSuccess) e = last;
   if (e != cudaSuccess) return set_error(GPIPE_ERR_CUDA, "distill launch: %s", cudaGetErrorString(e));
   return GPIPE_OK;
 }
