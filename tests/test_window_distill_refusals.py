@@ -1,0 +1,111 @@
+"""Each refusal of the windowed attention and of the distillation by its own
+message.  The calls' pointers overlap on purpose, which is refused last: a check
+that has gone missing shows as the overlap's message, and nothing is launched on
+addresses that do not exist.  No CUDA call is made here."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def b():
+    from micro_pipeline_re_gb300 import _build
+    _build.build()
+    from micro_pipeline_re_gb300 import binding
+    binding.lib()
+    return binding
+
+
+A = 1 << 20   # every pointer: aligned for everything
+ATTENTION = dict(nseq=2, seq=64, heads=4, kv_heads=2, window=16, sinks=4, lens=A, table=A, num_buckets=8,
+                 max_distance=16, qkv=A, o=A, dout=A, lse=A, dqkv=A, dtable=A, scratch=A)
+
+
+def attention(b, backward, **kw):
+    a = dict(ATTENTION, **kw)
+    form = [a["nseq"], a["seq"], a["heads"], a["kv_heads"], a["window"], a["sinks"], a["lens"] or None,
+            a["table"] or None, a["num_buckets"], a["max_distance"], a["qkv"] or None, a["o"] or None]
+    lib = b.lib()
+    if backward:
+        rc = lib.gpipe_op_attention_window_bwd(*form, a["dout"] or None, a["lse"] or None, a["dqkv"] or None,
+                                               a["dtable"] or None, a["scratch"] or None, None)
+    else:
+        rc = lib.gpipe_op_attention_window_fwd(*form, a["lse"] or None, None)
+    return rc, lib.gpipe_last_error(None).decode()
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_attention_calls_that_only_overlap(b, backward):
+    """The calls below are refused for nothing else."""
+    rc, said = attention(b, backward)
+    assert rc == -1 and "overlap" in said
+
+
+HEADS, SINKS, BUCKETS = "multiple of kv_heads", "window >= 1 and 0 <= sinks", "2 <= num_buckets"
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("bad,words", [
+    (dict(nseq=0), HEADS), (dict(nseq=-1), HEADS), (dict(seq=0), HEADS), (dict(heads=0), HEADS),
+    (dict(kv_heads=0), HEADS), (dict(kv_heads=3), HEADS), (dict(kv_heads=8), HEADS),
+    (dict(heads=4097, kv_heads=1), HEADS),
+    (dict(nseq=1 << 16, seq=1 << 16), "at most 2^30"),
+    (dict(nseq=1 << 18, seq=1 << 12, heads=4096, kv_heads=4096), "2^28 blocks"),
+    (dict(window=0), SINKS), (dict(window=-5), SINKS), (dict(sinks=-1), SINKS), (dict(sinks=65), SINKS),
+    (dict(num_buckets=0), "goes with num_buckets"), (dict(table=0), "goes with num_buckets"),
+    (dict(num_buckets=1), BUCKETS), (dict(num_buckets=65), BUCKETS), (dict(num_buckets=-2), BUCKETS),
+    (dict(max_distance=4), BUCKETS), (dict(max_distance=4097), BUCKETS),
+    (dict(qkv=0), "16-B aligned"), (dict(qkv=A + 8), "16-B aligned"), (dict(o=0), "16-B aligned"),
+    (dict(o=A + 8), "16-B aligned"), (dict(lse=0), "lse not NULL")])
+def test_attention_refusals(b, backward, bad, words):
+    rc, said = attention(b, backward, **bad)
+    assert rc == -1 and words in said and "overlap" not in said
+
+
+@pytest.mark.parametrize("bad,words", [
+    (dict(dout=0), "16-B aligned"), (dict(dout=A + 8), "16-B aligned"), (dict(dqkv=0), "16-B aligned"),
+    (dict(dqkv=A + 24), "16-B aligned"), (dict(scratch=0), "256-B aligned"), (dict(scratch=A + 128), "256-B aligned"),
+    (dict(table=0, num_buckets=0), "needs the table")])
+def test_attention_backward_refusals(b, bad, words):
+    rc, said = attention(b, True, **bad)
+    assert rc == -1 and words in said and "overlap" not in said
+
+
+DISTILL = dict(dtype=0, rows=4, vocab=32, logits=A, ld=32, topk=4, idx=A, val=A, t=2.0, kd=1.0, seq=4, tokens=A, row0=0,
+               ce=1.0, loss=A, dz=A, lddz=32)
+
+
+def distill(b, **kw):
+    a = dict(DISTILL, **kw)
+    lib = b.lib()
+    rc = lib.gpipe_op_distill(a["dtype"], a["rows"], a["vocab"], a["logits"] or None, a["ld"], a["topk"],
+                              a["idx"] or None, a["val"] or None, a["t"], a["kd"], a["seq"], a["tokens"] or None,
+                              a["row0"], a["ce"], a["loss"] or None, a["dz"] or None, a["lddz"], None)
+    return rc, lib.gpipe_last_error(None).decode()
+
+
+def test_distill_call_that_only_overlaps(b):
+    rc, said = distill(b)
+    assert rc == -1 and "overlap" in said
+
+
+SIZES, SCALES, NULLS, LABELS = "1 <= rows <= 2^27", "finite temperature > 0 and finite scales", "NULL", "seq >= 1 and row0"
+
+
+@pytest.mark.parametrize("bad,words", [
+    (dict(rows=0), SIZES), (dict(rows=(1 << 27) + 1), SIZES), (dict(vocab=0), SIZES),
+    (dict(vocab=(1 << 30) + 1, ld=1 << 31, lddz=1 << 31), SIZES), (dict(ld=31), SIZES), (dict(topk=0), SIZES),
+    (dict(topk=257), SIZES),
+    (dict(t=0.0), SCALES), (dict(t=-1.0), SCALES), (dict(t=float("nan")), SCALES), (dict(t=float("inf")), SCALES),
+    (dict(kd=-1.0), SCALES), (dict(kd=float("nan")), SCALES), (dict(kd=float("inf")), SCALES), (dict(ce=-1.0), SCALES),
+    (dict(ce=float("nan")), SCALES), (dict(ce=float("inf")), SCALES),
+    (dict(logits=0), NULLS), (dict(idx=0), NULLS), (dict(val=0), NULLS), (dict(loss=0), NULLS),
+    (dict(tokens=0), LABELS), (dict(seq=0), LABELS), (dict(row0=-1), LABELS),
+    (dict(logits=A + 2), "aligned to their elements"), (dict(dtype=1, logits=A + 1), "aligned to their elements"),
+    (dict(dz=A + 1), "aligned to their elements"), (dict(lddz=31), "lddz must be at least vocab")])
+def test_distill_refusals(b, bad, words):
+    rc, said = distill(b, **bad)
+    assert rc == -1 and words in said and "overlap" not in said
+
+
+def test_distill_refuses_other_types(b):
+    rc, said = distill(b, dtype=2)
+    assert rc == -6 and "dtype must be 0 or 1" in said
