@@ -141,6 +141,10 @@ int gpipe_op_attention_bwd(int nseq, int seq, int heads, const void* qkv, const 
  *             lse as -inf.
  *   table     fp32 [num_buckets, heads], or NULL with num_buckets 0.  An entry
  *             of -1e30 or less (-inf, the lowest finite value) hides its bucket.
+ *             Other finite entries may have any size: only how far they are from
+ *             the largest one that a query sees is rounded (the lse, which holds
+ *             that one, has its own 24 bits).  Heads with entries above 256 in
+ *             size take a slower path.
  *             A query that sees nothing has o = 0, lse = -inf, zero gradients.
  *   bucket(d) d itself below e = num_buckets / 2, then e + floor(log(d / e) /
  *             log(max_distance / e) * (num_buckets - e)), at most

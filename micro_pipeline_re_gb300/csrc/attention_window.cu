@@ -58,6 +58,7 @@
 #include <atomic>
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 
 #include "../../include/gpipe.h"
 #include "attention_tiles.cuh"
@@ -76,6 +77,15 @@ constexpr int kMaxSinks = 64;
 constexpr int kFwdColumns = 128, kBwdColumns = 32;  // of a tile that one thread has
 constexpr float kHidden = -1e30f;  // a table entry at or below it hides its bucket
 
+// Scores and lse carry a row's bias, and P in the backward pass is the exponential
+// of their difference, so what they are rounded by is an error of P: some six
+// roundings of 2^-24 of the bias, 2^-13 at 256.  A row whose visible entries are all
+// below -256, or one of them above 256, has the largest of them, its base, taken out
+// of the exponent instead: t - base loses nothing whatever their size, and lse alone
+// gets it back.
+constexpr float kBigBias = 256.f;
+__device__ __forceinline__ bool big_bias(float t) { return fabsf(t) > kBigBias && fabsf(t) < INFINITY; }
+
 struct WindowArgs {
   int nseq, seq, heads, kv_heads, window, sinks;
   const int32_t* lens;  // valid tokens per sequence, or NULL: seq
@@ -85,6 +95,10 @@ struct WindowArgs {
   int near[2];          // from it on buckets have as many distances as a row has columns: [0] 128, [1] 32
   int start[kMaxBuckets];  // (first distance << 8) | bucket of each
   __host__ __device__ int first(int rank) const { return start[rank] >> 8; }
+  __device__ __forceinline__ float entry(int rank, int head) const {
+    const float t = table[static_cast<int64_t>(start[rank] & 255) * heads + head];
+    return t <= kHidden ? -INFINITY : t;
+  }
 };
 
 __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
@@ -142,8 +156,7 @@ __device__ __forceinline__ void rows_barrier() {
   asm volatile("bar.sync 3, %0;" ::"n"(N) : "memory");
 }
 
-// The bias of one head in shared memory, in the log2 domain, and the rank of a
-// distance's bucket.
+// The bias of one head in shared memory, and the rank of a distance's bucket.
 //   value[kLow + d], d = -kLow .. near + kHigh - 1: by distance, for warps along
 //   some of whose rows the bucket changes near the diagonal; a negative distance
 //   is masked, whatever is read for it.  Such a warp has 32 rows and up to 128
@@ -151,6 +164,8 @@ __device__ __forceinline__ void rows_barrier() {
 //   by_rank[k]: a bucket's value.  It is all a row needs that lies in one bucket,
 //   and beyond `near`, where a row meets at most two of them.
 //   rank[d], d = 0 .. last (rank_of clamps).
+//   *big: whether the head has big entries.  Values are in the log2 domain where it
+//   has none, and as the table has them where it has.
 // A table of values for every distance would be 16 KB larger at 4096 and leave an
 // SM one backward CTA instead of two: that of 2 x 4096 tokens, 16 heads, 32
 // buckets up to 4096 and their gradient took 572 us instead of 355.
@@ -158,13 +173,14 @@ struct Bias {
   static constexpr int kLow = 128, kHigh = 160;
   float *value, *by_rank;
   uint8_t* rank;
+  int* big;
   int near, last;
   static __host__ __device__ constexpr int value_words(int near) { return (kLow + near + kHigh + 3) & ~3; }
   static __host__ __device__ constexpr int rank_bytes(int last) { return (last + 16) & ~15; }
   static __host__ __device__ constexpr int bytes(int near, int last) {
     return (value_words(near) + kMaxBuckets) * 4 + rank_bytes(last);
   }
-  __device__ __forceinline__ Bias(uint8_t* at, int near_, int last_) : near(near_), last(last_) {
+  __device__ __forceinline__ Bias(uint8_t* at, int* big_, int near_, int last_) : big(big_), near(near_), last(last_) {
     value = reinterpret_cast<float*>(at);
     by_rank = value + value_words(near);
     rank = reinterpret_cast<uint8_t*>(by_rank + kMaxBuckets);
@@ -181,14 +197,31 @@ struct Bias {
   template <int N>
   __device__ __forceinline__ void fill(const WindowArgs& a, int head, int tid) {
     rows_barrier<N>();  // nobody reads the previous head's any more
-    if (tid < a.ranks) {
-      const float t = a.table[static_cast<int64_t>(a.start[tid] & 255) * a.heads + head];
-      by_rank[tid] = t <= kHidden ? -INFINITY : t * kLog2e;
+    if (tid < kMaxBuckets) {  // two warps, each of which looks at all entries
+      // (a tile of a head with big entries takes a path of its own, in code apart from the others')
+      const float t = tid < a.ranks ? a.entry(tid, head) : 0.f, other = (tid ^ 32) < a.ranks ? a.entry(tid ^ 32, head) : 0.f;
+      const bool any = __any_sync(0xffffffffu, big_bias(t) || big_bias(other));
+      if (tid < a.ranks) by_rank[tid] = any ? t : t * kLog2e;
+      if (tid == 0) *big = any;
     }
     rows_barrier<N>();
     for (int x = tid; x < kLow + near + kHigh; x += N) value[x] = by_rank[rank_of(x - kLow)];
     rows_barrier<N>();
   }
+  // The base of query i's row: the largest entry that it sees, if that is big.  (Not
+  // kept: only heads with big entries ask for it.)
+  __device__ __forceinline__ float base(const WindowArgs& a, int i) const {
+    float x = -INFINITY;
+#pragma unroll 1
+    for (int k = rank_of(min(i, a.window - 1)); k >= 0; --k) x = fmaxf(x, by_rank[k]);
+    if (a.sinks > 0) {
+#pragma unroll 1
+      for (int k = rank_of(i), end = rank_of(i - a.sinks + 1); k >= end; --k) x = fmaxf(x, by_rank[k]);
+    }
+    return big_bias(x) ? x : 0.f;
+  }
+  // What distance d adds to a score (log2 domain) of a row with this base, in a head with big entries.
+  __device__ __forceinline__ float without(float base, int d) const { return (by_rank[rank_of(d)] - base) * kLog2e; }
 };
 
 // Bits 0..x of a word (x < 0: none, x >= 31: all).
@@ -322,7 +355,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 12);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   uint8_t* rest = reinterpret_cast<uint8_t*>(bar) + 256;
-  Bias bias(rest, a.near[0], a.last);
+  Bias bias(rest, reinterpret_cast<int*>(tslot + 2), a.near[0], a.last);
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int nqb = (a.seq + 127) / 128;
@@ -456,6 +489,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
       bias.fill_ranks<FWD_ROWS>(a, tid);
       bias.fill<FWD_ROWS>(a, h, tid);
     }
+    const bool big = BIAS && *bias.big;
     for (int t = 0; t < nt; ++t) {
       const int j0 = tile_key(t), w = width(t);
       const int d = qi - j0;  // distances d, d - 1, .. d - 127
@@ -480,7 +514,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
       // same all along the row, or with the bias by distance already added
       float sc = kScaleLog2, cb = 0.f;
       if (BIAS) {
-        if (flat) {
+        if (__builtin_expect(big, 0)) {
+          const float base = bias.base(a, qi);
+#pragma unroll
+          for (int i = 0; i < 128; ++i) sv[i] = fmaf(sv[i], kScaleLog2, bias.without(base, d - i));
+          sc = 1.f;
+        } else if (flat) {
           cb = bias.by_rank[rank];
         } else if (__all_sync(0xffffffffu, d - 127 >= bias.near)) {  // two buckets at most
           const float x = bias.by_rank[rank], y = bias.by_rank[other];
@@ -567,7 +606,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 2)
     stage_row32(tO, sQ, tid, 0, 1.0f / l, keep);  // in Q's place: its products are done
     stage_row32(tO + 32, sQ, tid, 4, 1.0f / l, keep);
     send_tile(&to, h * HD, q0, b, sQ, 1, FWD_ROWS, tid == 0);
-    if (qi < a.seq) lse[(row0 + qi) * a.heads + h] = keep ? (m + log2f(l)) * kLn2 : -INFINITY;
+    const float base = big ? bias.base(a, qi) : 0.f;
+    if (qi < a.seq) lse[(row0 + qi) * a.heads + h] = keep ? fmaf(m + log2f(l), kLn2, base) : -INFINITY;
   }
   tc_fence_before();
   __syncthreads();
@@ -606,7 +646,8 @@ __host__ __device__ constexpr int first_far_block(int window) { return (window +
 // scale is applied afterwards) or -D of the 64 queries in its first three columns,
 // as a sum of three bf16 terms (24 bits).  Both are tiles without swizzle: 8 rows
 // of 16 bytes (8 columns) follow each other, the two column halves are 128 bytes
-// apart, the groups of 8 rows 256.
+// apart, the groups of 8 rows 256.  (The second column half is zeros, but for
+// the mark of has_base; A is 0 there.)
 constexpr int kTerms = 2048;       // bytes of B for 64 queries
 constexpr int kOnes = 4096;        // of A
 __device__ __forceinline__ uint64_t terms_desc(uint32_t tile) {
@@ -620,25 +661,95 @@ __device__ __forceinline__ uint4 three_terms(float x) {
   return make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.f), 0u, 0u);
 }
 
+// Where the operands of query i are (the first of its two rows of 16 bytes).
+__device__ __forceinline__ int64_t terms_at(const WindowArgs& a, int64_t b, int h, int i) {
+  const int64_t at = (b * a.heads + h) * pad128(a.seq) + i;
+  return (at >> 6) * (2 * kTerms) + (i >> 3 & 7) * 256 + (i & 7) * 16;
+}
+// Whether the row's -lse is without its base: said in the first column of the second
+// half of the -lse operand, where A is 0.
+__device__ __forceinline__ bool has_base(const uint8_t* terms, const WindowArgs& a, int64_t b, int h, int i) {
+  return *reinterpret_cast<const uint16_t*>(terms + terms_at(a, b, h, i) + 128) != 0;
+}
+
+// Eight threads per (sequence, query, head) of the preparation, heads fastest.
+struct PrepItem {
+  int h, i;
+  int64_t b;
+  __device__ __forceinline__ explicit PrepItem(const WindowArgs& a) {
+    const int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
+    const int seqpad = pad128(a.seq);
+    h = static_cast<int>(item % a.heads);
+    const int64_t bi = item / a.heads;
+    i = static_cast<int>(bi % seqpad);
+    b = bi / seqpad;
+  }
+};
+
+// A row whose |lse| is above kBigLse and that has a base gets its -lse without the
+// base.  lse has too few bits for the difference, so the row's sum is made again, by
+// eight threads, each 8 columns.  (Below kBigLse lse itself is accurate enough, whatever the base.)
+constexpr float kBigLse = 128.f;
+__device__ __noinline__ void take_out_base(const WindowArgs& a, const __nv_bfloat16* qkv, float2* ld, uint8_t* terms) {
+  const PrepItem at(a);
+  const int64_t b = at.b;
+  const int h = at.h, i = at.i, sub = threadIdx.x & 7;
+  const uint32_t eight = 0xffu << (threadIdx.x & 24);
+  const int lo = max(0, i - a.window + 1), sinks = min(a.sinks, lo);  // keys 0 .. sinks - 1 and lo .. i
+  float base = -INFINITY;
+  for (int k = sub; k < a.ranks; k += 8) {
+    const int from = a.first(k), to = k + 1 < a.ranks ? a.first(k + 1) : a.seq;  // distances from .. to - 1
+    if (from <= i - lo || (sinks > 0 && from <= i && to > i - sinks + 1)) base = fmaxf(base, a.entry(k, h));
+  }
+#pragma unroll
+  for (int s = 4; s > 0; s >>= 1) base = fmaxf(base, __shfl_xor_sync(eight, base, s));
+  if (!big_bias(base)) return;
+  const int64_t stride = static_cast<int64_t>(a.heads + 2 * a.kv_heads) * HD;
+  const __nv_bfloat16* rows = qkv + b * a.seq * stride + 8 * sub;
+  const __nv_bfloat16* keys = rows + (a.heads + h / (a.heads / a.kv_heads)) * HD;
+  float q[8];
+  load8(rows + i * stride + h * HD, q);
+  // log2 sum_j 2^((s_ij - base) log2(e)) over the visible keys
+  float m = -INFINITY, l = 0.f;
+  int rank = a.ranks - 1;
+  for (int x = 0; x < sinks + i - lo + 1; ++x) {
+    const int j = x < sinks ? x : lo + x - sinks;
+    while (a.first(rank) > i - j) --rank;  // (distances fall; the first bucket begins at 0)
+    float k[8], s = 0.f;
+    load8(keys + j * stride, k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(q[e], k[e], s);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(eight, s, o);
+    s = fmaf(s, kScaleLog2, (a.entry(rank, h) - base) * kLog2e);
+    if (s > m) {
+      l *= ex2_approx(m == -INFINITY ? m : m - s);
+      m = s;
+    }
+    l += ex2_approx(m == -INFINITY ? s : s - m);
+  }
+  const float L = -(m + log2f(l));
+  uint8_t* to = terms + terms_at(a, b, h, i);
+  if (sub == 4) ld[(b * a.heads + h) * pad128(a.seq) + i].x = L;  // (each word by the thread that wrote it before)
+  if (sub == 0) *reinterpret_cast<uint4*>(to) = three_terms(L * (1.f / kScaleLog2));
+  if (sub == 1) *reinterpret_cast<uint4*>(to + 128) = make_uint4(1u, 0u, 0u, 0u);
+}
+
 // Bound by memory: reads o and dout, writes 136 bytes a (head, query), of which
 // 128 are the two operands.  8192 tokens, 16 heads: 10.4 us for 52 MB (5.0 TB/s).
-__global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_constant__ WindowArgs a,
-                                                               const __nv_bfloat16* __restrict__ o,
-                                                               const __nv_bfloat16* __restrict__ dout,
-                                                               const float* __restrict__ lse, float2* __restrict__ ld,
-                                                               uint8_t* __restrict__ terms) {
+__global__ void __launch_bounds__(256, 8) attn_window_prep_kernel(const __grid_constant__ WindowArgs a,
+                                                                  const __nv_bfloat16* __restrict__ qkv,
+                                                                  const __nv_bfloat16* __restrict__ o,
+                                                                  const __nv_bfloat16* __restrict__ dout,
+                                                                  const float* __restrict__ lse, float2* __restrict__ ld,
+                                                                  uint8_t* __restrict__ terms) {
   griddep_wait();
-  // eight threads per (sequence, query, head), each 8 of the 64 columns
-  const int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
-  const int sub = threadIdx.x & 7;
-  const int seqpad = pad128(a.seq);
-  const int h = static_cast<int>(item % a.heads);
-  const int64_t bi = item / a.heads;
-  const int i = static_cast<int>(bi % seqpad);
-  const int64_t b = bi / seqpad;
+  const PrepItem of(a);
+  const int h = of.h, i = of.i, sub = threadIdx.x & 7, seqpad = pad128(a.seq);  // sub: 8 of the 64 columns
+  const int64_t b = of.b;
   const bool in = b < a.nseq;
   const bool live = in && i < seq_len(a, static_cast<int>(in ? b : 0));
-  float d = 0.f, L = -INFINITY;
+  float d = 0.f, v = -INFINITY;  // lse
   if (live) {
     const int64_t row = (b * a.seq + i) * a.heads + h;
     float x[8], y[8];
@@ -646,9 +757,9 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
     load8(dout + row * HD + 8 * sub, y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) d = fmaf(x[e], y[e], d);
-    const float v = lse[row];
-    L = v == -INFINITY ? -INFINITY : -v * kLog2e;  // a row that sees nothing: P = 0
+    v = lse[row];
   }
+  float L = v == -INFINITY ? v : -v * kLog2e;  // a row that sees nothing: P = 0
 #pragma unroll
   for (int s = 4; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
   griddep_launch();  // nothing but stores is left, so the main kernel's CTAs take no room for long before they run
@@ -661,6 +772,7 @@ __global__ void __launch_bounds__(256) attn_window_prep_kernel(const __grid_cons
     *reinterpret_cast<uint4*>(tile + (i >> 3 & 7) * 256 + (sub & 1) * 128 + (i & 7) * 16) =
         sub & 1 ? make_uint4(0u, 0u, 0u, 0u) : three_terms(x);
   }
+  if (a.ranks && fabsf(v) > kBigLse && v != -INFINITY) take_out_base(a, qkv, ld, terms);
 }
 
 // Both kinds of CTA own 128 rows and walk 64-wide tiles; two CTAs share an SM,
@@ -683,6 +795,7 @@ struct BwdBars {
   uint64_t *full, *full2, *one, *bs, *bo, *bfin, *bsink, *bsd, *empty, *empty2, *bsc, *bp, *brow, *bq;
   uint32_t* tslot;
   volatile int* abort;
+  int* big;
   __device__ __forceinline__ explicit BwdBars(uint8_t* at) {
     full = reinterpret_cast<uint64_t*>(at);
     full2 = full + 3;
@@ -700,6 +813,7 @@ struct BwdBars {
     bq = full + 20;
     tslot = reinterpret_cast<uint32_t*>(full + 21);
     abort = reinterpret_cast<volatile int*>(tslot + 1);
+    big = reinterpret_cast<int*>(tslot + 2);
   }
   // first(): the first copies, which leave before anything else is set up
   template <typename F>
@@ -786,7 +900,7 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
   const BwdBars s(sm);
   uint8_t *sdO = sm + DQ_DO, *ringV = sm + DQ_V, *ringK = sm + DQ_K;
   uint8_t* rest = ringK + stages * T64;
-  Bias bias(rest, a.near[1], a.last);
+  Bias bias(rest, s.big, a.near[1], a.last);
   if (MODE) rest += Bias::bytes(a.near[1], a.last);
   float* row_e = reinterpret_cast<float*>(rest);                               // [2][128]
   float* accS = row_e + BWD_ROWS;                                              // [ranks + 1][256]
@@ -999,7 +1113,8 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
     };
     const float2 LD = ws_.ld[(static_cast<int64_t>(b) * a.heads + h) * pad128(a.seq) + qi];
     const f32x2 scale2 = pack2(kScaleLog2, kScaleLog2), D2 = pack2(LD.y, LD.y);
-    for (int t = 0; t < nt; ++t) {
+    auto tile = [&](auto big_head, float base, int t) {
+      constexpr bool BIG = decltype(big_head)::value;
       const bool sink = t >= nwin;
       const int j0 = tile_key(t) + 32 * g;  // the key of this thread's column 0
       const int d = qi - j0;                // distances d, d - 1, .. d - 31
@@ -1022,7 +1137,10 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
       }
       tc_fence_before();
       mbar_arrive1(s.bsc);
-      if (MODE && !flat) {
+      if (BIG) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kScaleLog2, bias.without(base, d - i) + LD.x);
+      } else if (MODE && !flat) {
         if (two()) {
           const float x = bias.by_rank[rank] + LD.x, y = bias.by_rank[bias.rank_of(d - 31)] + LD.x;
           const int first = last_of_first();
@@ -1132,6 +1250,12 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
           *reinterpret_cast<uint4*>(ringK + swz(r, 4 * g + i)) =
               make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
       }
+    };
+    if (MODE && __builtin_expect(*bias.big, 0)) {
+      const float base = has_base(ws_.terms, a, b, h, qi) ? bias.base(a, qi) : 0.f;
+      for (int t = 0; t < nt; ++t) tile(std::bool_constant<MODE != 0>(), base, t);
+    } else {
+      for (int t = 0; t < nt; ++t) tile(std::false_type(), 0.f, t);
     }
     if (MODE == 2) {
       put(a.ranks - 1, farS, farP);
@@ -1197,7 +1321,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
   const BwdBars s(sm);
   uint8_t *sK = sm + DKV_K, *sV = sm + DKV_V, *ring = sm + DKV_RING;
   uint8_t* rest = ring + stages * DKV_STAGE;
-  Bias bias(rest, a.near[1], a.last);
+  Bias bias(rest, s.big, a.near[1], a.last);
 
   const int tid = threadIdx.x, warp = warp_number(), ln = tid & 31;
   const int kvh = item % a.kv_heads;
@@ -1347,9 +1471,8 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       mbar_arrive1(s.bq);
     }
     const f32x2 scale2 = pack2(kScaleLog2, kScaleLog2);
-    for (int t = 0; t < niter; ++t) {
-      if (MODE && t == 0) bias.fill_ranks<BWD_ROWS>(a, tid);
-      if (MODE && qb == i0) bias.fill<BWD_ROWS>(a, hq, tid);
+    auto tile = [&](auto big_head, int t) {
+      constexpr bool BIG = decltype(big_head)::value;
       const int q0 = qb * 64 + 32 * g;  // the query of this thread's column 0
       const int d = q0 - kr;            // distances d .. d + 31
       int rank = 0, other = 0;
@@ -1363,7 +1486,12 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       tc_fence_after();
       float v[32];  // S^T - 8 lse
       ld_row32(tS + lane + 32 * g, v);
-      if (MODE && !flat) {
+      if (BIG) {  // a column's base: lane q has column q's
+        const float base = has_base(ws_.terms, a, b, hq, q0 + ln) ? bias.base(a, q0 + ln) : 0.f;
+#pragma unroll
+        for (int q = 0; q < 32; ++q)
+          v[q] = fmaf(v[q], kScaleLog2, bias.without(__shfl_sync(0xffffffffu, base, q), d + q));
+      } else if (MODE && !flat) {
         if (WIDE && __all_sync(0xffffffffu, d >= bias.near)) {  // two buckets at most
           const float x = bias.by_rank[rank], y = bias.by_rank[other];
           const int first = a.first(rank) - d;  // the column of the second bucket's first distance
@@ -1411,9 +1539,14 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive1(wrote_ds);
-      if (++qb == i0 + nq) {
-        qb = i0;
-        ++hq;
+    };
+    if (MODE) bias.fill_ranks<BWD_ROWS>(a, tid);
+    for (int t = 0; t < niter; ++hq) {
+      if (MODE) bias.fill<BWD_ROWS>(a, hq, tid);
+      if (MODE && __builtin_expect(*bias.big, 0)) {
+        for (qb = i0; qb < i0 + nq; ++qb, ++t) tile(std::bool_constant<MODE != 0>(), t);
+      } else {
+        for (qb = i0; qb < i0 + nq; ++qb, ++t) tile(std::false_type(), t);
       }
     }
     wait(done_v, (niter - 1) & 1);
@@ -1776,7 +1909,7 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
     return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: tensor map creation failed");
   const int64_t prep = static_cast<int64_t>(nseq) * pad128(seq) * heads * 8;
   (void)launch_k(attn_window_prep_kernel, static_cast<unsigned>((prep + 255) / 256), 256, 0, s, a,
-                 static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, w.ld, w.terms);
+                 static_cast<const __nv_bfloat16*>(qkv), static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, w.ld, w.terms);
   rc = check_launch("attention_window_bwd (prep)");
   if (rc) return rc;
   const int nqb = (seq + 127) / 128, n_dkv = nqb * kv_heads * nseq, n_dq = nqb * heads * nseq;
