@@ -13,7 +13,7 @@
 //
 // Both softmaxes share the maximum m of z: q_T = e^{(z - m) / T} / s_T.  The
 // subtraction comes first, so the exponent is exact to fp32 however large the
-// logits are.  The top tokens are few, so dz is written as if there were none
+// logits are; so it does in p.  The top tokens are few, so dz is written as if there were none
 // and their elements are written again; slots that name the same token are
 // added by the first of them, in slot order, so that nothing depends on timing.
 #include <atomic>
@@ -90,12 +90,12 @@ __device__ __forceinline__ bool teacher(const DistillArgs& a, float* tl, float* 
   tm = warp_max(tm);
   const float tb = tm == -INFINITY ? 0.f : tm;
   float ts = 0.f;
-  for (int k = lane; k < a.topk; k += 32) ts += expf(tl[k] - tb);
+  for (int k = lane; k < a.topk; k += 32) ts += expf((tl[k] - tb) * a.inv_t);
   ts = warp_sum(ts);
   const float log_ts = logf(ts);
   for (int k = lane; k < a.topk; k += 32) {
-    pk[k] = ts == 0.f ? 0.f : expf(tl[k] - tb) / ts;
-    tl[k] = tl[k] - tb - log_ts;
+    pk[k] = ts == 0.f ? 0.f : expf((tl[k] - tb) * a.inv_t) / ts;
+    tl[k] = (tl[k] - tb) * a.inv_t - log_ts;
   }
   return ts != 0.f;
 }
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_b
       i = -1;
     }
     idx[k] = i;
-    tl[k] = i >= 0 ? a.top_logit[r * a.topk + k] * a.inv_t : -INFINITY;
+    tl[k] = i >= 0 ? a.top_logit[r * a.topk + k] : -INFINITY;
     zt[k] = i >= 0 ? Elem<T>::ld(z + i) : 0.f;
   }
   if (tid == 0 && target >= 0) sh_z = Elem<T>::ld(z + target);
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           i = -1;
         }
         g.id[k] = i;
-        g.tl[k] = i >= 0 ? f.logit[k] * a.inv_t : -INFINITY;
+        g.tl[k] = i >= 0 ? f.logit[k] : -INFINITY;
         g.z[k] = i >= 0 ? Elem<T>::ld(z + i) : 0.f;
       }
       g.target = f.target;
@@ -541,15 +541,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       tm = warp_max(tm);
       const float tb = tm == -INFINITY ? 0.f : tm;
       float ts = 0.f;
-      for (int k = lane; k < a.topk; k += 32) ts += expf(sh.pk[b][k] - tb);
+      for (int k = lane; k < a.topk; k += 32) ts += expf((sh.pk[b][k] - tb) * a.inv_t);
       ts = warp_sum(ts);
       const float log_ts = logf(ts);
       teach_sync(b);
 #pragma unroll
       for (int k = 0; k < kSlots; ++k) {
         const int slot = t + k * kTeachThreads;
-        s.p[k] = ts == 0.f || id[k] < 0 ? 0.f : expf(tl[k] - tb) / ts;
-        s.logp[k] = tl[k] - tb - log_ts;
+        const float x = (tl[k] - tb) * a.inv_t;
+        s.p[k] = ts == 0.f || id[k] < 0 ? 0.f : expf(x) / ts;
+        s.logp[k] = x - log_ts;
         sh.pk[b][slot] = s.p[k];
       }
       if (t == 0) {
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logit
       i = -1;
     }
     idx[tid] = i;
-    tl[tid] = i >= 0 ? a.top_logit[r * a.topk + tid] * a.inv_t : -INFINITY;
+    tl[tid] = i >= 0 ? a.top_logit[r * a.topk + tid] : -INFINITY;
     zt[tid] = i >= 0 ? Elem<T>::ld(z + i) : 0.f;
   }
   if (tid == 0 && target >= 0) sh_z = Elem<T>::ld(z + target);
