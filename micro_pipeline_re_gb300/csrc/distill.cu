@@ -986,11 +986,11 @@ template <typename T, bool CE, Grad GRAD, bool ALIGNED>
 cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, int ctas, int per,
                           cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  if (once_per_device(done, [] {
-        return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE, GRAD, ALIGNED>,
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem));
-      }))
-    return cudaErrorInvalidValue;
+  const int rc = once_per_device(done, [] {
+    return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE, GRAD, ALIGNED>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem));
+  });
+  if (rc) return static_cast<cudaError_t>(rc);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kStreamThreads);
   cfg.dynamicSmemBytes = kStreamSmem;
@@ -1004,17 +1004,13 @@ cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, i
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   // as many clusters as run at once (a cluster lives within one GPC, so large ones may leave SMs over)
-  static std::atomic<int> at_once[kMaxCluster + 1];
-  int clusters = at_once[ctas].load(std::memory_order_relaxed);
-  if (clusters == 0) {
+  static PerDevice<kMaxCluster + 1> at_once;
+  int clusters = 0;
+  const cudaError_t e = at_once.get(ctas, [&](int* n) {
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / ctas * ctas));
-    if (cudaOccupancyMaxActiveClusters(&clusters, distill_stream_kernel<T, CE, GRAD, ALIGNED>, &cfg) != cudaSuccess ||
-        clusters < 1) {
-      (void)cudaGetLastError();
-      clusters = 1;
-    }
-    at_once[ctas].store(clusters, std::memory_order_relaxed);
-  }
+    return cudaOccupancyMaxActiveClusters(n, distill_stream_kernel<T, CE, GRAD, ALIGNED>, &cfg);
+  }, &clusters);
+  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>((rows < clusters ? rows : clusters) * ctas));
   return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE, GRAD, ALIGNED>, z, dz, a, rows, ctas, per);
 }

@@ -66,4 +66,29 @@ int once_per_device(std::atomic<unsigned long long>& done, F&& f) {
   return rc;
 }
 
+// Counts that the driver answers (above 0), by device and a small key, each asked
+// for once.  A query that fails is not remembered, nor are the answers of devices >= 64.
+template <int KEYS>
+class PerDevice {
+ public:
+  template <typename F>  // cudaError_t(int*)
+  cudaError_t get(int key, F&& ask, int* out) {
+    int dev = 0;
+    std::atomic<int>* at =
+        cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? &kept_[dev][key] : nullptr;
+    int n = at ? at->load(std::memory_order_relaxed) : 0;
+    if (n < 1) {
+      const cudaError_t e = ask(&n);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidValue;
+      if (at) at->store(n, std::memory_order_relaxed);
+    }
+    *out = n;
+    return cudaSuccess;
+  }
+
+ private:
+  std::atomic<int> kept_[64][KEYS] = {};
+};
+
 }  // namespace gp
