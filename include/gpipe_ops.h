@@ -211,7 +211,7 @@ int gpipe_op_cross_entropy_clip(int rows, int vocab, int seq, const int32_t* tok
  *                + ce_scale (-log q_1[target])
  *   dz           = kd_scale T (q_T - sum_k p_k onehot(i_k))
  *                + ce_scale (q_1 - onehot(target))
- * (T = temperature > 0; 1 / T and kd_scale T^2 finite).  The target of row r is that of
+ * (T = temperature >= 2^-126; kd_scale T^2 finite).  The target of row r is that of
  * gpipe_op_cross_entropy: tokens[row0 + r + 1] unless (row0 + r) % seq ==
  * seq - 1; tokens is not read when ce_scale = 0 and may then be NULL.  A row
  * whose slots are all empty (or whose filled teacher logits are all -inf) has

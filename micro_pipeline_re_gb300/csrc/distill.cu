@@ -17,6 +17,7 @@
 // and their elements are written again; slots that name the same token are
 // added by the first of them, in slot order, so that nothing depends on timing.
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "../../include/gpipe.h"
@@ -1083,8 +1084,10 @@ int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t l
   if (!(temperature > 0.f) || !(temperature < INFINITY) || !(kd_scale >= 0.f) || !(kd_scale < INFINITY) ||
       !(ce_scale >= 0.f) || !(ce_scale < INFINITY))
     return set_error(GPIPE_ERR_INVALID_ARG, "distill: need a finite temperature > 0 and finite scales >= 0");
-  if (!(1.f / temperature < INFINITY) || !(kd_scale * temperature * temperature < INFINITY))
-    return set_error(GPIPE_ERR_INVALID_ARG, "distill: 1 / temperature and kd_scale temperature^2 must be finite in fp32");
+  // (from 2^-126 on log2(e) / T, the kernels' factor, is finite too)
+  if (temperature < FLT_MIN || !(kd_scale * temperature * temperature < INFINITY))
+    return set_error(GPIPE_ERR_INVALID_ARG,
+                     "distill: the temperature must be at least 2^-126 and kd_scale temperature^2 finite in fp32");
   if (!logits || !top_idx || !top_logit || !loss_rows)
     return set_error(GPIPE_ERR_INVALID_ARG, "distill: NULL logits, top_idx, top_logit or loss_rows");
   if (ce_scale > 0.f && (!tokens || seq < 1 || row0 < 0))

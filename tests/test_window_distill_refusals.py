@@ -109,3 +109,16 @@ def test_distill_refusals(b, bad, words):
 def test_distill_refuses_other_types(b):
     rc, said = distill(b, dtype=2)
     assert rc == -6 and "dtype must be 0 or 1" in said
+
+
+@pytest.mark.parametrize("t", [1e-40, 2.0 ** -128, 3.5e-39, 4.2e-39, 1e-38])
+def test_distill_refuses_temperatures_below_the_normal_range(b, t):
+    """1 / T is finite from 2^-128 on, log2(e) / T only from 4.24e-39, and a number
+    below 2^-126 has fewer bits than the others."""
+    rc, said = distill(b, t=t)
+    assert rc == -1 and "temperature" in said and "overlap" not in said
+
+
+def test_distill_takes_the_smallest_normal_temperature(b):
+    rc, said = distill(b, t=2.0 ** -126)
+    assert rc == -1 and "overlap" in said
