@@ -152,7 +152,7 @@ int gpipe_op_attention_bwd(int nseq, int seq, int heads, const void* qkv, const 
  *             (gpipe_op_position_bucket_starts); 2 <= num_buckets <= 64,
  *             num_buckets / 2 < max_distance <= 4096.
  * Any seq >= 1; nseq * seq <= 2^30.  Cost grows with the visible pairs.  Outputs
- * that overlap each other or qkv are rejected. */
+ * that overlap each other or an input are rejected. */
 int gpipe_op_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
                                   const int32_t* lens, const float* table, int num_buckets,
                                   int max_distance, const void* qkv, void* o, float* lse, void* stream);
@@ -162,8 +162,10 @@ int gpipe_op_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, in
  * += sum of dS over the pairs of each bucket.  o and lse are the forward's, with
  * the same lens and table.  scratch: gpipe_op_attention_window_scratch_bytes,
  * 256-byte aligned, written before it is read (calls that may overlap on the
- * GPU, captured ones included, need one each).  dqkv and scratch may overlap
- * neither the inputs nor each other.  No atomics: results are bit-reproducible. */
+ * GPU, captured ones included, need one each, and a dtable_acc each: it is read,
+ * added to and written back).  dqkv, dtable_acc and scratch may overlap neither
+ * each other nor the inputs (but dtable_acc the table: the gradient is then added
+ * to it).  No atomics: results are bit-reproducible. */
 int gpipe_op_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
                                   const int32_t* lens, const float* table, int num_buckets,
                                   int max_distance, const void* qkv, const void* o, const void* dout,
@@ -221,8 +223,8 @@ int gpipe_op_cross_entropy_clip(int rows, int vocab, int seq, const int32_t* tok
  * set the device error flag.
  * dz is bf16 [rows, vocab] with leading dimension lddz, or NULL for the loss
  * alone.  It may be the logits themselves (same address, and the same row
- * stride in bytes: lddz = ld for bf16, 2 ld for fp32); any other overlap is
- * rejected.  Elements of a row behind the vocab-th are neither read nor written.
+ * stride in bytes: lddz = ld for bf16, 2 ld for fp32); any other overlap of dz
+ * or loss_rows with an input or each other is rejected.  Elements of a row behind the vocab-th are neither read nor written.
  * 1 <= topk <= 256, 1 <= rows <= 2^27, 1 <= vocab <= 2^30 (any; rows that start on
  * 16-byte boundaries take wide loads).  No atomics: results are bit-reproducible. */
 int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t ld, int topk,

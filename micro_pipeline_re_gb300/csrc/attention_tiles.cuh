@@ -13,6 +13,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "common.cuh"
 
@@ -121,6 +122,20 @@ inline EncodeFn encode_fn() {
 }
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A tensor's bytes, for the checks of outputs against the other tensors of a call.
+struct Range {
+  const void* at;
+  size_t bytes;  // 0 where the call has no such tensor
+};
+inline bool overlaps(Range out, std::initializer_list<Range> others) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out.at);
+  for (const Range& r : others) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(r.at);
+    if (out.bytes && r.bytes && a < b + r.bytes && b < a + out.bytes) return true;
+  }
+  return false;
+}
 
 }  // namespace attn
 }  // namespace gp

@@ -57,7 +57,6 @@
 
 #include <atomic>
 #include <cmath>
-#include <initializer_list>
 #include <type_traits>
 
 #include "../../include/gpipe.h"
@@ -1804,26 +1803,16 @@ int prepare_attention_window() {
   });
 }
 
-struct Range {
-  const void* at;
-  size_t bytes;
-};
 // The sizes of one call's tensors.
 struct Sizes {
-  size_t qkv, o, lse;
-  Sizes(const WindowArgs& a)
+  size_t qkv, o, lse, table, lens;
+  Sizes(const WindowArgs& a, int buckets)
       : qkv(static_cast<size_t>(a.nseq) * a.seq * (a.heads + 2 * a.kv_heads) * HD * 2),
         o(static_cast<size_t>(a.nseq) * a.seq * a.heads * HD * 2),
-        lse(static_cast<size_t>(a.nseq) * a.seq * a.heads * 4) {}
+        lse(static_cast<size_t>(a.nseq) * a.seq * a.heads * 4),
+        table(static_cast<size_t>(buckets) * a.heads * 4),
+        lens(a.lens ? static_cast<size_t>(a.nseq) * 4 : 0) {}
 };
-bool overlaps(Range out, std::initializer_list<Range> others) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(out.at);
-  for (const Range& r : others) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(r.at);
-    if (a < b + r.bytes && b < a + out.bytes) return true;
-  }
-  return false;
-}
 
 int check_launch(const char* what) {
   count_launch();
@@ -1857,9 +1846,11 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
   if (rc) return rc;
   if (!qkv || !o || !lse || !al16(qkv) || !al16(o))
     return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_fwd: qkv and o must be 16-B aligned, lse not NULL");
-  const Sizes size(a);
-  if (overlaps({o, size.o}, {{qkv, size.qkv}, {lse, size.lse}}) || overlaps({lse, size.lse}, {{qkv, size.qkv}}))
-    return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_fwd: o and lse may not overlap each other or qkv");
+  const Sizes size(a, buckets);
+  const Range out[] = {{o, size.o}, {lse, size.lse}};
+  for (const Range& r : out)
+    if (overlaps(r, {{qkv, size.qkv}, {table, size.table}, {lens, size.lens}}) || overlaps(out[0], {out[1]}))
+      return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_fwd: o and lse may not overlap each other or the inputs");
   rc = prepare_attention_window();
   if (rc) return rc;
   int* err = device_error_ptr();
@@ -1890,13 +1881,16 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   if (dtable_acc && !table)
     return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: a table gradient needs the table");
   const WindowScratch w = window_scratch(scratch, nseq, seq, heads, window, sinks, dtable_acc ? a.ranks : 0);
-  const Sizes size(a);
-  const Range read[] = {{qkv, size.qkv}, {o, size.o}, {dout, size.o}, {lse, size.lse}};
+  const Sizes size(a, buckets);
+  const Range dx = {dqkv, size.qkv}, tmp = {scratch, w.bytes}, dt = {dtable_acc, dtable_acc ? size.table : 0};
+  const Range read[] = {{qkv, size.qkv}, {o, size.o}, {dout, size.o}, {lse, size.lse}, {lens, size.lens}};
   for (const Range& r : read)
-    if (overlaps(r, {{dqkv, size.qkv}, {scratch, w.bytes}}))
-      return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: dqkv and scratch may not overlap the inputs");
-  if (overlaps({dqkv, size.qkv}, {{scratch, w.bytes}}))
-    return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: dqkv and scratch may not overlap");
+    if (overlaps(r, {dx, tmp, dt}))
+      return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: dqkv, dtable_acc and scratch may not overlap the inputs");
+  // (the table itself may take its gradient: it is added when nothing reads the table any more)
+  if (overlaps(dx, {tmp, dt, {table, size.table}}) || overlaps(tmp, {dt, {table, size.table}}))
+    return set_error(GPIPE_ERR_INVALID_ARG,
+                     "attention_window_bwd: dqkv, dtable_acc and scratch may not overlap each other or the inputs");
   rc = prepare_attention_window();
   if (rc) return rc;
   int* err = device_error_ptr();

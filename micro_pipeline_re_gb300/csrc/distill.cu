@@ -1095,17 +1095,21 @@ int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t l
   const size_t es = dtype == DT_F32 ? 4 : 2;
   if ((reinterpret_cast<uintptr_t>(logits) % es) || (reinterpret_cast<uintptr_t>(dz) % 2))
     return set_error(GPIPE_ERR_INVALID_ARG, "distill: logits and dz must be aligned to their elements");
-  bool in_place = false;
-  if (dz) {
-    if (lddz < vocab) return set_error(GPIPE_ERR_INVALID_ARG, "distill: lddz must be at least vocab");
-    const uintptr_t zb = reinterpret_cast<uintptr_t>(logits), db = reinterpret_cast<uintptr_t>(dz);
-    const uintptr_t ze = zb + (static_cast<uintptr_t>(rows - 1) * ld + vocab) * es;
-    const uintptr_t de = db + (static_cast<uintptr_t>(rows - 1) * lddz + vocab) * 2;
-    in_place = zb < de && db < ze;
-    if (in_place && !(zb == db && (rows == 1 || lddz * 2 == ld * static_cast<int64_t>(es))))
-      return set_error(GPIPE_ERR_INVALID_ARG,
-                       "distill: dz overlaps the logits, which needs the same address and the same row stride in bytes");
-  }
+  if (dz && lddz < vocab) return set_error(GPIPE_ERR_INVALID_ARG, "distill: lddz must be at least vocab");
+  using attn::overlaps;
+  using attn::Range;
+  const size_t nr = static_cast<size_t>(rows);
+  const Range in = {logits, ((nr - 1) * ld + vocab) * es}, out = {dz, dz ? ((nr - 1) * lddz + vocab) * 2 : 0};
+  const bool in_place = overlaps(out, {in});
+  if (in_place && !(dz == logits && (rows == 1 || lddz * 2 == ld * static_cast<int64_t>(es))))
+    return set_error(GPIPE_ERR_INVALID_ARG,
+                     "distill: dz overlaps the logits, which needs the same address and the same row stride in bytes");
+  // the tokens that are read: the last row's only if it has a target
+  Range labels = {nullptr, 0};
+  if (ce_scale > 0.f) labels = {tokens + row0 + 1, (nr - ((static_cast<int64_t>(row0) + rows) % seq == 0)) * 4};
+  const Range idx = {top_idx, nr * topk * 4}, val = {top_logit, nr * topk * 4}, loss = {loss_rows, nr * 4};
+  if (overlaps(loss, {in, out, idx, val, labels}) || overlaps(out, {idx, val, labels}))
+    return set_error(GPIPE_ERR_INVALID_ARG, "distill: loss_rows and dz may not overlap each other or the other inputs");
   DistillArgs a;
   a.vocab = vocab;
   a.topk = topk;

@@ -122,3 +122,57 @@ def test_distill_refuses_temperatures_below_the_normal_range(b, t):
 def test_distill_takes_the_smallest_normal_temperature(b):
     rc, said = distill(b, t=2.0 ** -126)
     assert rc == -1 and "overlap" in said
+
+
+# tensors that do not touch each other: 2 x 64 rows of 512 (qkv, dqkv) or 256 (o, dout) columns, bf16; 8 buckets x 4 heads
+M = 1 << 20
+APART = dict(qkv=M, o=2 * M, dout=3 * M, lse=4 * M, dqkv=5 * M, scratch=6 * M, table=8 * M, lens=9 * M, dtable=10 * M)
+BYTES = dict(qkv=128 * 1024, o=128 * 512, dout=128 * 512, lse=128 * 16, dqkv=128 * 1024, table=128, lens=8, dtable=128)
+
+
+def onto(what, other, apart, sizes):
+    """`what` onto the first bytes of `other`, and onto its last 16 (or as many as it has)."""
+    yield {what: apart[other]}
+    yield {what: apart[other] + max(0, sizes[other] - 256) // 256 * 256}
+
+
+@pytest.mark.parametrize("out", ["o", "lse"])
+@pytest.mark.parametrize("other", ["qkv", "table", "lens", "o", "lse"])
+def test_attention_forward_outputs_overlap_nothing(b, out, other):
+    if out == other:
+        return
+    for bad in onto(out, other, APART, BYTES):
+        rc, said = attention(b, False, **dict(APART, **bad))
+        assert rc == -1 and "overlap" in said, bad
+
+
+@pytest.mark.parametrize("out", ["dqkv", "dtable", "scratch"])
+@pytest.mark.parametrize("other", ["qkv", "o", "dout", "lse", "table", "lens", "dqkv", "dtable", "scratch"])
+def test_attention_backward_outputs_overlap_nothing(b, out, other):
+    if out == other or (out, other) == ("dtable", "table"):  # the table may take its own gradient
+        return
+    sizes = dict(BYTES, scratch=b.lib().gpipe_op_attention_window_scratch_bytes(2, 64, 4, 16, 4, 8))
+    for bad in onto(out, other, APART, sizes):
+        rc, said = attention(b, True, **dict(APART, **bad))
+        assert rc == -1 and "overlap" in said, bad
+
+
+# 4 rows of 32 fp32 logits, 4 slots, bf16 dz
+DAPART = dict(logits=M, idx=2 * M, val=3 * M, tokens=4 * M, loss=5 * M, dz=6 * M)
+DBYTES = dict(logits=512, idx=64, val=64, tokens=16, loss=16, dz=256)  # (the last row has no target)
+
+
+@pytest.mark.parametrize("out", ["loss", "dz"])
+@pytest.mark.parametrize("other", ["logits", "idx", "val", "tokens", "loss", "dz"])
+def test_distill_outputs_overlap_nothing(b, out, other):
+    if out == other:
+        return
+    for at in (DAPART[other] + (4 if other == "tokens" else 0), DAPART[other] + DBYTES[other] - 4):
+        rc, said = distill(b, **dict(DAPART, **{out: at}))
+        assert rc == -1 and "overlap" in said, at
+
+
+@pytest.mark.parametrize("dz,lddz", [(M, 32), (M + 64, 64), (M - 64, 64)])
+def test_distill_in_place_takes_the_same_rows(b, dz, lddz):
+    rc, said = distill(b, **dict(DAPART, dz=dz, lddz=lddz))
+    assert rc == -1 and "same address and the same row stride" in said
