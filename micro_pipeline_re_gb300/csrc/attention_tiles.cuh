@@ -122,6 +122,7 @@ inline EncodeFn encode_fn() {
 }
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A tensor's bytes, for the checks of outputs against the other tensors of a call.
 struct Range {

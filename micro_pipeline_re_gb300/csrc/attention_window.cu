@@ -1846,6 +1846,8 @@ int launch_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, int 
   if (rc) return rc;
   if (!qkv || !o || !lse || !al16(qkv) || !al16(o))
     return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_fwd: qkv and o must be 16-B aligned, lse not NULL");
+  if (!al4(lse) || !al4(lens) || !al4(table))
+    return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_fwd: lse, lens and table must be aligned to their elements");
   const Sizes size(a, buckets);
   const Range out[] = {{o, size.o}, {lse, size.lse}};
   for (const Range& r : out)
@@ -1876,6 +1878,9 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
   if (!qkv || !o || !dout || !lse || !dqkv || !al16(qkv) || !al16(o) || !al16(dout) || !al16(dqkv))
     return set_error(GPIPE_ERR_INVALID_ARG,
                      "attention_window_bwd: qkv, o, dout and dqkv must be 16-B aligned, lse not NULL");
+  if (!al4(lse) || !al4(lens) || !al4(table) || !al4(dtable_acc))
+    return set_error(GPIPE_ERR_INVALID_ARG,
+                     "attention_window_bwd: lse, lens, table and dtable_acc must be aligned to their elements");
   if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u))
     return set_error(GPIPE_ERR_INVALID_ARG, "attention_window_bwd: scratch must be 256-B aligned");
   if (dtable_acc && !table)

@@ -1093,8 +1093,9 @@ int launch_distill(int dtype, int rows, int vocab, const void* logits, int64_t l
   if (ce_scale > 0.f && (!tokens || seq < 1 || row0 < 0))
     return set_error(GPIPE_ERR_INVALID_ARG, "distill: ce_scale > 0 needs tokens, seq >= 1 and row0 >= 0");
   const size_t es = dtype == DT_F32 ? 4 : 2;
-  if ((reinterpret_cast<uintptr_t>(logits) % es) || (reinterpret_cast<uintptr_t>(dz) % 2))
-    return set_error(GPIPE_ERR_INVALID_ARG, "distill: logits and dz must be aligned to their elements");
+  if ((reinterpret_cast<uintptr_t>(logits) % es) || (reinterpret_cast<uintptr_t>(dz) % 2) || !attn::al4(top_idx) ||
+      !attn::al4(top_logit) || !attn::al4(loss_rows) || (ce_scale > 0.f && !attn::al4(tokens)))
+    return set_error(GPIPE_ERR_INVALID_ARG, "distill: tensors must be aligned to their elements");
   if (dz && lddz < vocab) return set_error(GPIPE_ERR_INVALID_ARG, "distill: lddz must be at least vocab");
   using attn::overlaps;
   using attn::Range;

@@ -176,3 +176,21 @@ def test_distill_outputs_overlap_nothing(b, out, other):
 def test_distill_in_place_takes_the_same_rows(b, dz, lddz):
     rc, said = distill(b, **dict(DAPART, dz=dz, lddz=lddz))
     assert rc == -1 and "same address and the same row stride" in said
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("name", ["lse", "lens", "table"])
+def test_attention_words_are_aligned(b, backward, name):
+    rc, said = attention(b, backward, **{name: A + 2})
+    assert rc == -1 and "aligned to their elements" in said
+
+
+def test_attention_table_gradient_is_aligned(b):
+    rc, said = attention(b, True, dtable=A + 2)
+    assert rc == -1 and "aligned to their elements" in said
+
+
+@pytest.mark.parametrize("name", ["idx", "val", "tokens", "loss"])
+def test_distill_words_are_aligned(b, name):
+    rc, said = distill(b, **{name: A + 2})
+    assert rc == -1 and "aligned to their elements" in said
