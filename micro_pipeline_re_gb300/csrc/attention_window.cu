@@ -114,6 +114,9 @@ __device__ __forceinline__ int seq_len(const WindowArgs& a, int b) {
 //             (256 x 96 + 128 x 48 = 384 x 80).
 constexpr int FWD_ROWS = 128, BWD_ROWS = 256;
 constexpr int FWD_THREADS = FWD_ROWS + 128, BWD_THREADS = BWD_ROWS + 128;
+constexpr int FWD_REGS = 128, BWD_REGS = 80;  // a thread at launch
+static_assert(FWD_ROWS * 208 + 128 * 48 == FWD_THREADS * FWD_REGS && BWD_ROWS * 96 + 128 * 48 == BWD_THREADS * BWD_REGS,
+              "what the row threads take is what the others give");
 
 // The whole warp waits; the answer is the same in every lane.
 __device__ __forceinline__ bool warp_await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
@@ -1786,9 +1789,6 @@ static_assert(dq_smem(2, Bias::bytes(kMaxDistance, kMaxDistance), dq_sums(kMaxBu
 int prepare_attention_window() {
   static std::atomic<unsigned long long> done{0};
   return once_per_device(done, []() -> int {
-    auto set = [](const void* f) {
-      return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    };
     const void* all[] = {reinterpret_cast<const void*>(attn_window_fwd_kernel<false>),
                          reinterpret_cast<const void*>(attn_window_fwd_kernel<true>),
                          reinterpret_cast<const void*>(attn_window_bwd_kernel<0, false>),
@@ -1796,8 +1796,15 @@ int prepare_attention_window() {
                          reinterpret_cast<const void*>(attn_window_bwd_kernel<1, true>),
                          reinterpret_cast<const void*>(attn_window_bwd_kernel<2, false>),
                          reinterpret_cast<const void*>(attn_window_bwd_kernel<2, true>)};
-    for (const void* f : all)
-      if (set(f) != cudaSuccess) return set_error(GPIPE_ERR_CUDA, "attention_window: shared-memory attribute failed");
+    for (const void* f : all) {
+      if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
+        return set_error(GPIPE_ERR_CUDA, "attention_window: shared-memory attribute failed");
+      // a block that is launched with fewer registers than its warps pass on would wait for them for ever
+      cudaFuncAttributes at;
+      const bool fwd = f == all[0] || f == all[1];
+      if (cudaFuncGetAttributes(&at, f) != cudaSuccess || at.numRegs < (fwd ? FWD_REGS : BWD_REGS))
+        return set_error(GPIPE_ERR_CUDA, "attention_window: built with fewer registers than its warps share out");
+    }
     if (!encode_fn()) return set_error(GPIPE_ERR_CUDA, "attention_window: cuTensorMapEncodeTiled entry point not found");
     return static_cast<int>(GPIPE_OK);
   });
