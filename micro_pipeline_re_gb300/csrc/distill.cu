@@ -338,10 +338,10 @@ __global__ void __launch_bounds__(TH) distill_row_kernel(const T* logits, __nv_b
 //                sums are known, its loss and, once pass B is done, the elements of
 //                its top tokens.
 //
-// Bound by memory where the label term is off (4096 x 131072 bf16: 381 us, 5.6
+// Bound by memory where the label term is off (4096 x 131072 bf16: 372 us, 5.8
 // TB/s); with it, four exponentials and some 14 instructions an element share the
-// bound with it (2048 x 32000 fp32: 76 us, 5.2 TB/s, an SM's quarters issuing in
-// 64 % of the cycles; 4096 x 131072 bf16: 492 us).  Part of the label's
+// bound with it (2048 x 32000 fp32: 77 us, 5.2 TB/s, an SM's quarters issuing in
+// 64 % of the cycles; 4096 x 131072 bf16: 474 us).  Part of the label's
 // exponentials as polynomials, for the exponentials' unit's sake, made 511 us of 473
 // (a quarter of them) and 667 us (all).  One CTA of 512 pass threads was as fast
 // as two of half the ring, and 64 teacher threads a group leave the pass warps the
@@ -399,16 +399,20 @@ struct Slots {
 // GRAD: the loss alone, or with dz by wide stores, or, where a row of dz is not aligned
 // for them when its logits are, by single ones (2048 x 32001 logits in rows of 32008, dz
 // in rows of 32001, bf16: 91 us; 82 where both are alike, 150 with rows read twice).
-// ALIGNED: every row of logits starts on a 16-byte boundary, so that a CTA's part is the
-// same of all rows (4096 x 131072 bf16 381 us, 386 with a part made row by row).
+// ROWS: any, or those that all start on a 16-byte boundary, so that a CTA's part is the
+// same of all rows and made once, or those that also end on one, so that nothing is read
+// beside the copies.  4096 x 131072 bf16 372 us, 381 as rows that may end anywhere; with
+// labels 474, 492 with a part made row by row.
 enum Grad { kLoss, kWide, kSingle };
-template <typename T, bool CE, Grad GRAD, bool ALIGNED>
+enum Rows { kAny, kAligned, kWhole };
+template <typename T, bool CE, Grad GRAD, Rows ROWS>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     distill_stream_kernel(const T* logits, __nv_bfloat16* dz, const __grid_constant__ DistillArgs a, int rows, int ctas,
                           int per) {
   extern __shared__ __align__(128) uint8_t ring[];
   StreamShared& sh = *reinterpret_cast<StreamShared*>(ring + kChunks * kChunk);
   volatile int* abort = &sh.abort;
+  constexpr bool ALIGNED = ROWS != kAny, EDGES = ROWS != kWhole;
   constexpr int E = 16 / static_cast<int>(sizeof(T)), kPer = kChunk / static_cast<int>(sizeof(T));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % ctas, clusters = gridDim.x / ctas;
@@ -430,6 +434,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     return p;
   };
   const int row0 = blockIdx.x / ctas;
+  const Part fixed = part_of(0);  // of every row, where ALIGNED
   const float c1 = kLog2e, ct = kLog2e * a.inv_t;
 
   if (tid == 0) {
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       int64_t count = 0;
       bool go = true;
       for (int r = row0; r < rows && go; r += clusters) {
-        const Part p = part_of(r);
+        const Part p = ALIGNED ? fixed : part_of(r);
         const uint8_t* src = reinterpret_cast<const uint8_t*>(logits + static_cast<int64_t>(r) * a.ld + p.from);
         for (int c = 0; c < p.chunks; ++c) {
           if (count >= kChunks && !lane_await(&sh.empty[slot], parity, a.err, DERR_TMA_WAIT, abort)) {
@@ -619,7 +624,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (g1 != 0.f) g += ex2_approx(x * c1) * g1;
         return f2bf(is_target ? g - a.ce : g);
       };
-      const Part part = part_of(r);
+      const Part part = ALIGNED ? fixed : part_of(r);
 #pragma unroll
       for (int k = 0; k < kSlots; ++k)
         if (s.me[k] >= part.lo && s.me[k] < part.hi) out[s.me[k]] = value(s.z[k] - m, s.sum[k], s.me[k] == s.target);
@@ -657,21 +662,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     for (int r = row0; r < rows; r += clusters, ++i) {
       const int b = i & 1;
       const uint32_t turn = (i >> 1) & 1;
-      const Part p = part_of(r);
+      const Part p = ALIGNED ? fixed : part_of(r);
       const int whole = p.whole, chunks = p.chunks;
       // the first and the last few elements, one a thread, kept for pass B (dz may lie over them by then)
       auto edge_of = [&] {
+        if (!EDGES) return -1;
         if (ALIGNED) return p.from + whole + tid < p.hi ? p.from + whole + tid : -1;
         const int at = tid < 16 ? tid : p.from + whole + tid - 16;
         return tid < 32 && at >= p.lo && at < (tid < 16 ? p.from : p.hi) ? at : -1;
       };
       float edge = -INFINITY;
       const int at_edge = edge_of();
-      if (at_edge >= 0) edge = Elem<T>::ld(logits + static_cast<int64_t>(r) * a.ld + at_edge);
+      if (EDGES && at_edge >= 0) edge = Elem<T>::ld(logits + static_cast<int64_t>(r) * a.ld + at_edge);
       // pass A: running maximum (one check a chunk) and the sums
       float m = edge;
       f32x2 s12 = 0ull, st2 = 0ull;
-      if (at_edge >= 0) s12 = st2 = pack2(edge == -INFINITY ? 0.f : ex2_approx(edge - edge), 0.f);  // 1 (NaN stays NaN)
+      if (EDGES && at_edge >= 0) s12 = st2 = pack2(edge == -INFINITY ? 0.f : ex2_approx(edge - edge), 0.f);  // 1 (NaN stays NaN)
       int sl = slot;
       uint32_t pa = parity;
       for (int c = 0; c < chunks; ++c) {
@@ -822,7 +828,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             parity ^= 1u;
           }
         }
-        if (at_edge >= 0) {
+        if (EDGES && at_edge >= 0) {
           float g, other;
           unpack2(grad2(add2(pack2(edge, edge), m2)), g, other);
           out[at_edge - p.from] = f2bf(g);
@@ -983,12 +989,12 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const T* logit
   if (tid == 0 && target >= 0) fix_up(a, idx, pk, a.topk, target, sh_z - m, target, gt, g1, out);
 }
 
-template <typename T, bool CE, Grad GRAD, bool ALIGNED>
+template <typename T, bool CE, Grad GRAD, Rows ROWS>
 cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, int ctas, int per,
                           cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   const int rc = once_per_device(done, [] {
-    return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE, GRAD, ALIGNED>,
+    return static_cast<int>(cudaFuncSetAttribute(distill_stream_kernel<T, CE, GRAD, ROWS>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem));
   });
   if (rc) return static_cast<cudaError_t>(rc);
@@ -1009,24 +1015,25 @@ cudaError_t launch_stream(const T* z, __nv_bfloat16* dz, const DistillArgs& a, i
   int clusters = 0;
   const cudaError_t e = at_once.get(ctas, [&](int* n) {
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / ctas * ctas));
-    return cudaOccupancyMaxActiveClusters(n, distill_stream_kernel<T, CE, GRAD, ALIGNED>, &cfg);
+    return cudaOccupancyMaxActiveClusters(n, distill_stream_kernel<T, CE, GRAD, ROWS>, &cfg);
   }, &clusters);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>((rows < clusters ? rows : clusters) * ctas));
-  return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE, GRAD, ALIGNED>, z, dz, a, rows, ctas, per);
+  return cudaLaunchKernelEx(&cfg, distill_stream_kernel<T, CE, GRAD, ROWS>, z, dz, a, rows, ctas, per);
 }
 
-template <typename T, Grad GRAD>
+template <typename T, Grad GRAD, Rows ROWS>
 cudaError_t launch_stream_ce(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, int ctas, int per,
-                             bool aligned, cudaStream_t s) {
-  const bool ce = a.ce > 0.f;
-  if constexpr (GRAD != kSingle) {
-    if (aligned)
-      return ce ? launch_stream<T, true, GRAD, true>(z, dz, a, rows, ctas, per, s)
-                : launch_stream<T, false, GRAD, true>(z, dz, a, rows, ctas, per, s);
-  }
-  return ce ? launch_stream<T, true, GRAD, false>(z, dz, a, rows, ctas, per, s)
-            : launch_stream<T, false, GRAD, false>(z, dz, a, rows, ctas, per, s);
+                             cudaStream_t s) {
+  return a.ce > 0.f ? launch_stream<T, true, GRAD, ROWS>(z, dz, a, rows, ctas, per, s)
+                    : launch_stream<T, false, GRAD, ROWS>(z, dz, a, rows, ctas, per, s);
+}
+template <typename T, Grad GRAD>
+cudaError_t launch_stream_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, int ctas, int per,
+                               bool aligned, cudaStream_t s) {
+  if (!aligned) return launch_stream_ce<T, GRAD, kAny>(z, dz, a, rows, ctas, per, s);
+  if (a.vocab * sizeof(T) % 16) return launch_stream_ce<T, GRAD, kAligned>(z, dz, a, rows, ctas, per, s);
+  return launch_stream_ce<T, GRAD, kWhole>(z, dz, a, rows, ctas, per, s);
 }
 
 // Clusters of `ctas` for slices of at most `most` elements; with rows for less than
@@ -1067,9 +1074,9 @@ cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int
   if (most * ctas < a.vocab || (!VEC && a.vocab * sizeof(T) <= kShortBytes))
     return launch_k(distill_kernel<T, VEC>, rows, kDistillThreads, 0, s, z, dz, a);
   const int per = ((a.vocab + ctas - 1) / ctas + 7) & ~7;
-  if (!dz) return launch_stream_ce<T, kLoss>(z, dz, a, rows, ctas, per, aligned, s);
-  if (wide) return launch_stream_ce<T, kWide>(z, dz, a, rows, ctas, per, aligned, s);
-  return launch_stream_ce<T, kSingle>(z, dz, a, rows, ctas, per, false, s);
+  if (!dz) return launch_stream_rows<T, kLoss>(z, dz, a, rows, ctas, per, aligned, s);
+  if (wide) return launch_stream_rows<T, kWide>(z, dz, a, rows, ctas, per, aligned, s);
+  return launch_stream_ce<T, kSingle, kAny>(z, dz, a, rows, ctas, per, s);
 }
 
 }  // namespace
