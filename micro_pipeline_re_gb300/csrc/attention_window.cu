@@ -888,11 +888,13 @@ constexpr int dkv_smem(int stages, int bias_bytes) {
 // what is there.  Beyond the narrow buckets a row meets at most two, and adds each
 // column to one of two sums: 2 x 4096 tokens, 16 heads, 32 buckets up to 4096 take
 // 322 us instead of 353 (backward), 64 of them 541 instead of 594.  P's sums only weigh the error of D, which is some 2^-9 of dS:
-// fp16 is more than they need.
+// fp16 is enough for them, as 2^14 P, which keeps its 11 bits down to sums of 2^-28 (a bucket that sums to
+// less in a row keeps some of that row's error of D, 2^-9 of a gradient of that size).
 //
 // Bound by the row threads' instructions: some 2000 cycles a tile with the
 // other CTA's work beside it, 4400 where the buckets change from column to
 // column.  Figures of the whole backward pass are at its kernel.
+constexpr float kSumP = 16384.f;
 template <int MODE, bool WIDE>
 __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
                               const CUtensorMap* td128, const CUtensorMap* tg, const WindowScratch& ws_,
@@ -1186,7 +1188,7 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
             farS += x0 + x1;
             farP += y0 + y1;
           } else {
-            put(rank, x0 + x1, y0 + y1);
+            put(rank, x0 + x1, kSumP * (y0 + y1));
           }
         } else if (two()) {
           const int first = last_of_first(), other = bias.rank_of(d - 31);
@@ -1195,10 +1197,10 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
           for (int i = 0; i < 32; ++i) {
             if (i <= first) {
               s0 += v[32 + i];
-              p0 += v[i];
+              p0 = fmaf(v[i], kSumP, p0);
             } else {
               s1 += v[32 + i];
-              p1 += v[i];
+              p1 = fmaf(v[i], kSumP, p1);
             }
           }
           put(rank, s0, p0);
@@ -1218,7 +1220,7 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             runS += v[32 + i];
-            runP += v[i];
+            runP = fmaf(v[i], kSumP, runP);
             const uint32_t ends_here = stop & (1u << i);
             store_if(ends_here, atS, runS, atP, runP);
             runS = ends_here ? 0.f : runS;
@@ -1260,13 +1262,13 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
       for (int t = 0; t < nt; ++t) tile(std::false_type(), 0.f, t);
     }
     if (MODE == 2) {
-      put(a.ranks - 1, farS, farP);
+      put(a.ranks - 1, farS, kSumP * farP);
       row_e[tid] = rowS;
       rows_barrier<BWD_ROWS>();
       // the error of D: a row's dS sum to it instead of 0 (a padded row's sums are 0 themselves)
       float e[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) e[c] = row_e[32 * c + ln] + row_e[32 * c + ln + 128];
+      for (int c = 0; c < 4; ++c) e[c] = (row_e[32 * c + ln] + row_e[32 * c + ln + 128]) * (1.f / kSumP);
       for (int k = warp; k < a.ranks; k += BWD_ISSUER) {
         float x = 0.f;
 #pragma unroll
