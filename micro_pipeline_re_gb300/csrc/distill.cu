@@ -91,12 +91,15 @@ __device__ __forceinline__ bool teacher(const DistillArgs& a, float* tl, float* 
   tm = warp_max(tm);
   const float tb = tm == -INFINITY ? 0.f : tm;
   float ts = 0.f;
-  for (int k = lane; k < a.topk; k += 32) ts += expf((tl[k] - tb) * a.inv_t);
+  for (int k = lane; k < a.topk; k += 32) {
+    tl[k] = (tl[k] - tb) * a.inv_t;
+    ts += pk[k] = expf(tl[k]);
+  }
   ts = warp_sum(ts);
   const float log_ts = logf(ts);
   for (int k = lane; k < a.topk; k += 32) {
-    pk[k] = ts == 0.f ? 0.f : expf((tl[k] - tb) * a.inv_t) / ts;
-    tl[k] = (tl[k] - tb) * a.inv_t - log_ts;
+    pk[k] = ts == 0.f ? 0.f : pk[k] / ts;
+    tl[k] -= log_ts;
   }
   return ts != 0.f;
 }
