@@ -165,7 +165,9 @@ int gpipe_op_attention_window_fwd(int nseq, int seq, int heads, int kv_heads, in
  * GPU, captured ones included, need one each, and a dtable_acc each: it is read,
  * added to and written back).  dqkv, dtable_acc and scratch may overlap neither
  * each other nor the inputs (but dtable_acc the table: the gradient is then added
- * to it).  No atomics: results are bit-reproducible. */
+ * to it).  Query heads that share a key/value head follow each other in its dK and
+ * dV, so a large group over a short sequence takes longer than its pairs alone would.
+ * No atomics: results are bit-reproducible. */
 int gpipe_op_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int window, int sinks,
                                   const int32_t* lens, const float* table, int num_buckets,
                                   int max_distance, const void* qkv, const void* o, const void* dout,

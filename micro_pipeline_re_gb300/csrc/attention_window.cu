@@ -17,14 +17,16 @@
 // window has left the first block, one narrow block of the sinks' keys.  Work
 // is therefore proportional to the visible pairs and not to the square of the
 // length.  The products are tcgen05.mma with the accumulators in tensor memory;
-// thread r of the 128 row threads owns row r of every accumulator, and warp 4
-// issues every copy and every product.
+// the row threads own their rows (a whole one each in the forward kernel, half of
+// one in the backward kernel), warps of their own issue the products (one forward,
+// two backward) and another one the copies.
 //
 // Scores are kept in the log2 domain: t = s * log2(e) / 8 + bias * log2(e), so
-// that an exponential is one ex2.  The bias enters in one of two ways: a tile
-// whose distances all lie in the last bucket takes it as a constant; a tile
-// nearer to the diagonal reads it from a table by distance in shared memory,
-// in which the rows of a warp read consecutive words.
+// that an exponential is one ex2.  The bias enters a tile in one of three ways,
+// each warp's by itself: as a constant of the row where every row of the warp lies
+// within one bucket; as one of two constants where the buckets are wider than the
+// tile; else by distance, from a table in shared memory in which the rows of a
+// warp read consecutive words.  Heads with large entries take a fourth (kBigBias).
 //
 // The backward pass uses no atomics, so its results are bit-reproducible:
 //   prep    -lse log2(e) and -D of every (head, query), in rows for the dQ CTAs
@@ -692,7 +694,7 @@ struct PrepItem {
 // base.  lse has too few bits for the difference, so the row's sum is made again, by
 // eight threads, each 8 columns.  (Below kBigLse lse itself is accurate enough, whatever the base.)
 constexpr float kBigLse = 128.f;
-__device__ __noinline__ void take_out_base(const WindowArgs& a, const __nv_bfloat16* qkv, float2* ld, uint8_t* terms) {
+__device__ __forceinline__ void take_out_base(const WindowArgs& a, const __nv_bfloat16* qkv, float2* ld, uint8_t* terms) {
   const PrepItem at(a);
   const int64_t b = at.b;
   const int h = at.h, i = at.i, sub = threadIdx.x & 7;
@@ -709,18 +711,23 @@ __device__ __noinline__ void take_out_base(const WindowArgs& a, const __nv_bfloa
   const int64_t stride = static_cast<int64_t>(a.heads + 2 * a.kv_heads) * HD;
   const __nv_bfloat16* rows = qkv + b * a.seq * stride + 8 * sub;
   const __nv_bfloat16* keys = rows + (a.heads + h / (a.heads / a.kv_heads)) * HD;
-  float q[8];
-  load8(rows + i * stride + h * HD, q);
+  const uint4 q = *reinterpret_cast<const uint4*>(rows + i * stride + h * HD);
   // log2 sum_j 2^((s_ij - base) log2(e)) over the visible keys
   float m = -INFINITY, l = 0.f;
   int rank = a.ranks - 1;
   for (int x = 0; x < sinks + i - lo + 1; ++x) {
     const int j = x < sinks ? x : lo + x - sinks;
     while (a.first(rank) > i - j) --rank;  // (distances fall; the first bucket begins at 0)
-    float k[8], s = 0.f;
-    load8(keys + j * stride, k);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(q[e], k[e], s);
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + j * stride);
+    float s = 0.f;
+    auto two = [&](uint32_t x, uint32_t y) {
+      const float2 u = unpack_bf16x2(x), w = unpack_bf16x2(y);
+      s = fmaf(u.y, w.y, fmaf(u.x, w.x, s));
+    };
+    two(q.x, k.x);
+    two(q.y, k.y);
+    two(q.z, k.z);
+    two(q.w, k.w);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(eight, s, o);
     s = fmaf(s, kScaleLog2, (a.entry(rank, h) - base) * kLog2e);
@@ -737,8 +744,10 @@ __device__ __noinline__ void take_out_base(const WindowArgs& a, const __nv_bfloa
   if (sub == 1) *reinterpret_cast<uint4*>(to + 128) = make_uint4(1u, 0u, 0u, 0u);
 }
 
-// Bound by memory: reads o and dout, writes 136 bytes a (head, query), of which
-// 128 are the two operands.  8192 tokens, 16 heads: 10.4 us for 52 MB (5.0 TB/s).
+// Bound by memory and its latency: reads o and dout, writes 72 bytes a (head, query),
+// of which 64 are the two operands.  8192 tokens, 16 heads: 10.6 us for 43 MB (4.1
+// TB/s, 60 % of the copy bandwidth).
+template <bool TABLE>
 __global__ void __launch_bounds__(256, 8) attn_window_prep_kernel(const __grid_constant__ WindowArgs a,
                                                                   const __nv_bfloat16* __restrict__ qkv,
                                                                   const __nv_bfloat16* __restrict__ o,
@@ -774,7 +783,7 @@ __global__ void __launch_bounds__(256, 8) attn_window_prep_kernel(const __grid_c
     *reinterpret_cast<uint4*>(tile + (i >> 3 & 7) * 256 + (sub & 1) * 128 + (i & 7) * 16) =
         sub & 1 ? make_uint4(0u, 0u, 0u, 0u) : three_terms(x);
   }
-  if (a.ranks && fabsf(v) > kBigLse && v != -INFINITY) take_out_base(a, qkv, ld, terms);
+  if (TABLE && fabsf(v) > kBigLse && v != -INFINITY) take_out_base(a, qkv, ld, terms);
 }
 
 // Both kinds of CTA own 128 rows and walk 64-wide tiles; two CTAs share an SM,
@@ -887,9 +896,10 @@ constexpr int dkv_smem(int stages, int bias_bytes) {
 // nowhere else, so its sums are stored; only the first and the last are added to
 // what is there.  Beyond the narrow buckets a row meets at most two, and adds each
 // column to one of two sums: 2 x 4096 tokens, 16 heads, 32 buckets up to 4096 take
-// 322 us instead of 353 (backward), 64 of them 541 instead of 594.  P's sums only weigh the error of D, which is some 2^-9 of dS:
-// fp16 is enough for them, as 2^14 P, which keeps its 11 bits down to sums of 2^-28 (a bucket that sums to
-// less in a row keeps some of that row's error of D, 2^-9 of a gradient of that size).
+// 322 us instead of 353 (backward), 64 of them 541 instead of 594.  P's sums only
+// weigh the error of D, which is some 2^-9 of dS: fp16 is enough for them, as sums
+// of 2^14 P, whose 11 bits reach down to 2^-28 (a bucket that sums to less in a row
+// keeps some of that row's error of D, 2^-9 of a gradient of that size).
 //
 // Bound by the row threads' instructions: some 2000 cycles a tile with the
 // other CTA's work beside it, 4400 where the buckets change from column to
@@ -1316,7 +1326,8 @@ __device__ void window_bwd_dq(const WindowArgs& a, const CUtensorMap* tq64, cons
 // rows' writes kept it busy, and a tile took 1.6 times as long.)
 //
 // Bound by the latency of that chain of four hand-offs, with the other CTA's to
-// fill it.
+// fill it.  The heads of a group follow each other in one CTA, which needs no partial
+// sums of dK and dV; with few key blocks and a large group that leaves SMs idle.
 template <int MODE, bool WIDE>
 __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, const CUtensorMap* tq128,
                                const CUtensorMap* td64, const CUtensorMap* tg, const WindowScratch& ws_,
@@ -1544,13 +1555,20 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
       tc_fence_before();
       mbar_arrive1(wrote_ds);
     };
-    if (MODE) bias.fill_ranks<BWD_ROWS>(a, tid);
-    for (int t = 0; t < niter; ++hq) {
-      if (MODE) bias.fill<BWD_ROWS>(a, hq, tid);
-      if (MODE && __builtin_expect(*bias.big, 0)) {
-        for (qb = i0; qb < i0 + nq; ++qb, ++t) tile(std::bool_constant<MODE != 0>(), t);
-      } else {
-        for (qb = i0; qb < i0 + nq; ++qb, ++t) tile(std::false_type(), t);
+    if (MODE) {
+      bias.fill_ranks<BWD_ROWS>(a, tid);
+      for (int t = 0; t < niter; ++hq) {
+        bias.fill<BWD_ROWS>(a, hq, tid);
+        if (__builtin_expect(*bias.big, 0)) {
+          for (qb = i0; qb < i0 + nq; ++qb, ++t) tile(std::bool_constant<MODE != 0>(), t);
+        } else {
+          for (qb = i0; qb < i0 + nq; ++qb, ++t) tile(std::false_type(), t);
+        }
+      }
+    } else {
+      for (int t = 0; t < niter; ++t) {
+        tile(std::false_type(), t);
+        if (++qb == i0 + nq) qb = i0;
       }
     }
     wait(done_v, (niter - 1) & 1);
@@ -1583,8 +1601,11 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
 // 2 x 4096 tokens, 16 heads, everything visible, 32 buckets with their gradient:
 // 283 us (five products: 606 TFLOP/s); the quarters of an SM issue in 56 % of the
 // cycles, the tensor cores are busy for 41 %, the exponentials' unit for 22 %.
-// 8192 tokens, a window of 2048, 16 sinks, buckets up to 1024: 305 us.  4 x 512 tokens, a window of
-// 128, no table: 21 us.
+// 8192 tokens, a window of 2048, 16 sinks, buckets up to 1024: 305 us.  4 x 512
+// tokens, a window of 128, no table: 21 us.
+// The row threads' 96 registers do not hold everything: the five forms spill (236 to
+// 516 bytes of reloads in the code), and at 2 x 4096 tokens 2.4 % of the
+// instructions are reloads, some seven a tile and warp.
 template <int MODE, bool WIDE>
 __global__ void __launch_bounds__(BWD_THREADS, 2)
     attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap tq128,
@@ -1916,7 +1937,7 @@ int launch_attention_window_bwd(int nseq, int seq, int heads, int kv_heads, int 
       !make_tmap(&tg, dqkv, cols, seq, nseq, 128))
     return set_error(GPIPE_ERR_CUDA, "attention_window_bwd: tensor map creation failed");
   const int64_t prep = static_cast<int64_t>(nseq) * pad128(seq) * heads * 8;
-  (void)launch_k(attn_window_prep_kernel, static_cast<unsigned>((prep + 255) / 256), 256, 0, s, a,
+  (void)launch_k(a.ranks ? attn_window_prep_kernel<true> : attn_window_prep_kernel<false>, static_cast<unsigned>((prep + 255) / 256), 256, 0, s, a,
                  static_cast<const __nv_bfloat16*>(qkv), static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, w.ld, w.terms);
   rc = check_launch("attention_window_bwd (prep)");
   if (rc) return rc;

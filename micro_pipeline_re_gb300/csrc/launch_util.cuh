@@ -24,8 +24,10 @@ bool pdl_enabled();
 void set_pdl_enabled(bool on);
 
 // heavy = true: the kernel holds most of an SM's shared memory / tensor
-// memory; it is never launched early, so a waiting copy cannot keep those from
-// kernels of other streams.
+// memory and is not launched early, so that a waiting copy cannot keep those from
+// kernels of other streams.  (One that takes its tensor memory after griddep_wait()
+// and whose predecessor lets it launch only at its very end, when nothing but stores
+// is left, may still go without: the windowed attention's backward kernel.)
 // Every launch carries its stream's priority as a launch attribute, so that a
 // kernel captured into a graph (instantiated with node priorities) keeps the
 // priority of the stream it was issued to: the step's critical-path streams
