@@ -222,7 +222,8 @@ int gpipe_op_cross_entropy_clip(int rows, int vocab, int seq, const int32_t* tok
  * no teacher term, a row without a target no label term.  Slots that name the
  * same token count as separate terms of the sum.  A token id of vocab or more
  * is treated as an empty slot, a target outside [0, vocab) as no target; both
- * set the device error flag.
+ * set the device error flag.  (A padded batch with labels: one call a sequence, with
+ * seq and rows its length and row0 0.)
  * dz is bf16 [rows, vocab] with leading dimension lddz, or NULL for the loss
  * alone.  It may be the logits themselves (same address, and the same row
  * stride in bytes: lddz = ld for bf16, 2 ld for fp32); any other overlap of dz

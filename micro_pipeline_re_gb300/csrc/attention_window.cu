@@ -693,6 +693,8 @@ struct PrepItem {
 // A row whose |lse| is above kBigLse and that has a base gets its -lse without the
 // base.  lse has too few bits for the difference, so the row's sum is made again, by
 // eight threads, each 8 columns.  (Below kBigLse lse itself is accurate enough, whatever the base.)
+// 8192 tokens, 16 heads, a window of 2048, 32 buckets, forward and backward: 428 us, 643 with -1e9 in the
+// first bucket, 6.3 ms with 1e4 added to all of them, which gives every row a base.
 constexpr float kBigLse = 128.f;
 __device__ __forceinline__ void take_out_base(const WindowArgs& a, const __nv_bfloat16* qkv, float2* ld, uint8_t* terms) {
   const PrepItem at(a);
@@ -1603,7 +1605,7 @@ __device__ void window_bwd_dkv(const WindowArgs& a, const CUtensorMap* tq64, con
 // cycles, the tensor cores are busy for 41 %, the exponentials' unit for 22 %.
 // 8192 tokens, a window of 2048, 16 sinks, buckets up to 1024: 305 us.  4 x 512
 // tokens, a window of 128, no table: 21 us.
-// The row threads' 96 registers do not hold everything: the five forms spill (236 to
+// The row threads' 96 registers do not hold everything: the five forms spill (264 to
 // 516 bytes of reloads in the code), and at 2 x 4096 tokens 2.4 % of the
 // instructions are reloads, some seven a tile and warp.
 template <int MODE, bool WIDE>

@@ -401,7 +401,7 @@ struct Slots {
 
 // GRAD: the loss alone, or with dz by wide stores, or, where a row of dz is not aligned
 // for them when its logits are, by single ones (2048 x 32001 logits in rows of 32008, dz
-// in rows of 32001, bf16: 91 us; 82 where both are alike, 150 with rows read twice).
+// in rows of 32001, bf16: 91 us; 81 where both are alike, 150 with rows read twice).
 // ROWS: any, or those that all start on a 16-byte boundary, so that a CTA's part is the
 // same of all rows and made once, or those that also end on one, so that nothing is read
 // beside the copies.  4096 x 131072 bf16 372 us, 381 as rows that may end anywhere; with
@@ -1053,13 +1053,13 @@ constexpr int kShortBytes = 16384;
 // Which kernel takes the rows:
 //   up to 16 KB (where all rows are aligned for wide loads and stores) or 4096
 //       elements   registers, in the fewest threads that keep 4 or 8 loads each (16
-//       or 32 of one element).  With 64 threads 65536 rows of 512 fp32 take 364 us at
-//       4 loads and 413 at 8, 8192 x 2048 take 88 with 256 x 4 and 60 with 64 x 8,
-//       8192 x 4096 take 91 with 256 x 4, 81 with 64 x 16 and 72 with 128 x 8
+//       or 32 of one element).  With 64 slots and 64 threads 65536 rows of 512 fp32
+//       take 234 us at 4 loads and 287 at 8, 8192 x 2048 take 84 with 256 x 4 and 46
+//       with 64 x 8, 8192 x 4096 take 88 with 256 x 4, 78 with 64 x 16 and 67 with 128 x 8
 //   longer         the stream: 2048 x 32000 fp32 76 us, 115 with the row in
-//       registers; 2048 x 32001 bf16, unaligned, 82 us, 149 read twice, 1000 x
-//       100001 fp32 144 and 280 (in registers; 350 read twice).  Unaligned bf16
-//       rows of 8 to 16 KB are read twice: 8192 x 5001 158 us, 184 in the stream
+//       registers; 2048 x 32001 bf16, unaligned, 81 us, 149 read twice, 1000 x
+//       100001 fp32 141 and 280 (in registers; 350 read twice).  Unaligned bf16
+//       rows of 8 to 16 KB are read twice: 8192 x 5001 130 us, 184 in the stream
 //   what no cluster of 8 holds   is read twice
 template <typename T, bool VEC>
 cudaError_t launch_rows(const T* z, __nv_bfloat16* dz, const DistillArgs& a, int rows, bool aligned, bool wide,
