@@ -159,3 +159,28 @@ def test_a_large_entry_leaves_the_other_heads_and_a_frozen_table_as_they_are(b, 
     assert torch.equal(o.view(rows, heads, HD)[:, 1:], c.o[:rows].view(rows, heads, HD)[:, 1:])
     assert torch.equal(lse[:, 1:], c.lse[:rows, 1:])
     assert torch.equal(first[:rows, HD:heads * HD], c.dqkv[:rows, HD:heads * HD])
+
+
+@pytest.mark.parametrize("value", [-300.0, -280.0, 1e4])
+@pytest.mark.parametrize("shape", SHAPES[1:], ids=lambda s: "x".join(str(x) for x in s[:8]))
+def test_large_scores_against_large_entries(b, shape, value):  # noqa: F811
+    """Scores of some 290 on the diagonal: with entries of -300 a row's lse is small
+    although its base is large, with larger ones it is not."""
+    c = LargeCase(b, *shape[:8], lens=shape[8], table=table_of("all", value, shape[6], shape[2]))
+    cols = shape[2] + shape[3]   # queries and keys, made alike so that each row's own key has the largest score
+    x = c.qkv.view(shape[0] * shape[1], -1, HD)
+    x[:, :shape[2]] = x[:, shape[2]:cols].repeat_interleave(shape[2] // shape[3], 1)
+    x[:, :cols] *= 6
+    c.fwd()
+    c.bwd()
+    c.check()
+
+
+@pytest.mark.parametrize("scale", [6.0, 30.0])
+def test_large_scores(b, scale):  # noqa: F811
+    """The bounds grow with the scores, as fp32 does."""
+    c = Case(b, 2, 200, 2, 1, 90, 3, 8, 40, lens=[200, 77])
+    c.qkv[:, :3 * HD] *= scale
+    c.fwd()
+    c.bwd()
+    c.check()
