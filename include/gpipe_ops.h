@@ -235,6 +235,38 @@ int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t
                      float kd_scale, int seq, const int32_t* tokens, int row0, float ce_scale,
                      float* loss_rows, void* dz, int64_t lddz, void* stream);
 
+/* Next-token softmax cross-entropy of the tied head without its logits, which are
+ * never held: per row of hidden states h (bf16 [rows, d], leading dimension ldh)
+ * over the table emb (bf16 [vocab, d]),
+ *   z = h E^T in fp32, limited to [-clip, clip] where clip > 0, p = softmax(z),
+ *   loss_rows[r] = w_r inv_count (-log p[target])
+ *   g    = w_r (p - onehot(target)), 0 where |z| > clip > 0, rounded to bf16
+ *   dh   = inv_count g E        bf16 [rows, d], leading dimension lddh, or NULL
+ *   demb = inv_count g^T h      [vocab, d], or NULL: demb_dtype 0 an fp32
+ *                               accumulator that receives it (+=), 1 bf16, written
+ * (dh and demb NULL: the loss alone.)  The target of row r is that of
+ * gpipe_op_cross_entropy, tokens[row0 + r + 1] unless (row0 + r) % seq == seq - 1;
+ * a negative id means that the row has none, one of vocab or more too, and sets
+ * the device error flag.  w_r = row_weight[r] (fp32 [rows]; NULL: 1).  A row
+ * without a target or of weight 0 has loss 0, a zero row of dh and no part in demb;
+ * its h is not used and may hold anything (NaN included).
+ * piece     columns of the vocabulary whose g exists at a time (rounded up to a
+ *           multiple of 256): more scratch and fewer launches with more of them.
+ *           0: as many as give g 256 MB.
+ * scratch   gpipe_op_head_loss_scratch_bytes (grads: 1 dh, 2 demb, 3 both), 256-byte
+ *           aligned, written before it is read (calls that may overlap on the GPU,
+ *           captured ones included, need one each, and outputs each).
+ * 1 <= rows <= 2^24, 1 <= vocab <= 2^27, d and leading dimensions multiples of 8,
+ * 16-byte aligned bases.  Outputs and scratch may overlap neither each other nor an
+ * input.  No atomics: results are bit-reproducible. */
+int gpipe_op_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, const void* emb_bf16, int seq,
+                       const int32_t* tokens, int row0, const float* row_weight, float inv_count, float clip,
+                       int piece, float* loss_rows, void* dh, int64_t lddh, int demb_dtype, void* demb, void* scratch,
+                       void* stream);
+
+/* Bytes of scratch; 0 for sizes that the call would reject. */
+size_t gpipe_op_head_loss_scratch_bytes(int rows, int d, int vocab, int piece, int grads);
+
 /* MSE rows: loss_rows[r] = sum_j (y - t)^2 * inv_count; dy = 2 (y - t) inv_count. */
 int gpipe_op_mse(int rows, int d, const float* y, const float* t, float inv_count,
                  float* loss_rows, float* dy, void* stream);
@@ -249,6 +281,30 @@ int gpipe_op_embedding_fwd(int rows, int d, int vocab, const int32_t* tokens, co
  * embedding row is owned by one CTA, which adds its tokens in ascending r. */
 int gpipe_op_embedding_bwd(int rows, int d, int vocab, const int32_t* tokens,
                            const void* dx_bf16, float* demb, void* stream);
+
+/* x[r,:] = scale emb[tokens[r],:] (bf16 table [vocab, d]), x of dtype elements with
+ * leading dimension ldx, rounded once from fp32 (bf16: and once from there).  A
+ * negative token is padding: a zero row.  A token id of vocab or more gives a zero
+ * row too and sets the device error flag.  1 <= rows <= 2^27, d and ldx multiples
+ * of 8, 16-byte aligned bases; x may not overlap an input. */
+int gpipe_op_embedding_scaled_fwd(int dtype, int rows, int d, int vocab, const int32_t* tokens, const void* emb_bf16,
+                                  float scale, void* x, int64_t ldx, void* stream);
+
+/* Its gradient: demb[tokens[r],:] += scale dx[r,:] (fp32 accumulator, dx of dtype
+ * elements with leading dimension lddx).  The rows are sorted by token first, so
+ * that a frequent token's are summed by many CTAs: in ascending r within pieces of
+ * up to 32 rows, the pieces in order, scaled once and added to demb.  Padding and
+ * ids out of range as above, with no gradient.  (gpipe_op_embedding_bwd adds one row
+ * after the other: less work for a handful of tokens, and no scratch.)
+ * scratch: gpipe_op_embedding_sorted_bwd_scratch_bytes, 256-byte aligned, written
+ * before it is read (calls that may overlap on the GPU, captured ones included, need
+ * one each, and a demb each).  demb and scratch may overlap neither each other nor
+ * the inputs.  No floating-point atomics: results are bit-reproducible. */
+int gpipe_op_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int32_t* tokens, const void* dx,
+                                  int64_t lddx, float scale, float* demb, void* scratch, void* stream);
+
+/* Bytes of scratch; 0 for sizes that the call would reject. */
+size_t gpipe_op_embedding_sorted_bwd_scratch_bytes(int rows, int d, int vocab);
 
 /* RMSProp over n parameters: v = decay v + (1-decay) g^2; w -= lr g/(sqrt(v)+eps);
  * w_bf16 (may be NULL) receives the round-to-nearest-even bf16 copy of w;

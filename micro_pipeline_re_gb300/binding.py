@@ -109,6 +109,15 @@ _SIGS = {
     "gpipe_op_mse": (c_int, [c_int, c_int, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_void_p]),
     "gpipe_op_embedding_fwd": (c_int, [c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
     "gpipe_op_embedding_bwd": (c_int, [c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "gpipe_op_embedding_scaled_fwd": (c_int, [c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_float, c_void_p,
+                                              c_int64, c_void_p]),
+    "gpipe_op_embedding_sorted_bwd_scratch_bytes": (c_size_t, [c_int, c_int, c_int]),
+    "gpipe_op_embedding_sorted_bwd": (c_int, [c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int64, c_float,
+                                              c_void_p, c_void_p, c_void_p]),
+    "gpipe_op_head_loss_scratch_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "gpipe_op_head_loss": (c_int, [c_int, c_int, c_int, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_int, c_void_p,
+                                   c_float, c_float, c_int, c_void_p, c_void_p, c_int64, c_int, c_void_p, c_void_p,
+                                   c_void_p]),
     "gpipe_op_rmsprop": (c_int, [c_size_t, c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_float, c_float,
                                  c_int, c_void_p]),
     "gpipe_op_cast_bf16": (c_int, [c_size_t, c_void_p, c_void_p, c_void_p]),

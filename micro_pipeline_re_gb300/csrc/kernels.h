@@ -138,6 +138,21 @@ int launch_embedding_fwd_io(int out_dtype, int rows, int d, int vocab, const int
 int launch_embedding_bwd_io(int dx_dtype, int rows, int d, int vocab, const int32_t* tokens, const void* dx,
                             float* demb, cudaStream_t stream);
 
+// Lookup with scaling and the gradient by sorted tokens (embedding.cu).
+int launch_embedding_scaled_fwd(int dtype, int rows, int d, int vocab, const int32_t* tokens, const void* emb,
+                                float scale, void* x, int64_t ldx, cudaStream_t stream);
+size_t embedding_sorted_bwd_scratch_bytes(int rows, int d, int vocab);
+int launch_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int32_t* tokens, const void* dx,
+                                int64_t lddx, float scale, float* demb, void* scratch, cudaStream_t stream);
+
+// The head's loss and its gradients without the logits (head_loss.cu); dh or demb
+// NULL: not wanted.  grads of the scratch size: 1 dh, 2 demb.
+size_t head_loss_scratch_bytes(int rows, int d, int vocab, int piece, int grads);
+int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, const void* emb, int seq,
+                     const int32_t* tokens, int row0, const float* row_weight, float inv_count, float clip, int piece,
+                     float* loss_rows, void* dh, int64_t lddh, int demb_dtype, void* demb, void* scratch,
+                     cudaStream_t stream);
+
 int launch_rmsprop(size_t n, float* w, float* g, float* v, void* w_bf16, float lr, float decay, float eps,
                    int zero_grad, cudaStream_t stream);
 int launch_cast_bf16(size_t n, const float* src, void* dst, cudaStream_t stream);

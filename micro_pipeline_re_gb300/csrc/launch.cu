@@ -234,6 +234,34 @@ int gpipe_op_embedding_bwd(int rows, int d, int vocab, const int32_t* tokens, co
   return gp::launch_embedding_bwd(rows, d, vocab, tokens, dx_bf16, demb, static_cast<cudaStream_t>(stream));
 }
 
+int gpipe_op_embedding_scaled_fwd(int dtype, int rows, int d, int vocab, const int32_t* tokens, const void* emb_bf16,
+                                  float scale, void* x, int64_t ldx, void* stream) {
+  return gp::launch_embedding_scaled_fwd(dtype, rows, d, vocab, tokens, emb_bf16, scale, x, ldx,
+                                         static_cast<cudaStream_t>(stream));
+}
+
+size_t gpipe_op_embedding_sorted_bwd_scratch_bytes(int rows, int d, int vocab) {
+  return gp::embedding_sorted_bwd_scratch_bytes(rows, d, vocab);
+}
+
+int gpipe_op_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int32_t* tokens, const void* dx,
+                                  int64_t lddx, float scale, float* demb, void* scratch, void* stream) {
+  return gp::launch_embedding_sorted_bwd(dtype, rows, d, vocab, tokens, dx, lddx, scale, demb, scratch,
+                                         static_cast<cudaStream_t>(stream));
+}
+
+size_t gpipe_op_head_loss_scratch_bytes(int rows, int d, int vocab, int piece, int grads) {
+  return gp::head_loss_scratch_bytes(rows, d, vocab, piece, grads);
+}
+
+int gpipe_op_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, const void* emb_bf16, int seq,
+                       const int32_t* tokens, int row0, const float* row_weight, float inv_count, float clip,
+                       int piece, float* loss_rows, void* dh, int64_t lddh, int demb_dtype, void* demb, void* scratch,
+                       void* stream) {
+  return gp::launch_head_loss(rows, d, vocab, h, ldh, emb_bf16, seq, tokens, row0, row_weight, inv_count, clip, piece,
+                              loss_rows, dh, lddh, demb_dtype, demb, scratch, static_cast<cudaStream_t>(stream));
+}
+
 int gpipe_op_rmsprop(size_t n, float* w, float* g, float* v, void* w_bf16, float lr, float decay, float eps,
                      int zero_grad, void* stream) {
   return gp::launch_rmsprop(n, w, g, v, w_bf16, lr, decay, eps, zero_grad, static_cast<cudaStream_t>(stream));
