@@ -2,13 +2,35 @@
 // tied matrix E, and its gradients with respect to h and E, made for a piece of
 // the vocabulary at a time.
 //
-//   z = h_r E^T (limited to [-clip, clip]),  m = max z,  s = sum e^{z - m}
-//   loss_r = w_r a ((m - z_t) + ln s),       a = inv_count
-//   g = w_r (e^{z - m} / s - onehot(t)),     dh = a g E,  dE = a g^T h
+//   z = h_r E^T (limited to [-clip, clip]),  p = softmax(z)
+//   loss_r = -w_r a log p_t,                 a = inv_count
+//   g = w_r (p - onehot(t)),                 dh = a g E,  dE = a g^T h
 //
-// Two passes over the vocabulary: the first leaves m, s and z_t of every row, the
-// second makes a piece of z again, turns it into g (bf16) and multiplies that by E
-// and by h.
+// Launches:
+//   1  head_gemm_kernel<kStats>   z tile by tile in tensor memory; of every row and
+//                                 128 columns only (rho, sum 2^{z log2 e - rho}) leaves
+//   2  head_rows_kernel           joins them, the loss, and what 3 needs of a row
+//   per piece of the vocabulary:
+//   3  head_gemm_kernel<kGrad>    z again, turned into g in the epilogue (bf16)
+//   4  head_gemm_kernel<kProducts>  both products of g, tiles of dh and of dE in one
+//                                 launch, so that one's last round fills the other's
+//   5  head_dh_kernel             sums of dh over pieces and parts of K into bf16
+//
+// Arithmetic.  Exponentials are powers of two, with an integer reference rho of each
+// row: the argument fma(z, log2 e, -rho) is rounded once, and sums move from one
+// reference to another exactly.  The target's column is left out of the sums, and its
+// logit is a dot product of its own in fp32 (tensor cores truncate as they add: 1024
+// terms left z_t up to 2e-5 short, which showed in the loss; this way 1e-7).  So
+//   loss = log1p(sum_{v != t} e^{z_v - z_t}),  g_t = -w sum_{v != t} p_v
+// keep their digits where p_t is close to 1.  g is rounded to bf16, relative to
+// each value, as gpipe_op_cross_entropy rounds its dz; inv_count multiplies the
+// finished fp32 sums, so that g_t, close to -w for most rows, is close to a whole number
+// and its rounding does not add up over the rows.
+//
+// Cost: 8 rows vocab d flops with both gradients, where 6 would do if the logits were
+// kept.  Memory: 2 B an element of one piece of g.
+#include <cuda.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -24,10 +46,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-struct HeadRow {  // what the passes know of a row
-  float m, s, zt, w;
-};
-
 struct HeadArgs {
   int rows, d, vocab, seq, row0;
   const int32_t* tokens;
@@ -35,105 +53,493 @@ struct HeadArgs {
   float inv_count, clip;
 };
 
+// What the gradient pass knows of a row: the reference and w / sum e^{z - ...} for
+// p, g of the target's column, and the target (-1: the row has none).
+struct HeadRow {
+  float rho, scale, gt;
+  int target;
+};
+
 // Target of row r, or -1 (none: the end of a sequence, a negative id, weight 0).
 __device__ __forceinline__ int head_target(const HeadArgs& a, int r, float& w, int* err) {
   w = a.weight ? a.weight[r] : 1.f;
-  const int64_t at = static_cast<int64_t>(a.row0) + r;
-  if (w == 0.f || at % a.seq == a.seq - 1) return -1;
+  const unsigned at = static_cast<unsigned>(a.row0) + static_cast<unsigned>(r);
+  if (w == 0.f || at % static_cast<unsigned>(a.seq) == static_cast<unsigned>(a.seq) - 1u) return -1;
   const int t = a.tokens[at + 1];
   if (t >= a.vocab && err) atomicExch(err, DERR_BAD_TOKEN);
   return t >= 0 && t < a.vocab ? t : -1;
 }
 
 __device__ __forceinline__ float limit(float z, float c) {  // keeps NaN
-  if (c <= 0.f) return z;
   return z > c ? c : (z < -c ? -c : z);
 }
 
-// A warp per row: h with the rows of no target set to zero (they may hold anything).
+// ---------------------------------------------------------------------------
+// The products: persistent, a pair of CTAs (cluster of two) per 256 x 256 tile.
+//   warp 0 / lane 0   copies through a ring of stages, each CTA its 128 rows of A and
+//                     128 columns of B of a k-block of 64; both complete on rank 0's
+//                     barrier
+//   warp 1 / lane 0 of rank 0   issues 256-row products into one of two accumulators
+//   warps 2..9        epilogue, each on its own: 32 rows, 128 columns, 32 at a time
+// (the organisation of the library's persistent GEMM on SM pairs).
+// ---------------------------------------------------------------------------
+enum Mode { kStats, kGrad, kProducts };
+enum DhOut { kDhStore, kDhAdd, kDhBf16 };  // fp32, fp32 added, bf16 and final
+
+constexpr int kTile = 256;     // rows and columns of a pair's tile
+constexpr int kK = 64;         // a k-block
+constexpr int kHeadThreads = 320;
+constexpr int kGroup = 16;     // row tiles that the tiles in flight share
+constexpr int kPlanPairs = 76; // pairs of SMs that the split of dh's K is planned for (any number runs it)
+
+template <Mode MODE>
+struct HeadCfg {
+  static constexpr int kHalf = 128 * kK * 2;  // bytes of one operand of a CTA's stage
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kBox = MODE == kStats ? 0 : (MODE == kGrad ? 2048 : 4096);  // 32 x 32 elements leaving
+  static constexpr int kStages = MODE == kProducts ? 5 : 6;
+  static constexpr int kOffBox = kStages * kStage;
+  static constexpr int kOffBar = kOffBox + 8 * 2 * kBox;
+  static constexpr int kSmem = 1024 + kOffBar + 512;
+  static_assert(kSmem <= 232448, "over the shared memory of a CTA");
+};
+
+struct HeadMaps {
+  CUtensorMap a, b;    // logits: h and the piece of E; products: g and the piece of E (dh)
+  CUtensorMap c;       // where the tiles leave to: g, or dh
+  CUtensorMap a2, b2, c2;  // products: g the other way round and h (dE), dE
+};
+
+struct HeadGemm {
+  HeadArgs row;
+  int cols;              // columns of the piece
+  int v0;                // its first
+  int m_tiles, n_tiles;  // logits: rows x columns; products: dh's rows x d
+  float2* parts;         // kStats: [rows][2 n_tiles]
+  const HeadRow* info;   // kGrad
+  // kProducts
+  int splits, rows_pad;  // parts of dh's K, each with a buffer of rows_pad rows
+  int dh_items, de_items, ahead, dh_out;
+  bool de_f32;
+};
+
+struct Item {
+  int m0, n0, k0, nk;  // origin of the tile; first k-block and their number
+  int split;
+  bool de;
+};
+
+// The tiles of a pair, in order.  Logits: every pairs-th of the grouped tile order
+// (row tiles fastest within a group, so the tiles in flight share bands of both operands).
+// Products: its share of dh's tiles first, which are few and long; then tiles of dE,
+// the pairs with one tile of dh less taking `ahead` of them before the others join in.
+template <Mode MODE>
+struct Walk {
+  int pair, pairs, i = 0, j = 0;
+  __device__ Walk(int p, int n) : pair(p), pairs(n) {}
+  __device__ __forceinline__ bool next(const HeadGemm& a, Item& it) {
+    it.split = 0;
+    it.de = false;
+    it.k0 = 0;
+    if (MODE != kProducts) {
+      const int t = pair + i++ * pairs;
+      if (t >= a.m_tiles * a.n_tiles) return false;
+      const int per_group = kGroup * a.n_tiles;
+      const int grp = t / per_group, r = t - grp * per_group, first = grp * kGroup;
+      const int gm = min(kGroup, a.m_tiles - first);
+      it.m0 = (first + r % gm) * kTile;
+      it.n0 = (r / gm) * kTile;
+      it.nk = (a.row.d + kK - 1) / kK;
+      return true;
+    }
+    const int t = pair + i * pairs;
+    if (t < a.dh_items) {
+      ++i;
+      const int n = t % a.n_tiles, m = t / a.n_tiles % a.m_tiles;
+      it.split = t / (a.n_tiles * a.m_tiles);
+      const int nk = (a.cols + kK - 1) / kK;
+      it.m0 = m * kTile;
+      it.n0 = n * kTile;
+      it.k0 = static_cast<int>(static_cast<int64_t>(nk) * it.split / a.splits);
+      it.nk = static_cast<int>(static_cast<int64_t>(nk) * (it.split + 1) / a.splits) - it.k0;
+      return true;
+    }
+    const int late = a.dh_items % pairs;  // pairs with one more tile of dh
+    const int ahead = pair >= late ? a.ahead : 0, rest = pairs - late;
+    const int e = j < ahead ? j * rest + (pair - late) : a.ahead * rest + (j - ahead) * pairs + pair;
+    ++j;
+    if (e >= a.de_items) return false;
+    it.de = true;
+    it.m0 = e / a.n_tiles * kTile;
+    it.n0 = e % a.n_tiles * kTile;
+    it.nk = (a.row.rows + kK - 1) / kK;
+    return true;
+  }
+};
+
+// Byte offset of 16-byte unit u of row r of a 32 x 32 box, as the tensor maps swizzle
+// it: 64-byte rows (bf16) or 128-byte rows (fp32).
+__device__ __forceinline__ uint32_t box_bf16(int r, int u) {
+  return static_cast<uint32_t>(r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ uint32_t box_f32(int r, int u) {
+  return static_cast<uint32_t>(r * 128 + ((u ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+
+__device__ __forceinline__ bool head_wait(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
+  if (*abort) return false;
+  if (mbar_wait_bounded(bar, parity, err, code)) return true;
+  *abort = 1;
+  return false;
+}
+
+// (rho, s) += the 32 logits of v: a row's running reference and sum.
+__device__ __forceinline__ void add_chunk(const float* v, float& rho, float& s) {
+  float m = fmaxf(v[0], v[1]);
+#pragma unroll
+  for (int j = 2; j < 32; j += 2) m = fmax3(m, v[j], v[j + 1]);
+  const float to = fmaxf(rho, ceilf(m * kLog2e));
+  if (to == -INFINITY) return;  // nothing but columns that are left out
+  const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-to, -to);
+  f32x2 sum[4];
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    float x, y;
+    unpack2(fma2(pack2(v[j], v[j + 1]), l2, ref), x, y);
+    const f32x2 e = pack2(ex2_approx(x), ex2_approx(y));
+    sum[(j >> 1) & 3] = j < 8 ? e : add2(sum[(j >> 1) & 3], e);
+  }
+  float x, y;
+  unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+  s = fmaf(s, ex2_approx(rho - to), x + y);
+  rho = to;
+}
+
+template <Mode MODE>
+__global__ void __launch_bounds__(kHeadThreads, 1)
+    head_gemm_kernel(const __grid_constant__ HeadMaps maps, const HeadGemm a, int* err) {
+  using Cfg = HeadCfg<MODE>;
+  constexpr int STAGES = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBar);
+  uint64_t* empty = full + STAGES;
+  uint64_t* accf = empty + STAGES;  // accumulator b holds a finished tile
+  uint64_t* acce = accf + 2;        // accumulator b has been drained
+  uint64_t* bfin = acce + 2;        // every product of the pair has completed
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bfin + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank() & 1u);
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 16);  // the epilogue warps of both CTAs
+    }
+    mbar_init(bfin, 1);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tslot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers exist before any copy or arrival names them
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  griddep_wait();  // global memory from here on
+
+  Walk<MODE> walk(pair, pairs);
+  Item it;
+  if (warp == 0) {
+    if (lane == 0) {
+      int n = 0;
+      while (!*abort && walk.next(a, it)) {
+        const int am = it.m0 + rank * 128, bn = it.n0 + rank * 128;
+        for (int kb = 0; kb < it.nk; ++kb, ++n) {
+          const int s = n % STAGES;
+          if (!head_wait(&empty[s], ((n / STAGES) & 1) ^ 1, err, DERR_TMA_WAIT, abort)) break;
+          uint8_t* sa = smem + s * Cfg::kStage;
+          uint8_t* sb = sa + Cfg::kHalf;
+          const int k = (it.k0 + kb) * kK;
+          const uint32_t fb = map_peer(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Cfg::kStage);
+          if (MODE != kProducts) {
+            tma_load_2d_pair(sa, &maps.a, k, am, fb);
+            tma_load_2d_pair(sb, &maps.b, k, bn, fb);
+          } else if (!it.de) {
+            tma_load_2d_pair(sa, &maps.a, k, am, fb);
+            tma_load_2d_pair(sb, &maps.b, bn, k, fb);
+            tma_load_2d_pair(sb + 8192, &maps.b, bn + 64, k, fb);
+          } else {
+            tma_load_2d_pair(sa, &maps.a2, am, k, fb);
+            tma_load_2d_pair(sa + 8192, &maps.a2, am + 64, k, fb);
+            tma_load_2d_pair(sb, &maps.b2, bn, k, fb);
+            tma_load_2d_pair(sb + 8192, &maps.b2, bn + 64, k, fb);
+          }
+        }
+      }
+      // no copy may still be landing in shared memory when a CTA of the pair leaves
+      if (rank == 0)
+        for (int j = (n > STAGES ? n - STAGES : 0); j < n; ++j)
+          mbar_wait_bounded(&full[j % STAGES], (j / STAGES) & 1, err, DERR_DRAIN_WAIT);
+    }
+    griddep_launch();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int n = 0, i = 0;
+      for (; walk.next(a, it); ++i) {
+        const int b = i & 1;
+        if (*abort || !mbar_wait_bounded_cluster(&acce[b], ((i >> 1) & 1) ^ 1, err, DERR_MMA_WAIT)) {
+          *abort = 1;
+          break;
+        }
+        tc_fence_after();
+        const bool a_mn = MODE == kProducts && it.de, b_mn = MODE == kProducts;
+        const uint32_t idesc = a_mn ? mma_idesc_bf16(kTile, kTile, true, true)
+                                    : mma_idesc_bf16(kTile, kTile, false, MODE == kProducts);
+        const uint32_t acc = tmem + b * kTile;
+        for (int kb = 0; kb < it.nk; ++kb, ++n) {
+          const int s = n % STAGES;
+          if (!head_wait(&full[s], (n / STAGES) & 1, err, DERR_MMA_WAIT, abort)) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * Cfg::kStage), sb = sa + Cfg::kHalf;
+#pragma unroll
+          for (int kk = 0; kk < kK / 16; ++kk) {
+            const uint64_t ad = a_mn ? sw128_desc(sa + kk * 2048, 8192, 1024) : sw128_desc(sa + kk * 32, 16, 1024);
+            const uint64_t bd = b_mn ? sw128_desc(sb + kk * 2048, 8192, 1024) : sw128_desc(sb + kk * 32, 16, 1024);
+            tc_mma_f16_pair(acc, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair(&empty[s], 3);  // both CTAs' stage s is free again
+        }
+        tc_commit_pair(&accf[b], 3);
+      }
+      tc_commit_pair(bfin, 1);
+      mbar_wait_bounded(bfin, 0, err, DERR_DRAIN_WAIT);
+    }
+    griddep_launch();
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* boxes = smem + Cfg::kOffBox + (warp - 2) * 2 * Cfg::kBox;
+    const uint32_t acce_leader = map_peer(smem_u32(acce), 0);
+    int staged = 0;
+    for (int i = 0; walk.next(a, it); ++i) {
+      const int b = i & 1;
+      const int mw = it.m0 + rank * 128 + q * 32, m = mw + lane;  // the warp's first row, the thread's
+      const int c0 = it.n0 + half * 128;                          // the warp's first column
+      const int width = MODE == kProducts ? a.row.d : a.cols;
+      const int nch = max(0, min(4, (width - c0 + 31) / 32));
+      // what the epilogue knows of the row, read while the products run
+      int target = -1;
+      HeadRow info = {0.f, 0.f, 0.f, -1};
+      if (MODE == kStats && m < a.row.rows) {
+        float w;
+        target = head_target(a.row, m, w, nullptr);
+      }
+      if (MODE == kGrad && m < a.row.rows) {
+        const float4 f = *reinterpret_cast<const float4*>(a.info + m);
+        info = HeadRow{f.x, f.y, f.z, __float_as_int(f.w)};
+        target = info.target - a.v0;
+      }
+      head_wait(&accf[b], (i >> 1) & 1, err, DERR_ACC_WAIT, abort);
+      tc_fence_after();
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + half * 128;
+      uint32_t ra[32];
+      if (nch > 0) tmem_ld32(tb, ra);
+      float rho = -INFINITY, sum = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c) {
+        tmem_ld_wait32(ra);
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ra[j]);
+        if (c + 1 < nch) tmem_ld32(tb + (c + 1) * 32, ra);  // lands while this chunk is worked on
+        const int col = c0 + c * 32;
+        const bool has_target = static_cast<unsigned>(target - col) < 32u;
+        if (MODE == kStats) {
+          if (a.row.clip > 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = limit(v[j], a.row.clip);
+          }
+          if (col + 32 > width) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col + j >= width) v[j] = -INFINITY;
+          }
+          if (__any_sync(0xffffffffu, has_target)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col + j == target) v[j] = -INFINITY;
+          }
+          add_chunk(v, rho, sum);
+          continue;
+        }
+        if (MODE == kGrad) {
+          const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-info.rho, -info.rho), sc = pack2(info.scale, info.scale);
+          if (a.row.clip > 0.f) {  // columns beyond the limit: marked, so that they come out as 0
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fabsf(v[j]) > a.row.clip ? -INFINITY : v[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float x, y;
+            unpack2(fma2(pack2(v[j], v[j + 1]), l2, ref), x, y);
+            unpack2(mul2(pack2(ex2_approx(x), ex2_approx(y)), sc), v[j], v[j + 1]);
+          }
+          if (__any_sync(0xffffffffu, has_target)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col + j == target) v[j] = info.gt;
+          }
+          if (info.target < 0) {  // whatever the row holds
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+        }
+        if (MODE == kProducts) {
+          const bool add_scale = it.de || a.dh_out == kDhBf16;
+          const float al = add_scale ? a.row.inv_count : 1.f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= al;
+        }
+        // the chunk leaves through one of the warp's two boxes
+        uint8_t* box = boxes + (staged++ & 1) * Cfg::kBox;
+        if (lane == 0) wait_read_1();
+        __syncwarp();
+        const bool f32 = MODE == kProducts && (it.de ? a.de_f32 : a.dh_out != kDhBf16);
+        if (f32) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<float4*>(box + box_f32(lane, u)) =
+                make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) store8(reinterpret_cast<__nv_bfloat16*>(box + box_bf16(lane, u)), v + 8 * u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (!*abort) {
+            if (MODE == kGrad) {
+              tma_store_2d(&maps.c, col, mw, box);
+            } else if (it.de) {
+              if (a.de_f32) tma_reduce_add_2d(&maps.c2, col, a.v0 + mw, box);
+              else tma_store_2d(&maps.c2, col, a.v0 + mw, box);
+            } else {
+              const int y = it.split * a.rows_pad + mw;
+              if (a.dh_out == kDhAdd) tma_reduce_add_2d(&maps.c, col, y, box);
+              else tma_store_2d(&maps.c, col, y, box);
+            }
+          }
+          bulk_commit();
+        }
+      }
+      if (MODE == kStats && m < a.row.rows)
+        a.parts[static_cast<int64_t>(m) * (2 * a.n_tiles) + (it.n0 / 128 + half)] = make_float2(rho, sum);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acce_leader + static_cast<uint32_t>(b * sizeof(uint64_t)));
+    }
+    griddep_launch();
+    if (MODE != kStats && lane == 0) bulk_wait_read_all();
+  }
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the pair's products may read its shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// A warp per row: joins the row's sums, takes the target's logit as a dot product, the
+// loss, what the gradient pass needs, and (hm not NULL) h with the rows that count for
+// nothing set to zero.
 __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_bfloat16* __restrict__ h, int64_t ldh,
-                                                        __nv_bfloat16* __restrict__ hm, HeadRow* __restrict__ info,
-                                                        int* err) {
+                                                        const __nv_bfloat16* __restrict__ emb,
+                                                        const float2* __restrict__ parts, int nparts,
+                                                        float* __restrict__ loss, HeadRow* __restrict__ info,
+                                                        __nv_bfloat16* __restrict__ hm, int* err) {
   griddep_wait();
   griddep_launch();
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= a.rows) return;
   float w;
   const int t = head_target(a, r, w, lane == 0 ? err : nullptr);
-  for (int c = lane * 8; c < a.d; c += 256) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (t >= 0) v = *reinterpret_cast<const uint4*>(h + r * ldh + c);
-    *reinterpret_cast<uint4*>(hm + static_cast<int64_t>(r) * a.d + c) = v;
-  }
-  if (lane == 0) info[r] = HeadRow{-INFINITY, 0.f, 0.f, t >= 0 ? w : 0.f};
-}
-
-// A CTA per row: the piece's columns into m, s and z_t.
-__global__ void __launch_bounds__(256) head_stats_kernel(HeadArgs a, const float* __restrict__ z, int64_t ldz, int v0,
-                                                         int cols, HeadRow* __restrict__ info) {
-  griddep_wait();
-  griddep_launch();
-  __shared__ float red[8];
-  const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const float* zr = z + r * ldz;
-  HeadRow row = info[r];
-  float m = row.m;
-  for (int c = tid; c < cols; c += 256) m = fmaxf(m, limit(zr[c], a.clip));
-  m = warp_max(m);
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
-  __syncthreads();
-  float s = 0.f;
-  for (int c = tid; c < cols; c += 256) s += ex2_approx((limit(zr[c], a.clip) - m) * kLog2e);
-  s = warp_sum(s);
-  if (lane == 0) red[warp] = s;
-  __syncthreads();
-  if (tid == 0) {
-    s = row.s > 0.f ? row.s * ex2_approx((row.m - m) * kLog2e) : 0.f;
-    for (int w = 0; w < 8; ++w) s += red[w];
-    float w;
-    const int t = head_target(a, r, w, nullptr);
-    if (t >= v0 && t < v0 + cols) row.zt = limit(zr[t - v0], a.clip);
-    info[r] = HeadRow{m, s, row.zt, row.w};
-  }
-}
-
-__global__ void __launch_bounds__(256) head_loss_kernel(int rows, float inv_count, const HeadRow* __restrict__ info,
-                                                        float* __restrict__ loss) {
-  griddep_wait();
-  griddep_launch();
-  const int r = blockIdx.x * 256 + threadIdx.x;
-  if (r >= rows) return;
-  const HeadRow i = info[r];
-  loss[r] = i.w != 0.f ? i.w * inv_count * ((i.m - i.zt) + logf(i.s)) : 0.f;
-}
-
-// A CTA per row: the piece of z into g (times inv_count), bf16.
-__global__ void __launch_bounds__(256) head_grad_kernel(HeadArgs a, const float* __restrict__ z, int64_t ldz, int v0,
-                                                        int cols, const HeadRow* __restrict__ info,
-                                                        __nv_bfloat16* __restrict__ g) {
-  griddep_wait();
-  griddep_launch();
-  const int r = blockIdx.x;
-  const float* zr = z + r * ldz;
-  const HeadRow i = info[r];
-  float w;
-  const int t = head_target(a, r, w, nullptr);
-  const float wa = i.w * a.inv_count, inv_s = 1.f / i.s;
-  for (int c = threadIdx.x; c < cols; c += 256) {
-    float v = 0.f;
-    if (t >= 0) {
-      const float x = zr[c];
-      v = wa * (ex2_approx((limit(x, a.clip) - i.m) * kLog2e) * inv_s - (v0 + c == t ? 1.f : 0.f));
-      if (a.clip > 0.f && fabsf(x) > a.clip) v = 0.f;
+  const float2* mine = parts + static_cast<int64_t>(r) * nparts;
+  float rho = -INFINITY, s = 0.f, zt = 0.f;
+  if (t >= 0) {
+    for (int i = lane; i < nparts; i += 32) {
+      const float2 p = mine[i];
+      const float to = fmaxf(rho, p.x);
+      if (to > -INFINITY) s = s * exp2f(rho - to) + p.y * exp2f(p.x - to);
+      else s += p.y;  // nothing there, or NaN
+      rho = to;
     }
-    g[r * ldz + c] = f2bf(v);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float rho2 = __shfl_xor_sync(0xffffffffu, rho, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      const float to = fmaxf(rho, rho2);
+      // (a sum in a fixed order for both lanes of a pair, so that all agree)
+      const float x = lane & o ? s2 : s, y = lane & o ? s : s2;
+      const float rx = lane & o ? rho2 : rho, ry = lane & o ? rho : rho2;
+      s = to > -INFINITY ? x * exp2f(rx - to) + y * exp2f(ry - to) : x + y;
+      rho = to;
+    }
   }
+  for (int c = lane * 8; c < a.d; c += 256) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (t >= 0) {
+      u = *reinterpret_cast<const uint4*>(h + r * ldh + c);
+      float e[8];
+      load8(emb + static_cast<int64_t>(t) * a.d + c, e);
+      const float2 p0 = unpack_bf16x2(u.x), p1 = unpack_bf16x2(u.y), p2 = unpack_bf16x2(u.z), p3 = unpack_bf16x2(u.w);
+      zt += ((p0.x * e[0] + p0.y * e[1]) + (p1.x * e[2] + p1.y * e[3])) +
+            ((p2.x * e[4] + p2.y * e[5]) + (p3.x * e[6] + p3.y * e[7]));
+    }
+    if (hm) *reinterpret_cast<uint4*>(hm + static_cast<int64_t>(r) * a.d + c) = u;
+  }
+  if (t < 0) {
+    if (lane == 0) {
+      loss[r] = 0.f;
+      if (info) info[r] = HeadRow{0.f, 0.f, 0.f, -1};
+    }
+    return;
+  }
+  zt = warp_sum(zt);
+  if (lane != 0) return;
+  bool cut = false;
+  if (a.clip > 0.f) {
+    cut = fabsf(zt) > a.clip;
+    zt = limit(zt, a.clip);
+  }
+  // odds of all other tokens together against the target: s 2^x
+  const float x = fmaf(-zt, kLog2e, rho);
+  const float odds = s * exp2f(x);
+  const float nll = x > 60.f ? fmaf(x, kLn2, logf(s)) : log1pf(odds);
+  loss[r] = w * a.inv_count * nll;
+  if (!info) return;
+  const float ref = fmaxf(rho, ceilf(zt * kLog2e));
+  const float total = (rho > -INFINITY ? s * exp2f(rho - ref) : s) + exp2f(fmaf(zt, kLog2e, -ref));
+  // x > 60: the others have all of it
+  const float others = x > 60.f ? (s == s ? 1.f : s) : odds / (1.f + odds);
+  info[r] = HeadRow{ref, w / total, cut ? 0.f : -w * others, t};
 }
 
-__global__ void __launch_bounds__(256) head_dh_kernel(int rows, int d, const float* __restrict__ src,
-                                                      __nv_bfloat16* __restrict__ dh, int64_t lddh) {
+// dh = inv_count times the sum of its parts, a warp per row.
+__global__ void __launch_bounds__(256) head_dh_kernel(int rows, int d, int splits, int rows_pad, float scale,
+                                                      const float* __restrict__ src, __nv_bfloat16* __restrict__ dh,
+                                                      int64_t lddh) {
   griddep_wait();
   griddep_launch();
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -141,10 +547,21 @@ __global__ void __launch_bounds__(256) head_dh_kernel(int rows, int d, const flo
   for (int c = lane * 8; c < d; c += 256) {
     float v[8];
     load8(src + static_cast<int64_t>(r) * d + c, v);
+    for (int p = 1; p < splits; ++p) {
+      float u[8];
+      load8(src + (static_cast<int64_t>(p) * rows_pad + r) * d + c, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += u[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= scale;
     store8(dh + r * lddh + c, v);
   }
 }
 
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
 int check(const char* what) {
   count_launch();
   const cudaError_t e = cudaGetLastError();
@@ -152,39 +569,143 @@ int check(const char* what) {
   return GPIPE_OK;
 }
 
+int up_to(int n, int m) { return (n + m - 1) / m; }
+
 bool sizes_ok(int rows, int d, int vocab, int piece) {
   return rows >= 1 && rows <= (1 << 24) && d >= 8 && d <= (1 << 16) && d % 8 == 0 && vocab >= 1 &&
-         vocab <= (1 << 27) && piece >= 0;
+         vocab <= (1 << 27) && piece >= 0 && static_cast<int64_t>(up_to(rows, kTile)) * up_to(vocab, kTile) <= (1 << 30);
 }
 
 // Columns of a piece: a multiple of 256; 0 asks for as many as make g 256 MB.
 int piece_columns(int rows, int vocab, int piece) {
   int64_t p = piece ? piece : std::max<int64_t>(2048, (static_cast<int64_t>(1) << 27) / rows);
-  p = std::min<int64_t>((p + 255) / 256 * 256, (static_cast<int64_t>(vocab) + 255) / 256 * 256);
+  p = std::min<int64_t>((p + kTile - 1) / kTile * kTile, (static_cast<int64_t>(vocab) + kTile - 1) / kTile * kTile);
   return static_cast<int>(p);
 }
 
-struct HeadScratch {
-  size_t info, hm, z, g, dh, bytes;
+// Tiles of dE that the pairs with one tile of dh less take first, and k-blocks that the
+// busiest pair then has.  A tile costs its k-blocks and two more (measured: filling
+// the ring and the last tile's epilogue).
+struct Balance {
+  int ahead;
+  int64_t longest;
 };
-HeadScratch head_scratch(int rows, int d, int piece, int grads) {
+Balance balance(int64_t dh_items, int dh_nk, int64_t de_items, int de_nk, int pairs) {
+  const int64_t ch = dh_nk + 2, ce = de_nk + 2, q = dh_items / pairs, late = dh_items % pairs, rest = pairs - late;
+  int64_t ahead = late ? (ch + ce / 2) / ce : 0;
+  ahead = std::min(ahead, (de_items + rest - 1) / rest);
+  const int64_t left = std::max<int64_t>(0, de_items - ahead * rest), each = (left + pairs - 1) / pairs;
+  const int64_t early = q * ch + (ahead + each) * ce;
+  return {static_cast<int>(ahead), late ? std::max(early, (q + 1) * ch + each * ce) : early};
+}
+
+// Parts of dh's K (the vocabulary): with few tiles of dh their long sums would be what
+// all else waits for.  Depends on the sizes alone, as do then the bits of dh.
+int dh_splits(int rows, int d, int cols, bool demb) {
+  const int64_t tiles = static_cast<int64_t>(up_to(rows, kTile)) * up_to(d, kTile);
+  const int64_t de_items = demb ? static_cast<int64_t>(up_to(cols, kTile)) * up_to(d, kTile) : 0;
+  const int nk = up_to(cols, kK), de_nk = up_to(rows, kK);
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= 16 && nk / s >= 8; ++s) {
+    // a part's 8 bytes an element through memory: 4 k-blocks' time a tile
+    const int64_t cost = balance(tiles * s, up_to(nk, s), de_items, de_nk, kPlanPairs).longest +
+                         (s > 1 ? 8 + 4 * s * tiles / kPlanPairs : 0);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct HeadScratch {
+  size_t parts, info, hm, g, dh, bytes;
+  int cols, splits, rows_pad;
+  bool direct;  // dh comes out of the products as it is
+};
+HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads) {
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   const size_t n = static_cast<size_t>(rows);
   HeadScratch s;
-  s.info = 0;
-  s.hm = up(n * sizeof(HeadRow));
-  s.z = s.hm + up(n * d * 2);
-  s.g = s.z + up(n * piece * 4);
-  s.dh = s.g + (grads ? up(n * piece * 2) : 0);
-  s.bytes = s.dh + (grads & 1 ? up(n * d * 4) : 0);
+  s.cols = piece_columns(rows, vocab, piece);
+  s.splits = grads & 1 ? dh_splits(rows, d, s.cols, grads & 2) : 1;
+  s.rows_pad = up_to(rows, kTile) * kTile;
+  s.direct = s.splits == 1 && s.cols >= vocab;
+  s.parts = 0;
+  s.info = up(n * 2 * up_to(vocab, kTile) * sizeof(float2));
+  s.hm = s.info + (grads ? up(n * sizeof(HeadRow)) : 0);
+  s.g = s.hm + (grads & 2 ? up(n * d * 2) : 0);
+  s.dh = s.g + (grads ? up(n * s.cols * 2) : 0);
+  s.bytes = s.dh + ((grads & 1) && !s.direct ? up(static_cast<size_t>(s.splits) * s.rows_pad * d * 4) : 0);
   return s;
+}
+
+// 2-D tensor of `outer` rows of `inner` elements, ld elements apart; boxes of
+// box_inner x box_outer.  Boxes that leave (32 x 32) have rows of 64 bytes in bf16.
+bool head_map(CUtensorMap* m, const void* base, bool f32, int64_t inner, int64_t outer, int64_t ld, int box_inner,
+              int box_outer) {
+  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn enc = known.load(std::memory_order_acquire);
+  if (!enc) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    enc = reinterpret_cast<EncodeFn>(p);
+    known.store(enc, std::memory_order_release);
+  }
+  const int es = f32 ? 4 : 2;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
+  cuuint32_t estr[2] = {1u, 1u};
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_inner * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Mode MODE>
+int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, int* err, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  const int rc = once_per_device(done, [] {
+    const cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               HeadCfg<MODE>::kSmem);
+    return e == cudaSuccess ? GPIPE_OK
+                            : set_error(GPIPE_ERR_CUDA, "head_loss: smem attribute: %s", cudaGetErrorString(e));
+  });
+  if (rc) return rc;
+  const int pairs = static_cast<int>(std::min<int64_t>(std::max(1, num_sms() / 2), items));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kHeadThreads);
+  cfg.dynamicSmemBytes = HeadCfg<MODE>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  set_priority_attr(attr[1], s);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  HeadGemm b = a;
+  if (MODE == kProducts)
+    b.ahead = balance(a.dh_items, up_to(up_to(a.cols, kK), a.splits), a.de_items, up_to(a.row.rows, kK), pairs).ahead;
+  (void)cudaLaunchKernelEx(&cfg, head_gemm_kernel<MODE>, maps, b, err);
+  return check(MODE == kStats ? "stats" : (MODE == kGrad ? "gradient" : "products"));
 }
 
 }  // namespace
 
 size_t head_loss_scratch_bytes(int rows, int d, int vocab, int piece, int grads) {
   if (!sizes_ok(rows, d, vocab, piece) || grads < 0 || grads > 3) return 0;
-  return head_scratch(rows, d, piece_columns(rows, vocab, piece), grads).bytes;
+  return head_scratch(rows, d, vocab, piece, grads).bytes;
 }
 
 int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, const void* emb, int seq,
@@ -196,7 +717,8 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   using attn::Range;
   if (!sizes_ok(rows, d, vocab, piece))
     return set_error(GPIPE_ERR_INVALID_ARG,
-                     "head_loss: need 1 <= rows <= 2^24, 8 <= d <= 2^16, d %% 8 == 0, 1 <= vocab <= 2^27 and piece >= 0");
+                     "head_loss: need 1 <= rows <= 2^24, 8 <= d <= 2^16, d %% 8 == 0, 1 <= vocab <= 2^27, "
+                     "piece >= 0 and at most 2^30 tiles of 256 x 256");
   if (demb && demb_dtype != DT_F32 && demb_dtype != DT_BF16)
     return set_error(GPIPE_ERR_UNSUPPORTED, "head_loss: demb_dtype must be 0 or 1");
   if (seq < 1 || row0 < 0 || static_cast<int64_t>(row0) + rows >= INT32_MAX)
@@ -213,8 +735,7 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256)
     return set_error(GPIPE_ERR_INVALID_ARG, "head_loss: scratch must be 256-B aligned");
   const int grads = (dh ? 1 : 0) | (demb ? 2 : 0);
-  const int cols = piece_columns(rows, vocab, piece);
-  const HeadScratch at = head_scratch(rows, d, cols, grads);
+  const HeadScratch at = head_scratch(rows, d, vocab, piece, grads);
   const size_t n = static_cast<size_t>(rows), table = static_cast<size_t>(vocab) * d;
   const Range in[4] = {{h, ((n - 1) * ldh + d) * 2},
                        {emb, table * 2},
@@ -235,79 +756,65 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   if (!err) return set_error(GPIPE_ERR_CUDA, "head_loss: no device error word");
 
   char* w = static_cast<char*>(scratch);
+  auto* parts = reinterpret_cast<float2*>(w + at.parts);
   auto* info = reinterpret_cast<HeadRow*>(w + at.info);
   auto* hm = reinterpret_cast<__nv_bfloat16*>(w + at.hm);
-  float* z = reinterpret_cast<float*>(w + at.z);
   auto* g = reinterpret_cast<__nv_bfloat16*>(w + at.g);
   float* dh32 = reinterpret_cast<float*>(w + at.dh);
+  const auto* e = static_cast<const __nv_bfloat16*>(emb);
   const HeadArgs a{rows, d, vocab, seq, row0, tokens, row_weight, inv_count, clip};
-  int rc;
-  (void)launch_k(head_rows_kernel, (rows + 7) / 8, 256, 0, st, a, static_cast<const __nv_bfloat16*>(h), ldh, hm, info,
-                 err);
+  HeadMaps maps = {};
+  HeadGemm q = {};
+  q.row = a;
+  q.cols = vocab;
+  q.m_tiles = up_to(rows, kTile);
+  q.n_tiles = up_to(vocab, kTile);
+  q.parts = parts;
+  q.info = info;
+  CUtensorMap map_h;
+  bool ok = head_map(&map_h, h, false, d, rows, ldh, kK, 128) && head_map(&maps.b, emb, false, d, vocab, d, kK, 128);
+  if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
+  maps.a = map_h;
+  int rc = launch_head_gemm<kStats>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st);
+  if (rc) return rc;
+  (void)launch_k(head_rows_kernel, up_to(rows, 8), 256, 0, st, a, static_cast<const __nv_bfloat16*>(h), ldh, e,
+                 static_cast<const float2*>(parts), 2 * q.n_tiles, loss_rows, grads ? info : nullptr,
+                 demb ? hm : nullptr, err);
   if ((rc = check("rows"))) return rc;
-  auto logits = [&](int v0, int kc) {
-    GemmDesc q;
-    q.M = rows;
-    q.N = kc;
-    q.K = d;
-    q.A = hm;
-    q.lda = d;
-    q.B = static_cast<const __nv_bfloat16*>(emb) + static_cast<int64_t>(v0) * d;
-    q.ldb = d;
-    q.epi = EPI_STORE_F32;
-    q.C = z;
-    q.ldc = cols;
-    return launch_gemm(q, st);
-  };
-  for (int v0 = 0; v0 < vocab; v0 += cols) {
-    const int kc = std::min(cols, vocab - v0);
-    if ((rc = logits(v0, kc))) return rc;
-    (void)launch_k(head_stats_kernel, rows, 256, 0, st, a, static_cast<const float*>(z), static_cast<int64_t>(cols),
-                   v0, kc, info);
-    if ((rc = check("stats"))) return rc;
-  }
-  (void)launch_k(head_loss_kernel, (rows + 255) / 256, 256, 0, st, rows, inv_count, static_cast<const HeadRow*>(info),
-                 loss_rows);
-  if ((rc = check("loss"))) return rc;
-  if (!grads) return GPIPE_OK;
-  if (dh && cudaMemsetAsync(dh32, 0, n * d * 4, st) != cudaSuccess)
-    return set_error(GPIPE_ERR_CUDA, "head_loss: memset");
-  for (int v0 = 0; v0 < vocab; v0 += cols) {
-    const int kc = std::min(cols, vocab - v0);
-    if ((rc = logits(v0, kc))) return rc;
-    (void)launch_k(head_grad_kernel, rows, 256, 0, st, a, static_cast<const float*>(z), static_cast<int64_t>(cols), v0,
-                   kc, static_cast<const HeadRow*>(info), g);
-    if ((rc = check("gradient"))) return rc;
-    const int64_t row_of = static_cast<int64_t>(v0) * d;
-    GemmDesc q;
-    q.ldb = d;
-    q.N = d;
-    q.b_kmajor = false;
-    q.A = g;
-    q.lda = cols;
-    q.ldc = d;
+  for (int v0 = 0; grads && v0 < vocab; v0 += at.cols) {
+    const int cols = std::min(at.cols, vocab - v0);
+    const auto* piece_of_e = e + static_cast<int64_t>(v0) * d;
+    q.cols = cols;
+    q.v0 = v0;
+    q.n_tiles = up_to(cols, kTile);
+    maps.a = map_h;
+    ok = head_map(&maps.b, piece_of_e, false, d, cols, d, kK, 128) &&
+         head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
+    if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
+    if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st))) return rc;
+    q.n_tiles = up_to(d, kTile);
+    q.splits = std::min(at.splits, up_to(cols, kK));
+    q.rows_pad = at.rows_pad;
+    q.dh_items = dh ? q.m_tiles * q.n_tiles * q.splits : 0;
+    q.de_items = demb ? up_to(cols, kTile) * q.n_tiles : 0;
+    q.dh_out = at.direct ? kDhBf16 : (v0 ? kDhAdd : kDhStore);
+    q.de_f32 = demb_dtype == DT_F32;
     if (dh) {
-      q.M = rows;
-      q.K = kc;
-      q.B = static_cast<const __nv_bfloat16*>(emb) + row_of;
-      q.epi = EPI_ACC_F32;
-      q.C = dh32;
-      if ((rc = launch_gemm(q, st))) return rc;
+      ok = head_map(&maps.a, g, false, cols, rows, at.cols, kK, 128) &&
+           head_map(&maps.b, piece_of_e, false, d, cols, d, kK, kK) &&
+           (at.direct ? head_map(&maps.c, dh, false, d, rows, lddh, 32, 32)
+                      : head_map(&maps.c, dh32, true, d, static_cast<int64_t>(at.splits) * at.rows_pad, d, 32, 32));
     }
-    if (demb) {
-      q.M = kc;
-      q.K = rows;
-      q.a_kmajor = false;
-      q.B = hm;
-      q.epi = demb_dtype == DT_F32 ? EPI_ACC_F32 : EPI_STORE;
-      q.C = demb_dtype == DT_F32 ? static_cast<void*>(static_cast<float*>(demb) + row_of)
-                                 : static_cast<void*>(static_cast<__nv_bfloat16*>(demb) + row_of);
-      if ((rc = launch_gemm(q, st))) return rc;
-    }
+    if (ok && demb)
+      ok = head_map(&maps.a2, g, false, cols, rows, at.cols, kK, kK) &&
+           head_map(&maps.b2, hm, false, d, rows, d, kK, kK) &&
+           head_map(&maps.c2, demb, q.de_f32, d, vocab, d, 32, 32);
+    if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
+    if ((rc = launch_head_gemm<kProducts>(maps, q, static_cast<int64_t>(q.dh_items) + q.de_items, err, st))) return rc;
   }
-  if (!dh) return GPIPE_OK;
-  (void)launch_k(head_dh_kernel, (rows + 7) / 8, 256, 0, st, rows, d, static_cast<const float*>(dh32),
-                 static_cast<__nv_bfloat16*>(dh), lddh);
+  if (!dh || at.direct) return GPIPE_OK;
+  (void)launch_k(head_dh_kernel, up_to(rows, 8), 256, 0, st, rows, d, at.splits, at.rows_pad, inv_count,
+                 static_cast<const float*>(dh32), static_cast<__nv_bfloat16*>(dh), lddh);
   return check("dh");
 }
 
