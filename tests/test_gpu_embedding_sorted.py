@@ -101,10 +101,11 @@ def test_lookup_is_the_rounded_product(b, rows, d, vocab, ldx, f32):
 
 GRADS = [(1, 8, 1, "uniform"), (2, 8, 1, "one"), (19, 64, 517, "uniform"), (31, 64, 3, "uniform"), (32, 72, 1, "one"),
          (33, 72, 1, "one"), (64, 128, 2, "sorted"), (65, 2048, 2, "uniform"), (100, 264, 40, "padded"),
+         (255, 1024, 9, "text"), (256, 2056, 1, "one"), (257, 2056, 1, "one"), (264, 72, 33, "sorted"),
          (1000, 712, 50, "text"), (2048, 1024, 32000, "uniform"), (4097, 512, 300, "text"), (8192, 64, 1000, "text"),
          (8193, 64, 1000, "text"), (9001, 136, 511, "uniform"), (9001, 136, 512, "padded"), (10000, 64, 7, "one"),
          (20000, 256, 131072, "text"), (40000, 64, 262143, "backwards"), (70001, 72, 900, "sorted"),
-         (300000, 16, 50000, "text"), (9000, 24, 400000, "uniform")]
+         (16384, 1024, 40, "padded"), (16385, 1096, 40, "padded"), (300000, 16, 50000, "text"), (9000, 24, 400000, "uniform")]
 
 
 @gpu
@@ -150,7 +151,7 @@ def test_ids_out_of_range_are_flagged_and_left_out(b, rows):
 def test_rows_of_a_token_are_added_in_order(b):
     """2^24 + 1 - 2^24 in fp32 is 0 from the left, 1 from the right."""
     import torch
-    for rows in (3, 9000):
+    for rows in (3, 700, 9000):
         tokens = torch.full((rows,), -1, device="cuda", dtype=torch.int32)
         at = [0, rows // 2, rows - 1]
         tokens[at] = 2
