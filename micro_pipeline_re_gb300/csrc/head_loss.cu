@@ -71,7 +71,9 @@ __device__ __forceinline__ int head_target(const HeadArgs& a, int r, float& w, i
 }
 
 __device__ __forceinline__ float limit(float z, float c) {  // keeps NaN
-  return z > c ? c : (z < -c ? -c : z);
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n\tmin.NaN.f32 %0, %0, %3;" : "=&f"(y) : "f"(z), "f"(-c), "f"(c));
+  return y;
 }
 
 // ---------------------------------------------------------------------------
@@ -187,18 +189,43 @@ __device__ __forceinline__ uint32_t box_f32(int r, int u) {
 }
 __device__ __forceinline__ void wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
+// Arrival at a barrier of the pair without the release of earlier writes, which costs
+// about 1200 clocks at cluster scope: what is handed back is tensor memory whose loads
+// have completed.
+__device__ __forceinline__ void arrive_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// Bounded wait of one that has time: the hint lets the hardware put the warp aside for
+// up to 20 us a try, so that it does not poll beside the warps that issue copies and
+// products.  Gives up at once after any earlier give-up in the CTA.
 __device__ __forceinline__ bool head_wait(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
   if (*abort) return false;
-  if (mbar_wait_bounded(bar, parity, err, code)) return true;
-  *abort = 1;
-  return false;
+  const uint32_t at = smem_u32(bar);
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(at), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(err, code);
+      *abort = 1;
+      return false;
+    }
+  }
 }
 
 // (rho, s) += the 32 logits of v: a row's running reference and sum.
 __device__ __forceinline__ void add_chunk(const float* v, float& rho, float& s) {
-  float m = fmaxf(v[0], v[1]);
+  float m4[4];
 #pragma unroll
-  for (int j = 2; j < 32; j += 2) m = fmax3(m, v[j], v[j + 1]);
+  for (int j = 0; j < 4; ++j)
+    m4[j] = fmax3(fmax3(fmax3(v[j], v[j + 4], v[j + 8]), v[j + 12], v[j + 16]), v[j + 20], fmaxf(v[j + 24], v[j + 28]));
+  const float m = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
   const float to = fmaxf(rho, ceilf(m * kLog2e));
   if (to == -INFINITY) return;  // nothing but columns that are left out
   const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-to, -to);
@@ -258,7 +285,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   cluster_sync();  // both CTAs' barriers exist before any copy or arrival names them
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  griddep_wait();  // global memory from here on
+  // global memory from here on.  The gradient pass's products read only h and E, which no
+  // launch of this call writes and which were there before its first one began (the
+  // launches before this one let it start only after their own wait); its epilogue waits
+  // for what it reads, the rows, and for the readers of what it writes.
+  if (MODE != kGrad) griddep_wait();
 
   Walk<MODE> walk(pair, pairs);
   Item it;
@@ -330,33 +361,51 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     }
     griddep_launch();
   } else {
+    if (MODE == kGrad) griddep_wait();
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* boxes = smem + Cfg::kOffBox + (warp - 2) * 2 * Cfg::kBox;
     const uint32_t acce_leader = map_peer(smem_u32(acce), 0);
     int staged = 0;
-    for (int i = 0; walk.next(a, it); ++i) {
+    // what the epilogue knows of its row of a tile, read a tile ahead
+    auto row_of = [&](const Item& t) {
+      const int m = t.m0 + rank * 128 + q * 32 + lane;
+      HeadRow info = {0.f, 0.f, 0.f, -1};
+      if (MODE == kStats && m < a.row.rows) {
+        float w;
+        info.target = head_target(a.row, m, w, nullptr);
+      }
+      if (MODE == kGrad && m < a.row.rows) {
+        const float4 f = *reinterpret_cast<const float4*>(a.info + m);
+        info = HeadRow{f.x, f.y, f.z, __float_as_int(f.w)};
+      }
+      return info;
+    };
+    Item ahead;
+    bool more = walk.next(a, ahead);
+    HeadRow info_ahead = more ? row_of(ahead) : HeadRow{0.f, 0.f, 0.f, -1};
+    for (int i = 0; more; ++i) {
+      it = ahead;
+      const HeadRow info = info_ahead;
+      more = walk.next(a, ahead);
+      if (more) info_ahead = row_of(ahead);
       const int b = i & 1;
       const int mw = it.m0 + rank * 128 + q * 32, m = mw + lane;  // the warp's first row, the thread's
       const int c0 = it.n0 + half * 128;                          // the warp's first column
       const int width = MODE == kProducts ? a.row.d : a.cols;
       const int nch = max(0, min(4, (width - c0 + 31) / 32));
-      // what the epilogue knows of the row, read while the products run
-      int target = -1;
-      HeadRow info = {0.f, 0.f, 0.f, -1};
-      if (MODE == kStats && m < a.row.rows) {
-        float w;
-        target = head_target(a.row, m, w, nullptr);
-      }
-      if (MODE == kGrad && m < a.row.rows) {
-        const float4 f = *reinterpret_cast<const float4*>(a.info + m);
-        info = HeadRow{f.x, f.y, f.z, __float_as_int(f.w)};
-        target = info.target - a.v0;
-      }
+      const int target = info.target - (MODE == kGrad ? a.v0 : 0);
       head_wait(&accf[b], (i >> 1) & 1, err, DERR_ACC_WAIT, abort);
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + half * 128;
+      // the accumulator is free again once its last columns are in registers
+      auto drained = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_relaxed(acce_leader + static_cast<uint32_t>(b * sizeof(uint64_t)));
+      };
       uint32_t ra[32];
       if (nch > 0) tmem_ld32(tb, ra);
+      else drained();
       float rho = -INFINITY, sum = 0.f;
 #pragma unroll 1
       for (int c = 0; c < nch; ++c) {
@@ -365,6 +414,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ra[j]);
         if (c + 1 < nch) tmem_ld32(tb + (c + 1) * 32, ra);  // lands while this chunk is worked on
+        else drained();
         const int col = c0 + c * 32;
         const bool has_target = static_cast<unsigned>(target - col) < 32u;
         if (MODE == kStats) {
@@ -447,9 +497,6 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       }
       if (MODE == kStats && m < a.row.rows)
         a.parts[static_cast<int64_t>(m) * (2 * a.n_tiles) + (it.n0 / 128 + half)] = make_float2(rho, sum);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acce_leader + static_cast<uint32_t>(b * sizeof(uint64_t)));
     }
     griddep_launch();
     if (MODE != kStats && lane == 0) bulk_wait_read_all();
@@ -470,33 +517,17 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
                                                         const float2* __restrict__ parts, int nparts,
                                                         float* __restrict__ loss, HeadRow* __restrict__ info,
                                                         __nv_bfloat16* __restrict__ hm, int* err) {
-  griddep_wait();
   griddep_launch();
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= a.rows) return;
+  if (r >= a.rows) {
+    griddep_wait();
+    return;
+  }
+  // before the wait: the call's inputs and hm, which its other launches do not touch before
+  // this one has ended (launched by the stats kernel, which had waited itself)
   float w;
   const int t = head_target(a, r, w, lane == 0 ? err : nullptr);
-  const float2* mine = parts + static_cast<int64_t>(r) * nparts;
-  float rho = -INFINITY, s = 0.f, zt = 0.f;
-  if (t >= 0) {
-    for (int i = lane; i < nparts; i += 32) {
-      const float2 p = mine[i];
-      const float to = fmaxf(rho, p.x);
-      if (to > -INFINITY) s = s * exp2f(rho - to) + p.y * exp2f(p.x - to);
-      else s += p.y;  // nothing there, or NaN
-      rho = to;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float rho2 = __shfl_xor_sync(0xffffffffu, rho, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      const float to = fmaxf(rho, rho2);
-      // (a sum in a fixed order for both lanes of a pair, so that all agree)
-      const float x = lane & o ? s2 : s, y = lane & o ? s : s2;
-      const float rx = lane & o ? rho2 : rho, ry = lane & o ? rho : rho2;
-      s = to > -INFINITY ? x * exp2f(rx - to) + y * exp2f(ry - to) : x + y;
-      rho = to;
-    }
-  }
+  float zt = 0.f;
   for (int c = lane * 8; c < a.d; c += 256) {
     uint4 u = make_uint4(0, 0, 0, 0);
     if (t >= 0) {
@@ -509,12 +540,33 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
     }
     if (hm) *reinterpret_cast<uint4*>(hm + static_cast<int64_t>(r) * a.d + c) = u;
   }
+  griddep_wait();
   if (t < 0) {
     if (lane == 0) {
       loss[r] = 0.f;
       if (info) info[r] = HeadRow{0.f, 0.f, 0.f, -1};
     }
     return;
+  }
+  const float2* mine = parts + static_cast<int64_t>(r) * nparts;
+  float rho = -INFINITY, s = 0.f;
+#pragma unroll 4
+  for (int i = lane; i < nparts; i += 32) {
+    const float2 p = mine[i];
+    const float to = fmaxf(rho, p.x);
+    if (to > -INFINITY) s = s * exp2f(rho - to) + p.y * exp2f(p.x - to);
+    else s += p.y;  // nothing there, or NaN
+    rho = to;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float rho2 = __shfl_xor_sync(0xffffffffu, rho, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const float to = fmaxf(rho, rho2);
+    // (a sum in a fixed order for both lanes of a pair, so that all agree)
+    const float x = lane & o ? s2 : s, y = lane & o ? s : s2;
+    const float rx = lane & o ? rho2 : rho, ry = lane & o ? rho : rho2;
+    s = to > -INFINITY ? x * exp2f(rx - to) + y * exp2f(ry - to) : x + y;
+    rho = to;
   }
   zt = warp_sum(zt);
   if (lane != 0) return;
@@ -686,14 +738,16 @@ int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, int
   cfg.blockDim = dim3(kHeadThreads);
   cfg.dynamicSmemBytes = HeadCfg<MODE>::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   set_priority_attr(attr[1], s);
+  attr[2].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[2].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 3;
   HeadGemm b = a;
   if (MODE == kProducts)
     b.ahead = balance(a.dh_items, up_to(up_to(a.cols, kK), a.splits), a.de_items, up_to(a.row.rows, kK), pairs).ahead;
