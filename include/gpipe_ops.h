@@ -256,7 +256,7 @@ int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t
  * scratch   gpipe_op_head_loss_scratch_bytes (grads: 1 dh, 2 demb, 3 both), 256-byte
  *           aligned, written before it is read (calls that may overlap on the GPU,
  *           captured ones included, need one each, and outputs each).
- * 1 <= rows <= 2^24, 1 <= vocab <= 2^27 (and at most 2^30 tiles of 256 x 256),
+ * 1 <= rows <= 2^24, 1 <= vocab <= 2^27 (and at most 2^26 tiles of 256 x 256),
  * d <= 2^16 and the leading dimensions multiples of 8, 16-byte aligned bases.  Outputs and scratch may overlap neither each other nor an
  * input.  No atomics: results are bit-reproducible. */
 int gpipe_op_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, const void* emb_bf16, int seq,

@@ -8,10 +8,13 @@
 //
 // Launches:
 //   1  head_gemm_kernel<kStats>   z tile by tile in tensor memory; of every row and
-//                                 128 columns only (rho, sum 2^{z log2 e - rho}) leaves
+//                                 128 columns only (rho, sum 2^{z log2 e - rho}) leaves.
+//                                 With gradients, the first piece's powers go to where
+//                                 its g will be (fp16, a reference each 32 columns)
 //   2  head_rows_kernel           joins them, the loss, and what 3 needs of a row
 //   per piece of the vocabulary:
-//   3  head_gemm_kernel<kGrad>    z again, turned into g in the epilogue (bf16)
+//   3  head_scale_kernel          the first piece: g from the powers, in place
+//      head_gemm_kernel<kGrad>    the others: z again, turned into g in the epilogue
 //   4  head_gemm_kernel<kProducts>  both products of g, tiles of dh and of dE in one
 //                                 launch, so that one's last round fills the other's
 //   5  head_dh_kernel             sums of dh over pieces and parts of K into bf16
@@ -22,13 +25,16 @@
 // logit is a dot product of its own in fp32 (tensor cores truncate as they add: 1024
 // terms left z_t up to 2e-5 short, which showed in the loss; this way 1e-7).  So
 //   loss = log1p(sum_{v != t} e^{z_v - z_t}),  g_t = -w sum_{v != t} p_v
-// keep their digits where p_t is close to 1.  g is rounded to bf16, relative to
+// keep their digits where p_t is close to 1 (dh gets back what g_t loses to its rounding,
+// which would be an error of the whole row).  g is rounded to bf16, relative to
 // each value, as gpipe_op_cross_entropy rounds its dz; inv_count multiplies the
 // finished fp32 sums, so that g_t, close to -w for most rows, is close to a whole number
 // and its rounding does not add up over the rows.
 //
-// Cost: 8 rows vocab d flops with both gradients, where 6 would do if the logits were
-// kept.  Memory: 2 B an element of one piece of g.
+// Cost: 6 rows vocab d flops with both gradients for the first piece, 8 for the others.
+// Memory: 2 B an element of one piece of g, which is all that is ever held of the logits.
+// The powers are fp16 because it has three bits more than bf16, 2^-28 of the largest of 32
+// down (their reference puts that near 2^14): g's rounding to bf16 stays the only one that tells.
 #include <cuda.h>
 
 #include <algorithm>
@@ -70,6 +76,9 @@ __device__ __forceinline__ int head_target(const HeadArgs& a, int r, float& w, i
   return t >= 0 && t < a.vocab ? t : -1;
 }
 
+// What a number loses to its rounding to bf16.
+__device__ __forceinline__ float lost(float x) { return x - bf2f(f2bf(x)); }
+
 __device__ __forceinline__ float limit(float z, float c) {  // keeps NaN
   float y;
   asm("max.NaN.f32 %0, %1, %2;\n\tmin.NaN.f32 %0, %0, %3;" : "=&f"(y) : "f"(z), "f"(-c), "f"(c));
@@ -92,13 +101,14 @@ constexpr int kTile = 256;     // rows and columns of a pair's tile
 constexpr int kK = 64;         // a k-block
 constexpr int kHeadThreads = 320;
 constexpr int kGroup = 16;     // row tiles that the tiles in flight share
+constexpr int kKeepWidth = 768;  // d from which reading the first piece's powers is cheaper than making z again
 constexpr int kPlanPairs = 76; // pairs of SMs that the split of dh's K is planned for (any number runs it)
 
 template <Mode MODE>
 struct HeadCfg {
   static constexpr int kHalf = 128 * kK * 2;  // bytes of one operand of a CTA's stage
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kBox = MODE == kStats ? 0 : (MODE == kGrad ? 2048 : 4096);  // 32 x 32 elements leaving
+  static constexpr int kBox = MODE == kProducts ? 4096 : 2048;  // 32 x 32 elements leaving
   static constexpr int kStages = MODE == kProducts ? 5 : 6;
   static constexpr int kOffBox = kStages * kStage;
   static constexpr int kOffBar = kOffBox + 8 * 2 * kBox;
@@ -118,7 +128,10 @@ struct HeadGemm {
   int v0;                // its first
   int m_tiles, n_tiles;  // logits: rows x columns; products: dh's rows x d
   float2* parts;         // kStats: [rows][2 n_tiles]
-  const HeadRow* info;   // kGrad
+  int keep;              // kStats: columns whose powers go to g (fp16), with
+  float* refs;           //   their references, [rows][keep / 32]
+  const HeadRow* info;   // kGrad, and kProducts where its dh is final
+  const __nv_bfloat16* emb;
   // kProducts
   int splits, rows_pad;  // parts of dh's K, each with a buffer of rows_pad rows
   int dh_items, de_items, ahead, dh_out;
@@ -189,6 +202,19 @@ __device__ __forceinline__ uint32_t box_f32(int r, int u) {
 }
 __device__ __forceinline__ void wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t u) {
+  float2 f;
+  asm("{\n .reg .f16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.f32.f16 %0, lo;\n cvt.f32.f16 %1, hi;\n}\n"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(u));
+  return f;
+}
+
 // Arrival at a barrier of the pair without the release of earlier writes, which costs
 // about 1200 clocks at cluster scope: what is handed back is tensor memory whose loads
 // have completed.
@@ -196,50 +222,69 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-// Bounded wait of one that has time: the hint lets the hardware put the warp aside for
-// up to 20 us a try, so that it does not poll beside the warps that issue copies and
-// products.  Gives up at once after any earlier give-up in the CTA.
-__device__ __forceinline__ bool head_wait(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
-  if (*abort) return false;
-  const uint32_t at = smem_u32(bar);
-  const unsigned long long t0 = globaltimer_ns();
-  while (true) {
-    uint32_t ok;
+// Bounded wait; CLUSTER: for arrivals from the peer CTA, too.  The hint lets the hardware
+// put the warp aside for up to 20 us a try, so that it does not poll beside the others.
+// Gives up at once after any earlier give-up in the CTA.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool try_wait_long(uint32_t at, uint32_t parity) {
+  uint32_t ok;
+  if (CLUSTER)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(at), "r"(parity), "r"(20000u)
+        : "memory");
+  else
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
         : "r"(at), "r"(parity), "r"(20000u)
         : "memory");
-    if (ok) return true;
+  return ok != 0;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool head_wait(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort) {
+  const uint32_t at = smem_u32(bar);
+  if (try_wait_long<CLUSTER>(at, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!try_wait_long<CLUSTER>(at, parity)) {
+    if (*abort) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       atomicExch(err, code);
       *abort = 1;
       return false;
     }
   }
+  return true;
 }
 
-// (rho, s) += the 32 logits of v: a row's running reference and sum.
-__device__ __forceinline__ void add_chunk(const float* v, float& rho, float& s) {
+// (rho, s) += the 32 logits of v: a row's running reference and sum.  v becomes the
+// powers 2^{v log2 e - rho}, at most 2^14.
+__device__ __forceinline__ void add_chunk(float* v, float& rho, float& s) {
   float m4[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     m4[j] = fmax3(fmax3(fmax3(v[j], v[j + 4], v[j + 8]), v[j + 12], v[j + 16]), v[j + 20], fmaxf(v[j + 24], v[j + 28]));
   const float m = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-  const float to = fmaxf(rho, ceilf(m * kLog2e));
-  if (to == -INFINITY) return;  // nothing but columns that are left out
-  const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-to, -to);
+  const float to = fmaxf(rho, ceilf(m * kLog2e) - 14.f);
+  // (nothing but columns that are left out: powers of 0, whatever the reference)
+  const float at = to == -INFINITY ? 0.f : to;
+  const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-at, -at);
   f32x2 sum[4];
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
     float x, y;
     unpack2(fma2(pack2(v[j], v[j + 1]), l2, ref), x, y);
-    const f32x2 e = pack2(ex2_approx(x), ex2_approx(y));
+    v[j] = ex2_approx(x);
+    v[j + 1] = ex2_approx(y);
+    const f32x2 e = pack2(v[j], v[j + 1]);
     sum[(j >> 1) & 3] = j < 8 ? e : add2(sum[(j >> 1) & 3], e);
   }
   float x, y;
   unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
-  s = fmaf(s, ex2_approx(rho - to), x + y);
+  s = fmaf(s, ex2_approx(rho - at), x + y);
   rho = to;
 }
 
@@ -332,10 +377,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       int n = 0, i = 0;
       for (; walk.next(a, it); ++i) {
         const int b = i & 1;
-        if (*abort || !mbar_wait_bounded_cluster(&acce[b], ((i >> 1) & 1) ^ 1, err, DERR_MMA_WAIT)) {
-          *abort = 1;
-          break;
-        }
+        if (!head_wait<true>(&acce[b], ((i >> 1) & 1) ^ 1, err, DERR_MMA_WAIT, abort)) break;
         tc_fence_after();
         const bool a_mn = MODE == kProducts && it.de, b_mn = MODE == kProducts;
         const uint32_t idesc = a_mn ? mma_idesc_bf16(kTile, kTile, true, true)
@@ -374,7 +416,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         float w;
         info.target = head_target(a.row, m, w, nullptr);
       }
-      if (MODE == kGrad && m < a.row.rows) {
+      if ((MODE == kGrad || (MODE == kProducts && !t.de && a.dh_out == kDhBf16)) && m < a.row.rows) {
         const float4 f = *reinterpret_cast<const float4*>(a.info + m);
         info = HeadRow{f.x, f.y, f.z, __float_as_int(f.w)};
       }
@@ -394,6 +436,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       const int width = MODE == kProducts ? a.row.d : a.cols;
       const int nch = max(0, min(4, (width - c0 + 31) / 32));
       const int target = info.target - (MODE == kGrad ? a.v0 : 0);
+      const float rest = MODE == kProducts && info.target >= 0 ? lost(info.gt) : 0.f;
       head_wait(&accf[b], (i >> 1) & 1, err, DERR_ACC_WAIT, abort);
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + half * 128;
@@ -406,7 +449,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       uint32_t ra[32];
       if (nch > 0) tmem_ld32(tb, ra);
       else drained();
-      float rho = -INFINITY, sum = 0.f;
+      float rho = -INFINITY, sum = 0.f, refs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
       for (int c = 0; c < nch; ++c) {
         tmem_ld_wait32(ra);
@@ -418,9 +461,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         const int col = c0 + c * 32;
         const bool has_target = static_cast<unsigned>(target - col) < 32u;
         if (MODE == kStats) {
+          uint32_t cut = 0;  // columns beyond the limit
           if (a.row.clip > 0.f) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = limit(v[j], a.row.clip);
+            for (int j = 0; j < 32; ++j) {
+              cut |= fabsf(v[j]) > a.row.clip ? 1u << j : 0u;
+              v[j] = limit(v[j], a.row.clip);
+            }
           }
           if (col + 32 > width) {
 #pragma unroll
@@ -433,7 +480,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
               if (col + j == target) v[j] = -INFINITY;
           }
           add_chunk(v, rho, sum);
-          continue;
+          if (it.n0 >= a.keep) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j == c) refs[j] = rho;
+          if (cut) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = cut >> j & 1u ? 0.f : v[j];
+          }
         }
         if (MODE == kGrad) {
           const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-info.rho, -info.rho), sc = pack2(info.scale, info.scale);
@@ -458,6 +512,18 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
           }
         }
         if (MODE == kProducts) {
+          if (rest != 0.f) {  // what g_t lost to its rounding
+            const __nv_bfloat16* e = a.emb + static_cast<int64_t>(info.target) * a.row.d + col;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              if (col + j < width) {
+                float w[8];
+                load8(e + j, w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[j + k] = fmaf(rest, w[k], v[j + k]);
+              }
+            }
+          }
           const bool add_scale = it.de || a.dh_out == kDhBf16;
           const float al = add_scale ? a.row.inv_count : 1.f;
 #pragma unroll
@@ -468,7 +534,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         if (lane == 0) wait_read_1();
         __syncwarp();
         const bool f32 = MODE == kProducts && (it.de ? a.de_f32 : a.dh_out != kDhBf16);
-        if (f32) {
+        if (MODE == kStats) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(box + box_bf16(lane, u)) =
+                make_uint4(pack_f16x2(v[8 * u], v[8 * u + 1]), pack_f16x2(v[8 * u + 2], v[8 * u + 3]),
+                           pack_f16x2(v[8 * u + 4], v[8 * u + 5]), pack_f16x2(v[8 * u + 6], v[8 * u + 7]));
+        } else if (f32) {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
             *reinterpret_cast<float4*>(box + box_f32(lane, u)) =
@@ -481,7 +553,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if (!*abort) {
-            if (MODE == kGrad) {
+            if (MODE != kProducts) {
               tma_store_2d(&maps.c, col, mw, box);
             } else if (it.de) {
               if (a.de_f32) tma_reduce_add_2d(&maps.c2, col, a.v0 + mw, box);
@@ -495,11 +567,15 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
           bulk_commit();
         }
       }
-      if (MODE == kStats && m < a.row.rows)
+      if (MODE == kStats && m < a.row.rows) {
         a.parts[static_cast<int64_t>(m) * (2 * a.n_tiles) + (it.n0 / 128 + half)] = make_float2(rho, sum);
+        if (it.n0 < a.keep)
+          *reinterpret_cast<float4*>(a.refs + static_cast<int64_t>(m) * (a.keep / 32) + it.n0 / 32 + 4 * half) =
+              make_float4(refs[0], refs[1], refs[2], refs[3]);
+      }
     }
     griddep_launch();
-    if (MODE != kStats && lane == 0) bulk_wait_read_all();
+    if (lane == 0) bulk_wait_read_all();
   }
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the pair's products may read its shared memory
@@ -516,7 +592,7 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
                                                         const __nv_bfloat16* __restrict__ emb,
                                                         const float2* __restrict__ parts, int nparts,
                                                         float* __restrict__ loss, HeadRow* __restrict__ info,
-                                                        __nv_bfloat16* __restrict__ hm, int* err) {
+                                                        __nv_bfloat16* __restrict__ hm, int64_t ldm, int* err) {
   griddep_launch();
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= a.rows) {
@@ -538,7 +614,7 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
       zt += ((p0.x * e[0] + p0.y * e[1]) + (p1.x * e[2] + p1.y * e[3])) +
             ((p2.x * e[4] + p2.y * e[5]) + (p3.x * e[6] + p3.y * e[7]));
     }
-    if (hm) *reinterpret_cast<uint4*>(hm + static_cast<int64_t>(r) * a.d + c) = u;
+    if (hm) *reinterpret_cast<uint4*>(hm + r * ldm + c) = u;
   }
   griddep_wait();
   if (t < 0) {
@@ -588,19 +664,61 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
   info[r] = HeadRow{ref, w / total, cut ? 0.f : -w * others, t};
 }
 
-// dh = inv_count times the sum of its parts, a warp per row.
+// g of the first piece from the powers that the first pass left in its place: 16 elements
+// a thread, all of one reference.
+__global__ void __launch_bounds__(256) head_scale_kernel(int rows, int cols, int64_t ldg, int slabs,
+                                                         const HeadRow* __restrict__ info,
+                                                         const float* __restrict__ refs, int nrefs, uint4* g) {
+  griddep_wait();
+  griddep_launch();
+  const int r = blockIdx.x / slabs, c = (blockIdx.x % slabs * 256 + threadIdx.x) * 16;
+  if (c >= cols) return;
+  const float4 f = *reinterpret_cast<const float4*>(info + r);
+  const int target = __float_as_int(f.w);
+  const float ref = refs[static_cast<int64_t>(r) * nrefs + c / 32];
+  uint4* at = g + (r * ldg + c) / 8;
+  uint4 u[2] = {at[0], at[1]};
+  // (a reference of -inf: powers of 0)
+  const float k = ref == -INFINITY ? 0.f : f.y * exp2f(ref - f.x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float2 p = unpack_f16x2(w[j]);
+      p.x *= k;
+      p.y *= k;
+      const int col = c + 8 * i + 2 * j;
+      if (col == target) p.x = f.z;
+      if (col + 1 == target) p.y = f.z;
+      w[j] = target < 0 ? 0u : pack_bf16x2(p.x, p.y);  // no target: zeros, whatever the row holds
+    }
+    at[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// dh = inv_count times the sum of its parts and of what g_t lost to its rounding, a warp
+// per row.
 __global__ void __launch_bounds__(256) head_dh_kernel(int rows, int d, int splits, int rows_pad, float scale,
-                                                      const float* __restrict__ src, __nv_bfloat16* __restrict__ dh,
-                                                      int64_t lddh) {
+                                                      const float* __restrict__ src, const HeadRow* __restrict__ info,
+                                                      const __nv_bfloat16* __restrict__ emb,
+                                                      __nv_bfloat16* __restrict__ dh, int64_t lddh) {
   griddep_wait();
   griddep_launch();
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= rows) return;
+  const float4 f = *reinterpret_cast<const float4*>(info + r);
+  const int target = __float_as_int(f.w);
+  const float rest = target >= 0 ? lost(f.z) : 0.f;
+  const __nv_bfloat16* e = emb + static_cast<int64_t>(max(target, 0)) * d;
   for (int c = lane * 8; c < d; c += 256) {
-    float v[8];
+    float v[8], u[8];
+    load8(e + c, u);
     load8(src + static_cast<int64_t>(r) * d + c, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fmaf(rest, u[j], v[j]);
+#pragma unroll 4
     for (int p = 1; p < splits; ++p) {
-      float u[8];
       load8(src + (static_cast<int64_t>(p) * rows_pad + r) * d + c, u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += u[j];
@@ -625,7 +743,7 @@ int up_to(int n, int m) { return (n + m - 1) / m; }
 
 bool sizes_ok(int rows, int d, int vocab, int piece) {
   return rows >= 1 && rows <= (1 << 24) && d >= 8 && d <= (1 << 16) && d % 8 == 0 && vocab >= 1 &&
-         vocab <= (1 << 27) && piece >= 0 && static_cast<int64_t>(up_to(rows, kTile)) * up_to(vocab, kTile) <= (1 << 30);
+         vocab <= (1 << 27) && piece >= 0 && static_cast<int64_t>(up_to(rows, kTile)) * up_to(vocab, kTile) <= (1 << 26);
 }
 
 // Columns of a piece: a multiple of 256; 0 asks for as many as make g 256 MB.
@@ -672,9 +790,10 @@ int dh_splits(int rows, int d, int cols, bool demb) {
 }
 
 struct HeadScratch {
-  size_t parts, info, hm, g, dh, bytes;
-  int cols, splits, rows_pad;
+  size_t parts, info, hm, refs, g, dh, bytes;
+  int cols, splits, rows_pad, ldm;
   bool direct;  // dh comes out of the products as it is
+  bool keep;    // the first piece's powers are kept
 };
 HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads) {
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
@@ -684,10 +803,13 @@ HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads) {
   s.splits = grads & 1 ? dh_splits(rows, d, s.cols, grads & 2) : 1;
   s.rows_pad = up_to(rows, kTile) * kTile;
   s.direct = s.splits == 1 && s.cols >= vocab;
+  s.keep = grads && d >= kKeepWidth;
+  s.ldm = up_to(d, kK) * kK;  // copies of rows that start on 128 bytes: d = 712 is 20 % slower than 704 or 720
   s.parts = 0;
   s.info = up(n * 2 * up_to(vocab, kTile) * sizeof(float2));
   s.hm = s.info + (grads ? up(n * sizeof(HeadRow)) : 0);
-  s.g = s.hm + (grads & 2 ? up(n * d * 2) : 0);
+  s.refs = s.hm + (grads & 2 ? up(n * s.ldm * 2) : 0);
+  s.g = s.refs + (s.keep ? up(n * (s.cols / 32) * 4) : 0);
   s.dh = s.g + (grads ? up(n * s.cols * 2) : 0);
   s.bytes = s.dh + ((grads & 1) && !s.direct ? up(static_cast<size_t>(s.splits) * s.rows_pad * d * 4) : 0);
   return s;
@@ -772,7 +894,7 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   if (!sizes_ok(rows, d, vocab, piece))
     return set_error(GPIPE_ERR_INVALID_ARG,
                      "head_loss: need 1 <= rows <= 2^24, 8 <= d <= 2^16, d %% 8 == 0, 1 <= vocab <= 2^27, "
-                     "piece >= 0 and at most 2^30 tiles of 256 x 256");
+                     "piece >= 0 and at most 2^26 tiles of 256 x 256");
   if (demb && demb_dtype != DT_F32 && demb_dtype != DT_BF16)
     return set_error(GPIPE_ERR_UNSUPPORTED, "head_loss: demb_dtype must be 0 or 1");
   if (seq < 1 || row0 < 0 || static_cast<int64_t>(row0) + rows >= INT32_MAX)
@@ -825,15 +947,21 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   q.n_tiles = up_to(vocab, kTile);
   q.parts = parts;
   q.info = info;
+  q.emb = e;
   CUtensorMap map_h;
   bool ok = head_map(&map_h, h, false, d, rows, ldh, kK, 128) && head_map(&maps.b, emb, false, d, vocab, d, kK, 128);
+  if (ok && at.keep) {
+    q.keep = at.cols;
+    q.refs = reinterpret_cast<float*>(w + at.refs);
+    ok = head_map(&maps.c, g, false, std::min(at.cols, vocab), rows, at.cols, 32, 32);
+  }
   if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
   maps.a = map_h;
   int rc = launch_head_gemm<kStats>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st);
   if (rc) return rc;
   (void)launch_k(head_rows_kernel, up_to(rows, 8), 256, 0, st, a, static_cast<const __nv_bfloat16*>(h), ldh, e,
                  static_cast<const float2*>(parts), 2 * q.n_tiles, loss_rows, grads ? info : nullptr,
-                 demb ? hm : nullptr, err);
+                 demb ? hm : nullptr, static_cast<int64_t>(at.ldm), err);
   if ((rc = check("rows"))) return rc;
   for (int v0 = 0; grads && v0 < vocab; v0 += at.cols) {
     const int cols = std::min(at.cols, vocab - v0);
@@ -841,11 +969,19 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
     q.cols = cols;
     q.v0 = v0;
     q.n_tiles = up_to(cols, kTile);
-    maps.a = map_h;
-    ok = head_map(&maps.b, piece_of_e, false, d, cols, d, kK, 128) &&
-         head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
-    if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
-    if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st))) return rc;
+    if (v0 == 0 && at.keep) {
+      const int slabs = up_to(cols, 16 * 256);
+      (void)launch_k(head_scale_kernel, rows * slabs, 256, 0, st, rows, cols, static_cast<int64_t>(at.cols), slabs,
+                     static_cast<const HeadRow*>(info), static_cast<const float*>(q.refs), at.cols / 32,
+                     reinterpret_cast<uint4*>(g));
+      if ((rc = check("scale"))) return rc;
+    } else {
+      maps.a = map_h;
+      ok = head_map(&maps.b, piece_of_e, false, d, cols, d, kK, 128) &&
+           head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
+      if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
+      if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st))) return rc;
+    }
     q.n_tiles = up_to(d, kTile);
     q.splits = std::min(at.splits, up_to(cols, kK));
     q.rows_pad = at.rows_pad;
@@ -861,14 +997,15 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
     }
     if (ok && demb)
       ok = head_map(&maps.a2, g, false, cols, rows, at.cols, kK, kK) &&
-           head_map(&maps.b2, hm, false, d, rows, d, kK, kK) &&
+           head_map(&maps.b2, hm, false, d, rows, at.ldm, kK, kK) &&
            head_map(&maps.c2, demb, q.de_f32, d, vocab, d, 32, 32);
     if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
     if ((rc = launch_head_gemm<kProducts>(maps, q, static_cast<int64_t>(q.dh_items) + q.de_items, err, st))) return rc;
   }
   if (!dh || at.direct) return GPIPE_OK;
   (void)launch_k(head_dh_kernel, up_to(rows, 8), 256, 0, st, rows, d, at.splits, at.rows_pad, inv_count,
-                 static_cast<const float*>(dh32), static_cast<__nv_bfloat16*>(dh), lddh);
+                 static_cast<const float*>(dh32), static_cast<const HeadRow*>(info), e, static_cast<__nv_bfloat16*>(dh),
+                 lddh);
   return check("dh");
 }
 

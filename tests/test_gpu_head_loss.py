@@ -7,7 +7,9 @@ Tolerances are worst-case bounds, counted in roundings (u = 2^-24 for fp32):
          z_t and the largest z are dz off each, the exponentials 2^-22 and the argument's
          rounding (d <= 128 in size where it matters: 2^-24 * 128 * 1.5 < 2^-16, weighted by
          e^-128; 2^-20 covers the maximum of x e^-x), the sums an addition each
-  g      2^-8 of its value for bf16 (half a step: finfo.eps / 2 = 2^-7 / 2), and e_p = 2 (2 dz + e_s) p for p
+  g      2^-8 of its value for bf16 (half a step: finfo.eps / 2 = 2^-7 / 2), and e_p = (2 (2 dz + e_s) + 2^-11) p +
+         2^-38 for p, which passes through fp16 (2^-11; below 2^-28 of the largest of its 32
+         neighbours, at most 1, steps of 2^-38)
   dh     sum_v |g_v| |E_v| (2^-8 + 2^-10) + e_p sum_v w p_v |E_v|, and 2^-8 of the result
   demb   the same over the rows; 2^-8 of the result as bf16
 (2^-10 covers the products' own additions: 2 u times up to 2^13 terms.)"""
@@ -102,7 +104,7 @@ def exact(p, clip=0.0, inv=None, row0=0):
     gr = pr.clone()
     gr.scatter_add_(1, t[:, None], -torch.ones_like(zt))
     gr *= w[:, None] * inside
-    e_p = (2 * (2 * dz + e_s)) * pr * w[:, None].abs() * inside
+    e_p = ((2 * (2 * dz + e_s) + 2.0 ** -11) * pr + 2.0 ** -38) * w[:, None].abs() * inside
     slack = gr.abs() * (2.0 ** -8 + 2.0 ** -10) + e_p
     a = abs(inv)
     dh, demb = inv * (gr @ e), inv * (gr.T @ h)
