@@ -10,7 +10,8 @@
 //   1  head_gemm_kernel<kStats>   z tile by tile in tensor memory; of every row and
 //                                 128 columns only (rho, sum 2^{z log2 e - rho}) leaves.
 //                                 With gradients, the first piece's powers go to where
-//                                 its g will be (fp16, a reference each 32 columns)
+//                                 its g will be (fp16).  Up to 64 rows without gradients:
+//      head_gemm_kernel<kFew>     the same with the vocabulary as the products' rows
 //   2  head_rows_kernel           joins them, the loss, and what 3 needs of a row
 //   per piece of the vocabulary:
 //   3  head_scale_kernel          the first piece: g from the powers, in place
@@ -33,12 +34,13 @@
 //
 // Cost: 6 rows vocab d flops with both gradients for the first piece, 8 for the others.
 // Memory: 2 B an element of one piece of g, which is all that is ever held of the logits.
-// The powers are fp16 because it has three bits more than bf16, 2^-28 of the largest of 32
-// down (their reference puts that near 2^14): g's rounding to bf16 stays the only one that tells.
+// The powers are fp16 because it has three bits more than bf16, 2^-28 of the largest of
+// 128 down (their reference puts that near 2^14): g's rounding to bf16 stays the only one that tells.
 #include <cuda.h>
 
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "../../include/gpipe.h"
 #include "attention_tiles.cuh"
@@ -94,26 +96,31 @@ __device__ __forceinline__ float limit(float z, float c) {  // keeps NaN
 //   warps 2..9        epilogue, each on its own: 32 rows, 128 columns, 32 at a time
 // (the organisation of the library's persistent GEMM on SM pairs).
 // ---------------------------------------------------------------------------
-enum Mode { kStats, kGrad, kProducts };
+enum Mode { kStats, kFew, kGrad, kProducts };
 enum DhOut { kDhStore, kDhAdd, kDhBf16 };  // fp32, fp32 added, bf16 and final
 
 constexpr int kTile = 256;     // rows and columns of a pair's tile
+constexpr int kFewRows = 64;   // kFew: rows of h, its columns
 constexpr int kK = 64;         // a k-block
 constexpr int kHeadThreads = 320;
 constexpr int kGroup = 16;     // row tiles that the tiles in flight share
 constexpr int kKeepWidth = 768;  // d from which reading the first piece's powers is cheaper than making z again
+constexpr int kWideRows = 1216;  // rows up to which each has a CTA to join its sums (eight an SM)
 constexpr int kPlanPairs = 76; // pairs of SMs that the split of dh's K is planned for (any number runs it)
 
 template <Mode MODE>
 struct HeadCfg {
-  static constexpr int kHalf = 128 * kK * 2;  // bytes of one operand of a CTA's stage
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kBox = MODE == kProducts ? 4096 : 2048;  // 32 x 32 elements leaving
-  static constexpr int kStages = MODE == kProducts ? 5 : 6;
+  static constexpr int kColumns = MODE == kFew ? kFewRows : kTile;  // of a pair's tile
+  static constexpr int kA = 128 * kK * 2;                           // bytes of the operands of a CTA's stage
+  static constexpr int kB = kColumns / 2 * kK * 2;
+  static constexpr int kStage = kA + kB;
+  // 32 x 32 elements leaving (kFew: being turned round)
+  static constexpr int kBox = MODE == kProducts ? 4096 : (MODE == kFew ? 32 * 33 * 2 : 2048);
+  static constexpr int kStages = MODE == kProducts ? 5 : (MODE == kFew ? 9 : 6);
   static constexpr int kOffBox = kStages * kStage;
   static constexpr int kOffBar = kOffBox + 8 * 2 * kBox;
   static constexpr int kSmem = 1024 + kOffBar + 512;
-  static_assert(kSmem <= 232448, "over the shared memory of a CTA");
+  static_assert(kOffBar % 8 == 0 && kSmem <= 232448, "over the shared memory of a CTA");
 };
 
 struct HeadMaps {
@@ -128,8 +135,7 @@ struct HeadGemm {
   int v0;                // its first
   int m_tiles, n_tiles;  // logits: rows x columns; products: dh's rows x d
   float2* parts;         // kStats: [rows][2 n_tiles]
-  int keep;              // kStats: columns whose powers go to g (fp16), with
-  float* refs;           //   their references, [rows][keep / 32]
+  int keep;              // kStats: columns whose powers go to g (fp16)
   const HeadRow* info;   // kGrad, and kProducts where its dh is final
   const __nv_bfloat16* emb;
   // kProducts
@@ -260,32 +266,35 @@ __device__ __forceinline__ bool head_wait(uint64_t* bar, uint32_t parity, int* e
   return true;
 }
 
-// (rho, s) += the 32 logits of v: a row's running reference and sum.  v becomes the
-// powers 2^{v log2 e - rho}, at most 2^14.
-__device__ __forceinline__ void add_chunk(float* v, float& rho, float& s) {
-  float m4[4];
+// N logits v of a row become the powers 2^{v log2 e - rho}, at most 2^14; their sum.
+template <int N>
+__device__ __forceinline__ float to_powers(float* v, float& rho) {
+  float m8[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    m4[j] = fmax3(fmax3(fmax3(v[j], v[j + 4], v[j + 8]), v[j + 12], v[j + 16]), v[j + 20], fmaxf(v[j + 24], v[j + 28]));
-  const float m = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-  const float to = fmaxf(rho, ceilf(m * kLog2e) - 14.f);
-  // (nothing but columns that are left out: powers of 0, whatever the reference)
-  const float at = to == -INFINITY ? 0.f : to;
+  for (int j = 0; j < 8; ++j) {
+    m8[j] = fmaxf(v[j], v[j + 8]);
+#pragma unroll
+    for (int k = 16; k < N; k += 16) m8[j] = fmax3(m8[j], v[j + k], v[j + k + 8]);
+  }
+  const float m = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+  rho = ceilf(m * kLog2e) - 14.f;
+  // (-inf: nothing but columns that are left out, powers of 0 whatever the reference)
+  const float at = rho == -INFINITY ? 0.f : rho;
   const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-at, -at);
-  f32x2 sum[4];
+  f32x2 sum[8];
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
+  for (int j = 0; j < N; j += 2) {
     float x, y;
     unpack2(fma2(pack2(v[j], v[j + 1]), l2, ref), x, y);
     v[j] = ex2_approx(x);
     v[j + 1] = ex2_approx(y);
     const f32x2 e = pack2(v[j], v[j + 1]);
-    sum[(j >> 1) & 3] = j < 8 ? e : add2(sum[(j >> 1) & 3], e);
+    sum[(j >> 1) & 7] = j < 16 ? e : add2(sum[(j >> 1) & 7], e);
   }
   float x, y;
-  unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
-  s = fmaf(s, ex2_approx(rho - at), x + y);
-  rho = to;
+  unpack2(add2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), add2(add2(sum[4], sum[5]), add2(sum[6], sum[7]))), x,
+          y);
+  return x + y;
 }
 
 template <Mode MODE>
@@ -342,12 +351,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     if (lane == 0) {
       int n = 0;
       while (!*abort && walk.next(a, it)) {
-        const int am = it.m0 + rank * 128, bn = it.n0 + rank * 128;
+        const int am = it.m0 + rank * 128, bn = it.n0 + rank * (Cfg::kColumns / 2);
         for (int kb = 0; kb < it.nk; ++kb, ++n) {
           const int s = n % STAGES;
           if (!head_wait(&empty[s], ((n / STAGES) & 1) ^ 1, err, DERR_TMA_WAIT, abort)) break;
           uint8_t* sa = smem + s * Cfg::kStage;
-          uint8_t* sb = sa + Cfg::kHalf;
+          uint8_t* sb = sa + Cfg::kA;
           const int k = (it.k0 + kb) * kK;
           const uint32_t fb = map_peer(smem_u32(&full[s]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Cfg::kStage);
@@ -381,13 +390,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         tc_fence_after();
         const bool a_mn = MODE == kProducts && it.de, b_mn = MODE == kProducts;
         const uint32_t idesc = a_mn ? mma_idesc_bf16(kTile, kTile, true, true)
-                                    : mma_idesc_bf16(kTile, kTile, false, MODE == kProducts);
+                                    : mma_idesc_bf16(kTile, Cfg::kColumns, false, MODE == kProducts);
         const uint32_t acc = tmem + b * kTile;
         for (int kb = 0; kb < it.nk; ++kb, ++n) {
           const int s = n % STAGES;
           if (!head_wait(&full[s], (n / STAGES) & 1, err, DERR_MMA_WAIT, abort)) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * Cfg::kStage), sb = sa + Cfg::kHalf;
+          const uint32_t sa = smem_u32(smem + s * Cfg::kStage), sb = sa + Cfg::kA;
 #pragma unroll
           for (int kk = 0; kk < kK / 16; ++kk) {
             const uint64_t ad = a_mn ? sw128_desc(sa + kk * 2048, 8192, 1024) : sw128_desc(sa + kk * 32, 16, 1024);
@@ -410,9 +419,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     int staged = 0;
     // what the epilogue knows of its row of a tile, read a tile ahead
     auto row_of = [&](const Item& t) {
-      const int m = t.m0 + rank * 128 + q * 32 + lane;
+      const int m = MODE == kFew ? t.n0 + half * 32 + lane : t.m0 + rank * 128 + q * 32 + lane;
       HeadRow info = {0.f, 0.f, 0.f, -1};
-      if (MODE == kStats && m < a.row.rows) {
+      if ((MODE == kStats || MODE == kFew) && m < a.row.rows) {
         float w;
         info.target = head_target(a.row, m, w, nullptr);
       }
@@ -434,89 +443,121 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       const int mw = it.m0 + rank * 128 + q * 32, m = mw + lane;  // the warp's first row, the thread's
       const int c0 = it.n0 + half * 128;                          // the warp's first column
       const int width = MODE == kProducts ? a.row.d : a.cols;
-      const int nch = max(0, min(4, (width - c0 + 31) / 32));
       const int target = info.target - (MODE == kGrad ? a.v0 : 0);
       const float rest = MODE == kProducts && info.target >= 0 ? lost(info.gt) : 0.f;
       head_wait(&accf[b], (i >> 1) & 1, err, DERR_ACC_WAIT, abort);
       tc_fence_after();
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + half * 128;
-      // the accumulator is free again once its last columns are in registers
-      auto drained = [&] {
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + half * (Cfg::kColumns / 2);
+      auto drained = [&] {  // the accumulator is free again
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_relaxed(acce_leader + static_cast<uint32_t>(b * sizeof(uint64_t)));
       };
-      uint32_t ra[32];
-      if (nch > 0) tmem_ld32(tb, ra);
-      else drained();
-      float rho = -INFINITY, sum = 0.f, refs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int c = 0; c < nch; ++c) {
+      if constexpr (MODE == kFew) {
+        // the thread has 32 rows of h at one column of the vocabulary, and wants it the other way round
+        uint32_t ra[32];
+        tmem_ld32(tb, ra);
         tmem_ld_wait32(ra);
+        drained();
+        float* box = reinterpret_cast<float*>(boxes);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) box[j * 33 + lane] = __uint_as_float(ra[j]);
+        __syncwarp();
         float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ra[j]);
-        if (c + 1 < nch) tmem_ld32(tb + (c + 1) * 32, ra);  // lands while this chunk is worked on
-        else drained();
-        const int col = c0 + c * 32;
-        const bool has_target = static_cast<unsigned>(target - col) < 32u;
-        if (MODE == kStats) {
-          uint32_t cut = 0;  // columns beyond the limit
-          if (a.row.clip > 0.f) {
+        for (int j = 0; j < 32; ++j) v[j] = box[lane * 33 + j];
+        __syncwarp();
+        const bool clip = a.row.clip > 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              cut |= fabsf(v[j]) > a.row.clip ? 1u << j : 0u;
+        for (int j = 0; j < 32; ++j) {
+          if (clip) v[j] = limit(v[j], a.row.clip);
+          if (mw + j >= a.row.vocab || mw + j == info.target) v[j] = -INFINITY;
+        }
+        float rho;
+        const float sum = to_powers<32>(v, rho);
+        const int r = it.n0 + half * 32 + lane;
+        if (r < a.row.rows)
+          a.parts[static_cast<int64_t>(r) * (8 * a.m_tiles) + (mw / 32)] = make_float2(rho, sum);
+      } else {
+        // all of the warp's columns at once: a load's latency is some 500 clocks, and one after
+        // the other they were two thirds of the epilogue
+        uint32_t ra[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tb + c * 32, ra + c * 32);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait32(ra + c * 32);
+        drained();
+        float v[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) v[j] = __uint_as_float(ra[j]);
+        const bool edge = c0 + 128 > width;
+        const bool has_target = static_cast<unsigned>(target - c0) < 128u;
+        if (MODE == kStats) {
+          float rho;
+          const bool kept = it.n0 < a.keep;
+          uint32_t cut[4] = {0, 0, 0, 0};  // columns beyond the limit
+          if (a.row.clip > 0.f) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 128; ++j) {
+              if (kept) cut[j >> 5] |= fabsf(v[j]) > a.row.clip ? 1u << (j & 31) : 0u;
               v[j] = limit(v[j], a.row.clip);
             }
           }
-          if (col + 32 > width) {
+          if (edge) {
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col + j >= width) v[j] = -INFINITY;
+            for (int j = 0; j < 128; ++j)
+              if (c0 + j >= width) v[j] = -INFINITY;
           }
           if (__any_sync(0xffffffffu, has_target)) {
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col + j == target) v[j] = -INFINITY;
+            for (int j = 0; j < 128; ++j)
+              if (c0 + j == target) v[j] = -INFINITY;
           }
-          add_chunk(v, rho, sum);
-          if (it.n0 >= a.keep) continue;
+          const float sum = to_powers<128>(v, rho);
+          if (m < a.row.rows)
+            a.parts[static_cast<int64_t>(m) * (2 * a.n_tiles) + (it.n0 / 128 + half)] = make_float2(rho, sum);
+          if (!kept) continue;
+          if (a.row.clip > 0.f) {
+            __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j == c) refs[j] = rho;
-          if (cut) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = cut >> j & 1u ? 0.f : v[j];
+            for (int j = 0; j < 128; ++j) v[j] = cut[j >> 5] >> (j & 31) & 1u ? 0.f : v[j];
           }
         }
         if (MODE == kGrad) {
           const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-info.rho, -info.rho), sc = pack2(info.scale, info.scale);
           if (a.row.clip > 0.f) {  // columns beyond the limit: marked, so that they come out as 0
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fabsf(v[j]) > a.row.clip ? -INFINITY : v[j];
+            for (int j = 0; j < 128; ++j) v[j] = fabsf(v[j]) > a.row.clip ? -INFINITY : v[j];
           }
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
+          for (int j = 0; j < 128; j += 2) {
             float x, y;
             unpack2(fma2(pack2(v[j], v[j + 1]), l2, ref), x, y);
             unpack2(mul2(pack2(ex2_approx(x), ex2_approx(y)), sc), v[j], v[j + 1]);
           }
           if (__any_sync(0xffffffffu, has_target)) {
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col + j == target) v[j] = info.gt;
+            for (int j = 0; j < 128; ++j)
+              if (c0 + j == target) v[j] = info.gt;
           }
-          if (info.target < 0) {  // whatever the row holds
+          if (__any_sync(0xffffffffu, info.target < 0)) {  // zeros, whatever the row holds
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            for (int j = 0; j < 128; ++j) v[j] = info.target < 0 ? 0.f : v[j];
           }
         }
         if (MODE == kProducts) {
-          if (rest != 0.f) {  // what g_t lost to its rounding
-            const __nv_bfloat16* e = a.emb + static_cast<int64_t>(info.target) * a.row.d + col;
+          if (__any_sync(0xffffffffu, rest != 0.f)) {  // what g_t lost to its rounding
+            __syncwarp();
+            const __nv_bfloat16* e = a.emb + static_cast<int64_t>(max(info.target, 0)) * a.row.d + c0;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              if (col + j < width) {
+            for (int j = 0; j < 128; j += 8) {
+              if (c0 + j < width) {
                 float w[8];
                 load8(e + j, w);
 #pragma unroll
@@ -524,54 +565,53 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
               }
             }
           }
-          const bool add_scale = it.de || a.dh_out == kDhBf16;
-          const float al = add_scale ? a.row.inv_count : 1.f;
+          const float al = it.de || a.dh_out == kDhBf16 ? a.row.inv_count : 1.f;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= al;
+          for (int j = 0; j < 128; ++j) v[j] *= al;
         }
-        // the chunk leaves through one of the warp's two boxes
-        uint8_t* box = boxes + (staged++ & 1) * Cfg::kBox;
-        if (lane == 0) wait_read_1();
-        __syncwarp();
+        // out, 32 columns at a time, through the warp's two boxes
         const bool f32 = MODE == kProducts && (it.de ? a.de_f32 : a.dh_out != kDhBf16);
-        if (MODE == kStats) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<uint4*>(box + box_bf16(lane, u)) =
-                make_uint4(pack_f16x2(v[8 * u], v[8 * u + 1]), pack_f16x2(v[8 * u + 2], v[8 * u + 3]),
-                           pack_f16x2(v[8 * u + 4], v[8 * u + 5]), pack_f16x2(v[8 * u + 6], v[8 * u + 7]));
-        } else if (f32) {
+        for (int c = 0; c < 4; ++c) {
+          const int col = c0 + c * 32;
+          if (col >= width) break;
+          uint8_t* box = boxes + (staged++ & 1) * Cfg::kBox;
+          if (lane == 0) wait_read_1();
+          __syncwarp();
+          const float* o = v + c * 32;
+          if (f32) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<float4*>(box + box_f32(lane, u)) =
-                make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-        } else {
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<float4*>(box + box_f32(lane, u)) =
+                  make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          } else if (MODE == kStats) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) store8(reinterpret_cast<__nv_bfloat16*>(box + box_bf16(lane, u)), v + 8 * u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (!*abort) {
-            if (MODE != kProducts) {
-              tma_store_2d(&maps.c, col, mw, box);
-            } else if (it.de) {
-              if (a.de_f32) tma_reduce_add_2d(&maps.c2, col, a.v0 + mw, box);
-              else tma_store_2d(&maps.c2, col, a.v0 + mw, box);
-            } else {
-              const int y = it.split * a.rows_pad + mw;
-              if (a.dh_out == kDhAdd) tma_reduce_add_2d(&maps.c, col, y, box);
-              else tma_store_2d(&maps.c, col, y, box);
-            }
+            for (int u = 0; u < 4; ++u)
+              *reinterpret_cast<uint4*>(box + box_bf16(lane, u)) =
+                  make_uint4(pack_f16x2(o[8 * u], o[8 * u + 1]), pack_f16x2(o[8 * u + 2], o[8 * u + 3]),
+                             pack_f16x2(o[8 * u + 4], o[8 * u + 5]), pack_f16x2(o[8 * u + 6], o[8 * u + 7]));
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) store8(reinterpret_cast<__nv_bfloat16*>(box + box_bf16(lane, u)), o + 8 * u);
           }
-          bulk_commit();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (!*abort) {
+              if (MODE != kProducts) {
+                tma_store_2d(&maps.c, col, mw, box);
+              } else if (it.de) {
+                if (a.de_f32) tma_reduce_add_2d(&maps.c2, col, a.v0 + mw, box);
+                else tma_store_2d(&maps.c2, col, a.v0 + mw, box);
+              } else {
+                const int y = it.split * a.rows_pad + mw;
+                if (a.dh_out == kDhAdd) tma_reduce_add_2d(&maps.c, col, y, box);
+                else tma_store_2d(&maps.c, col, y, box);
+              }
+            }
+            bulk_commit();
+          }
         }
-      }
-      if (MODE == kStats && m < a.row.rows) {
-        a.parts[static_cast<int64_t>(m) * (2 * a.n_tiles) + (it.n0 / 128 + half)] = make_float2(rho, sum);
-        if (it.n0 < a.keep)
-          *reinterpret_cast<float4*>(a.refs + static_cast<int64_t>(m) * (a.keep / 32) + it.n0 / 32 + 4 * half) =
-              make_float4(refs[0], refs[1], refs[2], refs[3]);
       }
     }
     griddep_launch();
@@ -585,16 +625,21 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   }
 }
 
-// A warp per row: joins the row's sums, takes the target's logit as a dot product, the
+// W warps per row: they join the row's sums, take the target's logit as a dot product, the
 // loss, what the gradient pass needs, and (hm not NULL) h with the rows that count for
 // nothing set to zero.
+template <int W>
 __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_bfloat16* __restrict__ h, int64_t ldh,
                                                         const __nv_bfloat16* __restrict__ emb,
                                                         const float2* __restrict__ parts, int nparts,
                                                         float* __restrict__ loss, HeadRow* __restrict__ info,
                                                         __nv_bfloat16* __restrict__ hm, int64_t ldm, int* err) {
+  static_assert(W == 1 || W == 8, "a warp or the CTA");
   griddep_launch();
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  __shared__ float shared[3][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = W == 1 ? blockIdx.x * 8 + warp : blockIdx.x;
+  const int at = W == 1 ? lane : threadIdx.x;
   if (r >= a.rows) {
     griddep_wait();
     return;
@@ -602,9 +647,9 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
   // before the wait: the call's inputs and hm, which its other launches do not touch before
   // this one has ended (launched by the stats kernel, which had waited itself)
   float w;
-  const int t = head_target(a, r, w, lane == 0 ? err : nullptr);
+  const int t = head_target(a, r, w, at == 0 ? err : nullptr);
   float zt = 0.f;
-  for (int c = lane * 8; c < a.d; c += 256) {
+  for (int c = at * 8; c < a.d; c += 256 * W) {
     uint4 u = make_uint4(0, 0, 0, 0);
     if (t >= 0) {
       u = *reinterpret_cast<const uint4*>(h + r * ldh + c);
@@ -616,9 +661,10 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
     }
     if (hm) *reinterpret_cast<uint4*>(hm + r * ldm + c) = u;
   }
+  zt = warp_sum(zt);
   griddep_wait();
   if (t < 0) {
-    if (lane == 0) {
+    if (at == 0) {
       loss[r] = 0.f;
       if (info) info[r] = HeadRow{0.f, 0.f, 0.f, -1};
     }
@@ -627,24 +673,37 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
   const float2* mine = parts + static_cast<int64_t>(r) * nparts;
   float rho = -INFINITY, s = 0.f;
 #pragma unroll 4
-  for (int i = lane; i < nparts; i += 32) {
+  for (int i = at; i < nparts; i += 32 * W) {
     const float2 p = mine[i];
     const float to = fmaxf(rho, p.x);
     if (to > -INFINITY) s = s * exp2f(rho - to) + p.y * exp2f(p.x - to);
     else s += p.y;  // nothing there, or NaN
     rho = to;
   }
+  auto join = [&](float rx, float x, float ry, float y) {
+    const float to = fmaxf(rx, ry);
+    s = to > -INFINITY ? x * exp2f(rx - to) + y * exp2f(ry - to) : x + y;
+    rho = to;
+  };
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float rho2 = __shfl_xor_sync(0xffffffffu, rho, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    const float to = fmaxf(rho, rho2);
-    // (a sum in a fixed order for both lanes of a pair, so that all agree)
-    const float x = lane & o ? s2 : s, y = lane & o ? s : s2;
-    const float rx = lane & o ? rho2 : rho, ry = lane & o ? rho : rho2;
-    s = to > -INFINITY ? x * exp2f(rx - to) + y * exp2f(ry - to) : x + y;
-    rho = to;
+    if (lane & o) join(rho2, s2, rho, s);  // (in a fixed order for both lanes of a pair, so that all agree)
+    else join(rho, s, rho2, s2);
   }
-  zt = warp_sum(zt);
+  if (W > 1) {
+    if (lane == 0) {
+      shared[0][warp] = rho;
+      shared[1][warp] = s;
+      shared[2][warp] = zt;
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int i = 1; i < W; ++i) {
+      join(rho, s, shared[0][i], shared[1][i]);
+      zt += shared[2][i];
+    }
+  }
   if (lane != 0) return;
   bool cut = false;
   if (a.clip > 0.f) {
@@ -666,16 +725,16 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
 
 // g of the first piece from the powers that the first pass left in its place: 16 elements
 // a thread, all of one reference.
-__global__ void __launch_bounds__(256) head_scale_kernel(int rows, int cols, int64_t ldg, int slabs,
+__global__ void __launch_bounds__(256) head_scale_kernel(int cols, int64_t ldg, int slabs,
                                                          const HeadRow* __restrict__ info,
-                                                         const float* __restrict__ refs, int nrefs, uint4* g) {
+                                                         const float2* __restrict__ parts, int nparts, uint4* g) {
   griddep_wait();
   griddep_launch();
   const int r = blockIdx.x / slabs, c = (blockIdx.x % slabs * 256 + threadIdx.x) * 16;
   if (c >= cols) return;
   const float4 f = *reinterpret_cast<const float4*>(info + r);
   const int target = __float_as_int(f.w);
-  const float ref = refs[static_cast<int64_t>(r) * nrefs + c / 32];
+  const float ref = parts[static_cast<int64_t>(r) * nparts + c / 128].x;
   uint4* at = g + (r * ldg + c) / 8;
   uint4 u[2] = {at[0], at[1]};
   // (a reference of -inf: powers of 0)
@@ -790,7 +849,7 @@ int dh_splits(int rows, int d, int cols, bool demb) {
 }
 
 struct HeadScratch {
-  size_t parts, info, hm, refs, g, dh, bytes;
+  size_t parts, info, hm, g, dh, bytes;
   int cols, splits, rows_pad, ldm;
   bool direct;  // dh comes out of the products as it is
   bool keep;    // the first piece's powers are kept
@@ -803,13 +862,13 @@ HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads) {
   s.splits = grads & 1 ? dh_splits(rows, d, s.cols, grads & 2) : 1;
   s.rows_pad = up_to(rows, kTile) * kTile;
   s.direct = s.splits == 1 && s.cols >= vocab;
-  s.keep = grads && d >= kKeepWidth;
+  // (a tile is made again for 256 rows, however few there are)
+  s.keep = grads && static_cast<int64_t>(d) * s.rows_pad >= static_cast<int64_t>(kKeepWidth) * rows;
   s.ldm = up_to(d, kK) * kK;  // copies of rows that start on 128 bytes: d = 712 is 20 % slower than 704 or 720
   s.parts = 0;
-  s.info = up(n * 2 * up_to(vocab, kTile) * sizeof(float2));
+  s.info = up(n * (!grads && rows <= kFewRows ? 8 : 2) * up_to(vocab, kTile) * sizeof(float2));
   s.hm = s.info + (grads ? up(n * sizeof(HeadRow)) : 0);
-  s.refs = s.hm + (grads & 2 ? up(n * s.ldm * 2) : 0);
-  s.g = s.refs + (s.keep ? up(n * (s.cols / 32) * 4) : 0);
+  s.g = s.hm + (grads & 2 ? up(n * s.ldm * 2) : 0);
   s.dh = s.g + (grads ? up(n * s.cols * 2) : 0);
   s.bytes = s.dh + ((grads & 1) && !s.direct ? up(static_cast<size_t>(s.splits) * s.rows_pad * d * 4) : 0);
   return s;
@@ -874,7 +933,7 @@ int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, int
   if (MODE == kProducts)
     b.ahead = balance(a.dh_items, up_to(up_to(a.cols, kK), a.splits), a.de_items, up_to(a.row.rows, kK), pairs).ahead;
   (void)cudaLaunchKernelEx(&cfg, head_gemm_kernel<MODE>, maps, b, err);
-  return check(MODE == kStats ? "stats" : (MODE == kGrad ? "gradient" : "products"));
+  return check(MODE == kStats || MODE == kFew ? "stats" : (MODE == kGrad ? "gradient" : "products"));
 }
 
 }  // namespace
@@ -948,20 +1007,36 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   q.parts = parts;
   q.info = info;
   q.emb = e;
+  const bool few = !grads && rows <= kFewRows;
+  const int nparts = (few ? 8 : 2) * q.n_tiles;
   CUtensorMap map_h;
-  bool ok = head_map(&map_h, h, false, d, rows, ldh, kK, 128) && head_map(&maps.b, emb, false, d, vocab, d, kK, 128);
+  bool ok = head_map(&map_h, h, false, d, rows, ldh, kK, few ? kFewRows / 2 : 128) &&
+            head_map(&maps.b, emb, false, d, vocab, d, kK, 128);
   if (ok && at.keep) {
     q.keep = at.cols;
-    q.refs = reinterpret_cast<float*>(w + at.refs);
     ok = head_map(&maps.c, g, false, std::min(at.cols, vocab), rows, at.cols, 32, 32);
   }
   if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
   maps.a = map_h;
-  int rc = launch_head_gemm<kStats>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st);
+  int rc;
+  if (few) {  // the vocabulary as rows
+    std::swap(maps.a, maps.b);
+    std::swap(q.m_tiles, q.n_tiles);
+    rc = launch_head_gemm<kFew>(maps, q, q.m_tiles, err, st);
+  } else {
+    rc = launch_head_gemm<kStats>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st);
+  }
   if (rc) return rc;
-  (void)launch_k(head_rows_kernel, up_to(rows, 8), 256, 0, st, a, static_cast<const __nv_bfloat16*>(h), ldh, e,
-                 static_cast<const float2*>(parts), 2 * q.n_tiles, loss_rows, grads ? info : nullptr,
-                 demb ? hm : nullptr, static_cast<int64_t>(at.ldm), err);
+  const auto* hb = static_cast<const __nv_bfloat16*>(h);
+  const float2* in_parts = parts;
+  HeadRow* rows_info = grads ? info : nullptr;
+  // with few rows a warp each would take long over their sums: 3 rows over 128616 columns 14 us
+  if (rows <= kWideRows && nparts >= 128)
+    (void)launch_k(head_rows_kernel<8>, rows, 256, 0, st, a, hb, ldh, e, in_parts, nparts, loss_rows, rows_info,
+                   demb ? hm : nullptr, static_cast<int64_t>(at.ldm), err);
+  else
+    (void)launch_k(head_rows_kernel<1>, up_to(rows, 8), 256, 0, st, a, hb, ldh, e, in_parts, nparts, loss_rows,
+                   rows_info, demb ? hm : nullptr, static_cast<int64_t>(at.ldm), err);
   if ((rc = check("rows"))) return rc;
   for (int v0 = 0; grads && v0 < vocab; v0 += at.cols) {
     const int cols = std::min(at.cols, vocab - v0);
@@ -971,8 +1046,8 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
     q.n_tiles = up_to(cols, kTile);
     if (v0 == 0 && at.keep) {
       const int slabs = up_to(cols, 16 * 256);
-      (void)launch_k(head_scale_kernel, rows * slabs, 256, 0, st, rows, cols, static_cast<int64_t>(at.cols), slabs,
-                     static_cast<const HeadRow*>(info), static_cast<const float*>(q.refs), at.cols / 32,
+      (void)launch_k(head_scale_kernel, rows * slabs, 256, 0, st, cols, static_cast<int64_t>(at.cols), slabs,
+                     static_cast<const HeadRow*>(info), static_cast<const float2*>(parts), nparts,
                      reinterpret_cast<uint4*>(g));
       if ((rc = check("scale"))) return rc;
     } else {

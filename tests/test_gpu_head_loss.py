@@ -9,7 +9,8 @@ Tolerances are worst-case bounds, counted in roundings (u = 2^-24 for fp32):
          e^-128; 2^-20 covers the maximum of x e^-x), the sums an addition each
   g      2^-8 of its value for bf16 (half a step: finfo.eps / 2 = 2^-7 / 2), and e_p = (2 (2 dz + e_s) + 2^-11) p +
          2^-38 for p, which passes through fp16 (2^-11; below 2^-28 of the largest of its 32
-         neighbours, at most 1, steps of 2^-38)
+         neighbours, at most 1, steps of 2^-38); all of g where |z| is within dz of clip, as it may
+         count as beyond it or not
   dh     sum_v |g_v| |E_v| (2^-8 + 2^-10) + e_p sum_v w p_v |E_v|, and 2^-8 of the result
   demb   the same over the rows; 2^-8 of the result as bf16
 (2^-10 covers the products' own additions: 2 u times up to 2^13 terms.)"""
@@ -89,9 +90,9 @@ def exact(p, clip=0.0, inv=None, row0=0):
     e = p["emb"].double()
     z = h @ e.T
     dz = (2 * d * U * (h.abs() @ e.abs().T).amax(1))[:, None]
-    inside = torch.ones_like(z)
+    inside, either = torch.ones_like(z), torch.zeros_like(z)
     if clip > 0:
-        assert float(((z.abs() - clip).abs() - dz).min()) > 0, "a logit too near the limit to say on which side it is"
+        either = ((z.abs() - clip).abs() <= dz).double()  # too near the limit to say on which side it is
         inside = (z.abs() < clip).double()
         z = z.clamp(-clip, clip)
     m = z.amax(1, keepdim=True)
@@ -103,9 +104,10 @@ def exact(p, clip=0.0, inv=None, row0=0):
     pr = (z - m).exp() / s
     gr = pr.clone()
     gr.scatter_add_(1, t[:, None], -torch.ones_like(zt))
+    slack = either * gr.abs() * w[:, None].abs()
     gr *= w[:, None] * inside
     e_p = ((2 * (2 * dz + e_s) + 2.0 ** -11) * pr + 2.0 ** -38) * w[:, None].abs() * inside
-    slack = gr.abs() * (2.0 ** -8 + 2.0 ** -10) + e_p
+    slack += gr.abs() * (2.0 ** -8 + 2.0 ** -10) + e_p
     a = abs(inv)
     dh, demb = inv * (gr @ e), inv * (gr.T @ h)
     return dict(loss=loss, loss_tol=loss_tol, dh=dh, dh_tol=a * (slack @ e.abs()) * 1.01 + 2.0 ** -8 * dh.abs(), demb=demb,
@@ -131,6 +133,13 @@ FORMS = [
     (1, 64, 1000, 5, 0, 0.0, False, "none", False),
     (1, 1024, 5000, 2, 0, 0.0, False, "both", True),
     (2, 8, 2, 3, 0, 0.0, False, "both", True),
+    (1, 8, 1, 2, 0, 0.0, False, "none", False),
+    (31, 136, 517, 4, 0, 4.0, True, "none", False),
+    (64, 1024, 9001, 64, 0, 0.0, False, "none", False),
+    (65, 200, 9001, 64, 0, 4.0, False, "none", False),
+    (3, 248, 40000, 5, 0, 0.0, False, "both", False),
+    (2000, 64, 20011, 90, 0, 5.0, True, "none", False),
+    (1300, 784, 2900, 90, 1024, 4.0, True, "both", False),
     (5, 64, 517, 5, 0, 0.0, False, "both", False),
     (7, 72, 255, 3, 256, 0.0, False, "both", True),
     (33, 200, 257, 11, 256, 0.0, True, "both", False),
