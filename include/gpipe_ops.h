@@ -250,9 +250,10 @@ int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t
  * the device error flag.  w_r = row_weight[r] (fp32 [rows]; NULL: 1).  A row
  * without a target or of weight 0 has loss 0, a zero row of dh and no part in demb;
  * its h is not used and may hold anything (NaN included).
- * piece     columns of the vocabulary whose g exists at a time (rounded up to a
- *           multiple of 256): more scratch and fewer launches with more of them.
- *           0: as many as give g 256 MB.
+ * piece     columns of the vocabulary that a launch works on (rounded up to a multiple
+ *           of 256): more scratch and fewer launches with more of them.  g exists for
+ *           one piece at a time, for two where the vocabulary takes several.  0: as
+ *           many as give g 256 MB.
  * scratch   gpipe_op_head_loss_scratch_bytes (grads: 1 dh, 2 demb, 3 both), 256-byte
  *           aligned, written before it is read (calls that may overlap on the GPU,
  *           captured ones included, need one each, and outputs each).

@@ -13,11 +13,12 @@
 //                                 its g will be (fp16).  Up to 64 rows without gradients:
 //      head_gemm_kernel<kFew>     the same with the vocabulary as the products' rows
 //   2  head_rows_kernel           joins them, the loss, and what 3 needs of a row
+//   3  head_scale_kernel          the first piece's g from the powers, in place
+//      head_gemm_kernel<kGrad>    or z again, turned into g in the epilogue
 //   per piece of the vocabulary:
-//   3  head_scale_kernel          the first piece: g from the powers, in place
-//      head_gemm_kernel<kGrad>    the others: z again, turned into g in the epilogue
 //   4  head_gemm_kernel<kProducts>  both products of g, tiles of dh and of dE in one
-//                                 launch, so that one's last round fills the other's
+//                                 launch, and the next piece's g, so that one's last
+//                                 round fills the other's
 //   5  head_dh_kernel             sums of dh over pieces and parts of K into bf16
 //
 // Arithmetic.  Exponentials are powers of two, with an integer reference rho of each
@@ -33,7 +34,8 @@
 // and its rounding does not add up over the rows.
 //
 // Cost: 6 rows vocab d flops with both gradients for the first piece, 8 for the others.
-// Memory: 2 B an element of one piece of g, which is all that is ever held of the logits.
+// Memory: 2 B an element of a piece of g, or of two where there are several, which is all
+// that is ever held of the logits.
 // The powers are fp16 because it has three bits more than bf16, 2^-28 of the largest of
 // 128 down (their reference puts that near 2^14): g's rounding to bf16 stays the only one that tells.
 #include <cuda.h>
@@ -127,6 +129,17 @@ struct HeadMaps {
   CUtensorMap a, b;    // logits: h and the piece of E; products: g and the piece of E (dh)
   CUtensorMap c;       // where the tiles leave to: g, or dh
   CUtensorMap a2, b2, c2;  // products: g the other way round and h (dE), dE
+  CUtensorMap a3, b3, c3;  // products: h, the next piece of E and its g
+};
+
+// A list of n tiles shared out to the pairs: those from `late` on, which have less to do
+// before it, take `ahead` each, then all take the others in turn.
+struct Share {
+  int n, late, ahead;
+  __device__ __forceinline__ int tile(int j, int pair, int pairs) const {  // a pair's j-th; n or more: none
+    const int rest = pairs - late, mine = pair >= late ? ahead : 0;
+    return j < mine ? j * rest + (pair - late) : ahead * rest + (j - mine) * pairs + pair;
+  }
 };
 
 struct HeadGemm {
@@ -140,37 +153,44 @@ struct HeadGemm {
   const __nv_bfloat16* emb;
   // kProducts
   int splits, rows_pad;  // parts of dh's K, each with a buffer of rows_pad rows
-  int dh_items, de_items, ahead, dh_out;
+  int dh_items, dh_out;
+  Share de, g;              // tiles of dE and of the next piece's g
   bool de_f32;
+  int g_tiles, g_cols, g_v0;  // the next piece's tiles across, columns and first column
 };
 
+enum Kind { kLogits, kDh, kDe };
 struct Item {
   int m0, n0, k0, nk;  // origin of the tile; first k-block and their number
   int split;
-  bool de;
+  Kind kind;
 };
 
 // The tiles of a pair, in order.  Logits: every pairs-th of the grouped tile order
 // (row tiles fastest within a group, so the tiles in flight share bands of both operands).
-// Products: its share of dh's tiles first, which are few and long; then tiles of dE,
-// the pairs with one tile of dh less taking `ahead` of them before the others join in.
+// Products: its share of dh's tiles, which are few and long, then of dE's and of the next
+// piece's g.
 template <Mode MODE>
 struct Walk {
-  int pair, pairs, i = 0, j = 0;
+  int pair, pairs, i = 0, j = 0, k = 0;
   __device__ Walk(int p, int n) : pair(p), pairs(n) {}
+  // tile t of a grid whose row tiles are fastest within groups of kGroup
+  __device__ __forceinline__ void logits(const HeadGemm& a, int t, int n_tiles, Item& it) {
+    const int per_group = kGroup * n_tiles;
+    const int grp = t / per_group, r = t - grp * per_group, first = grp * kGroup;
+    const int gm = min(kGroup, a.m_tiles - first);
+    it.m0 = (first + r % gm) * kTile;
+    it.n0 = (r / gm) * kTile;
+    it.nk = (a.row.d + kK - 1) / kK;
+    it.kind = kLogits;
+  }
   __device__ __forceinline__ bool next(const HeadGemm& a, Item& it) {
     it.split = 0;
-    it.de = false;
     it.k0 = 0;
     if (MODE != kProducts) {
       const int t = pair + i++ * pairs;
       if (t >= a.m_tiles * a.n_tiles) return false;
-      const int per_group = kGroup * a.n_tiles;
-      const int grp = t / per_group, r = t - grp * per_group, first = grp * kGroup;
-      const int gm = min(kGroup, a.m_tiles - first);
-      it.m0 = (first + r % gm) * kTile;
-      it.n0 = (r / gm) * kTile;
-      it.nk = (a.row.d + kK - 1) / kK;
+      logits(a, t, a.n_tiles, it);
       return true;
     }
     const int t = pair + i * pairs;
@@ -183,14 +203,18 @@ struct Walk {
       it.n0 = n * kTile;
       it.k0 = static_cast<int>(static_cast<int64_t>(nk) * it.split / a.splits);
       it.nk = static_cast<int>(static_cast<int64_t>(nk) * (it.split + 1) / a.splits) - it.k0;
+      it.kind = kDh;
       return true;
     }
-    const int late = a.dh_items % pairs;  // pairs with one more tile of dh
-    const int ahead = pair >= late ? a.ahead : 0, rest = pairs - late;
-    const int e = j < ahead ? j * rest + (pair - late) : a.ahead * rest + (j - ahead) * pairs + pair;
+    const int e = a.de.tile(j, pair, pairs);
+    if (e >= a.de.n) {
+      const int g = a.g.tile(k++, pair, pairs);
+      if (g >= a.g.n) return false;
+      logits(a, g, a.g_tiles, it);
+      return true;
+    }
     ++j;
-    if (e >= a.de_items) return false;
-    it.de = true;
+    it.kind = kDe;
     it.m0 = e / a.n_tiles * kTile;
     it.n0 = e % a.n_tiles * kTile;
     it.nk = (a.row.rows + kK - 1) / kK;
@@ -349,21 +373,25 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   Item it;
   if (warp == 0) {
     if (lane == 0) {
-      int n = 0;
+      int n = 0, s = 0;  // k-blocks so far; the stage of the next, whose ring has been round `turn` times (mod 2)
+      uint32_t turn = 0;
+      const uint32_t full_leader = map_peer(smem_u32(full), 0);
       while (!*abort && walk.next(a, it)) {
         const int am = it.m0 + rank * 128, bn = it.n0 + rank * (Cfg::kColumns / 2);
         for (int kb = 0; kb < it.nk; ++kb, ++n) {
-          const int s = n % STAGES;
-          if (!head_wait(&empty[s], ((n / STAGES) & 1) ^ 1, err, DERR_TMA_WAIT, abort)) break;
+          if (!head_wait(&empty[s], turn ^ 1, err, DERR_TMA_WAIT, abort)) break;
           uint8_t* sa = smem + s * Cfg::kStage;
           uint8_t* sb = sa + Cfg::kA;
           const int k = (it.k0 + kb) * kK;
-          const uint32_t fb = map_peer(smem_u32(&full[s]), 0);
+          const uint32_t fb = full_leader + s * 8;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Cfg::kStage);
           if (MODE != kProducts) {
             tma_load_2d_pair(sa, &maps.a, k, am, fb);
             tma_load_2d_pair(sb, &maps.b, k, bn, fb);
-          } else if (!it.de) {
+          } else if (it.kind == kLogits) {
+            tma_load_2d_pair(sa, &maps.a3, k, am, fb);
+            tma_load_2d_pair(sb, &maps.b3, k, bn, fb);
+          } else if (it.kind == kDh) {
             tma_load_2d_pair(sa, &maps.a, k, am, fb);
             tma_load_2d_pair(sb, &maps.b, bn, k, fb);
             tma_load_2d_pair(sb + 8192, &maps.b, bn + 64, k, fb);
@@ -372,6 +400,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
             tma_load_2d_pair(sa + 8192, &maps.a2, am + 64, k, fb);
             tma_load_2d_pair(sb, &maps.b2, bn, k, fb);
             tma_load_2d_pair(sb + 8192, &maps.b2, bn + 64, k, fb);
+          }
+          if (++s == STAGES) {
+            s = 0;
+            turn ^= 1;
           }
         }
       }
@@ -383,27 +415,36 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     griddep_launch();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      int n = 0, i = 0;
+      int i = 0, s = 0;
+      uint32_t turn = 0;
+      const uint32_t stages = smem_u32(smem);
       for (; walk.next(a, it); ++i) {
         const int b = i & 1;
         if (!head_wait<true>(&acce[b], ((i >> 1) & 1) ^ 1, err, DERR_MMA_WAIT, abort)) break;
         tc_fence_after();
-        const bool a_mn = MODE == kProducts && it.de, b_mn = MODE == kProducts;
-        const uint32_t idesc = a_mn ? mma_idesc_bf16(kTile, kTile, true, true)
-                                    : mma_idesc_bf16(kTile, Cfg::kColumns, false, MODE == kProducts);
+        const bool a_mn = MODE == kProducts && it.kind == kDe, b_mn = MODE == kProducts && it.kind != kLogits;
+        const uint32_t idesc = a_mn   ? mma_idesc_bf16(kTile, kTile, true, true)
+                               : b_mn ? mma_idesc_bf16(kTile, kTile, false, true)
+                                      : mma_idesc_bf16(kTile, Cfg::kColumns, false, false);
+        // descriptors but for the address, and their steps over 16 k (in units of 16 bytes): one
+        // thread issues a k-block's four products in the 0.3 us that they take
+        const uint64_t a_form = a_mn ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024),
+                       b_form = b_mn ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
+        const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
         const uint32_t acc = tmem + b * kTile;
-        for (int kb = 0; kb < it.nk; ++kb, ++n) {
-          const int s = n % STAGES;
-          if (!head_wait(&full[s], (n / STAGES) & 1, err, DERR_MMA_WAIT, abort)) break;
+        for (int kb = 0; kb < it.nk; ++kb) {
+          if (!head_wait(&full[s], turn, err, DERR_MMA_WAIT, abort)) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * Cfg::kStage), sb = sa + Cfg::kA;
+          const uint32_t at = (stages + s * Cfg::kStage) >> 4;
 #pragma unroll
-          for (int kk = 0; kk < kK / 16; ++kk) {
-            const uint64_t ad = a_mn ? sw128_desc(sa + kk * 2048, 8192, 1024) : sw128_desc(sa + kk * 32, 16, 1024);
-            const uint64_t bd = b_mn ? sw128_desc(sb + kk * 2048, 8192, 1024) : sw128_desc(sb + kk * 32, 16, 1024);
-            tc_mma_f16_pair(acc, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < kK / 16; ++kk)
+            tc_mma_f16_pair(acc, a_form + (at + kk * a_step), b_form + (at + (Cfg::kA >> 4) + kk * b_step), idesc,
+                            (kb | kk) != 0 ? 1u : 0u);
           tc_commit_pair(&empty[s], 3);  // both CTAs' stage s is free again
+          if (++s == STAGES) {
+            s = 0;
+            turn ^= 1;
+          }
         }
         tc_commit_pair(&accf[b], 3);
       }
@@ -425,7 +466,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         float w;
         info.target = head_target(a.row, m, w, nullptr);
       }
-      if ((MODE == kGrad || (MODE == kProducts && !t.de && a.dh_out == kDhBf16)) && m < a.row.rows) {
+      if ((MODE == kGrad ||
+           (MODE == kProducts && (t.kind == kLogits || (t.kind == kDh && a.dh_out == kDhBf16)))) &&
+          m < a.row.rows) {
         const float4 f = *reinterpret_cast<const float4*>(a.info + m);
         info = HeadRow{f.x, f.y, f.z, __float_as_int(f.w)};
       }
@@ -441,10 +484,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       if (more) info_ahead = row_of(ahead);
       const int b = i & 1;
       const int mw = it.m0 + rank * 128 + q * 32, m = mw + lane;  // the warp's first row, the thread's
-      const int c0 = it.n0 + half * 128;                          // the warp's first column
-      const int width = MODE == kProducts ? a.row.d : a.cols;
-      const int target = info.target - (MODE == kGrad ? a.v0 : 0);
-      const float rest = MODE == kProducts && info.target >= 0 ? lost(info.gt) : 0.f;
+      const int cw = it.n0 + half * 128;                          // the warp's first column
+      const bool grad = MODE == kGrad || (MODE == kProducts && it.kind == kLogits);
+      const int width = MODE != kProducts ? a.cols : (grad ? a.g_cols : a.row.d);
+      const int target = info.target - (MODE == kGrad ? a.v0 : (MODE == kProducts ? a.g_v0 : 0));
+      const float rest = MODE == kProducts && !grad && info.target >= 0 ? lost(info.gt) : 0.f;
       head_wait(&accf[b], (i >> 1) & 1, err, DERR_ACC_WAIT, abort);
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + half * (Cfg::kColumns / 2);
@@ -479,137 +523,144 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         if (r < a.row.rows)
           a.parts[static_cast<int64_t>(r) * (8 * a.m_tiles) + (mw / 32)] = make_float2(rho, sum);
       } else {
-        // all of the warp's columns at once: a load's latency is some 500 clocks, and one after
-        // the other they were two thirds of the epilogue
-        uint32_t ra[128];
+        // many columns at once: a load's latency is some 500 clocks, and 32 columns after the
+        // other they were two thirds of the epilogue
+        constexpr int kWide = MODE == kStats ? 128 : 64;
+#pragma unroll 1
+        for (int c1 = 0; c1 < 128; c1 += kWide) {
+          uint32_t ra[kWide];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tb + c * 32, ra + c * 32);
+          for (int c = 0; c < kWide / 32; ++c) tmem_ld32(tb + c1 + c * 32, ra + c * 32);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait32(ra + c * 32);
-        drained();
-        float v[128];
+          for (int c = 0; c < kWide / 32; ++c) tmem_ld_wait32(ra + c * 32);
+          if (c1 + kWide == 128) drained();
+          const int c0 = cw + c1;  // the first of these columns
+          float v[kWide];
 #pragma unroll
-        for (int j = 0; j < 128; ++j) v[j] = __uint_as_float(ra[j]);
-        const bool edge = c0 + 128 > width;
-        const bool has_target = static_cast<unsigned>(target - c0) < 128u;
-        if (MODE == kStats) {
-          float rho;
-          const bool kept = it.n0 < a.keep;
-          uint32_t cut[4] = {0, 0, 0, 0};  // columns beyond the limit
-          if (a.row.clip > 0.f) {
-            __syncwarp();
+          for (int j = 0; j < kWide; ++j) v[j] = __uint_as_float(ra[j]);
+          const bool edge = c0 + kWide > width;
+          const bool has_target = static_cast<unsigned>(target - c0) < static_cast<unsigned>(kWide);
+          if (MODE == kStats) {
+            float rho;
+            const bool kept = it.n0 < a.keep;
+            uint32_t cut[kWide / 32] = {};  // columns beyond the limit
+            if (a.row.clip > 0.f) {
+              __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 128; ++j) {
-              if (kept) cut[j >> 5] |= fabsf(v[j]) > a.row.clip ? 1u << (j & 31) : 0u;
-              v[j] = limit(v[j], a.row.clip);
-            }
-          }
-          if (edge) {
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (c0 + j >= width) v[j] = -INFINITY;
-          }
-          if (__any_sync(0xffffffffu, has_target)) {
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (c0 + j == target) v[j] = -INFINITY;
-          }
-          const float sum = to_powers<128>(v, rho);
-          if (m < a.row.rows)
-            a.parts[static_cast<int64_t>(m) * (2 * a.n_tiles) + (it.n0 / 128 + half)] = make_float2(rho, sum);
-          if (!kept) continue;
-          if (a.row.clip > 0.f) {
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 128; ++j) v[j] = cut[j >> 5] >> (j & 31) & 1u ? 0.f : v[j];
-          }
-        }
-        if (MODE == kGrad) {
-          const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-info.rho, -info.rho), sc = pack2(info.scale, info.scale);
-          if (a.row.clip > 0.f) {  // columns beyond the limit: marked, so that they come out as 0
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 128; ++j) v[j] = fabsf(v[j]) > a.row.clip ? -INFINITY : v[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 128; j += 2) {
-            float x, y;
-            unpack2(fma2(pack2(v[j], v[j + 1]), l2, ref), x, y);
-            unpack2(mul2(pack2(ex2_approx(x), ex2_approx(y)), sc), v[j], v[j + 1]);
-          }
-          if (__any_sync(0xffffffffu, has_target)) {
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (c0 + j == target) v[j] = info.gt;
-          }
-          if (__any_sync(0xffffffffu, info.target < 0)) {  // zeros, whatever the row holds
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 128; ++j) v[j] = info.target < 0 ? 0.f : v[j];
-          }
-        }
-        if (MODE == kProducts) {
-          if (__any_sync(0xffffffffu, rest != 0.f)) {  // what g_t lost to its rounding
-            __syncwarp();
-            const __nv_bfloat16* e = a.emb + static_cast<int64_t>(max(info.target, 0)) * a.row.d + c0;
-#pragma unroll
-            for (int j = 0; j < 128; j += 8) {
-              if (c0 + j < width) {
-                float w[8];
-                load8(e + j, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[j + k] = fmaf(rest, w[k], v[j + k]);
+              for (int j = 0; j < kWide; ++j) {
+                if (kept) cut[j >> 5] |= fabsf(v[j]) > a.row.clip ? 1u << (j & 31) : 0u;
+                v[j] = limit(v[j], a.row.clip);
               }
             }
+            if (edge) {
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < kWide; ++j)
+                if (c0 + j >= width) v[j] = -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, has_target)) {
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < kWide; ++j)
+                if (c0 + j == target) v[j] = -INFINITY;
+            }
+            const float sum = to_powers<kWide>(v, rho);
+            if (m < a.row.rows)
+              a.parts[static_cast<int64_t>(m) * (2 * a.n_tiles) + (it.n0 / 128 + half)] = make_float2(rho, sum);
+            if (!kept) continue;
+            if (a.row.clip > 0.f) {
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < kWide; ++j) v[j] = cut[j >> 5] >> (j & 31) & 1u ? 0.f : v[j];
+            }
           }
-          const float al = it.de || a.dh_out == kDhBf16 ? a.row.inv_count : 1.f;
+          if (grad) {
+            const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-info.rho, -info.rho), sc = pack2(info.scale, info.scale);
+            if (a.row.clip > 0.f) {  // columns beyond the limit: marked, so that they come out as 0
+              __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 128; ++j) v[j] *= al;
-        }
-        // out, 32 columns at a time, through the warp's two boxes
-        const bool f32 = MODE == kProducts && (it.de ? a.de_f32 : a.dh_out != kDhBf16);
+              for (int j = 0; j < kWide; ++j) v[j] = fabsf(v[j]) > a.row.clip ? -INFINITY : v[j];
+            }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = c0 + c * 32;
-          if (col >= width) break;
-          uint8_t* box = boxes + (staged++ & 1) * Cfg::kBox;
-          if (lane == 0) wait_read_1();
-          __syncwarp();
-          const float* o = v + c * 32;
-          if (f32) {
+            for (int j = 0; j < kWide; j += 2) {
+              float x, y;
+              unpack2(fma2(pack2(v[j], v[j + 1]), l2, ref), x, y);
+              unpack2(mul2(pack2(ex2_approx(x), ex2_approx(y)), sc), v[j], v[j + 1]);
+            }
+            if (__any_sync(0xffffffffu, has_target)) {
+              __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<float4*>(box + box_f32(lane, u)) =
-                  make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-          } else if (MODE == kStats) {
+              for (int j = 0; j < kWide; ++j)
+                if (c0 + j == target) v[j] = info.gt;
+            }
+            if (__any_sync(0xffffffffu, info.target < 0)) {  // zeros, whatever the row holds
+              __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              *reinterpret_cast<uint4*>(box + box_bf16(lane, u)) =
-                  make_uint4(pack_f16x2(o[8 * u], o[8 * u + 1]), pack_f16x2(o[8 * u + 2], o[8 * u + 3]),
-                             pack_f16x2(o[8 * u + 4], o[8 * u + 5]), pack_f16x2(o[8 * u + 6], o[8 * u + 7]));
-          } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) store8(reinterpret_cast<__nv_bfloat16*>(box + box_bf16(lane, u)), o + 8 * u);
+              for (int j = 0; j < kWide; ++j) v[j] = info.target < 0 ? 0.f : v[j];
+            }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (!*abort) {
-              if (MODE != kProducts) {
-                tma_store_2d(&maps.c, col, mw, box);
-              } else if (it.de) {
-                if (a.de_f32) tma_reduce_add_2d(&maps.c2, col, a.v0 + mw, box);
-                else tma_store_2d(&maps.c2, col, a.v0 + mw, box);
-              } else {
-                const int y = it.split * a.rows_pad + mw;
-                if (a.dh_out == kDhAdd) tma_reduce_add_2d(&maps.c, col, y, box);
-                else tma_store_2d(&maps.c, col, y, box);
+          if (MODE == kProducts && !grad) {
+            if (__any_sync(0xffffffffu, rest != 0.f)) {  // what g_t lost to its rounding
+              __syncwarp();
+              const __nv_bfloat16* e = a.emb + static_cast<int64_t>(max(info.target, 0)) * a.row.d + c0;
+#pragma unroll
+              for (int j = 0; j < kWide; j += 8) {
+                if (c0 + j < width) {
+                  float w[8];
+                  load8(e + j, w);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) v[j + k] = fmaf(rest, w[k], v[j + k]);
+                }
               }
             }
-            bulk_commit();
+            const float al = it.kind == kDe || a.dh_out == kDhBf16 ? a.row.inv_count : 1.f;
+#pragma unroll
+            for (int j = 0; j < kWide; ++j) v[j] *= al;
+          }
+          // out, 32 columns at a time, through the warp's two boxes
+          const bool f32 = MODE == kProducts && !grad && (it.kind == kDe ? a.de_f32 : a.dh_out != kDhBf16);
+#pragma unroll
+          for (int c = 0; c < kWide / 32; ++c) {
+            const int col = c0 + c * 32;
+            if (col >= width) break;
+            uint8_t* box = boxes + (staged++ & 1) * Cfg::kBox;
+            if (lane == 0) wait_read_1();
+            __syncwarp();
+            const float* o = v + c * 32;
+            if (f32) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4*>(box + box_f32(lane, u)) =
+                    make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+            } else if (MODE == kStats) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(box + box_bf16(lane, u)) =
+                    make_uint4(pack_f16x2(o[8 * u], o[8 * u + 1]), pack_f16x2(o[8 * u + 2], o[8 * u + 3]),
+                               pack_f16x2(o[8 * u + 4], o[8 * u + 5]), pack_f16x2(o[8 * u + 6], o[8 * u + 7]));
+            } else {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) store8(reinterpret_cast<__nv_bfloat16*>(box + box_bf16(lane, u)), o + 8 * u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (!*abort) {
+                if (MODE != kProducts) {
+                  tma_store_2d(&maps.c, col, mw, box);
+                } else if (grad) {
+                  tma_store_2d(&maps.c3, col, mw, box);
+                } else if (it.kind == kDe) {
+                  if (a.de_f32) tma_reduce_add_2d(&maps.c2, col, a.v0 + mw, box);
+                  else tma_store_2d(&maps.c2, col, a.v0 + mw, box);
+                } else {
+                  const int y = it.split * a.rows_pad + mw;
+                  if (a.dh_out == kDhAdd) tma_reduce_add_2d(&maps.c, col, y, box);
+                  else tma_store_2d(&maps.c, col, y, box);
+                }
+              }
+              bulk_commit();
+            }
           }
         }
       }
@@ -756,36 +807,36 @@ __global__ void __launch_bounds__(256) head_scale_kernel(int cols, int64_t ldg, 
   }
 }
 
-// dh = inv_count times the sum of its parts and of what g_t lost to its rounding, a warp
-// per row.
+// dh = inv_count times the sum of its parts and of what g_t lost to its rounding, 8 columns
+// a thread (a warp a row waits 11 us for 16 parts of 64 rows).
 __global__ void __launch_bounds__(256) head_dh_kernel(int rows, int d, int splits, int rows_pad, float scale,
                                                       const float* __restrict__ src, const HeadRow* __restrict__ info,
                                                       const __nv_bfloat16* __restrict__ emb,
                                                       __nv_bfloat16* __restrict__ dh, int64_t lddh) {
   griddep_wait();
   griddep_launch();
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const uint32_t groups = d / 8;
+  const int r = static_cast<int>(i / groups), c = static_cast<int>(i % groups) * 8;
   if (r >= rows) return;
   const float4 f = *reinterpret_cast<const float4*>(info + r);
   const int target = __float_as_int(f.w);
   const float rest = target >= 0 ? lost(f.z) : 0.f;
-  const __nv_bfloat16* e = emb + static_cast<int64_t>(max(target, 0)) * d;
-  for (int c = lane * 8; c < d; c += 256) {
-    float v[8], u[8];
-    load8(e + c, u);
-    load8(src + static_cast<int64_t>(r) * d + c, v);
+  float v[8], u[8];
+  load8(emb + static_cast<int64_t>(max(target, 0)) * d + c, u);
+  const float* at = src + static_cast<int64_t>(r) * d + c;
+  load8(at, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = fmaf(rest, u[j], v[j]);
-#pragma unroll 4
-    for (int p = 1; p < splits; ++p) {
-      load8(src + (static_cast<int64_t>(p) * rows_pad + r) * d + c, u);
+  for (int j = 0; j < 8; ++j) v[j] = fmaf(rest, u[j], v[j]);
+#pragma unroll 8
+  for (int p = 1; p < splits; ++p) {
+    load8(at + static_cast<int64_t>(p) * rows_pad * d, u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += u[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= scale;
-    store8(dh + r * lddh + c, v);
+    for (int j = 0; j < 8; ++j) v[j] += u[j];
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= scale;
+  store8(dh + r * lddh + c, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -805,41 +856,51 @@ bool sizes_ok(int rows, int d, int vocab, int piece) {
          vocab <= (1 << 27) && piece >= 0 && static_cast<int64_t>(up_to(rows, kTile)) * up_to(vocab, kTile) <= (1 << 26);
 }
 
-// Columns of a piece: a multiple of 256; 0 asks for as many as make g 256 MB.
+// Columns of a piece: a multiple of 256; 0 asks for as many as make g 256 MB, in one piece or
+// in two at a time.
 int piece_columns(int rows, int vocab, int piece) {
   int64_t p = piece ? piece : std::max<int64_t>(2048, (static_cast<int64_t>(1) << 27) / rows);
+  if (!piece && p < vocab) p = std::max<int64_t>(2048, p / 2);
   p = std::min<int64_t>((p + kTile - 1) / kTile * kTile, (static_cast<int64_t>(vocab) + kTile - 1) / kTile * kTile);
   return static_cast<int>(p);
 }
 
-// Tiles of dE that the pairs with one tile of dh less take first, and k-blocks that the
-// busiest pair then has.  A tile costs its k-blocks and two more (measured: filling
-// the ring and the last tile's epilogue).
-struct Balance {
-  int ahead;
+// How the pairs share dE's and g's tiles, and about how many k-blocks the busiest has.  A
+// tile costs its k-blocks and two more (measured: filling the ring and the last tile's
+// epilogue).
+struct Plan {
+  Share de, g;
   int64_t longest;
 };
-Balance balance(int64_t dh_items, int dh_nk, int64_t de_items, int de_nk, int pairs) {
-  const int64_t ch = dh_nk + 2, ce = de_nk + 2, q = dh_items / pairs, late = dh_items % pairs, rest = pairs - late;
-  int64_t ahead = late ? (ch + ce / 2) / ce : 0;
-  ahead = std::min(ahead, (de_items + rest - 1) / rest);
-  const int64_t left = std::max<int64_t>(0, de_items - ahead * rest), each = (left + pairs - 1) / pairs;
-  const int64_t early = q * ch + (ahead + each) * ce;
-  return {static_cast<int>(ahead), late ? std::max(early, (q + 1) * ch + each * ce) : early};
+Plan plan(int64_t dh_items, int dh_nk, int64_t de_items, int de_nk, int64_t g_items, int g_nk, int pairs) {
+  const int64_t ch = dh_nk + 2, ce = de_nk + 2, cg = g_nk + 2, q = dh_items / pairs, late = dh_items % pairs,
+                rest = pairs - late;
+  const int64_t ahead = late ? std::min((ch + ce / 2) / ce, de_items / rest) : 0, left = de_items - ahead * rest;
+  // what the pairs with one tile of dh less still have in hand, or those with one of dE less
+  const int64_t gap = late ? ch - ahead * ce : 0, late2 = gap > ce ? late : left % pairs,
+                gap2 = gap > ce ? gap : (late2 ? ce : 0);
+  const int64_t ahead2 = late2 ? std::min((gap2 + cg / 2) / cg, g_items / (pairs - late2)) : 0;
+  const int64_t before = q * ch + std::max<int64_t>(late ? ch : 0, ahead * ce) + (left + pairs - 1) / pairs * ce;
+  const int64_t even = (dh_items * ch + de_items * ce + g_items * cg + pairs - 1) / pairs + cg;
+  return {{static_cast<int>(de_items), static_cast<int>(late), static_cast<int>(ahead)},
+          {static_cast<int>(g_items), static_cast<int>(late2), static_cast<int>(ahead2)},
+          g_items ? std::max(before, even) : before};
 }
 
 // Parts of dh's K (the vocabulary): with few tiles of dh their long sums would be what
 // all else waits for.  Depends on the sizes alone, as do then the bits of dh.
-int dh_splits(int rows, int d, int cols, bool demb) {
+int dh_splits(int rows, int d, int cols, bool demb, bool more) {
   const int64_t tiles = static_cast<int64_t>(up_to(rows, kTile)) * up_to(d, kTile);
   const int64_t de_items = demb ? static_cast<int64_t>(up_to(cols, kTile)) * up_to(d, kTile) : 0;
+  const int64_t g_items = more ? static_cast<int64_t>(up_to(rows, kTile)) * up_to(cols, kTile) : 0;
   const int nk = up_to(cols, kK), de_nk = up_to(rows, kK);
   int best = 1;
   int64_t least = INT64_MAX;
-  for (int s = 1; s <= 16 && nk / s >= 8; ++s) {
-    // a part's 8 bytes an element through memory: 4 k-blocks' time a tile
-    const int64_t cost = balance(tiles * s, up_to(nk, s), de_items, de_nk, kPlanPairs).longest +
-                         (s > 1 ? 8 + 4 * s * tiles / kPlanPairs : 0);
+  for (int s = 1; s <= 64 && nk / s >= 8; ++s) {
+    // a part's 8 bytes an element through memory: 4 k-blocks' time a tile; the last kernel
+    // reads eight parts at a time, in about 2
+    const int64_t cost = plan(tiles * s, up_to(nk, s), de_items, de_nk, g_items, up_to(d, kK), kPlanPairs).longest +
+                         (s > 1 ? 8 + 4 * s * tiles / kPlanPairs + s / 4 : 0);
     if (cost < least) {
       least = cost;
       best = s;
@@ -849,7 +910,7 @@ int dh_splits(int rows, int d, int cols, bool demb) {
 }
 
 struct HeadScratch {
-  size_t parts, info, hm, g, dh, bytes;
+  size_t parts, info, hm, g, g2, dh, bytes;
   int cols, splits, rows_pad, ldm;
   bool direct;  // dh comes out of the products as it is
   bool keep;    // the first piece's powers are kept
@@ -859,7 +920,7 @@ HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads) {
   const size_t n = static_cast<size_t>(rows);
   HeadScratch s;
   s.cols = piece_columns(rows, vocab, piece);
-  s.splits = grads & 1 ? dh_splits(rows, d, s.cols, grads & 2) : 1;
+  s.splits = grads & 1 ? dh_splits(rows, d, s.cols, grads & 2, s.cols < vocab) : 1;
   s.rows_pad = up_to(rows, kTile) * kTile;
   s.direct = s.splits == 1 && s.cols >= vocab;
   // (a tile is made again for 256 rows, however few there are)
@@ -869,7 +930,8 @@ HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads) {
   s.info = up(n * (!grads && rows <= kFewRows ? 8 : 2) * up_to(vocab, kTile) * sizeof(float2));
   s.hm = s.info + (grads ? up(n * sizeof(HeadRow)) : 0);
   s.g = s.hm + (grads & 2 ? up(n * s.ldm * 2) : 0);
-  s.dh = s.g + (grads ? up(n * s.cols * 2) : 0);
+  s.g2 = s.g + (grads ? up(n * s.cols * 2) : 0);
+  s.dh = s.g2 + (grads && s.cols < vocab ? up(n * s.cols * 2) : 0);
   s.bytes = s.dh + ((grads & 1) && !s.direct ? up(static_cast<size_t>(s.splits) * s.rows_pad * d * 4) : 0);
   return s;
 }
@@ -930,8 +992,12 @@ int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, int
   cfg.attrs = attr;
   cfg.numAttrs = 3;
   HeadGemm b = a;
-  if (MODE == kProducts)
-    b.ahead = balance(a.dh_items, up_to(up_to(a.cols, kK), a.splits), a.de_items, up_to(a.row.rows, kK), pairs).ahead;
+  if (MODE == kProducts) {
+    const Plan p = plan(a.dh_items, up_to(up_to(a.cols, kK), a.splits), a.de.n, up_to(a.row.rows, kK), a.g.n,
+                        up_to(a.row.d, kK), pairs);
+    b.de = p.de;
+    b.g = p.g;
+  }
   (void)cudaLaunchKernelEx(&cfg, head_gemm_kernel<MODE>, maps, b, err);
   return check(MODE == kStats || MODE == kFew ? "stats" : (MODE == kGrad ? "gradient" : "products"));
 }
@@ -1038,47 +1104,62 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
     (void)launch_k(head_rows_kernel<1>, up_to(rows, 8), 256, 0, st, a, hb, ldh, e, in_parts, nparts, loss_rows,
                    rows_info, demb ? hm : nullptr, static_cast<int64_t>(at.ldm), err);
   if ((rc = check("rows"))) return rc;
-  for (int v0 = 0; grads && v0 < vocab; v0 += at.cols) {
-    const int cols = std::min(at.cols, vocab - v0);
+  __nv_bfloat16* now = g;
+  __nv_bfloat16* then = reinterpret_cast<__nv_bfloat16*>(w + at.g2);
+  q.n_tiles = up_to(std::min(at.cols, vocab), kTile);
+  if (grads) {
+    const int cols = std::min(at.cols, vocab);
+    if (at.keep) {
+      const int slabs = up_to(cols, 16 * 256);
+      (void)launch_k(head_scale_kernel, rows * slabs, 256, 0, st, cols, static_cast<int64_t>(at.cols), slabs,
+                     static_cast<const HeadRow*>(info), in_parts, nparts, reinterpret_cast<uint4*>(g));
+      if ((rc = check("scale"))) return rc;
+    } else {
+      q.cols = cols;
+      ok = head_map(&maps.b, emb, false, d, cols, d, kK, 128) && head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
+      if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
+      if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st))) return rc;
+    }
+  }
+  for (int v0 = 0; grads && v0 < vocab; v0 += at.cols, std::swap(now, then)) {
+    const int cols = std::min(at.cols, vocab - v0), next = v0 + cols;
     const auto* piece_of_e = e + static_cast<int64_t>(v0) * d;
     q.cols = cols;
     q.v0 = v0;
-    q.n_tiles = up_to(cols, kTile);
-    if (v0 == 0 && at.keep) {
-      const int slabs = up_to(cols, 16 * 256);
-      (void)launch_k(head_scale_kernel, rows * slabs, 256, 0, st, cols, static_cast<int64_t>(at.cols), slabs,
-                     static_cast<const HeadRow*>(info), static_cast<const float2*>(parts), nparts,
-                     reinterpret_cast<uint4*>(g));
-      if ((rc = check("scale"))) return rc;
-    } else {
-      maps.a = map_h;
-      ok = head_map(&maps.b, piece_of_e, false, d, cols, d, kK, 128) &&
-           head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
-      if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
-      if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st))) return rc;
+    q.g_v0 = next;
+    q.g_cols = std::min(at.cols, vocab - next);
+    q.g_tiles = up_to(q.g_cols, kTile);
+    q.g.n = q.m_tiles * q.g_tiles;
+    ok = true;
+    if (q.g.n) {
+      maps.a3 = map_h;
+      ok = head_map(&maps.b3, e + static_cast<int64_t>(next) * d, false, d, q.g_cols, d, kK, 128) &&
+           head_map(&maps.c3, then, false, q.g_cols, rows, at.cols, 32, 32);
     }
     q.n_tiles = up_to(d, kTile);
     q.splits = std::min(at.splits, up_to(cols, kK));
     q.rows_pad = at.rows_pad;
     q.dh_items = dh ? q.m_tiles * q.n_tiles * q.splits : 0;
-    q.de_items = demb ? up_to(cols, kTile) * q.n_tiles : 0;
+    q.de.n = demb ? up_to(cols, kTile) * q.n_tiles : 0;
     q.dh_out = at.direct ? kDhBf16 : (v0 ? kDhAdd : kDhStore);
     q.de_f32 = demb_dtype == DT_F32;
-    if (dh) {
-      ok = head_map(&maps.a, g, false, cols, rows, at.cols, kK, 128) &&
+    if (ok && dh) {
+      ok = head_map(&maps.a, now, false, cols, rows, at.cols, kK, 128) &&
            head_map(&maps.b, piece_of_e, false, d, cols, d, kK, kK) &&
            (at.direct ? head_map(&maps.c, dh, false, d, rows, lddh, 32, 32)
                       : head_map(&maps.c, dh32, true, d, static_cast<int64_t>(at.splits) * at.rows_pad, d, 32, 32));
     }
     if (ok && demb)
-      ok = head_map(&maps.a2, g, false, cols, rows, at.cols, kK, kK) &&
+      ok = head_map(&maps.a2, now, false, cols, rows, at.cols, kK, kK) &&
            head_map(&maps.b2, hm, false, d, rows, at.ldm, kK, kK) &&
            head_map(&maps.c2, demb, q.de_f32, d, vocab, d, 32, 32);
     if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
-    if ((rc = launch_head_gemm<kProducts>(maps, q, static_cast<int64_t>(q.dh_items) + q.de_items, err, st))) return rc;
+    const int64_t items = static_cast<int64_t>(q.dh_items) + q.de.n + q.g.n;
+    if ((rc = launch_head_gemm<kProducts>(maps, q, items, err, st))) return rc;
   }
   if (!dh || at.direct) return GPIPE_OK;
-  (void)launch_k(head_dh_kernel, up_to(rows, 8), 256, 0, st, rows, d, at.splits, at.rows_pad, inv_count,
+  const auto ctas = static_cast<unsigned>((static_cast<int64_t>(rows) * (d / 8) + 255) / 256);
+  (void)launch_k(head_dh_kernel, ctas, 256, 0, st, rows, d, at.splits, at.rows_pad, inv_count,
                  static_cast<const float*>(dh32), static_cast<const HeadRow*>(info), e, static_cast<__nv_bfloat16*>(dh),
                  lddh);
   return check("dh");

@@ -94,7 +94,7 @@ def test_head_scratch_bytes(b):
     up = lambda n: -(-n // 256) * 256  # noqa: E731
     rows, d, vocab = 1000, 712, 50001
     tiles = 196
-    info, copy, g = up(rows * 16), up(rows * 768 * 2), up(rows * 8192 * 2)
+    info, copy, g = up(rows * 16), up(rows * 768 * 2), 2 * up(rows * 8192 * 2)  # (several pieces: g of two)
     assert f(rows, d, vocab, 8192, 2) == up(rows * tiles * 16) + info + copy + g
     assert f(rows, d, vocab, 8000, 2) == f(rows, d, vocab, 8192, 2)
     with_dh = f(rows, d, vocab, 8192, 1) - (up(rows * tiles * 16) + info + g)
@@ -102,7 +102,8 @@ def test_head_scratch_bytes(b):
     # all of the vocabulary in one piece, however wide it is asked for
     assert f(64, 64, 1000, 1 << 20, 3) == f(64, 64, 1000, 1024, 3) == f(64, 64, 1000, 0, 3)
     # 256 MB of g at most, unless that is under 2048 columns
-    assert up(8192 * 16384 * 2) < f(8192, 64, 131072, 0, 2) < up(8192 * 16384 * 2) + 8192 * (512 * 16 + 16 + 128 + 64)
+    assert 2 ** 28 < f(8192, 64, 131072, 0, 2) < 2 ** 28 + 8192 * (512 * 16 + 16 + 128 + 64)
+    assert f(8192, 64, 131072, 0, 2) == f(8192, 64, 131072, 8192, 2)
     for bad in ((0, 64, 10, 0, 0), (1, 4, 10, 0, 0), (1, 64, 0, 0, 0), (1, 64, 10, -1, 0), (1, 64, 10, 0, 4),
                 (1, 64, 10, 0, -1), (1 << 24, 64, 1 << 27, 0, 0)):
         assert f(*bad) == 0
