@@ -294,7 +294,7 @@ int gpipe_op_embedding_scaled_fwd(int dtype, int rows, int d, int vocab, const i
 /* Its gradient: demb[tokens[r],:] += scale dx[r,:] (fp32 accumulator, dx of dtype
  * elements with leading dimension lddx).  The rows are sorted by token first, so
  * that a frequent token's are summed by many CTAs: in ascending r, cut where runs of
- * 8 or 32 sorted rows end, the parts in order, scaled once and added to demb.  Padding
+ * 8 or 64 sorted rows end, the parts in order, scaled once and added to demb.  Padding
  * and ids out of range as above, with no gradient.  (gpipe_op_embedding_bwd adds one
  * row after the other and needs no scratch.)
  * scratch: gpipe_op_embedding_sorted_bwd_scratch_bytes, 256-byte aligned, written

@@ -5,7 +5,7 @@
 // The gradient first sorts the rows by token, stably, so that the rows of one
 // token follow each other in ascending r (negative tokens and, after setting the
 // error flag, tokens of vocab or more get the key vocab and end up behind the
-// rest).  The sorted positions are cut into runs of 8 or 32; a group of threads
+// rest).  The sorted positions are cut into runs of 8 or 64; a group of threads
 // reads a run's rows one after the other, many in flight, and sums them by token in
 // order.  A token whose rows lie in one run is added to dE there; one that crosses
 // runs leaves a sum in each, which a last kernel adds in order and then to dE.  So a
@@ -26,12 +26,13 @@ namespace gp {
 namespace {
 
 constexpr int kShortRun = 8;     // sorted positions of a run: of few rows
-constexpr int kLongRun = 32;     // and of many
-constexpr int kLongRows = 16384;
+constexpr int kLongRun = 64;     // and of many
+constexpr int kLongRows = 24576;
 constexpr int kFewRows = 256;    // rows up to which one launch does all
 constexpr int kRankRows = 4096;  // rows up to which positions are counted by comparison
 constexpr int kDigit = 9;        // bits of a radix pass
 constexpr int kBins = 1 << kDigit;
+constexpr int kScatterThreads = 512;
 constexpr int kTile = 512;       // positions of a CTA of a radix pass, at least
 constexpr int kSortCtas = 128;   // and its CTAs, at most
 constexpr int kHalfRows = 1 << 18;  // rows up to which half of them
@@ -157,22 +158,22 @@ __global__ void __launch_bounds__(256) embed_count_kernel(int rows, int per, int
 }
 
 // Its keys to their places: behind all smaller digits, the same digit of earlier
-// CTAs and, in the CTA, of earlier warps (a warp has per / 8 consecutive positions)
-// and earlier lanes.  A warp's first 256 keys are read once, ahead of everything.  The
+// CTAs and, in the CTA, of earlier warps (a warp has per / 16 consecutive positions)
+// and earlier lanes.  A warp's first 128 keys are read once, ahead of everything.  The
 // next pass's counts (of whole numbers, so in any order) are made as the keys land.
-__global__ void __launch_bounds__(256) embed_scatter_kernel(int rows, int per, int vocab, int shift, bool first,
-                                                            const int* __restrict__ src,
-                                                            const int* __restrict__ src_order,
-                                                            const int* __restrict__ counts,
-                                                            int* __restrict__ next_counts, int* __restrict__ keys,
-                                                            int* __restrict__ order) {
+__global__ void __launch_bounds__(kScatterThreads) embed_scatter_kernel(
+    int rows, int per, int vocab, int shift, bool first, const int* __restrict__ src,
+    const int* __restrict__ src_order, const int* __restrict__ counts, int* __restrict__ next_counts,
+    int* __restrict__ keys, int* __restrict__ order) {
   griddep_wait();
   griddep_launch();
-  __shared__ __align__(16) int at[8][kBins], prior[8][kBins];
-  __shared__ int wsum[8];
-  constexpr int kOnce = 8;  // keys a lane keeps
+  constexpr int kWarps = kScatterThreads / 32;
+  static_assert(kScatterThreads == kBins, "thread t looks after bin t");
+  __shared__ int at[kWarps][kBins], total[kBins], prior[kBins];
+  __shared__ int wsum[kWarps];
+  constexpr int kOnce = 4;  // keys a lane keeps
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int seg = per / 8;
+  const int seg = per / kWarps;
   const int i0 = blockIdx.x * per + warp * seg, i1 = min(min(rows, static_cast<int>(blockIdx.x + 1) * per), i0 + seg);
   auto key_at = [&](int i) { return i < i1 ? key_of(src[i], first ? vocab : INT32_MAX) : -1; };
   auto row_at = [&](int i) { return i < i1 ? (src_order ? src_order[i] : i) : 0; };
@@ -182,13 +183,13 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(int rows, int per, i
     kept[e] = key_at(i0 + 32 * e + lane);
     rows_kept[e] = row_at(i0 + 32 * e + lane);
   }
-  // totals and those of earlier CTAs: a warp takes an eighth of the CTAs, a lane 16 bins
+  // totals and those of earlier CTAs: a warp takes a sixteenth of the CTAs, a lane 16 bins
   {
     int4 all[4], earlier[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) all[u] = earlier[u] = make_int4(0, 0, 0, 0);
 #pragma unroll 4
-    for (int c = warp; c < static_cast<int>(gridDim.x); c += 8) {
+    for (int c = warp; c < static_cast<int>(gridDim.x); c += kWarps) {
       const int in = c < static_cast<int>(blockIdx.x) ? ~0 : 0;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -203,35 +204,23 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(int rows, int per, i
         earlier[u].w += n.w & in;
       }
     }
+    total[tid] = 0;
+    prior[tid] = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) at[w][tid] = 0;
+    __syncthreads();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      *reinterpret_cast<int4*>(&at[warp][u * 128 + lane * 4]) = all[u];
-      *reinterpret_cast<int4*>(&prior[warp][u * 128 + lane * 4]) = earlier[u];
+      const int b = u * 128 + lane * 4;
+      const int4 n = all[u], e = earlier[u];
+      const int nn[4] = {n.x, n.y, n.z, n.w}, ee[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (nn[j]) atomicAdd(&total[b + j], nn[j]);
+        if (ee[j]) atomicAdd(&prior[b + j], ee[j]);
+      }
     }
   }
-  __syncthreads();
-  int total[2] = {0, 0}, before[2] = {0, 0};  // of thread t's bins 2t and 2t + 1
-#pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const int2 n = *reinterpret_cast<const int2*>(&at[w][2 * tid]), e = *reinterpret_cast<const int2*>(&prior[w][2 * tid]);
-    total[0] += n.x;
-    total[1] += n.y;
-    before[0] += e.x;
-    before[1] += e.y;
-  }
-  __syncthreads();
-  int sum = total[0] + total[1];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += up;
-  }
-  if (lane == 31) wsum[warp] = sum;
-  for (int b = tid; b < 8 * kBins; b += 256) (&at[0][0])[b] = 0;
-  __syncthreads();
-  int base = sum - total[0] - total[1];
-  for (int w = 0; w < warp; ++w) base += wsum[w];
-
   // the warps' counts, 32 keys at a time
   auto count = [&](int k) {
     const int bin = k < 0 ? kBins : (k >> shift) & (kBins - 1);
@@ -244,14 +233,22 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(int rows, int per, i
     if (32 * e < seg) count(kept[e]);
   for (int i = i0 + 32 * kOnce; i < i1; i += 32) count(key_at(i + lane));
   __syncthreads();
+  const int mine = total[tid];
+  int sum = mine;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    int next = base + before[e] + (e ? total[0] : 0);
-    for (int w = 0; w < 8; ++w) {
-      const int n = at[w][2 * tid + e];
-      at[w][2 * tid + e] = next;
-      next += n;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += up;
+  }
+  if (lane == 31) wsum[warp] = sum;
+  __syncthreads();
+  int next = sum - mine + prior[tid];
+  for (int w = 0; w < warp; ++w) next += wsum[w];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int n = at[w][tid];
+    at[w][tid] = next;
+    next += n;
   }
   __syncthreads();
   auto place = [&](int k, int row) {
@@ -440,7 +437,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(int rows, int d, int voc
 // 128 columns, which adds the runs' sums in order.  The others take a CTA for every 128
 // columns, whose warps add an eighth of the runs each, in order, and then those.
 template <int RUN>
-__global__ void __launch_bounds__(256) embed_join_kernel(int rows, int d, const int* __restrict__ keys, float scale,
+__global__ void __launch_bounds__(256, 6) embed_join_kernel(int rows, int d, const int* __restrict__ keys, float scale,
                                                          float* __restrict__ demb, const float* __restrict__ partial,
                                                          const int* __restrict__ joins) {
   griddep_wait();
@@ -449,7 +446,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(int rows, int d, const 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto add_runs = [&](int b, bool whole, int j0, int j1, int c) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
     for (int j = j0; j < j1; ++j) {
       const int64_t slot = static_cast<int64_t>(b + j) * 2 + (j == 0 && !whole ? 1 : 0);
       const float4 v = *reinterpret_cast<const float4*>(partial + slot * d + c);
@@ -460,25 +457,9 @@ __global__ void __launch_bounds__(256) embed_join_kernel(int rows, int d, const 
     }
     return a;
   };
-  const int few = joins[0];
-  for (int i = blockIdx.x; i < few; i += gridDim.x) {
-    const int b = joins[2 + i];
-    const int next = (b + 1) * RUN;  // the next run's first position, which has the token
-    const int k = keys[next];
-    const bool whole = keys[next - RUN] == k;  // slot 0 of its first run: it starts there
-    int n = 2;                                 // its runs
-#pragma unroll
-    for (int e = 0; e < kManyRuns; e += 32) {
-      const int64_t at = next + static_cast<int64_t>(1 + e + lane) * RUN;
-      n += __popc(__ballot_sync(0xffffffffu, at < rows && keys[at] == k));
-    }
-    for (int c = warp * 128 + lane * 4; c < d; c += 1024) {
-      const float4 a = add_runs(b, whole, 0, n, c);
-      add_to(demb + static_cast<int64_t>(k) * d + c, scale * a.x, scale * a.y, scale * a.z, scale * a.w);
-    }
-  }
   const int many = joins[1], slabs = (d + 127) / 128, runs = (rows + RUN - 1) / RUN;
-  for (int64_t u = blockIdx.x; u < static_cast<int64_t>(many) * slabs; u += gridDim.x) {
+  // (from the last CTA on, as the others' first ones take longest)
+  for (int64_t u = gridDim.x - 1 - blockIdx.x; u < static_cast<int64_t>(many) * slabs; u += gridDim.x) {
     const int b = joins[1 + runs - static_cast<int>(u / slabs)], c0 = static_cast<int>(u % slabs) * 128;
     const int next = (b + 1) * RUN;
     const int k = keys[next];
@@ -502,6 +483,23 @@ __global__ void __launch_bounds__(256) embed_join_kernel(int rows, int d, const 
       demb[static_cast<int64_t>(k) * d + c0 + tid] += scale * t;
     }
     __syncthreads();
+  }
+  const int few = joins[0];
+  for (int i = blockIdx.x; i < few; i += gridDim.x) {
+    const int b = joins[2 + i];
+    const int next = (b + 1) * RUN;  // the next run's first position, which has the token
+    const int k = keys[next];
+    const bool whole = keys[next - RUN] == k;  // slot 0 of its first run: it starts there
+    int n = 2;                                 // its runs
+#pragma unroll
+    for (int e = 0; e < kManyRuns; e += 32) {
+      const int64_t at = next + static_cast<int64_t>(1 + e + lane) * RUN;
+      n += __popc(__ballot_sync(0xffffffffu, at < rows && keys[at] == k));
+    }
+    for (int c = warp * 128 + lane * 4; c < d; c += 1024) {
+      const float4 a = add_runs(b, whole, 0, n, c);
+      add_to(demb + static_cast<int64_t>(k) * d + c, scale * a.x, scale * a.y, scale * a.z, scale * a.w);
+    }
   }
 }
 
@@ -625,7 +623,7 @@ int launch_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int
       int bits = 1;
       while (bits < 31 && (vocab >> bits) != 0) ++bits;  // keys 0 .. vocab
       const int ctas = std::min(rows <= kHalfRows ? kSortCtas / 2 : kSortCtas, (rows + kTile - 1) / kTile);
-      const int per = ((rows + ctas - 1) / ctas + 255) / 256 * 256;
+      const int per = ((rows + ctas - 1) / ctas + 511) / 512 * 512;
       const int grid = (rows + per - 1) / per;
       const int passes = (bits + kDigit - 1) / kDigit;
       (void)launch_k(embed_count_kernel, grid, 256, 0, s, rows, per, vocab, passes, tokens, counts, joins, err);
@@ -636,7 +634,7 @@ int launch_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int
         const int* now = counts + static_cast<int64_t>(p) * kSortCtas * kBins;
         int* then = p + 1 < passes ? counts + static_cast<int64_t>(p + 1) * kSortCtas * kBins : nullptr;
         have = p & 1;
-        (void)launch_k(embed_scatter_kernel, grid, 256, 0, s, rows, per, vocab, p * kDigit, p == 0, src, src_order,
+        (void)launch_k(embed_scatter_kernel, grid, kScatterThreads, 0, s, rows, per, vocab, p * kDigit, p == 0, src, src_order,
                        now, then, keys[have], order[have]);
         if (const int rc = check("embedding_sorted_bwd")) return rc;
         src = keys[have];

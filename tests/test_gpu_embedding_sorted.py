@@ -105,7 +105,7 @@ GRADS = [(1, 8, 1, "uniform"), (2, 8, 1, "one"), (19, 64, 517, "uniform"), (31, 
          (1000, 712, 50, "text"), (2048, 1024, 32000, "uniform"), (4097, 512, 300, "text"), (8192, 64, 1000, "text"),
          (8193, 64, 1000, "text"), (9001, 136, 511, "uniform"), (9001, 136, 512, "padded"), (10000, 64, 7, "one"),
          (20000, 256, 131072, "text"), (40000, 64, 262143, "backwards"), (70001, 72, 900, "sorted"),
-         (16384, 1024, 40, "padded"), (16385, 1096, 40, "padded"), (300000, 16, 50000, "text"), (9000, 24, 400000, "uniform")]
+         (24576, 264, 40, "padded"), (24577, 1096, 40, "padded"), (300000, 16, 50000, "text"), (9000, 24, 400000, "uniform")]
 
 
 @gpu

@@ -193,10 +193,10 @@ def test_embedding_scratch_bytes(b):
     up = lambda n: -(-n // 256) * 256  # noqa: E731
 
     def want(rows, d):
-        run = 8 if rows <= 16384 else 32
+        run = 8 if rows <= 24576 else 64
         runs = -(-rows // run)
-        return 4 * up((rows + 32) * 4) + 4 * 128 * 512 * 4 + up((runs + 2) * 4) + up(runs * 2 * d * 4)
-    for rows, d in ((1, 8), (19, 64), (16384, 1024), (16385, 1024), (131072, 512)):
+        return 4 * up((rows + 64) * 4) + 4 * 128 * 512 * 4 + up((runs + 2) * 4) + up(runs * 2 * d * 4)
+    for rows, d in ((1, 8), (19, 64), (24576, 1024), (24577, 1024), (131072, 512)):
         assert f(rows, d, 1000) == want(rows, d) == f(rows, d, 1)
     for bad in ((0, 64, 10), (1, 12, 10), (1, 64, 0), (1, 64, (1 << 30) + 1)):
         assert f(*bad) == 0
