@@ -249,7 +249,9 @@ int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t
  * a negative id means that the row has none, one of vocab or more too, and sets
  * the device error flag.  w_r = row_weight[r] (fp32 [rows]; NULL: 1).  A row
  * without a target or of weight 0 has loss 0, a zero row of dh and no part in demb;
- * its h is not used and may hold anything (NaN included).
+ * its h is not used and may hold anything (NaN included).  Logits of other rows keep
+ * their differences up to 2^24 in size; a NaN or an infinity shows in its own row's
+ * loss and dh, and in demb.
  * piece     columns of the vocabulary that a launch works on (rounded up to a multiple
  *           of 256): more scratch and fewer launches with more of them.  g exists for
  *           one piece at a time, for two where the vocabulary takes several.  0: as

@@ -224,3 +224,35 @@ def test_both_ends_of_a_tied_model_together(b):
     ref = w0 - 1e-3 * g0 / ((0.1 * g0 * g0).sqrt() + 1e-8)
     assert float((w.double() - ref).abs().max()) <= 1e-6 and float(grad.abs().max()) == 0
     assert torch.equal(emb, w.bfloat16()) and error(b) == 0
+
+
+@gpu
+@pytest.mark.parametrize("f32", [False, True])
+def test_more_than_2_to_the_31_elements(b, f32):
+    """Table, rows and accumulator beyond 32-bit offsets, with the tokens and rows that count at their ends."""
+    import torch
+    vocab, d, rows = 530000, 4096, 530000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    emb = torch.zeros(vocab, d, device="cuda", dtype=torch.bfloat16)
+    tokens = torch.full((rows,), -1, device="cuda", dtype=torch.int32)
+    at = torch.tensor([0, 1, 262143, 262144, 524287, 524288, rows - 2, rows - 1], device="cuda")
+    ids = torch.tensor([vocab - 1, 3, vocab - 1, vocab - 2, 524288, 3, vocab - 1, 524287], device="cuda", dtype=torch.int32)
+    tokens[at] = ids
+    emb[ids.long()] = torch.randn(8, d, generator=g, device="cuda").bfloat16()
+    x = lookup(b, tokens, emb, 1.5, f32)
+    want = emb[ids.long()].float() * 1.5
+    assert torch.equal(x[at], want if f32 else want.bfloat16())
+    assert float(x[2:262143].abs().max()) == 0 and float(x[524289:rows - 2].abs().max()) == 0
+    del emb
+    before = torch.zeros(vocab, d, device="cuda")
+    before[-1] = 1.0
+    x[tokens < 0] = float("nan")
+    gradient(b, tokens, x, d, before, 0.5)
+    total = torch.zeros(vocab, dtype=torch.float64, device="cuda")
+    for i in ids.unique().long().tolist():
+        rows_of = x[at[ids == i]].double()
+        want = (1.0 if i == vocab - 1 else 0.0) + 0.5 * rows_of.sum(0)
+        tol = U * (3 * rows_of.abs().sum(0) + 2 * want.abs() + 1)
+        assert float(((before[i].double() - want).abs() - tol).max()) <= 0
+        total[i] = 1
+    assert float(before[total == 0].abs().max()) == 0

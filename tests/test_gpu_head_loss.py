@@ -241,6 +241,42 @@ def test_large_logits(b):
 
 
 @gpu
+@pytest.mark.parametrize("rows", [20, 64, 65, 300])
+@pytest.mark.parametrize("grads", ["none", "both"])
+def test_huge_logits_with_ties(b, rows, grads):
+    """Logits that are whole multiples of 2^18 up to 2^24, exact in fp32: p is 1 / k for the k largest and 0 otherwise, and
+    the loss a multiple of 2^18 plus ln k, to 8 roundings of its size.  (20 rows: the powers kept; 300: z made again.)"""
+    import torch
+    d, vocab = 64, 1000
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    h = (torch.randint(-1, 2, (rows, d), generator=g, device="cuda").float() * 2.0 ** 10)
+    emb = (torch.randint(-1, 2, (vocab, d), generator=g, device="cuda").float() * 2.0 ** 8)
+    emb[1::2] = emb[::2]                      # every logit twice
+    h[0], emb[10], emb[11] = 2.0 ** 10, 2.0 ** 8, 2.0 ** 8   # 2^24 itself
+    tokens = torch.randint(0, vocab, (rows + 1,), generator=g, device="cuda", dtype=torch.int32)
+    z = h.double() @ emb.double().T
+    tokens[2::3] = z.argmax(1)[1::3].to(torch.int32)  # some targets among the largest
+    p = dict(rows=rows, d=d, vocab=vocab, seq=rows + 1, emb=emb.bfloat16(), tokens=tokens, h=h.bfloat16(), weight=None)
+    o = call(b, p, grads=grads, inv=1.0)
+    t, n = tokens[1:].long(), torch.arange(rows, device="cuda")
+    logp = torch.log_softmax(z, 1)
+    loss = -logp[n, t]
+    assert float(((o["loss"].double() - loss).abs() - 8 * U * (loss.abs() + z.abs().amax(1)) - 2.0 ** -18).max()) <= 0
+    small = loss < 100
+    assert bool(small.any()) and float((o["loss"].double() - loss)[small].abs().max()) <= 2.0 ** -18
+    if grads == "none":
+        return
+    grad = logp.exp()
+    grad[n, t] -= 1
+    e, hd = emb.double(), h.double()
+    slack = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18
+    dh, demb = grad @ e, grad.T @ hd
+    assert float(((o["dh"].double() - dh).abs() - slack * (grad.abs() @ e.abs()) - 2.0 ** -8 * dh.abs()).max()) <= 0
+    tol = slack * (grad.abs().T @ hd.abs()) + 2.0 ** -8 * demb.abs()
+    assert float(((o["demb"].double() - demb).abs() - tol).max()) <= 0
+
+
+@gpu
 def test_nan_and_inf_in_rows_that_count(b):
     """They show in their own row's loss and dh, and in no other row's."""
     import torch
@@ -329,3 +365,98 @@ def test_gradients_against_differences(b):
         scale = float((grad.double().abs() * move.abs()).sum())
         assert abs(float((hi - lo) / 2 - want)) <= 0.02 * scale + 1e-3, (name, float((hi - lo) / 2), float(want), scale,
                                                                          float(off.abs().max()))
+
+
+@gpu
+@pytest.mark.parametrize("grads", ["none", "h", "both"])
+@pytest.mark.parametrize("rows,d,vocab,piece", [(40, 64, 3000, 1024), (300, 800, 2000, 0), (700, 128, 9000, 2048)])
+def test_calls_in_a_row_that_write_each_others_inputs(b, grads, rows, d, vocab, piece):
+    """Launches overlap their predecessors: hidden states, table and tokens that a kernel of the library writes right
+    before a call and right after it, against the same calls one at a time."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    tables = [(torch.randn(vocab, d, generator=g, device="cuda") / d ** 0.5) for _ in range(3)]
+    p = make(rows, d, vocab, 37)
+    source = [torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int32) for _ in range(3)]
+
+    def chain(wait):
+        got, emb, h = [], torch.empty_like(p["emb"]), torch.empty_like(p["h"])
+        q = dict(p, emb=emb, h=h)
+        buf = call(b, dict(p), piece, grads=grads)  # (its scratch and outputs are used again)
+        lib, stream = b.lib(), b.current_stream()
+        for i in range(6):
+            b._check(lib.gpipe_op_cast_bf16(emb.numel(), tables[i % 3].data_ptr(), emb.data_ptr(), stream))
+            b._check(lib.gpipe_op_embedding_scaled_fwd(1, rows, d, vocab, source[(i + 1) % 3].data_ptr(), emb.data_ptr(),
+                                                       3.0, h.data_ptr(), d, stream))
+            if wait:
+                torch.cuda.synchronize()
+            call(b, q, piece, grads=grads, buf=buf)
+            if wait:
+                torch.cuda.synchronize()
+            keep = {}
+            for k in ("loss", "dh", "demb"):
+                if buf[k] is not None:  # copied by a kernel of torch's, which waits for the call to end
+                    keep[k] = buf[k].clone()
+            got.append(keep)
+        torch.cuda.synchronize()
+        return got
+    for one, other in zip(chain(True), chain(False)):
+        for k in one:
+            assert torch.equal(one[k], other[k]), k
+    # and without a foreign kernel between the calls
+    alone, emb, h = [], torch.empty_like(p["emb"]), torch.empty_like(p["h"])
+    lib, stream = b.lib(), b.current_stream()
+    bufs = [call(b, dict(p), piece, grads=grads) for _ in range(6)]
+    torch.cuda.synchronize()
+    for i in range(6):
+        b._check(lib.gpipe_op_cast_bf16(emb.numel(), tables[i % 3].data_ptr(), emb.data_ptr(), stream))
+        b._check(lib.gpipe_op_embedding_scaled_fwd(1, rows, d, vocab, source[(i + 1) % 3].data_ptr(), emb.data_ptr(), 3.0,
+                                                   h.data_ptr(), d, stream))
+        alone.append(call(b, dict(p, emb=emb, h=h), piece, grads=grads, buf=bufs[i]))
+    torch.cuda.synchronize()
+    for one, other in zip(chain(True), alone):
+        for k in one:
+            assert torch.equal(one[k], other[k]), k
+
+
+@gpu
+@pytest.mark.parametrize("f32", [False, True])
+def test_a_table_of_more_than_2_to_the_31_elements(b, f32):
+    """Targets at both ends; h near 0, so that p is about 1 / vocab everywhere but at the target, and the rows of dE can be
+    checked where they matter without the whole of it in 64 bits."""
+    import torch
+    rows, d, vocab = 24, 8192, 270001
+    g = torch.Generator(device="cuda").manual_seed(7)
+    emb = torch.empty(vocab, d, device="cuda", dtype=torch.bfloat16)
+    for r0 in range(0, vocab, 20000):
+        emb[r0:r0 + 20000] = (torch.randn(emb[r0:r0 + 20000].shape, generator=g, device="cuda") / d ** 0.5).bfloat16()
+    tokens = torch.randint(0, vocab, (rows + 1,), generator=g, device="cuda", dtype=torch.int32)
+    tokens[1], tokens[2], tokens[3] = vocab - 1, vocab - 2, 0
+    h = torch.randn(rows, d, generator=g, device="cuda").bfloat16()
+    p = dict(rows=rows, d=d, vocab=vocab, seq=rows + 1, emb=emb, tokens=tokens, h=h, weight=None)
+    demb = torch.ones(vocab, d, device="cuda") if f32 else None
+    o = call(b, p, piece=65536, f32=f32, demb=demb, inv=1.0)
+    z = torch.cat([h.double() @ emb[r0:r0 + 20000].double().T for r0 in range(0, vocab, 20000)], 1)
+    t = tokens[1:].long()
+    logp = torch.log_softmax(z, 1)
+    n = torch.arange(rows, device="cuda")
+    dz = 2 * d * U * float((h.double().abs() @ emb[t].double().abs().T).max()) * 2
+    assert float((o["loss"].double() + logp[n, t]).abs().max()) <= 2 * dz + 2.0 ** -18
+    grad = logp.exp()
+    grad[n, t] -= 1
+    dh = torch.zeros(rows, d, device="cuda", dtype=torch.float64)
+    size = torch.zeros_like(dh)
+    for r0 in range(0, vocab, 20000):
+        e = emb[r0:r0 + 20000].double()
+        dh += grad[:, r0:r0 + 20000] @ e
+        size += grad[:, r0:r0 + 20000].abs() @ e.abs()
+    slack = 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -11 + 4 * dz + 2.0 ** -18
+    assert float(((o["dh"].double() - dh).abs() - (slack * size + 2.0 ** -8 * dh.abs())).max()) <= 0
+    at = torch.cat([t, torch.tensor([1, 65535, 65536, 262143, 262144, vocab - 3], device="cuda")])
+    want = grad[:, at].T @ h.double()
+    tol = slack * (grad[:, at].abs().T @ h.double().abs()) + 2.0 ** -36
+    if f32:
+        want, tol = want + 1, tol + 8 * U * (want.abs() + 1)
+    else:
+        tol = tol + 2.0 ** -8 * want.abs()
+    assert float(((o["demb"][at].double() - want).abs() - tol).max()) <= 0
