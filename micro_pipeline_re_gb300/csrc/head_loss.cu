@@ -7,6 +7,7 @@
 //   g = w_r (p - onehot(t)),                 dh = a g E,  dE = a g^T h
 //
 // Launches:
+//      head_copy_kernel           (large calls whose h is not on 32-byte rows) a copy
 //   1  head_gemm_kernel<kStats>   z tile by tile in tensor memory; of every row and
 //                                 128 columns only (rho, sum 2^{z log2 e - rho}) leaves.
 //                                 With gradients, the first piece's powers go to where
@@ -120,6 +121,10 @@ constexpr int kGroup = 16;     // row tiles that the tiles in flight share
 // gradients over 32000 columns 2048 rows take 207 us kept and 188 made again at d = 512, 248
 // and 259 at 768, 297 and 321 at 1024; 512 rows 73 and 70, 97 and 97, 105 and 107
 constexpr int kKeepWidth = 768;
+// rows x vocab x d from which h is copied where its rows do not start on 32 bytes, the L2's
+// sectors: 2048 x 712 x 32000 take 76 us to read it as it is and 63 from rows of 768 (720
+// columns 61; 1016 and 1024 97 and 80), the copy about 3.  That E's rows lie like that hardly tells.
+constexpr int64_t kCopyWork = int64_t{1} << 33;
 constexpr int kWideRows = 1216;  // rows up to which each has a CTA to join its sums (eight an SM)
 constexpr int kPlanPairs = 76; // pairs of SMs that the split of dh's K is planned for (any number runs it)
 
@@ -376,10 +381,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   cluster_sync();  // both CTAs' barriers exist before any copy or arrival names them
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  // global memory from here on.  The gradient pass's products read only h and E, which no
-  // launch of this call writes and which were there before its first one began (the
-  // launches before this one let it start only after their own wait); its epilogue waits
-  // for what it reads, the rows, and for the readers of what it writes.
+  // global memory from here on.  The gradient pass's products read only h (or its copy) and
+  // E, which were there before the stats kernel's wait ended and which no launch behind that
+  // wait writes (each lets the next one start only after its own wait, or after that of the
+  // stats kernel); its epilogue waits for what it reads, the rows, and for the readers of
+  // what it writes.
   if (MODE != kGrad) griddep_wait();
 
   Walk<MODE> walk(pair, pairs);
@@ -689,6 +695,22 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   }
 }
 
+// h with the rows that count for nothing set to zero, in rows that start on 128 bytes; a
+// warp a row.
+__global__ void __launch_bounds__(256) head_copy_kernel(HeadArgs a, const __nv_bfloat16* __restrict__ h, int64_t ldh,
+                                                        __nv_bfloat16* __restrict__ hm, int64_t ldm) {
+  griddep_wait();
+  griddep_launch();
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= a.rows) return;
+  float w;
+  const bool live = head_target(a, r, w, nullptr) >= 0;
+#pragma unroll 4
+  for (int c = lane * 8; c < a.d; c += 256)
+    *reinterpret_cast<uint4*>(hm + r * ldm + c) =
+        live ? *reinterpret_cast<const uint4*>(h + r * ldh + c) : make_uint4(0, 0, 0, 0);
+}
+
 // W warps per row: they join the row's sums, take the target's logit as a dot product, the
 // loss, what the gradient pass needs, and (hm not NULL) h with the rows that count for
 // nothing set to zero.
@@ -927,8 +949,9 @@ struct HeadScratch {
   int cols, splits, rows_pad, ldm;
   bool direct;  // dh comes out of the products as it is
   bool keep;    // the first piece's powers are kept
+  bool copy;    // the products read a copy of h
 };
-HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads) {
+HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads, bool apart) {
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   const size_t n = static_cast<size_t>(rows);
   HeadScratch s;
@@ -942,7 +965,8 @@ HeadScratch head_scratch(int rows, int d, int vocab, int piece, int grads) {
   s.parts = 0;
   s.info = up(n * (!grads && rows <= kFewRows ? 8 : 2) * up_to(vocab, kTile) * sizeof(float2));
   s.hm = s.info + (grads ? up(n * sizeof(HeadRow)) : 0);
-  s.g = s.hm + (grads & 2 ? up(n * s.ldm * 2) : 0);
+  s.copy = apart && rows > kFewRows && static_cast<int64_t>(rows) * vocab >= kCopyWork / d;
+  s.g = s.hm + (s.copy || (grads & 2) ? up(n * s.ldm * 2) : 0);
   s.g2 = s.g + (grads ? up(n * s.cols * 2) : 0);
   s.dh = s.g2 + (grads && s.cols < vocab ? up(n * s.cols * 2) : 0);
   s.bytes = s.dh + ((grads & 1) && !s.direct ? up(static_cast<size_t>(s.splits) * s.rows_pad * d * 4) : 0);
@@ -1019,7 +1043,7 @@ int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, int
 
 size_t head_loss_scratch_bytes(int rows, int d, int vocab, int piece, int grads) {
   if (!sizes_ok(rows, d, vocab, piece) || grads < 0 || grads > 3) return 0;
-  return head_scratch(rows, d, vocab, piece, grads).bytes;
+  return head_scratch(rows, d, vocab, piece, grads, true).bytes;  // (h may lie in any way)
 }
 
 int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, const void* emb, int seq,
@@ -1049,7 +1073,8 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256)
     return set_error(GPIPE_ERR_INVALID_ARG, "head_loss: scratch must be 256-B aligned");
   const int grads = (dh ? 1 : 0) | (demb ? 2 : 0);
-  const HeadScratch at = head_scratch(rows, d, vocab, piece, grads);
+  const bool apart = (reinterpret_cast<uintptr_t>(h) | static_cast<uintptr_t>(ldh) * 2) % 32 != 0;
+  const HeadScratch at = head_scratch(rows, d, vocab, piece, grads, apart);
   const size_t n = static_cast<size_t>(rows), table = static_cast<size_t>(vocab) * d;
   const Range in[4] = {{h, ((n - 1) * ldh + d) * 2},
                        {emb, table * 2},
@@ -1089,7 +1114,14 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   const bool few = !grads && rows <= kFewRows;
   const int nparts = (few ? 8 : 2) * q.n_tiles;
   CUtensorMap map_h;
-  bool ok = head_map(&map_h, h, false, d, rows, ldh, kK, few ? kFewRows / 2 : 128) &&
+  int rc;
+  if (at.copy) {
+    (void)launch_k(head_copy_kernel, up_to(rows, 8), 256, 0, st, a, static_cast<const __nv_bfloat16*>(h), ldh, hm,
+                   static_cast<int64_t>(at.ldm));
+    if ((rc = check("copy"))) return rc;
+  }
+  // (kFew has h as the other operand, in boxes of its own; it is never copied)
+  bool ok = head_map(&map_h, at.copy ? hm : h, false, d, rows, at.copy ? at.ldm : ldh, kK, few ? kFewRows / 2 : 128) &&
             head_map(&maps.b, emb, false, d, vocab, d, kK, 128);
   if (ok && at.keep) {
     q.keep = at.cols;
@@ -1097,7 +1129,6 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   }
   if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
   maps.a = map_h;
-  int rc;
   if (few) {  // the vocabulary as rows
     std::swap(maps.a, maps.b);
     std::swap(q.m_tiles, q.n_tiles);
@@ -1109,13 +1140,14 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   const auto* hb = static_cast<const __nv_bfloat16*>(h);
   const float2* in_parts = parts;
   HeadRow* rows_info = grads ? info : nullptr;
+  __nv_bfloat16* to_copy = demb && !at.copy ? hm : nullptr;
   // with few rows a warp each would take long over their sums: 3 rows over 128616 columns 14 us
   if (rows <= kWideRows && nparts >= 128)
     (void)launch_k(head_rows_kernel<8>, rows, 256, 0, st, a, hb, ldh, e, in_parts, nparts, loss_rows, rows_info,
-                   demb ? hm : nullptr, static_cast<int64_t>(at.ldm), err);
+                   to_copy, static_cast<int64_t>(at.ldm), err);
   else
     (void)launch_k(head_rows_kernel<1>, up_to(rows, 8), 256, 0, st, a, hb, ldh, e, in_parts, nparts, loss_rows,
-                   rows_info, demb ? hm : nullptr, static_cast<int64_t>(at.ldm), err);
+                   rows_info, to_copy, static_cast<int64_t>(at.ldm), err);
   if ((rc = check("rows"))) return rc;
   __nv_bfloat16* now = g;
   __nv_bfloat16* then = reinterpret_cast<__nv_bfloat16*>(w + at.g2);
@@ -1129,7 +1161,8 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
       if ((rc = check("scale"))) return rc;
     } else {
       q.cols = cols;
-      ok = head_map(&maps.b, emb, false, d, cols, d, kK, 128) && head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
+      ok = (cols == vocab || head_map(&maps.b, emb, false, d, cols, d, kK, 128)) &&
+           head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
       if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
       if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st))) return rc;
     }

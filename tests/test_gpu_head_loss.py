@@ -156,6 +156,12 @@ FORMS = [
     (2048, 1024, 4000, 512, 0, 0.0, False, "both", False),
     (3000, 96, 700, 1000, 0, 0.0, False, "both", False),
     (4100, 320, 513, 64, 256, 0.0, True, "both", True),
+    (2048, 712, 6001, 90, 0, 0.0, True, "both", False),
+    (2048, 712, 6001, 90, 2048, 5.0, True, "both", True),
+    (3000, 136, 22000, 1000, 0, 0.0, True, "none", False),
+    (64, 1032, 131073, 50, 0, 0.0, False, "none", False),
+    (65, 1032, 131073, 50, 0, 0.0, True, "none", False),
+    (3000, 264, 11000, 1000, 0, 0.0, False, "h", False),
 ]
 
 

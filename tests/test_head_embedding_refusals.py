@@ -97,7 +97,8 @@ def test_head_scratch_bytes(b):
     info, copy, g = up(rows * 16), up(rows * 768 * 2), 2 * up(rows * 8192 * 2)  # (several pieces: g of two)
     assert f(rows, d, vocab, 8192, 2) == up(rows * tiles * 16) + info + copy + g
     assert f(rows, d, vocab, 8000, 2) == f(rows, d, vocab, 8192, 2)
-    with_dh = f(rows, d, vocab, 8192, 1) - (up(rows * tiles * 16) + info + g)
+    # (a copy of h: for dE, and for any large call, whose h may not lie on 32-byte rows)
+    with_dh = f(rows, d, vocab, 8192, 1) - (up(rows * tiles * 16) + info + copy + g)
     assert with_dh > 0 and with_dh % (1024 * d * 4) == 0          # parts of 1024 rows
     # all of the vocabulary in one piece, however wide it is asked for
     assert f(64, 64, 1000, 1 << 20, 3) == f(64, 64, 1000, 1024, 3) == f(64, 64, 1000, 0, 3)
