@@ -923,7 +923,8 @@ Plan plan(int64_t dh_items, int dh_nk, int64_t de_items, int de_nk, int64_t g_it
 }
 
 // Parts of dh's K (the vocabulary): with few tiles of dh their long sums would be what
-// all else waits for.  Depends on the sizes alone, as do then the bits of dh.
+// all else waits for.  Depends on the sizes and on whether dE is wanted, as do then the bits
+// of dh.
 int dh_splits(int rows, int d, int cols, bool demb, bool more) {
   const int64_t tiles = static_cast<int64_t>(up_to(rows, kTile)) * up_to(d, kTile);
   const int64_t de_items = demb ? static_cast<int64_t>(up_to(cols, kTile)) * up_to(d, kTile) : 0;
