@@ -28,8 +28,8 @@
 // logit is a dot product of its own in fp32 (tensor cores truncate as they add: 1024
 // terms left z_t up to 2e-5 short, which showed in the loss; this way 1e-7).  So
 //   loss = log1p(sum_{v != t} e^{z_v - z_t}),  g_t = -w sum_{v != t} p_v
-// keep their digits where p_t is close to 1 (dh gets back what g_t loses to its rounding,
-// which would be an error of the whole row).  g is rounded to bf16, relative to
+// keep their digits where p_t is close to 1 (dh, and dE of up to 64 rows, get back what g_t
+// loses to its rounding, which would be an error of a whole row).  g is rounded to bf16, relative to
 // each value, as gpipe_op_cross_entropy rounds its dz; inv_count multiplies the
 // finished fp32 sums, so that g_t, close to -w for most rows, is close to a whole number
 // and its rounding does not add up over the rows.
@@ -139,7 +139,8 @@ struct HeadCfg {
   static constexpr int kStages = MODE == kProducts ? 5 : (MODE == kFew ? 9 : 6);
   static constexpr int kOffBox = kStages * kStage;
   static constexpr int kOffBar = kOffBox + 8 * 2 * kBox;
-  static constexpr int kSmem = 1024 + kOffBar + 512;
+  static constexpr int kOffRest = kOffBar + 512;  // kProducts: (target, rest) of up to kFewRows rows
+  static constexpr int kSmem = 1024 + kOffRest + (MODE == kProducts ? kFewRows * 8 : 0);
   static_assert(kOffBar % 8 == 0 && kSmem <= 232448, "over the shared memory of a CTA");
 };
 
@@ -170,6 +171,8 @@ struct HeadGemm {
   const HeadRow* info;   // kGrad, and kProducts where its dh is final
   const __nv_bfloat16* emb;
   // kProducts
+  const __nv_bfloat16* hm;  // the rows that dE is made of
+  int64_t ldm;
   int splits, rows_pad;  // parts of dh's K, each with a buffer of rows_pad rows
   int dh_items, dh_out;
   Share de, g;              // tiles of dE and of the next piece's g
@@ -473,6 +476,18 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     griddep_launch();
   } else {
     if (MODE == kGrad) griddep_wait();
+    // With few rows a row of dE is mostly one target's, and would show its rounding: it gets
+    // back what g_t lost, too.
+    const bool few = MODE == kProducts && a.row.rows <= kFewRows;
+    int2* rests = reinterpret_cast<int2*>(smem + Cfg::kOffRest);
+    if (few) {
+      const int r = static_cast<int>(threadIdx.x) - 64;
+      if (r < a.row.rows) {
+        const float4 f = *reinterpret_cast<const float4*>(a.info + r);
+        rests[r] = make_int2(__float_as_int(f.w), __float_as_int(lost(f.z)));
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the epilogue's warps
+    }
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* boxes = smem + Cfg::kOffBox + (warp - 2) * 2 * Cfg::kBox;
     const uint32_t acce_leader = map_peer(smem_u32(acce), 0);
@@ -508,6 +523,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       const int width = MODE != kProducts ? a.cols : (grad ? a.g_cols : a.row.d);
       const int target = info.target - (MODE == kGrad ? a.v0 : (MODE == kProducts ? a.g_v0 : 0));
       const float rest = MODE == kProducts && !grad && info.target >= 0 ? lost(info.gt) : 0.f;
+      unsigned long long mine = 0;  // rows whose target is this row of dE
+      if (few && it.kind == kDe)
+        for (int r = 0; r < a.row.rows; ++r) mine |= static_cast<unsigned long long>(rests[r].x == a.v0 + m) << r;
       head_wait(&accf[b], (i >> 1) & 1, err, DERR_ACC_WAIT, abort);
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + half * (Cfg::kColumns / 2);
@@ -631,6 +649,24 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
                   for (int k = 0; k < 8; ++k) v[j + k] = fmaf(rest, w[k], v[j + k]);
                 }
               }
+            }
+            if (__any_sync(0xffffffffu, mine != 0)) {
+              __syncwarp();
+              for (unsigned long long todo = mine; todo; todo &= todo - 1) {
+                const int r = __ffsll(static_cast<long long>(todo)) - 1;
+                const float part = __int_as_float(rests[r].y);
+                const __nv_bfloat16* x = a.hm + r * a.ldm + c0;
+#pragma unroll
+                for (int j = 0; j < kWide; j += 8) {
+                  if (c0 + j < width) {
+                    float w[8];
+                    load8(x + j, w);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[j + k] = fmaf(part, w[k], v[j + k]);
+                  }
+                }
+              }
+              __syncwarp();
             }
             const float al = it.kind == kDe || a.dh_out == kDhBf16 ? a.row.inv_count : 1.f;
 #pragma unroll
@@ -1112,6 +1148,8 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   q.parts = parts;
   q.info = info;
   q.emb = e;
+  q.hm = hm;
+  q.ldm = at.ldm;
   const bool few = !grads && rows <= kFewRows;
   const int nparts = (few ? 8 : 2) * q.n_tiles;
   CUtensorMap map_h;
