@@ -139,8 +139,7 @@ struct HeadCfg {
   static constexpr int kStages = MODE == kProducts ? 5 : (MODE == kFew ? 9 : 6);
   static constexpr int kOffBox = kStages * kStage;
   static constexpr int kOffBar = kOffBox + 8 * 2 * kBox;
-  static constexpr int kOffRest = kOffBar + 512;  // kProducts: (target, rest) of up to kFewRows rows
-  static constexpr int kSmem = 1024 + kOffRest + (MODE == kProducts ? kFewRows * 8 : 0);
+  static constexpr int kSmem = 1024 + kOffBar + 512;
   static_assert(kOffBar % 8 == 0 && kSmem <= 232448, "over the shared memory of a CTA");
 };
 
@@ -477,16 +476,21 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   } else {
     if (MODE == kGrad) griddep_wait();
     // With few rows a row of dE is mostly one target's, and would show its rounding: it gets
-    // back what g_t lost, too.
+    // back what g_t lost, too.  Lane l knows the targets of rows l and l + 32.  (For more rows
+    // the search costs every tile: 2048 x 1024 x 32000 312 us instead of 293.)
     const bool few = MODE == kProducts && a.row.rows <= kFewRows;
-    int2* rests = reinterpret_cast<int2*>(smem + Cfg::kOffRest);
+    int few_target[2] = {-1, -1};
+    float few_rest[2] = {0.f, 0.f};
     if (few) {
-      const int r = static_cast<int>(threadIdx.x) - 64;
-      if (r < a.row.rows) {
-        const float4 f = *reinterpret_cast<const float4*>(a.info + r);
-        rests[r] = make_int2(__float_as_int(f.w), __float_as_int(lost(f.z)));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = 32 * u + lane;
+        if (r < a.row.rows) {
+          const float4 f = *reinterpret_cast<const float4*>(a.info + r);
+          few_target[u] = __float_as_int(f.w);
+          few_rest[u] = lost(f.z);
+        }
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");  // the epilogue's warps
     }
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* boxes = smem + Cfg::kOffBox + (warp - 2) * 2 * Cfg::kBox;
@@ -523,9 +527,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       const int width = MODE != kProducts ? a.cols : (grad ? a.g_cols : a.row.d);
       const int target = info.target - (MODE == kGrad ? a.v0 : (MODE == kProducts ? a.g_v0 : 0));
       const float rest = MODE == kProducts && !grad && info.target >= 0 ? lost(info.gt) : 0.f;
-      unsigned long long mine = 0;  // rows whose target is this row of dE
-      if (few && it.kind == kDe)
-        for (int r = 0; r < a.row.rows; ++r) mine |= static_cast<unsigned long long>(rests[r].x == a.v0 + m) << r;
+      unsigned hits[2] = {0, 0};  // rows whose target is among the warp's 32 rows of dE
+      if (few && it.kind == kDe) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          hits[u] = __ballot_sync(0xffffffffu, static_cast<unsigned>(few_target[u] - (a.v0 + mw)) < 32u);
+      }
       head_wait(&accf[b], (i >> 1) & 1, err, DERR_ACC_WAIT, abort);
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + half * (Cfg::kColumns / 2);
@@ -650,23 +657,27 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
                 }
               }
             }
-            if (__any_sync(0xffffffffu, mine != 0)) {
-              __syncwarp();
-              for (unsigned long long todo = mine; todo; todo &= todo - 1) {
-                const int r = __ffsll(static_cast<long long>(todo)) - 1;
-                const float part = __int_as_float(rests[r].y);
-                const __nv_bfloat16* x = a.hm + r * a.ldm + c0;
+            if (hits[0] | hits[1]) {
 #pragma unroll
-                for (int j = 0; j < kWide; j += 8) {
-                  if (c0 + j < width) {
-                    float w[8];
-                    load8(x + j, w);
+              for (int u = 0; u < 2; ++u)
+                for (unsigned todo = hits[u]; todo; todo &= todo - 1) {
+                  const int l = __ffs(todo) - 1;
+                  const int of = __shfl_sync(0xffffffffu, few_target[u], l) - (a.v0 + mw);
+                  const float part = __shfl_sync(0xffffffffu, few_rest[u], l);
+                  if (lane == of) {
+                    const __nv_bfloat16* x = a.hm + (32 * u + l) * a.ldm + c0;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[j + k] = fmaf(part, w[k], v[j + k]);
+                    for (int j = 0; j < kWide; j += 8) {
+                      if (c0 + j < width) {
+                        float w[8];
+                        load8(x + j, w);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[j + k] = fmaf(part, w[k], v[j + k]);
+                      }
+                    }
                   }
+                  __syncwarp();
                 }
-              }
-              __syncwarp();
             }
             const float al = it.kind == kDe || a.dh_out == kDhBf16 ? a.row.inv_count : 1.f;
 #pragma unroll
