@@ -250,8 +250,11 @@ int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t
  * the device error flag.  w_r = row_weight[r] (fp32 [rows]; NULL: 1).  A row
  * without a target or of weight 0 has loss 0, a zero row of dh and no part in demb;
  * its h is not used and may hold anything (NaN included).  Logits of other rows keep
- * their differences up to 2^24 in size; a NaN or an infinity shows in its own row's
- * loss and dh, and in demb.
+ * their differences up to 2^24 in size.  A NaN among a row's logits makes its loss, dh
+ * and all of demb NaN.  Without clip so does a logit of +inf; one of -inf counts as
+ * p = 0, and as a loss of +inf where it is the target's.  With clip > 0 an infinite
+ * logit counts as the limit, without a gradient.  (An infinity of h or E shows in its
+ * column of demb or dh besides, as 0 times it.)
  * piece     columns of the vocabulary that a launch works on (rounded up to a multiple
  *           of 256): more scratch and fewer launches with more of them.  g exists for
  *           one piece at a time, for two where the vocabulary takes several.  0: as

@@ -843,8 +843,9 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs a, const __nv_b
     cut = fabsf(zt) > a.clip;
     zt = limit(zt, a.clip);
   }
-  // odds of all other tokens together against the target: s 2^x
-  const float x = fmaf(-zt, kLog2e, rho);
+  // odds of all other tokens together against the target: s 2^x.  (A logit of +inf makes the others' s
+  // NaN by inf - inf; the target's is not among them)
+  const float x = zt == INFINITY ? NAN : fmaf(-zt, kLog2e, rho);
   const float odds = s * exp2f(x);
   const float nll = x > 60.f ? fmaf(x, kLn2, logf(s)) : log1pf(odds);
   loss[r] = w * a.inv_count * nll;
