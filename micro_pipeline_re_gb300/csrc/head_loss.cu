@@ -682,6 +682,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
             const float al = it.kind == kDe || a.dh_out == kDhBf16 ? a.row.inv_count : 1.f;
 #pragma unroll
             for (int j = 0; j < kWide; ++j) v[j] *= al;
+            // rows that count for nothing: zeros, where a table with a NaN made 0 times it
+            const bool none = it.kind == kDh && a.dh_out == kDhBf16 && info.target < 0;
+            if (__any_sync(0xffffffffu, none)) {
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < kWide; ++j) v[j] = none ? 0.f : v[j];
+            }
           }
           // out, 32 columns at a time, through the warp's two boxes
           const bool f32 = MODE == kProducts && !grad && (it.kind == kDe ? a.de_f32 : a.dh_out != kDhBf16);
@@ -918,7 +925,7 @@ __global__ void __launch_bounds__(256) head_dh_kernel(int rows, int d, int split
     for (int j = 0; j < 8; ++j) v[j] += u[j];
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= scale;
+  for (int j = 0; j < 8; ++j) v[j] = target < 0 ? 0.f : v[j] * scale;  // (0 times a table with a NaN is none)
   store8(dh + r * lddh + c, v);
 }
 
