@@ -297,16 +297,19 @@ int gpipe_op_embedding_scaled_fwd(int dtype, int rows, int d, int vocab, const i
                                   float scale, void* x, int64_t ldx, void* stream);
 
 /* Its gradient: demb[tokens[r],:] += scale dx[r,:] (fp32 accumulator, dx of dtype
- * elements with leading dimension lddx).  The rows are sorted by token first, so
- * that a frequent token's are summed by many CTAs: in ascending r, cut where runs of
- * 8 or 64 sorted rows end, the parts in order, scaled once and added to demb.  Padding
- * and ids out of range as above, with no gradient.  (gpipe_op_embedding_bwd adds one
- * row after the other and needs no scratch.)
+ * elements with leading dimension lddx), so that many CTAs sum a frequent token's rows.
+ * A token's rows are added in ascending r, in parts that are then added in order; the
+ * sum is scaled, rounded and added to demb.  The parts: up to 256 rows, quarters of the
+ * token's; more rows are sorted by token, stably, and cut into runs of 8 sorted rows (up
+ * to 24576) or 64, and a token of more than 16 runs has their sums added in eighths
+ * first.  Padding and ids out of range as above, with no gradient.
+ * (gpipe_op_embedding_bwd adds one row after the other and needs no scratch.)
  * scratch: gpipe_op_embedding_sorted_bwd_scratch_bytes, 256-byte aligned, written
  * before it is read (calls that may overlap on the GPU, captured ones included, need
  * one each, and a demb each).  demb and scratch may overlap neither each other nor
- * the inputs.  Every element of demb receives at most one addition (a subnormal one
- * counts as zero, as the GPU's reductions have it), so results are bit-reproducible. */
+ * the inputs.  Every element of demb receives at most one addition, by a reduction of
+ * the GPU's, which has subnormal operands and results as zero; so results are
+ * bit-reproducible. */
 int gpipe_op_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int32_t* tokens, const void* dx,
                                   int64_t lddx, float scale, float* demb, void* scratch, void* stream);
 

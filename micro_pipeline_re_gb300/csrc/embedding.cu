@@ -314,9 +314,14 @@ template <> struct Cols<__nv_bfloat16> {
     }
   }
 };
-// dE += v, an element's one addition of the call.
+// dE += v, an element's one addition of the call, always by the L2's reduction: a load, a
+// multiply-add and a store would round the scaled sum with the addition and keep subnormals,
+// where the others round it first and have them as zero.
 __device__ __forceinline__ void add_to(float* p, float a, float b, float c, float d) {
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ void add_to(float* p, float a) {
+  asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(a) : "memory");
 }
 
 // Up to kFewRows rows in one launch: CTA (r, y) sums 64 threads' columns of the rows of
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(256, 6) embed_join_kernel(int rows, int d, con
       float t = part[0][tid];
 #pragma unroll
       for (int w = 1; w < 8; ++w) t += part[w][tid];
-      demb[static_cast<int64_t>(k) * d + c0 + tid] += scale * t;
+      add_to(demb + static_cast<int64_t>(k) * d + c0 + tid, scale * t);
     }
     __syncthreads();
   }
