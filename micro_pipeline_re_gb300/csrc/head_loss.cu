@@ -1058,8 +1058,13 @@ bool head_map(CUtensorMap* m, const void* base, bool f32, int64_t inner, int64_t
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// early: launched while the launch before it runs, as only one behind another of the call is.
+// A CTA has most of an SM's shared memory and all of its tensor memory, and one that waited for a
+// foreign kernel would keep them from other streams for as long as that takes (a product of 0.7 ms
+// beside a call that waited for 25 ms of one CTA took those 25); within the call it is the launch
+// before's last tile or some microseconds.  The first pass so gives 1 to 1.6 us of its start away.
 template <Mode MODE>
-int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, int* err, cudaStream_t s) {
+int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, bool early, int* err, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   const int rc = once_per_device(done, [] {
     const cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1081,7 +1086,7 @@ int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, int
   attr[0].val.clusterDim.z = 1;
   set_priority_attr(attr[1], s);
   attr[2].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[2].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[2].val.programmaticStreamSerializationAllowed = early && pdl_enabled() ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 3;
   HeadGemm b = a;
@@ -1190,9 +1195,9 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
   if (few) {  // the vocabulary as rows
     std::swap(maps.a, maps.b);
     std::swap(q.m_tiles, q.n_tiles);
-    rc = launch_head_gemm<kFew>(maps, q, q.m_tiles, err, st);
+    rc = launch_head_gemm<kFew>(maps, q, q.m_tiles, false, err, st);
   } else {
-    rc = launch_head_gemm<kStats>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st);
+    rc = launch_head_gemm<kStats>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, at.copy, err, st);
   }
   if (rc) return rc;
   const auto* hb = static_cast<const __nv_bfloat16*>(h);
@@ -1222,7 +1227,7 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
       ok = (cols == vocab || head_map(&maps.b, emb, false, d, cols, d, kK, 128)) &&
            head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
       if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
-      if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, err, st))) return rc;
+      if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, true, err, st))) return rc;
     }
   }
   for (int v0 = 0; grads && v0 < vocab; v0 += at.cols, std::swap(now, then)) {
@@ -1259,7 +1264,7 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
            head_map(&maps.c2, demb, q.de_f32, d, vocab, d, 32, 32);
     if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
     const int64_t items = static_cast<int64_t>(q.dh_items) + q.de.n + q.g.n;
-    if ((rc = launch_head_gemm<kProducts>(maps, q, items, err, st))) return rc;
+    if ((rc = launch_head_gemm<kProducts>(maps, q, items, true, err, st))) return rc;
   }
   if (!dh || at.direct) return GPIPE_OK;
   const auto ctas = static_cast<unsigned>((static_cast<int64_t>(rows) * (d / 8) + 255) / 256);

@@ -1,12 +1,20 @@
 // Kernel launch with programmatic dependent launch (PDL).
 //
-// Every kernel of the library starts with griddep_wait() before it touches
-// global memory, which blocks until the preceding kernel in the stream has
+// Kernels of the library start with griddep_wait() before they touch
+// global memory (two named below aside), which blocks until the preceding kernel in the stream has
 // completed and its writes are visible; so letting the next kernel launch
 // early (PDL) only overlaps its launch and prologue with the predecessor's
 // tail, and never changes a result.  Kernels call griddep_launch() once their
 // remaining work no longer needs the SM resources a waiting successor would
 // take.
+//
+// Two kernels of the head's loss touch global memory before their wait: the one that joins
+// a row's sums reads the call's inputs and writes the copy of h, and the one that makes the
+// gradient reads h (or its copy) and the table.  Both stand behind that call's first pass over
+// the logits, which lets its successor launch only after its own griddep_wait(): whatever
+// came before the call has completed then, and no launch of the call between that pass and
+// them writes what they read or reads what they write.  This holds as long as the pass
+// waits before it lets go and no kernel that breaks it is put between them.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -27,7 +35,10 @@ void set_pdl_enabled(bool on);
 // memory and is not launched early, so that a waiting copy cannot keep those from
 // kernels of other streams.  (One that takes its tensor memory after griddep_wait()
 // and whose predecessor lets it launch only at its very end, when nothing but stores
-// is left, may still go without: the windowed attention's backward kernel.)
+// is left, may still go without: the windowed attention's backward kernel.  So may one
+// whose predecessor is of the same call and as short as its own launch, or fills the SMs itself:
+// the head loss's products behind its first pass, which is not launched early itself unless
+// the call copies h first.)
 // Every launch carries its stream's priority as a launch attribute, so that a
 // kernel captured into a graph (instantiated with node priorities) keeps the
 // priority of the stream it was issued to: the step's critical-path streams
