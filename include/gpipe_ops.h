@@ -240,7 +240,8 @@ int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t
  * over the table emb (bf16 [vocab, d]),
  *   z = h E^T in fp32, limited to [-clip, clip] where clip > 0, p = softmax(z),
  *   loss_rows[r] = w_r inv_count (-log p[target])
- *   g    = w_r (p - onehot(target)), 0 where |z| > clip > 0, rounded to bf16
+ *   g    = w_r (p - onehot(target)), 0 where |z| > clip > 0, rounded to bf16 (what the
+ *          target's column loses by it is given back to dh, and to demb of up to 64 rows)
  *   dh   = inv_count g E        bf16 [rows, d], leading dimension lddh, or NULL
  *   demb = inv_count g^T h      [vocab, d], or NULL: demb_dtype 0 an fp32
  *                               accumulator that receives it (+=), 1 bf16, written
@@ -258,13 +259,18 @@ int gpipe_op_distill(int dtype, int rows, int vocab, const void* logits, int64_t
  * piece     columns of the vocabulary that a launch works on (rounded up to a multiple
  *           of 256): more scratch and fewer launches with more of them.  g exists for
  *           one piece at a time, for two where the vocabulary takes several.  0: as
- *           many as give g 256 MB.
+ *           many as give g 256 MB in all, but 2048 at least (so more than 32768 rows
+ *           over several pieces have two buffers of 4096 bytes a row).  Results
+ *           depend on it by their roundings, and where the first piece's p passes
+ *           through fp16 (d >= 768, or less where the rows do not fill tiles of 256):
+ *           there those below 2^-38 of the largest of 128 columns may count as 0.
  * scratch   gpipe_op_head_loss_scratch_bytes (grads: 1 dh, 2 demb, 3 both), 256-byte
  *           aligned, written before it is read (calls that may overlap on the GPU,
  *           captured ones included, need one each, and outputs each).
  * 1 <= rows <= 2^24, 1 <= vocab <= 2^27 (and at most 2^26 tiles of 256 x 256),
- * d <= 2^16 and the leading dimensions multiples of 8, 16-byte aligned bases.  Outputs and scratch may overlap neither each other nor an
- * input.  No atomics: results are bit-reproducible. */
+ * d <= 2^16 and the leading dimensions multiples of 8, 16-byte aligned bases.  Outputs
+ * and scratch may overlap neither each other nor an input.  Every element receives its
+ * additions one launch after the other: results are bit-reproducible. */
 int gpipe_op_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, const void* emb_bf16, int seq,
                        const int32_t* tokens, int row0, const float* row_weight, float inv_count, float clip,
                        int piece, float* loss_rows, void* dh, int64_t lddh, int demb_dtype, void* demb, void* scratch,
@@ -303,7 +309,8 @@ int gpipe_op_embedding_scaled_fwd(int dtype, int rows, int d, int vocab, const i
  * token's; more rows are sorted by token, stably, and cut into runs of 8 sorted rows (up
  * to 24576) or 64, and a token of more than 16 runs has their sums added in eighths
  * first.  Padding and ids out of range as above, with no gradient.
- * (gpipe_op_embedding_bwd adds one row after the other and needs no scratch.)
+ * (gpipe_op_embedding_bwd adds one row after the other and needs no scratch; it is
+ * quicker for up to some 2000 rows whose tokens hardly repeat.)
  * scratch: gpipe_op_embedding_sorted_bwd_scratch_bytes, 256-byte aligned, written
  * before it is read (calls that may overlap on the GPU, captured ones included, need
  * one each, and a demb each).  demb and scratch may overlap neither each other nor

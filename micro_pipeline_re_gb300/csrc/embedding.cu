@@ -8,10 +8,12 @@
 // rest).  The sorted positions are cut into runs of 8 or 64; a group of threads
 // reads a run's rows one after the other, many in flight, and sums them by token in
 // order.  A token whose rows lie in one run is added to dE there; one that crosses
-// runs leaves a sum in each, which a last kernel adds in order and then to dE.  So a
-// frequent token's rows are read by many CTAs at once, and yet no sum depends on
-// which of them was first.  Every element of dE receives one addition a call (a
-// reduction in the L2: nobody waits for the old value).
+// runs leaves a sum in each, which a last kernel adds in order (more than 16 of them in
+// eighths first) and then to dE.  So a frequent token's rows are read by many CTAs at once,
+// and yet no sum depends on which of them was first.  Every element of dE receives one
+// addition a call (a reduction in the L2: nobody waits for the old value).
+//
+// Few rows are not sorted: one launch finds each token's rows and adds them in quarters.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -46,8 +48,8 @@ constexpr int kTile = 512;       // positions of a CTA of a radix pass, at least
 // (131072 rows of 8 columns 41 us with 64, 44 with 128).
 constexpr int kSortCtas = 128;
 constexpr int kHalfRows = 1 << 18;
-constexpr int kManyRuns = 16;  // runs from which a token's sums are joined by several CTAs
-constexpr int kJoinCtas = 8;   // join CTAs an SM
+constexpr int kManyRuns = 16;  // more runs than these have a token's sums joined by several CTAs
+constexpr int kJoinCtas = 8;   // join CTAs launched an SM, at most (6 at once)
 
 // ---------------------------------------------------------------------------
 // Lookup: a warp per row, 8 elements a lane and step; the product is rounded to
@@ -429,7 +431,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(int rows, int d, int voc
 #pragma unroll 1
   for (int q = 0; q < n; q += 8) {
     // (keys and order have room for a whole run behind the last row)
-    const int4 ka = *reinterpret_cast<const int4*>(keys + p0 + q), kb = *reinterpret_cast<const int4*>(keys + p0 + q + 4);
+    const int4 ka = *reinterpret_cast<const int4*>(keys + p0 + q),
+               kb = *reinterpret_cast<const int4*>(keys + p0 + q + 4);
     const int4 oa = *reinterpret_cast<const int4*>(order + p0 + q),
                ob = *reinterpret_cast<const int4*>(order + p0 + q + 4);
     const int kk[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
@@ -625,7 +628,8 @@ int launch_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int
     using T = std::remove_const_t<std::remove_pointer_t<decltype(in_rows)>>;
     if (rows <= kFewRows) {
       const int wide = 64 * Cols<T>::N;
-      (void)launch_k(embed_few_kernel<T>, dim3(rows, (d + wide - 1) / wide), 256, 0, s, rows, d, vocab, tokens, in_rows, lddx, scale, demb, err);
+      (void)launch_k(embed_few_kernel<T>, dim3(rows, (d + wide - 1) / wide), 256, 0, s, rows, d, vocab, tokens,
+                     in_rows, lddx, scale, demb, err);
       return check("embedding_sorted_bwd");
     }
     char* w = static_cast<char*>(scratch);
@@ -636,7 +640,8 @@ int launch_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int
     float* partial = reinterpret_cast<float*>(w + at.partial);
     int have = 0;
     if (rows <= kRankRows) {
-      (void)launch_k(embed_rank_kernel, (rows + 31) / 32, 256, 0, s, rows, vocab, tokens, keys[0], order[0], joins, err);
+      (void)launch_k(embed_rank_kernel, (rows + 31) / 32, 256, 0, s, rows, vocab, tokens, keys[0], order[0], joins,
+                     err);
       if (const int rc = check("embedding_sorted_bwd")) return rc;
     } else {
       int bits = 1;
@@ -653,8 +658,8 @@ int launch_embedding_sorted_bwd(int dtype, int rows, int d, int vocab, const int
         const int* now = counts + static_cast<int64_t>(p) * kSortCtas * kBins;
         int* then = p + 1 < passes ? counts + static_cast<int64_t>(p + 1) * kSortCtas * kBins : nullptr;
         have = p & 1;
-        (void)launch_k(embed_scatter_kernel, grid, kScatterThreads, 0, s, rows, per, vocab, p * kDigit, p == 0, src, src_order,
-                       now, then, keys[have], order[have]);
+        (void)launch_k(embed_scatter_kernel, grid, kScatterThreads, 0, s, rows, per, vocab, p * kDigit, p == 0, src,
+                       src_order, now, then, keys[have], order[have]);
         if (const int rc = check("embedding_sorted_bwd")) return rc;
         src = keys[have];
         src_order = order[have];

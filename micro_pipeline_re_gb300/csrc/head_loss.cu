@@ -34,14 +34,14 @@
 // finished fp32 sums, so that g_t, close to -w for most rows, is close to a whole number
 // and its rounding does not add up over the rows.
 //
-// Cost: 6 rows vocab d flops with both gradients for the first piece, 8 for the others.
+// Cost: 8 rows vocab d flops with both gradients, 6 for a first piece whose powers are kept.
 // Memory: 2 B an element of a piece of g, or of two where there are several, which is all
 // that is ever held of the logits.  The powers are fp16 because it has three bits more than
 // bf16, 2^-28 of the largest of 128 down (their reference puts that near 2^14): g's rounding
 // to bf16 stays the only one that tells.
 //
-// Measured at 2048 rows x 1024 x 32000 (134 GFLOP a product; ncu, and 290 us for all five in
-// a graph, 314 in a row, where the GPU meets its power limit): kStats 83 us with the powers
+// Measured at 2048 rows x 1024 x 32000 (134 GFLOP a product; ncu, and 291 us for all five in
+// a graph, 317 in a row, where the GPU meets its power limit): kStats 83 us with the powers
 // and 74 without (1805 TFLOP/s, 92 % of a library product's burst rate; tensor pipe 77 %
 // active), head_rows 5, head_scale 42 (262 MB, 6.3 TB/s), kProducts 149 (1802 TFLOP/s, tensor
 // pipe 87 %), head_dh 7.  An issuing thread whose waits read no clock unless they have to
@@ -112,18 +112,19 @@ enum DhOut { kDhStore, kDhAdd, kDhBf16 };  // fp32, fp32 added, bf16 and final
 
 constexpr int kTile = 256;     // rows and columns of a pair's tile
 // kFew: rows of h, its columns.  A tile of kStats costs 256 rows' products however few there
-// are: 1 row over 32000 x 1024 (65 MB, here from the L2) 16.9 us this way, 24.7 that way
+// are: 1 row over 32000 x 1024 (65 MB, here from the L2) 18.4 us this way, 26.6 that way; 64
+// rows 16.3 and 18.1
 constexpr int kFewRows = 64;
 constexpr int kK = 64;         // a k-block
 constexpr int kHeadThreads = 320;
 constexpr int kGroup = 16;     // row tiles that the tiles in flight share
 // d from which reading the first piece's powers is cheaper than making z again: with both
-// gradients over 32000 columns 2048 rows take 207 us kept and 188 made again at d = 512, 248
-// and 259 at 768, 297 and 321 at 1024; 512 rows 73 and 70, 97 and 97, 105 and 107
+// gradients over 32000 columns 2048 rows take 187 us kept and 181 made again at d = 512, 242
+// and 243 at 768, 291 and 314 at 1024; 512 rows 68 and 67, 83 and 84, 98 and 102
 constexpr int kKeepWidth = 768;
 // rows x vocab x d from which h is copied where its rows do not start on 32 bytes, the L2's
-// sectors: 2048 x 712 x 32000 take 76 us to read it as it is and 63 from rows of 768 (720
-// columns 61; 1016 and 1024 97 and 80), the copy about 3.  That E's rows lie like that hardly tells.
+// sectors: 2048 x 712 x 32000, the loss, take 75 us as it is and 62 with the copy (720 columns 60),
+// 2048 x 1016 96 and 82 (1024 columns 75).  That E's rows lie like that hardly tells.
 constexpr int64_t kCopyWork = int64_t{1} << 33;
 constexpr int kWideRows = 1216;  // rows up to which each has a CTA to join its sums (eight an SM)
 constexpr int kPlanPairs = 76; // pairs of SMs that the split of dh's K is planned for (any number runs it)
@@ -266,8 +267,11 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t u) {
 }
 
 // Arrival at a barrier of the pair without the release of earlier writes, which costs
-// about 1200 clocks at cluster scope: what is handed back is tensor memory whose loads
-// have completed.
+// about 1200 clocks at cluster scope.  No writes are handed over: each lane's loads of the
+// tensor memory have completed (tcgen05.wait::ld) and are ordered before what follows by its
+// tcgen05.fence::before_thread_sync, the lanes' before this one lane's arrival by __syncwarp(),
+// and the products behind the issuer's wait by its tcgen05.fence::after_thread_sync.  Generic
+// memory that a warp wrote before is not visible through it, and nobody reads any by it.
 __device__ __forceinline__ void arrive_relaxed(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
@@ -619,7 +623,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
             }
           }
           if (grad) {
-            const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-info.rho, -info.rho), sc = pack2(info.scale, info.scale);
+            const f32x2 l2 = pack2(kLog2e, kLog2e), ref = pack2(-info.rho, -info.rho);
+            const f32x2 sc = pack2(info.scale, info.scale);
             if (a.row.clip > 0.f) {  // columns beyond the limit: marked, so that they come out as 0
               __syncwarp();
 #pragma unroll
@@ -943,7 +948,8 @@ int up_to(int n, int m) { return (n + m - 1) / m; }
 
 bool sizes_ok(int rows, int d, int vocab, int piece) {
   return rows >= 1 && rows <= (1 << 24) && d >= 8 && d <= (1 << 16) && d % 8 == 0 && vocab >= 1 &&
-         vocab <= (1 << 27) && piece >= 0 && static_cast<int64_t>(up_to(rows, kTile)) * up_to(vocab, kTile) <= (1 << 26);
+         vocab <= (1 << 27) && piece >= 0 &&
+         static_cast<int64_t>(up_to(rows, kTile)) * up_to(vocab, kTile) <= (1 << 26);
 }
 
 // Columns of a piece: a multiple of 256; 0 asks for as many as make g 256 MB, in one piece or
@@ -1062,7 +1068,9 @@ bool head_map(CUtensorMap* m, const void* base, bool f32, int64_t inner, int64_t
 // A CTA has most of an SM's shared memory and all of its tensor memory, and one that waited for a
 // foreign kernel would keep them from other streams for as long as that takes (a product of 0.7 ms
 // beside a call that waited for 25 ms of one CTA took those 25); within the call it is the launch
-// before's last tile or some microseconds.  The first pass so gives 1 to 1.6 us of its start away.
+// before's last tile or some microseconds.  The first pass gives some of its start away by that:
+// calls in a row 18.6 us for 16.5 (5 x 64 x 517, both gradients), 22.6 for 19.1 (1 x 1024 x 32000),
+// 294 for 291 (2048 x 1024 x 32000, both), 57 for 51 (1 x 1024 x 131072).
 template <Mode MODE>
 int launch_head_gemm(const HeadMaps& maps, const HeadGemm& a, int64_t items, bool early, int* err, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
@@ -1227,7 +1235,8 @@ int launch_head_loss(int rows, int d, int vocab, const void* h, int64_t ldh, con
       ok = (cols == vocab || head_map(&maps.b, emb, false, d, cols, d, kK, 128)) &&
            head_map(&maps.c, g, false, cols, rows, at.cols, 32, 32);
       if (!ok) return set_error(GPIPE_ERR_CUDA, "head_loss: cuTensorMapEncodeTiled failed");
-      if ((rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, true, err, st))) return rc;
+      rc = launch_head_gemm<kGrad>(maps, q, static_cast<int64_t>(q.m_tiles) * q.n_tiles, true, err, st);
+      if (rc) return rc;
     }
   }
   for (int v0 = 0; grads && v0 < vocab; v0 += at.cols, std::swap(now, then)) {
